@@ -47,7 +47,8 @@ typedef enum {
     TXL_ERR_CUDA = -5,        /* a CUDA runtime or driver call failed */
     TXL_ERR_TIMEOUT = -6,     /* a kernel gave up waiting on an on-chip barrier */
     TXL_ERR_WORKSPACE = -7,   /* workspace missing or too small for the request */
-    TXL_ERR_INDEX = -8        /* a device-side index check failed (debug builds only) */
+    TXL_ERR_INDEX = -8        /* an index held on the device was out of range (page ids, parents,
+                                 source rows); debug builds: any device-side index check */
 } txl_status;
 
 typedef enum {
@@ -385,6 +386,133 @@ int txl_relattn_bwd(const void *q, const void *k, const void *v, const void *r, 
                     float *dv, float *dr, float *du, float *dv_bias, int B, int H, int M, int L,
                     int dh, float scale, int dtype, void *workspace, size_t workspace_bytes,
                     void *stream);
+
+/*
+ * Paged memory.  The memory of §3.2 for sequences whose lengths differ and
+ * change on the device: the projected keys and values of a sequence lie in pages
+ * of page_rows rows, listed by a page table.  The paper keeps one memory length
+ * for a batch; this form serves streams that begin, fork and advance apart (for
+ * instance by the accepted part of a drafted tree).
+ *
+ *   pool    device [2 * layers][n_pages][H][page_rows][dh]: plane 2 l holds layer
+ *           l's keys, plane 2 l + 1 its values; a page id names the same page
+ *           of every plane.  16-byte aligned.
+ *   table   device [B][slots] int32: page ids of a sequence.  Its table rows 0 ..
+ *           R-1 (R = slots * page_rows) are a ring: table row x is row x mod
+ *           page_rows of page table[b][x / page_rows].
+ *   begin   device [B] int32 in [0, R): table row of the oldest memory row
+ *   fill    device [B] int32 in [0, R]: memory rows held
+ *   ticket  device, one int32, zero before the first use (left at zero)
+ * Memory row t (0 = oldest) lies in table row (begin + t) mod R.  A memory that
+ * slides (keep rows of it, below) comes around to its own oldest pages, so the
+ * table of a sequence need not change as it advances; pages shared with another
+ * sequence (a fork) have to be copied before rows are put into them.
+ * dh must be 64, page_rows a multiple of 32 (a tile of keys never crosses a
+ * page), dtype TXL_BF16 or TXL_F32.
+ *
+ * What lies on the device is checked on the device.  A page id outside
+ * [0, n_pages) is never dereferenced: rows in it are not written and not
+ * attended to.  begin and fill are brought into their ranges.  Either records
+ * TXL_ERR_INDEX for txl_device_status.
+ * The struct lives in HOST memory; its contents are read during the call.
+ */
+typedef struct {
+    void *pool;
+    const int *table;
+    int *begin;
+    int *fill;
+    int *ticket;
+    int layers;
+    int n_pages;
+    int H;
+    int page_rows;
+    int dh;
+    int B;
+    int slots;
+    int dtype;
+} txl_paged_kv;
+
+/*
+ * A [B][H][rows][dh] operand with strides, in elements, of its first three
+ * dimensions (dh contiguous): for instance the heads of a projection's output
+ * [B][rows][H * dh].  The pointer must be 16-byte aligned and the strides of
+ * dimensions larger than one positive multiples of 16 bytes.
+ */
+typedef struct {
+    void *ptr;
+    long long stride_b, stride_h, stride_row;
+} txl_rows;
+
+/*
+ * txl_paged_append - put new rows behind the memory (§3.2: the memory takes the
+ * newest states) and, if asked, advance it.  For layers layer0 .. layer0 +
+ * n_layers - 1, every sequence b, head and t < n_new[b]:
+ *   memory row fill[b] + t  <-  row (rows ? rows[b][t] : t) of k and v
+ *   k, v    layer layer0 + l of them starts l * layer_stride elements on
+ *           (layer_stride is a multiple of 16 bytes); N rows each.
+ *   n_new   device [B], values taken into [0, max_rows]; NULL: max_rows
+ *   rows    device [B][rows_stride >= max_rows] of source rows in [0, N) (the
+ *           accepted nodes of a drafted tree, say; the same row may come more
+ *           than once), or NULL (then max_rows <= N)
+ * A source row outside [0, N) and rows the table has no room for (fill + n >
+ * R) are not written and record TXL_ERR_INDEX.
+ * begin_out, fill_out (device [B], both or neither): the state advanced to the
+ * newest `keep` rows (n' of n_new fit the table), keep in [0, R]:
+ *   fill_out = min(fill + n', keep), begin_out = (begin + fill + n' - fill_out) mod R
+ * They may be mem->begin and mem->fill themselves.  Then the call uses
+ * mem->ticket, and calls on the same memory must not overlap in time; without
+ * that, calls for different layers may.
+ * Errors: TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED (dh, page_rows, dtype, sizes
+ * past the grid limits), TXL_ERR_MISALIGNED, TXL_ERR_SHAPE, TXL_ERR_CUDA.
+ */
+int txl_paged_append(const txl_paged_kv *mem, int layer0, int n_layers, const txl_rows *k,
+                     const txl_rows *v, long long layer_stride, int N, const int *rows,
+                     int rows_stride, const int *n_new, int max_rows, int keep, int *begin_out,
+                     int *fill_out, void *stream);
+
+/*
+ * txl_paged_advance - the state part of txl_paged_append alone, for a caller
+ * that appended layer by layer: begin_out, fill_out (which may be mem->begin
+ * and mem->fill) from n_new (NULL: max_rows for every sequence), as above.
+ * Errors: as txl_paged_append.
+ */
+int txl_paged_advance(const txl_paged_kv *mem, const int *n_new, int max_rows, int keep,
+                      int *begin_out, int *fill_out, void *stream);
+
+/*
+ * txl_paged_copy - copy pages src[i] to pages dst[i], i < n (device int32), in
+ * every plane of the pool: a forked sequence's own copy of a page it will write,
+ * or pages moved together.  No page may be a destination twice, nor a source
+ * and a destination (unless src[i] = dst[i], which copies nothing).  A pair with
+ * an id outside [0, n_pages) is skipped and records TXL_ERR_INDEX.
+ * Errors: as txl_paged_append.
+ */
+int txl_paged_copy(const txl_paged_kv *mem, const int *src, const int *dst, int n, void *stream);
+
+/*
+ * txl_page_pool - host-side accounting of a pool's pages: which are free and by
+ * how many sequences each is used.  The caller owns the struct and both arrays
+ * of n_pages ints.  Host arithmetic only; not thread-safe.
+ *   txl_page_pool_init     every page free
+ *   txl_page_pool_alloc    n pages, each with one user; all or none: TXL_ERR_SHAPE when
+ *                          fewer are free
+ *   txl_page_pool_retain   one user more for each page (a fork shares it)
+ *   txl_page_pool_release  one user less; a page without users is free again.
+ *                          *n_freed (may be NULL): how many became free
+ * Errors: TXL_ERR_INVALID_ARG (NULL pointers, negative counts, ids out of range,
+ * pages that have no user; nothing is changed then).
+ */
+typedef struct {
+    int n_pages;
+    int n_free;
+    int *free_list; /* ids of the free pages, the next one to hand out last */
+    int *users;     /* per page */
+} txl_page_pool;
+
+int txl_page_pool_init(txl_page_pool *p, int n_pages, int *free_list, int *users);
+int txl_page_pool_alloc(txl_page_pool *p, int *pages, int n);
+int txl_page_pool_retain(txl_page_pool *p, const int *pages, int n);
+int txl_page_pool_release(txl_page_pool *p, const int *pages, int n, int *n_freed);
 
 /*
  * txl_device_status - synchronise `stream`, then read and clear the device

@@ -1,0 +1,156 @@
+"""The paged memory's host side (CPU only, nothing launches): the refusals of its
+entry points, and the page pool's accounting against a model of it."""
+
+import ctypes
+import random
+
+import pytest
+import torch
+
+import transformer_xl_relative_pos_gb300 as txl
+from transformer_xl_relative_pos_gb300 import _lib
+
+OK, INVALID, UNSUPPORTED, MISALIGNED, SHAPE = 0, -1, -2, -3, -4
+
+
+def kv(**kw):
+    """A txl_paged_kv of made-up, aligned addresses that are never read."""
+    a = dict(pool=1 << 20, table=4096, begin=8192, fill=12288, ticket=16384, layers=2, n_pages=10,
+             H=2, page_rows=32, dh=64, B=3, slots=3, dtype=txl.BF16)
+    a.update(kw)
+    return _lib._PagedKV(*(a[f] for f, _ in _lib._PagedKV._fields_))
+
+
+def rows(ptr=1 << 16, sb=2048, sh=64, sr=128):
+    return _lib._Rows(ptr, sb, sh, sr)
+
+
+BAD_KV = [(dict(pool=None), INVALID), (dict(table=None), INVALID), (dict(begin=None), INVALID),
+          (dict(fill=None), INVALID), (dict(layers=0), INVALID), (dict(n_pages=0), INVALID),
+          (dict(H=0), INVALID), (dict(B=0), INVALID), (dict(slots=0), INVALID),
+          (dict(page_rows=0), INVALID), (dict(dtype=5), INVALID), (dict(dh=128), UNSUPPORTED),
+          (dict(page_rows=48), UNSUPPORTED), (dict(page_rows=16), UNSUPPORTED),
+          (dict(B=65536), UNSUPPORTED), (dict(slots=1 << 26), UNSUPPORTED),
+          (dict(n_pages=1 << 30, H=2), UNSUPPORTED), (dict(pool=(1 << 20) + 8), MISALIGNED),
+          (dict(table=4098), MISALIGNED), (dict(fill=12290), MISALIGNED)]
+
+
+def append(mem=None, layer0=0, n_layers=1, k=None, v=None, layer_stride=0, N=8, idx=None,
+           idx_stride=0, n_new=None, max_rows=8, keep=0, begin_out=None, fill_out=None):
+    ref = ctypes.byref
+    return txl.lib().txl_paged_append(ref(mem or kv()), layer0, n_layers, ref(k or rows()),
+                                      ref(v or rows()), layer_stride, N, idx, idx_stride, n_new,
+                                      max_rows, keep, begin_out, fill_out, None)
+
+
+@pytest.mark.parametrize("kw,want", BAD_KV)
+def test_a_bad_memory_is_refused(kw, want):
+    m, L = kv(**kw), txl.lib()
+    assert append(mem=m) == want
+    assert L.txl_paged_advance(ctypes.byref(m), None, 1, 4, 20480, 24576, None) == want
+    assert L.txl_paged_copy(ctypes.byref(m), 4096, 8192, 1, None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(layer0=-1), INVALID), (dict(n_layers=0), INVALID), (dict(N=-1), INVALID),
+    (dict(max_rows=-1), INVALID), (dict(layer0=1, n_layers=2, layer_stride=64), SHAPE),
+    (dict(max_rows=9), SHAPE),                               # more rows than k has
+    (dict(idx=4096, idx_stride=7), SHAPE), (dict(idx=4098, idx_stride=8), MISALIGNED),
+    (dict(idx=4096, idx_stride=8, N=0), SHAPE),
+    (dict(n_new=4097), MISALIGNED),
+    (dict(k=rows(ptr=None)), INVALID), (dict(v=rows(ptr=None)), INVALID),
+    (dict(k=rows(ptr=65544)), MISALIGNED), (dict(v=rows(sr=4)), MISALIGNED),
+    (dict(k=rows(sb=0)), INVALID), (dict(k=rows(sh=-64)), INVALID),
+    (dict(n_layers=2, layer_stride=0), INVALID), (dict(n_layers=2, layer_stride=12), MISALIGNED),
+    (dict(begin_out=20480), INVALID), (dict(fill_out=20480), INVALID),
+    (dict(begin_out=20480, fill_out=20484), INVALID),        # overlap each other
+    (dict(begin_out=8196, fill_out=24576), INVALID),         # overlap the state in part
+    (dict(begin_out=20480, fill_out=24576, keep=97), SHAPE), # more than the table holds
+    (dict(begin_out=20480, fill_out=24576, keep=-1), INVALID),
+    (dict(begin_out=20482, fill_out=24576), MISALIGNED),
+    (dict(mem=kv(ticket=None), begin_out=8192, fill_out=12288), INVALID),
+    (dict(max_rows=0), OK),                                  # nothing to do
+])
+def test_append_refusals(kw, want):
+    assert append(**kw) == want
+
+
+def test_advance_and_copy_refusals():
+    L, m = txl.lib(), kv()
+    adv = lambda n, keep, b, f, rows=4: L.txl_paged_advance(ctypes.byref(m), n, rows, keep, b, f, None)
+    assert adv(None, 4, None, 24576) == INVALID and adv(None, 4, 20480, None) == INVALID
+    assert adv(None, -1, 20480, 24576) == INVALID and adv(None, 97, 20480, 24576) == SHAPE
+    assert adv(4097, 4, 20480, 24576) == MISALIGNED and adv(None, 4, 20480, 24576, -1) == INVALID
+    assert adv(None, 4, 8200, 24576) == INVALID
+    copy = lambda s, d, n: L.txl_paged_copy(ctypes.byref(m), s, d, n, None)
+    assert copy(None, 4096, 1) == INVALID and copy(4096, None, 1) == INVALID
+    assert copy(4096, 8192, -1) == INVALID and copy(4098, 8192, 1) == MISALIGNED
+    assert copy(None, None, 0) == OK
+
+
+def test_the_binding_refuses_host_tensors_and_bad_shapes():
+    pool = torch.zeros(2, 4, 1, 32, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        txl.PagedKV(pool, torch.zeros(1, 2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="pool must be"):
+        txl.PagedKV(pool[:1], torch.zeros(1, 2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="table must be"):
+        txl.PagedKV(pool, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="begin must be"):
+        txl.PagedKV(pool, torch.zeros(1, 2, dtype=torch.int32), begin=torch.zeros(2, dtype=torch.int32))
+
+
+def test_page_pool_against_a_model():
+    rng = random.Random(5)
+    pool, n = txl.PagePool(37), 37
+    users = [0] * n
+    held = []
+    for _ in range(3000):
+        what = rng.random()
+        if what < 0.4:
+            want = rng.randint(0, 9)
+            free = users.count(0)
+            if want > free:
+                with pytest.raises(txl.TxlError) as e:
+                    pool.alloc(want)
+                assert e.value.status == SHAPE
+            else:
+                got = pool.alloc(want)
+                assert len(set(got)) == want and all(users[p] == 0 for p in got)
+                for p in got:
+                    users[p] = 1
+                held.append(got)
+        elif what < 0.6 and held:
+            pages = rng.choice(held)
+            pool.retain(pages)
+            for p in pages:
+                users[p] += 1
+            held.append(list(pages))
+        elif held:
+            pages = held.pop(rng.randrange(len(held)))
+            freed = pool.release(pages)
+            for p in pages:
+                users[p] -= 1
+            assert freed == sum(users[p] == 0 for p in pages)
+        assert pool.n_free == users.count(0)
+        assert [pool.users(p) for p in range(n)] == users
+
+
+def test_page_pool_refusals_change_nothing():
+    pool = txl.PagePool(4)
+    a = pool.alloc(2)
+    for bad in ([a[0], 9], [a[0], -1], [a[0], 3]):           # 3 has no user
+        for call in (pool.retain, pool.release):
+            with pytest.raises(txl.TxlError) as e:
+                call(bad)
+            assert e.value.status == INVALID
+    with pytest.raises(txl.TxlError):
+        pool.release([a[0], a[0]])                           # one user, named twice
+    assert [pool.users(p) for p in a] == [1, 1] and pool.n_free == 2
+    pool.retain([a[0]])
+    assert pool.release([a[0], a[0], a[1]]) == 2             # two users, named twice
+    assert pool.n_free == 4 and sorted(pool.alloc(4)) == [0, 1, 2, 3]
+    assert txl.PagePool(0).alloc(0) == []
+    L = txl.lib()
+    assert L.txl_page_pool_init(None, 1, None, None) == INVALID
+    assert L.txl_page_pool_alloc(None, None, 0) == INVALID

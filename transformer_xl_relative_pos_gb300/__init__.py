@@ -19,6 +19,10 @@ N-layer summary, Appendix B reversed table and shift):
                   by relattn_fwd (k, v as strided views)
   qkv_project     one layer's q, k, v projections written into q and the k / v
                   window, with the memory update, in one launch
+  PagedKV, paged_* keys and values of the memory in pages, for sequences whose
+                  lengths differ: rows appended (a segment's, or the accepted
+                  nodes of a drafted tree), the state advanced, pages copied
+  PagePool        host-side accounting of those pages (free, shared)
   relattn_bwd     gradients of relattn_fwd for one segment (training within a
                   segment, the memory SG(m))
 """
@@ -30,6 +34,8 @@ from ._lib import (  # noqa: F401
     BF16,
     KVWindow,
     MemState,
+    PagedKV,
+    PagePool,
     TxlError,
     bwd_workspace_size,
     debug_checks,
@@ -43,6 +49,9 @@ from ._lib import (  # noqa: F401
     lib_path,
     mem_concat,
     mem_update,
+    paged_advance,
+    paged_append,
+    paged_copy,
     qkv_project,
     rel_pos_emb,
     relattn_bwd,

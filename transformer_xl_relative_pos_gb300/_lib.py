@@ -20,6 +20,9 @@ _c_int, _c_size, _c_p, _c_float, _c_u64 = (ctypes.c_int, ctypes.c_size_t, ctypes
                                            ctypes.c_float, ctypes.c_uint64)
 
 
+_c_ip = ctypes.POINTER(ctypes.c_int)
+
+
 class TxlError(RuntimeError):
     """A non-zero txl_status returned by the library."""
 
@@ -38,6 +41,28 @@ class KVWindow(ctypes.Structure):
     def __repr__(self):
         return (f"KVWindow(start={self.start}, fill={self.fill}, capacity={self.capacity}, "
                 f"M={self.M})")
+
+
+class _Rows(ctypes.Structure):
+    """txl_rows: a [B, H, rows, 64] operand by its pointer and element strides."""
+
+    _fields_ = [("ptr", _c_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_row", ctypes.c_longlong)]
+
+
+class _PagedKV(ctypes.Structure):
+    """txl_paged_kv."""
+
+    _fields_ = [("pool", _c_p), ("table", _c_p), ("begin", _c_p), ("fill", _c_p),
+                ("ticket", _c_p)] + [(f, ctypes.c_int) for f in (
+                    "layers", "n_pages", "H", "page_rows", "dh", "B", "slots", "dtype")]
+
+
+class _PagePool(ctypes.Structure):
+    """txl_page_pool."""
+
+    _fields_ = [("n_pages", ctypes.c_int), ("n_free", ctypes.c_int), ("free_list", _c_ip),
+                ("users", _c_ip)]
 
 
 class MemState(ctypes.Structure):
@@ -107,6 +132,17 @@ def lib():
                                             _c_int, _c_int, _c_int, _c_p]),
                 "txl_mem_update": (_c_int, [_c_p, ctypes.POINTER(MemState), _c_p, _c_int, _c_int,
                                             _c_int, _c_int, _c_p]),
+                "txl_paged_append": (_c_int, [ctypes.POINTER(_PagedKV), _c_int, _c_int,
+                                              ctypes.POINTER(_Rows), ctypes.POINTER(_Rows),
+                                              ctypes.c_longlong, _c_int, _c_p, _c_int, _c_p,
+                                              _c_int, _c_int, _c_p, _c_p, _c_p]),
+                "txl_paged_advance": (_c_int, [ctypes.POINTER(_PagedKV), _c_p, _c_int, _c_int,
+                                               _c_p, _c_p, _c_p]),
+                "txl_paged_copy": (_c_int, [ctypes.POINTER(_PagedKV), _c_p, _c_p, _c_int, _c_p]),
+                "txl_page_pool_init": (_c_int, [ctypes.POINTER(_PagePool), _c_int, _c_ip, _c_ip]),
+                "txl_page_pool_alloc": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
+                "txl_page_pool_retain": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
+                "txl_page_pool_release": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int, _c_ip]),
                 "txl_device_status": (_c_int, [_c_p]),
                 "txl_set_wait_limit_ns": (_c_u64, [_c_u64]),
                 "txl_debug_wait_timeout": (_c_int, [_c_u64, _c_p]),
@@ -395,6 +431,192 @@ def kv_window_view(buf, state: KVWindow, L: int, B: int, H: int):
     view (no copy), for relattn_fwd."""
     d = buf.shape[2]
     return buf.view(B, H, state.capacity, d)[:, :, state.start:state.start + state.fill + L]
+
+
+class PagedKV:
+    """Keys and values of the memory in pages (txl_paged_kv), for sequences whose
+    lengths differ and advance on the device.
+
+    pool [2 * layers, n_pages, H, page_rows, 64] (bf16 or fp32): planes 2l and
+    2l + 1 hold layer l's keys and values.  table [B, slots] int32: page ids; a
+    sequence's table rows 0 .. slots * page_rows - 1 form a ring.  begin, fill [B]
+    int32: table row of its oldest memory row, and how many it holds (both zero
+    when omitted).  Holds the tensors, of which the calls below read and write
+    the contents; all on one device."""
+
+    def __init__(self, pool, table, begin=None, fill=None):
+        if pool.dim() != 5 or pool.shape[0] % 2 or pool.shape[0] == 0:
+            raise ValueError("pool must be [2 * layers, n_pages, H, page_rows, 64]")
+        if table.dim() != 2:
+            raise ValueError("table must be [B, slots]")
+        B = table.shape[0]
+        zeros = lambda: torch.zeros(B, dtype=torch.int32, device=pool.device)
+        self.pool, self.table = pool, table
+        self.begin = zeros() if begin is None else begin
+        self.fill = zeros() if fill is None else fill
+        self.ticket = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self.layers, self.B, self.slots = pool.shape[0] // 2, B, table.shape[1]
+        self.n_pages, self.H, self.page_rows = pool.shape[1:4]
+        ints = [(table, "table"), (self.begin, "begin"), (self.fill, "fill")]
+        for t, name in ints[1:]:
+            if tuple(t.shape) != (B,):
+                raise ValueError(f"{name} must be [B]")
+        _same_device(pool, *(t for t, _ in ints))
+        self._c = _PagedKV(_dev(pool, "pool"), *(_dev(t, n, torch.int32) for t, n in ints),
+                           self.ticket.data_ptr(), self.layers, self.n_pages, self.H,
+                           self.page_rows, pool.shape[4], B, self.slots, _code(pool.dtype))
+
+    @property
+    def rows(self) -> int:
+        """Table rows of a sequence: the most memory rows it can hold."""
+        return self.slots * self.page_rows
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices ({first.device}, {t.device})")
+
+
+def _rows(t, name: str, mem: PagedKV, offset: int = 0):
+    """txl_rows of t [B, H, rows, 64] (any strides, the last dimension dense)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
+    if t.dtype != mem.pool.dtype:
+        raise ValueError(f"{name} must be {mem.pool.dtype}, got {t.dtype}")
+    if t.shape[-4:-2] != (mem.B, mem.H) or t.shape[-1] != mem.pool.shape[4]:
+        raise ValueError(f"{name} must be [B, H, rows, dh] of the memory, got {tuple(t.shape)}")
+    if t.shape[-2] > 0 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Rows(t.data_ptr(), t.stride(-4), t.stride(-3), t.stride(-2))
+
+
+def _counts(n, name: str, B: int):
+    if n is None:
+        return None
+    if tuple(n.shape) != (B,):
+        raise ValueError(f"{name} must be [B]")
+    return _dev(n, name, torch.int32)
+
+
+def _state_out(mem: PagedKV, state_out):
+    if state_out is None:
+        return None, None
+    begin, fill = state_out
+    for t, name in ((begin, "begin"), (fill, "fill")):
+        if tuple(t.shape) != (mem.B,):
+            raise ValueError(f"state_out: {name} must be [B]")
+    _same_device(mem.pool, begin, fill)
+    return _dev(begin, "begin", torch.int32), _dev(fill, "fill", torch.int32)
+
+
+def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
+                 keep: int | None = None, state_out=None, stream=None):
+    """Put rows of k and v behind the memory's rows, in its pages.
+
+    k, v [B, H, N, 64] for one layer, or [n, B, H, N, 64] for layers layer ..
+    layer + n - 1 (any strides, the last dimension dense).  Sequence b takes
+    n_new[b] rows (int32 on the device; all when omitted): rows 0, 1, ... of k
+    and v, or rows[b, 0], rows[b, 1], ... with rows [B, width] int32 (the accepted
+    nodes of a drafted tree).  With ``keep``, the state is advanced to the
+    newest ``keep`` rows: in ``mem``, or in the tensors ``state_out`` = (begin,
+    fill) instead."""
+    if k.dim() not in (4, 5) or k.shape != v.shape:
+        raise ValueError("k and v must have one shape, [B, H, N, 64] or [n, B, H, N, 64]")
+    if k.dim() == 5 and k.shape[0] > 1 and k.stride(0) != v.stride(0):
+        raise ValueError("k and v must have the same layer stride")
+    ck, cv = _rows(k, "k", mem), _rows(v, "v", mem)
+    _same_device(mem.pool, k, v, n_new, rows)
+    n_layers = k.shape[0] if k.dim() == 5 else 1
+    N = k.shape[-2]
+    if rows is not None and (rows.dim() != 2 or rows.shape[0] != mem.B):
+        raise ValueError("rows must be [B, width]")
+    if state_out is not None and keep is None:
+        raise ValueError("state_out needs keep")
+    if keep is not None and state_out is None:
+        state_out = (mem.begin, mem.fill)
+    b_out, f_out = _state_out(mem, state_out)
+    with torch.cuda.device(mem.pool.device):
+        _check(lib().txl_paged_append(
+            ctypes.byref(mem._c), int(layer), int(n_layers), ctypes.byref(ck), ctypes.byref(cv),
+            int(k.stride(0)) if k.dim() == 5 else 0, int(N),
+            _dev(rows, "rows", torch.int32) if rows is not None else None,
+            int(rows.shape[1]) if rows is not None else 0, _counts(n_new, "n_new", mem.B),
+            int(rows.shape[1]) if rows is not None else int(N), int(keep or 0), b_out, f_out,
+            _stream(mem.pool, stream)), "txl_paged_append")
+    return mem
+
+
+def paged_advance(mem: PagedKV, n, *, keep: int, state_out=None, stream=None):
+    """Advance the state of rows appended without ``keep`` (layer by layer):
+    sequence b has n[b] new rows (int32 on the device), or n each (an int), and keeps
+    its newest ``keep`` rows.  Written to ``mem``, or to ``state_out``."""
+    counts = None if isinstance(n, int) else n
+    if counts is not None:
+        _same_device(mem.pool, counts)
+    b_out, f_out = _state_out(mem, (mem.begin, mem.fill) if state_out is None else state_out)
+    with torch.cuda.device(mem.pool.device):
+        _check(lib().txl_paged_advance(
+            ctypes.byref(mem._c), _counts(counts, "n", mem.B),
+            int(n) if counts is None else mem.rows, int(keep), b_out, f_out,
+            _stream(mem.pool, stream)), "txl_paged_advance")
+    return mem
+
+
+def paged_copy(mem: PagedKV, src, dst, *, stream=None):
+    """Copy pages src[i] to pages dst[i] (int32 on the device) in every plane of the
+    pool.  No page may be a destination twice, or a source and a destination."""
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be one-dimensional and of one length")
+    _same_device(mem.pool, src, dst)
+    with torch.cuda.device(mem.pool.device):
+        _check(lib().txl_paged_copy(ctypes.byref(mem._c), _dev(src, "src", torch.int32),
+                                    _dev(dst, "dst", torch.int32), int(src.numel()),
+                                    _stream(mem.pool, stream)), "txl_paged_copy")
+    return mem
+
+
+class PagePool:
+    """Host-side accounting of a pool's pages (txl_page_pool): which are free,
+    and how many sequences use each."""
+
+    def __init__(self, n_pages: int):
+        n = int(n_pages)
+        self._arrays = ((ctypes.c_int * max(n, 1))(), (ctypes.c_int * max(n, 1))())
+        self._c = _PagePool()
+        _check(lib().txl_page_pool_init(ctypes.byref(self._c), n, *self._arrays),
+               "txl_page_pool_init")
+
+    @property
+    def n_free(self) -> int:
+        return self._c.n_free
+
+    def users(self, page: int) -> int:
+        if not 0 <= page < self._c.n_pages:
+            raise IndexError(page)
+        return self._arrays[1][page]
+
+    def alloc(self, n: int) -> list[int]:
+        """n pages with one user each; raises TxlError when fewer are free."""
+        out = (ctypes.c_int * max(int(n), 1))()
+        _check(lib().txl_page_pool_alloc(ctypes.byref(self._c), out, int(n)), "txl_page_pool_alloc")
+        return list(out[:int(n)])
+
+    def retain(self, pages):
+        """One user more for each page (a fork shares it)."""
+        ids = (ctypes.c_int * max(len(pages), 1))(*pages)
+        _check(lib().txl_page_pool_retain(ctypes.byref(self._c), ids, len(pages)),
+               "txl_page_pool_retain")
+
+    def release(self, pages) -> int:
+        """One user less for each page; returns how many became free."""
+        ids = (ctypes.c_int * max(len(pages), 1))(*pages)
+        freed = ctypes.c_int(0)
+        _check(lib().txl_page_pool_release(ctypes.byref(self._c), ids, len(pages),
+                                           ctypes.byref(freed)), "txl_page_pool_release")
+        return freed.value
 
 
 def device_status(stream=None) -> int:

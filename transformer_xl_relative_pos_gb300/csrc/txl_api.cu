@@ -12,6 +12,7 @@
 
 #include "kernels.h"
 #include "decode.h"
+#include "paged.h"
 #include "txl.h"
 
 namespace {
@@ -845,4 +846,177 @@ extern "C" int txl_relattn_bwd(const void *q, const void *k, const void *v, cons
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = status;
     return cuda_status(txl::launch_relattn_bwd(p, as_stream(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Paged memory, and the attention of drafted trees that reads it.
+// ---------------------------------------------------------------------------
+namespace {
+
+int elem_size(int dtype) { return dtype == TXL_F32 ? 4 : 2; }
+
+// The struct's own fields (not what its pointers hold, which is on the device).
+int check_paged(const txl_paged_kv *m)
+{
+    if (!m || !m->pool || !m->table || !m->begin || !m->fill) return TXL_ERR_INVALID_ARG;
+    if (m->layers < 1 || m->n_pages < 1 || m->H < 1 || m->page_rows < 1 || m->dh < 1 || m->B < 1 ||
+        m->slots < 1)
+        return TXL_ERR_INVALID_ARG;
+    if (m->dtype != TXL_F32 && m->dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
+    if (m->dh != 64 || m->page_rows % txl::kPageRowUnit != 0) return TXL_ERR_UNSUPPORTED;
+    // table rows (twice, for sums of two) and page planes are counted in ints
+    if ((long long)m->slots * m->page_rows > 0x3fffffffLL ||
+        (long long)m->n_pages * m->H > 0x7ffffffeLL || m->B > 65535 || 2LL * m->layers > 65535)
+        return TXL_ERR_UNSUPPORTED;
+    if (!aligned(m->pool, 16)) return TXL_ERR_MISALIGNED;
+    for (const void *p : {(const void *)m->table, (const void *)m->begin, (const void *)m->fill})
+        if (!aligned(p, 4)) return TXL_ERR_MISALIGNED;
+    return TXL_OK;
+}
+
+// Strides of the dimensions that have more than one entry.
+int check_rows(const txl_rows *x, int B, int H, int N, int dtype)
+{
+    if (!x || !x->ptr) return TXL_ERR_INVALID_ARG;
+    if (!aligned(x->ptr, 16)) return TXL_ERR_MISALIGNED;
+    const int unit = 16 / elem_size(dtype);
+    const long long stride[3] = {x->stride_b, x->stride_h, x->stride_row};
+    const int count[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i) {
+        if (count[i] <= 1) continue;
+        if (stride[i] < 1) return TXL_ERR_INVALID_ARG;
+        if (stride[i] % unit != 0) return TXL_ERR_MISALIGNED;
+    }
+    return TXL_OK;
+}
+
+txl::RowsView rows_view(const txl_rows *x) { return {x->ptr, x->stride_b, x->stride_h, x->stride_row}; }
+
+txl::PagedView paged_view(const txl_paged_kv *m)
+{
+    return {m->table, m->begin, m->fill, m->n_pages, m->H, m->page_rows, m->slots, m->B,
+            m->slots * m->page_rows};
+}
+
+// begin_out / fill_out against the state: separate, or the very same arrays
+// (*in_place); arrays that overlap in part, or each other, are refused.
+int check_state_out(const txl_paged_kv *m, const int *begin_out, const int *fill_out, bool *in_place)
+{
+    *in_place = false;
+    if (!begin_out && !fill_out) return TXL_OK;
+    if (!begin_out || !fill_out) return TXL_ERR_INVALID_ARG;
+    if (!aligned(begin_out, 4) || !aligned(fill_out, 4)) return TXL_ERR_MISALIGNED;
+    const auto overlap = [m](const int *a, const int *b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return (x < y ? y - x : x - y) < (uintptr_t)m->B * sizeof(int);
+    };
+    if (overlap(begin_out, fill_out)) return TXL_ERR_INVALID_ARG;
+    for (const int *o : {begin_out, (const int *)fill_out})
+        for (const int *i : {(const int *)m->begin, (const int *)m->fill}) {
+            if (!overlap(o, i)) continue;
+            if (o != i) return TXL_ERR_INVALID_ARG;
+            *in_place = true;
+        }
+    return TXL_OK;
+}
+
+} // namespace
+
+extern "C" int txl_paged_append(const txl_paged_kv *mem, int layer0, int n_layers,
+                                const txl_rows *k, const txl_rows *v, long long layer_stride,
+                                int N, const int *rows, int rows_stride, const int *n_new,
+                                int max_rows, int keep, int *begin_out, int *fill_out,
+                                void *stream)
+{
+    int rc = check_paged(mem);
+    if (rc != TXL_OK) return rc;
+    if (layer0 < 0 || n_layers < 1 || N < 0 || max_rows < 0 || keep < 0) return TXL_ERR_INVALID_ARG;
+    if ((long long)layer0 + n_layers > mem->layers) return TXL_ERR_SHAPE;
+    if (!rows && max_rows > N) return TXL_ERR_SHAPE;
+    if (rows && (rows_stride < max_rows)) return TXL_ERR_SHAPE;
+    if (rows && !aligned(rows, 4)) return TXL_ERR_MISALIGNED;
+    if (n_new && !aligned(n_new, 4)) return TXL_ERR_MISALIGNED;
+    bool in_place = false;
+    if ((rc = check_state_out(mem, begin_out, fill_out, &in_place)) != TXL_OK) return rc;
+    if (begin_out && keep > mem->slots * mem->page_rows) return TXL_ERR_SHAPE;
+    if (in_place && !mem->ticket) return TXL_ERR_INVALID_ARG;
+    if (in_place && !aligned(mem->ticket, 4)) return TXL_ERR_MISALIGNED;
+    if (max_rows > 0 && N < 1) return TXL_ERR_SHAPE;
+    if (max_rows == 0)  // no new rows: at most the state moves (a smaller keep)
+        return begin_out ? txl_paged_advance(mem, nullptr, 0, keep, begin_out, fill_out, stream)
+                         : TXL_OK;
+    if ((rc = check_rows(k, mem->B, mem->H, N, mem->dtype)) != TXL_OK) return rc;
+    if ((rc = check_rows(v, mem->B, mem->H, N, mem->dtype)) != TXL_OK) return rc;
+    if (n_layers > 1 && layer_stride < 1) return TXL_ERR_INVALID_ARG;
+    if (n_layers > 1 && layer_stride % (16 / elem_size(mem->dtype)) != 0) return TXL_ERR_MISALIGNED;
+    // blocks are counted in an int (the ticket), a block's rows times heads times vectors too
+    if ((long long)((max_rows + 31LL) / 32) * mem->B * 2 * n_layers > 0x7fffffffLL ||
+        mem->H > (1 << 20))
+        return TXL_ERR_UNSUPPORTED;
+    cudaError_t err;
+    unsigned int *status = status_word(&err);
+    if (!status) return TXL_ERR_CUDA;
+    txl::AppendParams p{};
+    p.mem = paged_view(mem);
+    p.pool = mem->pool;
+    p.k = rows_view(k);
+    p.v = rows_view(v);
+    p.layer_stride = layer_stride;
+    p.layer0 = layer0;
+    p.n_layers = n_layers;
+    p.N = N;
+    p.esize = elem_size(mem->dtype);
+    p.rows = rows;
+    p.rows_stride = rows_stride;
+    p.n_new = n_new;
+    p.max_rows = max_rows;
+    p.keep = keep;
+    p.begin_out = begin_out;
+    p.fill_out = fill_out;
+    p.ticket = in_place ? mem->ticket : nullptr;
+    p.status = status;
+    return cuda_status(txl::launch_paged_append(p, as_stream(stream)));
+}
+
+extern "C" int txl_paged_advance(const txl_paged_kv *mem, const int *n_new, int max_rows, int keep,
+                                 int *begin_out, int *fill_out, void *stream)
+{
+    int rc = check_paged(mem);
+    if (rc != TXL_OK) return rc;
+    if (max_rows < 0 || keep < 0 || !begin_out || !fill_out) return TXL_ERR_INVALID_ARG;
+    if (n_new && !aligned(n_new, 4)) return TXL_ERR_MISALIGNED;
+    bool in_place = false;
+    if ((rc = check_state_out(mem, begin_out, fill_out, &in_place)) != TXL_OK) return rc;
+    if (keep > mem->slots * mem->page_rows) return TXL_ERR_SHAPE;
+    cudaError_t err;
+    unsigned int *status = status_word(&err);
+    if (!status) return TXL_ERR_CUDA;
+    txl::AppendParams p{};
+    p.mem = paged_view(mem);
+    p.n_new = n_new;
+    p.max_rows = max_rows;
+    p.keep = keep;
+    p.begin_out = begin_out;
+    p.fill_out = fill_out;
+    p.status = status;
+    return cuda_status(txl::launch_paged_advance(p, as_stream(stream)));
+}
+
+extern "C" int txl_paged_copy(const txl_paged_kv *mem, const int *src, const int *dst, int n,
+                              void *stream)
+{
+    const int rc = check_paged(mem);
+    if (rc != TXL_OK) return rc;
+    if (n < 0) return TXL_ERR_INVALID_ARG;
+    if (n == 0) return TXL_OK;
+    if (!src || !dst) return TXL_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return TXL_ERR_MISALIGNED;
+    const long long page_vec =
+        (long long)mem->H * mem->page_rows * mem->dh * elem_size(mem->dtype) / 16;
+    if ((page_vec / 2048 + 1) * n > 0x7fffffffLL) return TXL_ERR_UNSUPPORTED;
+    cudaError_t err;
+    unsigned int *status = status_word(&err);
+    if (!status) return TXL_ERR_CUDA;
+    return cuda_status(txl::launch_paged_copy(mem->pool, 2 * mem->layers, mem->n_pages, page_vec,
+                                              src, dst, n, status, as_stream(stream)));
 }
