@@ -515,6 +515,45 @@ int txl_page_pool_retain(txl_page_pool *p, const int *pages, int n);
 int txl_page_pool_release(txl_page_pool *p, const int *pages, int n, int *n_freed);
 
 /*
+ * txl_relattn_tree_fwd - relative-position attention (§3.3) of a tree of
+ * drafted tokens over a paged memory: the verification step of speculative
+ * decoding, and with a chain of nodes (each the parent of the next) or a single
+ * node an ordinary decoding step.  Node i of sequence b has parent parents[b][i]
+ * in [0, i), or none (-1: it follows the memory directly; any other value is
+ * taken as -1 and records TXL_ERR_INDEX).  Its depth d_i is 0 without a parent,
+ * else its parent's plus one.  With F = fill[b] memory rows, for node i < n_b:
+ *   memory row t   distance F + d_i - t
+ *   node a         distance d_i - d_a, visible when a is i or an ancestor of i
+ *   A_ij = scale * ((q_i + u).k_j + (q_i + v_bias).r[r_rows - 1 - distance])
+ *   out_i = sum_j softmax_j(A_i.) v_j,  lse_i = log sum_j exp(A_ij)
+ * over the visible nodes and memory rows whose distance is below r_rows (a
+ * memory longer than the table is attended to as far as the table goes).
+ *
+ *   q, out        [B][H][N][dh]    (strided; out must not overlap the inputs)
+ *   k_new, v_new  [B][H][N][dh]    the nodes' keys and values
+ *   mem, layer    the memory and the layer of it to read; nothing is written
+ *   r             [H][r_rows][dh] dense, u, v_bias [H][dh]; as txl_relattn_fwd
+ *   parents       device [B], parents_stride ints apart (0: one tree for all)
+ *   n_nodes       device [B], values taken into [0, N]; NULL: N
+ *   lse           [B][H][N] fp32 or NULL
+ * Rows i >= n_b of out and lse are left as they were; those rows of q, k_new and
+ * v_new, and what the pages hold outside the memory rows, have no influence.
+ * All of mem->dtype.  TXL_BF16: products on the tensor cores, fp32 sums; the
+ * probabilities enter as bf16 pairs (value and residual).  TXL_F32: fp32
+ * arithmetic.  1 <= N <= 64, dh = 64.
+ * n_splits: key ranges per (b, h), merged inside a thread-block cluster: 0 lets
+ * the library choose, at most 8 (larger requests are refused).  No workspace.
+ * Errors: TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED (N > 64, dh, page_rows, dtype,
+ * n_splits > 8, sizes past the grid limits), TXL_ERR_MISALIGNED, TXL_ERR_SHAPE
+ * (layer not in the pool, r_rows < 1), TXL_ERR_CUDA.
+ */
+int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new, const txl_rows *v_new,
+                         const txl_paged_kv *mem, int layer, const void *r, int r_rows,
+                         const void *u, const void *v_bias, const int *parents,
+                         long long parents_stride, const int *n_nodes, const txl_rows *out,
+                         float *lse, int N, float scale, int n_splits, void *stream);
+
+/*
  * txl_device_status - synchronise `stream`, then read and clear the device
  * status word in which kernels record barrier time-outs (and, in a debug
  * build, failed index checks).  Returns TXL_OK, TXL_ERR_TIMEOUT (a time-out was

@@ -154,3 +154,32 @@ def test_page_pool_refusals_change_nothing():
     L = txl.lib()
     assert L.txl_page_pool_init(None, 1, None, None) == INVALID
     assert L.txl_page_pool_alloc(None, None, 0) == INVALID
+
+
+def tree_call(mem=None, q=None, k=None, v=None, out=None, layer=0, r=1 << 16, r_rows=8, u=1 << 16,
+              vb=1 << 16, parents=4096, stride=8, n=None, lse=None, N=8, scale=0.125, n_splits=0):
+    ref = ctypes.byref
+    return txl.lib().txl_relattn_tree_fwd(ref(q or rows()), ref(k or rows()), ref(v or rows()),
+                                          ref(mem or kv()), layer, r, r_rows, u, vb, parents, stride, n,
+                                          ref(out or rows()), lse, N, scale, n_splits, None)
+
+
+@pytest.mark.parametrize("kw,want", BAD_KV)
+def test_tree_refuses_a_bad_memory(kw, want):
+    assert tree_call(mem=kv(**kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(r=None), INVALID), (dict(u=None), INVALID), (dict(vb=None), INVALID),
+    (dict(parents=None), INVALID), (dict(N=0), INVALID), (dict(layer=-1), INVALID),
+    (dict(n_splits=-1), INVALID), (dict(stride=-1), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(layer=2), SHAPE), (dict(r_rows=0), SHAPE), (dict(stride=7), SHAPE),
+    (dict(N=65, stride=65), UNSUPPORTED), (dict(n_splits=9), UNSUPPORTED),
+    (dict(r_rows=1 << 30), UNSUPPORTED),
+    (dict(r=(1 << 16) + 8), MISALIGNED), (dict(u=(1 << 16) + 2), MISALIGNED),
+    (dict(parents=4098), MISALIGNED), (dict(n=4098), MISALIGNED), (dict(lse=4098), MISALIGNED),
+    (dict(q=rows(ptr=None)), INVALID), (dict(out=rows(ptr=None)), INVALID),
+    (dict(k=rows(ptr=8)), MISALIGNED), (dict(v=rows(sr=4)), MISALIGNED), (dict(out=rows(sh=0)), INVALID),
+])
+def test_tree_refusals(kw, want):
+    assert tree_call(**kw) == want

@@ -22,6 +22,7 @@ N-layer summary, Appendix B reversed table and shift):
   PagedKV, paged_* keys and values of the memory in pages, for sequences whose
                   lengths differ: rows appended (a segment's, or the accepted
                   nodes of a drafted tree), the state advanced, pages copied
+  relattn_tree_fwd  attention of a tree of drafted tokens over that memory
   PagePool        host-side accounting of those pages (free, shared)
   relattn_bwd     gradients of relattn_fwd for one segment (training within a
                   segment, the memory SG(m))
@@ -58,6 +59,7 @@ from ._lib import (  # noqa: F401
     relattn_fwd,
     relattn_fwd_noalloc,
     relattn_plan,
+    relattn_tree_fwd,
     set_wait_limit_ns,
     status_string,
     version,

@@ -139,6 +139,11 @@ def lib():
                 "txl_paged_advance": (_c_int, [ctypes.POINTER(_PagedKV), _c_p, _c_int, _c_int,
                                                _c_p, _c_p, _c_p]),
                 "txl_paged_copy": (_c_int, [ctypes.POINTER(_PagedKV), _c_p, _c_p, _c_int, _c_p]),
+                "txl_relattn_tree_fwd": (_c_int, [ctypes.POINTER(_Rows)] * 3 +
+                                         [ctypes.POINTER(_PagedKV), _c_int, _c_p, _c_int, _c_p,
+                                          _c_p, _c_p, ctypes.c_longlong, _c_p,
+                                          ctypes.POINTER(_Rows), _c_p, _c_int, _c_float, _c_int,
+                                          _c_p]),
                 "txl_page_pool_init": (_c_int, [ctypes.POINTER(_PagePool), _c_int, _c_ip, _c_ip]),
                 "txl_page_pool_alloc": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
                 "txl_page_pool_retain": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
@@ -576,6 +581,53 @@ def paged_copy(mem: PagedKV, src, dst, *, stream=None):
                                     _dev(dst, "dst", torch.int32), int(src.numel()),
                                     _stream(mem.pool, stream)), "txl_paged_copy")
     return mem
+
+
+def relattn_tree_fwd(q, k_new, v_new, mem: PagedKV, layer: int, r, u, v_bias, parents, scale: float,
+                     *, n_nodes=None, out=None, lse=None, n_splits: int = 0, stream=None):
+    """Relative-position attention of a tree of drafted tokens over layer ``layer``
+    of a paged memory: node i attends to the memory's rows, to its ancestors and to
+    itself, at the distances its depth gives.
+
+    q, k_new, v_new [B, H, N, 64], N <= 64 (any strides, the last dimension dense);
+    parents [B, N] (or [N], one tree for all) int32 on the device: an earlier node,
+    or -1; r, u, v_bias as for :func:`relattn_fwd`, r [H, r_rows, 64] being
+    attended as far as it goes; all of the memory's dtype (bf16 or fp32).
+    n_nodes [B] int32: nodes of each sequence (all N when omitted); the rows of
+    out and lse behind them are left as they were.  ``out``: a tensor to fill
+    ([B, H, N, 64], any strides); ``lse``: True, or a tensor [B, H, N] fp32.
+    Returns ``out`` or ``(out, lse)``."""
+    if out is None:
+        # (zeros: rows behind n_nodes are not written)
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    want_lse = lse is not None and lse is not False
+    if lse is True:
+        lse = torch.zeros(q.shape[:3], dtype=torch.float32, device=q.device)
+    if not (q.dim() == 4 and q.shape == k_new.shape == v_new.shape == out.shape):
+        raise ValueError("q, k_new, v_new and out must have one shape, [B, H, N, 64]")
+    if want_lse and lse.shape != q.shape[:3]:
+        raise ValueError("lse must be [B, H, N]")
+    B, H, N, dh = q.shape
+    dt = mem.pool.dtype
+    if r.dim() != 3 or r.shape[0] != H or r.shape[2] != dh:
+        raise ValueError("r must be [H, r_rows, 64]")
+    if tuple(u.shape) != (H, dh) or tuple(v_bias.shape) != (H, dh):
+        raise ValueError("u and v_bias must be [H, 64]")
+    if tuple(parents.shape) not in ((B, N), (N,)):
+        raise ValueError("parents must be [B, N] or [N]")
+    _same_device(mem.pool, q, k_new, v_new, r, u, v_bias, parents, n_nodes, out,
+                 lse if want_lse else None)
+    cq, ck, cv, co = (_rows(t, name, mem) for t, name in
+                      ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out")))
+    with torch.cuda.device(mem.pool.device):
+        _check(lib().txl_relattn_tree_fwd(
+            ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv), ctypes.byref(mem._c), int(layer),
+            _dev(r, "r", dt), int(r.shape[1]), _dev(u, "u", dt), _dev(v_bias, "v_bias", dt),
+            _dev(parents, "parents", torch.int32), N if parents.dim() == 2 else 0,
+            _counts(n_nodes, "n_nodes", B), ctypes.byref(co),
+            _dev(lse, "lse", torch.float32) if want_lse else None, int(N), float(scale),
+            int(n_splits), _stream(mem.pool, stream)), "txl_relattn_tree_fwd")
+    return (out, lse) if want_lse else out
 
 
 class PagePool:

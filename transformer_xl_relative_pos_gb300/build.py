@@ -25,9 +25,11 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libtxl_gb300_debug.so")
 
 SOURCES = ["txl_api.cu", "relattn_tc.cu", "relattn_combine.cu", "relattn_decode.cu",
            "relattn_decode_mma.cu", "relattn_f32.cu", "relpos.cu", "mem.cu", "relattn_noalloc.cu",
-           "project.cu", "relattn_bwd.cu", "paged.cu", "page_pool.cu"]
+           "project.cu", "relattn_bwd.cu", "paged.cu", "page_pool.cu",
+           "relattn_tree.cu", "relattn_tree_f32.cu"]
 HEADERS = [os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "decode.h"),
            os.path.join(CSRC, "decode_common.cuh"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "paged.h"),
+           os.path.join(CSRC, "tree_common.cuh"),
            os.path.join(INCLUDE, "txl.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -82,7 +82,6 @@ struct TreeParams {
 // over the table [H][r_rows][64], all in boxes of 32 rows, 128-byte swizzle.
 cudaError_t launch_relattn_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                 const CUtensorMap &tm_r, const TreeParams &p, cudaStream_t s);
-int tree_blocks_per_sm(int N);
 cudaError_t launch_relattn_tree_f32(const TreeParams &p, cudaStream_t s);
 
 } // namespace txl

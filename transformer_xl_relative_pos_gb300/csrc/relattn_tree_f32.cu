@@ -1,0 +1,277 @@
+// Relative-position attention of a tree of drafted tokens over a paged memory in
+// fp32 on the CUDA cores (FFMA, no TF32): the exact path, as relattn_f32.cu is for
+// dense segments.  "Transformer-XL: Attentive Language Models Beyond a Fixed-Length
+// Context", §3.3 score, Appendix B reversed table; the shift by the nodes' depths
+// and the split of the keys are those of relattn_tree.cu.
+//
+// Per key, head and node it computes 3 x 64 multiply-adds; reading 512 bytes of k
+// and v for them, it is bound by those products from a few nodes on.  Each row that
+// many products share sits in registers, the other operand comes from shared
+// memory four floats at a time:
+//   scores   lane = key: the lane's k row (then its table row) against the warp's
+//            nodes, whose q + u (q + v) every lane reads alike
+//   P.V      lane = two dimensions of 32 value rows, against the probabilities,
+//            which every lane reads alike
+#include "tree_common.cuh"
+
+namespace txl {
+namespace {
+
+using namespace tree;
+
+template <int MT>
+struct CfgF32 {
+    static constexpr int DCAP = 16 * MT;       // depths are below this
+    static constexpr int RW = GK + DCAP;       // columns of the product ring
+    static constexpr int Q = MT * 2 * 16 * DH; // floats: q + u, q + v of the nodes
+    static constexpr int WARP = 16 * RW + 16 * GK;  // floats per warp: ring, probabilities
+    static constexpr int OFF_WARP = Q * 4;
+    static constexpr int OFF_TOPO = OFF_WARP + WARPS * WARP * 4;
+    static constexpr int SMEM = OFF_TOPO + (int)sizeof(Topology);
+    static_assert(sizeof(Rec) <= WARP * 4, "a warp's record fits over its ring");
+    static_assert(OFF_TOPO % 16 == 0 && OFF_WARP % 16 == 0 && (WARP * 4) % 16 == 0, "alignment");
+};
+
+template <int MT>
+__global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const TreeParams p)
+{
+    using C = CfgF32<MT>;
+    constexpr int KG = WARPS / MT, DCAP = C::DCAP, RW = C::RW;
+    extern __shared__ __align__(16) uint8_t smem_f32[];
+    uint8_t *smem = smem_f32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int mt = warp % MT, kg = warp / MT;
+    const int split = blockIdx.x % p.n_splits;
+    const int bh = blockIdx.x / p.n_splits;
+    const int b = bh / p.mem.H, h = bh - b * p.mem.H;
+    const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
+    if (n == 0) return;  // (every block of the cluster)
+
+    float *qs = reinterpret_cast<float *>(smem);
+    float *ring = reinterpret_cast<float *>(smem + C::OFF_WARP) + warp * C::WARP;
+    float *prob = ring + 16 * RW;
+    Topology &topo = *reinterpret_cast<Topology *>(smem + C::OFF_TOPO);
+
+    // q + u and q + v of the nodes (those past n: zero)
+    for (int e = threadIdx.x; e < MT * 16 * DH; e += WARPS * 32) {
+        const int i = e / DH, c = e % DH;
+        const float *q = static_cast<const float *>(p.q.ptr) + b * p.q.sb + h * p.q.sh + i * p.q.sr;
+        const float x = i < n ? q[c] : 0.f;
+        float *dst = qs + (i / 16) * (2 * 16 * DH) + (i % 16) * DH + c;
+        dst[0] = x + static_cast<const float *>(p.u)[h * DH + c];
+        dst[16 * DH] = x + static_cast<const float *>(p.vb)[h * DH + c];
+    }
+    build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
+
+    int begin, fill;
+    paged_state(p.mem, b, p.status, begin, fill);
+    const Chunks ck = group_chunks(p, begin, fill, split * KG + kg, p.n_splits * KG);
+    const int rows = min(16, n - mt * 16);  // this warp's nodes (none: <= 0)
+    const float4 *qu = reinterpret_cast<const float4 *>(qs + mt * (2 * 16 * DH));
+    const float4 *qv = qu + 16 * DH / 4;
+    const float *table = static_cast<const float *>(p.r) + (long long)h * p.r_rows * DH;
+
+    float m[16], l[16], acc[16][2];  // l: this lane's keys only
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        m[i] = -INFINITY;
+        l[i] = acc[i][0] = acc[i][1] = 0.f;
+    }
+    int depth_max = 0;
+    for (int i = 0; i < rows; ++i) depth_max = max(depth_max, topo.depth[mt * 16 + i]);
+
+    // dot products of the warp's nodes with one row per lane (null: zero)
+    auto dots = [&](const float *row, const float4 *q, float (&out)[16]) {
+        float4 x[DH / 4];
+#pragma unroll
+        for (int c = 0; c < DH / 4; ++c)
+            x[c] = row ? __ldg(reinterpret_cast<const float4 *>(row) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i >= rows) break;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < DH / 4; ++c) {
+                const float4 a = q[i * (DH / 4) + c];
+                s0 = fmaf(a.x, x[c].x, s0);
+                s1 = fmaf(a.y, x[c].y, s1);
+                s0 = fmaf(a.z, x[c].z, s0);
+                s1 = fmaf(a.w, x[c].w, s1);
+            }
+            out[i] = s0 + s1;
+        }
+    };
+    // (q + v).r of table row `row` into ring column col (below RW), when keep
+    auto table_dots = [&](int row, int col, bool keep) {
+        float c[16];
+        dots(row >= 0 && row < p.r_rows ? table + (long long)row * DH : nullptr, qv, c);
+        TXL_CHECK(!keep || (col >= 0 && col < RW), p.status);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < rows && keep) ring[i * RW + col] = c[i];
+    };
+    // Masked scores (log2 units) of this lane's key into the running softmax, then
+    // P.V over the chunk's value rows.  value(key): the row, or null (zero).  mixed: keys
+    // may be hidden from some nodes only (bit i of this lane's `hidden`); the value,
+    // which may be an infinity or NaN, then must not reach them.
+    auto step = [&](float (&s)[16], bool mixed, unsigned hidden, auto &&value) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i >= rows) break;
+            float mx = s[i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = max_nan(mx, m[i]);
+            if (!(mx == m[i])) {
+                const float f = m[i] == -INFINITY ? 0.f : ex2f(m[i] - mx);
+                m[i] = mx;
+                l[i] *= f;
+                acc[i][0] *= f;
+                acc[i][1] *= f;
+            }
+            const float e = s[i] == -INFINITY ? 0.f : ex2f(s[i] - mx);
+            l[i] += e;
+            prob[i * GK + lane] = (hidden >> i) & 1 ? -1.f : e;
+        }
+        float2 v[GK];
+#pragma unroll
+        for (int key = 0; key < GK; ++key) {
+            const float *row = value(key);
+            v[key] = row ? __ldg(reinterpret_cast<const float2 *>(row) + lane) : make_float2(0.f, 0.f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i >= rows) break;
+#pragma unroll
+            for (int c = 0; c < GK / 4; ++c) {
+                const float4 e = *reinterpret_cast<const float4 *>(prob + i * GK + 4 * c);
+                const float w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (mixed && w[x] < 0.f) continue;
+                    acc[i][0] = fmaf(w[x], v[4 * c + x].x, acc[i][0]);
+                    acc[i][1] = fmaf(w[x], v[4 * c + x].y, acc[i][1]);
+                }
+            }
+        }
+        __syncwarp();
+    };
+
+    if (rows > 0 && split == p.n_splits - 1 && kg == 0) {
+        // ---- the nodes among themselves: distances 0 .. DCAP - 1 ------------------
+        for (int c = 0; c < DCAP; c += 32) table_dots(p.r_rows - DCAP + c + lane, c + lane, c + lane < DCAP);
+        __syncwarp();
+        const float *kn = static_cast<const float *>(p.k.ptr) + b * p.k.sb + h * p.k.sh;
+        const float *vn = static_cast<const float *>(p.v.ptr) + b * p.v.sb + h * p.v.sh;
+        const int a_end = mt * 16 + rows;  // (no node is an ancestor of an earlier one)
+        for (int a0 = 0; a0 < a_end; a0 += GK) {
+            const int a = a0 + lane;
+            float s[16];
+            dots(a < a_end ? kn + a * p.k.sr : nullptr, qu, s);
+            const int da = a < a_end ? topo.depth[a] : 0;
+            unsigned hidden = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (i >= rows) break;
+                const int dist = topo.depth[mt * 16 + i] - da;
+                const bool seen = a < a_end && ((topo.anc[mt * 16 + i] >> a) & 1) && dist < p.r_rows;
+                TXL_CHECK(!seen || (dist >= 0 && dist < DCAP), p.status);
+                hidden |= seen ? 0u : 1u << i;
+                s[i] = seen ? (s[i] + ring[i * RW + DCAP - 1 - dist]) * p.scale_log2 : -INFINITY;
+            }
+            step(s, true, hidden, [&](int key) { return a0 + key < a_end ? vn + (a0 + key) * p.v.sr : nullptr; });
+        }
+    }
+    if (rows > 0 && ck.count > 0)  // the DCAP table rows before the first chunk's
+        for (int c = 0; c < DCAP; c += 32)
+            table_dots(p.r_rows - 1 - fill + ck.c0 * GK - ck.off - DCAP + c + lane, c + lane,
+                       c + lane < DCAP);
+
+    // ---- the memory, chunk by chunk ---------------------------------------------
+    int wpos = DCAP;  // ring column of the chunk's first table row
+    for (int item = 0; item < (rows > 0 ? ck.count : 0); ++item) {
+        const int c = ck.c0 + item, j0 = c * GK - ck.off;
+        int page, row;
+        chunk_place(p.mem, ck, b, c, p.status, page, row);
+        const long long at = page >= 0 ? (((long long)page * p.mem.H + h) * p.mem.P + row) * DH : 0;
+        const float *kp = static_cast<const float *>(p.kpage) + at;
+        const float *vp = static_cast<const float *>(p.vpage) + at;
+        const int key_lo = -j0, key_hi = page >= 0 ? fill - j0 : 0;  // memory rows of the chunk
+        const bool mine = lane >= key_lo && lane < key_hi;
+        float s[16];
+        dots(mine ? kp + lane * DH : nullptr, qu, s);
+        int col = wpos + lane;
+        col -= col >= RW ? RW : 0;
+        table_dots(p.r_rows - 1 - fill + j0 + lane, col, true);
+        __syncwarp();
+        const int reach = fill - p.r_rows - j0;  // depth d sees keys above reach + d
+        const bool mixed = reach + depth_max >= 0;
+        unsigned hidden = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i >= rows) break;
+            const int d = topo.depth[mt * 16 + i];
+            int x = wpos + lane - d;
+            x += x < 0 ? RW : 0;
+            x -= x >= RW ? RW : 0;
+            const bool seen = mine && lane > reach + d;
+            hidden |= mixed && !seen ? 1u << i : 0u;  // (else a missing key's zero value is harmless)
+            s[i] = seen ? (s[i] + ring[i * RW + x]) * p.scale_log2 : -INFINITY;
+        }
+        step(s, mixed, hidden,
+             [&](int key) { return key >= key_lo && key < key_hi ? vp + key * DH : nullptr; });
+        wpos += GK;
+        wpos -= wpos >= RW ? RW : 0;
+    }
+
+    // ---- this warp's record, over its ring ----------------------------------------
+    const auto rec = [smem](int w) {
+        return reinterpret_cast<Rec *>(smem + C::OFF_WARP + w * C::WARP * 4);
+    };
+    __syncwarp();
+    Rec *r = rec(warp);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i >= rows) break;
+        float sum = l[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+            r->m[i] = m[i];
+            r->l[i] = sum;
+        }
+        reinterpret_cast<float2 *>(r->a[i])[lane] = make_float2(acc[i][0], acc[i][1]);
+    }
+    finish<MT, float>(rec, p, b, h, n, warp, lane);
+}
+
+cudaError_t ensure_attr()
+{
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    const auto set = [](auto *k, int bytes) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    if ((e = set(relattn_tree_f32_kernel<1>, CfgF32<1>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_f32_kernel<2>, CfgF32<2>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_f32_kernel<4>, CfgF32<4>::SMEM)) != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return cudaSuccess;
+}
+
+} // namespace
+
+cudaError_t launch_relattn_tree_f32(const TreeParams &p, cudaStream_t s)
+{
+    const cudaError_t e = ensure_attr();
+    if (e != cudaSuccess) return e;
+    if (p.N <= 16) return launch_clusters(relattn_tree_f32_kernel<1>, p, CfgF32<1>::SMEM, s, p);
+    if (p.N <= 32) return launch_clusters(relattn_tree_f32_kernel<2>, p, CfgF32<2>::SMEM, s, p);
+    return launch_clusters(relattn_tree_f32_kernel<4>, p, CfgF32<4>::SMEM, s, p);
+}
+
+} // namespace txl

@@ -1,0 +1,242 @@
+// Device code shared by the two kernels of txl_relattn_tree_fwd (relattn_tree.cu,
+// bf16 on the tensor cores; relattn_tree_f32.cu): the drafted tree's depths and
+// ancestors, the split of a memory's keys, and the merge of the warps' and the
+// blocks' partial results.
+//
+// A block has four warps.  A warp holds 16 of the tree's nodes (node tile mt)
+// and takes a range of the keys (key group kg): with MT node tiles there are
+// 4 / MT key groups.  The blocks of one (batch, head) are a thread-block cluster;
+// its key groups share the memory in contiguous runs of 32-key chunks.
+#pragma once
+
+#include "decode_common.cuh"
+#include "paged.h"
+
+namespace txl {
+namespace tree {
+
+using namespace ptx;
+using decode::cluster_addr;
+using decode::cluster_rank;
+using decode::cluster_sync;
+using decode::ex2f;
+using decode::ld_cluster_f32;
+using decode::ld_cluster_f32x2;
+
+constexpr int DH = kTcDH;  // 64
+constexpr int WARPS = 4;
+constexpr int GK = 32;     // keys per chunk
+
+// max that keeps a NaN: a row with a NaN score gives NaN, as the formula does.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Per node of the block's sequence: depth, and the mask of itself and its ancestors.
+struct Topology {
+    unsigned long long anc[kTreeMaxNodes];
+    int depth[kTreeMaxNodes];
+    int hop[kTreeMaxNodes];
+};
+
+// By pointer doubling: after round r a node knows its 2^r nearest ancestors.  A
+// parent that is not an earlier node counts as none, so there is no cycle.  All
+// threads of the block; ends with a barrier.
+__device__ __forceinline__ void build_topology(Topology &t, const int *parents, int n,
+                                               unsigned int *status)
+{
+    const int i = threadIdx.x;
+    unsigned long long anc = 0;
+    int hop = -1, depth = 0;
+    if (i < n) {
+        hop = parents[i];
+        if (hop < -1 || hop >= i) {
+            atomicOr(status, TXL_STATUS_INDEX);
+            hop = -1;
+        }
+        anc = 1ull << i;
+        depth = hop >= 0 ? 1 : 0;
+    }
+    for (int span = 1; span < n; span *= 2) {
+        if (i < n) {
+            t.anc[i] = anc;
+            t.depth[i] = depth;
+            t.hop[i] = hop;
+        }
+        __syncthreads();
+        if (hop >= 0) {
+            anc |= t.anc[hop];
+            depth += t.depth[hop];
+            hop = t.hop[hop];
+        }
+        __syncthreads();
+    }
+    if (i < n) {
+        t.anc[i] = anc;
+        t.depth[i] = depth;
+    }
+    __syncthreads();
+}
+
+// The chunks of one key group: 32-row chunks of the table ring, aligned to it
+// (so that none crosses a page).  Chunk c holds memory rows 32 c - off .. + 31.
+struct Chunks {
+    int begin, fill;  // the sequence's state
+    int off;          // begin mod 32
+    int c0, count;    // this group's first chunk, and how many
+};
+
+__device__ __forceinline__ Chunks group_chunks(const TreeParams &p, int begin, int fill, int group,
+                                               int groups)
+{
+    Chunks k;
+    k.begin = begin;
+    k.fill = fill;
+    k.off = begin & (GK - 1);
+    // Rows the table reaches from a node of depth 0; deeper ones reach fewer.
+    const int t_lo = max(0, fill - p.r_rows + 1);
+    const int first = (k.off + t_lo) / GK;
+    const int all = fill > t_lo ? (k.off + fill + GK - 1) / GK - first : 0;
+    k.c0 = first + (int)((long long)all * group / groups);
+    k.count = first + (int)((long long)all * (group + 1) / groups) - k.c0;
+    return k;
+}
+
+// Page and row in it of chunk c (its first row; page out of range: -1).
+__device__ __forceinline__ void chunk_place(const PagedView &m, const Chunks &k, int b, int c,
+                                            unsigned int *status, int &page, int &row)
+{
+    int x = k.begin - k.off + c * GK;  // below 2 R
+    x -= x >= m.R ? m.R : 0;
+    const int slot = x / m.P;
+    row = x - slot * m.P;
+    TXL_CHECK(x >= 0 && x < m.R && row % GK == 0, status);
+    page = m.table[(long long)b * m.slots + slot];
+    if (page < 0 || page >= m.n_pages) {
+        atomicOr(status, TXL_STATUS_INDEX);
+        page = -1;
+    }
+}
+
+// One warp's result for its 16 nodes: running maximum (log2 units), sum of
+// probabilities, unnormalised output.
+struct Rec {
+    float m[16];
+    float l[16];
+    float a[16][DH];
+};
+
+__device__ __forceinline__ void put_row(__nv_bfloat16 *dst, int lane, float x, float y)
+{
+    reinterpret_cast<__nv_bfloat162 *>(dst)[lane] = __floats2bfloat162_rn(x, y);
+}
+
+__device__ __forceinline__ void put_row(float *dst, int lane, float x, float y)
+{
+    reinterpret_cast<float2 *>(dst)[lane] = make_float2(x, y);
+}
+
+// Every thread of the block, after each warp wrote its record (warp w's at
+// rec(w), w = kg * MT + mt): merge the key groups of each node, then the blocks
+// of the cluster, whose warps share the nodes; write out and lse of the n nodes.
+template <int MT, typename T, typename RecOf>
+__device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, int h, int n, int warp,
+                                       int lane)
+{
+    constexpr int KG = WARPS / MT;
+    constexpr float LN2 = 0.69314718055994531f;
+    T *out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + b * p.out.sb + h * p.out.sh;
+    float *lse = p.lse ? p.lse + ((long long)b * p.mem.H + h) * p.N : nullptr;
+    __syncthreads();
+    for (int i = warp; i < n; i += WARPS) {
+        const int mt = i / 16, ii = i % 16;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < KG; ++g) mx = max_nan(mx, rec(g * MT + mt)->m[ii]);
+        float ls = 0.f, o0 = 0.f, o1 = 0.f;
+        if (mx != -INFINITY) {
+#pragma unroll
+            for (int g = 0; g < KG; ++g) {
+                const Rec *r = rec(g * MT + mt);
+                if (r->m[ii] == -INFINITY) continue;
+                const float w = ex2f(r->m[ii] - mx);
+                const float2 a = reinterpret_cast<const float2 *>(r->a[ii])[lane];
+                ls += w * r->l[ii];
+                o0 = fmaf(w, a.x, o0);
+                o1 = fmaf(w, a.y, o1);
+            }
+        }
+        const float inv = ls == 0.f ? 0.f : 1.f / ls;
+        const float lse2 = ls == 0.f ? -INFINITY : mx + log2f(ls);
+        if (p.n_splits == 1) {
+            put_row(out + i * p.out.sr, lane, o0 * inv, o1 * inv);
+            if (lse && lane == 0) lse[i] = lse2 * LN2;
+        } else {
+            // this block's normalised partial, in place of key group 0's (each lane
+            // overwrites what it alone has read)
+            Rec *r = rec(mt);
+            reinterpret_cast<float2 *>(r->a[ii])[lane] = make_float2(o0 * inv, o1 * inv);
+            __syncwarp();
+            if (lane == 0) r->m[ii] = lse2;
+        }
+    }
+    if (p.n_splits == 1) return;
+    cluster_sync();
+    for (int i = (int)cluster_rank() * WARPS + warp; i < n; i += WARPS * p.n_splits) {
+        const Rec *r = rec(i / 16);
+        const uint32_t a_lse = smem_u32(&r->m[i % 16]);
+        const uint32_t a_o = smem_u32(&r->a[i % 16][2 * lane]);
+        float part[kTreeMaxCluster];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < kTreeMaxCluster; ++s) {
+            part[s] = s < p.n_splits ? ld_cluster_f32(cluster_addr(a_lse, (uint32_t)s)) : -INFINITY;
+            mx = max_nan(mx, part[s]);
+        }
+        float ws = 0.f, o0 = 0.f, o1 = 0.f;
+        if (mx != -INFINITY) {
+#pragma unroll
+            for (int s = 0; s < kTreeMaxCluster; ++s) {
+                if (part[s] == -INFINITY) continue;
+                const float w = ex2f(part[s] - mx);
+                const float2 o = ld_cluster_f32x2(cluster_addr(a_o, (uint32_t)s));
+                ws += w;
+                o0 = fmaf(w, o.x, o0);
+                o1 = fmaf(w, o.y, o1);
+            }
+        }
+        const float inv = ws == 0.f ? 0.f : 1.f / ws;
+        put_row(out + i * p.out.sr, lane, o0 * inv, o1 * inv);
+        if (lse && lane == 0) lse[i] = ws == 0.f ? -INFINITY : (mx + log2f(ws)) * LN2;
+    }
+    cluster_sync();  // the others have read this block's shared memory
+}
+
+// Launch KERN with one cluster of n_splits blocks per (batch, head).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), const TreeParams &p, int smem, cudaStream_t s,
+                            const Args &...args)
+{
+    const long long blocks = (long long)p.mem.B * p.mem.H * p.n_splits;
+    if (blocks <= 0 || blocks > 0x7fffffffLL || p.n_splits > kTreeMaxCluster)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(WARPS * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.n_splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.n_splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+} // namespace tree
+} // namespace txl

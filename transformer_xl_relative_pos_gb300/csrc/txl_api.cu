@@ -1020,3 +1020,82 @@ extern "C" int txl_paged_copy(const txl_paged_kv *mem, const int *src, const int
     return cuda_status(txl::launch_paged_copy(mem->pool, 2 * mem->layers, mem->n_pages, page_vec,
                                               src, dst, n, status, as_stream(stream)));
 }
+
+namespace {
+
+// Key ranges of a head: the caller's n_splits or, for 0, as many as keep one wave
+// of resident blocks, at most one per 128 table rows (the host does not know the
+// fills) and at most a cluster's worth.
+int tree_splits(long long BH, int table_rows, int n_splits)
+{
+    if (n_splits > 0) return n_splits;
+    const long long slots = 2LL * sm_count();
+    return (int)std::max<long long>(
+        1, std::min<long long>(std::min<long long>(slots / BH, ((long long)table_rows + 127) / 128),
+                               txl::kTreeMaxCluster));
+}
+
+} // namespace
+
+extern "C" int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new,
+                                    const txl_rows *v_new, const txl_paged_kv *mem, int layer,
+                                    const void *r, int r_rows, const void *u, const void *v_bias,
+                                    const int *parents, long long parents_stride,
+                                    const int *n_nodes, const txl_rows *out, float *lse, int N,
+                                    float scale, int n_splits, void *stream)
+{
+    int rc = check_paged(mem);
+    if (rc != TXL_OK) return rc;
+    if (!r || !u || !v_bias || !parents) return TXL_ERR_INVALID_ARG;
+    if (N < 1 || n_splits < 0 || parents_stride < 0 || layer < 0) return TXL_ERR_INVALID_ARG;
+    if (!(scale == scale)) return TXL_ERR_INVALID_ARG;  // NaN
+    if (layer >= mem->layers || r_rows < 1) return TXL_ERR_SHAPE;
+    if (N > txl::kTreeMaxNodes || n_splits > txl::kTreeMaxCluster || r_rows > 0x3fffffff)
+        return TXL_ERR_UNSUPPORTED;
+    if (parents_stride > 0 && parents_stride < N && mem->B > 1) return TXL_ERR_SHAPE;
+    for (const txl_rows *x : {q, k_new, v_new, out})
+        if ((rc = check_rows(x, mem->B, mem->H, N, mem->dtype)) != TXL_OK) return rc;
+    for (const void *p : {r, u, v_bias})
+        if (!aligned(p, 16)) return TXL_ERR_MISALIGNED;
+    for (const void *p : {(const void *)parents, (const void *)n_nodes, (const void *)lse})
+        if (!aligned(p, 4)) return TXL_ERR_MISALIGNED;
+    const long long BH = (long long)mem->B * mem->H;
+    const int splits = tree_splits(BH, mem->slots * mem->page_rows, n_splits);
+    if (BH * splits > 0x7fffffffLL) return TXL_ERR_UNSUPPORTED;
+    cudaError_t err;
+    unsigned int *status = status_word(&err);
+    if (!status) return TXL_ERR_CUDA;
+
+    txl::TreeParams p{};
+    p.mem = paged_view(mem);
+    p.q = rows_view(q);
+    p.k = rows_view(k_new);
+    p.v = rows_view(v_new);
+    p.out = rows_view(out);
+    p.r = r;
+    p.u = u;
+    p.vb = v_bias;
+    const long long plane = (long long)mem->n_pages * mem->H * mem->page_rows * mem->dh *
+                            elem_size(mem->dtype);
+    p.kpage = static_cast<const char *>(mem->pool) + 2LL * layer * plane;
+    p.vpage = static_cast<const char *>(p.kpage) + plane;
+    p.lse = lse;
+    p.parents = parents;
+    p.parents_stride = parents_stride;
+    p.n_nodes = n_nodes;
+    p.N = N;
+    p.r_rows = r_rows;
+    p.n_splits = splits;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = status;
+    p.wait_ns = g_wait_ns;
+    if (mem->dtype == TXL_F32)
+        return cuda_status(txl::launch_relattn_tree_f32(p, as_stream(stream)));
+    CUtensorMap tk, tv, tr;
+    const long long planes = (long long)mem->n_pages * mem->H;
+    if (!make_map(&tk, p.kpage, mem->page_rows, planes, txl::kPageRowUnit) ||
+        !make_map(&tv, p.vpage, mem->page_rows, planes, txl::kPageRowUnit) ||
+        !make_map(&tr, r, r_rows, mem->H, txl::kPageRowUnit))
+        return TXL_ERR_CUDA;
+    return cuda_status(txl::launch_relattn_tree(tk, tv, tr, p, as_stream(stream)));
+}
