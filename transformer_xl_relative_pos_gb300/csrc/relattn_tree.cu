@@ -47,6 +47,7 @@ constexpr int ROWB = DH * 2;               // bytes of a row
 constexpr int BOX = GK * ROWB;             // 4096: one 32-row box
 constexpr int ST_K = 0, ST_V = BOX, ST_R = 2 * BOX;
 constexpr int STAGE = 3 * BOX;             // 12288
+constexpr int kNodesCost = 2;              // the nodes among themselves, in chunks of memory
 
 template <int MT>
 struct Cfg {
@@ -73,18 +74,20 @@ struct Cfg {
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
                  "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The same for an A operand whose 16 rows are alike.
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[2], uint32_t b0,
-                                         uint32_t b1)
+// The same from a zero accumulator.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1)
 {
-    const uint32_t rows[4] = {a[0], a[0], a[1], a[1]};
-    mma16816(c, rows, b0, b1);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr)
@@ -124,75 +127,131 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w)
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// The running softmax and output of a warp's 16 nodes: this lane's rows are g and
-// g + 8 (index 0, 1), its output columns 8 nd + 2 t, + 1.
+// The running softmax and output of a warp's nodes: NR rows per lane (g, and g + 8
+// when NR = 2); its output columns are 8 nd + 2 t, + 1.  With NR = 1 (at most 8 nodes)
+// the accumulators' rows g + 8 hold the products with the probabilities' residuals.
+template <int NR>
 struct State {
-    float m[2], l[2];
+    float m[NR], l[NR];
     float acc[8][4];
 };
 
-// One chunk's masked scores s (log2 units; s[nt][e] of row g, s[nt][2 + e] of row
-// g + 8, key 8 nt + 2 t + e) into probabilities, rescaling the state to the new maximum.
-__device__ __forceinline__ void softmax_step(State &st, float (&s)[4][4])
+// One chunk's masked scores s (log2 units; s[nt][2 r + e]: row r of this lane, key
+// 8 nt + 2 t + e) into probabilities, rescaling the state to the new maximum.
+template <int NR>
+__device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR])
 {
-    float mx[2];
+    float mx[NR], ms[NR];
+    bool moved = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        mx[r] = s[0][2 * r];
+    for (int r = 0; r < NR; ++r) {
+        mx[r] = st.m[r];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            if (nt) mx[r] = max_nan(mx[r], s[nt][2 * r]);
-            mx[r] = max_nan(mx[r], s[nt][2 * r + 1]);
-        }
+        for (int nt = 0; nt < 4; ++nt) mx[r] = max3_nan(mx[r], s[nt][2 * r], s[nt][2 * r + 1]);
         mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        mx[r] = max_nan(mx[r], st.m[r]);
+        // a row without a visible key so far: any finite value makes its probabilities zero
+        ms[r] = mx[r] == -INFINITY ? 0.f : mx[r];
+        moved |= !(mx[r] == st.m[r]);
     }
-    // (a row without a visible key so far keeps maximum -inf: its sums are zero, and
-    // the selects below leave them so)
-    const bool moved = !(mx[0] == st.m[0]) || !(mx[1] == st.m[1]);
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float f = st.m[r] == -INFINITY ? 0.f : ex2f(st.m[r] - mx[r]);
+        for (int r = 0; r < NR; ++r) {
+            const float f = ex2f(st.m[r] - ms[r]);  // (0 from -inf: the sums are zero then)
             st.m[r] = mx[r];
             st.l[r] *= f;
 #pragma unroll
-            for (int nd = 0; nd < 8; ++nd) {
-                st.acc[nd][2 * r] *= f;
-                st.acc[nd][2 * r + 1] *= f;
-            }
+            for (int nd = 0; nd < 8; ++nd)
+#pragma unroll
+                for (int e = 0; e < 4 / NR; ++e) st.acc[nd][2 * r + e] *= f;
         }
     }
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int r = 0; r < NR; ++r) {
+        float sum[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = s[nt][e];
-            s[nt][e] = x == -INFINITY ? 0.f : ex2f(x - st.m[e >> 1]);
-            st.l[e >> 1] += s[nt][e];
+        for (int nt = 0; nt < 4; ++nt) {
+            s[nt][2 * r] = ex2f(s[nt][2 * r] - ms[r]);
+            s[nt][2 * r + 1] = ex2f(s[nt][2 * r + 1] - ms[r]);
+            sum[nt] = s[nt][2 * r] + s[nt][2 * r + 1];
         }
+        st.l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
 }
 
-// A operands of P.V for keys 16 kk .. 16 kk + 15 of a chunk, value and residual.
-__device__ __forceinline__ void p_operand(const float (&s)[4][4], int kk, uint32_t (&hi)[4],
-                                          uint32_t (&lo)[4])
+// acc += P.V over 32 keys, v[kk][nd]: fragments of keys 16 kk .. + 15, dimensions
+// 8 nd .. + 7.  The probabilities enter as value and residual.
+template <int NR>
+__device__ __forceinline__ void pv_step(State<NR> &st, const float (&s)[4][2 * NR], int kk,
+                                        const uint32_t (&v)[8][2])
+{
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if constexpr (NR == 2) {
+            hi[2 * c] = split_bf16x2(s[2 * kk + c][0], s[2 * kk + c][1], lo[2 * c]);
+            hi[2 * c + 1] = split_bf16x2(s[2 * kk + c][2], s[2 * kk + c][3], lo[2 * c + 1]);
+        } else {
+            hi[2 * c] = split_bf16x2(s[2 * kk + c][0], s[2 * kk + c][1], hi[2 * c + 1]);
+        }
+#pragma unroll
+    for (int nd = 0; nd < 8; ++nd) mma16816(st.acc[nd], hi, v[nd][0], v[nd][1]);
+    if constexpr (NR == 2) {
+#pragma unroll
+        for (int nd = 0; nd < 8; ++nd) mma16816(st.acc[nd], lo, v[nd][0], v[nd][1]);
+    }
+}
+
+// Step ks of 16 dimensions of (q + bias).b for four tiles of eight rows b, whose
+// fragments are words w, w + 1 of f: first the products with q (HALF: with q and the bias at
+// once), then those with the bias.
+template <bool HALF, int W>
+__device__ __forceinline__ void q_products(float (&c)[4][4], const uint32_t (&aq)[4][4],
+                                           const uint32_t (&bias)[4][4], int ks, const uint32_t (&f)[4][W],
+                                           int w)
 {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        hi[2 * c] = split_bf16x2(s[2 * kk + c][0], s[2 * kk + c][1], lo[2 * c]);
-        hi[2 * c + 1] = split_bf16x2(s[2 * kk + c][2], s[2 * kk + c][3], lo[2 * c + 1]);
+    for (int nt = 0; nt < 4; ++nt) {
+        if constexpr (HALF) {
+            if (ks == 0) mma16816_first(c[nt], bias[0], f[nt][w], f[nt][w + 1]);
+            else mma16816(c[nt], bias[ks], f[nt][w], f[nt][w + 1]);
+        } else {
+            if (ks == 0) mma16816_first(c[nt], aq[0], f[nt][w], f[nt][w + 1]);
+            else mma16816(c[nt], aq[ks], f[nt][w], f[nt][w + 1]);
+        }
     }
 }
 
-template <int MT>
+template <bool HALF, int W>
+__device__ __forceinline__ void bias_products(float (&c)[4][4], const uint32_t (&bias)[4][4], int ks,
+                                              const uint32_t (&f)[4][W], int w)
+{
+    if constexpr (!HALF) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mma16816(c[nt], bias[ks], f[nt][w], f[nt][w + 1]);
+    }
+}
+
+// Element e (0, 1) of this lane's row r in a product's fragment.
+template <bool HALF>
+__device__ __forceinline__ float element(const float (&c)[4], int r, int e)
+{
+    return HALF ? c[e] + c[2 + e] : c[2 * r + e];
+}
+
+// MT node tiles of 16; HALF: at most 8 nodes (one tile, whose rows 8 to 15 then take u, v
+// and the probabilities' residuals: half the MMAs).
+template <int MT, bool HALF>
 __global__ void __launch_bounds__(WARPS * 32, 2)
     relattn_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_r, const TreeParams p)
 {
     using C = Cfg<MT>;
+    static_assert(!HALF || MT == 1, "half a tile");
     constexpr int KG = C::KG, NSTG = C::NSTG, DCAP = C::DCAP, RW = C::RW, LD = C::LD;
+    constexpr int NR = HALF ? 1 : 2;           // nodes per lane
+    constexpr int TB = DCAP / 8 < 4 ? DCAP / 8 : 4;  // table tiles loaded at once
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -202,6 +261,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     const int split = blockIdx.x % p.n_splits;
     const int bh = blockIdx.x / p.n_splits;
     const int b = bh / p.mem.H, h = bh - b * p.mem.H;
+    int begin, fill;
+    paged_state(p.mem, b, p.status, begin, fill);
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
     if (n == 0) return;  // (every block of the cluster)
 
@@ -221,36 +282,38 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
         }
         fence_barrier_init();
     }
-    __syncthreads();
+    // (only the leader uses full before build_topology's barriers)
 
-    int begin, fill;
-    paged_state(p.mem, b, p.status, begin, fill);
-    const Chunks ck = group_chunks(p, begin, fill, split * KG + kg, p.n_splits * KG);
+    const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split * KG + kg, p.n_splits * KG);
     const uint64_t pol_stream = policy_evict_first();  // k, v: read once
     const uint64_t pol_keep = policy_evict_last();     // table: shared by the batch
-    // Copies of this group's item into its stage.  Boxes are always complete (rows
-    // past a tensor's ends arrive as zeros): a page id out of range becomes a plane
-    // past the pool's end, and its rows are masked.
-    auto issue = [&](int item) {
-        const int c = ck.c0 + item, st = item % NSTG;
-        int page, row;
-        chunk_place(p.mem, ck, b, c, p.status, page, row);
+    const int trow0 = p.r_rows - 1 - fill + ck.c0 * GK - ck.off;  // table row of the first chunk's key 0
+    // Copies of this group's next item into its stage (the leader).  Boxes are always
+    // complete (rows past a tensor's ends arrive as zeros): a page id out of range
+    // becomes a plane past the pool's end, and its rows are masked.  The id of a page
+    // is loaded an item ahead.
+    int issued = 0, slot = ck.slot, row = ck.row;
+    int page = leader && ck.count > 0 ? page_at(p.mem, b, slot, p.status) : -1;
+    auto issue = [&]() {
+        const int st = issued % NSTG;
         const int plane = page >= 0 ? page * p.mem.H + h : p.mem.n_pages * p.mem.H;
         stage_ok[st] = page >= 0;
         uint8_t *dst = ring + st * STAGE;
         mbar_arrive_expect_tx(full + st, (uint32_t)STAGE);
         tma_load_3d_hint(dst + ST_K, &tm_k, full + st, 0, row, plane, pol_stream);
         tma_load_3d_hint(dst + ST_V, &tm_v, full + st, 0, row, plane, pol_stream);
-        tma_load_3d_hint(dst + ST_R, &tm_r, full + st, 0, p.r_rows - 1 - fill + c * GK - ck.off, h,
-                         pol_keep);
+        tma_load_3d_hint(dst + ST_R, &tm_r, full + st, 0, trow0 + issued * GK, h, pol_keep);
+        ++issued;
+        if (next_chunk(p.mem, slot, row) && issued < ck.count) page = page_at(p.mem, b, slot, p.status);
     };
-    int issued = 0;
     if (leader)
-        for (; issued < min(NSTG, ck.count); ++issued) issue(issued);
+        while (issued < min(NSTG, ck.count)) issue();
 
     // A operands, dimensions 16 ks + 2 t, + 1 (registers 0, 1) and + 8, + 9 (2, 3): rows
-    // g, g + 8 of the tile's q; u and v, alike in every row.
-    uint32_t aq[4][4], au[4][2], av[4][2];
+    // g, g + 8 of the tile's q; u and v, alike in every row.  HALF: au holds q in rows g
+    // and u in rows g + 8, av q and v; a product's two rows are then added.
+    const int i0 = mt * 16 + g;  // this lane's first node (the second: + 8)
+    uint32_t aq[4][4], au[4][4], av[4][4];
     {
         const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q.ptr) + b * p.q.sb + h * p.q.sh;
         const uint32_t *urow = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.u) + h * DH);
@@ -260,170 +323,199 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int w = 8 * ks + 4 * half + t;
-                au[ks][half] = urow[w];
-                av[ks][half] = vrow[w];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int i = mt * 16 + g + 8 * r;
+                for (int r = 0; r < NR; ++r)
                     aq[ks][2 * half + r] =
-                        i < n ? reinterpret_cast<const uint32_t *>(qb + i * p.q.sr)[w] : 0;
-                }
+                        i0 + 8 * r < n ? reinterpret_cast<const uint32_t *>(qb + (i0 + 8 * r) * p.q.sr)[w] : 0;
+                au[ks][2 * half + 1] = __ldg(urow + w);
+                av[ks][2 * half + 1] = __ldg(vrow + w);
+                au[ks][2 * half] = HALF ? aq[ks][2 * half] : au[ks][2 * half + 1];
+                av[ks][2 * half] = HALF ? aq[ks][2 * half] : av[ks][2 * half + 1];
             }
     }
-    build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
-    const int i0 = mt * 16 + g, i1 = i0 + 8;  // this lane's nodes
-    const int d0 = i0 < n ? topo.depth[i0] : 0, d1 = i1 < n ? topo.depth[i1] : 0;
-
-    State st;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        st.m[r] = -INFINITY;
-        st.l[r] = 0.f;
-    }
-#pragma unroll
-    for (int nd = 0; nd < 8; ++nd)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.acc[nd][e] = 0.f;
-
-    // Products (q + v).r of 8 table rows from global memory (rows outside the table:
-    // zero) into ring columns col .. col + 7.
-    const __nv_bfloat16 *table = static_cast<const __nv_bfloat16 *>(p.r) + (long long)h * p.r_rows * DH;
-    auto table_tile = [&](int row0, int col) {
-        const int row = row0 + g;
-        uint32_t w[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) w[x] = 0;
-        if (row >= 0 && row < p.r_rows) {
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(table + (long long)row * DH);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) w[x] = __ldg(src + 4 * x + t);
-        }
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            mma16816(c, aq[ks], w[2 * ks], w[2 * ks + 1]);
-            mma16816(c, av[ks], w[2 * ks], w[2 * ks + 1]);
-        }
+    auto put_products = [&](const float (&c)[4], int col) {
         TXL_CHECK(col >= 0 && col + 8 <= RW, p.status);
-        *reinterpret_cast<float2 *>(scr + g * LD + col + 2 * t) = make_float2(c[0], c[1]);
-        *reinterpret_cast<float2 *>(scr + (g + 8) * LD + col + 2 * t) = make_float2(c[2], c[3]);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+            *reinterpret_cast<float2 *>(scr + (g + 8 * r) * LD + col + 2 * t) =
+                make_float2(element<HALF>(c, r, 0), element<HALF>(c, r, 1));
+    };
+    // 32 contiguous bytes' worth of a row in fragment order: word x holds dimensions
+    // 8 x + 2 t, + 1 (words 2 ks, 2 ks + 1: step ks).
+    auto load_row = [&](uint32_t (&w)[8], const __nv_bfloat16 *src, bool there) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            w[x] = there ? __ldg(reinterpret_cast<const uint32_t *>(src) + 4 * x + t) : 0;
+    };
+    // TB tiles of eight table rows from global memory (rows outside the table: zero),
+    // and their products into ring columns col ...
+    const __nv_bfloat16 *table = static_cast<const __nv_bfloat16 *>(p.r) + (long long)h * p.r_rows * DH;
+    auto load_table = [&](auto &w, int row0) {
+#pragma unroll
+        for (int x = 0; x < TB; ++x) {
+            const int tr = row0 + 8 * x + g;
+            load_row(w[x], table + (long long)tr * DH, tr >= 0 && tr < p.r_rows);
+        }
+    };
+    auto table_products = [&](const auto &w, int col) {
+#pragma unroll
+        for (int x = 0; x < TB; ++x) {
+            float c[4];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                if (ks == 0) mma16816_first(c, av[0], w[x][0], w[x][1]);
+                else mma16816(c, av[ks], w[x][2 * ks], w[x][2 * ks + 1]);
+                if (!HALF) mma16816(c, aq[ks], w[x][2 * ks], w[x][2 * ks + 1]);
+            }
+            put_products(c, col + 8 * x);
+        }
     };
     // P.V of one chunk, element by element: for a chunk whose keys are not all
     // visible to the same nodes and whose values hold an infinity or NaN, which must
-    // not reach the nodes that do not see the key.  hidden: bit 4 nt + e of this lane's
-    // elements.  col0: 32 free ring columns.
-    auto pv_by_element = [&](const float (&s)[4][4], uint32_t hidden, int col0, auto &&value) {
+    // not reach the nodes that do not see the key.  hidden: bit 4 nt + 2 r + e of this
+    // lane's elements.  col0: 32 free ring columns.
+    State<NR> st;
+    auto pv_by_element = [&](const auto &s, uint32_t hidden, int col0, auto &&value) {
         auto at = [&](int key) { const int c = col0 + key; return c >= RW ? c - RW : c; };
         __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 2 * NR; ++e)
                 scr[(g + 8 * (e >> 1)) * LD + at(8 * nt + 2 * t + (e & 1))] =
                     (hidden >> (4 * nt + e)) & 1 ? -1.f : s[nt][e];
         __syncwarp();
         for (int key = 0; key < GK; ++key) {
-            const float p0 = scr[g * LD + at(key)], p1 = scr[(g + 8) * LD + at(key)];
 #pragma unroll
-            for (int nd = 0; nd < 8; ++nd)
+            for (int r = 0; r < NR; ++r) {
+                const float pr = scr[(g + 8 * r) * LD + at(key)];
+                if (pr < 0.f) continue;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float x = value(key, 8 * nd + 2 * t + e);
-                    if (!(p0 < 0.f)) st.acc[nd][e] = fmaf(p0, x, st.acc[nd][e]);
-                    if (!(p1 < 0.f)) st.acc[nd][2 + e] = fmaf(p1, x, st.acc[nd][2 + e]);
-                }
+                for (int nd = 0; nd < 8; ++nd)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        st.acc[nd][2 * r + e] = fmaf(pr, value(key, 8 * nd + 2 * t + e), st.acc[nd][2 * r + e]);
+            }
         }
         __syncwarp();
     };
 
     const bool active = mt * 16 < n;  // this warp has nodes
-    if (active && split == p.n_splits - 1 && kg == 0) {
-        // ---- the nodes among themselves: distances 0 .. DCAP - 1 ------------------
-        for (int c = 0; c < DCAP; c += 8) table_tile(p.r_rows - DCAP + c, c);
-        __syncwarp();
-        const unsigned long long anc0 = i0 < n ? topo.anc[i0] : 0, anc1 = i1 < n ? topo.anc[i1] : 0;
-        const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.k.ptr) + b * p.k.sb + h * p.k.sh;
-        const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.v.ptr) + b * p.v.sb + h * p.v.sh;
-        // (no node is an ancestor of an earlier one: this tile's nodes see nodes up to their own)
-        const int a_end = min(n, mt * 16 + 16);
-        for (int a0 = 0; a0 < a_end; a0 += GK) {
-            float s[4][4];
+    // The last group takes the nodes among themselves.  What that needs from global
+    // memory is loaded ahead of the tree's construction, and otherwise the table rows
+    // before the first chunk's.
+    const bool owner = active && split == p.n_splits - 1 && kg == KG - 1;
+    const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.k.ptr) + b * p.k.sb + h * p.k.sh;
+    const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.v.ptr) + b * p.v.sb + h * p.v.sh;
+    // (no node is an ancestor of an earlier one: this tile's nodes see nodes up to their own)
+    const int a_end = min(n, mt * 16 + 16);
+    uint32_t kw[4][8], vw[2][8][2], tw[TB][8];
+    auto load_nodes = [&](int a0) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int row = a0 + 8 * nt + g;
-                uint32_t w[8];
+        for (int nt = 0; nt < 4; ++nt) {
+            const int a = a0 + 8 * nt + g;
+            load_row(kw[nt], kn + a * p.k.sr, a < a_end);
+        }
+        // V fragments: rows (keys) 16 kk + 2 t, + 1 and + 8, + 9, column 8 nd + g
 #pragma unroll
-                for (int x = 0; x < 8; ++x) w[x] = 0;
-                if (row < a_end) {
-                    const uint32_t *src = reinterpret_cast<const uint32_t *>(kn + row * p.k.sr);
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) w[x] = src[4 * x + t];
-                }
+            for (int x = 0; x < 2; ++x) {
+                const int key = a0 + 16 * kk + 8 * x + 2 * t;
+                const __nv_bfloat16 *src = vn + key * p.v.sr + g;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    mma16816(s[nt], aq[ks], w[2 * ks], w[2 * ks + 1]);
-                    mma16816(s[nt], au[ks], w[2 * ks], w[2 * ks + 1]);
+                for (int nd = 0; nd < 8; ++nd) {
+                    uint32_t w = 0;
+                    if (key < a_end) w = __bfloat16_as_ushort(src[8 * nd]);
+                    if (key + 1 < a_end) w |= (uint32_t)__bfloat16_as_ushort(src[p.v.sr + 8 * nd]) << 16;
+                    vw[kk][nd][x] = w;
                 }
             }
+    };
+    if (owner) {
+        load_table(tw, p.r_rows - DCAP);
+        load_nodes(0);
+    } else if (active && ck.count > 0) {
+        load_table(tw, trow0 - DCAP);
+    }
+    build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
+    int depth[NR], depth_max = 0;
+    unsigned long long anc[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const bool there = i0 + 8 * r < n;
+        depth[r] = there ? topo.depth[i0 + 8 * r] : 0;
+        anc[r] = there ? topo.anc[i0 + 8 * r] : 0;
+        depth_max = max(depth_max, depth[r]);
+        st.m[r] = -INFINITY;
+        st.l[r] = 0.f;
+    }
+    depth_max = __reduce_max_sync(0xffffffffu, depth_max);
+#pragma unroll
+    for (int nd = 0; nd < 8; ++nd)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.acc[nd][e] = 0.f;
+
+    if (owner) {
+        // ---- the nodes among themselves: distances 0 .. DCAP - 1 ------------------
+        table_products(tw, 0);
+#pragma unroll
+        for (int c = TB * 8; c < DCAP; c += TB * 8) {
+            load_table(tw, p.r_rows - DCAP + c);
+            table_products(tw, c);
+        }
+        __syncwarp();
+        for (int a0 = 0; a0 < a_end; a0 += GK) {
+            if (a0 > 0) load_nodes(a0);
+            float c[4][4], s[4][2 * NR];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                q_products<HALF>(c, aq, au, ks, kw, 2 * ks);
+                bias_products<HALF>(c, au, ks, kw, 2 * ks);
+            }
             uint32_t hidden = 0;
+            bool bad = false;
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int a = a0 + 8 * nt + 2 * t + (e & 1);
-                    const int dist = (e < 2 ? d0 : d1) - (a < n ? topo.depth[a] : 0);
-                    const bool seen = a < n && (((e < 2 ? anc0 : anc1) >> a) & 1) && dist < p.r_rows;
+                for (int e = 0; e < 2 * NR; ++e) {
+                    const int r = e >> 1, a = a0 + 8 * nt + 2 * t + (e & 1);
+                    const int dist = depth[r] - (a < n ? topo.depth[a] : 0);
+                    const bool seen = a < n && ((anc[r] >> a) & 1) && dist < p.r_rows;
                     TXL_CHECK(!seen || (dist >= 0 && dist < DCAP), p.status);
                     hidden |= seen ? 0u : 1u << (4 * nt + e);
-                    s[nt][e] = seen ? (s[nt][e] + scr[(g + 8 * (e >> 1)) * LD + DCAP - 1 - dist]) * p.scale_log2
+                    s[nt][e] = seen ? (element<HALF>(c[nt], r, e & 1) + scr[(g + 8 * r) * LD + DCAP - 1 - dist]) *
+                                          p.scale_log2
                                     : -INFINITY;
                 }
             softmax_step(st, s);
-            // V fragments: key rows 16 kk + 2 t, + 1 (and + 8, + 9), column 8 nd + g
-            uint32_t vw[2][8][2];
-            bool bad = false;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int nd = 0; nd < 8; ++nd)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int key = a0 + 16 * kk + 8 * x + 2 * t;
-                        const __nv_bfloat16 *src = vn + key * p.v.sr + 8 * nd + g;
-                        uint32_t w = 0;
-                        if (key < a_end) w = __bfloat16_as_ushort(src[0]);
-                        if (key + 1 < a_end) w |= (uint32_t)__bfloat16_as_ushort(src[p.v.sr]) << 16;
-                        vw[kk][nd][x] = w;
-                        bad |= nonfinite2(w);
-                    }
+                for (int nd = 0; nd < 8; ++nd) bad |= nonfinite2(vw[kk][nd][0]) | nonfinite2(vw[kk][nd][1]);
             if (__any_sync(0xffffffffu, bad)) {
                 pv_by_element(s, hidden, DCAP, [&](int key, int dim) {
                     return a0 + key < a_end ? __bfloat162float(vn[(a0 + key) * p.v.sr + dim]) : 0.f;
                 });
-                continue;
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                uint32_t hi[4], lo[4];
-                p_operand(s, kk, hi, lo);
-#pragma unroll
-                for (int nd = 0; nd < 8; ++nd) {
-                    mma16816(st.acc[nd], hi, vw[kk][nd][0], vw[kk][nd][1]);
-                    mma16816(st.acc[nd], lo, vw[kk][nd][0], vw[kk][nd][1]);
-                }
+            } else {
+                pv_step(st, s, 0, vw[0]);
+                pv_step(st, s, 1, vw[1]);
             }
         }
         __syncwarp();  // the ring's columns are free again
+        if (ck.count > 0) load_table(tw, trow0 - DCAP);
     }
-    if (active && ck.count > 0)  // the DCAP table rows before the first chunk's
-        for (int c = 0; c < DCAP; c += 8)
-            table_tile(p.r_rows - 1 - fill + ck.c0 * GK - ck.off - DCAP + c, c);
+    if (active && ck.count > 0) {  // the DCAP table rows before the first chunk's
+        table_products(tw, 0);
+#pragma unroll
+        for (int c = TB * 8; c < DCAP; c += TB * 8) {
+            load_table(tw, trow0 - DCAP + c);
+            table_products(tw, c);
+        }
+    }
 
     // ---- the memory, chunk by chunk ---------------------------------------------
     const int lr = lane & 7, lm = lane >> 3;  // matrix-load roles: row, matrix
-    const int depth_max = __reduce_max_sync(0xffffffffu, max(d0, d1));
     int wpos = DCAP;                          // ring column of the chunk's first table row
     bool ok = true;
     for (int item = 0; item < ck.count; ++item) {
@@ -435,71 +527,72 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             const uint32_t sk = smem_u32(base + ST_K), sv = smem_u32(base + ST_V), sr = smem_u32(base + ST_R);
             const int j0 = (ck.c0 + item) * GK - ck.off;  // memory row of the chunk's first key
 
-            // content and position products
-            float s[4][4];
+            // content and position products, eight independent accumulators in turn (one
+            // after the other, each MMA would wait for the one before)
+            float c[4][4], cr[4][4];
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+                uint32_t bk[4][4], br[4][4];
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    ldsm_x4(bk[nt], sk + swz(8 * nt + lr, 4 * h2 + lm));
+                    ldsm_x4(br[nt], sr + swz(8 * nt + lr, 4 * h2 + lm));
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    q_products<HALF>(c, aq, au, 2 * h2 + x, bk, 2 * x);
+                    q_products<HALF>(cr, aq, av, 2 * h2 + x, br, 2 * x);
+                    bias_products<HALF>(c, au, 2 * h2 + x, bk, 2 * x);
+                    bias_products<HALF>(cr, av, 2 * h2 + x, br, 2 * x);
+                }
+            }
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
-                const int row = 8 * nt + lr;
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                    uint32_t bk[4], br[4];
-                    ldsm_x4(bk, sk + swz(row, 4 * h2 + lm));
-                    ldsm_x4(br, sr + swz(row, 4 * h2 + lm));
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int ks = 2 * h2 + x;
-                        mma16816(s[nt], aq[ks], bk[2 * x], bk[2 * x + 1]);
-                        mma16816(c, aq[ks], br[2 * x], br[2 * x + 1]);
-                        mma16816(s[nt], au[ks], bk[2 * x], bk[2 * x + 1]);
-                        mma16816(c, av[ks], br[2 * x], br[2 * x + 1]);
-                    }
-                }
-                int col = wpos + 8 * nt;
-                col -= col >= RW ? RW : 0;
-                TXL_CHECK(col >= 0 && col + 8 <= RW, p.status);
-                *reinterpret_cast<float2 *>(scr + g * LD + col + 2 * t) = make_float2(c[0], c[1]);
-                *reinterpret_cast<float2 *>(scr + (g + 8) * LD + col + 2 * t) = make_float2(c[2], c[3]);
+                const int col = wpos + 8 * nt;
+                put_products(cr[nt], col >= RW ? col - RW : col);
             }
             __syncwarp();
             // scores: the position product of key jj and a node of depth d stands
-            // d columns before the chunk's own column jj
+            // d columns before the chunk's own column jj, in the window of RW columns that
+            // begins at the ring column after the chunk's last
+            int next = wpos + GK;
+            next -= next >= RW ? RW : 0;
+            float s[4][2 * NR];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int r = 0; r < NR; ++r) {
+                const int first = next + DCAP + 2 * t - depth[r];
+                const float *at = scr + (g + 8 * r) * LD + first;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    int col = wpos + 8 * nt + 2 * t + (e & 1) - (e < 2 ? d0 : d1);
-                    col += col < 0 ? RW : 0;
-                    col -= col >= RW ? RW : 0;
-                    TXL_CHECK(col >= 0 && col < RW, p.status);
-                    s[nt][e] = (s[nt][e] + scr[(g + 8 * (e >> 1)) * LD + col]) * p.scale_log2;
-                }
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int jj = 8 * nt + e;
+                        const float *from = jj >= RW - first ? at - RW : at;
+                        TXL_CHECK(from + jj >= scr + (g + 8 * r) * LD && from + jj < scr + (g + 8 * r) * LD + RW,
+                                  p.status);
+                        s[nt][2 * r + e] = (element<HALF>(c[nt], r, e) + from[jj]) * p.scale_log2;
+                    }
+            }
             // Keys that are not memory rows (the chunk sticks out at either end, or its
             // page is unknown) or that the table does not reach from the node.
             const bool page_ok = stage_ok[stg] != 0;
             const bool out_of_memory = j0 < 0 || j0 + GK > fill || !page_ok;
             const bool partly_hidden = j0 < fill + depth_max - p.r_rows + 1;
+            const int key_lo = -j0, key_hi = page_ok ? fill - j0 : 0;  // memory rows of the chunk
             uint32_t hidden = 0;
             if (out_of_memory || partly_hidden) {
-                const int lo0 = max(0, fill + d0 - p.r_rows + 1) - j0;
-                const int lo1 = max(0, fill + d1 - p.r_rows + 1) - j0;
-                const int hi = page_ok ? fill - j0 : 0;
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2 * NR; ++e) {
                         const int jj = 8 * nt + 2 * t + (e & 1);
-                        if (jj < (e < 2 ? lo0 : lo1) || jj >= hi) {
+                        if (jj < max(0, fill + depth[e >> 1] - p.r_rows + 1) - j0 || jj >= key_hi) {
                             s[nt][e] = -INFINITY;
                             hidden |= 1u << (4 * nt + e);
                         }
                     }
             }
             softmax_step(st, s);
-            // P.V
-            const int key_lo = -j0, key_hi = page_ok ? fill - j0 : 0;  // memory rows of the chunk
             bool bad = false;
             if (partly_hidden) {
                 // lane = key: does a memory row hold an infinity or NaN
@@ -512,8 +605,6 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
                 }
                 bad = __any_sync(0xffffffffu, bad);
             }
-            int next = wpos + GK;
-            next -= next >= RW ? RW : 0;
             if (bad) {
                 pv_by_element(s, hidden, next, [&](int key, int dim) {
                     const uint8_t *at = base + ST_V + swz(key, dim >> 3) + 2 * (dim & 7);
@@ -522,32 +613,29 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             } else {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t hi[4], lo[4];
-                    p_operand(s, kk, hi, lo);
-                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    uint32_t bv[8][2];
+#pragma unroll
+                    for (int np = 0; np < 4; ++np) {
+                        uint32_t w[4];
+                        ldsm_x4_t(w, sv + swz(16 * kk + (lm & 1) * 8 + lr, 2 * np + (lm >> 1)));
+                        bv[2 * np][0] = w[0];
+                        bv[2 * np][1] = w[1];
+                        bv[2 * np + 1][0] = w[2];
+                        bv[2 * np + 1][1] = w[3];
+                    }
                     if (out_of_memory) {
                         // this lane's fragment rows: keys 16 kk + 2 t, + 1 and + 8, + 9
                         const int key = 16 * kk + 2 * t;
                         auto in = [&](int x) { return x >= key_lo && x < key_hi; };
-                        keep0 = (in(key) ? 0xffffu : 0u) | (in(key + 1) ? 0xffff0000u : 0u);
-                        keep1 = (in(key + 8) ? 0xffffu : 0u) | (in(key + 9) ? 0xffff0000u : 0u);
-                    }
-                    const int row = 16 * kk + (lm & 1) * 8 + lr;
+                        const uint32_t keep0 = (in(key) ? 0xffffu : 0u) | (in(key + 1) ? 0xffff0000u : 0u);
+                        const uint32_t keep1 = (in(key + 8) ? 0xffffu : 0u) | (in(key + 9) ? 0xffff0000u : 0u);
 #pragma unroll
-                    for (int np = 0; np < 4; ++np) {
-                        uint32_t bv[4];
-                        ldsm_x4_t(bv, sv + swz(row, 2 * np + (lm >> 1)));
-                        if (out_of_memory) {
-                            bv[0] &= keep0;
-                            bv[1] &= keep1;
-                            bv[2] &= keep0;
-                            bv[3] &= keep1;
+                        for (int nd = 0; nd < 8; ++nd) {
+                            bv[nd][0] &= keep0;
+                            bv[nd][1] &= keep1;
                         }
-                        mma16816(st.acc[2 * np], hi, bv[0], bv[1]);
-                        mma16816(st.acc[2 * np + 1], hi, bv[2], bv[3]);
-                        mma16816(st.acc[2 * np], lo, bv[0], bv[1]);
-                        mma16816(st.acc[2 * np + 1], lo, bv[2], bv[3]);
                     }
+                    pv_step(st, s, kk, bv);
                 }
             }
             wpos = next;
@@ -556,10 +644,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
         fence_proxy_async_smem();
         __syncwarp();
         if constexpr (MT == 1) {
-            if (item + NSTG < ck.count) {
-                if (lane == 0) issue(item + NSTG);
-                ++issued;
-            }
+            if (leader && issued < ck.count) issue();
         } else {
             // The group's other warps may lag: refill the previous item's stage, once
             // all have left it.
@@ -567,12 +652,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             if (item > 0 && item - 1 + NSTG < ck.count) {
                 if (leader) {
                     const int prev = item - 1;
-                    if (mbar_wait(empty + prev % NSTG, (prev / NSTG) & 1, abort_flag, p.wait_ns)) {
-                        issue(prev + NSTG);
-                        ++issued;
-                    } else {
-                        ok = false;
-                    }
+                    ok = mbar_wait(empty + prev % NSTG, (prev / NSTG) & 1, abort_flag, p.wait_ns);
+                    if (ok) issue();
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
@@ -600,7 +681,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     __syncwarp();
     Rec *mine = rec(warp);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NR; ++r) {
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
         if (t == 0) {
@@ -610,7 +691,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
 #pragma unroll
         for (int nd = 0; nd < 8; ++nd)
             *reinterpret_cast<float2 *>(&mine->a[g + 8 * r][8 * nd + 2 * t]) =
-                make_float2(st.acc[nd][2 * r], st.acc[nd][2 * r + 1]);
+                make_float2(element<HALF>(st.acc[nd], r, 0), element<HALF>(st.acc[nd], r, 1));
     }
     finish<MT, __nv_bfloat16>(rec, p, b, h, n, warp, lane);
 }
@@ -626,9 +707,10 @@ cudaError_t ensure_attr()
     const auto set = [](auto *k, int bytes) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     };
-    if ((e = set(relattn_tree_kernel<1>, Cfg<1>::SMEM)) != cudaSuccess) return e;
-    if ((e = set(relattn_tree_kernel<2>, Cfg<2>::SMEM)) != cudaSuccess) return e;
-    if ((e = set(relattn_tree_kernel<4>, Cfg<4>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_kernel<1, true>, Cfg<1>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_kernel<1, false>, Cfg<1>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_kernel<2, false>, Cfg<2>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_kernel<4, false>, Cfg<4>::SMEM)) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
     return cudaSuccess;
 }
@@ -640,9 +722,10 @@ cudaError_t launch_relattn_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v
 {
     const cudaError_t e = ensure_attr();
     if (e != cudaSuccess) return e;
-    if (p.N <= 16) return launch_clusters(relattn_tree_kernel<1>, p, Cfg<1>::SMEM, s, tm_k, tm_v, tm_r, p);
-    if (p.N <= 32) return launch_clusters(relattn_tree_kernel<2>, p, Cfg<2>::SMEM, s, tm_k, tm_v, tm_r, p);
-    return launch_clusters(relattn_tree_kernel<4>, p, Cfg<4>::SMEM, s, tm_k, tm_v, tm_r, p);
+    if (p.N <= 8) return launch_clusters(relattn_tree_kernel<1, true>, p, Cfg<1>::SMEM, s, tm_k, tm_v, tm_r, p);
+    if (p.N <= 16) return launch_clusters(relattn_tree_kernel<1, false>, p, Cfg<1>::SMEM, s, tm_k, tm_v, tm_r, p);
+    if (p.N <= 32) return launch_clusters(relattn_tree_kernel<2, false>, p, Cfg<2>::SMEM, s, tm_k, tm_v, tm_r, p);
+    return launch_clusters(relattn_tree_kernel<4, false>, p, Cfg<4>::SMEM, s, tm_k, tm_v, tm_r, p);
 }
 
 } // namespace txl

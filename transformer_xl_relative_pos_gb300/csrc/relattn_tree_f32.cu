@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
 
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);
-    const Chunks ck = group_chunks(p, begin, fill, split * KG + kg, p.n_splits * KG);
+    const Chunks ck = group_chunks(p, begin, fill, 2, split * KG + kg, p.n_splits * KG);
     const int rows = min(16, n - mt * 16);  // this warp's nodes (none: <= 0)
     const float4 *qu = reinterpret_cast<const float4 *>(qs + mt * (2 * 16 * DH));
     const float4 *qv = qu + 16 * DH / 4;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
         __syncwarp();
     };
 
-    if (rows > 0 && split == p.n_splits - 1 && kg == 0) {
+    if (rows > 0 && split == p.n_splits - 1 && kg == KG - 1) {
         // ---- the nodes among themselves: distances 0 .. DCAP - 1 ------------------
         for (int c = 0; c < DCAP; c += 32) table_dots(p.r_rows - DCAP + c + lane, c + lane, c + lane < DCAP);
         __syncwarp();
@@ -190,10 +190,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
 
     // ---- the memory, chunk by chunk ---------------------------------------------
     int wpos = DCAP;  // ring column of the chunk's first table row
+    int slot = ck.slot, row = ck.row, page = ck.count > 0 ? page_at(p.mem, b, slot, p.status) : -1;
     for (int item = 0; item < (rows > 0 ? ck.count : 0); ++item) {
         const int c = ck.c0 + item, j0 = c * GK - ck.off;
-        int page, row;
-        chunk_place(p.mem, ck, b, c, p.status, page, row);
         const long long at = page >= 0 ? (((long long)page * p.mem.H + h) * p.mem.P + row) * DH : 0;
         const float *kp = static_cast<const float *>(p.kpage) + at;
         const float *vp = static_cast<const float *>(p.vpage) + at;
@@ -223,6 +222,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
              [&](int key) { return key >= key_lo && key < key_hi ? vp + key * DH : nullptr; });
         wpos += GK;
         wpos -= wpos >= RW ? RW : 0;
+        if (next_chunk(p.mem, slot, row) && item + 1 < ck.count) page = page_at(p.mem, b, slot, p.status);
     }
 
     // ---- this warp's record, over its ring ----------------------------------------

@@ -35,6 +35,13 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Per node of the block's sequence: depth, and the mask of itself and its ancestors.
 struct Topology {
     unsigned long long anc[kTreeMaxNodes];
@@ -84,41 +91,52 @@ __device__ __forceinline__ void build_topology(Topology &t, const int *parents, 
 // The chunks of one key group: 32-row chunks of the table ring, aligned to it
 // (so that none crosses a page).  Chunk c holds memory rows 32 c - off .. + 31.
 struct Chunks {
-    int begin, fill;  // the sequence's state
-    int off;          // begin mod 32
-    int c0, count;    // this group's first chunk, and how many
+    int off;        // begin mod 32
+    int c0, count;  // this group's first chunk, and how many
+    int slot, row;  // table slot of the first chunk, and its first row there
 };
 
-__device__ __forceinline__ Chunks group_chunks(const TreeParams &p, int begin, int fill, int group,
-                                               int groups)
+// A head's chunks in contiguous runs over its key groups.  The last group also takes
+// the nodes among themselves, which count as `nodes_cost` chunks behind the
+// memory's.
+__device__ __forceinline__ Chunks group_chunks(const TreeParams &p, int begin, int fill, int nodes_cost,
+                                               int group, int groups)
 {
     Chunks k;
-    k.begin = begin;
-    k.fill = fill;
     k.off = begin & (GK - 1);
     // Rows the table reaches from a node of depth 0; deeper ones reach fewer.
     const int t_lo = max(0, fill - p.r_rows + 1);
     const int first = (k.off + t_lo) / GK;
     const int all = fill > t_lo ? (k.off + fill + GK - 1) / GK - first : 0;
-    k.c0 = first + (int)((long long)all * group / groups);
-    k.count = first + (int)((long long)all * (group + 1) / groups) - k.c0;
+    const int from = min(all, (int)((long long)(all + nodes_cost) * group / groups));
+    const int to = min(all, (int)((long long)(all + nodes_cost) * (group + 1) / groups));
+    k.c0 = first + from;
+    k.count = to - from;
+    int x = begin - k.off + k.c0 * GK;  // below 2 R, and R itself when there is no chunk
+    x -= x >= p.mem.R ? p.mem.R : 0;
+    k.slot = x / p.mem.P;
+    k.row = x - k.slot * p.mem.P;
     return k;
 }
 
-// Page and row in it of chunk c (its first row; page out of range: -1).
-__device__ __forceinline__ void chunk_place(const PagedView &m, const Chunks &k, int b, int c,
-                                            unsigned int *status, int &page, int &row)
+// Page id in table slot `slot` of sequence b (out of range: -1, and recorded).
+__device__ __forceinline__ int page_at(const PagedView &m, int b, int slot, unsigned int *status)
 {
-    int x = k.begin - k.off + c * GK;  // below 2 R
-    x -= x >= m.R ? m.R : 0;
-    const int slot = x / m.P;
-    row = x - slot * m.P;
-    TXL_CHECK(x >= 0 && x < m.R && row % GK == 0, status);
-    page = m.table[(long long)b * m.slots + slot];
-    if (page < 0 || page >= m.n_pages) {
-        atomicOr(status, TXL_STATUS_INDEX);
-        page = -1;
-    }
+    TXL_CHECK(slot >= 0 && slot < m.slots, status);
+    const int page = m.table[(long long)b * m.slots + slot];
+    if (page >= 0 && page < m.n_pages) return page;
+    atomicOr(status, TXL_STATUS_INDEX);
+    return -1;
+}
+
+// The table position one chunk on.  True when another page begins.
+__device__ __forceinline__ bool next_chunk(const PagedView &m, int &slot, int &row)
+{
+    row += GK;
+    if (row < m.P) return false;
+    row = 0;
+    if (++slot == m.slots) slot = 0;
+    return true;
 }
 
 // One warp's result for its 16 nodes: running maximum (log2 units), sum of
