@@ -132,18 +132,15 @@ def lib():
                                             _c_int, _c_int, _c_int, _c_p]),
                 "txl_mem_update": (_c_int, [_c_p, ctypes.POINTER(MemState), _c_p, _c_int, _c_int,
                                             _c_int, _c_int, _c_p]),
-                "txl_paged_append": (_c_int, [ctypes.POINTER(_PagedKV), _c_int, _c_int,
-                                              ctypes.POINTER(_Rows), ctypes.POINTER(_Rows),
-                                              ctypes.c_longlong, _c_int, _c_p, _c_int, _c_p,
-                                              _c_int, _c_int, _c_p, _c_p, _c_p]),
-                "txl_paged_advance": (_c_int, [ctypes.POINTER(_PagedKV), _c_p, _c_int, _c_int,
-                                               _c_p, _c_p, _c_p]),
-                "txl_paged_copy": (_c_int, [ctypes.POINTER(_PagedKV), _c_p, _c_p, _c_int, _c_p]),
-                "txl_relattn_tree_fwd": (_c_int, [ctypes.POINTER(_Rows)] * 3 +
-                                         [ctypes.POINTER(_PagedKV), _c_int, _c_p, _c_int, _c_p,
-                                          _c_p, _c_p, ctypes.c_longlong, _c_p,
-                                          ctypes.POINTER(_Rows), _c_p, _c_int, _c_float, _c_int,
-                                          _c_p]),
+                # (the structs txl_paged_kv and txl_rows by address)
+                "txl_paged_append": (_c_int, [_c_p, _c_int, _c_int, _c_p, _c_p, ctypes.c_longlong,
+                                              _c_int, _c_p, _c_int, _c_p, _c_int, _c_int, _c_p,
+                                              _c_p, _c_p]),
+                "txl_paged_advance": (_c_int, [_c_p, _c_p, _c_int, _c_int, _c_p, _c_p, _c_p]),
+                "txl_paged_copy": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_p]),
+                "txl_relattn_tree_fwd": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_int,
+                                                  _c_p, _c_p, _c_p, ctypes.c_longlong, _c_p, _c_p,
+                                                  _c_p, _c_int, _c_float, _c_int, _c_p]),
                 "txl_page_pool_init": (_c_int, [ctypes.POINTER(_PagePool), _c_int, _c_ip, _c_ip]),
                 "txl_page_pool_alloc": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
                 "txl_page_pool_retain": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
@@ -466,10 +463,14 @@ class PagedKV:
         for t, name in ints[1:]:
             if tuple(t.shape) != (B,):
                 raise ValueError(f"{name} must be [B]")
-        _same_device(pool, *(t for t, _ in ints))
         self._c = _PagedKV(_dev(pool, "pool"), *(_dev(t, n, torch.int32) for t, n in ints),
                            self.ticket.data_ptr(), self.layers, self.n_pages, self.H,
                            self.page_rows, pool.shape[4], B, self.slots, _code(pool.dtype))
+        self._at = ctypes.addressof(self._c)
+        self._dtype, self._index = pool.dtype, pool.get_device()
+        for t, name in ints:
+            _ptr(t, name, torch.int32, t.shape, self._index)
+        self._shape = (B, self.H, pool.shape[4])
 
     @property
     def rows(self) -> int:
@@ -477,44 +478,71 @@ class PagedKV:
         return self.slots * self.page_rows
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices ({first.device}, {t.device})")
+# The calls on a paged memory are made once per layer and token: their checks cost
+# one comparison each where nothing is wrong.
+_Rows4 = ctypes.c_longlong * 16  # four txl_rows: pointer and three strides each
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t, name: str, mem: PagedKV, offset: int = 0):
-    """txl_rows of t [B, H, rows, 64] (any strides, the last dimension dense)."""
+def _refuse(t, name: str, dtype, shape, index: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
-    if t.dtype != mem.pool.dtype:
-        raise ValueError(f"{name} must be {mem.pool.dtype}, got {t.dtype}")
-    if t.shape[-4:-2] != (mem.B, mem.H) or t.shape[-1] != mem.pool.shape[4]:
-        raise ValueError(f"{name} must be [B, H, rows, dh] of the memory, got {tuple(t.shape)}")
-    if t.shape[-2] > 0 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Rows(t.data_ptr(), t.stride(-4), t.stride(-3), t.stride(-2))
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on another device than the memory")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be {list(shape)}, contiguous (rows operands: in the last "
+                     f"dimension), got {list(t.shape)} with strides {t.stride()}")
 
 
-def _counts(n, name: str, B: int):
-    if n is None:
-        return None
-    if tuple(n.shape) != (B,):
-        raise ValueError(f"{name} must be [B]")
-    return _dev(n, name, torch.int32)
+def _ptr(t, name: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous tensor of this dtype, shape and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == index and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _row_operands(shape, mem: PagedKV, *operands):
+    """txl_rows, in one array, of (tensor, name) pairs of this shape [..., B, H, N, 64]."""
+    words = []
+    for t, name in operands:
+        if not (isinstance(t, torch.Tensor) and t.dtype is mem._dtype and t.shape == shape and
+                t.get_device() == mem._index):
+            _refuse(t, name, mem._dtype, shape, mem._index)
+        st = t.stride()
+        if st[-1] != 1 and t.numel() > 0:
+            _refuse(t, name, mem._dtype, shape, mem._index)
+        words += (t.data_ptr(), st[-4], st[-3], st[-2])
+    return _Rows4(*words)
+
+
+def _paged_call(mem: PagedKV, name: str, stream, *args):
+    """The library's function on the memory's device and (unless given) its current
+    stream."""
+    index = mem._index
+    if stream is None:
+        stream = (_raw_stream(index) if _raw_stream is not None
+                  else torch.cuda.current_stream(index).cuda_stream)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        _check(rc, name)
 
 
 def _state_out(mem: PagedKV, state_out):
-    if state_out is None:
-        return None, None
-    begin, fill = state_out
-    for t, name in ((begin, "begin"), (fill, "fill")):
-        if tuple(t.shape) != (mem.B,):
-            raise ValueError(f"state_out: {name} must be [B]")
-    _same_device(mem.pool, begin, fill)
-    return _dev(begin, "begin", torch.int32), _dev(fill, "fill", torch.int32)
+    begin, fill = (mem.begin, mem.fill) if state_out is None else state_out
+    shape = (mem.B,)
+    return (_ptr(begin, "begin", torch.int32, shape, mem._index),
+            _ptr(fill, "fill", torch.int32, shape, mem._index))
 
 
 def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
@@ -528,29 +556,34 @@ def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
     nodes of a drafted tree).  With ``keep``, the state is advanced to the
     newest ``keep`` rows: in ``mem``, or in the tensors ``state_out`` = (begin,
     fill) instead."""
-    if k.dim() not in (4, 5) or k.shape != v.shape:
-        raise ValueError("k and v must have one shape, [B, H, N, 64] or [n, B, H, N, 64]")
-    if k.dim() == 5 and k.shape[0] > 1 and k.stride(0) != v.stride(0):
-        raise ValueError("k and v must have the same layer stride")
-    ck, cv = _rows(k, "k", mem), _rows(v, "v", mem)
-    _same_device(mem.pool, k, v, n_new, rows)
-    n_layers = k.shape[0] if k.dim() == 5 else 1
-    N = k.shape[-2]
-    if rows is not None and (rows.dim() != 2 or rows.shape[0] != mem.B):
-        raise ValueError("rows must be [B, width]")
-    if state_out is not None and keep is None:
+    B, H, dh = mem._shape
+    shape = k.shape
+    layers, layer_stride = 1, 0
+    if len(shape) == 5:
+        layers, layer_stride = shape[0], k.stride(0)
+        if layers > 1 and v.stride()[0] != layer_stride:
+            raise ValueError("k and v must have the same layer stride")
+    if len(shape) not in (4, 5) or shape[-4] != B or shape[-3] != H or shape[-1] != dh:
+        raise ValueError(f"k and v must be [B, H, N, dh] or [n, B, H, N, dh] of the memory, got "
+                         f"{list(shape)}")
+    N = width = shape[-2]
+    kv = _row_operands(shape, mem, (k, "k"), (v, "v"))
+    at = ctypes.addressof(kv)
+    index = mem._index
+    rows_at = n_at = b_out = f_out = None
+    if rows is not None:
+        if rows.dim() != 2:
+            raise ValueError("rows must be [B, width]")
+        width = rows.shape[1]
+        rows_at = _ptr(rows, "rows", torch.int32, (B, width), index)
+    if n_new is not None:
+        n_at = _ptr(n_new, "n_new", torch.int32, (B,), index)
+    if keep is not None:
+        b_out, f_out = _state_out(mem, state_out)
+    elif state_out is not None:
         raise ValueError("state_out needs keep")
-    if keep is not None and state_out is None:
-        state_out = (mem.begin, mem.fill)
-    b_out, f_out = _state_out(mem, state_out)
-    with torch.cuda.device(mem.pool.device):
-        _check(lib().txl_paged_append(
-            ctypes.byref(mem._c), int(layer), int(n_layers), ctypes.byref(ck), ctypes.byref(cv),
-            int(k.stride(0)) if k.dim() == 5 else 0, int(N),
-            _dev(rows, "rows", torch.int32) if rows is not None else None,
-            int(rows.shape[1]) if rows is not None else 0, _counts(n_new, "n_new", mem.B),
-            int(rows.shape[1]) if rows is not None else int(N), int(keep or 0), b_out, f_out,
-            _stream(mem.pool, stream)), "txl_paged_append")
+    _paged_call(mem, "txl_paged_append", stream, mem._at, layer, layers, at, at + 32, layer_stride, N,
+                rows_at, width if rows is not None else 0, n_at, width, keep or 0, b_out, f_out)
     return mem
 
 
@@ -558,28 +591,23 @@ def paged_advance(mem: PagedKV, n, *, keep: int, state_out=None, stream=None):
     """Advance the state of rows appended without ``keep`` (layer by layer):
     sequence b has n[b] new rows (int32 on the device), or n each (an int), and keeps
     its newest ``keep`` rows.  Written to ``mem``, or to ``state_out``."""
-    counts = None if isinstance(n, int) else n
-    if counts is not None:
-        _same_device(mem.pool, counts)
-    b_out, f_out = _state_out(mem, (mem.begin, mem.fill) if state_out is None else state_out)
-    with torch.cuda.device(mem.pool.device):
-        _check(lib().txl_paged_advance(
-            ctypes.byref(mem._c), _counts(counts, "n", mem.B),
-            int(n) if counts is None else mem.rows, int(keep), b_out, f_out,
-            _stream(mem.pool, stream)), "txl_paged_advance")
+    n_at, most = None, n
+    if not isinstance(n, int):
+        n_at, most = _ptr(n, "n", torch.int32, (mem.B,), mem._index), mem.rows
+    b_out, f_out = _state_out(mem, state_out)
+    _paged_call(mem, "txl_paged_advance", stream, mem._at, n_at, most, keep, b_out, f_out)
     return mem
 
 
 def paged_copy(mem: PagedKV, src, dst, *, stream=None):
     """Copy pages src[i] to pages dst[i] (int32 on the device) in every plane of the
     pool.  No page may be a destination twice, or a source and a destination."""
-    if src.dim() != 1 or src.shape != dst.shape:
+    if src.dim() != 1:
         raise ValueError("src and dst must be one-dimensional and of one length")
-    _same_device(mem.pool, src, dst)
-    with torch.cuda.device(mem.pool.device):
-        _check(lib().txl_paged_copy(ctypes.byref(mem._c), _dev(src, "src", torch.int32),
-                                    _dev(dst, "dst", torch.int32), int(src.numel()),
-                                    _stream(mem.pool, stream)), "txl_paged_copy")
+    shape = src.shape
+    _paged_call(mem, "txl_paged_copy", stream, mem._at,
+                _ptr(src, "src", torch.int32, shape, mem._index),
+                _ptr(dst, "dst", torch.int32, shape, mem._index), shape[0])
     return mem
 
 
@@ -597,36 +625,33 @@ def relattn_tree_fwd(q, k_new, v_new, mem: PagedKV, layer: int, r, u, v_bias, pa
     out and lse behind them are left as they were.  ``out``: a tensor to fill
     ([B, H, N, 64], any strides); ``lse``: True, or a tensor [B, H, N] fp32.
     Returns ``out`` or ``(out, lse)``."""
+    B, H, dh = mem._shape
+    shape, index, dt = q.shape, mem._index, mem._dtype
+    if len(shape) != 4 or shape[0] != B or shape[1] != H or shape[3] != dh:
+        raise ValueError(f"q must be [B, H, N, dh] of the memory, got {list(shape)}")
+    N = shape[2]
     if out is None:
         # (zeros: rows behind n_nodes are not written)
-        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.zeros(shape, dtype=dt, device=q.device)
+    lse_at = n_at = None
     want_lse = lse is not None and lse is not False
-    if lse is True:
-        lse = torch.zeros(q.shape[:3], dtype=torch.float32, device=q.device)
-    if not (q.dim() == 4 and q.shape == k_new.shape == v_new.shape == out.shape):
-        raise ValueError("q, k_new, v_new and out must have one shape, [B, H, N, 64]")
-    if want_lse and lse.shape != q.shape[:3]:
-        raise ValueError("lse must be [B, H, N]")
-    B, H, N, dh = q.shape
-    dt = mem.pool.dtype
-    if r.dim() != 3 or r.shape[0] != H or r.shape[2] != dh:
+    if want_lse:
+        if lse is True:
+            lse = torch.zeros(shape[:3], dtype=torch.float32, device=q.device)
+        lse_at = _ptr(lse, "lse", torch.float32, shape[:3], index)
+    ops = _row_operands(shape, mem, (q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out"))
+    at = ctypes.addressof(ops)
+    if r.dim() != 3:
         raise ValueError("r must be [H, r_rows, 64]")
-    if tuple(u.shape) != (H, dh) or tuple(v_bias.shape) != (H, dh):
-        raise ValueError("u and v_bias must be [H, 64]")
-    if tuple(parents.shape) not in ((B, N), (N,)):
-        raise ValueError("parents must be [B, N] or [N]")
-    _same_device(mem.pool, q, k_new, v_new, r, u, v_bias, parents, n_nodes, out,
-                 lse if want_lse else None)
-    cq, ck, cv, co = (_rows(t, name, mem) for t, name in
-                      ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out")))
-    with torch.cuda.device(mem.pool.device):
-        _check(lib().txl_relattn_tree_fwd(
-            ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv), ctypes.byref(mem._c), int(layer),
-            _dev(r, "r", dt), int(r.shape[1]), _dev(u, "u", dt), _dev(v_bias, "v_bias", dt),
-            _dev(parents, "parents", torch.int32), N if parents.dim() == 2 else 0,
-            _counts(n_nodes, "n_nodes", B), ctypes.byref(co),
-            _dev(lse, "lse", torch.float32) if want_lse else None, int(N), float(scale),
-            int(n_splits), _stream(mem.pool, stream)), "txl_relattn_tree_fwd")
+    r_rows = r.shape[1]
+    if n_nodes is not None:
+        n_at = _ptr(n_nodes, "n_nodes", torch.int32, (B,), index)
+    stride = N if parents.dim() == 2 else 0
+    _paged_call(mem, "txl_relattn_tree_fwd", stream, at, at + 32, at + 64, mem._at, layer,
+                _ptr(r, "r", dt, (H, r_rows, dh), index), r_rows, _ptr(u, "u", dt, (H, dh), index),
+                _ptr(v_bias, "v_bias", dt, (H, dh), index),
+                _ptr(parents, "parents", torch.int32, (B, N) if stride else (N,), index), stride, n_at,
+                at + 96, lse_at, N, scale, n_splits)
     return (out, lse) if want_lse else out
 
 
