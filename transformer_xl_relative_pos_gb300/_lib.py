@@ -482,6 +482,7 @@ class PagedKV:
 # one comparison each where nothing is wrong.
 _Rows4 = ctypes.c_longlong * 16  # four txl_rows: pointer and three strides each
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _refuse(t, name: str, dtype, shape, index: int):
@@ -499,23 +500,29 @@ def _refuse(t, name: str, dtype, shape, index: int):
 
 def _ptr(t, name: str, dtype, shape, index: int) -> int:
     """Address of a contiguous tensor of this dtype, shape and device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
-            t.get_device() == index and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, index)
-    return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.get_device() == index and t.shape == shape and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, index)
 
 
 def _row_operands(shape, mem: PagedKV, *operands):
     """txl_rows, in one array, of (tensor, name) pairs of this shape [..., B, H, N, 64]."""
     words = []
+    dtype, index = mem._dtype, mem._index
     for t, name in operands:
-        if not (isinstance(t, torch.Tensor) and t.dtype is mem._dtype and t.shape == shape and
-                t.get_device() == mem._index):
-            _refuse(t, name, mem._dtype, shape, mem._index)
-        st = t.stride()
-        if st[-1] != 1 and t.numel() > 0:
-            _refuse(t, name, mem._dtype, shape, mem._index)
-        words += (t.data_ptr(), st[-4], st[-3], st[-2])
+        try:
+            if t.dtype is dtype and t.get_device() == index and t.shape == shape:
+                st = t.stride()
+                if st[-1] == 1 or t.numel() == 0:
+                    words += (t.data_ptr(), *st[-4:-1])
+                    continue
+        except AttributeError:
+            pass
+        _refuse(t, name, dtype, shape, index)
     return _Rows4(*words)
 
 
@@ -529,7 +536,7 @@ def _paged_call(mem: PagedKV, name: str, stream, *args):
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(index):

@@ -9,6 +9,7 @@ namespace txl {
 
 constexpr int kTreeMaxNodes = 64;   // nodes of a drafted tree (one 64-bit ancestor mask)
 constexpr int kTreeMaxCluster = 8;  // key ranges of a head: one portable thread-block cluster
+constexpr int kTreeMaxSorted = 255; // sequences whose blocks can be ordered by length
 constexpr int kPageRowUnit = 32;    // page_rows is a multiple of this: keys of one tile
 
 // Device view of a paged memory (txl_paged_kv).
@@ -73,6 +74,7 @@ struct TreeParams {
     long long parents_stride;
     const int *n_nodes;
     int N, r_rows, n_splits;
+    int by_length;              // blocks of the longest memories first (B <= kTreeMaxSorted)
     float scale_log2;           // scale * log2(e)
     unsigned int *status;
     unsigned long long wait_ns;

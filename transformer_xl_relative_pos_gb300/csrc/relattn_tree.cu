@@ -43,6 +43,12 @@ namespace {
 
 using namespace tree;
 
+constexpr int WARPS = 4, ROWS = 16;        // warps that compute, nodes of a warp
+constexpr int THREADS = 2 * WARPS * 32;    // and as many for the copies, one per key group
+// Registers a thread of the two kinds (warpgroups) after the split of the 128 that two
+// blocks of 256 threads per SM leave; their sum must not exceed 256.
+constexpr int REGS_COMPUTE = 216, REGS_COPY = 40;
+static_assert(REGS_COMPUTE + REGS_COPY <= 256, "the block's registers at launch");
 constexpr int ROWB = DH * 2;               // bytes of a row
 constexpr int BOX = GK * ROWB;             // 4096: one 32-row box
 constexpr int ST_K = 0, ST_V = BOX, ST_R = 2 * BOX;
@@ -65,8 +71,10 @@ struct Cfg {
     static constexpr int OFF_FLAG = OFF_OK + KG * NSTG * 4;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // slack for the manual alignment
     // where a warp leaves its record: its private ring, or (shared ring) its scratch
-    static_assert(MT == 1 || sizeof(Rec) <= SCR, "a warp's record fits in its scratch");
-    static_assert(sizeof(Rec) <= NSTG * STAGE, "a warp's record fits in its ring");
+    static_assert(MT == 1 || sizeof(Rec<ROWS>) <= SCR, "a warp's record fits in its scratch");
+    static_assert(sizeof(Rec<ROWS>) <= NSTG * STAGE, "a warp's record fits in its ring");
+    static_assert((kTreeMaxSorted + 1) * 4 <= sizeof(Topology) && kTreeMaxSorted <= THREADS,
+                  "the order by length is found in the topology's place");
     static_assert(OFF_BAR % 8 == 0 && OFF_TOPO % 8 == 0, "8-byte alignment");
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks per SM");
 };
@@ -242,7 +250,7 @@ __device__ __forceinline__ float element(const float (&c)[4], int r, int e)
 // MT node tiles of 16; HALF: at most 8 nodes (one tile, whose rows 8 to 15 then take u, v
 // and the probabilities' residuals: half the MMAs).
 template <int MT, bool HALF>
-__global__ void __launch_bounds__(WARPS * 32, 2)
+__global__ void __launch_bounds__(THREADS, 2)
     relattn_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_r, const TreeParams p)
@@ -260,54 +268,91 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     const int g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.n_splits;
     const int bh = blockIdx.x / p.n_splits;
-    const int b = bh / p.mem.H, h = bh - b * p.mem.H;
+    const int rank = bh / p.mem.H, h = bh - rank * p.mem.H;
+    const int b = pick_sequence(p, rank, reinterpret_cast<int *>(smem + C::OFF_TOPO));
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
     if (n == 0) return;  // (every block of the cluster)
 
-    uint8_t *ring = smem + kg * NSTG * STAGE;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + kg * NSTG;
-    uint64_t *empty = full + KG * NSTG;
-    volatile int *stage_ok = reinterpret_cast<volatile int *>(smem + C::OFF_OK) + kg * NSTG;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // full, then empty, [KG][NSTG]
+    volatile int *stage_ok = reinterpret_cast<volatile int *>(smem + C::OFF_OK);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     Topology &topo = *reinterpret_cast<Topology *>(smem + C::OFF_TOPO);
-    float *scr = reinterpret_cast<float *>(smem + C::OFF_SCR + warp * C::SCR);
-    const bool leader = mt == 0 && lane == 0;  // issues its key group's copies
-    if (threadIdx.x == 0) *abort_flag = 0;
-    if (leader) {
-        for (int s = 0; s < NSTG; ++s) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, MT);
-        }
-        fence_barrier_init();
-    }
-    // (only the leader uses full before build_topology's barriers)
-
-    const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split * KG + kg, p.n_splits * KG);
-    const uint64_t pol_stream = policy_evict_first();  // k, v: read once
-    const uint64_t pol_keep = policy_evict_last();     // table: shared by the batch
-    const int trow0 = p.r_rows - 1 - fill + ck.c0 * GK - ck.off;  // table row of the first chunk's key 0
-    // Copies of this group's next item into its stage (the leader).  Boxes are always
-    // complete (rows past a tensor's ends arrive as zeros): a page id out of range
-    // becomes a plane past the pool's end, and its rows are masked.  The id of a page
-    // is loaded an item ahead.
-    int issued = 0, slot = ck.slot, row = ck.row;
-    int page = leader && ck.count > 0 ? page_at(p.mem, b, slot, p.status) : -1;
-    auto issue = [&]() {
-        const int st = issued % NSTG;
-        const int plane = page >= 0 ? page * p.mem.H + h : p.mem.n_pages * p.mem.H;
-        stage_ok[st] = page >= 0;
-        uint8_t *dst = ring + st * STAGE;
-        mbar_arrive_expect_tx(full + st, (uint32_t)STAGE);
-        tma_load_3d_hint(dst + ST_K, &tm_k, full + st, 0, row, plane, pol_stream);
-        tma_load_3d_hint(dst + ST_V, &tm_v, full + st, 0, row, plane, pol_stream);
-        tma_load_3d_hint(dst + ST_R, &tm_r, full + st, 0, trow0 + issued * GK, h, pol_keep);
-        ++issued;
-        if (next_chunk(p.mem, slot, row) && issued < ck.count) page = page_at(p.mem, b, slot, p.status);
+    const auto rec = [smem](int w) {
+        return reinterpret_cast<Rec<ROWS> *>(MT == 1 ? smem + w * NSTG * STAGE
+                                                     : smem + C::OFF_SCR + w * C::SCR);
     };
-    if (leader)
-        while (issued < min(NSTG, ck.count)) issue();
+
+    if (warp >= WARPS) {
+        // ===================== the copies: a warp per key group, its lane 0 ============
+        // Boxes are always complete (rows past a tensor's ends arrive as zeros): a page
+        // id out of range becomes a plane past the pool's end, and its rows are masked.
+        // The id of a page is loaded an item ahead.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
+        const int group = warp - WARPS;
+        const bool mine = group < KG && lane == 0;
+        Chunks ck{};
+        int slot = 0, row = 0, page = -1, issued = 0;
+        uint64_t *full = bars + group * NSTG, *empty = full + KG * NSTG;
+        const uint64_t pol_stream = policy_evict_first();  // k, v: read once
+        const uint64_t pol_keep = policy_evict_last();     // table: shared by the batch
+        auto issue = [&]() {
+            const int st = group * NSTG + issued % NSTG;
+            const int plane = page >= 0 ? page * p.mem.H + h : p.mem.n_pages * p.mem.H;
+            uint64_t *bar = bars + st;
+            stage_ok[st] = page >= 0;
+            uint8_t *dst = smem + st * STAGE;
+            mbar_arrive_expect_tx(bar, (uint32_t)STAGE);
+            tma_load_3d_hint(dst + ST_K, &tm_k, bar, 0, row, plane, pol_stream);
+            tma_load_3d_hint(dst + ST_V, &tm_v, bar, 0, row, plane, pol_stream);
+            tma_load_3d_hint(dst + ST_R, &tm_r, bar, 0,
+                             p.r_rows - 1 - fill + (ck.c0 + issued) * GK - ck.off, h, pol_keep);
+            ++issued;
+            if (next_chunk(p.mem, slot, row) && issued < ck.count) page = page_at(p.mem, b, slot, p.status);
+        };
+        if (warp == WARPS && lane == 0) *abort_flag = 0;
+        if (mine) {
+            ck = group_chunks(p, begin, fill, kNodesCost, split * KG + group, p.n_splits * KG);
+            slot = ck.slot;
+            row = ck.row;
+            if (ck.count > 0) page = page_at(p.mem, b, slot, p.status);
+            for (int s = 0; s < NSTG; ++s) {
+                mbar_init(full + s, 1);
+                mbar_init(empty + s, MT);
+            }
+            fence_barrier_init();
+            while (issued < min(NSTG, ck.count)) issue();
+        }
+        __syncwarp();
+        build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
+        if (mine) {
+            // refill each stage when the group's warps have left it
+            bool ok = true;
+            while (ok && issued < ck.count) {
+                ok = mbar_wait(empty + issued % NSTG, (issued / NSTG + 1) & 1, abort_flag, p.wait_ns);
+                if (ok) issue();
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+            }
+            // the copies in flight land before shared memory is used for anything else
+            const int zero = 0;
+            for (int x = max(0, issued - NSTG); x < issued; ++x)
+                mbar_wait(full + x % NSTG, (x / NSTG) & 1, &zero, p.wait_ns);
+        }
+        __syncwarp();
+        finish_barriers(p);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_COMPUTE));
+
+    const uint8_t *ring = smem + kg * NSTG * STAGE;
+    uint64_t *full = bars + kg * NSTG, *empty = full + KG * NSTG;
+    float *scr = reinterpret_cast<float *>(smem + C::OFF_SCR + warp * C::SCR);
+    const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split * KG + kg, p.n_splits * KG);
+    const int trow0 = p.r_rows - 1 - fill + ck.c0 * GK - ck.off;  // table row of the first chunk's key 0
 
     // A operands, dimensions 16 ks + 2 t, + 1 (registers 0, 1) and + 8, + 9 (2, 3): rows
     // g, g + 8 of the tile's q; u and v, alike in every row.  HALF: au holds q in rows g
@@ -575,7 +620,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             }
             // Keys that are not memory rows (the chunk sticks out at either end, or its
             // page is unknown) or that the table does not reach from the node.
-            const bool page_ok = stage_ok[stg] != 0;
+            const bool page_ok = stage_ok[kg * NSTG + stg] != 0;
             const bool out_of_memory = j0 < 0 || j0 + GK > fill || !page_ok;
             const bool partly_hidden = j0 < fill + depth_max - p.r_rows + 1;
             const int key_lo = -j0, key_hi = page_ok ? fill - j0 : 0;  // memory rows of the chunk
@@ -640,46 +685,19 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             }
             wpos = next;
         }
-        // The stage is read: order this lane's reads before the copy that refills it.
-        fence_proxy_async_smem();
         __syncwarp();
-        if constexpr (MT == 1) {
-            if (leader && issued < ck.count) issue();
-        } else {
-            // The group's other warps may lag: refill the previous item's stage, once
-            // all have left it.
-            if (lane == 0) mbar_arrive(empty + stg);
-            if (item > 0 && item - 1 + NSTG < ck.count) {
-                if (leader) {
-                    const int prev = item - 1;
-                    ok = mbar_wait(empty + prev % NSTG, (prev / NSTG) & 1, abort_flag, p.wait_ns);
-                    if (ok) issue();
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-            }
-        }
+        if (lane == 0) mbar_arrive(empty + stg);  // this warp has read the stage
     }
-    if (!ok) {
-        // Time-out: record it, and let this group's copies in flight land before the
-        // block's shared memory is used for anything else or released.
-        if (lane == 0) {
-            *abort_flag = 1;
-            atomicOr(p.status, TXL_STATUS_TIMEOUT);
-            const int zero = 0;
-            if (leader)
-                for (int x = max(0, issued - NSTG); x < issued; ++x)
-                    mbar_wait(full + x % NSTG, (x / NSTG) & 1, &zero, p.wait_ns);
-        }
-        __syncwarp();
+    if (!ok && lane == 0) {
+        *abort_flag = 1;
+        atomicOr(p.status, TXL_STATUS_TIMEOUT);
     }
 
     // ---- this warp's record ------------------------------------------------------
-    const auto rec = [smem](int w) {
-        return reinterpret_cast<Rec *>(MT == 1 ? smem + w * NSTG * STAGE : smem + C::OFF_SCR + w * C::SCR);
-    };
+    // over the copies' stages (all of this group's items have landed and been read, and
+    // with one node tile nobody else reads them), or over the scratch
     __syncwarp();
-    Rec *mine = rec(warp);
+    Rec<ROWS> *mine = rec(warp);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
@@ -693,7 +711,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             *reinterpret_cast<float2 *>(&mine->a[g + 8 * r][8 * nd + 2 * t]) =
                 make_float2(element<HALF>(st.acc[nd], r, 0), element<HALF>(st.acc[nd], r, 1));
     }
-    finish<MT, __nv_bfloat16>(rec, p, b, h, n, warp, lane);
+    finish<WARPS, ROWS, MT, __nv_bfloat16>(rec, p, b, h, n, warp, lane);
 }
 
 // The dynamic shared-memory attribute of the kernels, once per device.
@@ -722,10 +740,13 @@ cudaError_t launch_relattn_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v
 {
     const cudaError_t e = ensure_attr();
     if (e != cudaSuccess) return e;
-    if (p.N <= 8) return launch_clusters(relattn_tree_kernel<1, true>, p, Cfg<1>::SMEM, s, tm_k, tm_v, tm_r, p);
-    if (p.N <= 16) return launch_clusters(relattn_tree_kernel<1, false>, p, Cfg<1>::SMEM, s, tm_k, tm_v, tm_r, p);
-    if (p.N <= 32) return launch_clusters(relattn_tree_kernel<2, false>, p, Cfg<2>::SMEM, s, tm_k, tm_v, tm_r, p);
-    return launch_clusters(relattn_tree_kernel<4, false>, p, Cfg<4>::SMEM, s, tm_k, tm_v, tm_r, p);
+    const auto run = [&](auto *kern, int smem) {
+        return launch_clusters(kern, p, THREADS, smem, s, tm_k, tm_v, tm_r, p);
+    };
+    if (p.N <= 8) return run(relattn_tree_kernel<1, true>, Cfg<1>::SMEM);
+    if (p.N <= 16) return run(relattn_tree_kernel<1, false>, Cfg<1>::SMEM);
+    if (p.N <= 32) return run(relattn_tree_kernel<2, false>, Cfg<2>::SMEM);
+    return run(relattn_tree_kernel<4, false>, Cfg<4>::SMEM);
 }
 
 } // namespace txl

@@ -19,21 +19,29 @@ namespace {
 
 using namespace tree;
 
+constexpr int WARPS = 8, ROWS = 8;   // warps of a block, nodes of a warp
+constexpr int MAX_MT = kTreeMaxNodes / ROWS;
+constexpr int SLD = DH + 4;          // row stride of staged rows (floats): a lane's own row is then
+                                     // read without bank conflicts, four floats at a time
+
 template <int MT>
 struct CfgF32 {
-    static constexpr int DCAP = 16 * MT;       // depths are below this
+    static constexpr int DCAP = ROWS * MT;     // depths are below this
     static constexpr int RW = GK + DCAP;       // columns of the product ring
-    static constexpr int Q = MT * 2 * 16 * DH; // floats: q + u, q + v of the nodes
-    static constexpr int WARP = 16 * RW + 16 * GK;  // floats per warp: ring, probabilities
+    static constexpr int Q = MT * 2 * ROWS * DH;  // floats: q + u, q + v of the nodes
+    // floats per warp: ring, probabilities, 32 rows on their way to the lanes
+    static constexpr int WARP = ROWS * RW + ROWS * GK + GK * SLD;
+    static constexpr int REC = (int)sizeof(Rec<ROWS>);  // a warp's record goes over them
     static constexpr int OFF_WARP = Q * 4;
-    static constexpr int OFF_TOPO = OFF_WARP + WARPS * WARP * 4;
+    static constexpr int STEP = WARP * 4 > REC ? WARP * 4 : REC;  // bytes per warp
+    static constexpr int OFF_TOPO = OFF_WARP + WARPS * STEP;
     static constexpr int SMEM = OFF_TOPO + (int)sizeof(Topology);
-    static_assert(sizeof(Rec) <= WARP * 4, "a warp's record fits over its ring");
-    static_assert(OFF_TOPO % 16 == 0 && OFF_WARP % 16 == 0 && (WARP * 4) % 16 == 0, "alignment");
+    static_assert(SMEM <= 232448, "shared memory budget exceeded");
+    static_assert(OFF_TOPO % 16 == 0 && OFF_WARP % 16 == 0 && STEP % 16 == 0, "alignment");
 };
 
 template <int MT>
-__global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const TreeParams p)
+__global__ void __launch_bounds__(WARPS * 32) relattn_tree_f32_kernel(const TreeParams p)
 {
     using C = CfgF32<MT>;
     constexpr int KG = WARPS / MT, DCAP = C::DCAP, RW = C::RW;
@@ -43,51 +51,64 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
     const int mt = warp % MT, kg = warp / MT;
     const int split = blockIdx.x % p.n_splits;
     const int bh = blockIdx.x / p.n_splits;
-    const int b = bh / p.mem.H, h = bh - b * p.mem.H;
+    const int rank = bh / p.mem.H, h = bh - rank * p.mem.H;
+    const int b = pick_sequence(p, rank, reinterpret_cast<int *>(smem + C::OFF_TOPO));
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
     if (n == 0) return;  // (every block of the cluster)
 
     float *qs = reinterpret_cast<float *>(smem);
-    float *ring = reinterpret_cast<float *>(smem + C::OFF_WARP) + warp * C::WARP;
-    float *prob = ring + 16 * RW;
+    float *ring = reinterpret_cast<float *>(smem + C::OFF_WARP + warp * C::STEP);
+    float *prob = ring + ROWS * RW, *rows32 = prob + ROWS * GK;
     Topology &topo = *reinterpret_cast<Topology *>(smem + C::OFF_TOPO);
 
     // q + u and q + v of the nodes (those past n: zero)
-    for (int e = threadIdx.x; e < MT * 16 * DH; e += WARPS * 32) {
+    for (int e = threadIdx.x; e < MT * ROWS * DH; e += WARPS * 32) {
         const int i = e / DH, c = e % DH;
         const float *q = static_cast<const float *>(p.q.ptr) + b * p.q.sb + h * p.q.sh + i * p.q.sr;
         const float x = i < n ? q[c] : 0.f;
-        float *dst = qs + (i / 16) * (2 * 16 * DH) + (i % 16) * DH + c;
+        float *dst = qs + (i / ROWS) * (2 * ROWS * DH) + (i % ROWS) * DH + c;
         dst[0] = x + static_cast<const float *>(p.u)[h * DH + c];
-        dst[16 * DH] = x + static_cast<const float *>(p.vb)[h * DH + c];
+        dst[ROWS * DH] = x + static_cast<const float *>(p.vb)[h * DH + c];
     }
     build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
 
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);
     const Chunks ck = group_chunks(p, begin, fill, 2, split * KG + kg, p.n_splits * KG);
-    const int rows = min(16, n - mt * 16);  // this warp's nodes (none: <= 0)
-    const float4 *qu = reinterpret_cast<const float4 *>(qs + mt * (2 * 16 * DH));
-    const float4 *qv = qu + 16 * DH / 4;
+    const int rows = min(ROWS, n - mt * ROWS);  // this warp's nodes (none: <= 0)
+    const float4 *qu = reinterpret_cast<const float4 *>(qs + mt * (2 * ROWS * DH));
+    const float4 *qv = qu + ROWS * DH / 4;
     const float *table = static_cast<const float *>(p.r) + (long long)h * p.r_rows * DH;
 
-    float m[16], l[16], acc[16][2];  // l: this lane's keys only
+    float m[ROWS], l[ROWS], acc[ROWS][2];  // l: this lane's keys only
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         m[i] = -INFINITY;
         l[i] = acc[i][0] = acc[i][1] = 0.f;
     }
     int depth_max = 0;
-    for (int i = 0; i < rows; ++i) depth_max = max(depth_max, topo.depth[mt * 16 + i]);
+    for (int i = 0; i < rows; ++i) depth_max = max(depth_max, topo.depth[mt * ROWS + i]);
 
-    // dot products of the warp's nodes with one row per lane (null: zero)
-    auto dots = [&](const float *row, const float4 *q, float (&out)[16]) {
+    // Dot products of the warp's nodes with one row per lane, row(x) of 32 (null: zero).
+    // The rows are read in order, half a warp a row, and handed out through shared
+    // memory: a lane reading its own row would touch 32 lines at a time.
+    auto dots = [&](auto &&row, const float4 *q, float (&out)[ROWS]) {
         float4 x[DH / 4];
 #pragma unroll
-        for (int c = 0; c < DH / 4; ++c)
-            x[c] = row ? __ldg(reinterpret_cast<const float4 *>(row) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < DH / 4; ++c) {
+            const float *src = row(2 * c + (lane >> 4));
+            x[c] = src ? __ldg(reinterpret_cast<const float4 *>(src) + (lane & 15))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int c = 0; c < DH / 4; ++c)
+            *reinterpret_cast<float4 *>(rows32 + (2 * c + (lane >> 4)) * SLD + 4 * (lane & 15)) = x[c];
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < DH / 4; ++c) x[c] = *reinterpret_cast<const float4 *>(rows32 + lane * SLD + 4 * c);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
             if (i >= rows) break;
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -101,22 +122,24 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
             out[i] = s0 + s1;
         }
     };
-    // (q + v).r of table row `row` into ring column col (below RW), when keep
-    auto table_dots = [&](int row, int col, bool keep) {
-        float c[16];
-        dots(row >= 0 && row < p.r_rows ? table + (long long)row * DH : nullptr, qv, c);
+    // (q + v).r of table rows row0 .. row0 + 31 (outside the table: zero); this lane's into
+    // ring column col, when keep
+    auto table_dots = [&](int row0, int col, bool keep) {
+        float c[ROWS];
+        dots([&](int x) { return row0 + x >= 0 && row0 + x < p.r_rows ? table + (long long)(row0 + x) * DH : nullptr; },
+             qv, c);
         TXL_CHECK(!keep || (col >= 0 && col < RW), p.status);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < ROWS; ++i)
             if (i < rows && keep) ring[i * RW + col] = c[i];
     };
     // Masked scores (log2 units) of this lane's key into the running softmax, then
     // P.V over the chunk's value rows.  value(key): the row, or null (zero).  mixed: keys
     // may be hidden from some nodes only (bit i of this lane's `hidden`); the value,
     // which may be an infinity or NaN, then must not reach them.
-    auto step = [&](float (&s)[16], bool mixed, unsigned hidden, auto &&value) {
+    auto step = [&](float (&s)[ROWS], bool mixed, unsigned hidden, auto &&value) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             if (i >= rows) break;
             float mx = s[i];
 #pragma unroll
@@ -141,7 +164,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             if (i >= rows) break;
 #pragma unroll
             for (int c = 0; c < GK / 4; ++c) {
@@ -160,22 +183,22 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
 
     if (rows > 0 && split == p.n_splits - 1 && kg == KG - 1) {
         // ---- the nodes among themselves: distances 0 .. DCAP - 1 ------------------
-        for (int c = 0; c < DCAP; c += 32) table_dots(p.r_rows - DCAP + c + lane, c + lane, c + lane < DCAP);
+        for (int c = 0; c < DCAP; c += 32) table_dots(p.r_rows - DCAP + c, c + lane, c + lane < DCAP);
         __syncwarp();
         const float *kn = static_cast<const float *>(p.k.ptr) + b * p.k.sb + h * p.k.sh;
         const float *vn = static_cast<const float *>(p.v.ptr) + b * p.v.sb + h * p.v.sh;
-        const int a_end = mt * 16 + rows;  // (no node is an ancestor of an earlier one)
+        const int a_end = mt * ROWS + rows;  // (no node is an ancestor of an earlier one)
         for (int a0 = 0; a0 < a_end; a0 += GK) {
             const int a = a0 + lane;
-            float s[16];
-            dots(a < a_end ? kn + a * p.k.sr : nullptr, qu, s);
+            float s[ROWS];
+            dots([&](int x) { return a0 + x < a_end ? kn + (a0 + x) * p.k.sr : nullptr; }, qu, s);
             const int da = a < a_end ? topo.depth[a] : 0;
             unsigned hidden = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 if (i >= rows) break;
-                const int dist = topo.depth[mt * 16 + i] - da;
-                const bool seen = a < a_end && ((topo.anc[mt * 16 + i] >> a) & 1) && dist < p.r_rows;
+                const int dist = topo.depth[mt * ROWS + i] - da;
+                const bool seen = a < a_end && ((topo.anc[mt * ROWS + i] >> a) & 1) && dist < p.r_rows;
                 TXL_CHECK(!seen || (dist >= 0 && dist < DCAP), p.status);
                 hidden |= seen ? 0u : 1u << i;
                 s[i] = seen ? (s[i] + ring[i * RW + DCAP - 1 - dist]) * p.scale_log2 : -INFINITY;
@@ -185,7 +208,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
     }
     if (rows > 0 && ck.count > 0)  // the DCAP table rows before the first chunk's
         for (int c = 0; c < DCAP; c += 32)
-            table_dots(p.r_rows - 1 - fill + ck.c0 * GK - ck.off - DCAP + c + lane, c + lane,
+            table_dots(p.r_rows - 1 - fill + ck.c0 * GK - ck.off - DCAP + c, c + lane,
                        c + lane < DCAP);
 
     // ---- the memory, chunk by chunk ---------------------------------------------
@@ -198,19 +221,19 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
         const float *vp = static_cast<const float *>(p.vpage) + at;
         const int key_lo = -j0, key_hi = page >= 0 ? fill - j0 : 0;  // memory rows of the chunk
         const bool mine = lane >= key_lo && lane < key_hi;
-        float s[16];
-        dots(mine ? kp + lane * DH : nullptr, qu, s);
+        float s[ROWS];
+        dots([&](int x) { return x >= key_lo && x < key_hi ? kp + x * DH : nullptr; }, qu, s);
         int col = wpos + lane;
         col -= col >= RW ? RW : 0;
-        table_dots(p.r_rows - 1 - fill + j0 + lane, col, true);
+        table_dots(p.r_rows - 1 - fill + j0, col, true);
         __syncwarp();
         const int reach = fill - p.r_rows - j0;  // depth d sees keys above reach + d
         const bool mixed = reach + depth_max >= 0;
         unsigned hidden = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             if (i >= rows) break;
-            const int d = topo.depth[mt * 16 + i];
+            const int d = topo.depth[mt * ROWS + i];
             int x = wpos + lane - d;
             x += x < 0 ? RW : 0;
             x -= x >= RW ? RW : 0;
@@ -227,12 +250,12 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
 
     // ---- this warp's record, over its ring ----------------------------------------
     const auto rec = [smem](int w) {
-        return reinterpret_cast<Rec *>(smem + C::OFF_WARP + w * C::WARP * 4);
+        return reinterpret_cast<Rec<ROWS> *>(smem + C::OFF_WARP + w * C::STEP);
     };
     __syncwarp();
-    Rec *r = rec(warp);
+    Rec<ROWS> *r = rec(warp);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         if (i >= rows) break;
         float sum = l[i];
 #pragma unroll
@@ -243,7 +266,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
         }
         reinterpret_cast<float2 *>(r->a[i])[lane] = make_float2(acc[i][0], acc[i][1]);
     }
-    finish<MT, float>(rec, p, b, h, n, warp, lane);
+    finish<WARPS, ROWS, MT, float>(rec, p, b, h, n, warp, lane);
 }
 
 cudaError_t ensure_attr()
@@ -259,6 +282,7 @@ cudaError_t ensure_attr()
     if ((e = set(relattn_tree_f32_kernel<1>, CfgF32<1>::SMEM)) != cudaSuccess) return e;
     if ((e = set(relattn_tree_f32_kernel<2>, CfgF32<2>::SMEM)) != cudaSuccess) return e;
     if ((e = set(relattn_tree_f32_kernel<4>, CfgF32<4>::SMEM)) != cudaSuccess) return e;
+    if ((e = set(relattn_tree_f32_kernel<MAX_MT>, CfgF32<MAX_MT>::SMEM)) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
     return cudaSuccess;
 }
@@ -269,9 +293,12 @@ cudaError_t launch_relattn_tree_f32(const TreeParams &p, cudaStream_t s)
 {
     const cudaError_t e = ensure_attr();
     if (e != cudaSuccess) return e;
-    if (p.N <= 16) return launch_clusters(relattn_tree_f32_kernel<1>, p, CfgF32<1>::SMEM, s, p);
-    if (p.N <= 32) return launch_clusters(relattn_tree_f32_kernel<2>, p, CfgF32<2>::SMEM, s, p);
-    return launch_clusters(relattn_tree_f32_kernel<4>, p, CfgF32<4>::SMEM, s, p);
+    const int mt = (p.N + ROWS - 1) / ROWS;
+    const auto run = [&](auto *kern, int smem) { return launch_clusters(kern, p, WARPS * 32, smem, s, p); };
+    if (mt <= 1) return run(relattn_tree_f32_kernel<1>, CfgF32<1>::SMEM);
+    if (mt <= 2) return run(relattn_tree_f32_kernel<2>, CfgF32<2>::SMEM);
+    if (mt <= 4) return run(relattn_tree_f32_kernel<4>, CfgF32<4>::SMEM);
+    return run(relattn_tree_f32_kernel<MAX_MT>, CfgF32<MAX_MT>::SMEM);
 }
 
 } // namespace txl

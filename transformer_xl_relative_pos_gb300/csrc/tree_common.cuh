@@ -3,9 +3,9 @@
 // ancestors, the split of a memory's keys, and the merge of the warps' and the
 // blocks' partial results.
 //
-// A block has four warps.  A warp holds 16 of the tree's nodes (node tile mt)
-// and takes a range of the keys (key group kg): with MT node tiles there are
-// 4 / MT key groups.  The blocks of one (batch, head) are a thread-block cluster;
+// A block's NW warps that compute hold ROWS of the tree's nodes each (node tile mt)
+// and take a range of the keys (key group kg): with MT node tiles there are
+// NW / MT key groups.  The blocks of one (batch, head) are a thread-block cluster;
 // its key groups share the memory in contiguous runs of 32-key chunks.
 #pragma once
 
@@ -24,7 +24,6 @@ using decode::ld_cluster_f32;
 using decode::ld_cluster_f32x2;
 
 constexpr int DH = kTcDH;  // 64
-constexpr int WARPS = 4;
 constexpr int GK = 32;     // keys per chunk
 
 // max that keeps a NaN: a row with a NaN score gives NaN, as the formula does.
@@ -48,6 +47,28 @@ struct Topology {
     int depth[kTreeMaxNodes];
     int hop[kTreeMaxNodes];
 };
+
+// Sequence of this block: the ranks of the grid (rank = block / (H * n_splits)) in
+// order, or, by_length, longest memory first: with more blocks than are resident at
+// once and unlike lengths, the blocks that start last are then the short ones.
+// All threads of the block, of which there are at least B; scratch: B + 1 ints.
+__device__ __forceinline__ int pick_sequence(const TreeParams &p, int rank, int *scratch)
+{
+    if (!p.by_length) return rank;
+    const int B = p.mem.B, i = threadIdx.x;
+    const int mine = i < B ? p.mem.fill[i] : 0;
+    if (i < B) scratch[i] = mine;
+    __syncthreads();
+    if (i < B) {
+        int before = 0;
+        for (int j = 0; j < B; ++j) before += scratch[j] > mine || (scratch[j] == mine && j < i);
+        if (before == rank) scratch[B] = i;
+    }
+    __syncthreads();
+    const int b = scratch[B];
+    __syncthreads();  // the scratch is free again
+    return b;
+}
 
 // By pointer doubling: after round r a node knows its 2^r nearest ancestors.  A
 // parent that is not an earlier node counts as none, so there is no cycle.  All
@@ -139,12 +160,13 @@ __device__ __forceinline__ bool next_chunk(const PagedView &m, int &slot, int &r
     return true;
 }
 
-// One warp's result for its 16 nodes: running maximum (log2 units), sum of
+// One warp's result for its nodes: running maximum (log2 units), sum of
 // probabilities, unnormalised output.
+template <int ROWS>
 struct Rec {
-    float m[16];
-    float l[16];
-    float a[16][DH];
+    float m[ROWS];
+    float l[ROWS];
+    float a[ROWS][DH];
 };
 
 __device__ __forceinline__ void put_row(__nv_bfloat16 *dst, int lane, float x, float y)
@@ -160,17 +182,17 @@ __device__ __forceinline__ void put_row(float *dst, int lane, float x, float y)
 // Every thread of the block, after each warp wrote its record (warp w's at
 // rec(w), w = kg * MT + mt): merge the key groups of each node, then the blocks
 // of the cluster, whose warps share the nodes; write out and lse of the n nodes.
-template <int MT, typename T, typename RecOf>
+template <int NW, int ROWS, int MT, typename T, typename RecOf>
 __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, int h, int n, int warp,
                                        int lane)
 {
-    constexpr int KG = WARPS / MT;
+    constexpr int KG = NW / MT;
     constexpr float LN2 = 0.69314718055994531f;
     T *out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + b * p.out.sb + h * p.out.sh;
     float *lse = p.lse ? p.lse + ((long long)b * p.mem.H + h) * p.N : nullptr;
     __syncthreads();
-    for (int i = warp; i < n; i += WARPS) {
-        const int mt = i / 16, ii = i % 16;
+    for (int i = warp; i < n; i += NW) {
+        const int mt = i / ROWS, ii = i % ROWS;
         float mx = -INFINITY;
 #pragma unroll
         for (int g = 0; g < KG; ++g) mx = max_nan(mx, rec(g * MT + mt)->m[ii]);
@@ -178,7 +200,7 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
         if (mx != -INFINITY) {
 #pragma unroll
             for (int g = 0; g < KG; ++g) {
-                const Rec *r = rec(g * MT + mt);
+                const Rec<ROWS> *r = rec(g * MT + mt);
                 if (r->m[ii] == -INFINITY) continue;
                 const float w = ex2f(r->m[ii] - mx);
                 const float2 a = reinterpret_cast<const float2 *>(r->a[ii])[lane];
@@ -195,7 +217,7 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
         } else {
             // this block's normalised partial, in place of key group 0's (each lane
             // overwrites what it alone has read)
-            Rec *r = rec(mt);
+            Rec<ROWS> *r = rec(mt);
             reinterpret_cast<float2 *>(r->a[ii])[lane] = make_float2(o0 * inv, o1 * inv);
             __syncwarp();
             if (lane == 0) r->m[ii] = lse2;
@@ -203,10 +225,10 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
     }
     if (p.n_splits == 1) return;
     cluster_sync();
-    for (int i = (int)cluster_rank() * WARPS + warp; i < n; i += WARPS * p.n_splits) {
-        const Rec *r = rec(i / 16);
-        const uint32_t a_lse = smem_u32(&r->m[i % 16]);
-        const uint32_t a_o = smem_u32(&r->a[i % 16][2 * lane]);
+    for (int i = (int)cluster_rank() * NW + warp; i < n; i += NW * p.n_splits) {
+        const Rec<ROWS> *r = rec(i / ROWS);
+        const uint32_t a_lse = smem_u32(&r->m[i % ROWS]);
+        const uint32_t a_o = smem_u32(&r->a[i % ROWS][2 * lane]);
         float part[kTreeMaxCluster];
         float mx = -INFINITY;
 #pragma unroll
@@ -233,17 +255,26 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
     cluster_sync();  // the others have read this block's shared memory
 }
 
+// The barriers of finish, for warps that have no results.
+__device__ __forceinline__ void finish_barriers(const TreeParams &p)
+{
+    __syncthreads();
+    if (p.n_splits == 1) return;
+    cluster_sync();
+    cluster_sync();
+}
+
 // Launch KERN with one cluster of n_splits blocks per (batch, head).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), const TreeParams &p, int smem, cudaStream_t s,
-                            const Args &...args)
+cudaError_t launch_clusters(void (*kern)(KArgs...), const TreeParams &p, int threads, int smem,
+                            cudaStream_t s, const Args &...args)
 {
     const long long blocks = (long long)p.mem.B * p.mem.H * p.n_splits;
     if (blocks <= 0 || blocks > 0x7fffffffLL || p.n_splits > kTreeMaxCluster)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    cfg.blockDim = dim3(WARPS * 32, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
