@@ -118,6 +118,19 @@ __device__ __forceinline__ uint32_t swz(int row, int c)
     return (uint32_t)(row * ROWB + ((c ^ (row & 7)) << 4));
 }
 
+// Scratch accesses by 32-bit shared-memory address.
+__device__ __forceinline__ float ld_scr(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_scr2(uint32_t addr, float x, float y)
+{
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -144,10 +157,11 @@ struct State {
     float acc[8][4];
 };
 
-// One chunk's masked scores s (log2 units; s[nt][2 r + e]: row r of this lane, key
+// One chunk's masked scores s (before the scale; s[nt][2 r + e]: row r of this lane, key
 // 8 nt + 2 t + e) into probabilities, rescaling the state to the new maximum.
+// scale > 0, to log2 units.
 template <int NR>
-__device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR])
+__device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR], float scale)
 {
     float mx[NR], ms[NR];
     bool moved = false;
@@ -159,13 +173,13 @@ __device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR
         mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
         // a row without a visible key so far: any finite value makes its probabilities zero
-        ms[r] = mx[r] == -INFINITY ? 0.f : mx[r];
+        ms[r] = mx[r] == -INFINITY ? 0.f : mx[r] * scale;
         moved |= !(mx[r] == st.m[r]);
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            const float f = ex2f(st.m[r] - ms[r]);  // (0 from -inf: the sums are zero then)
+            const float f = ex2f(fmaf(st.m[r], scale, -ms[r]));  // (0 from -inf: the sums are zero then)
             st.m[r] = mx[r];
             st.l[r] *= f;
 #pragma unroll
@@ -179,8 +193,8 @@ __device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR
         float sum[4];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-            s[nt][2 * r] = ex2f(s[nt][2 * r] - ms[r]);
-            s[nt][2 * r + 1] = ex2f(s[nt][2 * r + 1] - ms[r]);
+            s[nt][2 * r] = ex2f(fmaf(s[nt][2 * r], scale, -ms[r]));
+            s[nt][2 * r + 1] = ex2f(fmaf(s[nt][2 * r + 1], scale, -ms[r]));
             sum[nt] = s[nt][2 * r] + s[nt][2 * r + 1];
         }
         st.l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -351,6 +365,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     const uint8_t *ring = smem + kg * NSTG * STAGE;
     uint64_t *full = bars + kg * NSTG, *empty = full + KG * NSTG;
     float *scr = reinterpret_cast<float *>(smem + C::OFF_SCR + warp * C::SCR);
+    const uint32_t scr_at = smem_u32(scr);
     const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split * KG + kg, p.n_splits * KG);
     const int trow0 = p.r_rows - 1 - fill + ck.c0 * GK - ck.off;  // table row of the first chunk's key 0
 
@@ -358,6 +373,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     // g, g + 8 of the tile's q; u and v, alike in every row.  HALF: au holds q in rows g
     // and u in rows g + 8, av q and v; a product's two rows are then added.
     const int i0 = mt * 16 + g;  // this lane's first node (the second: + 8)
+    // With the scale's sign in the A operands (zeros for scale 0) the scores want a
+    // positive factor only.
+    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u, some = p.scale_log2 == 0.f ? 0u : ~0u;
     uint32_t aq[4][4], au[4][4], av[4][4];
     {
         const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q.ptr) + b * p.q.sb + h * p.q.sh;
@@ -371,9 +390,11 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
                     aq[ks][2 * half + r] =
-                        i0 + 8 * r < n ? reinterpret_cast<const uint32_t *>(qb + (i0 + 8 * r) * p.q.sr)[w] : 0;
-                au[ks][2 * half + 1] = __ldg(urow + w);
-                av[ks][2 * half + 1] = __ldg(vrow + w);
+                        i0 + 8 * r < n
+                            ? (reinterpret_cast<const uint32_t *>(qb + (i0 + 8 * r) * p.q.sr)[w] ^ sign) & some
+                            : 0;
+                au[ks][2 * half + 1] = (__ldg(urow + w) ^ sign) & some;
+                av[ks][2 * half + 1] = (__ldg(vrow + w) ^ sign) & some;
                 au[ks][2 * half] = HALF ? aq[ks][2 * half] : au[ks][2 * half + 1];
                 av[ks][2 * half] = HALF ? aq[ks][2 * half] : av[ks][2 * half + 1];
             }
@@ -382,8 +403,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         TXL_CHECK(col >= 0 && col + 8 <= RW, p.status);
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-            *reinterpret_cast<float2 *>(scr + (g + 8 * r) * LD + col + 2 * t) =
-                make_float2(element<HALF>(c, r, 0), element<HALF>(c, r, 1));
+            st_scr2(scr_at + ((g + 8 * r) * LD + col + 2 * t) * 4, element<HALF>(c, r, 0), element<HALF>(c, r, 1));
     };
     // 32 contiguous bytes' worth of a row in fragment order: word x holds dimensions
     // 8 x + 2 t, + 1 (words 2 ks, 2 ks + 1: step ks).
@@ -529,11 +549,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const bool seen = a < n && ((anc[r] >> a) & 1) && dist < p.r_rows;
                     TXL_CHECK(!seen || (dist >= 0 && dist < DCAP), p.status);
                     hidden |= seen ? 0u : 1u << (4 * nt + e);
-                    s[nt][e] = seen ? (element<HALF>(c[nt], r, e & 1) + scr[(g + 8 * r) * LD + DCAP - 1 - dist]) *
-                                          p.scale_log2
+                    s[nt][e] = seen ? element<HALF>(c[nt], r, e & 1) + scr[(g + 8 * r) * LD + DCAP - 1 - dist]
                                     : -INFINITY;
                 }
-            softmax_step(st, s);
+            softmax_step(st, s, scale);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -606,16 +625,15 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 const int first = next + DCAP + 2 * t - depth[r];
-                const float *at = scr + (g + 8 * r) * LD + first;
+                const uint32_t at = scr_at + ((g + 8 * r) * LD + first) * 4;
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int jj = 8 * nt + e;
-                        const float *from = jj >= RW - first ? at - RW : at;
-                        TXL_CHECK(from + jj >= scr + (g + 8 * r) * LD && from + jj < scr + (g + 8 * r) * LD + RW,
-                                  p.status);
-                        s[nt][2 * r + e] = (element<HALF>(c[nt], r, e) + from[jj]) * p.scale_log2;
+                        const bool wraps = jj >= RW - first;
+                        TXL_CHECK(first + jj - (wraps ? RW : 0) >= 0 && first + jj - (wraps ? RW : 0) < RW, p.status);
+                        s[nt][2 * r + e] = element<HALF>(c[nt], r, e) + ld_scr((wraps ? at - RW * 4 : at) + 4 * jj);
                     }
             }
             // Keys that are not memory rows (the chunk sticks out at either end, or its
@@ -637,7 +655,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                         }
                     }
             }
-            softmax_step(st, s);
+            softmax_step(st, s, scale);
             bool bad = false;
             if (partly_hidden) {
                 // lane = key: does a memory row hold an infinity or NaN
@@ -703,7 +721,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
         if (t == 0) {
-            mine->m[g + 8 * r] = st.m[r];
+            mine->m[g + 8 * r] = st.m[r] * scale;  // log2 units
             mine->l[g + 8 * r] = st.l[r];
         }
 #pragma unroll

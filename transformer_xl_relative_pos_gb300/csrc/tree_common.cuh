@@ -201,8 +201,7 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
 #pragma unroll
             for (int g = 0; g < KG; ++g) {
                 const Rec<ROWS> *r = rec(g * MT + mt);
-                if (r->m[ii] == -INFINITY) continue;
-                const float w = ex2f(r->m[ii] - mx);
+                const float w = ex2f(r->m[ii] - mx);  // (0 from -inf)
                 const float2 a = reinterpret_cast<const float2 *>(r->a[ii])[lane];
                 ls += w * r->l[ii];
                 o0 = fmaf(w, a.x, o0);
@@ -240,7 +239,7 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
         if (mx != -INFINITY) {
 #pragma unroll
             for (int s = 0; s < kTreeMaxCluster; ++s) {
-                if (part[s] == -INFINITY) continue;
+                if (s >= p.n_splits) continue;
                 const float w = ex2f(part[s] - mx);
                 const float2 o = ld_cluster_f32x2(cluster_addr(a_o, (uint32_t)s));
                 ws += w;
