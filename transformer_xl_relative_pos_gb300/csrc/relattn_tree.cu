@@ -33,9 +33,9 @@
 // whatever the page holds: their scores are masked and their values, which
 // may be NaN, are zeroed in the fragments.
 //
-// The nodes' own keys and values, and the table rows before a group's first
-// chunk, are few: they go from global memory straight into fragments while
-// the first copies are on their way.
+// The nodes' own keys and values come through the ring of the last group, ahead of its
+// chunks; the table rows before a group's first chunk go from global memory straight into
+// fragments while the first copies are on their way.
 #include "tree_common.cuh"
 
 namespace txl {
@@ -47,7 +47,7 @@ constexpr int WARPS = 4, ROWS = 16;        // warps that compute, nodes of a war
 constexpr int THREADS = 2 * WARPS * 32;    // and as many for the copies, one per key group
 // Registers a thread of the two kinds (warpgroups) after the split of the 128 that two
 // blocks of 256 threads per SM leave; their sum must not exceed 256.
-constexpr int REGS_COMPUTE = 216, REGS_COPY = 40;
+constexpr int REGS_COMPUTE = 208, REGS_COPY = 48;
 static_assert(REGS_COMPUTE + REGS_COPY <= 256, "the block's registers at launch");
 constexpr int ROWB = DH * 2;               // bytes of a row
 constexpr int BOX = GK * ROWB;             // 4096: one 32-row box
@@ -140,6 +140,21 @@ __device__ __forceinline__ uint32_t split_bf16x2(float x0, float x1, uint32_t &r
     const uint32_t hi = pack_bf16x2(x0, x1);
     res = pack_bf16x2(x0 - bf_lo(hi), x1 - bf_hi(hi));
     return hi;
+}
+
+// 16 bytes into shared memory without passing through registers, or zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// The mbarrier's phase also waits for this thread's copies so far (its pending count
+// is raised by one until they are there).
+__device__ __forceinline__ void cp_async_hold(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // A bf16 whose exponent bits are all ones (infinity or NaN) in either half.
@@ -288,6 +303,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     paged_state(p.mem, b, p.status, begin, fill);
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
     if (n == 0) return;  // (every block of the cluster)
+    const int parent = threadIdx.x < n ? p.parents[b * p.parents_stride + threadIdx.x] : -1;
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // full, then empty, [KG][NSTG]
     volatile int *stage_ok = reinterpret_cast<volatile int *>(smem + C::OFF_OK);
@@ -305,48 +321,72 @@ __global__ void __launch_bounds__(THREADS, 2)
         // The id of a page is loaded an item ahead.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
         const int group = warp - WARPS;
-        const bool mine = group < KG && lane == 0;
-        Chunks ck{};
-        int slot = 0, row = 0, page = -1, issued = 0;
-        uint64_t *full = bars + group * NSTG, *empty = full + KG * NSTG;
-        const uint64_t pol_stream = policy_evict_first();  // k, v: read once
-        const uint64_t pol_keep = policy_evict_last();     // table: shared by the batch
-        auto issue = [&]() {
-            const int st = group * NSTG + issued % NSTG;
-            const int plane = page >= 0 ? page * p.mem.H + h : p.mem.n_pages * p.mem.H;
-            uint64_t *bar = bars + st;
-            stage_ok[st] = page >= 0;
-            uint8_t *dst = smem + st * STAGE;
-            mbar_arrive_expect_tx(bar, (uint32_t)STAGE);
-            tma_load_3d_hint(dst + ST_K, &tm_k, bar, 0, row, plane, pol_stream);
-            tma_load_3d_hint(dst + ST_V, &tm_v, bar, 0, row, plane, pol_stream);
-            tma_load_3d_hint(dst + ST_R, &tm_r, bar, 0,
-                             p.r_rows - 1 - fill + (ck.c0 + issued) * GK - ck.off, h, pol_keep);
-            ++issued;
-            if (next_chunk(p.mem, slot, row) && issued < ck.count) page = page_at(p.mem, b, slot, p.status);
-        };
+        const bool mine = group < KG;
         if (warp == WARPS && lane == 0) *abort_flag = 0;
-        if (mine) {
-            ck = group_chunks(p, begin, fill, kNodesCost, split * KG + group, p.n_splits * KG);
-            slot = ck.slot;
-            row = ck.row;
-            if (ck.count > 0) page = page_at(p.mem, b, slot, p.status);
+        if (mine && lane == 0) {
             for (int s = 0; s < NSTG; ++s) {
-                mbar_init(full + s, 1);
-                mbar_init(empty + s, MT);
+                mbar_init(bars + group * NSTG + s, 1);
+                mbar_init(bars + (KG + group) * NSTG + s, MT);
             }
             fence_barrier_init();
-            while (issued < min(NSTG, ck.count)) issue();
         }
         __syncwarp();
-        build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
-        if (mine) {
-            // refill each stage when the group's warps have left it
-            bool ok = true;
-            while (ok && issued < ck.count) {
-                ok = mbar_wait(empty + issued % NSTG, (issued / NSTG + 1) & 1, abort_flag, p.wait_ns);
-                if (ok) issue();
+        Chunks ck{};
+        if (mine) ck = group_chunks(p, begin, fill, kNodesCost, split * KG + group, p.n_splits * KG);
+        const int nodes = split == p.n_splits - 1 && group == KG - 1 ? (n + GK - 1) / GK : 0;
+        const int items = mine ? nodes + ck.count : 0;
+        int slot = ck.slot, row = ck.row, page = -1;
+        if (mine && ck.count > 0 && lane == 0) page = page_at(p.mem, b, slot, p.status);
+        const uint64_t pol_stream = policy_evict_first();  // k, v: read once
+        const uint64_t pol_keep = policy_evict_last();     // table: shared by the batch
+        const int trow0 = p.r_rows - 1 - fill + ck.c0 * GK - ck.off;  // table row of the first chunk's key 0
+        // One item into its stage (the whole warp): for the group that takes the nodes
+        // among themselves boxes of them, then its chunks.
+        auto issue = [&](int item) {
+            const int st = group * NSTG + item % NSTG;
+            uint64_t *bar = bars + st;
+            uint8_t *dst = smem + st * STAGE;
+            if (item < nodes) {
+                // 32 rows of the nodes' k and v (past the last: zeros), swizzled as TMA does
+                const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.k.ptr) + b * p.k.sb + h * p.k.sh;
+                const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.v.ptr) + b * p.v.sb + h * p.v.sh;
+                const uint32_t at = smem_u32(dst);
+#pragma unroll 2
+                for (int x = lane; x < GK * 8; x += 32) {
+                    const int a = item * GK + (x >> 3), c = x & 7;
+                    const bool there = a < n;
+                    cp_async16(at + ST_K + swz(x >> 3, c), kn + (there ? a * p.k.sr + 8 * c : 0), there);
+                    cp_async16(at + ST_V + swz(x >> 3, c), vn + (there ? a * p.v.sr + 8 * c : 0), there);
+                }
+                cp_async_hold(bar);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            } else if (lane == 0) {
+                fence_proxy_async_smem();  // (the stage may have held nodes, written without TMA)
+                const int plane = page >= 0 ? page * p.mem.H + h : p.mem.n_pages * p.mem.H;
+                stage_ok[st] = page >= 0;
+                mbar_arrive_expect_tx(bar, (uint32_t)STAGE);
+                tma_load_3d_hint(dst + ST_K, &tm_k, bar, 0, row, plane, pol_stream);
+                tma_load_3d_hint(dst + ST_V, &tm_v, bar, 0, row, plane, pol_stream);
+                tma_load_3d_hint(dst + ST_R, &tm_r, bar, 0, trow0 + (item - nodes) * GK, h, pol_keep);
+                if (next_chunk(p.mem, slot, row) && item + 1 < items) page = page_at(p.mem, b, slot, p.status);
             }
+        };
+        int issued = 0;
+        for (; issued < min(NSTG, items); ++issued) issue(issued);
+        __syncwarp();
+        build_topology(topo, parent, n, p.status);
+        // refill each stage when the group's warps have left it
+        bool ok = true;
+        for (; issued < items; ++issued) {
+            if (lane == 0)
+                ok = mbar_wait(bars + (KG + group) * NSTG + issued % NSTG, (issued / NSTG + 1) & 1, abort_flag,
+                               p.wait_ns);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            issue(issued);
+        }
+        if (lane == 0) {
             if (!ok) {
                 *abort_flag = 1;
                 atomicOr(p.status, TXL_STATUS_TIMEOUT);
@@ -354,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             // the copies in flight land before shared memory is used for anything else
             const int zero = 0;
             for (int x = max(0, issued - NSTG); x < issued; ++x)
-                mbar_wait(full + x % NSTG, (x / NSTG) & 1, &zero, p.wait_ns);
+                mbar_wait(bars + group * NSTG + x % NSTG, (x / NSTG) & 1, &zero, p.wait_ns);
         }
         __syncwarp();
         finish_barriers(p);
@@ -440,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // not reach the nodes that do not see the key.  hidden: bit 4 nt + 2 r + e of this
     // lane's elements.  col0: 32 free ring columns.
     State<NR> st;
-    auto pv_by_element = [&](const auto &s, uint32_t hidden, int col0, auto &&value) {
+    auto pv_by_element = [&](const auto &s, uint32_t hidden, int col0, const uint8_t *values) {
         auto at = [&](int key) { const int c = col0 + key; return c >= RW ? c - RW : c; };
         __syncwarp();
 #pragma unroll
@@ -450,60 +490,56 @@ __global__ void __launch_bounds__(THREADS, 2)
                 scr[(g + 8 * (e >> 1)) * LD + at(8 * nt + 2 * t + (e & 1))] =
                     (hidden >> (4 * nt + e)) & 1 ? -1.f : s[nt][e];
         __syncwarp();
+#pragma unroll 1
         for (int key = 0; key < GK; ++key) {
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 const float pr = scr[(g + 8 * r) * LD + at(key)];
                 if (pr < 0.f) continue;
 #pragma unroll
-                for (int nd = 0; nd < 8; ++nd)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        st.acc[nd][2 * r + e] = fmaf(pr, value(key, 8 * nd + 2 * t + e), st.acc[nd][2 * r + e]);
+                for (int nd = 0; nd < 8; ++nd) {
+                    const uint32_t v2 = *reinterpret_cast<const uint32_t *>(values + swz(key, nd) + 4 * t);
+                    st.acc[nd][2 * r] = fmaf(pr, bf_lo(v2), st.acc[nd][2 * r]);
+                    st.acc[nd][2 * r + 1] = fmaf(pr, bf_hi(v2), st.acc[nd][2 * r + 1]);
+                }
             }
         }
         __syncwarp();
     };
+    // Whether a value row lo .. hi - 1 of a box holds an infinity or NaN (lane = key).
+    auto nonfinite_values = [&](const uint8_t *values, int lo, int hi) {
+        bool bad = false;
+        if (lane >= lo && lane < hi) {
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(values + swz(lane, x));
+                bad |= nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
+            }
+        }
+        return __any_sync(0xffffffffu, bad) != 0;
+    };
+    const int lr = lane & 7, lm = lane >> 3;  // matrix-load roles: row, matrix
+    // V fragments of keys 16 kk .. 16 kk + 15 of a box
+    auto load_v = [&](uint32_t (&bv)[8][2], uint32_t sv, int kk) {
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            uint32_t w[4];
+            ldsm_x4_t(w, sv + swz(16 * kk + (lm & 1) * 8 + lr, 2 * np + (lm >> 1)));
+            bv[2 * np][0] = w[0];
+            bv[2 * np][1] = w[1];
+            bv[2 * np + 1][0] = w[2];
+            bv[2 * np + 1][1] = w[3];
+        }
+    };
 
     const bool active = mt * 16 < n;  // this warp has nodes
-    // The last group takes the nodes among themselves.  What that needs from global
-    // memory is loaded ahead of the tree's construction, and otherwise the table rows
-    // before the first chunk's.
-    const bool owner = active && split == p.n_splits - 1 && kg == KG - 1;
-    const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.k.ptr) + b * p.k.sb + h * p.k.sh;
-    const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.v.ptr) + b * p.v.sb + h * p.v.sh;
-    // (no node is an ancestor of an earlier one: this tile's nodes see nodes up to their own)
-    const int a_end = min(n, mt * 16 + 16);
-    uint32_t kw[4][8], vw[2][8][2], tw[TB][8];
-    auto load_nodes = [&](int a0) {
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            const int a = a0 + 8 * nt + g;
-            load_row(kw[nt], kn + a * p.k.sr, a < a_end);
-        }
-        // V fragments: rows (keys) 16 kk + 2 t, + 1 and + 8, + 9, column 8 nd + g
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int key = a0 + 16 * kk + 8 * x + 2 * t;
-                const __nv_bfloat16 *src = vn + key * p.v.sr + g;
-#pragma unroll
-                for (int nd = 0; nd < 8; ++nd) {
-                    uint32_t w = 0;
-                    if (key < a_end) w = __bfloat16_as_ushort(src[8 * nd]);
-                    if (key + 1 < a_end) w |= (uint32_t)__bfloat16_as_ushort(src[p.v.sr + 8 * nd]) << 16;
-                    vw[kk][nd][x] = w;
-                }
-            }
-    };
-    if (owner) {
-        load_table(tw, p.r_rows - DCAP);
-        load_nodes(0);
-    } else if (active && ck.count > 0) {
-        load_table(tw, trow0 - DCAP);
-    }
-    build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
+    // The last group takes the nodes among themselves.  The table rows for them, or before
+    // the first chunk's, are loaded ahead of the tree's construction.
+    const bool nodes_here = split == p.n_splits - 1 && kg == KG - 1, owner = active && nodes_here;
+    const int nodes = nodes_here ? (n + GK - 1) / GK : 0;  // boxes of nodes ahead of the chunks
+    uint32_t tw[TB][8];
+    if (active && (owner || ck.count > 0)) load_table(tw, (owner ? p.r_rows : trow0) - DCAP);
+    build_topology(topo, parent, n, p.status);
     int depth[NR], depth_max = 0;
     unsigned long long anc[NR];
 #pragma unroll
@@ -521,6 +557,12 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.acc[nd][e] = 0.f;
 
+    bool ok = true;
+    if (!active)  // (a warp without nodes only lets the stages go)
+        for (int box = 0; box < nodes && ok; ++box) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full + box % NSTG, (box / NSTG) & 1, abort_flag, p.wait_ns));
+            if (lane == 0 && ok) mbar_arrive(empty + box % NSTG);
+        }
     if (owner) {
         // ---- the nodes among themselves: distances 0 .. DCAP - 1 ------------------
         table_products(tw, 0);
@@ -530,41 +572,58 @@ __global__ void __launch_bounds__(THREADS, 2)
             table_products(tw, c);
         }
         __syncwarp();
-        for (int a0 = 0; a0 < a_end; a0 += GK) {
-            if (a0 > 0) load_nodes(a0);
-            float c[4][4], s[4][2 * NR];
+        for (int box = 0; box < nodes && ok; ++box) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full + box % NSTG, (box / NSTG) & 1, abort_flag, p.wait_ns));
+            // (no node is an ancestor of an earlier one: boxes past this tile are hidden)
+            if (ok && box * GK < mt * 16 + 16) {
+                const uint8_t *base = ring + (box % NSTG) * STAGE;
+                const int a0 = box * GK;
+                float c[4][4], s[4][2 * NR];
+                const uint32_t sk = smem_u32(base + ST_K);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                q_products<HALF>(c, aq, au, ks, kw, 2 * ks);
-                bias_products<HALF>(c, au, ks, kw, 2 * ks);
-            }
-            uint32_t hidden = 0;
-            bool bad = false;
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    uint32_t bk[4][4];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+                    for (int nt = 0; nt < 4; ++nt) ldsm_x4(bk[nt], sk + swz(8 * nt + lr, 4 * h2 + lm));
 #pragma unroll
-                for (int e = 0; e < 2 * NR; ++e) {
-                    const int r = e >> 1, a = a0 + 8 * nt + 2 * t + (e & 1);
-                    const int dist = depth[r] - (a < n ? topo.depth[a] : 0);
-                    const bool seen = a < n && ((anc[r] >> a) & 1) && dist < p.r_rows;
-                    TXL_CHECK(!seen || (dist >= 0 && dist < DCAP), p.status);
-                    hidden |= seen ? 0u : 1u << (4 * nt + e);
-                    s[nt][e] = seen ? element<HALF>(c[nt], r, e & 1) + scr[(g + 8 * r) * LD + DCAP - 1 - dist]
-                                    : -INFINITY;
+                    for (int x = 0; x < 2; ++x) {
+                        q_products<HALF>(c, aq, au, 2 * h2 + x, bk, 2 * x);
+                        bias_products<HALF>(c, au, 2 * h2 + x, bk, 2 * x);
+                    }
                 }
-            softmax_step(st, s, scale);
+                uint32_t hidden = 0;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+                for (int r = 0; r < NR; ++r) {
+                    const unsigned long long mine = anc[r] >> a0;
 #pragma unroll
-                for (int nd = 0; nd < 8; ++nd) bad |= nonfinite2(vw[kk][nd][0]) | nonfinite2(vw[kk][nd][1]);
-            if (__any_sync(0xffffffffu, bad)) {
-                pv_by_element(s, hidden, DCAP, [&](int key, int dim) {
-                    return a0 + key < a_end ? __bfloat162float(vn[(a0 + key) * p.v.sr + dim]) : 0.f;
-                });
-            } else {
-                pv_step(st, s, 0, vw[0]);
-                pv_step(st, s, 1, vw[1]);
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int a = 8 * nt + 2 * t + e;
+                            const bool related = (mine >> a) & 1;
+                            const int dist = related ? depth[r] - topo.depth[a0 + a] : 0;
+                            const bool seen = related && dist < p.r_rows;
+                            TXL_CHECK(dist >= 0 && dist < DCAP, p.status);
+                            hidden |= seen ? 0u : 1u << (4 * nt + 2 * r + e);
+                            s[nt][2 * r + e] = seen ? element<HALF>(c[nt], r, e) +
+                                                          ld_scr(scr_at + ((g + 8 * r) * LD + DCAP - 1 - dist) * 4)
+                                                    : -INFINITY;
+                        }
+                }
+                softmax_step(st, s, scale);
+                if (nonfinite_values(base + ST_V, 0, GK)) {
+                    pv_by_element(s, hidden, DCAP, base + ST_V);
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        uint32_t bv[8][2];
+                        load_v(bv, smem_u32(base + ST_V), kk);
+                        pv_step(st, s, kk, bv);
+                    }
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + box % NSTG);
         }
         __syncwarp();  // the ring's columns are free again
         if (ck.count > 0) load_table(tw, trow0 - DCAP);
@@ -579,17 +638,15 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
 
     // ---- the memory, chunk by chunk ---------------------------------------------
-    const int lr = lane & 7, lm = lane >> 3;  // matrix-load roles: row, matrix
-    int wpos = DCAP;                          // ring column of the chunk's first table row
-    bool ok = true;
-    for (int item = 0; item < ck.count; ++item) {
+    int wpos = DCAP;  // ring column of the chunk's first table row
+    for (int item = nodes; ok && item < nodes + ck.count; ++item) {
         const int stg = item % NSTG;
         ok = __all_sync(0xffffffffu, mbar_wait(full + stg, (item / NSTG) & 1, abort_flag, p.wait_ns));
         if (!ok) break;
         if (active) {
             const uint8_t *base = ring + stg * STAGE;
             const uint32_t sk = smem_u32(base + ST_K), sv = smem_u32(base + ST_V), sr = smem_u32(base + ST_R);
-            const int j0 = (ck.c0 + item) * GK - ck.off;  // memory row of the chunk's first key
+            const int j0 = (ck.c0 + item - nodes) * GK - ck.off;  // memory row of the chunk's first key
 
             // content and position products, eight independent accumulators in turn (one
             // after the other, each MMA would wait for the one before)
@@ -656,36 +713,13 @@ __global__ void __launch_bounds__(THREADS, 2)
                     }
             }
             softmax_step(st, s, scale);
-            bool bad = false;
-            if (partly_hidden) {
-                // lane = key: does a memory row hold an infinity or NaN
-                if (lane >= key_lo && lane < key_hi) {
-#pragma unroll 1
-                    for (int x = 0; x < 8; ++x) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(base + ST_V + swz(lane, x));
-                        bad |= nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
-                    }
-                }
-                bad = __any_sync(0xffffffffu, bad);
-            }
-            if (bad) {
-                pv_by_element(s, hidden, next, [&](int key, int dim) {
-                    const uint8_t *at = base + ST_V + swz(key, dim >> 3) + 2 * (dim & 7);
-                    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at));
-                });
+            if (partly_hidden && nonfinite_values(base + ST_V, key_lo, key_hi)) {
+                pv_by_element(s, hidden, next, base + ST_V);
             } else {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     uint32_t bv[8][2];
-#pragma unroll
-                    for (int np = 0; np < 4; ++np) {
-                        uint32_t w[4];
-                        ldsm_x4_t(w, sv + swz(16 * kk + (lm & 1) * 8 + lr, 2 * np + (lm >> 1)));
-                        bv[2 * np][0] = w[0];
-                        bv[2 * np][1] = w[1];
-                        bv[2 * np + 1][0] = w[2];
-                        bv[2 * np + 1][1] = w[3];
-                    }
+                    load_v(bv, sv, kk);
                     if (out_of_memory) {
                         // this lane's fragment rows: keys 16 kk + 2 t, + 1 and + 8, + 9
                         const int key = 16 * kk + 2 * t;

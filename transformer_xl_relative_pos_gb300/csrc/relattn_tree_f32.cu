@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(WARPS * 32) relattn_tree_f32_kernel(const Tree
     const int b = pick_sequence(p, rank, reinterpret_cast<int *>(smem + C::OFF_TOPO));
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
     if (n == 0) return;  // (every block of the cluster)
+    const int parent = threadIdx.x < n ? p.parents[b * p.parents_stride + threadIdx.x] : -1;
 
     float *qs = reinterpret_cast<float *>(smem);
     float *ring = reinterpret_cast<float *>(smem + C::OFF_WARP + warp * C::STEP);
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(WARPS * 32) relattn_tree_f32_kernel(const Tree
         dst[0] = x + static_cast<const float *>(p.u)[h * DH + c];
         dst[ROWS * DH] = x + static_cast<const float *>(p.vb)[h * DH + c];
     }
-    build_topology(topo, p.parents + b * p.parents_stride, n, p.status);
+    build_topology(topo, parent, n, p.status);
 
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);

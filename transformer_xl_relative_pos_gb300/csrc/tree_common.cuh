@@ -72,15 +72,15 @@ __device__ __forceinline__ int pick_sequence(const TreeParams &p, int rank, int 
 
 // By pointer doubling: after round r a node knows its 2^r nearest ancestors.  A
 // parent that is not an earlier node counts as none, so there is no cycle.  All
-// threads of the block; ends with a barrier.
-__device__ __forceinline__ void build_topology(Topology &t, const int *parents, int n,
+// threads of the block, thread i with node i's parent; ends with a barrier.
+__device__ __forceinline__ void build_topology(Topology &t, int parent, int n,
                                                unsigned int *status)
 {
     const int i = threadIdx.x;
     unsigned long long anc = 0;
     int hop = -1, depth = 0;
     if (i < n) {
-        hop = parents[i];
+        hop = parent;
         if (hop < -1 || hop >= i) {
             atomicOr(status, TXL_STATUS_INDEX);
             hop = -1;
@@ -228,23 +228,30 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
         const Rec<ROWS> *r = rec(i / ROWS);
         const uint32_t a_lse = smem_u32(&r->m[i % ROWS]);
         const uint32_t a_o = smem_u32(&r->a[i % ROWS][2 * lane]);
+        // (every load on its way before the first is used; ranks past the last: rank 0
+        // again, without weight)
         float part[kTreeMaxCluster];
+        float2 o[kTreeMaxCluster];
+#pragma unroll
+        for (int s = 0; s < kTreeMaxCluster; ++s) {
+            const uint32_t from = s < p.n_splits ? s : 0;
+            part[s] = ld_cluster_f32(cluster_addr(a_lse, from));
+            o[s] = ld_cluster_f32x2(cluster_addr(a_o, from));
+        }
         float mx = -INFINITY;
 #pragma unroll
         for (int s = 0; s < kTreeMaxCluster; ++s) {
-            part[s] = s < p.n_splits ? ld_cluster_f32(cluster_addr(a_lse, (uint32_t)s)) : -INFINITY;
+            part[s] = s < p.n_splits ? part[s] : -INFINITY;
             mx = max_nan(mx, part[s]);
         }
         float ws = 0.f, o0 = 0.f, o1 = 0.f;
         if (mx != -INFINITY) {
 #pragma unroll
             for (int s = 0; s < kTreeMaxCluster; ++s) {
-                if (s >= p.n_splits) continue;
-                const float w = ex2f(part[s] - mx);
-                const float2 o = ld_cluster_f32x2(cluster_addr(a_o, (uint32_t)s));
+                const float w = ex2f(part[s] - mx);  // (0 from -inf)
                 ws += w;
-                o0 = fmaf(w, o.x, o0);
-                o1 = fmaf(w, o.y, o1);
+                o0 = fmaf(w, o[s].x, o0);
+                o1 = fmaf(w, o[s].y, o1);
             }
         }
         const float inv = ws == 0.f ? 0.f : 1.f / ws;
