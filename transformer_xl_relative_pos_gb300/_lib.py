@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -480,7 +481,7 @@ class PagedKV:
 
 # The calls on a paged memory are made once per layer and token: their checks cost
 # one comparison each where nothing is wrong.
-_Rows4 = ctypes.c_longlong * 16  # four txl_rows: pointer and three strides each
+_rows_struct = struct.Struct("@Pqqq").pack  # txl_rows
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -509,21 +510,17 @@ def _ptr(t, name: str, dtype, shape, index: int) -> int:
     _refuse(t, name, dtype, shape, index)
 
 
-def _row_operands(shape, mem: PagedKV, *operands):
-    """txl_rows, in one array, of (tensor, name) pairs of this shape [..., B, H, N, 64]."""
-    words = []
-    dtype, index = mem._dtype, mem._index
-    for t, name in operands:
-        try:
-            if t.dtype is dtype and t.get_device() == index and t.shape == shape:
-                st = t.stride()
-                if st[-1] == 1 or t.numel() == 0:
-                    words += (t.data_ptr(), *st[-4:-1])
-                    continue
-        except AttributeError:
-            pass
-        _refuse(t, name, dtype, shape, index)
-    return _Rows4(*words)
+def _row_operand(t, name: str, shape, mem: PagedKV) -> bytes:
+    """txl_rows of a tensor of this shape [..., B, H, N, 64], of the memory's dtype and
+    device."""
+    try:
+        if t.dtype is mem._dtype and t.get_device() == mem._index and t.shape == shape:
+            st = t.stride()
+            if st[-1] == 1 or t.numel() == 0:
+                return _rows_struct(t.data_ptr(), st[-4], st[-3], st[-2])
+    except AttributeError:
+        pass
+    _refuse(t, name, mem._dtype, shape, mem._index)
 
 
 def _paged_call(mem: PagedKV, name: str, stream, *args):
@@ -574,8 +571,7 @@ def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
         raise ValueError(f"k and v must be [B, H, N, dh] or [n, B, H, N, dh] of the memory, got "
                          f"{list(shape)}")
     N = width = shape[-2]
-    kv = _row_operands(shape, mem, (k, "k"), (v, "v"))
-    at = ctypes.addressof(kv)
+    rows_k, rows_v = _row_operand(k, "k", shape, mem), _row_operand(v, "v", shape, mem)
     index = mem._index
     rows_at = n_at = b_out = f_out = None
     if rows is not None:
@@ -589,7 +585,7 @@ def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
         b_out, f_out = _state_out(mem, state_out)
     elif state_out is not None:
         raise ValueError("state_out needs keep")
-    _paged_call(mem, "txl_paged_append", stream, mem._at, layer, layers, at, at + 32, layer_stride, N,
+    _paged_call(mem, "txl_paged_append", stream, mem._at, layer, layers, rows_k, rows_v, layer_stride, N,
                 rows_at, width if rows is not None else 0, n_at, width, keep or 0, b_out, f_out)
     return mem
 
@@ -646,19 +642,19 @@ def relattn_tree_fwd(q, k_new, v_new, mem: PagedKV, layer: int, r, u, v_bias, pa
         if lse is True:
             lse = torch.zeros(shape[:3], dtype=torch.float32, device=q.device)
         lse_at = _ptr(lse, "lse", torch.float32, shape[:3], index)
-    ops = _row_operands(shape, mem, (q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out"))
-    at = ctypes.addressof(ops)
     if r.dim() != 3:
         raise ValueError("r must be [H, r_rows, 64]")
     r_rows = r.shape[1]
     if n_nodes is not None:
         n_at = _ptr(n_nodes, "n_nodes", torch.int32, (B,), index)
     stride = N if parents.dim() == 2 else 0
-    _paged_call(mem, "txl_relattn_tree_fwd", stream, at, at + 32, at + 64, mem._at, layer,
+    _paged_call(mem, "txl_relattn_tree_fwd", stream, _row_operand(q, "q", shape, mem),
+                _row_operand(k_new, "k_new", shape, mem), _row_operand(v_new, "v_new", shape, mem),
+                mem._at, layer,
                 _ptr(r, "r", dt, (H, r_rows, dh), index), r_rows, _ptr(u, "u", dt, (H, dh), index),
                 _ptr(v_bias, "v_bias", dt, (H, dh), index),
                 _ptr(parents, "parents", torch.int32, (B, N) if stride else (N,), index), stride, n_at,
-                at + 96, lse_at, N, scale, n_splits)
+                _row_operand(out, "out", shape, mem), lse_at, N, scale, n_splits)
     return (out, lse) if want_lse else out
 
 

@@ -80,10 +80,10 @@ struct TreeParams {
     unsigned long long wait_ns;
 };
 
-// bf16: tm_k, tm_v over the layer's key / value planes [n_pages * H][P][64], tm_r
-// over the table [H][r_rows][64], all in boxes of 32 rows, 128-byte swizzle.
-cudaError_t launch_relattn_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                                const CUtensorMap &tm_r, const TreeParams &p, cudaStream_t s);
+// bf16: tm_kv over the layer's key planes and then its value planes [2 * n_pages * H][P][64],
+// tm_r over the table [H][r_rows][64], in boxes of 32 rows, 128-byte swizzle.
+cudaError_t launch_relattn_tree(const CUtensorMap &tm_kv, const CUtensorMap &tm_r, const TreeParams &p,
+                                cudaStream_t s);
 cudaError_t launch_relattn_tree_f32(const TreeParams &p, cudaStream_t s);
 
 } // namespace txl

@@ -280,8 +280,7 @@ __device__ __forceinline__ float element(const float (&c)[4], int r, int e)
 // and the probabilities' residuals: half the MMAs).
 template <int MT, bool HALF>
 __global__ void __launch_bounds__(THREADS, 2)
-    relattn_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v,
+    relattn_tree_kernel(const __grid_constant__ CUtensorMap tm_kv,
                         const __grid_constant__ CUtensorMap tm_r, const TreeParams p)
 {
     using C = Cfg<MT>;
@@ -363,11 +362,12 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (lane == 0) mbar_arrive(bar);
             } else if (lane == 0) {
                 fence_proxy_async_smem();  // (the stage may have held nodes, written without TMA)
-                const int plane = page >= 0 ? page * p.mem.H + h : p.mem.n_pages * p.mem.H;
+                const int planes = p.mem.n_pages * p.mem.H;  // of keys; then as many of values
+                const int plane = page >= 0 ? page * p.mem.H + h : 2 * planes;
                 stage_ok[st] = page >= 0;
                 mbar_arrive_expect_tx(bar, (uint32_t)STAGE);
-                tma_load_3d_hint(dst + ST_K, &tm_k, bar, 0, row, plane, pol_stream);
-                tma_load_3d_hint(dst + ST_V, &tm_v, bar, 0, row, plane, pol_stream);
+                tma_load_3d_hint(dst + ST_K, &tm_kv, bar, 0, row, plane, pol_stream);
+                tma_load_3d_hint(dst + ST_V, &tm_kv, bar, 0, row, page >= 0 ? plane + planes : plane, pol_stream);
                 tma_load_3d_hint(dst + ST_R, &tm_r, bar, 0, trow0 + (item - nodes) * GK, h, pol_keep);
                 if (next_chunk(p.mem, slot, row) && item + 1 < items) page = page_at(p.mem, b, slot, p.status);
             }
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             *reinterpret_cast<float2 *>(&mine->a[g + 8 * r][8 * nd + 2 * t]) =
                 make_float2(element<HALF>(st.acc[nd], r, 0), element<HALF>(st.acc[nd], r, 1));
     }
-    finish<WARPS, ROWS, MT, __nv_bfloat16>(rec, p, b, h, n, warp, lane);
+    finish<WARPS, KG, MT, __nv_bfloat16>(rec, p, b, h, n, warp, lane);
 }
 
 // The dynamic shared-memory attribute of the kernels, once per device.
@@ -787,13 +787,13 @@ cudaError_t ensure_attr()
 
 } // namespace
 
-cudaError_t launch_relattn_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                                const CUtensorMap &tm_r, const TreeParams &p, cudaStream_t s)
+cudaError_t launch_relattn_tree(const CUtensorMap &tm_kv, const CUtensorMap &tm_r, const TreeParams &p,
+                                cudaStream_t s)
 {
     const cudaError_t e = ensure_attr();
     if (e != cudaSuccess) return e;
     const auto run = [&](auto *kern, int smem) {
-        return launch_clusters(kern, p, THREADS, smem, s, tm_k, tm_v, tm_r, p);
+        return launch_clusters(kern, p, THREADS, smem, s, tm_kv, tm_r, p);
     };
     if (p.N <= 8) return run(relattn_tree_kernel<1, true>, Cfg<1>::SMEM);
     if (p.N <= 16) return run(relattn_tree_kernel<1, false>, Cfg<1>::SMEM);

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(WARPS * 32) relattn_tree_f32_kernel(const Tree
         }
         reinterpret_cast<float2 *>(r->a[i])[lane] = make_float2(acc[i][0], acc[i][1]);
     }
-    finish<WARPS, ROWS, MT, float>(rec, p, b, h, n, warp, lane);
+    finish<WARPS, KG, MT, float>(rec, p, b, h, n, warp, lane);
 }
 
 cudaError_t ensure_attr()

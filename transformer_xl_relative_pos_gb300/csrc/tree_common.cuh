@@ -9,6 +9,8 @@
 // its key groups share the memory in contiguous runs of 32-key chunks.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_common.cuh"
 #include "paged.h"
 
@@ -164,6 +166,7 @@ __device__ __forceinline__ bool next_chunk(const PagedView &m, int &slot, int &r
 // probabilities, unnormalised output.
 template <int ROWS>
 struct Rec {
+    static constexpr int N = ROWS;
     float m[ROWS];
     float l[ROWS];
     float a[ROWS][DH];
@@ -179,86 +182,106 @@ __device__ __forceinline__ void put_row(float *dst, int lane, float x, float y)
     reinterpret_cast<float2 *>(dst)[lane] = make_float2(x, y);
 }
 
-// Every thread of the block, after each warp wrote its record (warp w's at
-// rec(w), w = kg * MT + mt): merge the key groups of each node, then the blocks
-// of the cluster, whose warps share the nodes; write out and lse of the n nodes.
-template <int NW, int ROWS, int MT, typename T, typename RecOf>
+// The last barrier of a cluster: the other blocks have read this one's shared memory
+// (their loads are complete: nothing to order).
+__device__ __forceinline__ void cluster_done()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// NW warps, after each wrote its record (those of node tile mt: rec(mt), rec(mt + MT), ...,
+// KG of them) and all threads of the block entered: merge the key groups of each node, then
+// the blocks of the cluster, whose warps share the nodes; write out and lse of the n nodes.
+// A partial result stays unnormalised until the last merge:
+//   m = max m_g, l = sum 2^(m_g - m) l_g, a = sum 2^(m_g - m) a_g, out = a / l.
+template <int NW, int KG, int MT, typename T, typename RecOf>
 __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, int h, int n, int warp,
                                        int lane)
 {
-    constexpr int KG = NW / MT;
+    constexpr int ROWS = std::remove_pointer_t<decltype(rec(0))>::N;
     constexpr float LN2 = 0.69314718055994531f;
     T *out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + b * p.out.sb + h * p.out.sh;
     float *lse = p.lse ? p.lse + ((long long)b * p.mem.H + h) * p.N : nullptr;
+    auto write = [&](int i, float m, float l, float o0, float o1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        put_row(out + i * p.out.sr, lane, o0 * inv, o1 * inv);
+        if (lse && lane == 0) lse[i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+    };
     __syncthreads();
-    for (int i = warp; i < n; i += NW) {
-        const int mt = i / ROWS, ii = i % ROWS;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < KG; ++g) mx = max_nan(mx, rec(g * MT + mt)->m[ii]);
-        float ls = 0.f, o0 = 0.f, o1 = 0.f;
-        if (mx != -INFINITY) {
+    if (KG > 1 || p.n_splits == 1) {
+#pragma unroll 2
+        for (int i = warp; i < n; i += NW) {
+            const int mt = i / ROWS, ii = i % ROWS;
+            float m[KG], l[KG];
+            float2 a[KG];
+            float mx = -INFINITY;
 #pragma unroll
             for (int g = 0; g < KG; ++g) {
-                const Rec<ROWS> *r = rec(g * MT + mt);
-                const float w = ex2f(r->m[ii] - mx);  // (0 from -inf)
-                const float2 a = reinterpret_cast<const float2 *>(r->a[ii])[lane];
-                ls += w * r->l[ii];
-                o0 = fmaf(w, a.x, o0);
-                o1 = fmaf(w, a.y, o1);
+                const auto *r = rec(g * MT + mt);
+                m[g] = r->m[ii];
+                l[g] = r->l[ii];
+                a[g] = reinterpret_cast<const float2 *>(r->a[ii])[lane];
+                mx = max_nan(mx, m[g]);
             }
-        }
-        const float inv = ls == 0.f ? 0.f : 1.f / ls;
-        const float lse2 = ls == 0.f ? -INFINITY : mx + log2f(ls);
-        if (p.n_splits == 1) {
-            put_row(out + i * p.out.sr, lane, o0 * inv, o1 * inv);
-            if (lse && lane == 0) lse[i] = lse2 * LN2;
-        } else {
-            // this block's normalised partial, in place of key group 0's (each lane
-            // overwrites what it alone has read)
-            Rec<ROWS> *r = rec(mt);
-            reinterpret_cast<float2 *>(r->a[ii])[lane] = make_float2(o0 * inv, o1 * inv);
-            __syncwarp();
-            if (lane == 0) r->m[ii] = lse2;
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            float ls = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+            for (int g = 0; g < KG; ++g) {
+                const float w = ex2f(m[g] - ref);  // (0 from -inf)
+                ls = fmaf(w, l[g], ls);
+                o0 = fmaf(w, a[g].x, o0);
+                o1 = fmaf(w, a[g].y, o1);
+            }
+            if (p.n_splits == 1) {
+                write(i, mx, ls, o0, o1);
+            } else {
+                // in place of key group 0's (each lane overwrites what it alone has read,
+                // or what all have)
+                auto *r = rec(mt);
+                __syncwarp();
+                reinterpret_cast<float2 *>(r->a[ii])[lane] = make_float2(o0, o1);
+                if (lane == 0) {
+                    r->m[ii] = mx;
+                    r->l[ii] = ls;
+                }
+            }
         }
     }
     if (p.n_splits == 1) return;
     cluster_sync();
     for (int i = (int)cluster_rank() * NW + warp; i < n; i += NW * p.n_splits) {
-        const Rec<ROWS> *r = rec(i / ROWS);
-        const uint32_t a_lse = smem_u32(&r->m[i % ROWS]);
-        const uint32_t a_o = smem_u32(&r->a[i % ROWS][2 * lane]);
+        const auto *r = rec(i / ROWS);
+        const uint32_t at_m = smem_u32(&r->m[i % ROWS]), at_l = smem_u32(&r->l[i % ROWS]);
+        const uint32_t at_a = smem_u32(&r->a[i % ROWS][2 * lane]);
         // (every load on its way before the first is used; ranks past the last: rank 0
         // again, without weight)
-        float part[kTreeMaxCluster];
-        float2 o[kTreeMaxCluster];
+        float m[kTreeMaxCluster], l[kTreeMaxCluster];
+        float2 a[kTreeMaxCluster];
 #pragma unroll
         for (int s = 0; s < kTreeMaxCluster; ++s) {
             const uint32_t from = s < p.n_splits ? s : 0;
-            part[s] = ld_cluster_f32(cluster_addr(a_lse, from));
-            o[s] = ld_cluster_f32x2(cluster_addr(a_o, from));
+            m[s] = ld_cluster_f32(cluster_addr(at_m, from));
+            l[s] = ld_cluster_f32(cluster_addr(at_l, from));
+            a[s] = ld_cluster_f32x2(cluster_addr(at_a, from));
         }
         float mx = -INFINITY;
 #pragma unroll
         for (int s = 0; s < kTreeMaxCluster; ++s) {
-            part[s] = s < p.n_splits ? part[s] : -INFINITY;
-            mx = max_nan(mx, part[s]);
+            m[s] = s < p.n_splits ? m[s] : -INFINITY;
+            mx = max_nan(mx, m[s]);
         }
-        float ws = 0.f, o0 = 0.f, o1 = 0.f;
-        if (mx != -INFINITY) {
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float ls = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
-            for (int s = 0; s < kTreeMaxCluster; ++s) {
-                const float w = ex2f(part[s] - mx);  // (0 from -inf)
-                ws += w;
-                o0 = fmaf(w, o[s].x, o0);
-                o1 = fmaf(w, o[s].y, o1);
-            }
+        for (int s = 0; s < kTreeMaxCluster; ++s) {
+            const float w = ex2f(m[s] - ref);  // (0 from -inf)
+            ls = fmaf(w, l[s], ls);
+            o0 = fmaf(w, a[s].x, o0);
+            o1 = fmaf(w, a[s].y, o1);
         }
-        const float inv = ws == 0.f ? 0.f : 1.f / ws;
-        put_row(out + i * p.out.sr, lane, o0 * inv, o1 * inv);
-        if (lse && lane == 0) lse[i] = ws == 0.f ? -INFINITY : (mx + log2f(ws)) * LN2;
+        write(i, mx, ls, o0, o1);
     }
-    cluster_sync();  // the others have read this block's shared memory
+    cluster_done();
 }
 
 // The barriers of finish, for warps that have no results.
@@ -267,7 +290,7 @@ __device__ __forceinline__ void finish_barriers(const TreeParams &p)
     __syncthreads();
     if (p.n_splits == 1) return;
     cluster_sync();
-    cluster_sync();
+    cluster_done();
 }
 
 // Launch KERN with one cluster of n_splits blocks per (batch, head).

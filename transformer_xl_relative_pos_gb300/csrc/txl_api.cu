@@ -864,9 +864,9 @@ int check_paged(const txl_paged_kv *m)
         return TXL_ERR_INVALID_ARG;
     if (m->dtype != TXL_F32 && m->dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
     if (m->dh != 64 || m->page_rows % txl::kPageRowUnit != 0) return TXL_ERR_UNSUPPORTED;
-    // table rows (twice, for sums of two) and page planes are counted in ints
+    // table rows and page planes (twice each) are counted in ints
     if ((long long)m->slots * m->page_rows > 0x3fffffffLL ||
-        (long long)m->n_pages * m->H > 0x7ffffffeLL || m->B > 65535 || 2LL * m->layers > 65535)
+        (long long)m->n_pages * m->H > 0x3fffffffLL || m->B > 65535 || 2LL * m->layers > 65535)
         return TXL_ERR_UNSUPPORTED;
     if (!aligned(m->pool, 16)) return TXL_ERR_MISALIGNED;
     for (const void *p : {(const void *)m->table, (const void *)m->begin, (const void *)m->fill})
@@ -1094,11 +1094,9 @@ extern "C" int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new,
     p.wait_ns = g_wait_ns;
     if (mem->dtype == TXL_F32)
         return cuda_status(txl::launch_relattn_tree_f32(p, as_stream(stream)));
-    CUtensorMap tk, tv, tr;
-    const long long planes = (long long)mem->n_pages * mem->H;
-    if (!make_map(&tk, p.kpage, mem->page_rows, planes, txl::kPageRowUnit) ||
-        !make_map(&tv, p.vpage, mem->page_rows, planes, txl::kPageRowUnit) ||
+    CUtensorMap tkv, tr;
+    if (!make_map(&tkv, p.kpage, mem->page_rows, 2LL * mem->n_pages * mem->H, txl::kPageRowUnit) ||
         !make_map(&tr, r, r_rows, mem->H, txl::kPageRowUnit))
         return TXL_ERR_CUDA;
-    return cuda_status(txl::launch_relattn_tree(tk, tv, tr, p, as_stream(stream)));
+    return cuda_status(txl::launch_relattn_tree(tkv, tr, p, as_stream(stream)));
 }
