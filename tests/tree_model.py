@@ -8,7 +8,8 @@ fp32; sums of the tensor cores may drop bits instead of rounding, hence 2 u):
       E_ij <= 2 u * 132 * scale * (sum |q + u||k| + sum |q + v||r| + the biases' parts)
     and 4 u |A_ij| for the scalings to log2 units and back;
   * a probability then carries the factor exp(+-2 max_j E_ij), exp2's own error (2^-22)
-    and, on the bf16 path, 2^-16 for being held as two bf16 values;
+    and, on the bf16 path, 2^-16 for being held as two bf16 values, or, in trees of more
+    than 16 nodes, 2^-8 for being rounded to one (half a step of bf16, relative);
   * the sums over K keys, 16 at a time, add (K / 16 + 64) 2 u;
 so |out - want| <= half a step of the output type + (those) * sum_j p_j |v_j|, and
 |lse - want| <= max E + 2^-22 + (K / 16 + 64) 2 u + 4 u |lse|.
@@ -53,7 +54,9 @@ def tree_attention(q, k_new, v_new, mem, layer, r, u, vb, parents, scale, counts
     q, kn, vn, r, u, vb = map(f64, (q, k_new, v_new, r, u, vb))
     par = np.broadcast_to(parents.cpu().numpy(), (B, N))
     half = HALF_STEP[mem.pool.dtype]
-    extra = 2.0 ** -22 + (2.0 ** -16 if mem.pool.dtype == torch.bfloat16 else 0.0)
+    extra = 2.0 ** -22
+    if mem.pool.dtype == torch.bfloat16:
+        extra += 2.0 ** -16 if N <= 16 else 2.0 ** -8
     res = [np.full(s, np.nan) for s in ((B, H, N, dh), (B, H, N)) * 2]
     out, lse, out_b, lse_b = res
     R = r.shape[1]

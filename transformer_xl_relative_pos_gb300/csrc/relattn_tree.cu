@@ -53,7 +53,6 @@ constexpr int ROWB = DH * 2;               // bytes of a row
 constexpr int BOX = GK * ROWB;             // 4096: one 32-row box
 constexpr int ST_K = 0, ST_V = BOX, ST_R = 2 * BOX;
 constexpr int STAGE = 3 * BOX;             // 12288
-constexpr int kNodesCost = 2;              // the nodes among themselves, in chunks of memory
 
 template <int MT>
 struct Cfg {
@@ -73,7 +72,7 @@ struct Cfg {
     // where a warp leaves its record: its private ring, or (shared ring) its scratch
     static_assert(MT == 1 || sizeof(Rec<ROWS>) <= SCR, "a warp's record fits in its scratch");
     static_assert(sizeof(Rec<ROWS>) <= NSTG * STAGE, "a warp's record fits in its ring");
-    static_assert((kTreeMaxSorted + 1) * 4 <= sizeof(Topology) && kTreeMaxSorted <= THREADS,
+    static_assert((kTreeMaxSorted + 1) * 4 <= sizeof(Topology),
                   "the order by length is found in the topology's place");
     static_assert(OFF_BAR % 8 == 0 && OFF_TOPO % 8 == 0, "8-byte alignment");
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks per SM");
@@ -112,12 +111,6 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr));
 }
 
-// Byte offset of 16-byte piece c of row `row` in a 128-byte-swizzled box.
-__device__ __forceinline__ uint32_t swz(int row, int c)
-{
-    return (uint32_t)(row * ROWB + ((c ^ (row & 7)) << 4));
-}
-
 // Scratch accesses by 32-bit shared-memory address.
 __device__ __forceinline__ float ld_scr(uint32_t addr)
 {
@@ -131,9 +124,6 @@ __device__ __forceinline__ void st_scr2(uint32_t addr, float x, float y)
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
 // bf16 pair of (x0, x1), and in `res` the pair of what the rounding left over.
 __device__ __forceinline__ uint32_t split_bf16x2(float x0, float x1, uint32_t &res)
 {
@@ -142,25 +132,11 @@ __device__ __forceinline__ uint32_t split_bf16x2(float x0, float x1, uint32_t &r
     return hi;
 }
 
-// 16 bytes into shared memory without passing through registers, or zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
-                 : "memory");
-}
-
 // The mbarrier's phase also waits for this thread's copies so far (its pending count
 // is raised by one until they are there).
 __device__ __forceinline__ void cp_async_hold(uint64_t *bar)
 {
     asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// A bf16 whose exponent bits are all ones (infinity or NaN) in either half.
-__device__ __forceinline__ bool nonfinite2(uint32_t w)
-{
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
 // The running softmax and output of a warp's nodes: NR rows per lane (g, and g + 8
@@ -216,16 +192,19 @@ __device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR
     }
 }
 
-// acc += P.V over 32 keys, v[kk][nd]: fragments of keys 16 kk .. + 15, dimensions
-// 8 nd .. + 7.  The probabilities enter as value and residual.
-template <int NR>
+// acc += P.V over 16 keys 16 kk .. + 15, v[nd]: their fragments of dimensions 8 nd .. + 7.
+// The probabilities enter as bf16 and, with LO (NR = 1: always), their residuals.
+template <bool LO, int NR>
 __device__ __forceinline__ void pv_step(State<NR> &st, const float (&s)[4][2 * NR], int kk,
                                         const uint32_t (&v)[8][2])
 {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-        if constexpr (NR == 2) {
+        if constexpr (!LO && NR == 2) {
+            hi[2 * c] = pack_bf16x2(s[2 * kk + c][0], s[2 * kk + c][1]);
+            hi[2 * c + 1] = pack_bf16x2(s[2 * kk + c][2], s[2 * kk + c][3]);
+        } else if constexpr (NR == 2) {
             hi[2 * c] = split_bf16x2(s[2 * kk + c][0], s[2 * kk + c][1], lo[2 * c]);
             hi[2 * c + 1] = split_bf16x2(s[2 * kk + c][2], s[2 * kk + c][3], lo[2 * c + 1]);
         } else {
@@ -233,7 +212,7 @@ __device__ __forceinline__ void pv_step(State<NR> &st, const float (&s)[4][2 * N
         }
 #pragma unroll
     for (int nd = 0; nd < 8; ++nd) mma16816(st.acc[nd], hi, v[nd][0], v[nd][1]);
-    if constexpr (NR == 2) {
+    if constexpr (LO && NR == 2) {
 #pragma unroll
         for (int nd = 0; nd < 8; ++nd) mma16816(st.acc[nd], lo, v[nd][0], v[nd][1]);
     }
@@ -618,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     for (int kk = 0; kk < 2; ++kk) {
                         uint32_t bv[8][2];
                         load_v(bv, smem_u32(base + ST_V), kk);
-                        pv_step(st, s, kk, bv);
+                        pv_step<MT == 1>(st, s, kk, bv);
                     }
                 }
             }
@@ -732,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                             bv[nd][1] &= keep1;
                         }
                     }
-                    pv_step(st, s, kk, bv);
+                    pv_step<MT == 1>(st, s, kk, bv);
                 }
             }
             wpos = next;

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(WARPS * 32) relattn_tree_f32_kernel(const Tree
 
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);
-    const Chunks ck = group_chunks(p, begin, fill, 2, split * KG + kg, p.n_splits * KG);
+    const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split * KG + kg, p.n_splits * KG);
     const int rows = min(ROWS, n - mt * ROWS);  // this warp's nodes (none: <= 0)
     const float4 *qu = reinterpret_cast<const float4 *>(qs + mt * (2 * ROWS * DH));
     const float4 *qv = qu + ROWS * DH / 4;

@@ -27,6 +27,7 @@ using decode::ld_cluster_f32x2;
 
 constexpr int DH = kTcDH;  // 64
 constexpr int GK = 32;     // keys per chunk
+constexpr int kNodesCost = 2;  // the nodes among themselves, in chunks of memory
 
 // max that keeps a NaN: a row with a NaN score gives NaN, as the formula does.
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -43,6 +44,29 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c)
     return d;
 }
 
+// Byte offset of 16-byte piece c of row `row` in a 128-byte-swizzled box of 128-byte rows.
+__device__ __forceinline__ uint32_t swz(int row, int c)
+{
+    return (uint32_t)(row * DH * 2 + ((c ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 16 bytes into shared memory without passing through registers, or zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// A bf16 whose exponent bits are all ones (infinity or NaN) in either half.
+__device__ __forceinline__ bool nonfinite2(uint32_t w)
+{
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
 // Per node of the block's sequence: depth, and the mask of itself and its ancestors.
 struct Topology {
     unsigned long long anc[kTreeMaxNodes];
@@ -53,15 +77,15 @@ struct Topology {
 // Sequence of this block: the ranks of the grid (rank = block / (H * n_splits)) in
 // order, or, by_length, longest memory first: with more blocks than are resident at
 // once and unlike lengths, the blocks that start last are then the short ones.
-// All threads of the block, of which there are at least B; scratch: B + 1 ints.
+// All threads of the block; scratch: B + 1 ints.
 __device__ __forceinline__ int pick_sequence(const TreeParams &p, int rank, int *scratch)
 {
     if (!p.by_length) return rank;
-    const int B = p.mem.B, i = threadIdx.x;
-    const int mine = i < B ? p.mem.fill[i] : 0;
-    if (i < B) scratch[i] = mine;
+    const int B = p.mem.B;
+    for (int i = threadIdx.x; i < B; i += blockDim.x) scratch[i] = p.mem.fill[i];
     __syncthreads();
-    if (i < B) {
+    for (int i = threadIdx.x; i < B; i += blockDim.x) {
+        const int mine = scratch[i];
         int before = 0;
         for (int j = 0; j < B; ++j) before += scratch[j] > mine || (scratch[j] == mine && j < i);
         if (before == rank) scratch[B] = i;
@@ -164,12 +188,12 @@ __device__ __forceinline__ bool next_chunk(const PagedView &m, int &slot, int &r
 
 // One warp's result for its nodes: running maximum (log2 units), sum of
 // probabilities, unnormalised output.
-template <int ROWS>
+template <int ROWS, int LD = DH>
 struct Rec {
     static constexpr int N = ROWS;
     float m[ROWS];
     float l[ROWS];
-    float a[ROWS][DH];
+    float a[ROWS][LD];
 };
 
 __device__ __forceinline__ void put_row(__nv_bfloat16 *dst, int lane, float x, float y)
