@@ -618,12 +618,23 @@ __global__ void __launch_bounds__(THREADS, 2)
 
     // ---- the memory, chunk by chunk ---------------------------------------------
     int wpos = DCAP;  // ring column of the chunk's first table row
-    for (int item = nodes; ok && item < nodes + ck.count; ++item) {
-        const int stg = item % NSTG;
-        ok = __all_sync(0xffffffffu, mbar_wait(full + stg, (item / NSTG) & 1, abort_flag, p.wait_ns));
-        if (!ok) break;
+    const int items = nodes + ck.count;
+    int stg = nodes % NSTG, phase = (nodes / NSTG) & 1;
+    bool ready = false;  // the item's stage was seen full ahead of its turn
+    for (int item = nodes; ok && item < items; ++item) {
+        if (!__all_sync(0xffffffffu, ready)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full + stg, phase, abort_flag, p.wait_ns));
+            if (!ok) break;
+        }
+        const int this_stg = stg;
+        if (++stg == NSTG) {
+            stg = 0;
+            phase ^= 1;
+        }
+        const bool page_ok = stage_ok[kg * NSTG + this_stg] != 0;
+        ready = false;
         if (active) {
-            const uint8_t *base = ring + stg * STAGE;
+            const uint8_t *base = ring + this_stg * STAGE;
             const uint32_t sk = smem_u32(base + ST_K), sv = smem_u32(base + ST_V), sr = smem_u32(base + ST_R);
             const int j0 = (ck.c0 + item - nodes) * GK - ck.off;  // memory row of the chunk's first key
 
@@ -674,7 +685,6 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
             // Keys that are not memory rows (the chunk sticks out at either end, or its
             // page is unknown) or that the table does not reach from the node.
-            const bool page_ok = stage_ok[kg * NSTG + stg] != 0;
             const bool out_of_memory = j0 < 0 || j0 + GK > fill || !page_ok;
             const bool partly_hidden = j0 < fill + depth_max - p.r_rows + 1;
             const int key_lo = -j0, key_hi = page_ok ? fill - j0 : 0;  // memory rows of the chunk
@@ -691,14 +701,18 @@ __global__ void __launch_bounds__(THREADS, 2)
                         }
                     }
             }
+            // what the softmax's latencies leave time for: the values, and whether the next
+            // stage is there
+            uint32_t bv[2][8][2];
+            load_v(bv[0], sv, 0);
+            load_v(bv[1], sv, 1);
+            ready = item + 1 < items && mbar_test(full + stg, phase);
             softmax_step(st, s, scale);
             if (partly_hidden && nonfinite_values(base + ST_V, key_lo, key_hi)) {
                 pv_by_element(s, hidden, next, base + ST_V);
             } else {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t bv[8][2];
-                    load_v(bv, sv, kk);
                     if (out_of_memory) {
                         // this lane's fragment rows: keys 16 kk + 2 t, + 1 and + 8, + 9
                         const int key = 16 * kk + 2 * t;
@@ -707,17 +721,17 @@ __global__ void __launch_bounds__(THREADS, 2)
                         const uint32_t keep1 = (in(key + 8) ? 0xffffu : 0u) | (in(key + 9) ? 0xffff0000u : 0u);
 #pragma unroll
                         for (int nd = 0; nd < 8; ++nd) {
-                            bv[nd][0] &= keep0;
-                            bv[nd][1] &= keep1;
+                            bv[kk][nd][0] &= keep0;
+                            bv[kk][nd][1] &= keep1;
                         }
                     }
-                    pv_step<MT == 1>(st, s, kk, bv);
+                    pv_step<MT == 1>(st, s, kk, bv[kk]);
                 }
             }
             wpos = next;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty + stg);  // this warp has read the stage
+        if (lane == 0) mbar_arrive(empty + this_stg);  // this warp has read the stage
     }
     if (!ok && lane == 0) {
         *abort_flag = 1;
