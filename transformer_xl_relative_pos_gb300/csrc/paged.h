@@ -85,5 +85,9 @@ struct TreeParams {
 cudaError_t launch_relattn_tree(const CUtensorMap &tm_kv, const CUtensorMap &tm_r, const TreeParams &p,
                                 cudaStream_t s);
 cudaError_t launch_relattn_tree_f32(const TreeParams &p, cudaStream_t s);
+// Thread-block clusters of n_splits blocks that the current device holds at once, for
+// trees of N nodes (0 when that cannot be found).
+int tree_max_clusters(int N, int n_splits);
+int tree_max_clusters_f32(int N, int n_splits);
 
 } // namespace txl

@@ -780,18 +780,33 @@ cudaError_t ensure_attr()
 
 } // namespace
 
+// f(kernel, its shared memory, its index) for trees of N nodes.
+template <typename F>
+static auto with_kernel(int N, F f)
+{
+    if (N <= 8) return f(relattn_tree_kernel<1, true>, Cfg<1>::SMEM, 0);
+    if (N <= 16) return f(relattn_tree_kernel<1, false>, Cfg<1>::SMEM, 1);
+    if (N <= 32) return f(relattn_tree_kernel<2, false>, Cfg<2>::SMEM, 2);
+    return f(relattn_tree_kernel<4, false>, Cfg<4>::SMEM, 3);
+}
+
 cudaError_t launch_relattn_tree(const CUtensorMap &tm_kv, const CUtensorMap &tm_r, const TreeParams &p,
                                 cudaStream_t s)
 {
     const cudaError_t e = ensure_attr();
     if (e != cudaSuccess) return e;
-    const auto run = [&](auto *kern, int smem) {
+    return with_kernel(p.N, [&](auto *kern, int smem, int) {
         return launch_clusters(kern, p, THREADS, smem, s, tm_kv, tm_r, p);
-    };
-    if (p.N <= 8) return run(relattn_tree_kernel<1, true>, Cfg<1>::SMEM);
-    if (p.N <= 16) return run(relattn_tree_kernel<1, false>, Cfg<1>::SMEM);
-    if (p.N <= 32) return run(relattn_tree_kernel<2, false>, Cfg<2>::SMEM);
-    return run(relattn_tree_kernel<4, false>, Cfg<4>::SMEM);
+    });
+}
+
+int tree_max_clusters(int N, int n_splits)
+{
+    static ClusterCache cache[4];
+    if (ensure_attr() != cudaSuccess) return 0;
+    return with_kernel(N, [&](auto *kern, int smem, int i) {
+        return cache[i].get(n_splits, [&] { return max_clusters(kern, n_splits, THREADS, smem); });
+    });
 }
 
 } // namespace txl

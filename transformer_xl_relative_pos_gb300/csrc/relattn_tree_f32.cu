@@ -290,16 +290,33 @@ cudaError_t ensure_attr()
 
 } // namespace
 
+// f(kernel, its shared memory, its index) for trees of N nodes.
+template <typename F>
+static auto with_kernel(int N, F f)
+{
+    const int mt = (N + ROWS - 1) / ROWS;
+    if (mt <= 1) return f(relattn_tree_f32_kernel<1>, CfgF32<1>::SMEM, 0);
+    if (mt <= 2) return f(relattn_tree_f32_kernel<2>, CfgF32<2>::SMEM, 1);
+    if (mt <= 4) return f(relattn_tree_f32_kernel<4>, CfgF32<4>::SMEM, 2);
+    return f(relattn_tree_f32_kernel<MAX_MT>, CfgF32<MAX_MT>::SMEM, 3);
+}
+
 cudaError_t launch_relattn_tree_f32(const TreeParams &p, cudaStream_t s)
 {
     const cudaError_t e = ensure_attr();
     if (e != cudaSuccess) return e;
-    const int mt = (p.N + ROWS - 1) / ROWS;
-    const auto run = [&](auto *kern, int smem) { return launch_clusters(kern, p, WARPS * 32, smem, s, p); };
-    if (mt <= 1) return run(relattn_tree_f32_kernel<1>, CfgF32<1>::SMEM);
-    if (mt <= 2) return run(relattn_tree_f32_kernel<2>, CfgF32<2>::SMEM);
-    if (mt <= 4) return run(relattn_tree_f32_kernel<4>, CfgF32<4>::SMEM);
-    return run(relattn_tree_f32_kernel<MAX_MT>, CfgF32<MAX_MT>::SMEM);
+    return with_kernel(p.N, [&](auto *kern, int smem, int) {
+        return launch_clusters(kern, p, WARPS * 32, smem, s, p);
+    });
+}
+
+int tree_max_clusters_f32(int N, int n_splits)
+{
+    static ClusterCache cache[4];
+    if (ensure_attr() != cudaSuccess) return 0;
+    return with_kernel(N, [&](auto *kern, int smem, int i) {
+        return cache[i].get(n_splits, [&] { return max_clusters(kern, n_splits, WARPS * 32, smem); });
+    });
 }
 
 } // namespace txl

@@ -9,6 +9,7 @@
 // its key groups share the memory in contiguous runs of 32-key chunks.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "decode_common.cuh"
@@ -317,7 +318,25 @@ __device__ __forceinline__ void finish_barriers(const TreeParams &p)
     cluster_done();
 }
 
-// Launch KERN with one cluster of n_splits blocks per (batch, head).
+// Configuration of a launch with one cluster of n_splits blocks per (batch, head).
+struct ClusterConfig {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    ClusterConfig(long long blocks, int n_splits, int threads, int smem, cudaStream_t s)
+    {
+        cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+        cfg.blockDim = dim3((unsigned)threads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)n_splits;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = n_splits > 1 ? 1 : 0;
+    }
+};
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kern)(KArgs...), const TreeParams &p, int threads, int smem,
                             cudaStream_t s, const Args &...args)
@@ -325,20 +344,41 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), const TreeParams &p, int thr
     const long long blocks = (long long)p.mem.B * p.mem.H * p.n_splits;
     if (blocks <= 0 || blocks > 0x7fffffffLL || p.n_splits > kTreeMaxCluster)
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.n_splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.n_splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    ClusterConfig c(blocks, p.n_splits, threads, smem, s);
+    return cudaLaunchKernelEx(&c.cfg, kern, args...);
 }
+
+// Clusters of n_splits blocks the current device holds at once (0: unknown).
+template <typename... KArgs>
+int max_clusters(void (*kern)(KArgs...), int n_splits, int threads, int smem)
+{
+    ClusterConfig c(n_splits, n_splits, threads, smem, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &c.cfg) != cudaSuccess) {
+        cudaGetLastError();  // (no sticky error is left to a later launch check)
+        return 0;
+    }
+    return n;
+}
+
+// max_clusters of one kernel, found once per device and size.
+struct ClusterCache {
+    std::atomic<int> n[64][kTreeMaxCluster + 1] = {};  // plus one; 0: not found yet
+    template <typename F>
+    int get(int n_splits, F find)
+    {
+        int dev = 0;
+        if (n_splits < 1 || n_splits > kTreeMaxCluster || cudaGetDevice(&dev) != cudaSuccess || dev < 0 ||
+            dev >= 64)
+            return 0;
+        int v = n[dev][n_splits].load(std::memory_order_relaxed);
+        if (v == 0) {
+            v = find() + 1;
+            n[dev][n_splits].store(v, std::memory_order_relaxed);
+        }
+        return v - 1;
+    }
+};
 
 } // namespace tree
 } // namespace txl
