@@ -183,3 +183,79 @@ def test_tree_refuses_a_bad_memory(kw, want):
 ])
 def test_tree_refusals(kw, want):
     assert tree_call(**kw) == want
+
+
+class FakeKV:
+    """What PagedMemory uses of PagedKV, with tensors on the CPU."""
+
+    def __init__(self, pool, table):
+        self.pool, self.table = pool, table
+        self.begin = torch.zeros(table.shape[0], dtype=torch.int32)
+        self.fill = torch.zeros(table.shape[0], dtype=torch.int32)
+        self.n_pages, self.H, self.page_rows = pool.shape[1:4]
+        self.slots = table.shape[1]
+        self.rows = self.slots * self.page_rows
+
+
+def fake_copy(kv, src, dst):
+    assert len(set(dst.tolist())) == len(dst) and not set(dst.tolist()) & set(src.tolist())
+    kv.pool[:, dst.long()] = kv.pool[:, src.long()]
+
+
+def fake_append(kv, k, v, *, layer=0, n_new=None, rows=None, keep=None):
+    written = set()
+    for b in range(kv.table.shape[0]):
+        n = k.shape[-2] if n_new is None else int(n_new[b])
+        begin, fill = int(kv.begin[b]), int(kv.fill[b])
+        assert fill + n <= kv.rows
+        for t in range(n):
+            x = (begin + fill + t) % kv.rows
+            page = int(kv.table[b, x // kv.page_rows])
+            src = t if rows is None else int(rows[b, t])
+            assert page >= 0
+            written.add((b, page))
+            kv.pool[0::2, page, :, x % kv.page_rows] = k[:, b, :, src]
+            kv.pool[1::2, page, :, x % kv.page_rows] = v[:, b, :, src]
+        left = min(fill + n, keep)
+        kv.begin[b], kv.fill[b] = (begin + fill + n - left) % kv.rows, left
+    pages = [p for _, p in written]
+    assert len(pages) == len(set(pages)), "two sequences wrote one page"
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_paged_memory_against_lists_of_rows(monkeypatch, seed):
+    import paged_ops
+    from transformer_xl_relative_pos_gb300 import paged
+    monkeypatch.setattr(paged.txl, "PagedKV", FakeKV)
+    monkeypatch.setattr(paged.txl, "paged_copy", fake_copy)
+    monkeypatch.setattr(paged.txl, "paged_append", fake_append)
+    M, max_new, P = [(70, 40, 32), (0, 7, 32), (100, 9, 64), (33, 64, 96)][seed % 4]
+    make = lambda: paged.PagedMemory(2, 4, 1, M, max_new, device="cpu", dtype=torch.float32,
+                                     page_rows=P, dh=2)
+    paged_ops.run(make, "cpu", seed)
+
+
+def test_paged_memory_refusals_change_nothing(monkeypatch):
+    from transformer_xl_relative_pos_gb300 import paged
+    monkeypatch.setattr(paged.txl, "PagedKV", FakeKV)
+    monkeypatch.setattr(paged.txl, "paged_copy", fake_copy)
+    monkeypatch.setattr(paged.txl, "paged_append", fake_append)
+    mem = paged.PagedMemory(1, 2, 1, 64, 40, device="cpu", dtype=torch.float32, page_rows=32, dh=2,
+                            n_pages=3)
+    k = torch.ones(2, 1, 40, 2)
+    mem.append(k[None], k[None], [40, 10])                   # three pages of three
+    table = mem._table.copy()
+    with pytest.raises(txl.TxlError) as e:
+        mem.append(k[None], k[None], [0, 30])
+    assert e.value.status == SHAPE
+    for bad in (lambda: mem.append(k[None], k[None], [1]), lambda: mem.append(k[None], k[None], [1, -1]),
+                lambda: mem.append(k[None], k[None], rows=[[0], [40]]),
+                lambda: mem.append(k[None], k[None], rows=[[0]]),
+                lambda: mem.append(k[None], k[None], [2, 2], rows=[[0], [0, 1]]),
+                lambda: mem.reserve(41), lambda: paged.PagedMemory(1, 1, 1, 4, 0, device="cpu")):
+        with pytest.raises(ValueError):
+            bad()
+    assert (mem._table == table).all() and mem.fill == [40, 10] and mem.pages.n_free == 0
+    mem.free(0)
+    mem.append(k[None], k[None], [0, 30])
+    assert mem.fill == [0, 40]

@@ -24,6 +24,7 @@ N-layer summary, Appendix B reversed table and shift):
                   nodes of a drafted tree), the state advanced, pages copied
   relattn_tree_fwd  attention of a tree of drafted tokens over that memory
   PagePool        host-side accounting of those pages (free, shared)
+  PagedMemory     both together: sequences that append, fork and end apart
   relattn_bwd     gradients of relattn_fwd for one segment (training within a
                   segment, the memory SG(m))
 """
@@ -65,3 +66,4 @@ from ._lib import (  # noqa: F401
     version,
     workspace_size,
 )
+from .paged import PagedMemory  # noqa: F401,E402

@@ -32,6 +32,14 @@ periodically (every M / gcd(M, L) segments for the rings), so one graph per
 combination of positions covers the stream.  A capture records the states the
 eager calls leave behind, and a replay sets the host-side states to them.
 
+With ``paged`` the projected keys and values of every sequence lie in pages
+(PagedMemory), so that sequences of a batch advance apart: ``draft`` runs a tree
+of drafted tokens against the memories (one launch of txl_relattn_tree_fwd per
+layer) without changing them, ``accept`` puts the accepted nodes' keys and values
+behind them (one launch for all layers), and ``fork`` lets one sequence continue as
+a copy of another.  A segment is then a chain of at most 64 drafted tokens, all of
+them accepted.
+
 Torch is used here for the dense projections, LayerNorm and the feed-forward
 only; the attention, the positional table and the memory run in the CUDA
 library.
@@ -44,6 +52,7 @@ import math
 import torch
 
 from . import _lib as txl
+from .paged import PagedMemory
 
 LN_EPS = 1e-5
 
@@ -93,8 +102,16 @@ class XLStack:
     to ``device`` in ``dtype``.  ``segment(tokens)`` processes one segment
     [B, L] and returns the top layer's states [B, L, d] (``dtype``)."""
 
+    MAX_DRAFT = 64  # nodes of a drafted tree
+
     def __init__(self, params: dict, H: int, M: int, device, dtype=torch.bfloat16,
-                 cache_kv: bool = False, graphs: bool = False):
+                 cache_kv: bool = False, graphs: bool = False, paged: bool = False):
+        if paged and (cache_kv or graphs):
+            raise ValueError("paged keeps its own keys and values (no cache_kv) and is not "
+                             "replayed from graphs")
+        self.paged = paged
+        self.memory = None       # paged: the PagedMemory
+        self._draft = None       # paged: q, k and v of the last draft
         self.H, self.M, self.dtype, self.device = H, M, dtype, torch.device(device)
         self.cache_kv = cache_kv
         self.graphs = graphs
@@ -126,6 +143,11 @@ class XLStack:
     def reset(self, B: int):
         self._graphs = {}
         self._full_segments = 0
+        if self.paged:
+            self.memory = PagedMemory(len(self.layers), B, self.H, self.M, self.MAX_DRAFT,
+                                      device=self.device, dtype=self.dtype, dh=self.dh)
+            self._draft = None
+            return
         self.mems = [torch.zeros(B, self.M, self.d, dtype=self.dtype, device=self.device)
                      for _ in self.layers]
         self.states = [txl.MemState(0, 0, self.M) for _ in self.layers]
@@ -152,6 +174,10 @@ class XLStack:
         next (§3.2: the memory of each layer; with cache_kv also the windows of
         projected keys and values), with the host-side ring and window states.
         ``restore`` on a fresh stack continues the stream exactly."""
+        if self.paged:
+            if self.memory is None:
+                raise RuntimeError("checkpoint: no segment has run yet")
+            return {"paged": self.memory.checkpoint()}
         if self.mems is None:
             raise RuntimeError("checkpoint: no segment has run yet")
         torch.cuda.synchronize(self.device)
@@ -164,6 +190,12 @@ class XLStack:
 
     def restore(self, ck: dict):
         """Load a ``checkpoint`` (same parameters, shapes and options)."""
+        if self.paged != ("paged" in ck):
+            raise ValueError("restore: the checkpoint is of a stack with other options")
+        if self.paged:
+            self.reset(len(ck["paged"]["fill"]))
+            self.memory.restore(ck["paged"])
+            return
         B = ck["mems"][0].shape[0]
         self.reset(B)
         for mem, saved, st, snap in zip(self.mems, ck["mems"], self.states, ck["states"]):
@@ -181,6 +213,8 @@ class XLStack:
 
     def memories(self):
         """Each layer's memory in logical order (oldest first), [B, fill, d]."""
+        if self.paged:
+            raise RuntimeError("a paged stack keeps keys and values, not hidden states")
         out = []
         for mem, st in zip(self.mems, self.states):
             B = mem.shape[0]
@@ -225,6 +259,11 @@ class XLStack:
         the result lives in the graph's memory and is overwritten by the next
         replay of the same ring position."""
         B, L = tokens.shape
+        if self.paged:
+            parents = torch.arange(-1, L - 1, dtype=torch.int32)
+            h = self.draft(tokens, parents)
+            self.accept([range(L)] * B)
+            return h
         if self.mems is None or self.mems[0].shape[0] != B:
             self.reset(B)
         if self.cache_kv and (self.kvbufs is None or self._kv_L != L):
@@ -260,6 +299,60 @@ class XLStack:
             self._restore(st, snap)
         return out
 
+    def draft(self, tokens: torch.Tensor, parents: torch.Tensor, n_nodes=None) -> torch.Tensor:
+        """The top layer's states [B, N, d] of a tree of N <= 64 drafted tokens
+        [B, N] per sequence (paged): node i follows node parents[b, i] < i of its
+        sequence, or with -1 the memory; parents [N]: one tree for all.  n_nodes: nodes of
+        each sequence, when not all N (the states behind them are of no meaning).  The
+        memories stay as they are; ``accept`` goes on from here."""
+        if not self.paged:
+            raise RuntimeError("draft: the stack is not paged")
+        B, N = tokens.shape
+        if not 1 <= N <= self.MAX_DRAFT:
+            raise ValueError(f"draft: 1 to {self.MAX_DRAFT} tokens")
+        if self.memory is None or self.memory.B != B:
+            self.reset(B)
+        i32 = lambda t: torch.as_tensor(t).to(device=self.device, dtype=torch.int32).contiguous()
+        parents = i32(parents)
+        n_nodes = None if n_nodes is None else i32(n_nodes)
+        H, dh = self.H, self.dh
+        h = self.emb[tokens.to(self.device)]
+        # q, k and v of every layer as its projection leaves them
+        qkv = torch.empty(len(self.layers), B, N, 3, H, dh, dtype=self.dtype, device=self.device)
+        for n, lay in enumerate(self.layers):
+            torch.mm(h.reshape(B * N, -1), lay["W_qkv"].t(), out=qkv[n].view(B * N, -1))
+            q, k, v = (qkv[n, :, :, i].transpose(1, 2) for i in range(3))
+            a = torch.zeros(B, N, H, dh, dtype=self.dtype, device=self.device)
+            txl.relattn_tree_fwd(q, k, v, self.memory.kv, n, self._r(n, self.M + self.MAX_DRAFT),
+                                 self.u, self.v_bias, parents, self.scale, n_nodes=n_nodes,
+                                 out=a.transpose(1, 2))
+            h = self._rest_of_layer(lay, h, a.view(B, N, -1)).to(self.dtype)
+        self._draft = qkv
+        return h
+
+    def accept(self, rows):
+        """Accept nodes of the last draft: rows[b] lists those of sequence b in the
+        order of the text (a path of its tree from a first token on; none: []).  Their
+        keys and values go behind the memory of every layer, which keeps the newest M."""
+        if self._draft is None:
+            raise RuntimeError("accept: nothing is drafted")
+        k, v = (self._draft[:, :, :, i].transpose(2, 3) for i in (1, 2))
+        self.memory.append(k, v, rows=[list(r) for r in rows])
+        self._draft = None
+
+    def fork(self, src: int, dst: int):
+        """Let sequence dst of a paged stack continue as a copy of sequence src."""
+        if self.memory is None:
+            raise RuntimeError("fork: the stack is not paged, or no segment has run yet")
+        self.memory.fork(src, dst)
+        self._draft = None
+
+    def _rest_of_layer(self, lay: dict, h: torch.Tensor, a: torch.Tensor) -> torch.Tensor:
+        """A layer from its attention output a [B, L, H * dh] on (fp32)."""
+        o = layer_norm((a @ lay["W_o"].t()).float() + lay["b_o"].float() + h.float())
+        f = torch.relu(o.to(self.dtype) @ lay["W_1"].t() + lay["b_1"])
+        return layer_norm(o + (f @ lay["W_2"].t()).float() + lay["b_2"].float())
+
     def _segment(self, tokens: torch.Tensor) -> torch.Tensor:
         B, L = tokens.shape
         h = self.emb[tokens]
@@ -289,9 +382,7 @@ class XLStack:
             r = self._r(n, M_cur + L)
             a_heads = txl.relattn_fwd(q, k, v, r, self.u, self.v_bias, M_cur, self.scale)
             a = a_heads.transpose(1, 2).reshape(B, L, -1)
-            o = layer_norm((a @ lay["W_o"].t()).float() + lay["b_o"].float() + h.float())
-            f = torch.relu(o.to(self.dtype) @ lay["W_1"].t() + lay["b_1"])
-            h_next = layer_norm(o + (f @ lay["W_2"].t()).float() + lay["b_2"].float())
+            h_next = self._rest_of_layer(lay, h, a)
             if self.taps is not None:
                 self.taps.append({"h": h, "mem": mem_now, "q": q, "k": k, "v": v, "r": r,
                                   "M": M_cur, "a": a_heads, "h_out": h_next.to(self.dtype)})
