@@ -259,3 +259,34 @@ def test_paged_memory_refusals_change_nothing(monkeypatch):
     mem.free(0)
     mem.append(k[None], k[None], [0, 30])
     assert mem.fill == [0, 40]
+
+
+def test_paged_memory_refuses_sequences_layers_and_checkpoints_of_others(monkeypatch):
+    from transformer_xl_relative_pos_gb300 import paged
+    monkeypatch.setattr(paged.txl, "PagedKV", FakeKV)
+    monkeypatch.setattr(paged.txl, "paged_copy", fake_copy)
+    monkeypatch.setattr(paged.txl, "paged_append", fake_append)
+    make = lambda layers=2, H=1, dtype=torch.float32: paged.PagedMemory(
+        layers, 2, H, 64, 40, device="cpu", dtype=dtype, page_rows=32, dh=2)
+    mem = make()
+    k = torch.ones(2, 2, 1, 8, 2)
+    mem.append(k, k)
+    table, ck = mem._table.copy(), mem.checkpoint()
+    for bad in (lambda: mem.free(-1), lambda: mem.free(2), lambda: mem.fork(0, -1), lambda: mem.fork(-2, 1),
+                lambda: mem.fork(0, 2)):
+        with pytest.raises(IndexError):
+            bad()
+    for bad in (lambda: mem.append(k[0], k[0]), lambda: mem.append(k[:1], k[:1])):
+        with pytest.raises(ValueError):
+            bad()
+    for other in (make(layers=1), make(H=2), make(dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            other.restore(ck)
+        assert other.fill == [0, 0] and other.pages.n_free == other.kv.n_pages
+    assert (mem._table == table).all() and mem.fill == [8, 8]
+
+
+def test_the_tensors_of_a_memory_are_not_replaced():
+    for name in ("pool", "table", "begin", "fill", "ticket"):
+        with pytest.raises(AttributeError):
+            setattr(txl.PagedKV.__new__(txl.PagedKV), name, None)

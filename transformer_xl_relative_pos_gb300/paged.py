@@ -29,7 +29,7 @@ class PagedMemory:
                  dtype=torch.bfloat16, page_rows: int = 64, n_pages: int | None = None, dh: int = 64):
         if M < 0 or max_new < 1:
             raise ValueError("PagedMemory: M >= 0 and max_new >= 1")
-        self.M, self.max_new, self.B = M, max_new, B
+        self.M, self.max_new, self.B, self.layers = M, max_new, B, layers
         slots = -(-(M + max_new) // page_rows) + 1
         n = B * slots if n_pages is None else n_pages
         self.device = torch.device(device)
@@ -53,6 +53,11 @@ class PagedMemory:
         if max(counts) > self.max_new:
             raise ValueError(f"at most {self.max_new} rows at once")
         return counts
+
+    def _sequence(self, b: int) -> int:
+        if not 0 <= b < self.B:
+            raise IndexError(f"no sequence {b} of {self.B}")
+        return b
 
     def _upload(self):
         self.kv.table.copy_(torch.from_numpy(self._table))
@@ -99,12 +104,14 @@ class PagedMemory:
             txl.paged_copy(self.kv, self._ints(src), self._ints(dst))
         self._upload()
 
-    def append(self, k, v, n=None, rows=None, layer: int = 0):
-        """Append rows of k and v ([B, H, N, dh], or [layers, B, H, N, dh] from
-        ``layer`` on) and advance to the newest M.  n: rows per sequence (all N when
+    def append(self, k, v, n=None, rows=None):
+        """Append rows of k and v ([layers, B, H, N, dh]; with one layer also
+        [B, H, N, dh]) and advance to the newest M.  n: rows per sequence (all N when
         omitted); rows: per sequence the source rows (e.g. the accepted nodes of a
         drafted tree), n then being their numbers."""
         idx = None
+        if (k.shape[0] if k.dim() == 5 else 1) != self.layers:
+            raise ValueError(f"k and v must hold the rows of all {self.layers} layers")
         if rows is not None:
             if n is None:
                 n = [len(r) for r in rows]
@@ -124,7 +131,7 @@ class PagedMemory:
                 raise ValueError("more rows than k and v hold")
         self.reserve(counts)
         same = idx is None and min(counts) == k.shape[-2]
-        txl.paged_append(self.kv, k, v, layer=layer, rows=idx,
+        txl.paged_append(self.kv, k, v, rows=idx,
                          n_new=None if same else self._ints(counts), keep=self.M)
         R = self.kv.rows
         for b, c in enumerate(counts):
@@ -134,7 +141,7 @@ class PagedMemory:
 
     def free(self, b: int):
         """End sequence b: its memory is empty and its pages have one user less."""
-        held = [int(p) for p in self._table[b] if p >= 0]
+        held = [int(p) for p in self._table[self._sequence(b)] if p >= 0]
         self.pages.release(held)
         self._table[b] = -1
         self.begin[b] = self.fill[b] = 0
@@ -144,7 +151,7 @@ class PagedMemory:
 
     def fork(self, src: int, dst: int):
         """Sequence dst becomes a copy of src, sharing its pages (dst's own are freed)."""
-        if src == dst:
+        if self._sequence(src) == self._sequence(dst):
             return
         self.free(dst)
         self.pages.retain([int(p) for p in self._table[src] if p >= 0])
@@ -199,12 +206,14 @@ class PagedMemory:
 
     def restore(self, ck: dict):
         """Load a checkpoint (same shapes and options)."""
-        if ck["table"].shape != self._table.shape or len(ck["users"]) > self.kv.n_pages:
+        pool = self.kv.pool[:, :len(ck["users"])]
+        if (ck["table"].shape != self._table.shape or ck["pool"].shape != pool.shape or
+                ck["pool"].dtype != pool.dtype):
             raise ValueError("restore: a memory of other shapes")
         self._table = ck["table"].copy()
         self.begin, self.fill = list(ck["begin"]), list(ck["fill"])
         self._recount(dict(enumerate(ck["users"])))
-        self.kv.pool[:, :len(ck["users"])].copy_(ck["pool"])
+        pool.copy_(ck["pool"])
         self.kv.begin.copy_(self._ints(self.begin))
         self.kv.fill.copy_(self._ints(self.fill))
         self._upload()
