@@ -37,7 +37,7 @@ class Case:
     """A memory whose unused page rows hold NaN, and operands for one call."""
 
     def __init__(self, B, H, N, fills, P=64, slots=None, layers=1, layer=0, kind="near", dtype="bf16",
-                 r_rows=None, counts=None, layout="stacked", begin=None, std=1.0, seed=0):
+                 r_rows=None, counts=None, layout="stacked", begin=None, std=1.0, scale=0.125, seed=0):
         g = self.g = torch.Generator().manual_seed(seed + 1000 * N + B)
         dt = DT[dtype]
         fills = [fills] * B if isinstance(fills, int) else list(fills)
@@ -55,6 +55,7 @@ class Case:
                                torch.tensor(fills, dtype=torch.int32).to(dev()))
         self.layer, self.B, self.H, self.N, self.dt = layer, B, H, N, dt
         self.counts = [N] * B if counts is None else counts
+        self.scale = scale
         self.parents = tree(kind, B, N, g)
         rnd = lambda *s, std=std: (torch.randn(*s, generator=g) * std).to(dt).to(dev())
         self.r = rnd(H, r_rows or max(fills) + N, 64)
@@ -74,12 +75,12 @@ class Case:
         if self.counts != [self.N] * self.B:
             n = torch.tensor(self.counts, dtype=torch.int32).to(dev())
         return txl.relattn_tree_fwd(self.q, self.k, self.v, self.mem, self.layer, self.r, self.u, self.vb,
-                                    self.parents, 0.125, n_nodes=n, out=self.out, lse=self.lse,
+                                    self.parents, self.scale, n_nodes=n, out=self.out, lse=self.lse,
                                     n_splits=n_splits, **kw)
 
     def want(self):
         return tree_attention(self.q, self.k, self.v, self.mem, self.layer, self.r, self.u, self.vb,
-                              self.parents, 0.125, self.counts)
+                              self.parents, self.scale, self.counts)
 
     def check(self, n_splits=0, status=0, want=None):
         self.call(n_splits)
@@ -297,6 +298,80 @@ def test_graphs_and_streams(dtype):
         out, lse, out_b, lse_b = c.want()
         assert (np.abs(c.out.cpu().double().numpy() - out) <= out_b).all()
         assert (np.abs(c.lse.cpu().double().numpy() - lse) <= lse_b).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 0.3, -1e-3])
+@pytest.mark.parametrize("N", [5, 13, 30, 64])
+def test_scales_of_either_sign(N, scale, dtype):
+    Case(2, 2, N, [130, 33], scale=scale, r_rows=120, dtype=dtype, seed=23).check(2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H", [(40, 10), (255, 2), (256, 2)])
+def test_many_sequences_of_unlike_lengths(B, H, dtype):
+    # more blocks than are resident at once: the longest memories come first (up to 255
+    # sequences); equal lengths and sequences without nodes among them
+    g = torch.Generator().manual_seed(B)
+    fills = torch.randint(0, 130, (B,), generator=g).tolist()
+    fills[1] = fills[7] = fills[B - 1]
+    counts = [2] * B
+    counts[3] = counts[B - 2] = 0
+    Case(B, H, 2, fills, P=32, counts=counts, dtype=dtype, seed=24).check()
+
+
+def test_outputs_made_by_the_call_belong_to_its_stream():
+    # Work waits on the current stream; a call on another stream must not come to lie
+    # before the filling of its own outputs.
+    c = Case(2, 2, 12, [100, 40], counts=[12, 5], seed=25)
+    n = torch.tensor(c.counts, dtype=torch.int32).to(dev())
+    args = (c.q, c.k, c.v, c.mem, 0, c.r, c.u, c.vb, c.parents, 0.125)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    big = torch.randn(4096, 4096, device=dev())
+    for stream in (side, side.cuda_stream):
+        for _ in range(20):
+            big = torch.mm(big, big).clamp_(-1, 1)
+        out, lse = txl.relattn_tree_fwd(*args, n_nodes=n, lse=True, stream=stream)
+        torch.cuda.synchronize()
+        want, want_lse, out_b, lse_b = c.want()
+        left = np.isnan(want_lse)
+        assert (out.float().cpu().numpy()[left] == 0).all() and (lse.cpu().numpy()[left] == 0).all()
+        assert (np.abs(out.cpu().double().numpy() - want) <= out_b)[~left].all()
+        assert (np.abs(lse.cpu().double().numpy() - want_lse) <= lse_b)[~left].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    # Pages behind 2^33 bytes of a plane: rows appended to them, attended to and copied,
+    # as in a small pool, bit for bit.
+    dt, H, P, B, N = DT[dtype], 2, 128, 2, 20
+    size = H * P * 64
+    far = (2 ** 33) // (size * dt.itemsize)
+    big = txl.PagedKV(torch.empty(2, far + 8, H, P, 64, dtype=dt, device=dev()),
+                      torch.tensor([[far + 1, far + 4], [far + 6, far + 3]], dtype=torch.int32, device=dev()))
+    small = txl.PagedKV(torch.empty(2, 8, H, P, 64, dtype=dt, device=dev()),
+                        torch.tensor([[1, 4], [6, 3]], dtype=torch.int32, device=dev()))
+    g = torch.Generator().manual_seed(26)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(dt).to(dev())
+    k, v = rnd(B, H, 200, 64), rnd(B, H, 200, 64)
+    q, kn, vn = rnd(B, H, N, 64), rnd(B, H, N, 64), rnd(B, H, N, 64)
+    r, u, vb, parents = rnd(H, 200, 64), rnd(H, 64), rnd(H, 64), tree("near", B, N, g)
+    got = []
+    for mem, at in ((big, far), (small, 0)):
+        txl.paged_append(mem, k, v, keep=200)
+        out = [txl.relattn_tree_fwd(q, kn, vn, mem, 0, r, u, vb, parents, 0.125)]
+        ids = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev()) + at
+        txl.paged_copy(mem, ids(1, 6), ids(0, 7))
+        mem.table.copy_(torch.stack([ids(0, 4), ids(7, 3)]))
+        mem.pool[:, at + 1].zero_(), mem.pool[:, at + 6].zero_()
+        out.append(txl.relattn_tree_fwd(q, kn, vn, mem, 0, r, u, vb, parents, 0.125))
+        got.append(out)
+    assert txl.device_status() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[0][0])
+    assert torch.equal(got[1][1], got[1][0]) and torch.isfinite(got[0][0]).all()
+    del big
+    torch.cuda.empty_cache()
 
 
 def test_drafting_together():

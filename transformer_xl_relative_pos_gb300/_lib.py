@@ -2,6 +2,7 @@
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -445,7 +446,7 @@ class PagedKV:
     sequence's table rows 0 .. slots * page_rows - 1 form a ring.  begin, fill [B]
     int32: table row of its oldest memory row, and how many it holds (both zero
     when omitted).  Holds the tensors, of which the calls below read and write
-    the contents; all on one device."""
+    the contents, not the tensors themselves; all on one device."""
 
     def __init__(self, pool, table, begin=None, fill=None):
         if pool.dim() != 5 or pool.shape[0] % 2 or pool.shape[0] == 0:
@@ -454,24 +455,27 @@ class PagedKV:
             raise ValueError("table must be [B, slots]")
         B = table.shape[0]
         zeros = lambda: torch.zeros(B, dtype=torch.int32, device=pool.device)
-        self.pool, self.table = pool, table
-        self.begin = zeros() if begin is None else begin
-        self.fill = zeros() if fill is None else fill
-        self.ticket = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        begin = zeros() if begin is None else begin
+        fill = zeros() if fill is None else fill
+        ticket = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._tensors = pool, table, begin, fill, ticket
         self.layers, self.B, self.slots = pool.shape[0] // 2, B, table.shape[1]
         self.n_pages, self.H, self.page_rows = pool.shape[1:4]
-        ints = [(table, "table"), (self.begin, "begin"), (self.fill, "fill")]
+        ints = [(table, "table"), (begin, "begin"), (fill, "fill")]
         for t, name in ints[1:]:
             if tuple(t.shape) != (B,):
                 raise ValueError(f"{name} must be [B]")
         self._c = _PagedKV(_dev(pool, "pool"), *(_dev(t, n, torch.int32) for t, n in ints),
-                           self.ticket.data_ptr(), self.layers, self.n_pages, self.H,
+                           ticket.data_ptr(), self.layers, self.n_pages, self.H,
                            self.page_rows, pool.shape[4], B, self.slots, _code(pool.dtype))
         self._at = ctypes.addressof(self._c)
         self._dtype, self._index = pool.dtype, pool.get_device()
         for t, name in ints:
             _ptr(t, name, torch.int32, t.shape, self._index)
         self._shape = (B, self.H, pool.shape[4])
+
+    # (not to be replaced: the calls use their addresses)
+    pool, table, begin, fill, ticket = (property(lambda self, i=i: self._tensors[i]) for i in range(5))
 
     @property
     def rows(self) -> int:
@@ -540,6 +544,16 @@ def _paged_call(mem: PagedKV, name: str, stream, *args):
             rc = fn(*args, stream)
     if rc != 0:
         _check(rc, name)
+
+
+def _on_stream(mem: PagedKV, stream):
+    """Where a call makes its outputs: on its own stream, so that neither their filling
+    nor what used their memory before comes after the kernel."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=mem._index)
+    return torch.cuda.stream(stream)
 
 
 def _state_out(mem: PagedKV, state_out):
@@ -626,21 +640,25 @@ def relattn_tree_fwd(q, k_new, v_new, mem: PagedKV, layer: int, r, u, v_bias, pa
     attended as far as it goes; all of the memory's dtype (bf16 or fp32).
     n_nodes [B] int32: nodes of each sequence (all N when omitted); the rows of
     out and lse behind them are left as they were.  ``out``: a tensor to fill
-    ([B, H, N, 64], any strides); ``lse``: True, or a tensor [B, H, N] fp32.
+    ([B, H, N, 64], any strides); ``lse``: True, or a tensor [B, H, N] fp32.  Those made
+    here hold zeros behind n_nodes.
     Returns ``out`` or ``(out, lse)``."""
     B, H, dh = mem._shape
     shape, index, dt = q.shape, mem._index, mem._dtype
     if len(shape) != 4 or shape[0] != B or shape[1] != H or shape[3] != dh:
         raise ValueError(f"q must be [B, H, N, dh] of the memory, got {list(shape)}")
     N = shape[2]
-    if out is None:
-        # (zeros: rows behind n_nodes are not written)
-        out = torch.zeros(shape, dtype=dt, device=q.device)
     lse_at = n_at = None
     want_lse = lse is not None and lse is not False
+    if out is None or lse is True:
+        # (zeros where there may be rows behind n_nodes, which are not written)
+        make = torch.empty if n_nodes is None else torch.zeros
+        with _on_stream(mem, stream):
+            if out is None:
+                out = make(shape, dtype=dt, device=q.device)
+            if lse is True:
+                lse = make(shape[:3], dtype=torch.float32, device=q.device)
     if want_lse:
-        if lse is True:
-            lse = torch.zeros(shape[:3], dtype=torch.float32, device=q.device)
         lse_at = _ptr(lse, "lse", torch.float32, shape[:3], index)
     if r.dim() != 3:
         raise ValueError("r must be [H, r_rows, 64]")

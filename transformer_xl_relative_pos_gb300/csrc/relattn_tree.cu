@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
-    if (n == 0) return;  // (every block of the cluster)
+    if (n == 0) return finish_barriers(p);  // nothing of this sequence is written
     const int parent = threadIdx.x < n ? p.parents[b * p.parents_stride + threadIdx.x] : -1;
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // full, then empty, [KG][NSTG]

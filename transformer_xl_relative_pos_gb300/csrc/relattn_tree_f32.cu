@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
     const int rank = bh / p.mem.H, h = bh - rank * p.mem.H;
     const int b = pick_sequence(p, rank, reinterpret_cast<int *>(smem + C::OFF_TOPO));
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
-    if (n == 0) return;  // (every block of the cluster)
+    if (n == 0) return finish_barriers(p);  // nothing of this sequence is written
     const int parent = threadIdx.x < n ? p.parents[b * p.parents_stride + threadIdx.x] : -1;
 
     float *qs = reinterpret_cast<float *>(smem);
