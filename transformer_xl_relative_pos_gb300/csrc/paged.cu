@@ -11,7 +11,7 @@ namespace txl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowTile = 32;      // memory rows per block
+constexpr int kRowTile = 16;      // memory rows per block: more make too few blocks for a prompt (below)
 constexpr int kVecPerThread = 4;  // 16-byte vectors in flight per thread
 
 // n_new of sequence b taken into [0, max_rows] and to the room its table has.
@@ -40,13 +40,18 @@ __device__ __forceinline__ void advance(const AppendParams &p, int b)
     p.fill_out[b] = left;
 }
 
-// Rows [32 x, 32 x + 32) of sequence y's new rows into plane z (layer, key or
+// Rows [16 x, 16 x + 16) of sequence y's new rows into plane z (layer, key or
 // value) of its pages.  The addresses of a row (its page, its source) are found once per
 // row and block, in shared memory; then the rows' vectors go over the threads, a
 // row's heads and vectors innermost (a projection's output [rows][H][64] is read
 // in order; each head's row lands as 128 or 256 contiguous bytes of a page).
-// The first measured form of this kernel; bound by DRAM for prompts and by the chain of dependent
-// loads state -> table -> source -> store for a few rows.
+// Bound by DRAM for prompts: one layer, 16 sequences of 16 heads, 1600 rows each into empty
+// memories, 34.7 us for 210 MB read and written (6.05 TB/s, 89 % of a plain copy's rate; 32 rows a
+// block 37.6, 64 rows 41.7: the last wave of blocks is then a larger part).  Bound by the
+// chain of dependent loads state -> table -> source -> store for a few rows: the accepted
+// paths (1 to 8 rows) of 64 sequences of 16 heads in 12 layers 8.2 us for 28 MB, of one sequence
+// 2.5 us.  Keys and values by one block, which would walk that chain once: 9.3 and 38 us;
+// heads outermost: 8.4 and 36 us; eight vectors in flight: 11.4 and 42 us.
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p)
 {
     __shared__ long long s_dst[kRowTile];  // vector index of head 0's row in the plane; -1: none
@@ -81,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
         uint4 *dst = static_cast<uint4 *>(p.pool) +
                      (long long)(2 * layer + kv) * m.n_pages * m.H * m.P * V;
         const long long head_vec = (long long)m.P * V;
-        const int total = rows * m.H * V;      // <= 32 * H * 16
+        const int total = rows * m.H * V;      // <= 16 * H * 16
         for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kVecPerThread) {
             uint4 val[kVecPerThread];
             long long at[kVecPerThread];
@@ -95,8 +100,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
                 const long long d = s_dst[tt];
                 if (d < 0) continue;
                 at[c] = d + h * head_vec + vec;
-                val[c] = __ldcs(reinterpret_cast<const uint4 *>(
-                             src + (h * in.sh + s_src[tt] * in.sr) * p.esize) + vec);
+                val[c] = reinterpret_cast<const uint4 *>(
+                    src + (h * in.sh + s_src[tt] * in.sr) * p.esize)[vec];
             }
 #pragma unroll
             for (int c = 0; c < kVecPerThread; ++c)
@@ -129,9 +134,11 @@ __global__ void __launch_bounds__(kThreads) paged_advance_kernel(const AppendPar
     if (b < p.mem.B) advance(p, b);
 }
 
-// Page src[y] to page dst[y] of plane z; page_vec 16-byte vectors a page, x-th
-// part of it.
-constexpr int kCopyVec = 8;  // vectors per thread, all in flight at once
+// Part x mod parts of page src[x / parts] to page dst[x / parts] of plane y; page_vec 16-byte
+// vectors a page.  Bound by DRAM: 48 pages of 64 rows and 16 heads in 12 layers 45.1 us for
+// 302 MB (6.70 TB/s, 99 % of a plain copy's rate); a single page of 8 heads 1.7 us, which is the
+// launch and two dependent loads.  With eight vectors a thread 45.5 and 2.0 us.
+constexpr int kCopyVec = 2;  // vectors per thread, all in flight at once
 
 __global__ void __launch_bounds__(kThreads) paged_copy_kernel(uint4 *__restrict__ pool, int n_pages,
                                                               long long page_vec,
@@ -153,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(uint4 *__restrict_
     uint4 v[kCopyVec];
 #pragma unroll
     for (int c = 0; c < kCopyVec; ++c)
-        if (base + c * kThreads < page_vec) v[c] = __ldcs(from + base + c * kThreads);
+        if (base + c * kThreads < page_vec) v[c] = from[base + c * kThreads];
 #pragma unroll
     for (int c = 0; c < kCopyVec; ++c)
         if (base + c * kThreads < page_vec) to[base + c * kThreads] = v[c];

@@ -950,7 +950,7 @@ extern "C" int txl_paged_append(const txl_paged_kv *mem, int layer0, int n_layer
     if (n_layers > 1 && layer_stride < 1) return TXL_ERR_INVALID_ARG;
     if (n_layers > 1 && layer_stride % (16 / elem_size(mem->dtype)) != 0) return TXL_ERR_MISALIGNED;
     // blocks are counted in an int (the ticket), a block's rows times heads times vectors too
-    if ((long long)((max_rows + 31LL) / 32) * mem->B * 2 * n_layers > 0x7fffffffLL ||
+    if ((max_rows + 15LL) / 16 * mem->B * 2 * n_layers > 0x7fffffffLL ||
         mem->H > (1 << 20))
         return TXL_ERR_UNSUPPORTED;
     cudaError_t err;
@@ -1013,7 +1013,7 @@ extern "C" int txl_paged_copy(const txl_paged_kv *mem, const int *src, const int
     if (!aligned(src, 4) || !aligned(dst, 4)) return TXL_ERR_MISALIGNED;
     const long long page_vec =
         (long long)mem->H * mem->page_rows * mem->dh * elem_size(mem->dtype) / 16;
-    if ((page_vec / 2048 + 1) * n > 0x7fffffffLL) return TXL_ERR_UNSUPPORTED;
+    if ((page_vec / 512 + 1) * n > 0x7fffffffLL) return TXL_ERR_UNSUPPORTED;
     cudaError_t err;
     unsigned int *status = status_word(&err);
     if (!status) return TXL_ERR_CUDA;
