@@ -103,13 +103,17 @@ def parse_args():
     ap.add_argument("--decode", action="store_true",
                     help="time decode-shaped calls (a few new tokens against a long memory) "
                          "and their HBM bandwidth, instead of the headline step")
+    ap.add_argument("--tree", action="store_true",
+                    help="time the attention of drafted trees over a paged memory (and the append of "
+                         "an accepted path), instead of the headline step")
     ap.add_argument("--configs", action="store_true",
                     help="time one attention call of every bf16 workload shape, instead of the "
                          "headline step")
     ap.add_argument("--shapes", nargs="*", default=None,
-                    help="with --decode: B,L,M triples (default: the long-memory decode set)")
+                    help="with --decode: B,L,M triples (default: the long-memory decode set); with "
+                         "--tree: B,N,M of N nodes")
     ap.add_argument("--calls", type=int, default=10,
-                    help="with --decode or --configs: graph replays timed per shape (30 calls each)")
+                    help="with --decode, --tree or --configs: graph replays timed per shape (30 calls each)")
     ap.add_argument("--project", action="store_true",
                     help="time one layer's fused projection (txl_qkv_project) at the 12-layer "
                          "stream's shape against the unfused calls it replaces")
@@ -832,6 +836,88 @@ def run_decode(args):
             "splits": splits}}), flush=True)
 
 
+TREE_SHAPES = [(1, 1, 1600), (8, 8, 3800), (4, 26, 517), (16, 64, 3800), (64, 16, 3800)]
+
+
+def run_tree(args):
+    """Graph-replayed time and achieved HBM bandwidth of txl_relattn_tree_fwd (B sequences
+    of N drafted nodes, 16 heads, M memory rows each, pages of 64) and of
+    txl_paged_append putting eight of the nodes behind the memory."""
+    import torch
+    import transformer_xl_relative_pos_gb300 as txl
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    pk = peaks()
+    shapes = [tuple(int(x) for x in s.split(",")) for s in args.shapes] if args.shapes else TREE_SHAPES
+    H, P = 16, 64
+    for B, N, M in shapes:
+        n_acc = min(N, 8)
+        nbytes = 2 * (2 * B * H * (M + N) * 64 + H * (M + N) * 64 + 2 * B * H * N * 64) + 4 * B * H * N
+        acc_bytes = 2 * 2 * 2 * B * H * n_acc * 64
+        n_sets = max(1, min(3, -(-3 * 126 * 2 ** 20 // nbytes)))  # > L2 of traffic between reuses
+        g = torch.Generator(device=dev).manual_seed(B * 7919 + N * 31 + M)
+        mk = lambda *sh: (torch.randn(*sh, device=dev, generator=g) * 0.5).to(torch.bfloat16)
+        slots = -(-(M + N) // P) + 1
+        full = lambda x: torch.full((B,), x, dtype=torch.int32, device=dev)
+        ids = torch.arange(N, dtype=torch.int32, device=dev)
+        parents = torch.where(ids > 0, (ids - 1) // 2, -1).int()  # a binary tree
+        rows = ids[:n_acc].expand(B, n_acc).contiguous()
+        sets = []
+        for _ in range(n_sets):
+            table = torch.randperm(B * slots, device=dev, generator=g).int().view(B, slots)
+            mem = txl.PagedKV(mk(2, B * slots, H, P, 64), table, full(5), full(M))
+            sets.append((mem, mk(B, N, 3, H, 64), mk(H, M + N, 64)))
+        u, vb = mk(H, 64) * 0.2, mk(H, 64) * 0.2
+        out = torch.empty(B, N, H, 64, dtype=torch.bfloat16, device=dev).transpose(1, 2)
+        lse = torch.empty(B, H, N, device=dev)
+        state = torch.zeros(2, B, dtype=torch.int32, device=dev)
+
+        def tree(i):
+            mem, qkv, r = sets[i % n_sets]
+            q, k, v = (qkv[:, :, j].transpose(1, 2) for j in range(3))
+            txl.relattn_tree_fwd(q, k, v, mem, 0, r, u, vb, parents, 0.125, out=out, lse=lse)
+
+        def accept(i):
+            mem, qkv, _ = sets[i % n_sets]
+            k, v = (qkv[:, :, j].transpose(1, 2) for j in (1, 2))
+            txl.paged_append(mem, k, v, rows=rows, keep=M, state_out=(state[0], state[1]))
+
+        us, acc_us = graph_us(tree, args.calls, 30), graph_us(accept, args.calls, 30)
+        assert txl.device_status() == 0
+        gbs = nbytes / (us * 1e-6) / 1e9
+        print(json.dumps({"tree": {
+            "B": B, "H": H, "N": N, "M": M, "dtype": "bf16", "us_per_call": us, "algorithmic_bytes": nbytes,
+            "achieved_gbs": gbs, "peak_gbs": pk["hbm_gbs"], "hbm_frac": gbs / pk["hbm_gbs"],
+            "input_sets": n_sets, "append_us": acc_us, "append_rows": n_acc,
+            "append_bytes": acc_bytes}}), flush=True)
+        del sets
+
+
+def graph_us(call, reps, per):
+    """Device time of one call(i), i = 0, 1, ..., from replays of a graph of `per` of them."""
+    import torch
+    torch.cuda.synchronize()  # (the operands were made on another stream)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        for i in range(3):
+            call(i)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for i in range(per):
+            call(i)
+    graph.replay()
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record(stream)
+    with torch.cuda.stream(stream):
+        for _ in range(reps):
+            graph.replay()
+    e1.record(stream)
+    torch.cuda.synchronize()
+    return e0.elapsed_time(e1) * 1e3 / (reps * per)
+
+
 def run_configs(args):
     """Graph-replayed attention calls of every bf16 workload shape (random
     operands, rotating input sets larger than L2): TFLOP/s, fraction of the
@@ -1093,6 +1179,9 @@ def main():
         return
     if args.decode:
         run_decode(args)
+        return
+    if args.tree:
+        run_tree(args)
         return
     if args.configs:
         run_configs(args)

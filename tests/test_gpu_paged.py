@@ -272,3 +272,18 @@ def test_the_binding_refuses():
             bad()
         assert e.value.status == status
     assert txl.device_status() == 0
+
+
+def test_bench_tree_line():
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "bench.py", "--tree", "--shapes", "2,5,200", "--calls", "2"], cwd=root,
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    line = json.loads(r.stdout.strip().splitlines()[-1])["tree"]
+    # keys and values of 2 x 16 x 205 rows, the table, q and out, the log-sums
+    assert line["algorithmic_bytes"] == 2 * 64 * 16 * (2 * 2 * 205 + 205 + 2 * 2 * 5) + 4 * 2 * 16 * 5
+    assert line["us_per_call"] > 0 and line["append_us"] > 0 and 0 < line["hbm_frac"]
