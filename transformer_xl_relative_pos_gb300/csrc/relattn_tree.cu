@@ -45,10 +45,6 @@ using namespace tree;
 
 constexpr int WARPS = 4, ROWS = 16;        // warps that compute, nodes of a warp
 constexpr int THREADS = 2 * WARPS * 32;    // and as many for the copies, one per key group
-// Registers a thread of the two kinds (warpgroups) after the split of the 128 that two
-// blocks of 256 threads per SM leave; their sum must not exceed 256.
-constexpr int REGS_COMPUTE = 208, REGS_COPY = 48;
-static_assert(REGS_COMPUTE + REGS_COPY <= 256, "the block's registers at launch");
 constexpr int ROWB = DH * 2;               // bytes of a row
 constexpr int BOX = GK * ROWB;             // 4096: one 32-row box
 constexpr int ST_K = 0, ST_V = BOX, ST_R = 2 * BOX;
@@ -57,15 +53,26 @@ constexpr int STAGE = 3 * BOX;             // 12288
 template <int MT>
 struct Cfg {
     static constexpr int KG = WARPS / MT;      // key groups of a block
-    static constexpr int NSTG = MT == 1 ? 2 : MT == 2 ? 3 : 7;  // ring stages of a group
+    static constexpr int NSTG = MT == 1 ? 2 : MT == 2 ? 3 : 6;  // ring stages of a group
+    // With four node tiles the products with u and v, alike for all nodes, are made once per
+    // chunk by the three warps that have no copies, in turn (shared_biases): 48 MMAs of a
+    // warp's 80 remain.  16 sequences of 16 heads, 64 nodes, 3800 rows: 141 us, 156 without.  With
+    // two node tiles (and one such warp per key group) 32 nodes took 87 us against 83.
+    static constexpr bool SHARED = MT == 4;
+    static constexpr int HELPERS = WARPS - 1;
+    static_assert(!SHARED || (KG == 1 && NSTG % HELPERS == 0), "a stage has one helper, which sees its every phase");
+    // Registers a thread of the two kinds (warpgroups) after the split of the 128 that two
+    // blocks of 256 threads per SM leave.
+    static constexpr int REGS_COPY = SHARED ? 64 : 48, REGS_COMPUTE = 256 - REGS_COPY;
     static constexpr int DCAP = 16 * MT;       // depths are below this
     static constexpr int RW = GK + DCAP;       // columns of the product ring
     static constexpr int LD = RW + 8;          // its row stride (floats): 8 mod 16, so that the
                                                // quads' paired stores do not conflict
     static constexpr int SCR = 16 * LD * 4;    // bytes per warp
     static constexpr int OFF_SCR = KG * NSTG * STAGE;
-    static constexpr int OFF_BAR = OFF_SCR + WARPS * SCR;  // full[KG][NSTG], empty[KG][NSTG]
-    static constexpr int OFF_TOPO = OFF_BAR + 2 * KG * NSTG * 8;
+    static constexpr int OFF_BIAS = OFF_SCR + WARPS * SCR;  // SHARED: u.k and v.r of a stage's rows
+    static constexpr int OFF_BAR = OFF_BIAS + (SHARED ? NSTG * 2 * GK * 4 : 0);  // full[KG][NSTG], empty, biased
+    static constexpr int OFF_TOPO = OFF_BAR + 3 * KG * NSTG * 8;
     static constexpr int OFF_OK = OFF_TOPO + (int)sizeof(Topology);  // page of a stage valid
     static constexpr int OFF_FLAG = OFF_OK + KG * NSTG * 4;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // slack for the manual alignment
@@ -117,6 +124,11 @@ __device__ __forceinline__ float ld_scr(uint32_t addr)
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void ld_scr2(uint32_t addr, float &x, float &y)
+{
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void st_scr2(uint32_t addr, float x, float y)
@@ -255,6 +267,65 @@ __device__ __forceinline__ float element(const float (&c)[4], int r, int e)
     return HALF ? c[e] + c[2 + e] : c[2 * r + e];
 }
 
+// u.k_j and v.r_t of the block's chunks, every HELPERS-th item from item `first` on (one warp):
+// summed by the tensor cores in fp32, as the products with q are.  Per item it waits for
+// the copies and arrives on the stage's `biased`, for which every warp that computes waits
+// before it lets the stage go: none of the barriers runs ahead of another by two phases.
+template <int MT>
+__device__ __forceinline__ void shared_biases(const TreeParams &p, int begin, int fill, int n, int h, int split,
+                                              int first, uint8_t *smem, int lane)
+{
+    using C = Cfg<MT>;
+    constexpr int NSTG = C::NSTG;
+    const int t = lane & 3, lr = lane & 7, lm = lane >> 3;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR), *biased = full + 2 * NSTG;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
+    const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split, p.n_splits);
+    const int nodes = split == p.n_splits - 1 ? (n + GK - 1) / GK : 0;  // (items without biases)
+    const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u, some = p.scale_log2 == 0.f ? 0u : ~0u;
+    // A operands whose rows are all u, or all v: registers 0 = 1 and 2 = 3 of each step
+    uint32_t a[2][4][2];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const int w = h * (DH / 2) + 4 * x + t;
+        a[0][x >> 1][x & 1] = (__ldg(static_cast<const uint32_t *>(p.u) + w) ^ sign) & some;
+        a[1][x >> 1][x & 1] = (__ldg(static_cast<const uint32_t *>(p.vb) + w) ^ sign) & some;
+    }
+    for (int item = first; item < nodes + ck.count; item += C::HELPERS) {
+        const int st = item % NSTG;
+        if (!__all_sync(0xffffffffu, mbar_wait(full + st, (item / NSTG) & 1, abort_flag, p.wait_ns))) {
+            if (lane == 0) {
+                *abort_flag = 1;
+                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+            }
+            return;
+        }
+        if (item >= nodes) {
+            float *out = reinterpret_cast<float *>(smem + C::OFF_BIAS) + st * 2 * GK;
+#pragma unroll
+            for (int uv = 0; uv < 2; ++uv) {
+                const uint32_t rows = smem_u32(smem) + st * STAGE + (uv ? ST_R : ST_K);
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    uint32_t b[2][4];
+                    float c[4];
+                    ldsm_x4(b[0], rows + swz(8 * nt + lr, lm));
+                    ldsm_x4(b[1], rows + swz(8 * nt + lr, 4 + lm));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint32_t a4[4] = {a[uv][ks][0], a[uv][ks][0], a[uv][ks][1], a[uv][ks][1]};
+                        if (ks == 0) mma16816_first(c, a4, b[0][0], b[0][1]);
+                        else mma16816(c, a4, b[ks >> 1][2 * (ks & 1)], b[ks >> 1][2 * (ks & 1) + 1]);
+                    }
+                    if (lane < 4) *reinterpret_cast<float2 *>(out + uv * GK + 8 * nt + 2 * t) = make_float2(c[0], c[1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(biased + st);
+    }
+}
+
 // MT node tiles of 16; HALF: at most 8 nodes (one tile, whose rows 8 to 15 then take u, v
 // and the probabilities' residuals: half the MMAs).
 template <int MT, bool HALF>
@@ -283,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (n == 0) return finish_barriers(p);  // nothing of this sequence is written
     const int parent = threadIdx.x < n ? p.parents[b * p.parents_stride + threadIdx.x] : -1;
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // full, then empty, [KG][NSTG]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // full, empty, biased, [KG][NSTG] each
     volatile int *stage_ok = reinterpret_cast<volatile int *>(smem + C::OFF_OK);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     Topology &topo = *reinterpret_cast<Topology *>(smem + C::OFF_TOPO);
@@ -297,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         // Boxes are always complete (rows past a tensor's ends arrive as zeros): a page
         // id out of range becomes a plane past the pool's end, and its rows are masked.
         // The id of a page is loaded an item ahead.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPY));
         const int group = warp - WARPS;
         const bool mine = group < KG;
         if (warp == WARPS && lane == 0) *abort_flag = 0;
@@ -305,6 +376,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int s = 0; s < NSTG; ++s) {
                 mbar_init(bars + group * NSTG + s, 1);
                 mbar_init(bars + (KG + group) * NSTG + s, MT);
+                mbar_init(bars + (2 * KG + group) * NSTG + s, 1);
             }
             fence_barrier_init();
         }
@@ -376,13 +448,17 @@ __global__ void __launch_bounds__(THREADS, 2)
                 mbar_wait(bars + group * NSTG + x % NSTG, (x / NSTG) & 1, &zero, p.wait_ns);
         }
         __syncwarp();
+        if constexpr (C::SHARED) {
+            if (!mine) shared_biases<MT>(p, begin, fill, n, h, split, group - 1, smem, lane);
+        }
         finish_barriers(p);
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_COMPUTE));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_COMPUTE));
 
     const uint8_t *ring = smem + kg * NSTG * STAGE;
     uint64_t *full = bars + kg * NSTG, *empty = full + KG * NSTG;
+    uint64_t *filled = C::SHARED ? empty + KG * NSTG : full;  // an item's data are there
     float *scr = reinterpret_cast<float *>(smem + C::OFF_SCR + warp * C::SCR);
     const uint32_t scr_at = smem_u32(scr);
     const Chunks ck = group_chunks(p, begin, fill, kNodesCost, split * KG + kg, p.n_splits * KG);
@@ -539,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     bool ok = true;
     if (!active)  // (a warp without nodes only lets the stages go)
         for (int box = 0; box < nodes && ok; ++box) {
-            ok = __all_sync(0xffffffffu, mbar_wait(full + box % NSTG, (box / NSTG) & 1, abort_flag, p.wait_ns));
+            ok = __all_sync(0xffffffffu, mbar_wait(filled + box % NSTG, (box / NSTG) & 1, abort_flag, p.wait_ns));
             if (lane == 0 && ok) mbar_arrive(empty + box % NSTG);
         }
     if (owner) {
@@ -552,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         __syncwarp();
         for (int box = 0; box < nodes && ok; ++box) {
-            ok = __all_sync(0xffffffffu, mbar_wait(full + box % NSTG, (box / NSTG) & 1, abort_flag, p.wait_ns));
+            ok = __all_sync(0xffffffffu, mbar_wait(filled + box % NSTG, (box / NSTG) & 1, abort_flag, p.wait_ns));
             // (no node is an ancestor of an earlier one: boxes past this tile are hidden)
             if (ok && box * GK < mt * 16 + 16) {
                 const uint8_t *base = ring + (box % NSTG) * STAGE;
@@ -626,7 +702,12 @@ __global__ void __launch_bounds__(THREADS, 2)
             ok = __all_sync(0xffffffffu, mbar_wait(full + stg, phase, abort_flag, p.wait_ns));
             if (!ok) break;
         }
-        const int this_stg = stg;
+        const int this_stg = stg, this_phase = phase;
+        // (SHARED: the products with u and v of this item are there)
+        auto biased = [&] {
+            return !C::SHARED ||
+                   __all_sync(0xffffffffu, mbar_wait(filled + this_stg, this_phase, abort_flag, p.wait_ns));
+        };
         if (++stg == NSTG) {
             stg = 0;
             phase ^= 1;
@@ -638,7 +719,8 @@ __global__ void __launch_bounds__(THREADS, 2)
             const uint32_t sk = smem_u32(base + ST_K), sv = smem_u32(base + ST_V), sr = smem_u32(base + ST_R);
             const int j0 = (ck.c0 + item - nodes) * GK - ck.off;  // memory row of the chunk's first key
 
-            // content and position products, eight independent accumulators in turn (one
+            // content and position products (SHARED: those with q; the others' sums are added
+            // behind them), eight independent accumulators in turn (one
             // after the other, each MMA would wait for the one before)
             float c[4][4], cr[4][4];
 #pragma unroll
@@ -653,8 +735,21 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (int x = 0; x < 2; ++x) {
                     q_products<HALF>(c, aq, au, 2 * h2 + x, bk, 2 * x);
                     q_products<HALF>(cr, aq, av, 2 * h2 + x, br, 2 * x);
-                    bias_products<HALF>(c, au, 2 * h2 + x, bk, 2 * x);
-                    bias_products<HALF>(cr, av, 2 * h2 + x, br, 2 * x);
+                    bias_products<HALF || C::SHARED>(c, au, 2 * h2 + x, bk, 2 * x);
+                    bias_products<HALF || C::SHARED>(cr, av, 2 * h2 + x, br, 2 * x);
+                }
+            }
+            ok = biased();
+            if (!ok) break;
+            if constexpr (C::SHARED) {
+                const uint32_t bias = smem_u32(smem + C::OFF_BIAS) + this_stg * 2 * GK * 4 + 8 * t;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    float b0, b1;
+                    ld_scr2(bias + 32 * nt, b0, b1);
+                    c[nt][0] += b0, c[nt][1] += b1, c[nt][2] += b0, c[nt][3] += b1;
+                    ld_scr2(bias + GK * 4 + 32 * nt, b0, b1);
+                    cr[nt][0] += b0, cr[nt][1] += b1, cr[nt][2] += b0, cr[nt][3] += b1;
                 }
             }
 #pragma unroll
@@ -729,6 +824,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                 }
             }
             wpos = next;
+        } else {
+            ok = biased();
+            if (!ok) break;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + this_stg);  // this warp has read the stage
