@@ -353,6 +353,7 @@ template <typename... KArgs>
 int max_clusters(void (*kern)(KArgs...), int n_splits, int threads, int smem)
 {
     ClusterConfig c(n_splits, n_splits, threads, smem, nullptr);
+    c.cfg.numAttrs = 1;  // (a cluster of one block too)
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &c.cfg) != cudaSuccess) {
         cudaGetLastError();  // (no sticky error is left to a later launch check)

@@ -4,6 +4,7 @@
 // relattn_combine.cu, relattn_f32.cu, relpos.cu, mem.cu); this file only
 // checks and dispatches.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -1023,17 +1024,40 @@ extern "C" int txl_paged_copy(const txl_paged_kv *mem, const int *src, const int
 
 namespace {
 
-// Key ranges of a head: the caller's n_splits or, for 0, as many as let every head's
-// cluster be resident at once, at most one per 128 table rows (the host does not know
-// the fills) and at most a cluster's worth.  What fits counts, not the number of
-// blocks: 48 heads of 3800 rows take 13.0 us in 240 blocks (5 ranges), all resident, and 18.5 us
-// in 288, whose clusters of 6 do not all find room.
+// Key ranges of a head: the caller's n_splits or, for 0, by the cost of S ranges (at most a
+// cluster's worth and one per 128 table rows; the host does not know the fills)
+//   waves(S) * (chunks / S + kSplitCost)
+// where a wave is as many clusters of S blocks as are resident at once, and a block costs
+// kSplitCost chunks besides its keys (launch, the tree, merges).  A last wave of at most half
+// the clusters counts three quarters: its blocks have an SM to themselves.  The most ranges that
+// are resident at once (or one range, in several waves) give way to more when those cost
+// clearly less; memories of unlike lengths, longest first, pack several waves better than this
+// says, hence the two margins.  Measured (16 heads, 3800 rows): 8 sequences of 8 nodes 21.7 us
+// in 2 ranges (1 wave), 24.7 in 4; 10 sequences of 64 nodes 114 us in 3 ranges (2 waves), 139 in
+// 1 (1 wave); 16 sequences 141 us in 1, 157 in 2; 20 sequences 222 us in 3, 245 in 1 (2 waves); 13
+// sequences of 500 to 3800 rows 79 us in 2, 128 in 1; 40 such of 8 nodes 63 us in 1, 76 in 2.
+constexpr int kSplitCost = 10;
+
 int tree_splits(long long BH, int table_rows, int N, bool f32, int n_splits)
 {
     if (n_splits > 0) return n_splits;
-    int s = std::min(txl::kTreeMaxCluster, (table_rows + 127) / 128);
-    while (s > 1 && BH > (f32 ? txl::tree_max_clusters_f32(N, s) : txl::tree_max_clusters(N, s))) --s;
-    return s;
+    const float chunks = (float)((table_rows + 31) / 32);
+    int best = 1;
+    float least = INFINITY;
+    for (int s = std::min(txl::kTreeMaxCluster, (table_rows + 127) / 128); s >= 1; --s) {
+        const int resident = f32 ? txl::tree_max_clusters_f32(N, s) : txl::tree_max_clusters(N, s);
+        if (resident < 1) continue;
+        const long long full = BH / resident, rest = BH % resident;
+        const float last = rest == 0 ? 0.f : full > 0 && 2 * rest <= resident ? 0.75f : 1.f;
+        const float cost = ((float)full + last) * (chunks / (float)s + kSplitCost);
+        const bool one_wave = BH <= resident;
+        if (cost * (one_wave ? 0.95f : s == 1 ? 0.85f : 1.f) <= least) {
+            least = cost;
+            best = s;
+        }
+        if (one_wave) break;  // fewer ranges are one wave of longer ones
+    }
+    return best;
 }
 
 } // namespace
