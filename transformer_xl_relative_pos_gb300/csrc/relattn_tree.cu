@@ -53,6 +53,7 @@ constexpr int STAGE = 3 * BOX;             // 12288
 template <int MT>
 struct Cfg {
     static constexpr int KG = WARPS / MT;      // key groups of a block
+    static_assert(KG == tree_key_groups(16 * MT), "as the choice of key ranges has it");
     static constexpr int NSTG = MT == 1 ? 2 : MT == 2 ? 3 : 6;  // ring stages of a group
     // With four node tiles the products with u and v, alike for all nodes, are made once per
     // chunk by the three warps that have no copies, in turn (shared_biases): 48 MMAs of a

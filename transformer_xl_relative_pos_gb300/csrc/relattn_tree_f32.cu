@@ -27,6 +27,7 @@ template <int MT_, int ROWS_>
 struct CfgF32 {
     static constexpr int MT = MT_, ROWS = ROWS_, KG = WARPS / MT;
     static constexpr int NODES = MT * ROWS;
+    static_assert(KG == tree_key_groups(NODES), "as the choice of key ranges has it");
     static constexpr int DCAP = NODES;         // depths are below this
     static constexpr int RW = GK + DCAP;       // columns of the product ring
     static constexpr int Q = 2 * NODES * SLD;  // floats: q + u, q + v of the nodes

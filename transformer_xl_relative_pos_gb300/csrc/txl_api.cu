@@ -1025,7 +1025,8 @@ extern "C" int txl_paged_copy(const txl_paged_kv *mem, const int *src, const int
 namespace {
 
 // Key ranges of a head: the caller's n_splits or, for 0, by the cost of S ranges (at most a
-// cluster's worth and one per 128 table rows; the host does not know the fills)
+// cluster's worth, and no more than leave each key group of a block a chunk of 32 rows; the
+// host does not know the fills)
 //   waves(S) * (chunks / S + kSplitCost)
 // where a wave is as many clusters of S blocks as are resident at once, and a block costs
 // kSplitCost chunks besides its keys (launch, the tree, merges).  A last wave of at most half
@@ -1035,7 +1036,8 @@ namespace {
 // says, hence the two margins.  Measured (16 heads, 3800 rows): 8 sequences of 8 nodes 21.7 us
 // in 2 ranges (1 wave), 24.7 in 4; 10 sequences of 64 nodes 114 us in 3 ranges (2 waves), 139 in
 // 1 (1 wave); 16 sequences 141 us in 1, 157 in 2; 20 sequences 222 us in 3, 245 in 1 (2 waves); 13
-// sequences of 500 to 3800 rows 79 us in 2, 128 in 1; 40 such of 8 nodes 63 us in 1, 76 in 2.
+// sequences of 500 to 3800 rows 79 us in 2, 98 in 4, 128 in 1; 40 such of 8 nodes 63 us in 1, 76 in
+// 2.  Eight heads, 64 nodes, one sequence of 260 rows: 10.1 us in 8, 15.1 in 3.
 constexpr int kSplitCost = 10;
 
 int tree_splits(long long BH, int table_rows, int N, bool f32, int n_splits)
@@ -1044,7 +1046,8 @@ int tree_splits(long long BH, int table_rows, int N, bool f32, int n_splits)
     const float chunks = (float)((table_rows + 31) / 32);
     int best = 1;
     float least = INFINITY;
-    for (int s = std::min(txl::kTreeMaxCluster, (table_rows + 127) / 128); s >= 1; --s) {
+    const int unit = 32 * txl::tree_key_groups(N);
+    for (int s = std::min(txl::kTreeMaxCluster, (table_rows + unit - 1) / unit); s >= 1; --s) {
         const int resident = f32 ? txl::tree_max_clusters_f32(N, s) : txl::tree_max_clusters(N, s);
         if (resident < 1) continue;
         const long long full = BH / resident, rest = BH % resident;
