@@ -539,8 +539,9 @@ int txl_page_pool_release(txl_page_pool *p, const int *pages, int n, int *n_free
  * Rows i >= n_b of out and lse are left as they were; those rows of q, k_new and
  * v_new, and what the pages hold outside the memory rows, have no influence.
  * All of mem->dtype.  TXL_BF16: products on the tensor cores, fp32 sums; the
- * probabilities enter as bf16 pairs (value and residual).  TXL_F32: fp32
- * arithmetic.  1 <= N <= 64, dh = 64.
+ * probabilities enter as bf16 pairs (value and residual), or, for N > 16, rounded to
+ * one bf16 value.  TXL_F32: fp32 arithmetic.  1 <= N <= 64, dh = 64.  mem's arrays,
+ * parents and n_nodes must not change while the call runs.
  * n_splits: key ranges per (b, h), merged inside a thread-block cluster: 0 lets
  * the library choose, at most 8 (larger requests are refused).  No workspace.
  * Errors: TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED (N > 64, dh, page_rows, dtype,

@@ -46,7 +46,7 @@ __device__ __forceinline__ void advance(const AppendParams &p, int b)
 // row's heads and vectors innermost (a projection's output [rows][H][64] is read
 // in order; each head's row lands as 128 or 256 contiguous bytes of a page).
 // Bound by DRAM for prompts: one layer, 16 sequences of 16 heads, 1600 rows each into empty
-// memories, 34.7 us for 210 MB read and written (6.05 TB/s, 89 % of a plain copy's rate; 32 rows a
+// memories, 34.7 us for 210 MB read and written (6.05 TB/s, 0.9 of a plain copy's rate; 32 rows a
 // block 37.6, 64 rows 41.7: the last wave of blocks is then a larger part).  Bound by the
 // chain of dependent loads state -> table -> source -> store for a few rows: the accepted
 // paths (1 to 8 rows) of 64 sequences of 16 heads in 12 layers 8.2 us for 28 MB, of one sequence
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) paged_advance_kernel(const AppendPar
 
 // Part x mod parts of page src[x / parts] to page dst[x / parts] of plane y; page_vec 16-byte
 // vectors a page.  Bound by DRAM: 48 pages of 64 rows and 16 heads in 12 layers 45.1 us for
-// 302 MB (6.70 TB/s, 99 % of a plain copy's rate); a single page of 8 heads 1.7 us, which is the
+// 302 MB (6.70 TB/s, a plain copy's rate); a single page of 8 heads 1.7 us, which is the
 // launch and two dependent loads.  With eight vectors a thread 45.5 and 2.0 us.
 constexpr int kCopyVec = 2;  // vectors per thread, all in flight at once
 

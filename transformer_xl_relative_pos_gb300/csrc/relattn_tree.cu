@@ -21,10 +21,21 @@
 //            are read back shifted by the nodes' depths; the next chunk's
 //            window needs D of them again, so no table row is multiplied twice.
 //   P.V      2 steps of 16 keys x 8 tiles of 8 dimensions
-// q and u (or v) enter as they are, one MMA each into the same accumulator: the
-// scores are exact products summed in fp32.  P enters as two bf16 values (value and
-// residual), to about 2^-17 relative, so that the output's own rounding is the one
-// that shows.
+// q and u (or v) enter as they are, one MMA each into the same accumulator (at most 8
+// nodes: q and the bias as the two halves of one tile's rows): the scores are exact products
+// summed in fp32.  P enters as two bf16 values (value and residual), to about 2^-17
+// relative, so that the output's own rounding is the one that shows; in trees of more than 16
+// nodes, where the MMAs count, as one, 2^-8 (half a step of bf16, as large as the output's own
+// rounding; 16 sequences of 64 nodes 180 us with residuals, 161 without, at that time).
+//
+// Measured (16 heads, 3800 rows, graph replays over inputs larger than L2): 19 sequences fill the two blocks of every SM, and take 46 us for 8 nodes
+// (0.99 of a plain copy's rate, bound by DRAM), 52 us for 16 (0.88), 82 us for 32 and 140 us for 64.
+// Those two are bound by latency: two warps that compute per SM quarter, whose matrix
+// instructions, shared-memory accesses and issue slots are each about half busy.  One sequence
+// of one node over 1600 rows takes 6.7 us, of which 2 are an empty kernel's and the rest a chain of
+// dependent steps: state, page ids, copies, products, the merges of warps and blocks.
+// What was tried for the wide trees and was slower: tcgen05 tiles of 128 rows [q; u; v] (bound by
+// shared memory), 32 nodes a warp (registers), three blocks per SM (A operands re-read).
 //
 // Copies: each key group has a ring of stages [32 k rows | 32 v rows | 32 table
 // rows], three TMA boxes on one mbarrier, swizzled so that the matrix loads are
