@@ -308,16 +308,17 @@ def test_scales_of_either_sign(N, scale, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B,H", [(40, 10), (255, 2), (256, 2)])
-def test_many_sequences_of_unlike_lengths(B, H, dtype):
-    # more blocks than are resident at once: the longest memories come first (up to 255
-    # sequences); equal lengths and sequences without nodes among them
+@pytest.mark.parametrize("B,H,slots", [(40, 10, 64), (64, 5, 64), (33, 16, 64), (40, 10, 6), (65, 5, 64), (256, 2, 6)])
+def test_many_sequences_of_unlike_lengths(B, H, slots, dtype):
+    # more blocks than are resident at once: the longest memories come first (up to 64
+    # sequences, with tables of 2048 rows and more); equal lengths and sequences without
+    # nodes among them
     g = torch.Generator().manual_seed(B)
     fills = torch.randint(0, 130, (B,), generator=g).tolist()
     fills[1] = fills[7] = fills[B - 1]
     counts = [2] * B
     counts[3] = counts[B - 2] = 0
-    Case(B, H, 2, fills, P=32, counts=counts, dtype=dtype, seed=24).check()
+    Case(B, H, 2, fills, P=32, slots=slots, counts=counts, dtype=dtype, seed=24).check()
 
 
 def test_outputs_made_by_the_call_belong_to_its_stream():

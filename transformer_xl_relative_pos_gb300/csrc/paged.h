@@ -9,7 +9,7 @@ namespace txl {
 
 constexpr int kTreeMaxNodes = 64;   // nodes of a drafted tree (one 64-bit ancestor mask)
 constexpr int kTreeMaxCluster = 8;  // key ranges of a head: one portable thread-block cluster
-constexpr int kTreeMaxSorted = 255; // sequences whose blocks can be ordered by length
+constexpr int kTreeMaxSorted = 64;  // sequences whose blocks can be ordered by length
 // Key groups of a block in a tree of N nodes: its four warps that compute hold 16 nodes each.
 constexpr int tree_key_groups(int N) { return N <= 16 ? 4 : N <= 32 ? 2 : 1; }
 constexpr int kPageRowUnit = 32;    // page_rows is a multiple of this: keys of one tile

@@ -91,8 +91,6 @@ struct Cfg {
     // where a warp leaves its record: its private ring, or (shared ring) its scratch
     static_assert(MT == 1 || sizeof(Rec<ROWS>) <= SCR, "a warp's record fits in its scratch");
     static_assert(sizeof(Rec<ROWS>) <= NSTG * STAGE, "a warp's record fits in its ring");
-    static_assert((kTreeMaxSorted + 1) * 4 <= sizeof(Topology),
-                  "the order by length is found in the topology's place");
     static_assert(OFF_BAR % 8 == 0 && OFF_TOPO % 8 == 0, "8-byte alignment");
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks per SM");
 };
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int split = blockIdx.x % p.n_splits;
     const int bh = blockIdx.x / p.n_splits;
     const int rank = bh / p.mem.H, h = bh - rank * p.mem.H;
-    const int b = pick_sequence(p, rank, reinterpret_cast<int *>(smem + C::OFF_TOPO));
+    const int b = pick_sequence(p, rank, *reinterpret_cast<Topology *>(smem + C::OFF_TOPO));
     int begin, fill;
     paged_state(p.mem, b, p.status, begin, fill);
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;

@@ -41,7 +41,6 @@ struct CfgF32 {
     static constexpr int OFF_TOPO = OFF_WARP + WARPS * WARP * 4;
     static constexpr int SMEM = OFF_TOPO + (int)sizeof(Topology);
     static_assert(sizeof(WarpRec) <= WARP * 4, "a warp's record fits");
-    static_assert((kTreeMaxSorted + 1) * 4 <= sizeof(Topology), "the order by length is found in the topology's place");
     static_assert(SMEM <= 232448, "shared memory budget exceeded");
     static_assert(OFF_TOPO % 16 == 0 && RING % 4 == 0 && PROB % 4 == 0 && WARP % 4 == 0, "alignment");
 };
@@ -62,7 +61,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) relattn_tree_f32_kernel(const T
     const int split = blockIdx.x % p.n_splits;
     const int bh = blockIdx.x / p.n_splits;
     const int rank = bh / p.mem.H, h = bh - rank * p.mem.H;
-    const int b = pick_sequence(p, rank, reinterpret_cast<int *>(smem + C::OFF_TOPO));
+    const int b = pick_sequence(p, rank, *reinterpret_cast<Topology *>(smem + C::OFF_TOPO));
     const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), p.N) : p.N;
     if (n == 0) return finish_barriers(p);  // nothing of this sequence is written
     const int parent = threadIdx.x < n ? p.parents[b * p.parents_stride + threadIdx.x] : -1;

@@ -73,28 +73,29 @@ struct Topology {
     unsigned long long anc[kTreeMaxNodes];
     int depth[kTreeMaxNodes];
     int hop[kTreeMaxNodes];
+    int picked;  // pick_sequence's
 };
 
 // Sequence of this block: the ranks of the grid (rank = block / (H * n_splits)) in
 // order, or, by_length, longest memory first: with more blocks than are resident at
 // once and unlike lengths, the blocks that start last are then the short ones.
-// All threads of the block; scratch: B + 1 ints.
-__device__ __forceinline__ int pick_sequence(const TreeParams &p, int rank, int *scratch)
+// Every block finds the one of its rank: a warp has all lengths in its lanes, and counts for
+// its share of the sequences how many come before.  All threads of the block.
+__device__ __forceinline__ int pick_sequence(const TreeParams &p, int rank, Topology &topo)
 {
+    static_assert(kTreeMaxSorted == 64, "two lengths a lane");
     if (!p.by_length) return rank;
-    const int B = p.mem.B;
-    for (int i = threadIdx.x; i < B; i += blockDim.x) scratch[i] = p.mem.fill[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < B; i += blockDim.x) {
-        const int mine = scratch[i];
-        int before = 0;
-        for (int j = 0; j < B; ++j) before += scratch[j] > mine || (scratch[j] == mine && j < i);
-        if (before == rank) scratch[B] = i;
+    const int B = p.mem.B, lane = threadIdx.x & 31;
+    constexpr int NONE = (int)0x80000000;
+    const int f0 = lane < B ? p.mem.fill[lane] : NONE, f1 = lane + 32 < B ? p.mem.fill[lane + 32] : NONE;
+    for (int i = threadIdx.x >> 5; i < B; i += blockDim.x >> 5) {
+        const int mine = __shfl_sync(0xffffffffu, i < 32 ? f0 : f1, i & 31);
+        const unsigned before0 = __ballot_sync(0xffffffffu, f0 > mine || (f0 == mine && lane < i));
+        const unsigned before1 = __ballot_sync(0xffffffffu, f1 > mine || (f1 == mine && lane + 32 < i));
+        if (lane == 0 && __popc(before0) + __popc(before1) == rank) topo.picked = i;
     }
     __syncthreads();
-    const int b = scratch[B];
-    __syncthreads();  // the scratch is free again
-    return b;
+    return topo.picked;
 }
 
 // By pointer doubling: after round r a node knows its 2^r nearest ancestors.  A

@@ -1114,9 +1114,13 @@ extern "C" int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new,
     p.N = N;
     p.r_rows = r_rows;
     p.n_splits = splits;
-    // More blocks than one wave holds: the longest memories first (64 sequences of 16
-    // heads with 950 to 3800 rows: 135 us in the grid's order, 126 us so).
-    p.by_length = BH * splits > 2LL * sm_count() && mem->B > 1 && mem->B <= txl::kTreeMaxSorted;
+    // More blocks than one wave holds and room for long memories: the longest first, which
+    // costs every block about 1.3 us at its start.  16 heads: 64 sequences of 16 nodes and 950 to 3800
+    // rows 137 us in the grid's order, 127 us so; 24 of 64 nodes and 500 to 3800 rows 176 and 131; but 64
+    // sequences of 8 nodes and 250 to 900 rows 40.5 and 44.0, of one node and 500 to 1600 rows 54.5
+    // and 59.5, 100 sequences of 950 to 3800 rows 154 and 167.
+    p.by_length = BH * splits > 2LL * sm_count() && mem->B > 1 && mem->B <= txl::kTreeMaxSorted &&
+                  mem->slots * mem->page_rows >= 2048;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = status;
     p.wait_ns = g_wait_ns;
