@@ -449,7 +449,7 @@ typedef struct {
  * n_layers - 1, every sequence b, head and t < n_new[b]:
  *   memory row fill[b] + t  <-  row (rows ? rows[b][t] : t) of k and v
  *   k, v    layer layer0 + l of them starts l * layer_stride elements on
- *           (layer_stride is a multiple of 16 bytes); N rows each.
+ *           (layer_stride is a multiple of 16 bytes); N rows each, outside the pool.
  *   n_new   device [B], values taken into [0, max_rows]; NULL: max_rows
  *   rows    device [B][rows_stride >= max_rows] of source rows in [0, N) (the
  *           accepted nodes of a drafted tree, say; the same row may come more

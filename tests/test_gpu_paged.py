@@ -230,6 +230,37 @@ def test_append_and_copy_in_a_graph_and_on_another_stream():
     check(mem, want)
 
 
+def test_the_same_row_twice_and_one_page_copied_to_several():
+    mem, g = make(2, 3, 32, 4, 2, "bf16", seed=31, fill=[10, 40])
+    k, v = operand(2, 2, 3, 5, "bf16", g, "stacked")
+    rows = [[4, 4, 0, 4], [1, 1, 1, 1]]
+    want = model_append(mem, k, v, 0, [4, 3], rows, 60)
+    txl.paged_append(mem, k, v, rows=torch.tensor(rows, dtype=torch.int32, device=dev()),
+                     n_new=torch.tensor([4, 3], dtype=torch.int32, device=dev()), keep=60)
+    check(mem, want)
+    pool = mem.pool.cpu().clone()
+    free = [p for p in range(mem.n_pages) if p not in mem.table.cpu()]
+    page = int(mem.table[0, 0])
+    pool[:, free] = pool[:, [page] * len(free)]
+    ids = lambda x: torch.tensor(x, dtype=torch.int32, device=dev())
+    txl.paged_copy(mem, ids([page] * len(free)), ids(free))
+    check(mem, (pool, *want[1:]))
+
+
+def test_layers_appended_at_once_on_streams():
+    # Without a state to advance, calls for different layers of one memory may overlap.
+    mem, g = make(3, 4, 64, 6, 4, "bf16", seed=32, fill=[0, 100, 250])
+    k, v = operand(4, 3, 4, 100, "bf16", g, "stacked")
+    want = model_append(mem, k, v, 0, [100] * 3, None, 200)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for i, s in enumerate(streams):
+        txl.paged_append(mem, k[i], v[i], layer=i, stream=s)
+    torch.cuda.synchronize()
+    txl.paged_advance(mem, 100, keep=200)
+    check(mem, want)
+
+
 def test_calls_for_different_memories_at_once():
     mems = [make(3, 4, 64, 8, 2, "bf16", seed=20 + i, fill=[7, 100, 300]) for i in range(2)]
     ops = [operand(2, 3, 4, 90, "bf16", g, "stacked") for _, g in mems]
