@@ -21,8 +21,15 @@ def kv(**kw):
     return _lib._PagedKV(*(a[f] for f, _ in _lib._PagedKV._fields_))
 
 
+class Rows(ctypes.Structure):
+    """txl_rows."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("stride_row", ctypes.c_longlong)]
+
+
 def rows(ptr=1 << 16, sb=2048, sh=64, sr=128):
-    return _lib._Rows(ptr, sb, sh, sr)
+    return Rows(ptr, sb, sh, sr)
 
 
 BAD_KV = [(dict(pool=None), INVALID), (dict(table=None), INVALID), (dict(begin=None), INVALID),

@@ -45,13 +45,6 @@ class KVWindow(ctypes.Structure):
                 f"M={self.M})")
 
 
-class _Rows(ctypes.Structure):
-    """txl_rows: a [B, H, rows, 64] operand by its pointer and element strides."""
-
-    _fields_ = [("ptr", _c_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
-                ("stride_row", ctypes.c_longlong)]
-
-
 class _PagedKV(ctypes.Structure):
     """txl_paged_kv."""
 
