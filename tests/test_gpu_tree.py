@@ -4,7 +4,9 @@ counts from one to 64, memories from none to long ones that begin and end inside
 a tile and go around their ring, tables shorter than the memory, NaN and infinities in
 every place that must have no influence, key ranges, layouts, both types."""
 
-import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -373,6 +375,27 @@ def test_offsets_past_32_bits(dtype):
     assert torch.equal(got[1][1], got[1][0]) and torch.isfinite(got[0][0]).all()
     del big
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_first_call_of_a_process_may_be_captured(dtype):
+    # (attributes and occupancy of the kernels are looked up during a capture then)
+    code = ("import sys; sys.path[:0] = ['tests', '.']\n"
+            "import torch, numpy as np\n"
+            "from test_gpu_tree import Case\n"
+            f"c = Case(2, 2, 12, [200, 64], dtype='{dtype}', seed=27)\n"
+            "torch.cuda.synchronize()\n"
+            "g = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(g):\n"
+            "    c.call()\n"
+            "g.replay()\n"
+            "torch.cuda.synchronize()\n"
+            "out, lse, out_b, lse_b = c.want()\n"
+            "assert (np.abs(c.out.cpu().double().numpy() - out) <= out_b).all()\n"
+            "print('ok')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-3000:]
 
 
 def test_drafting_together():
