@@ -1,0 +1,59 @@
+"""txl_relattn_tree_fwd where its result is known without a tolerance for rounding: a node's result
+does not depend on its neighbours' queries."""
+
+import numpy as np
+import pytest
+import torch
+
+import transformer_xl_relative_pos_gb300 as txl
+from parity import dev
+from test_gpu_tree import Case
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [2, 8, 9, 16, 26, 40, 64])
+def test_a_node_does_not_depend_on_its_neighbours_queries(N, dtype):
+    # The running maxima of a tile's nodes rise in other chunks than their neighbours': a
+    # node's own sums are not touched then.  Node i with all other queries zero, bit for bit.
+    c = Case(1, 2, N, [1500], kind="chain", dtype=dtype, std=4.0, seed=31)
+    c.call(1)
+    out, lse, q = c.out.clone(), c.lse.clone(), c.q.clone()
+    for i in (0, N // 2, N - 1):
+        c.q.zero_()
+        c.q[:, :, i] = q[:, :, i]
+        c.call(1)
+        assert torch.equal(c.lse[:, :, i], lse[:, :, i]), i
+        assert torch.equal(c.out[:, :, i], out[:, :, i]), i
+    assert txl.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_lse_of_a_constant_beside_rising_scores(N, dtype):
+    # Even nodes: every score is a (one exact product), so lse = scale * a + log(keys), whatever
+    # the odd nodes' maxima do in every chunk.  Roundings on the way: log2(e), its product with
+    # the scale, the score in log2 units, the last sum, ln(2) and its product: six half steps of
+    # lse; the sum of K equal terms (K / 16 + 64) * 2 u, exp2 2^-22.
+    F, a = 3200, 11520.0
+    c = Case(1, 1, N, [F], dtype=dtype, P=64, begin=[0], seed=32, kind="wide")
+    page = c.mem.table[0].long()
+    keys = torch.zeros(c.mem.slots * 64, 64, dtype=torch.float32)
+    t = torch.arange(F)
+    keys[:F, 0], keys[:F, 1] = 1.0, (t // 32).float()
+    c.mem.pool[0, page, 0] = keys.view(-1, 64, 64).to(c.dt).to(dev())
+    c.r.zero_(), c.u.zero_(), c.vb.zero_(), c.q.zero_(), c.k.zero_()
+    c.k[..., 0] = 1.0
+    c.q[:, :, 0::2, 0] = a
+    c.q[:, :, 1::2, 1] = 16.0
+    c.parents.fill_(-1)
+    c.call(1)
+    K = F + 1
+    want = 0.125 * a + np.log(K)
+    bound = 6 * U * want + (K / 16 + 64) * 2 * U + 2.0 ** -22
+    got = c.lse[0, 0, 0::2].cpu().double().numpy()
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got - want).max(), bound)
+    assert txl.device_status() == 0

@@ -186,13 +186,15 @@ __device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR
         mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
         // a row without a visible key so far: any finite value makes its probabilities zero
-        ms[r] = mx[r] == -INFINITY ? 0.f : mx[r] * scale;
+        ms[r] = mx[r] == -INFINITY ? 0.f : __fmul_rn(mx[r], scale);
         moved |= !(mx[r] == st.m[r]);
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            const float f = ex2f(fmaf(st.m[r], scale, -ms[r]));  // (0 from -inf: the sums are zero then)
+            // The old maximum as it was rounded when it was the new one, not fused with the
+            // difference: a row whose maximum has not moved is rescaled by exactly one.
+            const float f = ex2f(__fmul_rn(st.m[r], scale) - ms[r]);  // (0 from -inf: the sums are zero then)
             st.m[r] = mx[r];
             st.l[r] *= f;
 #pragma unroll
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
         if (t == 0) {
-            mine->m[g + 8 * r] = st.m[r] * scale;  // log2 units
+            mine->m[g + 8 * r] = __fmul_rn(st.m[r], scale);  // log2 units
             mine->l[g + 8 * r] = st.l[r];
         }
 #pragma unroll
