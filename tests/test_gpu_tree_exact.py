@@ -1,5 +1,5 @@
 """txl_relattn_tree_fwd where its result is known without a tolerance for rounding: a node's result
-does not depend on its neighbours' queries."""
+does not depend on its neighbours' queries, and infinite values show as the formula has them."""
 
 import numpy as np
 import pytest
@@ -57,3 +57,32 @@ def test_lse_of_a_constant_beside_rising_scores(N, dtype):
     got = c.lse[0, 0, 0::2].cpu().double().numpy()
     assert (np.abs(got - want) <= bound).all(), (np.abs(got - want).max(), bound)
     assert txl.device_status() == 0
+
+
+def check_infinite_values(N, n_splits, dtype):
+    # Rows that every node sees: an infinity is the sum's, infinities of either sign and NaN
+    # give NaN, and the other dimensions are as without them.
+    c = Case(1, 2, N, [300], dtype=dtype, seed=33, begin=[11])
+    out, lse, out_b, lse_b = c.want()
+    x = (11 + torch.arange(300)) % c.mem.rows
+    page, row = c.mem.table[0].cpu().long()[x // 64], x % 64
+    inf, nan = float("inf"), float("nan")
+    for t, dim, value in ((3, 5, inf), (130, 5, inf), (40, 6, -inf), (299, 20, inf), (0, 21, -inf),
+                          (100, 7, inf), (250, 7, -inf), (77, 8, nan)):
+        c.mem.pool[1, page[t], :, row[t], dim] = value
+    c.call(n_splits)
+    torch.cuda.synchronize()
+    assert txl.device_status() == 0
+    got = c.out.cpu().double().numpy()
+    for dim, value in ((5, inf), (6, -inf), (20, inf), (21, -inf)):
+        assert (got[..., dim] == value).all(), (dim, got[..., dim])
+    assert np.isnan(got[..., [7, 8]]).all()
+    rest = [d for d in range(64) if d not in (5, 6, 7, 8, 20, 21)]
+    assert (np.abs(got - out) <= out_b)[..., rest].all()
+    assert (np.abs(c.lse.cpu().double().numpy() - lse) <= lse_b).all()
+
+
+@pytest.mark.parametrize("N,dtype,n_splits", [(N, "f32", s) for N in (1, 5, 8, 13, 17, 64) for s in (0, 1, 3, 7)] +
+                         [(N, "bf16", s) for N in (17, 32, 40, 64) for s in (0, 1, 2, 5)])
+def test_infinite_values_in_key_ranges(N, n_splits, dtype):
+    check_infinite_values(N, n_splits, dtype)

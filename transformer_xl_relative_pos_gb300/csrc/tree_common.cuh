@@ -280,7 +280,7 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
         const uint32_t at_m = smem_u32(&r->m[i % ROWS]), at_l = smem_u32(&r->l[i % ROWS]);
         const uint32_t at_a = smem_u32(&r->a[i % ROWS][2 * lane]);
         // (every load on its way before the first is used; ranks past the last: rank 0
-        // again, without weight)
+        // again, its values replaced by an empty result's, as zero weight times an infinity is NaN)
         float m[kTreeMaxCluster], l[kTreeMaxCluster];
         float2 a[kTreeMaxCluster];
 #pragma unroll
@@ -293,7 +293,10 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
         float mx = -INFINITY;
 #pragma unroll
         for (int s = 0; s < kTreeMaxCluster; ++s) {
-            m[s] = s < p.n_splits ? m[s] : -INFINITY;
+            if (s >= p.n_splits) {
+                m[s] = -INFINITY;
+                l[s] = a[s].x = a[s].y = 0.f;
+            }
             mx = max_nan(mx, m[s]);
         }
         const float ref = mx == -INFINITY ? 0.f : mx;
