@@ -86,3 +86,9 @@ def check_infinite_values(N, n_splits, dtype):
                          [(N, "bf16", s) for N in (17, 32, 40, 64) for s in (0, 1, 2, 5)])
 def test_infinite_values_in_key_ranges(N, n_splits, dtype):
     check_infinite_values(N, n_splits, dtype)
+
+
+@pytest.mark.parametrize("n_splits", [0, 1, 2, 5])
+@pytest.mark.parametrize("N", [1, 5, 7, 8, 9, 13, 16])
+def test_infinite_values_with_probabilities_in_two_parts(N, n_splits):
+    check_infinite_values(N, n_splits, "bf16")

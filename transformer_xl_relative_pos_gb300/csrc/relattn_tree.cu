@@ -162,19 +162,31 @@ __device__ __forceinline__ void cp_async_hold(uint64_t *bar)
 }
 
 // The running softmax and output of a warp's nodes: NR rows per lane (g, and g + 8
-// when NR = 2); its output columns are 8 nd + 2 t, + 1.  With NR = 1 (at most 8 nodes)
-// the accumulators' rows g + 8 hold the products with the probabilities' residuals.
-template <int NR>
+// when NR = 2); its output columns are 8 nd + 2 t, + 1.  LO: the products with the
+// probabilities' residuals, kept apart until the end, as a residual (of either sign, or zero)
+// times an infinity must not meet the infinity of the product itself.  With NR = 1 (at most 8
+// nodes) they are the accumulators' rows g + 8, with NR = 2 accumulators of their own.
+template <int NR, bool LO>
 struct State {
+    static constexpr bool APART = LO && NR == 2;
     float m[NR], l[NR];
     float acc[8][4];
+    float res[APART ? 8 : 1][4];
+    // Column e (0, 1) of this lane's row r in tile nd: an infinite product stands by itself.
+    __device__ __forceinline__ float out(int nd, int r, int e) const
+    {
+        const float x = acc[nd][2 * r + e];
+        if constexpr (!LO) return x;
+        const float y = NR == 1 ? acc[nd][2 + e] : res[APART ? nd : 0][2 * r + e];
+        return fabsf(x) == INFINITY ? x : x + y;
+    }
 };
 
 // One chunk's masked scores s (before the scale; s[nt][2 r + e]: row r of this lane, key
 // 8 nt + 2 t + e) into probabilities, rescaling the state to the new maximum.
 // scale > 0, to log2 units.
-template <int NR>
-__device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR], float scale)
+template <int NR, bool LO>
+__device__ __forceinline__ void softmax_step(State<NR, LO> &st, float (&s)[4][2 * NR], float scale)
 {
     float mx[NR], ms[NR];
     bool moved = false;
@@ -200,7 +212,10 @@ __device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR
 #pragma unroll
             for (int nd = 0; nd < 8; ++nd)
 #pragma unroll
-                for (int e = 0; e < 4 / NR; ++e) st.acc[nd][2 * r + e] *= f;
+                for (int e = 0; e < 4 / NR; ++e) {
+                    st.acc[nd][2 * r + e] *= f;
+                    if constexpr (State<NR, LO>::APART) st.res[nd][2 * r + e] *= f;
+                }
         }
     }
 #pragma unroll
@@ -218,8 +233,8 @@ __device__ __forceinline__ void softmax_step(State<NR> &st, float (&s)[4][2 * NR
 
 // acc += P.V over 16 keys 16 kk .. + 15, v[nd]: their fragments of dimensions 8 nd .. + 7.
 // The probabilities enter as bf16 and, with LO (NR = 1: always), their residuals.
-template <bool LO, int NR>
-__device__ __forceinline__ void pv_step(State<NR> &st, const float (&s)[4][2 * NR], int kk,
+template <int NR, bool LO>
+__device__ __forceinline__ void pv_step(State<NR, LO> &st, const float (&s)[4][2 * NR], int kk,
                                         const uint32_t (&v)[8][2])
 {
     uint32_t hi[4], lo[4];
@@ -238,7 +253,7 @@ __device__ __forceinline__ void pv_step(State<NR> &st, const float (&s)[4][2 * N
     for (int nd = 0; nd < 8; ++nd) mma16816(st.acc[nd], hi, v[nd][0], v[nd][1]);
     if constexpr (LO && NR == 2) {
 #pragma unroll
-        for (int nd = 0; nd < 8; ++nd) mma16816(st.acc[nd], lo, v[nd][0], v[nd][1]);
+        for (int nd = 0; nd < 8; ++nd) mma16816(st.res[nd], lo, v[nd][0], v[nd][1]);
     }
 }
 
@@ -546,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // visible to the same nodes and whose values hold an infinity or NaN, which must
     // not reach the nodes that do not see the key.  hidden: bit 4 nt + 2 r + e of this
     // lane's elements.  col0: 32 free ring columns.
-    State<NR> st;
+    State<NR, MT == 1> st;
     auto pv_by_element = [&](const auto &s, uint32_t hidden, int col0, const uint8_t *values) {
         auto at = [&](int key) { const int c = col0 + key; return c >= RW ? c - RW : c; };
         __syncwarp();
@@ -622,7 +637,10 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
     for (int nd = 0; nd < 8; ++nd)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.acc[nd][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+            st.acc[nd][e] = 0.f;
+            if constexpr (decltype(st)::APART) st.res[nd][e] = 0.f;
+        }
 
     bool ok = true;
     if (!active)  // (a warp without nodes only lets the stages go)
@@ -685,7 +703,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     for (int kk = 0; kk < 2; ++kk) {
                         uint32_t bv[8][2];
                         load_v(bv, smem_u32(base + ST_V), kk);
-                        pv_step<MT == 1>(st, s, kk, bv);
+                        pv_step(st, s, kk, bv);
                     }
                 }
             }
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                             bv[kk][nd][1] &= keep1;
                         }
                     }
-                    pv_step<MT == 1>(st, s, kk, bv[kk]);
+                    pv_step(st, s, kk, bv[kk]);
                 }
             }
             wpos = next;
@@ -864,7 +882,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
         for (int nd = 0; nd < 8; ++nd)
             *reinterpret_cast<float2 *>(&mine->a[g + 8 * r][8 * nd + 2 * t]) =
-                make_float2(element<HALF>(st.acc[nd], r, 0), element<HALF>(st.acc[nd], r, 1));
+                make_float2(st.out(nd, r, 0), st.out(nd, r, 1));
     }
     finish<WARPS, KG, MT, __nv_bfloat16>(rec, p, b, h, n, warp, lane);
 }
