@@ -527,7 +527,10 @@ int txl_page_pool_release(txl_page_pool *p, const int *pages, int n, int *n_free
  *   A_ij = scale * ((q_i + u).k_j + (q_i + v_bias).r[r_rows - 1 - distance])
  *   out_i = sum_j softmax_j(A_i.) v_j,  lse_i = log sum_j exp(A_ij)
  * over the visible nodes and memory rows whose distance is below r_rows (a
- * memory longer than the table is attended to as far as the table goes).
+ * memory longer than the table is attended to as far as the table goes).  A node sees
+ * itself at least.  Infinite values of what it sees show as in the formula, and so does a row
+ * whose every score is -infinity (out NaN, lse -infinity); q.k and u.k, and q.r and
+ * v_bias.r, are summed apart: infinities of unlike sign in them make the row NaN.
  *
  *   q, out        [B][H][N][dh]    (strided; out must not overlap the inputs)
  *   k_new, v_new  [B][H][N][dh]    the nodes' keys and values

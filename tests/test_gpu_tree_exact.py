@@ -1,5 +1,6 @@
 """txl_relattn_tree_fwd where its result is known without a tolerance for rounding: a node's result
-does not depend on its neighbours' queries, and infinite values show as the formula has them."""
+does not depend on its neighbours' queries, infinite values show as the formula has them, and
+nodes whose every score is -infinity."""
 
 import numpy as np
 import pytest
@@ -92,3 +93,22 @@ def test_infinite_values_in_key_ranges(N, n_splits, dtype):
 @pytest.mark.parametrize("N", [1, 5, 7, 8, 9, 13, 16])
 def test_infinite_values_with_probabilities_in_two_parts(N, n_splits):
     check_infinite_values(N, n_splits, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("F,n_splits", [(0, 1), (90, 1), (90, 4)])
+@pytest.mark.parametrize("N", [1, 8, 12, 30, 64])
+def test_nodes_whose_every_score_is_minus_infinity(N, F, n_splits, dtype):
+    # softmax of nothing but -infinity is 0 / 0: out NaN, lse -infinity.  The other half of the
+    # heads is as ever.
+    c = Case(2, 2, N, [F, F], kind="chain", dtype=dtype, seed=34)
+    out, lse, out_b, lse_b = c.want()
+    c.q[:, 0, :, 3], c.u[0, 3] = 1.0, 0.5
+    c.k[:, 0, :, 3] = -float("inf")
+    c.mem.pool[0, :, 0, :, 3] = -float("inf")
+    c.call(n_splits)
+    torch.cuda.synchronize()
+    assert txl.device_status() == 0
+    got, got_lse = c.out.cpu().double().numpy(), c.lse.cpu().double().numpy()
+    assert np.isnan(got[:, 0]).all() and (got_lse[:, 0] == -np.inf).all()
+    assert (np.abs(got - out) <= out_b)[:, 1].all() and (np.abs(got_lse - lse) <= lse_b)[:, 1].all()

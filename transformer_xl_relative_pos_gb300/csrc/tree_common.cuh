@@ -220,6 +220,8 @@ __device__ __forceinline__ void cluster_done()
 // the blocks of the cluster, whose warps share the nodes; write out and lse of the n nodes.
 // A partial result stays unnormalised until the last merge:
 //   m = max m_g, l = sum 2^(m_g - m) l_g, a = sum 2^(m_g - m) a_g, out = a / l.
+// Every node sees itself at least, so l = 0 only where all its scores are -infinity: 0 / 0, NaN
+// as in the formula.
 template <int NW, int KG, int MT, typename T, typename RecOf>
 __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, int h, int n, int warp,
                                        int lane)
@@ -229,9 +231,9 @@ __device__ __forceinline__ void finish(RecOf rec, const TreeParams &p, int b, in
     T *out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + b * p.out.sb + h * p.out.sh;
     float *lse = p.lse ? p.lse + ((long long)b * p.mem.H + h) * p.N : nullptr;
     auto write = [&](int i, float m, float l, float o0, float o1) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = 1.f / l;
         put_row(out + i * p.out.sr, lane, o0 * inv, o1 * inv);
-        if (lse && lane == 0) lse[i] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        if (lse && lane == 0) lse[i] = (m + log2f(l)) * LN2;
     };
     __syncthreads();
     if (KG > 1 || p.n_splits == 1) {
