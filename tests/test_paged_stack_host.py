@@ -1,0 +1,74 @@
+"""The paged stack's host side on the CPU: with fakes of the device calls (the attention of a draft
+by the 64-bit model of tests/tree_model.py), restoring checkpoints."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import txl_inputs
+from test_paged_host import FakeKV, fake_append, fake_copy
+from tree_model import tree_attention
+from transformer_xl_relative_pos_gb300 import model, paged
+
+W = txl_inputs.Workload("paged_host", B=2, H=2, dh=4, L=8, M=70, d_model=8, dtype="f32", seed=61,
+                        d_ff=16, n_layer=2, n_seg=3, vocab=31)
+
+
+def fake_tree(q, k_new, v_new, mem, layer, r, u, v_bias, parents, scale, *, n_nodes=None, out=None, **kw):
+    B, N = q.shape[0], q.shape[2]
+    counts = [N] * B if n_nodes is None else n_nodes.tolist()
+    got = torch.from_numpy(tree_attention(q, k_new, v_new, mem, layer, r, u, v_bias, parents, scale, counts)[0])
+    out.copy_(torch.where(torch.isnan(got), out.double(), got))
+    return out
+
+
+@pytest.fixture(autouse=True)
+def on_the_cpu(monkeypatch):
+    monkeypatch.setattr(paged.txl, "PagedKV", FakeKV)
+    monkeypatch.setattr(paged.txl, "paged_copy", fake_copy)
+    monkeypatch.setattr(paged.txl, "paged_append", fake_append)
+    monkeypatch.setattr(model.txl, "relattn_tree_fwd", fake_tree)
+    monkeypatch.setattr(model.txl, "rel_pos_emb", lambda K, d, dtype, device: torch.from_numpy(
+        oracle.reversed_table(oracle.sinusoid_table(K, d))).to(dtype))
+
+
+def stack(M=W.M, H=W.H):
+    return model.XLStack(txl_inputs.draw_stack(W), H, M, "cpu", torch.float32, paged=True)
+
+
+def tokens(B, N, seed=0):
+    return torch.randint(0, W.vocab, (B, N), generator=torch.Generator().manual_seed(seed))
+
+
+def memory(M, max_new, P=32, fill=0):
+    mem = paged.PagedMemory(1, 2, 1, M, max_new, device="cpu", dtype=torch.float32, page_rows=P, dh=2)
+    while mem.fill[0] < fill:
+        k = torch.ones(1, 2, 1, min(max_new, fill - mem.fill[0]), 2)
+        mem.append(k, k)
+    return mem
+
+
+@pytest.mark.parametrize("theirs,ours,P", [((150, 10), (60, 100), 32), ((60, 100), (150, 10), 32),
+                                           ((128, 64), (70, 64), 64), ((70, 64), (128, 64), 64)])
+def test_a_checkpoint_of_another_memory_length_is_refused(theirs, ours, P):
+    # The tables have one shape, the lengths that the memories slide by do not.
+    a, b = memory(*theirs, P, fill=theirs[0]), memory(*ours, P, fill=20)
+    assert a.kv.table.shape == b.kv.table.shape
+    before = b._table.copy(), list(b.begin), list(b.fill), b.pages.n_free, b.kv.pool.clone()
+    with pytest.raises(ValueError):
+        b.restore(a.checkpoint())
+    assert (b._table == before[0]).all() and (b.begin, b.fill) == before[1:3]
+    assert b.pages.n_free == before[3] and torch.equal(b.kv.pool, before[4])
+
+
+def test_a_checkpoint_that_names_no_length_is_refused_by_its_fills():
+    # (as an earlier version wrote them)
+    a = memory(128, 64, 64, fill=100)
+    ck = a.checkpoint()
+    ck = {k: ck[k] for k in ("pool", "table", "begin", "fill", "users")}
+    with pytest.raises(ValueError):
+        memory(70, 64, 64).restore(ck)
+    b = memory(128, 64, 64)
+    b.restore(ck)
+    assert b.fill == [100, 100]

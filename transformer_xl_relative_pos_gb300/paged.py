@@ -201,7 +201,7 @@ class PagedMemory:
         """Host copy of the memory (compacted first)."""
         n = self.compact()
         return {"pool": self.kv.pool[:, :n].to("cpu", copy=True), "table": self._table.copy(),
-                "begin": list(self.begin), "fill": list(self.fill),
+                "begin": list(self.begin), "fill": list(self.fill), "M": self.M, "max_new": self.max_new,
                 "users": [self.pages.users(p) for p in range(n)]}
 
     def restore(self, ck: dict):
@@ -210,6 +210,10 @@ class PagedMemory:
         if (ck["table"].shape != self._table.shape or ck["pool"].shape != pool.shape or
                 ck["pool"].dtype != pool.dtype):
             raise ValueError("restore: a memory of other shapes")
+        # (slots are rounded up to pages: memories of other lengths can have tables of one shape)
+        if ((ck.get("M", self.M), ck.get("max_new", self.max_new)) != (self.M, self.max_new) or
+                max(ck["fill"]) > self.M):
+            raise ValueError("restore: a memory of another length or of other appends")
         self._table = ck["table"].copy()
         self.begin, self.fill = list(ck["begin"]), list(ck["fill"])
         self._recount(dict(enumerate(ck["users"])))
