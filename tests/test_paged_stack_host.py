@@ -72,3 +72,32 @@ def test_a_checkpoint_that_names_no_length_is_refused_by_its_fills():
     b = memory(128, 64, 64)
     b.restore(ck)
     assert b.fill == [100, 100]
+
+
+def test_a_refused_checkpoint_leaves_the_stack_as_it_is():
+    a, other = stack(), stack(M=40)
+    for s in (a, other):
+        s.segment(tokens(2, 8, seed=1))
+    h = a.draft(tokens(2, 3, seed=2), torch.tensor([-1, 0, 0]))
+    memory, ck = a.memory, other.checkpoint()
+    for bad in (ck, {"paged": dict(a.checkpoint()["paged"], M=71)},
+                {"paged": dict(a.checkpoint()["paged"], pool=ck["paged"]["pool"].double())}):
+        with pytest.raises(ValueError):
+            a.restore(bad)
+        assert a.memory is memory and a.memory.fill == [8, 8]
+    assert torch.equal(a.draft(tokens(2, 3, seed=2), torch.tensor([-1, 0, 0])), h)
+    a.accept([[0, 2], [0]])
+    assert a.memory.fill == [10, 9]
+
+
+def test_a_checkpoint_resumes():
+    a, b = stack(), stack()
+    a.segment(tokens(2, 8, seed=1))
+    ck = a.checkpoint()
+    want = a.segment(tokens(2, 5, seed=2))
+    b.segment(tokens(2, 9, seed=3))
+    b.draft(tokens(2, 2, seed=4), torch.tensor([-1, 0]))
+    b.restore(ck)
+    with pytest.raises(RuntimeError):
+        b.accept([[0], [0]])                 # (what was drafted before is of another memory)
+    assert torch.equal(b.segment(tokens(2, 5, seed=2)), want)

@@ -144,8 +144,7 @@ class XLStack:
         self._graphs = {}
         self._full_segments = 0
         if self.paged:
-            self.memory = PagedMemory(len(self.layers), B, self.H, self.M, self.MAX_DRAFT,
-                                      device=self.device, dtype=self.dtype, dh=self.dh)
+            self.memory = self._paged_memory(B)
             self._draft = None
             return
         self.mems = [torch.zeros(B, self.M, self.d, dtype=self.dtype, device=self.device)
@@ -157,6 +156,10 @@ class XLStack:
         # (window positions then repeat with the rings')
         self.kvbufs = self.kv_windows = None
         self._kv_L = None
+
+    def _paged_memory(self, B: int) -> PagedMemory:
+        return PagedMemory(len(self.layers), B, self.H, self.M, self.MAX_DRAFT, device=self.device,
+                           dtype=self.dtype, dh=self.dh)
 
     def _kv_reset(self, B: int, L: int):
         period = self.M // math.gcd(self.M, L) if self.M > 0 else 1
@@ -193,8 +196,9 @@ class XLStack:
         if self.paged != ("paged" in ck):
             raise ValueError("restore: the checkpoint is of a stack with other options")
         if self.paged:
-            self.reset(len(ck["paged"]["fill"]))
-            self.memory.restore(ck["paged"])
+            memory = self._paged_memory(len(ck["paged"]["fill"]))
+            memory.restore(ck["paged"])   # (a refusal leaves the running streams as they are)
+            self.memory, self._draft = memory, None
             return
         B = ck["mems"][0].shape[0]
         self.reset(B)
