@@ -1,5 +1,6 @@
 """The paged stack's host side on the CPU: with fakes of the device calls (the attention of a draft
-by the 64-bit model of tests/tree_model.py), restoring checkpoints."""
+by the 64-bit model of tests/tree_model.py), restoring checkpoints and
+what accept takes."""
 
 import numpy as np
 import pytest
@@ -101,3 +102,36 @@ def test_a_checkpoint_resumes():
     with pytest.raises(RuntimeError):
         b.accept([[0], [0]])                 # (what was drafted before is of another memory)
     assert torch.equal(b.segment(tokens(2, 5, seed=2)), want)
+
+
+@pytest.mark.parametrize("form", ["tensor", "list"])
+def test_only_paths_of_drafted_nodes_are_accepted(form):
+    # Sequence 0: 0 -> 1 -> 2, 0 -> 3 -> 4 -> 5; sequence 1: 0 -> 1, 2 -> 3 (4 and 5 are not drafted).
+    parents, n_nodes = [[-1, 0, 1, 0, 3, 4], [-1, 0, -1, 2, 3, 4]], [6, 4]
+    a = stack()
+    a.segment(tokens(2, 8, seed=1))
+    if form == "tensor":
+        parents, n_nodes = torch.tensor(parents), torch.tensor(n_nodes)
+    a.draft(tokens(2, 6, seed=2), parents, n_nodes)
+    for bad in ([[0, 1, 3], []],             # 3 follows 0
+                [[0, 2], []], [[1], []],     # an ancestor left out
+                [[1, 0], []], [[0, 0], []],  # out of order, twice
+                [[], [2, 3, 4]], [[], [4]],  # behind the sequence's nodes
+                [[], [0, 1, 2]],             # another root's
+                [[6], []], [[-1], []], [[0]], [[0], [0], [0]]):
+        with pytest.raises(ValueError):
+            a.accept(bad)
+        assert a.memory.fill == [8, 8]
+    if form == "tensor":                     # what the caller does with them afterwards is of no account
+        parents.fill_(-1), n_nodes.zero_()
+    a.accept([[0, 3, 4], (2, 3)])
+    assert a.memory.fill == [11, 10]
+
+
+def test_one_tree_for_all_and_parents_that_are_no_earlier_nodes():
+    a = stack()
+    a.draft(tokens(2, 4, seed=3), torch.tensor([9, 0, 2, -7]))   # node 0, 2 and 3 follow the memory
+    with pytest.raises(ValueError):
+        a.accept([[0, 1, 2], []])
+    a.accept([[0, 1], np.array([3])])
+    assert a.memory.fill == [2, 1]

@@ -111,7 +111,7 @@ class XLStack:
                              "replayed from graphs")
         self.paged = paged
         self.memory = None       # paged: the PagedMemory
-        self._draft = None       # paged: q, k and v of the last draft
+        self._draft = None       # paged: q, k and v of the last draft, its parents and n_nodes
         self.H, self.M, self.dtype, self.device = H, M, dtype, torch.device(device)
         self.cache_kv = cache_kv
         self.graphs = graphs
@@ -316,6 +316,8 @@ class XLStack:
             raise ValueError(f"draft: 1 to {self.MAX_DRAFT} tokens")
         if self.memory is None or self.memory.B != B:
             self.reset(B)
+        # accept() looks at the tree as it was given (read back there if it lies on the device)
+        given = [None if t is None else torch.as_tensor(t).clone() for t in (parents, n_nodes)]
         i32 = lambda t: torch.as_tensor(t).to(device=self.device, dtype=torch.int32).contiguous()
         parents = i32(parents)
         n_nodes = None if n_nodes is None else i32(n_nodes)
@@ -331,17 +333,36 @@ class XLStack:
                                  self.u, self.v_bias, parents, self.scale, n_nodes=n_nodes,
                                  out=a.transpose(1, 2))
             h = self._rest_of_layer(lay, h, a.view(B, N, -1)).to(self.dtype)
-        self._draft = qkv
+        self._draft = qkv, *given
         return h
 
     def accept(self, rows):
         """Accept nodes of the last draft: rows[b] lists those of sequence b in the
         order of the text (a path of its tree from a first token on; none: []).  Their
-        keys and values go behind the memory of every layer, which keeps the newest M."""
+        keys and values go behind the memory of every layer, which keeps the newest M.
+        Anything but such paths of drafted nodes is refused (ValueError)."""
         if self._draft is None:
             raise RuntimeError("accept: nothing is drafted")
-        k, v = (self._draft[:, :, :, i].transpose(2, 3) for i in (1, 2))
-        self.memory.append(k, v, rows=[list(r) for r in rows])
+        qkv, parents, n_nodes = self._draft
+        B, N = qkv.shape[1:3]
+        rows = [[int(i) for i in r] for r in rows]
+        if len(rows) != B:
+            raise ValueError(f"accept: one path for each of the {B} sequences")
+        parents = parents.expand(B, N).tolist()
+        counts = [N] * B if n_nodes is None else n_nodes.tolist()
+        for b, path in enumerate(rows):
+            before = -1
+            for i in path:
+                if not 0 <= i < min(N, counts[b]):
+                    raise ValueError(f"accept: sequence {b} has no drafted node {i}")
+                # (a parent that is no earlier node counts as none, as in the attention)
+                parent = parents[b][i] if 0 <= parents[b][i] < i else -1
+                if parent != before:
+                    raise ValueError(f"accept: node {i} of sequence {b} does not follow "
+                                     f"{f'node {before}' if before >= 0 else 'its memory'}")
+                before = i
+        k, v = (qkv[:, :, :, i].transpose(2, 3) for i in (1, 2))
+        self.memory.append(k, v, rows=rows)
         self._draft = None
 
     def fork(self, src: int, dst: int):
