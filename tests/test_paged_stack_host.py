@@ -1,6 +1,6 @@
 """The paged stack's host side on the CPU: with fakes of the device calls (the attention of a draft
-by the 64-bit model of tests/tree_model.py), restoring checkpoints and
-what accept takes."""
+by the 64-bit model of tests/tree_model.py), restoring checkpoints,
+what accept takes, and taps."""
 
 import numpy as np
 import pytest
@@ -135,3 +135,27 @@ def test_one_tree_for_all_and_parents_that_are_no_earlier_nodes():
         a.accept([[0, 1, 2], []])
     a.accept([[0, 1], np.array([3])])
     assert a.memory.fill == [2, 1]
+
+
+def test_taps_of_a_draft_hold_every_layer():
+    # Sequences of 8 and 10 rows, and a chain of 5: each layer's attention and output follow from
+    # what its tap holds, and a tap keeps it when the memory goes on.
+    a = stack()
+    a.segment(tokens(2, 8, seed=1))
+    a.draft(tokens(2, 2, seed=2), torch.tensor([-1, 0]))
+    a.accept([[], [0, 1]])
+    a.taps = []
+    h = a.segment(tokens(2, 5, seed=3))
+    assert len(a.taps) == W.n_layer and torch.equal(a.taps[-1]["h_out"], h)
+    a.segment(tokens(2, 8, seed=4))
+    for n, tap in enumerate(a.taps[:W.n_layer]):
+        assert tap["M"] == [8, 10] and torch.equal(tap["h"], a.taps[n - 1]["h_out"] if n else tap["h"])
+        for b, M in enumerate(tap["M"]):
+            k, v = (torch.cat([m, x[b]], 1)[None].double().numpy() for m, x in zip(tap["mem"][b], (tap["k"], tap["v"])))
+            rel = oracle.distance_table(tap["r"][:, -(M + 5):].double().numpy())
+            want, _ = oracle.relattn(tap["q"][b:b + 1], k, v, rel, a.u, a.v_bias, M, 5, a.scale)
+            # (the attention is exact here, its output rounded to fp32)
+            assert np.allclose(tap["a"][b].numpy(), want[0], rtol=2.0 ** -23, atol=1e-12)
+            lay = {x: w.numpy() for x, w in a.layers[n].items()}
+            out = oracle.layer_post(tap["a"][b:b + 1].transpose(1, 2).reshape(1, 5, -1), tap["h"][b:b + 1], lay)
+            assert np.abs(tap["h_out"][b].numpy() - out[0]).max() < 1e-5

@@ -137,7 +137,9 @@ class XLStack:
         # When set to a list, each eager segment appends, per layer, the layer's
         # input h, its memory, the attention operands (q, k, v, r, M), the
         # attention output a [B, H, L, dh] and the layer's output h' (all on the
-        # device): what a per-layer check of the stack needs.
+        # device): what a per-layer check of the stack needs.  A paged draft (or
+        # segment) does so with the nodes' q, k and v and their parents; M and mem are
+        # lists then, of each sequence's memory length and its keys and values [H, M, dh].
         self.taps = None
 
     def reset(self, B: int):
@@ -332,7 +334,13 @@ class XLStack:
             txl.relattn_tree_fwd(q, k, v, self.memory.kv, n, self._r(n, self.M + self.MAX_DRAFT),
                                  self.u, self.v_bias, parents, self.scale, n_nodes=n_nodes,
                                  out=a.transpose(1, 2))
-            h = self._rest_of_layer(lay, h, a.view(B, N, -1)).to(self.dtype)
+            h_next = self._rest_of_layer(lay, h, a.view(B, N, -1)).to(self.dtype)
+            if self.taps is not None:
+                self.taps.append({"h": h, "mem": [self.memory.rows(n, b) for b in range(B)], "q": q,
+                                  "k": k, "v": v, "r": self._r(n, self.M + self.MAX_DRAFT),
+                                  "M": list(self.memory.fill), "a": a.transpose(1, 2), "h_out": h_next,
+                                  "parents": parents})
+            h = h_next
         self._draft = qkv, *given
         return h
 

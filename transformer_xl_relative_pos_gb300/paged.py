@@ -139,6 +139,17 @@ class PagedMemory:
             self.fill[b] = min(total, self.M)
             self.begin[b] = (self.begin[b] + total - self.fill[b]) % R
 
+    def rows(self, layer: int, b: int):
+        """Copies of layer ``layer``'s keys and values of sequence b, each [H, fill, dh], oldest
+        row first."""
+        if not 0 <= layer < self.layers:
+            raise IndexError(f"no layer {layer} of {self.layers}")
+        x = (self.begin[self._sequence(b)] + np.arange(self.fill[b])) % self.kv.rows
+        page, row = (torch.from_numpy(i.astype(np.int64)).to(self.device)
+                     for i in (self._table[b, x // self.kv.page_rows], x % self.kv.page_rows))
+        k, v = (self.kv.pool[2 * layer + i][page, :, row].transpose(0, 1).contiguous() for i in (0, 1))
+        return k, v
+
     def free(self, b: int):
         """End sequence b: its memory is empty and its pages have one user less."""
         held = [int(p) for p in self._table[self._sequence(b)] if p >= 0]
