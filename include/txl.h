@@ -461,7 +461,8 @@ typedef struct {
  *   fill_out = min(fill + n', keep), begin_out = (begin + fill + n' - fill_out) mod R
  * They may be mem->begin and mem->fill themselves.  Then the call uses
  * mem->ticket, and calls on the same memory must not overlap in time; without
- * that, calls for different layers may.
+ * that, calls for different layers may.  They overlap neither the table, n_new nor rows
+ * (TXL_ERR_INVALID_ARG), except that n_new may be one of them where they are the state.
  * Errors: TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED (dh, page_rows, dtype, sizes
  * past the grid limits), TXL_ERR_MISALIGNED, TXL_ERR_SHAPE, TXL_ERR_CUDA.
  */
@@ -473,7 +474,8 @@ int txl_paged_append(const txl_paged_kv *mem, int layer0, int n_layers, const tx
 /*
  * txl_paged_advance - the state part of txl_paged_append alone, for a caller
  * that appended layer by layer: begin_out, fill_out (which may be mem->begin
- * and mem->fill) from n_new (NULL: max_rows for every sequence), as above.
+ * and mem->fill, and n_new one of them) from n_new (NULL: max_rows for every sequence), as
+ * above.
  * Errors: as txl_paged_append.
  */
 int txl_paged_advance(const txl_paged_kv *mem, const int *n_new, int max_rows, int keep,

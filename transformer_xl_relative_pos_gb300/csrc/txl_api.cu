@@ -899,6 +899,13 @@ txl::PagedView paged_view(const txl_paged_kv *m)
             m->slots * m->page_rows};
 }
 
+// Whether na ints at a and nb at b share any.
+bool overlap(const int *a, long long na, const int *b, long long nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < (uintptr_t)na * sizeof(int) : x - y < (uintptr_t)nb * sizeof(int);
+}
+
 // begin_out / fill_out against the state: separate, or the very same arrays
 // (*in_place); arrays that overlap in part, or each other, are refused.
 int check_state_out(const txl_paged_kv *m, const int *begin_out, const int *fill_out, bool *in_place)
@@ -907,10 +914,7 @@ int check_state_out(const txl_paged_kv *m, const int *begin_out, const int *fill
     if (!begin_out && !fill_out) return TXL_OK;
     if (!begin_out || !fill_out) return TXL_ERR_INVALID_ARG;
     if (!aligned(begin_out, 4) || !aligned(fill_out, 4)) return TXL_ERR_MISALIGNED;
-    const auto overlap = [m](const int *a, const int *b) {
-        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-        return (x < y ? y - x : x - y) < (uintptr_t)m->B * sizeof(int);
-    };
+    const auto overlap = [m](const int *a, const int *b) { return ::overlap(a, m->B, b, m->B); };
     if (overlap(begin_out, fill_out)) return TXL_ERR_INVALID_ARG;
     for (const int *o : {begin_out, (const int *)fill_out})
         for (const int *i : {(const int *)m->begin, (const int *)m->fill}) {
@@ -919,6 +923,20 @@ int check_state_out(const txl_paged_kv *m, const int *begin_out, const int *fill
             *in_place = true;
         }
     return TXL_OK;
+}
+
+// The table, n_new and rows are read while the outputs are written.  n_new may be an output itself
+// where each sequence's count is last read by the thread that then writes its state (one_reader).
+bool output_overlaps_input(const txl_paged_kv *m, const int *begin_out, const int *fill_out, const int *n_new,
+                           bool one_reader, const int *rows, long long n_rows)
+{
+    for (const int *o : {begin_out, fill_out}) {
+        if (!o) continue;
+        if (overlap(o, m->B, m->table, (long long)m->B * m->slots)) return true;
+        if (n_new && overlap(o, m->B, n_new, m->B) && !(one_reader && o == n_new)) return true;
+        if (rows && overlap(o, m->B, rows, n_rows)) return true;
+    }
+    return false;
 }
 
 } // namespace
@@ -939,6 +957,9 @@ extern "C" int txl_paged_append(const txl_paged_kv *mem, int layer0, int n_layer
     if (n_new && !aligned(n_new, 4)) return TXL_ERR_MISALIGNED;
     bool in_place = false;
     if ((rc = check_state_out(mem, begin_out, fill_out, &in_place)) != TXL_OK) return rc;
+    // (in place the last block reads n_new again, one thread a sequence)
+    if (output_overlaps_input(mem, begin_out, fill_out, n_new, in_place, rows, (long long)mem->B * rows_stride))
+        return TXL_ERR_INVALID_ARG;
     if (begin_out && keep > mem->slots * mem->page_rows) return TXL_ERR_SHAPE;
     if (in_place && !mem->ticket) return TXL_ERR_INVALID_ARG;
     if (in_place && !aligned(mem->ticket, 4)) return TXL_ERR_MISALIGNED;
@@ -988,6 +1009,7 @@ extern "C" int txl_paged_advance(const txl_paged_kv *mem, const int *n_new, int 
     if (n_new && !aligned(n_new, 4)) return TXL_ERR_MISALIGNED;
     bool in_place = false;
     if ((rc = check_state_out(mem, begin_out, fill_out, &in_place)) != TXL_OK) return rc;
+    if (output_overlaps_input(mem, begin_out, fill_out, n_new, true, nullptr, 0)) return TXL_ERR_INVALID_ARG;
     if (keep > mem->slots * mem->page_rows) return TXL_ERR_SHAPE;
     cudaError_t err;
     unsigned int *status = status_word(&err);
