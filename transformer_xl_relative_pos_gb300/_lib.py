@@ -561,10 +561,10 @@ def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
     """Put rows of k and v behind the memory's rows, in its pages.
 
     k, v [B, H, N, 64] for one layer, or [n, B, H, N, 64] for layers layer ..
-    layer + n - 1 (any strides, the last dimension dense).  Sequence b takes
+    layer + n - 1 (any positive strides of 16 bytes' multiples, the last dimension dense).  Sequence b takes
     n_new[b] rows (int32 on the device; all when omitted): rows 0, 1, ... of k
     and v, or rows[b, 0], rows[b, 1], ... with rows [B, width] int32 (the accepted
-    nodes of a drafted tree).  With ``keep``, the state is advanced to the
+    nodes of a drafted tree); n_new is taken into [0, N], or [0, width].  With ``keep``, the state is advanced to the
     newest ``keep`` rows: in ``mem``, or in the tensors ``state_out`` = (begin,
     fill) instead."""
     B, H, dh = mem._shape
@@ -597,13 +597,20 @@ def paged_append(mem: PagedKV, k, v, *, layer: int = 0, n_new=None, rows=None,
     return mem
 
 
-def paged_advance(mem: PagedKV, n, *, keep: int, state_out=None, stream=None):
+def paged_advance(mem: PagedKV, n, *, keep: int, max_rows: int | None = None, state_out=None,
+                  stream=None):
     """Advance the state of rows appended without ``keep`` (layer by layer):
     sequence b has n[b] new rows (int32 on the device), or n each (an int), and keeps
-    its newest ``keep`` rows.  Written to ``mem``, or to ``state_out``."""
+    its newest ``keep`` rows.  Counts on the device are taken into [0, max_rows], as
+    the append takes them into the rows it was given (by default the table's rows).
+    Written to ``mem``, or to ``state_out``."""
     n_at, most = None, n
     if not isinstance(n, int):
         n_at, most = _ptr(n, "n", torch.int32, (mem.B,), mem._index), mem.rows
+        if max_rows is not None:
+            most = max_rows
+    elif max_rows is not None and n > max_rows:
+        raise ValueError(f"n is more than max_rows = {max_rows}")
     b_out, f_out = _state_out(mem, state_out)
     _paged_call(mem, "txl_paged_advance", stream, mem._at, n_at, most, keep, b_out, f_out)
     return mem
@@ -627,13 +634,14 @@ def relattn_tree_fwd(q, k_new, v_new, mem: PagedKV, layer: int, r, u, v_bias, pa
     of a paged memory: node i attends to the memory's rows, to its ancestors and to
     itself, at the distances its depth gives.
 
-    q, k_new, v_new [B, H, N, 64], N <= 64 (any strides, the last dimension dense);
+    q, k_new, v_new [B, H, N, 64], N <= 64 (any positive strides of 16 bytes' multiples, the last
+    dimension dense);
     parents [B, N] (or [N], one tree for all) int32 on the device: an earlier node,
     or -1; r, u, v_bias as for :func:`relattn_fwd`, r [H, r_rows, 64] being
     attended as far as it goes; all of the memory's dtype (bf16 or fp32).
     n_nodes [B] int32: nodes of each sequence (all N when omitted); the rows of
     out and lse behind them are left as they were.  ``out``: a tensor to fill
-    ([B, H, N, 64], any strides); ``lse``: True, or a tensor [B, H, N] fp32.  Those made
+    ([B, H, N, 64], strides as q's, no row over another); ``lse``: True, or a tensor [B, H, N] fp32.  Those made
     here hold zeros behind n_nodes.
     Returns ``out`` or ``(out, lse)``."""
     B, H, dh = mem._shape
