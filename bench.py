@@ -842,7 +842,8 @@ TREE_SHAPES = [(1, 1, 1600), (8, 8, 3800), (4, 26, 517), (16, 64, 3800), (64, 16
 def run_tree(args):
     """Graph-replayed time and achieved HBM bandwidth of txl_relattn_tree_fwd (B sequences
     of N drafted nodes, 16 heads, M memory rows each, pages of 64) and of
-    txl_paged_append putting eight of the nodes behind the memory."""
+    txl_paged_append putting eight of the nodes behind the memory (few rows, which stay
+    in L2 at every shape)."""
     import torch
     import transformer_xl_relative_pos_gb300 as txl
     dev = torch.device("cuda", 0)
@@ -854,7 +855,7 @@ def run_tree(args):
         n_acc = min(N, 8)
         nbytes = 2 * (2 * B * H * (M + N) * 64 + H * (M + N) * 64 + 2 * B * H * N * 64) + 4 * B * H * N
         acc_bytes = 2 * 2 * 2 * B * H * n_acc * 64
-        n_sets = max(1, min(3, -(-3 * 126 * 2 ** 20 // nbytes)))  # > L2 of traffic between reuses
+        n_sets, per, resident = input_sets(nbytes)
         g = torch.Generator(device=dev).manual_seed(B * 7919 + N * 31 + M)
         mk = lambda *sh: (torch.randn(*sh, device=dev, generator=g) * 0.5).to(torch.bfloat16)
         slots = -(-(M + N) // P) + 1
@@ -882,15 +883,25 @@ def run_tree(args):
             k, v = (qkv[:, :, j].transpose(1, 2) for j in (1, 2))
             txl.paged_append(mem, k, v, rows=rows, keep=M, state_out=(state[0], state[1]))
 
-        us, acc_us = graph_us(tree, args.calls, 30), graph_us(accept, args.calls, 30)
+        us, acc_us = graph_us(tree, args.calls, per), graph_us(accept, args.calls, per)
         assert txl.device_status() == 0
         gbs = nbytes / (us * 1e-6) / 1e9
         print(json.dumps({"tree": {
             "B": B, "H": H, "N": N, "M": M, "dtype": "bf16", "us_per_call": us, "algorithmic_bytes": nbytes,
-            "achieved_gbs": gbs, "peak_gbs": pk["hbm_gbs"], "hbm_frac": gbs / pk["hbm_gbs"],
+            "achieved_gbs": gbs, "peak_gbs": pk["hbm_gbs"], "l2_resident": resident,
+            "hbm_frac": None if resident else gbs / pk["hbm_gbs"],
             "input_sets": n_sets, "append_us": acc_us, "append_rows": n_acc,
-            "append_bytes": acc_bytes}}), flush=True)
+            "append_bytes": acc_bytes, "append_l2_resident": True}}), flush=True)
         del sets
+
+
+def input_sets(nbytes, most=512):
+    """For calls that read nbytes each: how many sets of inputs a replayed graph goes through so
+    that three times L2 lies between two uses of one, how many calls it then holds (each set as
+    often, 30 at least), and whether so many sets are too many and the inputs stay in L2."""
+    want = max(1, -(-3 * 126 * 2 ** 20 // nbytes))
+    n = min(want, most)
+    return n, n * -(-30 // n), n < want
 
 
 def graph_us(call, reps, per):
