@@ -823,14 +823,15 @@ def run_decode(args):
     for B, L, M in shapes:
         K = M + L
         nbytes = 2 * (2 * B * H * K * 64 + H * K * 64 + 2 * B * H * L * 64)  # k, v, r, q, out (bf16)
-        n_sets = max(1, min(3, -(-3 * 126 * 2 ** 20 // nbytes)))  # > L2 of traffic between reuses
-        us = attn_call_us(B, H, L, M, reps=args.calls, per=30, n_sets=n_sets)
+        n_sets, per, resident = input_sets(nbytes)
+        us = attn_call_us(B, H, L, M, reps=args.calls, per=per, n_sets=n_sets)
         gbs = nbytes / (us * 1e-6) / 1e9
         kernel, splits = txl.relattn_plan(B, H, M, L, workspace_bytes=txl.workspace_size(B, H, L, 64, 64))
         print(json.dumps({"decode": {
             "B": B, "H": H, "L": L, "M": M, "dtype": "bf16", "us_per_call": us,
             "algorithmic_bytes": nbytes, "achieved_gbs": gbs, "peak_gbs": pk["hbm_gbs"],
-            "hbm_frac": gbs / pk["hbm_gbs"], "input_sets": n_sets,
+            "l2_resident": resident, "hbm_frac": None if resident else gbs / pk["hbm_gbs"],
+            "input_sets": n_sets,
             "path": {"decode": "decode kernel (CUDA cores)", "decode_mma": "decode kernel (warp MMAs)",
                      "tc": "tensor-core kernel"}[kernel],
             "splits": splits}}), flush=True)
