@@ -534,7 +534,8 @@ int txl_page_pool_release(txl_page_pool *p, const int *pages, int n, int *n_free
  * whose every score is -infinity (out NaN, lse -infinity); q.k and u.k, and q.r and
  * v_bias.r, are summed apart: infinities of unlike sign in them make the row NaN.
  *
- *   q, out        [B][H][N][dh]    (strided; out must not overlap the inputs)
+ *   q, out        [B][H][N][dh]    (strided; out must not overlap the inputs, nor one
+ *                 row of it another)
  *   k_new, v_new  [B][H][N][dh]    the nodes' keys and values
  *   mem, layer    the memory and the layer of it to read; nothing is written
  *   r             [H][r_rows][dh] dense, u, v_bias [H][dh]; as txl_relattn_fwd
@@ -544,9 +545,9 @@ int txl_page_pool_release(txl_page_pool *p, const int *pages, int n, int *n_free
  * Rows i >= n_b of out and lse are left as they were; those rows of q, k_new and
  * v_new, and what the pages hold outside the memory rows, have no influence.
  * All of mem->dtype.  TXL_BF16: products on the tensor cores, fp32 sums; the
- * probabilities enter as bf16 pairs (value and residual), or, for N > 16, rounded to
- * one bf16 value.  TXL_F32: fp32 arithmetic.  1 <= N <= 64, dh = 64.  mem's arrays,
- * parents and n_nodes must not change while the call runs.
+ * probabilities enter as bf16 pairs (value and residual), or, for N > 16 (the width of the
+ * call, whatever n_nodes says), rounded to one bf16 value.  TXL_F32: fp32 arithmetic.
+ * 1 <= N <= 64, dh = 64.  mem's arrays, parents and n_nodes must not change while the call runs.
  * n_splits: key ranges per (b, h), merged inside a thread-block cluster: 0 lets
  * the library choose, at most 8 (larger requests are refused).  No workspace.
  * Errors: TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED (N > 64, dh, page_rows, dtype,

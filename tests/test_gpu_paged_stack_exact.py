@@ -108,3 +108,18 @@ def test_a_checkpoint_of_a_stack_of_another_memory_is_refused():
         a.restore(other.checkpoint())
     assert a.memory.fill == [30, 30, 30]
     assert torch.equal(a.draft(m.MORE, torch.arange(-1, 19)), want)
+
+
+@pytest.mark.parametrize("M", [0, 1, 40])
+def test_nothing_accepted_changes_nothing(M):
+    a = XLStack(m.params(), m.W.H, M, dev(), torch.float32, paged=True)
+    a.segment(m.PROMPT)
+    before = [[x.clone() for b in range(m.W.B) for x in a.memory.rows(n, b)] for n in range(m.W.n_layer)]
+    want = a.draft(m.MORE, torch.arange(-1, 19)).clone()
+    a.accept([[], [], []])
+    assert a.memory.fill == [min(M, 30)] * m.W.B
+    assert torch.equal(a.draft(m.MORE, torch.arange(-1, 19)), want)
+    for n in range(m.W.n_layer):
+        after = [x for b in range(m.W.B) for x in a.memory.rows(n, b)]
+        assert all(x.shape[1] == min(M, 30) and torch.equal(x, y) for x, y in zip(before[n], after))
+    assert txl.device_status() == 0

@@ -49,8 +49,8 @@ __device__ __forceinline__ void advance(const AppendParams &p, int b)
 // memories, 34.7 us for 210 MB read and written (6.05 TB/s, 0.9 of a plain copy's rate; 32 rows a
 // block 37.6, 64 rows 41.7: the last wave of blocks is then a larger part).  Bound by the
 // chain of dependent loads state -> table -> source -> store for a few rows: the accepted
-// paths (1 to 8 rows) of 64 sequences of 16 heads in 12 layers 8.2 us for 28 MB, of one sequence
-// 2.5 us.  Keys and values by one block, which would walk that chain once: 9.3 and 38 us;
+// paths (1 to 8 rows) of 64 sequences of 16 heads in 12 layers 8 us for 28 MB in L2, 9.5 from HBM, of
+// one sequence 2.5 us.  Keys and values by one block, which would walk that chain once: 9.3 and 38 us;
 // heads outermost: 8.4 and 36 us; eight vectors in flight: 11.4 and 42 us.
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p)
 {
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kThreads) paged_advance_kernel(const AppendPar
 
 // Part x mod parts of page src[x / parts] to page dst[x / parts] of plane y; page_vec 16-byte
 // vectors a page.  Bound by DRAM: 48 pages of 64 rows and 16 heads in 12 layers 45.1 us for
-// 302 MB (6.70 TB/s, a plain copy's rate); a single page of 8 heads 1.7 us, which is the
-// launch and two dependent loads.  With eight vectors a thread 45.5 and 2.0 us.
+// 302 MB (6.70 TB/s, a plain copy's rate); a single page of 8 heads 1.8 us in
+// L2, 2.3 from HBM, which is the launch and two dependent loads.  With eight vectors a thread 45.5 and 2.0 us.
 constexpr int kCopyVec = 2;  // vectors per thread, all in flight at once
 
 __global__ void __launch_bounds__(kThreads) paged_copy_kernel(uint4 *__restrict__ pool, int n_pages,

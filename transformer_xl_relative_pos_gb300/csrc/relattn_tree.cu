@@ -28,11 +28,12 @@
 // nodes, where the MMAs count, as one, 2^-8 (half a step of bf16, as large as the output's own
 // rounding; 16 sequences of 64 nodes 180 us with residuals, 161 without, at that time).
 //
-// Measured (16 heads, 3800 rows, graph replays over inputs larger than L2): 19 sequences fill the two blocks of every SM, and take 46 us for 8 nodes
-// (0.99 of a plain copy's rate, bound by DRAM), 52 us for 16 (0.88), 82 us for 32 and 140 us for 64.
-// Those two are bound by latency: two warps that compute per SM quarter, whose matrix
-// instructions, shared-memory accesses and issue slots are each about half busy.  One sequence
-// of one node over 1600 rows takes 6.7 us, of which 2 are an empty kernel's and the rest a chain of
+// Measured (16 heads, 3800 rows, graph replays over inputs larger than L2): 19 sequences fill the two
+// blocks of every SM, and take 46 us for 8 nodes (0.99 of a plain copy's rate, bound by DRAM), 53 us for 16
+// (0.86), 82 us for 32 and 140 us for 64.  The last two are bound by latency: two warps that compute per
+// SM quarter, whose matrix instructions, shared-memory accesses and issue slots are each about half
+// busy.  One sequence of one node over 1600 rows takes 7.5 us (6.5 when its memory is in L2
+// already), of which 2 are an empty kernel's and the rest a chain of
 // dependent steps: state, page ids, copies, products, the merges of warps and blocks.
 // What was tried for the wide trees and was slower: tcgen05 tiles of 128 rows [q; u; v] (bound by
 // shared memory), 32 nodes a warp (registers), three blocks per SM (A operands re-read).
@@ -165,7 +166,8 @@ __device__ __forceinline__ void cp_async_hold(uint64_t *bar)
 // when NR = 2); its output columns are 8 nd + 2 t, + 1.  LO: the products with the
 // probabilities' residuals, kept apart until the end, as a residual (of either sign, or zero)
 // times an infinity must not meet the infinity of the product itself.  With NR = 1 (at most 8
-// nodes) they are the accumulators' rows g + 8, with NR = 2 accumulators of their own.
+// nodes) they are the accumulators' rows g + 8, with NR = 2 accumulators of their own (19 x 16 nodes of
+// 3800 rows 53.4 us, 52.2 with one set of accumulators; no registers spill).
 template <int NR, bool LO>
 struct State {
     static constexpr bool APART = LO && NR == 2;

@@ -12,8 +12,8 @@
 //   P.V      ROWS / 4 nodes x 8 dimensions, 8 steps of 4 keys
 // With 16 nodes that is eight loads for 64 multiply-adds.  Row strides of 4 mod 32 floats keep
 // the loads free of bank conflicts.  Measured: 13 nodes, two sequences of 8 heads and up to 777
-// rows 14.5 us (a lane per key, without register tiles, 29); 64 nodes, six sequences of 16
-// heads and 1500 rows 154 us (455 without), 23 TFLOP/s: a third of the CUDA cores' rate, the
+// rows 17.2 us, 14.7 when the memory is in L2 (a lane per key, without register tiles, 29); 64
+// nodes, six sequences of 16 heads and 1500 rows 158 us, 153 in L2 (455 without), 23 TFLOP/s: a third of the CUDA cores' rate, the
 // operands' loads and the staging between the products taking the rest.
 #include "tree_common.cuh"
 

@@ -1136,11 +1136,14 @@ extern "C" int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new,
     p.N = N;
     p.r_rows = r_rows;
     p.n_splits = splits;
-    // More blocks than one wave holds and room for long memories: the longest first, which
-    // costs every block about 1.3 us at its start.  16 heads: 64 sequences of 16 nodes and 950 to 3800
-    // rows 137 us in the grid's order, 127 us so; 24 of 64 nodes and 500 to 3800 rows 176 and 131; but 64
-    // sequences of 8 nodes and 250 to 900 rows 40.5 and 44.0, of one node and 500 to 1600 rows 54.5
-    // and 59.5, 100 sequences of 950 to 3800 rows 154 and 167.
+    // More blocks than one wave holds and room for long memories: the longest first.  Finding a
+    // block's sequence costs a call of several waves 3 to 5 us, which only waves of long and unlike
+    // blocks give back.  16 heads, the grid's order against this one: 64 sequences of 16 nodes and
+    // 950 to 3800 rows 139.7 and 129.8 us, 24 of 64 nodes and 500 to 3800 rows 174.9 and 130.9, 40 of 8
+    // nodes and 500 to 3800 rows 68.5 and 63.6; but 64 of 8 nodes and 250 to 900 rows 40.5 and 44.4,
+    // 1000 to 1900 rows 72.8 and 77.5, and 64 of 16 nodes and 3800 rows each 186.1 and 189.9.  The host
+    // does not know the lengths, only the tables' size.  At most 64 sequences: a warp ranks them by two
+    // lengths a lane; larger batches keep the grid's order.
     p.by_length = BH * splits > 2LL * sm_count() && mem->B > 1 && mem->B <= txl::kTreeMaxSorted &&
                   mem->slots * mem->page_rows >= 2048;
     p.scale_log2 = scale * 1.4426950408889634f;
