@@ -48,7 +48,7 @@ typedef enum {
     TXL_ERR_TIMEOUT = -6,     /* a kernel gave up waiting on an on-chip barrier */
     TXL_ERR_WORKSPACE = -7,   /* workspace missing or too small for the request */
     TXL_ERR_INDEX = -8        /* an index held on the device was out of range (page ids, parents,
-                                 source rows); debug builds: any device-side index check */
+                                 source rows, token ids); debug builds: any device-side index check */
 } txl_status;
 
 typedef enum {
@@ -559,6 +559,108 @@ int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new, const txl_row
                          const void *u, const void *v_bias, const int *parents,
                          long long parents_stride, const int *n_nodes, const txl_rows *out,
                          float *lse, int N, float scale, int n_splits, void *stream);
+
+/*
+ * The two ends of the model: the embedding of tokens (§3.3: h^0 is the word
+ * embedding sequence) and the log probabilities of tokens under
+ * softmax(h E^T) (§3: the language model's output), each with its gradient.  The
+ * table may be tied (one [V][d] array for both).
+ *
+ * Token ids and targets lie on the device as int32 or int64 (txl_index_type).  -1
+ * stands for none (padding); any other value outside [0, V) is taken as -1 and
+ * records TXL_ERR_INDEX for txl_device_status.
+ * Rows of d elements: d a multiple of 8, at most 65536; row strides in elements, multiples
+ * of 16 bytes, at least d (so h may be, say, the last position of every segment);
+ * pointers of rows 16-byte, of other arrays as their element, workspaces 256-byte
+ * aligned.  Outputs overlap neither inputs nor one another.  Workspaces are the
+ * caller's, their contents undefined before and after; calls that may run at the same
+ * time need one each.  n, N and V up to 2^28; n or N = 0 is allowed.
+ */
+typedef enum {
+    TXL_I32 = 4,
+    TXL_I64 = 8
+} txl_index_type;
+
+/*
+ * txl_embed_fwd - out_t = scale * emb[token_t] (t < n), a row of zeros without a token.
+ *   tokens [n]; emb [V] rows of d, emb_stride apart; out [n][d] dense.  emb and out of dtype
+ *   (TXL_F32 or TXL_BF16); the product is rounded once, and with scale = 1 rows are
+ *   copied bit for bit.
+ * Errors: TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED, TXL_ERR_MISALIGNED,
+ * TXL_ERR_SHAPE (a stride below d), TXL_ERR_CUDA.
+ */
+int txl_embed_fwd(const void *tokens, int index_type, const void *emb, long long emb_stride,
+                  void *out, int n, int V, int d, float scale, int dtype, void *stream);
+
+/*
+ * txl_embed_bwd - gradient of the table: demb_v = scale * sum_{t: token_t = v} dout_t.
+ *   tokens [n]; dout [n] rows of d, dout_stride apart, of dtype; demb [V][d] dense of
+ *   grad_dtype.  Every row of demb is written (zeros for tokens that do not occur); with
+ *   accumulate, which needs grad_dtype TXL_F32, the sums are added to demb instead and other
+ *   rows are left alone (the gradient of a tied table, say, after txl_logprob_bwd).
+ *   dout of positions without a token is not read.
+ * Sums are fp32, in an order that the tokens alone determine: results repeat bit for bit.
+ *   workspace: txl_embed_bwd_workspace_size(n, V, d) bytes (0 for sizes out of range).
+ * Errors: as txl_embed_fwd, and TXL_ERR_WORKSPACE.
+ */
+size_t txl_embed_bwd_workspace_size(int n, int V, int d);
+int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long long dout_stride,
+                  void *demb, int n, int V, int d, float scale, int dtype, int grad_dtype,
+                  int accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * txl_logprob_fwd - log probabilities of given tokens, the distributions' entropy and their
+ * largest alternatives.  With z_ij = scale * h_i.w_j over the vocabulary, for i < N:
+ *   lse_i     = log sum_j exp z_ij
+ *   logp_i    = z_i,targets[i] - lse_i            (0 without a target)
+ *   entropy_i = lse_i - sum_j p_ij z_ij,  p_ij = exp(z_ij - lse_i)
+ *   top_ids[i][0 .. top-1]  the `top` largest z_ij in descending order, equal ones by
+ *             ascending j;  top_logp the z - lse of them.  The top + 4 largest by their
+ *             fp32 sums are ordered by sums carried beyond fp32.  NaN logits are not
+ *             listed; places without a number hold id -1 and NaN.
+ * The logits are never written.
+ *   h [N] rows, w [V] rows of d, strides apart, both of dtype; targets [N] or NULL
+ *   logp, lse, entropy [N] fp32, top_logp [N][top] fp32, top_ids [N][top] int32: each may
+ *   be NULL (the last two only when top = 0)
+ *   top in [0, 16]
+ * TXL_BF16: products on the tensor cores, fp32 sums.  TXL_F32: operands as three bf16 terms
+ * each (their leading 24 bits; values beneath bf16's subnormals are lost), six products on
+ * the tensor cores, fp32 sums; there an infinite element of h or w makes a logit it enters NaN.
+ * A logit of -infinity has probability zero; a row with a logit of +infinity or NaN gives NaN.
+ *   workspace: txl_logprob_fwd_workspace_size(N, V, d, top, dtype) bytes (0 for arguments
+ *   out of range).
+ * Errors: as txl_embed_bwd; TXL_ERR_UNSUPPORTED for top > 16.
+ */
+size_t txl_logprob_fwd_workspace_size(int N, int V, int d, int top, int dtype);
+int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long w_stride,
+                    const void *targets, int index_type, float *logp, float *lse, float *entropy,
+                    float *top_logp, int *top_ids, int N, int V, int d, int top, float scale,
+                    int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * txl_logprob_bwd - gradients of h and w for dlogp = dL/dlogp and dentropy = dL/dentropy:
+ *   G_ij = dlogp_i (1[j = targets[i]] - p_ij) - dentropy_i p_ij (log p_ij + entropy_i)
+ *   dh_i = scale sum_j G_ij w_j          dw_j = scale sum_i G_ij h_i
+ *   h, w, targets, scale as in the forward call; lse and entropy its outputs (entropy may be
+ *   NULL without dentropy).  dlogp, dentropy [N] fp32: targets and dlogp are given together
+ *   or both NULL; one of dlogp and dentropy at least is given.
+ *   dh [N][d] dense of dtype, dw [V][d] dense of grad_dtype (TXL_F32 h and w: TXL_F32); one of
+ *   them may be NULL.  Written, not accumulated.
+ * A row without a target and with dentropy 0 (or NULL) has no part, whatever its h and
+ * statistics hold: its dh is zero.
+ * G enters its products with w, and with h for a bf16 dw, rounded to bf16; with h for an fp32 dw
+ * of bf16 operands as a bf16 pair (value and residual), and for fp32 operands as three terms.
+ * Sums are fp32 in a fixed order: results repeat bit for bit.
+ *   workspace: txl_logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype) bytes (G in chunks
+ *   of the vocabulary, up to about 1 GiB, and partial sums).
+ * Errors: as txl_logprob_fwd.
+ */
+size_t txl_logprob_bwd_workspace_size(int N, int V, int d, int dtype, int grad_dtype);
+int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long w_stride,
+                    const void *targets, int index_type, const float *lse, const float *entropy,
+                    const float *dlogp, const float *dentropy, void *dh, void *dw, int N, int V,
+                    int d, float scale, int dtype, int grad_dtype, void *workspace,
+                    size_t workspace_bytes, void *stream);
 
 /*
  * txl_device_status - synchronise `stream`, then read and clear the device

@@ -27,6 +27,11 @@ N-layer summary, Appendix B reversed table and shift):
   PagedMemory     both together: sequences that append, fork and end apart
   relattn_bwd     gradients of relattn_fwd for one segment (training within a
                   segment, the memory SG(m))
+  embed_fwd, embed_bwd  the scaled rows of the embedding table for given tokens, and
+                  the table's gradient
+  logprob_fwd     log probabilities of given tokens under softmax(h E^T), with the
+                  entropy and the most probable alternatives, without the logits
+  logprob_bwd     its gradients of h and of the table
 """
 
 from __future__ import annotations
@@ -35,6 +40,7 @@ from ._lib import (  # noqa: F401
     F32,
     BF16,
     KVWindow,
+    LogProbs,
     MemState,
     PagedKV,
     PagePool,
@@ -44,11 +50,18 @@ from ._lib import (  # noqa: F401
     debug_index_probe,
     debug_wait_timeout,
     device_status,
+    embed_bwd,
+    embed_bwd_workspace_size,
+    embed_fwd,
     kv_window_advance,
     kv_window_append,
     kv_window_view,
     lib,
     lib_path,
+    logprob_bwd,
+    logprob_bwd_workspace_size,
+    logprob_fwd,
+    logprob_fwd_workspace_size,
     mem_concat,
     mem_update,
     paged_advance,

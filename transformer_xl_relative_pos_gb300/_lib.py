@@ -7,6 +7,7 @@ import ctypes
 import os
 import struct
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -23,6 +24,7 @@ _c_int, _c_size, _c_p, _c_float, _c_u64 = (ctypes.c_int, ctypes.c_size_t, ctypes
 
 
 _c_ip = ctypes.POINTER(ctypes.c_int)
+_c_ll = ctypes.c_longlong
 
 
 class TxlError(RuntimeError):
@@ -140,6 +142,19 @@ def lib():
                 "txl_page_pool_alloc": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
                 "txl_page_pool_retain": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int]),
                 "txl_page_pool_release": (_c_int, [ctypes.POINTER(_PagePool), _c_ip, _c_int, _c_ip]),
+                "txl_embed_fwd": (_c_int, [_c_p, _c_int, _c_p, _c_ll, _c_p, _c_int, _c_int, _c_int,
+                                           _c_float, _c_int, _c_p]),
+                "txl_embed_bwd_workspace_size": (_c_size, [_c_int, _c_int, _c_int]),
+                "txl_embed_bwd": (_c_int, [_c_p, _c_int, _c_p, _c_ll, _c_p, _c_int, _c_int, _c_int,
+                                           _c_float, _c_int, _c_int, _c_int, _c_p, _c_size, _c_p]),
+                "txl_logprob_fwd_workspace_size": (_c_size, [_c_int] * 5),
+                "txl_logprob_fwd": (_c_int, [_c_p, _c_ll, _c_p, _c_ll, _c_p, _c_int, _c_p, _c_p, _c_p,
+                                             _c_p, _c_p, _c_int, _c_int, _c_int, _c_int, _c_float,
+                                             _c_int, _c_p, _c_size, _c_p]),
+                "txl_logprob_bwd_workspace_size": (_c_size, [_c_int] * 5),
+                "txl_logprob_bwd": (_c_int, [_c_p, _c_ll, _c_p, _c_ll, _c_p, _c_int, _c_p, _c_p, _c_p,
+                                             _c_p, _c_p, _c_p, _c_int, _c_int, _c_int, _c_float,
+                                             _c_int, _c_int, _c_p, _c_size, _c_p]),
                 "txl_device_status": (_c_int, [_c_p]),
                 "txl_set_wait_limit_ns": (_c_u64, [_c_u64]),
                 "txl_debug_wait_timeout": (_c_int, [_c_u64, _c_p]),
@@ -716,6 +731,240 @@ class PagePool:
         _check(lib().txl_page_pool_release(ctypes.byref(self._c), ids, len(pages),
                                            ctypes.byref(freed)), "txl_page_pool_release")
         return freed.value
+
+
+# ---------------------------------------------------------------------------
+# the model's two ends: token embedding and log probabilities
+# ---------------------------------------------------------------------------
+
+_INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _on_device(index: int, name: str, stream, *args):
+    """The library's function on device ``index`` and (unless given) its current stream."""
+    if stream is None:
+        stream = (_raw_stream(index) if _raw_stream is not None
+                  else torch.cuda.current_stream(index).cuda_stream)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
+    if _current_device() == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        _check(rc, name)
+
+
+def _made_on(index: int, stream):
+    """Where a call makes its outputs and workspace: on its own stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    return torch.cuda.stream(stream)
+
+
+def _table(t, name: str) -> tuple[int, int, int, int]:
+    """Device, rows, width and row stride of a [V, d] table or a matrix of rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, d], got {list(t.shape)}")
+    _code(t.dtype)
+    rows, d = t.shape
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension (strides {t.stride()})")
+    return t.get_device(), rows, d, (t.stride(0) if rows > 1 else d)
+
+
+def _rows_of(t, name: str, d: int, dtype, index: int) -> tuple[int, int]:
+    """Rows and row stride of a [..., d] operand whose rows are equally spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on another device than the table")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 1 or shape[-1] != d:
+        raise ValueError(f"{name} must be [..., {d}], got {list(shape)}")
+    n = t.numel() // d
+    if n == 0 or (n == 1 and (d == 1 or strides[-1] == 1)):
+        return n, d
+    if d > 1 and strides[-1] != 1:
+        raise ValueError(f"{name} must be dense in its last dimension (strides {strides})")
+    stride, run = None, 1
+    for size, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * run:
+            raise ValueError(f"{name} must have equally spaced rows (strides {strides})")
+        run *= size
+    return n, stride
+
+
+def _ids(t, name: str, n: int, index: int) -> tuple[int, int]:
+    """Address and index type of n contiguous token ids."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on another device than the table")
+    if t.dtype not in _INDEX_BYTES:
+        raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} ids, contiguous, got {list(t.shape)} with strides "
+                         f"{t.stride()}")
+    return t.data_ptr(), _INDEX_BYTES[t.dtype]
+
+
+def _room(workspace, size: int, index: int, stream):
+    """A workspace of at least ``size`` bytes: the caller's, or one made here."""
+    if workspace is None:
+        with _made_on(index, stream):
+            workspace = torch.empty(max(size, 256), dtype=torch.uint8,
+                                    device=torch.device("cuda", index))
+    elif workspace.get_device() != index:
+        raise ValueError("workspace is on another device than the table")
+    return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def embed_fwd(tokens, emb, *, scale: float = 1.0, out=None, stream=None):
+    """Rows of the table emb [V, d] (bf16 or fp32, rows at any stride of 16 bytes' multiples)
+    times ``scale`` for the ids ``tokens`` (int32 or int64, any shape): [*tokens.shape, d].  -1:
+    a row of zeros."""
+    index, V, d, stride = _table(emb, "emb")
+    n = tokens.numel()
+    at, kind = _ids(tokens, "tokens", n, index)
+    shape = (*tokens.shape, d)
+    if out is None:
+        with _made_on(index, stream):
+            out = torch.empty(shape, dtype=emb.dtype, device=emb.device)
+    _on_device(index, "txl_embed_fwd", stream, at, kind, emb.data_ptr(), stride,
+               _ptr(out, "out", emb.dtype, shape, index), n, V, d, scale, _code(emb.dtype))
+    return out
+
+
+def embed_bwd_workspace_size(n: int, V: int, d: int) -> int:
+    """Bytes of device workspace embed_bwd needs for n tokens."""
+    return int(lib().txl_embed_bwd_workspace_size(int(n), int(V), int(d)))
+
+
+def embed_bwd(dout, tokens, V: int, *, scale: float = 1.0, dtype=torch.float32, out=None,
+              accumulate: bool = False, workspace=None, stream=None):
+    """Gradient [V, d] of the table of :func:`embed_fwd` for dout [*tokens.shape, d] (equally
+    spaced rows), in ``dtype`` (or that of ``out``); with ``accumulate`` added to ``out`` (fp32).
+    ``workspace``: a device buffer of at least :func:`embed_bwd_workspace_size` bytes (allocated
+    when omitted)."""
+    n, d, index = tokens.numel(), dout.shape[-1], dout.get_device()
+    rows, stride = _rows_of(dout, "dout", d, dout.dtype, index)
+    if rows != n:
+        raise ValueError(f"dout must have a row for each of the {n} tokens, got {list(dout.shape)}")
+    at, kind = _ids(tokens, "tokens", n, index)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        with _made_on(index, stream):
+            out = torch.empty(V, d, dtype=dtype, device=dout.device)
+    workspace, ws, ws_bytes = _room(workspace, embed_bwd_workspace_size(n, V, d), index, stream)
+    _on_device(index, "txl_embed_bwd", stream, at, kind, dout.data_ptr(), stride,
+               _ptr(out, "out", out.dtype, (V, d), index), n, V, d, scale, _code(dout.dtype),
+               _code(out.dtype), int(accumulate), ws, ws_bytes)
+    return out
+
+
+class LogProbs(NamedTuple):
+    """What logprob_fwd gives for states [..., d]: logp, lse and entropy [...] (fp32), and the
+    largest alternatives top_logp (fp32) and top_ids (int32) [..., top], or None."""
+
+    logp: torch.Tensor | None
+    lse: torch.Tensor | None
+    entropy: torch.Tensor | None
+    top_logp: torch.Tensor | None = None
+    top_ids: torch.Tensor | None = None
+
+
+def logprob_fwd_workspace_size(N: int, V: int, d: int, dtype=torch.bfloat16, *, top: int = 0) -> int:
+    """Bytes of device workspace logprob_fwd needs for N states."""
+    return int(lib().txl_logprob_fwd_workspace_size(int(N), int(V), int(d), int(top), _code(dtype)))
+
+
+def logprob_fwd(h, w, targets=None, *, scale: float = 1.0, top: int = 0, out: LogProbs | None = None,
+                workspace=None, stream=None) -> LogProbs:
+    """Under softmax(scale * h w^T), for each of the states h [..., d] (equally spaced rows) over
+    the table w [V, d] (both bf16 or both fp32): the log probability of its target (int32 or
+    int64, -1: none, gives 0), the log-sum-exp, the entropy, and the ``top`` (up to 16) most
+    probable tokens.  The logits are never written.  ``out``: a LogProbs of tensors to fill (None
+    entries are left out); ``workspace``: a device buffer of at least
+    :func:`logprob_fwd_workspace_size` bytes (allocated when omitted)."""
+    index, V, d, w_stride = _table(w, "w")
+    N, h_stride = _rows_of(h, "h", d, w.dtype, index)
+    shape = tuple(h.shape[:-1])
+    at, kind = (None, 4) if targets is None else _ids(targets, "targets", N, index)
+    if out is None:
+        with _made_on(index, stream):
+            f = lambda *s: torch.empty(*shape, *s, dtype=torch.float32, device=h.device)
+            out = LogProbs(None if targets is None else f(), f(), f(), f(top) if top else None,
+                           torch.empty(*shape, top, dtype=torch.int32, device=h.device) if top else None)
+    f32 = torch.float32
+    at_of = lambda t, name, dt, s: None if t is None else _ptr(t, name, dt, s, index)
+    ptrs = [at_of(out.logp, "logp", f32, shape), at_of(out.lse, "lse", f32, shape),
+            at_of(out.entropy, "entropy", f32, shape), at_of(out.top_logp, "top_logp", f32, (*shape, top)),
+            at_of(out.top_ids, "top_ids", torch.int32, (*shape, top))]
+    code = _code(w.dtype)
+    size = 0 if workspace is not None else logprob_fwd_workspace_size(N, V, d, w.dtype, top=top)
+    workspace, ws, ws_bytes = _room(workspace, size, index, stream)
+    _on_device(index, "txl_logprob_fwd", stream, h.data_ptr(), h_stride, w.data_ptr(), w_stride, at,
+               kind, *ptrs, N, V, d, top, scale, code, ws, ws_bytes)
+    return out
+
+
+def logprob_bwd_workspace_size(N: int, V: int, d: int, dtype=torch.bfloat16, *,
+                               grad_dtype=None) -> int:
+    """Bytes of device workspace logprob_bwd needs for N states."""
+    grad = dtype if grad_dtype is None else grad_dtype
+    return int(lib().txl_logprob_bwd_workspace_size(int(N), int(V), int(d), _code(dtype), _code(grad)))
+
+
+def logprob_bwd(h, w, targets, lse, dlogp, *, entropy=None, dentropy=None, scale: float = 1.0,
+                grads=None, grad_dtype=None, workspace=None, stream=None):
+    """Gradients (dh, dw) of h and w of :func:`logprob_fwd` for the gradients ``dlogp`` of its log
+    probabilities (None with targets None) and ``dentropy`` of its entropies (may be None), from its
+    ``lse`` and ``entropy``.  dh has h's type and shape, dw ``grad_dtype`` (w's type when omitted;
+    fp32 for bf16 states too).  ``grads``: the tensors to fill instead, None for one that is not
+    wanted; ``workspace``: a device buffer of at least :func:`logprob_bwd_workspace_size` bytes
+    (allocated when omitted)."""
+    index, V, d, w_stride = _table(w, "w")
+    N, h_stride = _rows_of(h, "h", d, w.dtype, index)
+    shape = tuple(h.shape[:-1])
+    at, kind = (None, 4) if targets is None else _ids(targets, "targets", N, index)
+    if grads is None:
+        with _made_on(index, stream):
+            grads = (torch.empty(h.shape, dtype=h.dtype, device=h.device),
+                     torch.empty(V, d, dtype=w.dtype if grad_dtype is None else grad_dtype,
+                                 device=w.device))
+    dh, dw = grads
+    grad = w.dtype if dw is None else dw.dtype
+    f32 = torch.float32
+    at_of = lambda t, name, dt, s: None if t is None else _ptr(t, name, dt, s, index)
+    size = (0 if workspace is not None
+            else logprob_bwd_workspace_size(N, V, d, w.dtype, grad_dtype=grad))
+    workspace, ws, ws_bytes = _room(workspace, size, index, stream)
+    _on_device(index, "txl_logprob_bwd", stream, h.data_ptr(), h_stride, w.data_ptr(), w_stride, at,
+               kind, _ptr(lse, "lse", f32, shape, index), at_of(entropy, "entropy", f32, shape),
+               at_of(dlogp, "dlogp", f32, shape), at_of(dentropy, "dentropy", f32, shape),
+               at_of(dh, "dh", w.dtype, h.shape), at_of(dw, "dw", grad, (V, d)), N, V, d, scale,
+               _code(w.dtype), _code(grad), ws, ws_bytes)
+    return dh, dw
 
 
 def device_status(stream=None) -> int:

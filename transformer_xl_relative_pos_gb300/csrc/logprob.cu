@@ -1,0 +1,780 @@
+// Log probabilities of tokens and their gradient.
+//
+//   z_ij   = scale * h_i . w_j                        (w: the tied table, V rows)
+//   lse_i  = log sum_j exp z_ij,  logp_i = z_i,t(i) - lse_i
+//   H_i    = lse_i - sum_j p_ij z_ij,  the largest few z_ij
+//   G_ij   = g_i (1[j = t(i)] - p_ij) - e_i p_ij (log p_ij + H_i)
+//   dh_i   = scale sum_j G_ij w_j,  dW_j = scale sum_i G_ij h_i
+//
+// One GEMM kernel on tcgen05 (bf16 operands, fp32 accumulators in TMEM), in
+// four modes that differ in their operands' layout and in what becomes of a tile:
+//   kStats   h W^T; a block keeps 128 rows and walks over a range of the
+//            vocabulary, each row's running maximum, sum, weighted sum, target
+//            logit and largest logits in the registers of the thread that owns it:
+//            the N x V logits are never written.  launch_logprob_merge joins the
+//            ranges.
+//   kGrad    h W^T again; a tile becomes G, as bf16 terms in the workspace
+//   kDh, kDw G W and G^T h
+// fp32 operands are three bf16 terms each (their leading 24 bits); a product of two
+// such operands is the six products of terms whose weight is above 2^-24.
+#include "vocab.h"
+#include "ptx.cuh"
+
+namespace txl {
+namespace {
+
+using namespace ptx;
+
+constexpr int BM = 128, BK = 64, NS = 4, MAX_BN = 256;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int B_BYTES = MAX_BN * BK * 2;
+constexpr int STAGE = A_BYTES + B_BYTES;
+constexpr int OFF_BAR = NS * STAGE;
+constexpr int N_BAR = 2 * NS + 4;
+constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
+constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
+constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
+
+static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
+
+enum Mode { kStats, kGrad, kDh, kDw };
+
+// Tile `t` of the `n_tiles` that item `item` consists of.
+struct Tile {
+    int m, n, kb_lo, kb_hi;
+};
+
+template <Mode MODE>
+__device__ __forceinline__ int item_tiles(const GemmParams &p, int item)
+{
+    if (MODE != kStats) return 1;
+    const int s = item / p.mb;
+    return (int)((long long)(s + 1) * p.nb / p.splits) - (int)((long long)s * p.nb / p.splits);
+}
+
+template <Mode MODE>
+__device__ __forceinline__ Tile item_tile(const GemmParams &p, int item, int t)
+{
+    if (MODE == kStats) {
+        const int s = item / p.mb;
+        return {item - s * p.mb, (int)((long long)s * p.nb / p.splits) + t, 0, p.kb};
+    }
+    if (MODE == kGrad) {  // (neighbouring blocks share a tile of w)
+        const int n = item / p.mb;
+        return {item - n * p.mb, n, 0, p.kb};
+    }
+    const int per = p.mb * p.nb, s = item / per, mn = item - s * per;
+    return {mn / p.nb, mn % p.nb, (int)((long long)s * p.kb / p.splits),
+            (int)((long long)(s + 1) * p.kb / p.splits)};
+}
+
+// What a thread keeps of its row while it walks over the vocabulary (log2 units).
+template <int LIST>
+struct RowStats {
+    float m, s, es, zt;
+    float val[LIST > 0 ? LIST : 1];
+    int id[LIST > 0 ? LIST : 1];
+
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY;
+        s = es = zt = 0.f;
+#pragma unroll
+        for (int j = 0; j < LIST; ++j) {
+            val[j] = __int_as_float(0x7fffffff);  // NaN: an empty place, which any number takes
+            id[j] = -1;
+        }
+    }
+    // Places in descending order; an equal value that comes later goes behind.
+    __device__ __forceinline__ void insert(float v, int j0)
+    {
+#pragma unroll
+        for (int j = LIST - 1; j > 0; --j) {
+            const bool above = !(v <= val[j - 1]), here = !(v <= val[j]);
+            val[j] = above ? val[j - 1] : here ? v : val[j];
+            id[j] = above ? id[j - 1] : here ? j0 : id[j];
+        }
+        if (LIST > 0 && !(v <= val[0])) {
+            val[0] = v;
+            id[0] = j0;
+        }
+    }
+};
+
+__device__ __forceinline__ float pick(const float (&t)[32], int i)
+{
+    float a[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) a[k] = (i & 16) ? t[k + 16] : t[k];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = (i & 8) ? a[k + 8] : a[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = (i & 4) ? a[k + 4] : a[k];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) a[k] = (i & 2) ? a[k + 2] : a[k];
+    return (i & 1) ? a[1] : a[0];
+}
+
+// 32 logits of a row, columns col0 .. col0 + cnt - 1 of the vocabulary (t: log2 units, -inf
+// behind cnt).
+template <int LIST>
+__device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], int col0, int cnt,
+                                     int target)
+{
+    float mx = t[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) mx = fmaxf(mx, t[i]);
+    const float m_new = fmaxf(r.m, mx);
+    const float mu = m_new == -INFINITY ? 0.f : m_new;
+    if (m_new > r.m) {
+        const float diff = r.m - mu;  // (-inf before the first finite logit: sums are zero)
+        const float f = ex2(diff);
+        r.es = (r.s > 0.f || r.s != r.s) ? (r.es + r.s * diff) * f : 0.f;
+        r.s *= f;
+        r.m = m_new;
+    }
+    float cs[2] = {0.f, 0.f}, ce[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float d = t[i] - mu, e = ex2(d);
+        cs[i & 1] += e;
+        // (a logit of -inf has weight zero)
+        ce[i & 1] = fmaf(e, fmaxf(d, -1e30f), ce[i & 1]);
+    }
+    r.s += cs[0] + cs[1];
+    r.es += ce[0] + ce[1];
+    const int at = target - col0;
+    if (__any_sync(0xffffffffu, (unsigned)at < (unsigned)cnt)) {
+        const float v = pick(t, at & 31);
+        if ((unsigned)at < (unsigned)cnt) r.zt = v;
+    }
+    if (LIST > 0) {
+        const float thr = r.val[LIST - 1];
+        if (__any_sync(0xffffffffu, !(mx <= thr))) {
+            unsigned cand = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                cand |= (!(t[i] <= thr) && t[i] == t[i]) ? 1u << i : 0u;
+            if (cnt < 32) cand &= (1u << cnt) - 1;
+            while (__any_sync(0xffffffffu, cand != 0)) {
+                const int i = cand ? __ffs(cand) - 1 : 0;
+                const float v = pick(t, i);
+                if (cand && !(v <= r.val[LIST - 1])) r.insert(v, col0 + i);
+                cand &= cand - 1;
+            }
+        }
+    }
+}
+
+template <Mode MODE, int LIST>
+__global__ void __launch_bounds__(256, 1)
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                      const GemmParams p)
+{
+    constexpr bool A_MN = MODE == kDw, B_MN = MODE == kDh || MODE == kDw;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+    uint64_t *empty = full + NS;
+    uint64_t *acc_full = empty + NS;
+    uint64_t *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + s, 1);
+            mbar_init(acc_empty + s, 128);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, TM_COLS);
+        tmem_relinquish();
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint64_t wait_ns = p.wait_ns;
+
+    if (warp == 0) {
+        // ===================== TMA producer =====================================
+        if (lane == 0) {
+            prefetch_tensormap(&tm_a);
+            prefetch_tensormap(&tm_b);
+            bool ok = true;
+            int it = 0;  // stages filled
+            for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
+                const int nt = item_tiles<MODE>(p, item);
+                for (int t = 0; t < nt && ok; ++t) {
+                    const Tile w = item_tile<MODE>(p, item, t);
+                    const int m0 = w.m * BM, n0 = w.n * p.bn;
+                    for (int pr = 0; pr < p.n_pairs && ok; ++pr) {
+                        const int pa = (p.pair_a >> (4 * pr)) & 15, pb = (p.pair_b >> (4 * pr)) & 15;
+                        for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
+                            const int s = it % NS;
+                            if (!(ok = mbar_wait(empty + s, ((it / NS) & 1) ^ 1, abort_flag, wait_ns))) break;
+                            uint8_t *st = smem + s * STAGE;
+                            mbar_arrive_expect_tx(full + s, A_BYTES + p.bn * BK * 2);
+                            if (A_MN) {
+                                for (int x = 0; x < BM / 64; ++x)
+                                    tma_load_3d(st + x * SLAB, &tm_a, full + s, m0 + x * 64, kb * BK, pa);
+                            } else {
+                                tma_load_3d(st, &tm_a, full + s, kb * BK, m0, pa);
+                            }
+                            if (B_MN) {
+                                for (int x = 0; x < p.bn / 64; ++x)
+                                    tma_load_3d(st + A_BYTES + x * SLAB, &tm_b, full + s, n0 + x * 64,
+                                                p.b_row0 + kb * BK, pb);
+                            } else {
+                                tma_load_3d(st + A_BYTES, &tm_b, full + s, kb * BK, p.b_row0 + n0, pb);
+                            }
+                            ++it;
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+                *abort_flag = 1;
+                const int zero = 0;
+                for (int i = max(0, it - NS); i < it; ++i)
+                    mbar_wait(full + i % NS, (i / NS) & 1, &zero, wait_ns);
+            }
+        }
+    } else if (warp == 1) {
+        // ===================== MMA issuer =======================================
+        const uint32_t ID = idesc_bf16_f32(BM, p.bn, B_MN) | (A_MN ? 1u << 15 : 0u);
+        const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + A_BYTES);
+        const uint64_t dA = A_MN ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
+        const uint64_t dB = B_MN ? sdesc_sw128_mn(b0, SLAB) : sdesc_sw128(b0);
+        constexpr int STEP_A = A_MN ? 16 * 128 / 16 : 2, STEP_B = B_MN ? 16 * 128 / 16 : 2;
+        auto elect = []() -> bool {
+            uint32_t el;
+            asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+                         : "=r"(el));
+            return el != 0;
+        };
+        bool ok = true;
+        int it = 0, tile = 0;
+        for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
+            const int nt = item_tiles<MODE>(p, item);
+            for (int t = 0; t < nt && ok; ++t) {
+                const Tile w = item_tile<MODE>(p, item, t);
+                const int steps = p.n_pairs * (w.kb_hi - w.kb_lo);
+                const int buf = tile & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile >> 1) & 1) ^ 1, abort_flag, wait_ns));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t acc = tmem + buf * MAX_BN;
+                for (int k = 0; k < steps; ++k, ++it) {
+                    const int s = it % NS;
+                    ok = __all_sync(0xffffffffu, mbar_wait(full + s, (it / NS) & 1, abort_flag, wait_ns));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t off = (uint64_t)((s * STAGE) >> 4);
+                    if (elect()) {
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            mma_bf16_ss(acc, dA + off + kk * STEP_A, dB + off + kk * STEP_B, ID,
+                                        (k > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(empty + s);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elect()) mma_commit(acc_full + buf);
+                __syncwarp();
+                ++tile;
+            }
+        }
+        if (!ok) {
+            // let what was issued drain before the memory is freed
+            if (lane == 0) {
+                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (elect()) mma_commit(acc_full + (tile & 1));
+            __syncwarp();
+            const int zero = 0;
+            mbar_wait(acc_full + (tile & 1), (tile >> 1) & 1, &zero, wait_ns);
+        }
+    } else if (warp >= 4) {
+        // ===================== epilogue: thread = row ===========================
+        const int wq = warp - 4;
+        const int row = wq * 32 + lane;
+        const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
+        constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+        const float c2 = p.scale * kLog2e;
+        bool ok = true;
+        int tile = 0;
+        for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
+            const int nt = item_tiles<MODE>(p, item);
+            RowStats<LIST> r;
+            int target = -1;
+            float g1 = 0.f, ge = 0.f, lse2 = 0.f, ent = 0.f;
+            bool live = false;
+            if (MODE == kStats || MODE == kGrad) {
+                const int m = item_tile<MODE>(p, item, 0).m * BM + row;
+                if (m < p.M) {
+                    if (p.targets) target = token_at(p.targets, p.index_bytes, m, p.V, p.status);
+                    if (MODE == kGrad) {
+                        if (target >= 0 && p.dlogp) g1 = p.dlogp[m] * p.scale;
+                        if (p.dentropy) {
+                            ge = p.dentropy[m] * p.scale;
+                            ent = p.entropy[m];
+                        }
+                        lse2 = p.lse[m] * kLog2e;
+                        live = target >= 0 || (p.dentropy && p.dentropy[m] != 0.f);
+                    }
+                }
+                if (MODE == kStats) r.clear();
+            }
+            for (int t = 0; t < nt && ok; ++t, ++tile) {
+                const Tile w = item_tile<MODE>(p, item, t);
+                const int buf = tile & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (tile >> 1) & 1, abort_flag, wait_ns)) &&
+                     !*abort_flag;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const int m = w.m * BM + row, n0 = w.n * p.bn;
+                // (a warp whose rows lie behind the last has nothing to do)
+                const int cols = m - lane < p.M ? min(p.bn, p.N - n0) : 0;
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t raw[32];
+                    tmem_ld32(tq + buf * MAX_BN + c, raw);
+                    tmem_ld_wait(raw);
+                    const int cnt = min(32, cols - c);
+                    if (w.kb_lo == w.kb_hi)  // (an empty part: nothing was accumulated)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) raw[i] = 0;
+                    if (MODE == kStats) {
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = i < cnt ? __uint_as_float(raw[i]) * c2 : -INFINITY;
+                        take<LIST>(r, v, n0 + c, cnt, target);
+                    } else if (MODE == kGrad) {
+                        float v[32];
+                        const int at = target - (p.b_row0 + n0 + c);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float lp = fmaf(__uint_as_float(raw[i]), c2, -lse2);
+                            const float pr = ex2(lp);
+                            float f = g1;
+                            if (p.dentropy) f = fmaf(ge, fmaf(fmaxf(lp, -1e30f), kLn2, ent), f);
+                            v[i] = -pr * f + (i == at ? g1 : 0.f);
+                            if (!live) v[i] = 0.f;
+                        }
+                        if (m < p.M) {
+                            for (int g = 0; g < p.g_pieces; ++g) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(p.g + g * p.g_plane + (long long)m * p.g_ld + n0 + c);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                                                        pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                                                        pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                                if (g + 1 < p.g_pieces)
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) {
+                                        const float hi = __bfloat162float(__float2bfloat16_rn(v[i]));
+                                        v[i] = isfinite(v[i]) ? v[i] - hi : 0.f;
+                                    }
+                            }
+                        }
+                    } else if (m < p.M) {
+                        const int s = p.part ? item / (p.mb * p.nb) : 0;
+                        const long long at = ((long long)s * p.M + m) * p.N + n0 + c;
+                        // (cnt is a multiple of 8: rows of the operands are)
+                        if (p.part || !p.out_bf16) {
+                            float *dst = (p.part ? p.part : static_cast<float *>(p.out)) + at;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (4 * q < cnt)
+                                    reinterpret_cast<uint4 *>(dst)[q] =
+                                        make_uint4(raw[4 * q], raw[4 * q + 1], raw[4 * q + 2], raw[4 * q + 3]);
+                        } else {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
+                            const float *v = reinterpret_cast<const float *>(raw);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (8 * q < cnt)
+                                    dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                                                        pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                                                        pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(acc_empty + buf);
+            }
+            if (MODE == kStats && ok) {
+                const int s = item / p.mb, m = (item - s * p.mb) * BM + row;
+                if (m < p.M) {
+                    p.stats[(long long)s * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
+#pragma unroll
+                    for (int j = 0; j < LIST; ++j) {
+                        const long long at = ((long long)s * LIST + j) * p.M + m;
+                        p.list_val[at] = r.val[j];
+                        p.list_id[at] = r.id[j];
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.status, TXL_STATUS_TIMEOUT);
+            *abort_flag = 1;
+        }
+        tc_fence_before_sync();
+    }
+
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, TM_COLS);
+    }
+}
+
+template <Mode MODE, int LIST>
+cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p, cudaStream_t s)
+{
+    static bool attr_set[64] = {};  // the attribute is set once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(vocab_gemm_kernel<MODE, LIST>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const unsigned grid = (unsigned)min(p.n_items, device_sm_count());
+    vocab_gemm_kernel<MODE, LIST><<<grid, 256, SMEM_BYTES, s>>>(a, b, p);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// joining the vocabulary ranges of a row
+// ---------------------------------------------------------------------------
+
+// a + b exactly as hi + lo (Knuth's two-sum).
+__device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
+{
+    const float s = __fadd_rn(hi, x), bb = __fadd_rn(s, -hi);
+    lo += (hi - (s - bb)) + (x - bb);
+    hi = s;
+}
+
+// h_i . w_j to about 2^-45 of its terms' size, over a warp: products split exactly (a bf16
+// product is an fp32 value; an fp32 one is a product and its rounding error by fma), sums
+// carried with their errors.
+template <bool BF16>
+__device__ double dot_exact(const void *h, const void *w, int d, int lane)
+{
+    float hi = 0.f, lo = 0.f;
+    if (BF16) {
+        const uint4 *a = static_cast<const uint4 *>(h), *b = static_cast<const uint4 *>(w);
+        for (int c = lane; c < d / 8; c += 32) {
+            const uint4 x = __ldg(a + c), y = __ldg(b + c);
+            const uint32_t *xp = &x.x, *yp = &y.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                two_sum(hi, lo, __fmul_rn(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16)));
+                two_sum(hi, lo, __fmul_rn(__uint_as_float(xp[i] & 0xffff0000u),
+                                          __uint_as_float(yp[i] & 0xffff0000u)));
+            }
+        }
+    } else {
+        const float4 *a = static_cast<const float4 *>(h), *b = static_cast<const float4 *>(w);
+        for (int c = lane; c < d / 4; c += 32) {
+            const float4 x = __ldg(a + c), y = __ldg(b + c);
+            const float *xp = &x.x, *yp = &y.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float q = __fmul_rn(xp[i], yp[i]);
+                two_sum(hi, lo, q);
+                lo += fmaf(xp[i], yp[i], -q);
+            }
+        }
+    }
+    double z = (double)hi + (double)lo;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    return z;
+}
+
+constexpr int kMergeWarps = 4;
+constexpr int kLaneLists = kMaxStatSplits / 32;
+
+// One warp per row.
+template <bool BF16, int LIST>
+__global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const MergeParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (row >= p.N) return;
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr float kLn2 = 0.6931471805599453f;
+    const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
+    // softmax statistics: lane s holds ranges s, s + 32, ...
+    float4 st[kLaneLists];
+    float m = -INFINITY, zt = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kLaneLists; ++i) {
+        const int s = lane + 32 * i;
+        st[i] = s < p.splits ? p.stats[(long long)s * p.N + row] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        m = fmaxf(m, st[i].x);
+        nan = nan || st[i].y != st[i].y;
+        zt += st[i].w;  // (zero but in the target's range)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+        zt += __shfl_xor_sync(FULL, zt, o);
+    }
+    const float mu = m == -INFINITY ? 0.f : m;
+    float sum = 0.f, es = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLaneLists; ++i) {
+        if (st[i].y == 0.f) continue;
+        const float d = st[i].x - mu, f = exp2f(d);
+        sum += st[i].y * f;
+        es += (st[i].z + st[i].y * d) * f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(FULL, sum, o);
+        es += __shfl_xor_sync(FULL, es, o);
+    }
+    if (__any_sync(FULL, nan)) sum = __int_as_float(0x7fffffff);
+    const float l2 = log2f(sum);
+    const float lse = (m + l2) * kLn2;
+    if (lane == 0) {
+        if (p.logp) p.logp[row] = target >= 0 ? (zt - m - l2) * kLn2 : 0.f;
+        if (p.lse) p.lse[row] = lse;
+        if (p.entropy) p.entropy[row] = (l2 - es / sum) * kLn2;
+    }
+    if (LIST == 0) return;
+    // the largest LIST of all ranges: rounds over the lists' heads
+    float head[kLaneLists];
+    int head_id[kLaneLists], taken[kLaneLists] = {};
+    auto load_head = [&](int i) {
+        const int s = lane + 32 * i;
+        head[i] = -INFINITY;
+        head_id[i] = -1;
+        if (s < p.splits && taken[i] < LIST) {
+            const long long at = ((long long)s * LIST + taken[i]) * p.N + row;
+            head_id[i] = p.list_id[at];
+            if (head_id[i] >= 0) head[i] = p.list_val[at];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kLaneLists; ++i) load_head(i);
+    const int want = min(p.top + kSpareTop, LIST);
+    float my_val = 0.f;   // candidate of lane c
+    int my_id = -1;
+    for (int c = 0; c < want; ++c) {
+        float v = -INFINITY;
+        int id = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < kLaneLists; ++i)
+            if (head_id[i] >= 0 && (head[i] > v || (head[i] == v && head_id[i] < id))) {
+                v = head[i];
+                id = head_id[i];
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float ov = __shfl_xor_sync(FULL, v, o);
+            const int oid = __shfl_xor_sync(FULL, id, o);
+            if (ov > v || (ov == v && oid < id)) {
+                v = ov;
+                id = oid;
+            }
+        }
+        if (id == 0x7fffffff) break;
+        if (lane == c) {
+            my_val = v;
+            my_id = id;
+        }
+#pragma unroll
+        for (int i = 0; i < kLaneLists; ++i)
+            if (head_id[i] == id) {
+                ++taken[i];
+                load_head(i);
+            }
+    }
+    // their exact order
+    const int esize = BF16 ? 2 : 4;
+    const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
+    double z = (double)my_val * 0.6931471805599453;
+    for (int c = 0; c < want; ++c) {
+        const int id = __shfl_sync(FULL, my_id, c);
+        if (id < 0) break;
+        const double e = dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane) *
+                         (double)p.scale;
+        if (lane == c && isfinite(e)) z = e;
+    }
+    int rank = 0;
+    for (int c = 0; c < want; ++c) {
+        const double oz = __shfl_sync(FULL, z, c);
+        const int oid = __shfl_sync(FULL, my_id, c);
+        if (oid >= 0 && (oz > z || (oz == z && oid < my_id))) ++rank;
+    }
+    const int found = __popc(__ballot_sync(FULL, my_id >= 0));
+    if (my_id >= 0 && rank < p.top) {
+        p.top_ids[(long long)row * p.top + rank] = my_id;
+        p.top_logp[(long long)row * p.top + rank] = (float)(z - (double)lse);
+    }
+    if (lane >= found && lane < p.top) {  // fewer numbers than places
+        p.top_ids[(long long)row * p.top + lane] = -1;
+        p.top_logp[(long long)row * p.top + lane] = __int_as_float(0x7fffffff);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// small passes
+// ---------------------------------------------------------------------------
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float4 *part, int parts, long long vecs,
+                                                        void *out)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= vecs) return;
+    float4 a = __ldcs(part + i);
+    for (int s = 1; s < parts; ++s) {
+        const float4 b = __ldcs(part + s * vecs + i);
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+    }
+    if (BF16)
+        reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    else
+        reinterpret_cast<float4 *>(out)[i] = a;
+}
+
+// x = t0 + t1 + t2, each the bf16 nearest to what is left (exact but for what falls below
+// bf16's range).  An infinite or NaN value is its first term; a finite one that rounds to
+// infinity is cut instead.
+__global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long long ld, int rows, int d,
+                                                        __nv_bfloat16 *planes)
+{
+    const long long pairs = (long long)rows * (d / 2);
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= pairs) return;
+    const int r = (int)(i / (d / 2)), c = (int)(i - (long long)r * (d / 2)) * 2;
+    const float2 v = *reinterpret_cast<const float2 *>(x + r * ld + c);
+    float a = v.x, b = v.y;
+    for (int t = 0; t < kMaxPieces; ++t) {
+        auto term = [](float y) {
+            const __nv_bfloat16 n = __float2bfloat16_rn(y);
+            return __hisinf(n) && !isinf(y) ? __float2bfloat16_rz(y) : n;
+        };
+        const __nv_bfloat16 ta = term(a), tb = term(b);
+        __nv_bfloat162 o;
+        o.x = ta;
+        o.y = tb;
+        *reinterpret_cast<__nv_bfloat162 *>(planes + ((long long)t * rows + r) * d + c) = o;
+        a = isfinite(a) ? a - __bfloat162float(ta) : 0.f;
+        b = isfinite(b) ? b - __bfloat162float(tb) : 0.f;
+    }
+}
+
+// Copy of h with zeros in rows that have no part in the gradient (whatever those hold).
+__global__ void __launch_bounds__(256) live_rows_kernel(const LiveRowsParams p)
+{
+    const int vecs = p.row_bytes / 16;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (long long)p.N * vecs) return;
+    const int r = (int)(i / vecs), c = (int)(i - (long long)r * vecs);
+    const bool live = (p.targets && token_at(p.targets, p.index_bytes, r, p.V, p.status) >= 0) ||
+                      (p.dentropy && p.dentropy[r] != 0.f);
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.h) + r * p.ld_bytes) + c;
+    static_cast<uint4 *>(p.out)[i] = live ? *src : make_uint4(0, 0, 0, 0);
+}
+
+} // namespace
+
+cudaError_t launch_logprob_stats(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
+                                 int list, cudaStream_t s)
+{
+    if (list == 0) return launch_gemm<kStats, 0>(a, b, p, s);
+    return list == 12 ? launch_gemm<kStats, 12>(a, b, p, s) : launch_gemm<kStats, 20>(a, b, p, s);
+}
+
+cudaError_t launch_logprob_grad(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
+                                cudaStream_t s)
+{
+    return launch_gemm<kGrad, 0>(a, b, p, s);
+}
+
+cudaError_t launch_product_dh(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
+                              cudaStream_t s)
+{
+    return launch_gemm<kDh, 0>(a, b, p, s);
+}
+
+cudaError_t launch_product_dw(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
+                              cudaStream_t s)
+{
+    return launch_gemm<kDw, 0>(a, b, p, s);
+}
+
+cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void *out, bool bf16,
+                             cudaStream_t s)
+{
+    const long long vecs = elems / 4;
+    const unsigned grid = (unsigned)((vecs + 255) / 256);
+    if (bf16) sum_parts_kernel<true><<<grid, 256, 0, s>>>(reinterpret_cast<const float4 *>(part), parts, vecs, out);
+    else sum_parts_kernel<false><<<grid, 256, 0, s>>>(reinterpret_cast<const float4 *>(part), parts, vecs, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
+                             cudaStream_t s)
+{
+    const long long pairs = (long long)rows * (d / 2);
+    split_f32_kernel<<<(unsigned)((pairs + 255) / 256), 256, 0, s>>>(x, ld, rows, d, planes);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_live_rows(const LiveRowsParams &p, cudaStream_t s)
+{
+    const long long vecs = (long long)p.N * (p.row_bytes / 16);
+    live_rows_kernel<<<(unsigned)((vecs + 255) / 256), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_logprob_merge(const MergeParams &p, bool bf16, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
+    const int threads = kMergeWarps * 32;
+    if (bf16) {
+        if (p.list == 0) logprob_merge_kernel<true, 0><<<grid, threads, 0, s>>>(p);
+        else if (p.list == 12) logprob_merge_kernel<true, 12><<<grid, threads, 0, s>>>(p);
+        else logprob_merge_kernel<true, 20><<<grid, threads, 0, s>>>(p);
+    } else {
+        if (p.list == 0) logprob_merge_kernel<false, 0><<<grid, threads, 0, s>>>(p);
+        else if (p.list == 12) logprob_merge_kernel<false, 12><<<grid, threads, 0, s>>>(p);
+        else logprob_merge_kernel<false, 20><<<grid, threads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+} // namespace txl

@@ -14,6 +14,7 @@
 #include "kernels.h"
 #include "decode.h"
 #include "paged.h"
+#include "vocab.h"
 #include "txl.h"
 
 namespace {
@@ -89,6 +90,21 @@ bool make_map(CUtensorMap *map, const void *base, long long rows, long long oute
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+// 3-D bf16 view [planes][rows][inner] (rows ld elements apart) in 64 x box_rows boxes.
+bool encode_planes(CUtensorMap *map, const void *base, long long inner, long long rows, long long ld,
+                   long long planes, long long plane, unsigned box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)plane * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count()
@@ -291,6 +307,26 @@ int relattn_decode(const void *q, const void *k, const void *v, long long kv_str
 }
 
 } // namespace
+
+namespace txl {
+
+unsigned int *device_status_word()
+{
+    cudaError_t e;
+    return status_word(&e);
+}
+
+unsigned long long wait_limit_ns() { return g_wait_ns; }
+
+int device_sm_count() { return sm_count(); }
+
+bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long long rows,
+                     long long ld, long long planes, long long plane, unsigned box_rows)
+{
+    return encode_planes(map, base, inner, rows, ld, planes, plane, box_rows);
+}
+
+} // namespace txl
 
 extern "C" {
 

@@ -1,0 +1,153 @@
+// Internal launch interface of the model's two ends: the token embedding
+// (embed.cu) and the log probabilities of tokens (logprob.cu).  Not part of the
+// public ABI.
+#pragma once
+
+#include "kernels.h"
+
+namespace txl {
+
+// From txl_api.cu: device status word of the current device (null on a CUDA error), the
+// barrier time limit, SMs of the current device.
+unsigned int *device_status_word();
+unsigned long long wait_limit_ns();
+int device_sm_count();
+// bf16 view [planes][rows][inner], rows ld elements apart, planes plane elements apart, with a
+// 64 x box_rows box and 128-byte swizzle.
+bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long long rows,
+                     long long ld, long long planes, long long plane, unsigned box_rows);
+
+// ---------------------------------------------------------------------------
+// token ids
+// ---------------------------------------------------------------------------
+
+// Token i of an int32 or int64 array: its id in [0, V), or -1 for none.  Any other value is
+// taken as none and recorded.
+__device__ __forceinline__ int token_at(const void *tokens, int index_bytes, long long i, int V,
+                                        unsigned int *status)
+{
+    const long long t = index_bytes == 8 ? __ldg(static_cast<const long long *>(tokens) + i)
+                                         : __ldg(static_cast<const int *>(tokens) + i);
+    if (t < -1 || t >= V) {
+        atomicOr(status, TXL_STATUS_INDEX);
+        return -1;
+    }
+    return (int)t;
+}
+
+// ---------------------------------------------------------------------------
+// embedding
+// ---------------------------------------------------------------------------
+
+struct EmbedParams {
+    const void *tokens;
+    const void *emb;       // [V][emb_ld]
+    void *out;             // [n][d]
+    long long emb_ld;      // elements
+    int index_bytes, n, V, d;
+    float scale;
+    unsigned int *status;
+};
+cudaError_t launch_embed_fwd(const EmbedParams &p, bool bf16, cudaStream_t s);
+
+struct EmbedBwdParams {
+    const void *tokens;
+    const void *dout;      // [n][dout_ld]
+    void *demb;            // [V][d]
+    long long dout_ld;
+    int index_bytes, n, V, d;
+    float scale;
+    int accumulate;
+    unsigned int *status;
+};
+size_t embed_bwd_workspace_bytes(int n, int V, int d);
+cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16, void *workspace,
+                             cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// log probabilities
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxTop = 16;      // alternatives of a row
+constexpr int kSpareTop = 4;     // candidates kept beyond them, for the exact order
+constexpr int kMaxStatSplits = 160;  // vocabulary ranges of a row
+constexpr int kMaxPieces = 3;    // bf16 terms of an fp32 operand
+
+// Candidates kept per row and vocabulary range for `top` alternatives.
+constexpr int list_length(int top) { return top == 0 ? 0 : top <= 8 ? 12 : 20; }
+
+// One GEMM over 128 x bn tiles, bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
+// Which operands, and what becomes of a tile, is the kernel's mode.
+struct GemmParams {
+    int M, N;              // rows and columns of the product
+    int mb, nb, bn;        // tiles, and columns of one (a multiple of 64, at most 256)
+    int kb;                // 64-wide steps along the contraction
+    int splits;            // statistics: ranges of the columns; products: of the contraction
+    int n_items;
+    int n_pairs;           // products of terms: term (pair_a >> 4 i) & 15 of A by that of B
+    unsigned pair_a, pair_b;
+    int b_row0;            // offset of B's rows (the vocabulary chunk's first)
+    unsigned int *status;
+    unsigned long long wait_ns;
+    // statistics and gradient of the logits
+    const void *targets;   // or null
+    int index_bytes;
+    int V;                 // the whole vocabulary
+    float scale;
+    float4 *stats;         // [splits][M]: maximum, sum, weighted sum (log2 units), target's logit
+    float *list_val;       // [splits][list][M]
+    int *list_id;
+    const float *lse, *entropy, *dlogp, *dentropy;  // (the last two may be null)
+    __nv_bfloat16 *g;      // [g_pieces][M][g_ld]
+    long long g_ld, g_plane;
+    int g_pieces;
+    // products
+    float *part;           // [splits][M][N], or null: out directly
+    void *out;             // [M][N]
+    int out_bf16;
+};
+
+cudaError_t launch_logprob_stats(const CUtensorMap &tm_h, const CUtensorMap &tm_w,
+                                 const GemmParams &p, int list, cudaStream_t s);
+cudaError_t launch_logprob_grad(const CUtensorMap &tm_h, const CUtensorMap &tm_w,
+                                const GemmParams &p, cudaStream_t s);
+// dh = G W (G rows of the vocabulary) and dW = G^T h (contraction over the rows).
+cudaError_t launch_product_dh(const CUtensorMap &tm_g, const CUtensorMap &tm_w, const GemmParams &p,
+                              cudaStream_t s);
+cudaError_t launch_product_dw(const CUtensorMap &tm_g, const CUtensorMap &tm_h, const GemmParams &p,
+                              cudaStream_t s);
+// out = sum over the parts, in their order.
+cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void *out, bool bf16,
+                             cudaStream_t s);
+// fp32 rows as three bf16 terms: planes [3][rows][d].
+cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
+                             cudaStream_t s);
+
+struct LiveRowsParams {
+    const void *h;         // rows ld_bytes apart
+    void *out;             // [N][row_bytes]
+    long long ld_bytes;
+    int N, V, row_bytes, index_bytes;
+    const void *targets;
+    const float *dentropy;
+    unsigned int *status;
+};
+cudaError_t launch_live_rows(const LiveRowsParams &p, cudaStream_t s);
+
+struct MergeParams {
+    const float4 *stats;
+    const float *list_val;
+    const int *list_id;
+    int splits, N, V, d, top, list;
+    const void *h, *w;
+    long long h_ld, w_ld;
+    const void *targets;
+    int index_bytes;
+    float scale;
+    float *logp, *lse, *entropy, *top_logp;
+    int *top_ids;
+    unsigned int *status;
+};
+cudaError_t launch_logprob_merge(const MergeParams &p, bool bf16, cudaStream_t s);
+
+} // namespace txl

@@ -1,0 +1,500 @@
+// C-ABI entry points of the token embedding and of the log probabilities (include/txl.h):
+// argument validation, work division, workspace layout, launches.
+#include <algorithm>
+
+#include "txl.h"
+#include "vocab.h"
+
+namespace {
+
+using txl::GemmParams;
+
+bool on(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int status_of(cudaError_t e) { return e == cudaSuccess ? TXL_OK : TXL_ERR_CUDA; }
+cudaStream_t stream_of(void *s) { return static_cast<cudaStream_t>(s); }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+long long up64(long long x) { return (x + 63) / 64 * 64; }
+int elem(int dtype) { return dtype == TXL_BF16 ? 2 : 4; }
+
+constexpr int kMaxRows = 1 << 28;   // rows, tokens
+constexpr int kMaxVocab = 1 << 28;
+constexpr int kMaxWidth = 1 << 16;
+
+int check_type(int dtype)
+{
+    return dtype == TXL_F32 || dtype == TXL_BF16 ? TXL_OK : TXL_ERR_INVALID_ARG;
+}
+
+int check_ids(const void *ids, int index_type)
+{
+    if (index_type != TXL_I32 && index_type != TXL_I64) return TXL_ERR_INVALID_ARG;
+    return on(ids, (size_t)index_type) ? TXL_OK : TXL_ERR_MISALIGNED;
+}
+
+// A [rows][d] operand whose rows are stride elements apart.
+int check_rows(const void *p, long long stride, int rows, int d, int dtype)
+{
+    if (stride < 1) return TXL_ERR_INVALID_ARG;
+    if (stride < d && rows > 1) return TXL_ERR_SHAPE;
+    if (!on(p, 16) || (stride * elem(dtype)) % 16 != 0) return TXL_ERR_MISALIGNED;
+    return stride > (1LL << 36) ? TXL_ERR_UNSUPPORTED : TXL_OK;
+}
+
+int check_sizes(int n, int V, int d)
+{
+    if (n < 0 || V < 1 || d < 1) return TXL_ERR_INVALID_ARG;
+    if (d % 8 != 0 || n > kMaxRows || V > kMaxVocab || d > kMaxWidth) return TXL_ERR_UNSUPPORTED;
+    return TXL_OK;
+}
+
+// ---------------------------------------------------------------------------
+// work division of the log probabilities
+// ---------------------------------------------------------------------------
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// Columns of a tile over `cols` columns: as few tiles as 256 columns allow, of equal width.
+int tile_columns(long long cols)
+{
+    const int n = ceil_div(cols, 256);
+    return (int)std::min<long long>(256, up64(ceil_div(cols, n)));
+}
+
+// Parts of `steps` equal steps for each of `units` blocks of work, one block per SM at a time:
+// waves * (steps of the longest part + what a part costs besides).
+int choose_parts(long long units, int steps, int most, double extra)
+{
+    const int sms = txl::device_sm_count();
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= std::min(steps, most); ++s) {
+        const double waves = (double)((units * s + sms - 1) / sms);
+        const double cost = waves * (ceil_div(steps, s) + extra) + 0.002 * s;
+        if (s == 1 || cost < least) {
+            best = s;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+struct StatsPlan {
+    int mb, nb, bn, splits, list;
+    size_t h_planes, w_planes, stats, val, id, total;  // offsets
+};
+
+StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
+{
+    StatsPlan s{};
+    s.mb = ceil_div(N, 128);
+    s.bn = tile_columns(V);
+    if (s.bn < 256 && V > 256) s.bn = 256;
+    s.nb = ceil_div(V, s.bn);
+    s.splits = choose_parts(s.mb, s.nb, txl::kMaxStatSplits, 0.5);
+    s.list = txl::list_length(top);
+    size_t o = 0;
+    const size_t row = (size_t)d * 2 * txl::kMaxPieces;
+    s.h_planes = o;
+    if (dtype == TXL_F32) o = up256(o + N * row);
+    s.w_planes = o;
+    if (dtype == TXL_F32) o = up256(o + V * row);
+    s.stats = o;
+    o = up256(o + (size_t)s.splits * N * sizeof(float4));
+    s.val = o;
+    o = up256(o + (size_t)s.splits * s.list * N * 4);
+    s.id = o;
+    s.total = up256(o + (size_t)s.splits * s.list * N * 4);
+    return s;
+}
+
+constexpr size_t kGradBytes = (size_t)1 << 30;  // of G in the workspace: vocabulary chunks beyond
+
+struct GradPlan {
+    int chunk, chunks;            // vocabulary rows at a time
+    int pieces;                   // terms of G
+    int bn, mb_h, mb_w, nb;       // tiles of dh and of a chunk's dW
+    int split_h, split_w, parts_h;
+    long long g_ld, g_plane;
+    size_t live, h_planes, w_planes, g, part_h, part_w, total;
+};
+
+GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
+{
+    GradPlan g{};
+    g.pieces = dtype == TXL_F32 ? 3 : grad_dtype == TXL_F32 ? 2 : 1;
+    const long long most = (long long)(kGradBytes / ((size_t)g.pieces * 2 * std::max(N, 1)));
+    g.chunk = V;
+    if (V > std::max(64LL, most)) g.chunk = (int)std::max(64LL, most / 64 * 64);
+    g.chunks = ceil_div(V, g.chunk);
+    if (g.chunks > 1) g.chunk = (int)up64(ceil_div(V, g.chunks));
+    g.chunks = ceil_div(V, g.chunk);
+    g.g_ld = up64(g.chunk);
+    g.g_plane = g.g_ld * N;
+    g.bn = tile_columns(d);
+    g.nb = ceil_div(d, g.bn);
+    g.mb_h = ceil_div(N, 128);
+    g.mb_w = ceil_div(g.chunk, 128);
+    // (a part costs its tile's write and the sum's reads: about eight steps of 64)
+    g.split_h = choose_parts((long long)g.mb_h * g.nb, ceil_div(g.chunk, 64), 16, 8.0);
+    g.split_w = choose_parts((long long)g.mb_w * g.nb, ceil_div(N, 64), 16, 8.0);
+    g.parts_h = g.chunks * g.split_h;
+    size_t o = 0;
+    const size_t row = (size_t)d * 2 * txl::kMaxPieces;
+    g.live = o;
+    o = up256(o + (size_t)N * d * elem(dtype));
+    g.h_planes = o;
+    if (dtype == TXL_F32) o = up256(o + N * row);
+    g.w_planes = o;
+    if (dtype == TXL_F32) o = up256(o + V * row);
+    g.g = o;
+    o = up256(o + (size_t)g.pieces * g.g_plane * 2);
+    g.part_h = o;
+    if (g.parts_h > 1) o = up256(o + (size_t)g.parts_h * N * d * 4);
+    g.part_w = o;
+    if (g.split_w > 1) o = up256(o + (size_t)g.split_w * g.chunk * d * 4);
+    g.total = o;
+    return g;
+}
+
+// Products of terms of two operands with pa and pb bf16 terms, the smallest first.
+void set_pairs(GemmParams &p, int pa, int pb)
+{
+    static constexpr int order[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+    p.n_pairs = 0;
+    for (const auto &o : order)
+        if (o[0] < pa && o[1] < pb) {
+            p.pair_a |= (unsigned)o[0] << (4 * p.n_pairs);
+            p.pair_b |= (unsigned)o[1] << (4 * p.n_pairs);
+            ++p.n_pairs;
+        }
+}
+
+// The bf16 terms of a [rows][d] operand: itself, or its planes in the workspace.
+struct Operand {
+    const void *p;
+    long long ld;
+    int planes;
+    long long plane;
+};
+
+Operand operand(const void *p, long long ld, const char *planes, int rows, int d, int dtype)
+{
+    if (dtype == TXL_BF16) return {p, ld, 1, ld * rows};
+    return {planes, d, txl::kMaxPieces, (long long)rows * d};
+}
+
+bool map_of(CUtensorMap *map, const Operand &o, int rows, int d, unsigned box_rows)
+{
+    return txl::make_map_planes(map, o.p, d, rows, o.ld, o.planes, o.plane, box_rows);
+}
+
+} // namespace
+
+extern "C" {
+
+int txl_embed_fwd(const void *tokens, int index_type, const void *emb, long long emb_stride,
+                  void *out, int n, int V, int d, float scale, int dtype, void *stream)
+{
+    int rc;
+    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(n, V, d)) != TXL_OK) return rc;
+    if ((rc = check_ids(tokens, index_type)) != TXL_OK) return rc;
+    if (!emb || (n > 0 && (!tokens || !out)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if ((rc = check_rows(emb, emb_stride, V, d, dtype)) != TXL_OK) return rc;
+    if (!on(out, 16)) return TXL_ERR_MISALIGNED;
+    if (n == 0) return TXL_OK;
+    if ((long long)n * d / 4 / 1024 > 0x7ffffff0LL) return TXL_ERR_UNSUPPORTED;
+    txl::EmbedParams p{};
+    p.status = txl::device_status_word();
+    if (!p.status) return TXL_ERR_CUDA;
+    p.tokens = tokens;
+    p.index_bytes = index_type;
+    p.emb = emb;
+    p.emb_ld = emb_stride;
+    p.out = out;
+    p.n = n;
+    p.V = V;
+    p.d = d;
+    p.scale = scale;
+    return status_of(txl::launch_embed_fwd(p, dtype == TXL_BF16, stream_of(stream)));
+}
+
+size_t txl_embed_bwd_workspace_size(int n, int V, int d)
+{
+    if (check_sizes(n, V, d) != TXL_OK) return 0;
+    return n == 0 ? 0 : txl::embed_bwd_workspace_bytes(n, V, d);
+}
+
+int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long long dout_stride,
+                  void *demb, int n, int V, int d, float scale, int dtype, int grad_dtype,
+                  int accumulate, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_type(grad_dtype)) != TXL_OK) return rc;
+    if ((rc = check_sizes(n, V, d)) != TXL_OK) return rc;
+    if ((rc = check_ids(tokens, index_type)) != TXL_OK) return rc;
+    if (!demb || (n > 0 && (!tokens || !dout)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if (accumulate && grad_dtype != TXL_F32) return TXL_ERR_UNSUPPORTED;
+    if (n > 0 && (rc = check_rows(dout, dout_stride, n, d, dtype)) != TXL_OK) return rc;
+    if (!on(demb, 16)) return TXL_ERR_MISALIGNED;
+    cudaStream_t s = stream_of(stream);
+    if (n == 0)
+        return accumulate ? TXL_OK
+                          : status_of(cudaMemsetAsync(demb, 0, (size_t)V * d * elem(grad_dtype), s));
+    if (!workspace || workspace_bytes < txl::embed_bwd_workspace_bytes(n, V, d)) return TXL_ERR_WORKSPACE;
+    if (!on(workspace, 256)) return TXL_ERR_MISALIGNED;
+    txl::EmbedBwdParams p{};
+    p.status = txl::device_status_word();
+    if (!p.status) return TXL_ERR_CUDA;
+    p.tokens = tokens;
+    p.index_bytes = index_type;
+    p.dout = dout;
+    p.dout_ld = dout_stride;
+    p.demb = demb;
+    p.n = n;
+    p.V = V;
+    p.d = d;
+    p.scale = scale;
+    p.accumulate = accumulate != 0;
+    return status_of(txl::launch_embed_bwd(p, dtype == TXL_BF16, grad_dtype == TXL_BF16, workspace, s));
+}
+
+size_t txl_logprob_fwd_workspace_size(int N, int V, int d, int top, int dtype)
+{
+    if (check_sizes(N, V, d) != TXL_OK || check_type(dtype) != TXL_OK || top < 0 || top > txl::kMaxTop)
+        return 0;
+    return N == 0 ? 0 : plan_stats(N, V, d, dtype, top).total;
+}
+
+int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long w_stride,
+                    const void *targets, int index_type, float *logp, float *lse, float *entropy,
+                    float *top_logp, int *top_ids, int N, int V, int d, int top, float scale,
+                    int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(N, V, d)) != TXL_OK) return rc;
+    if ((rc = check_ids(targets, index_type)) != TXL_OK) return rc;
+    if (top < 0 || !w || (N > 0 && !h) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if (top > txl::kMaxTop) return TXL_ERR_UNSUPPORTED;
+    if (N > 0 && top > 0 && (!top_logp || !top_ids)) return TXL_ERR_INVALID_ARG;
+    if (N > 0 && !logp && !lse && !entropy && top == 0) return TXL_ERR_INVALID_ARG;
+    if (N > 0 && (rc = check_rows(h, h_stride, N, d, dtype)) != TXL_OK) return rc;
+    if ((rc = check_rows(w, w_stride, V, d, dtype)) != TXL_OK) return rc;
+    for (const void *p : {(const void *)logp, (const void *)lse, (const void *)entropy,
+                          (const void *)top_logp, (const void *)top_ids})
+        if (!on(p, 4)) return TXL_ERR_MISALIGNED;
+    if (N == 0) return TXL_OK;
+    const StatsPlan s = plan_stats(N, V, d, dtype, top);
+    if (!workspace || workspace_bytes < s.total) return TXL_ERR_WORKSPACE;
+    if (!on(workspace, 256)) return TXL_ERR_MISALIGNED;
+    cudaStream_t st = stream_of(stream);
+    char *ws = static_cast<char *>(workspace);
+    unsigned int *status = txl::device_status_word();
+    if (!status) return TXL_ERR_CUDA;
+
+    if (dtype == TXL_F32) {
+        cudaError_t e = txl::launch_split_f32(static_cast<const float *>(h), h_stride, N, d,
+                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), st);
+        if (e == cudaSuccess)
+            e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), st);
+        if (e != cudaSuccess) return TXL_ERR_CUDA;
+    }
+    const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
+    const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
+    CUtensorMap tm_h, tm_w;
+    if (!map_of(&tm_h, oh, N, d, 128) || !map_of(&tm_w, ow, V, d, (unsigned)s.bn)) return TXL_ERR_CUDA;
+    GemmParams p{};
+    p.M = N;
+    p.N = V;
+    p.V = V;
+    p.mb = s.mb;
+    p.nb = s.nb;
+    p.bn = s.bn;
+    p.kb = ceil_div(d, 64);
+    p.splits = s.splits;
+    p.n_items = s.mb * s.splits;
+    set_pairs(p, oh.planes, ow.planes);
+    p.status = status;
+    p.wait_ns = txl::wait_limit_ns();
+    p.targets = targets;
+    p.index_bytes = index_type;
+    p.scale = scale;
+    p.stats = reinterpret_cast<float4 *>(ws + s.stats);
+    p.list_val = reinterpret_cast<float *>(ws + s.val);
+    p.list_id = reinterpret_cast<int *>(ws + s.id);
+    if (txl::launch_logprob_stats(tm_h, tm_w, p, s.list, st) != cudaSuccess) return TXL_ERR_CUDA;
+
+    txl::MergeParams m{};
+    m.stats = p.stats;
+    m.list_val = p.list_val;
+    m.list_id = p.list_id;
+    m.splits = s.splits;
+    m.N = N;
+    m.V = V;
+    m.d = d;
+    m.top = top;
+    m.list = s.list;
+    m.h = h;
+    m.w = w;
+    m.h_ld = h_stride;
+    m.w_ld = w_stride;
+    m.targets = targets;
+    m.index_bytes = index_type;
+    m.scale = scale;
+    m.logp = logp;
+    m.lse = lse;
+    m.entropy = entropy;
+    m.top_logp = top_logp;
+    m.top_ids = top_ids;
+    m.status = status;
+    return status_of(txl::launch_logprob_merge(m, dtype == TXL_BF16, st));
+}
+
+size_t txl_logprob_bwd_workspace_size(int N, int V, int d, int dtype, int grad_dtype)
+{
+    if (check_sizes(N, V, d) != TXL_OK || check_type(dtype) != TXL_OK || check_type(grad_dtype) != TXL_OK)
+        return 0;
+    return N == 0 ? 0 : plan_grad(N, V, d, dtype, grad_dtype).total;
+}
+
+int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long w_stride,
+                    const void *targets, int index_type, const float *lse, const float *entropy,
+                    const float *dlogp, const float *dentropy, void *dh, void *dw, int N, int V,
+                    int d, float scale, int dtype, int grad_dtype, void *workspace,
+                    size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_type(grad_dtype)) != TXL_OK) return rc;
+    if ((rc = check_sizes(N, V, d)) != TXL_OK) return rc;
+    if ((rc = check_ids(targets, index_type)) != TXL_OK) return rc;
+    if (!w || (!dh && !dw) || (N > 0 && (!h || !lse)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if ((targets == nullptr) != (dlogp == nullptr)) return TXL_ERR_INVALID_ARG;
+    if (N > 0 && ((!dlogp && !dentropy) || (dentropy && !entropy))) return TXL_ERR_INVALID_ARG;
+    if (dtype == TXL_F32 && grad_dtype != TXL_F32) return TXL_ERR_UNSUPPORTED;
+    if (N > 0 && (rc = check_rows(h, h_stride, N, d, dtype)) != TXL_OK) return rc;
+    if ((rc = check_rows(w, w_stride, V, d, dtype)) != TXL_OK) return rc;
+    if (!on(dh, 16) || !on(dw, 16)) return TXL_ERR_MISALIGNED;
+    for (const void *p : {(const void *)lse, (const void *)entropy, (const void *)dlogp, (const void *)dentropy})
+        if (!on(p, 4)) return TXL_ERR_MISALIGNED;
+    cudaStream_t st = stream_of(stream);
+    if (N == 0)
+        return dw ? status_of(cudaMemsetAsync(dw, 0, (size_t)V * d * elem(grad_dtype), st)) : TXL_OK;
+    const GradPlan g = plan_grad(N, V, d, dtype, grad_dtype);
+    if (!workspace || workspace_bytes < g.total) return TXL_ERR_WORKSPACE;
+    if (!on(workspace, 256)) return TXL_ERR_MISALIGNED;
+    char *ws = static_cast<char *>(workspace);
+    unsigned int *status = txl::device_status_word();
+    if (!status) return TXL_ERR_CUDA;
+
+    // h without the rows that have no part, then both operands' bf16 terms
+    txl::LiveRowsParams l{};
+    l.h = h;
+    l.out = ws + g.live;
+    l.ld_bytes = h_stride * elem(dtype);
+    l.N = N;
+    l.V = V;
+    l.row_bytes = d * elem(dtype);
+    l.index_bytes = index_type;
+    l.targets = targets;
+    l.dentropy = dentropy;
+    l.status = status;
+    cudaError_t e = txl::launch_live_rows(l, st);
+    if (dtype == TXL_F32) {
+        if (e == cudaSuccess)
+            e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), d, N, d,
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), st);
+        if (e == cudaSuccess)
+            e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), st);
+    }
+    if (e != cudaSuccess) return TXL_ERR_CUDA;
+    const Operand oh = operand(ws + g.live, d, ws + g.h_planes, N, d, dtype);
+    const Operand ow = operand(w, w_stride, ws + g.w_planes, V, d, dtype);
+
+    GemmParams base{};
+    base.status = status;
+    base.wait_ns = txl::wait_limit_ns();
+    base.V = V;
+    base.scale = scale;
+    base.targets = targets;
+    base.index_bytes = index_type;
+    base.lse = lse;
+    base.entropy = entropy;
+    base.dlogp = dlogp;
+    base.dentropy = dentropy;
+    base.g = reinterpret_cast<__nv_bfloat16 *>(ws + g.g);
+    base.g_ld = g.g_ld;
+    base.g_plane = g.g_plane;
+    base.g_pieces = g.pieces;
+    const int bn_v = std::min<long long>(256, up64(std::min(V, g.chunk)));
+    CUtensorMap h_rows, w_rows, h_cols, w_cols;
+    if (!map_of(&h_rows, oh, N, d, 128) || !map_of(&w_rows, ow, V, d, (unsigned)bn_v) ||
+        !map_of(&h_cols, oh, N, d, 64) || !map_of(&w_cols, ow, V, d, 64))
+        return TXL_ERR_CUDA;
+    for (int c = 0; c < g.chunks; ++c) {
+        const int v0 = c * g.chunk, cols = std::min(g.chunk, V - v0);
+        // G of the chunk
+        GemmParams p = base;
+        p.M = N;
+        p.N = cols;
+        p.mb = g.mb_h;
+        p.bn = bn_v;
+        p.nb = ceil_div(cols, bn_v);
+        p.kb = ceil_div(d, 64);
+        p.splits = 1;
+        p.n_items = p.mb * p.nb;
+        p.b_row0 = v0;
+        set_pairs(p, oh.planes, ow.planes);
+        if (txl::launch_logprob_grad(h_rows, w_rows, p, st) != cudaSuccess) return TXL_ERR_CUDA;
+        const Operand og = {ws + g.g, g.g_ld, g.pieces, g.g_plane};
+        if (dh) {
+            CUtensorMap tm_g;
+            if (!map_of(&tm_g, og, N, cols, 128)) return TXL_ERR_CUDA;
+            GemmParams q = base;
+            q.M = N;
+            q.N = d;
+            q.mb = g.mb_h;
+            q.nb = g.nb;
+            q.bn = g.bn;
+            q.kb = ceil_div(cols, 64);
+            q.splits = g.split_h;
+            q.n_items = q.mb * q.nb * q.splits;
+            q.b_row0 = v0;
+            q.part = g.parts_h > 1 ? reinterpret_cast<float *>(ws + g.part_h) + (size_t)c * g.split_h * N * d
+                                   : nullptr;
+            q.out = dh;
+            q.out_bf16 = dtype == TXL_BF16;
+            set_pairs(q, dtype == TXL_F32 ? g.pieces : 1, ow.planes);
+            if (txl::launch_product_dh(tm_g, w_cols, q, st) != cudaSuccess) return TXL_ERR_CUDA;
+        }
+        if (dw) {
+            CUtensorMap tm_g;
+            if (!map_of(&tm_g, og, N, cols, 64)) return TXL_ERR_CUDA;
+            char *out = static_cast<char *>(dw) + (size_t)v0 * d * elem(grad_dtype);
+            GemmParams q = base;
+            q.M = cols;
+            q.N = d;
+            q.mb = ceil_div(cols, 128);
+            q.nb = g.nb;
+            q.bn = g.bn;
+            q.kb = ceil_div(N, 64);
+            q.splits = g.split_w;
+            q.n_items = q.mb * q.nb * q.splits;
+            q.part = g.split_w > 1 ? reinterpret_cast<float *>(ws + g.part_w) : nullptr;
+            q.out = out;
+            q.out_bf16 = grad_dtype == TXL_BF16;
+            set_pairs(q, g.pieces, oh.planes);
+            if (txl::launch_product_dw(tm_g, h_cols, q, st) != cudaSuccess) return TXL_ERR_CUDA;
+            if (q.part && txl::launch_sum_parts(q.part, g.split_w, (long long)cols * d, out,
+                                                grad_dtype == TXL_BF16, st) != cudaSuccess)
+                return TXL_ERR_CUDA;
+        }
+    }
+    if (dh && g.parts_h > 1 &&
+        txl::launch_sum_parts(reinterpret_cast<float *>(ws + g.part_h), g.parts_h, (long long)N * d, dh,
+                              dtype == TXL_BF16, st) != cudaSuccess)
+        return TXL_ERR_CUDA;
+    return TXL_OK;
+}
+
+} // extern "C"
