@@ -36,6 +36,13 @@ constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual align
 constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
 
+// The tensor core's fp32 accumulators cut each addition instead of rounding it, so a sum of
+// `steps` additions (16 products each) comes out too small, on average by 0.2 (terms of random
+// sign) to 0.3 (terms of one sign) times steps * 2^-24 of its value (measured for 4 to 256 steps);
+// results that are fp32 are scaled by the mean of that.  1024 wide: root mean square error 15 to 19
+// times 2^-24 without it, 3 to 9 with it.
+__device__ __forceinline__ float uncut(int steps) { return fmaf((float)steps, 0.27f * 5.9604645e-8f, 1.f); }
+
 static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 
@@ -314,15 +321,15 @@ __global__ void __launch_bounds__(256, 1)
         const int wq = warp - 4;
         const int row = wq * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
-        constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-        const float c2 = p.scale * kLog2e;
+        constexpr float kLog2e = 1.4426950408889634f;
+        const float zscale = p.scale * uncut(p.kb * (BK / 16)), c2 = zscale * kLog2e;
         bool ok = true;
         int tile = 0;
         for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
             const int nt = item_tiles<MODE>(p, item);
             RowStats<LIST> r;
             int target = -1;
-            float g1 = 0.f, ge = 0.f, lse2 = 0.f, ent = 0.f;
+            float g1 = 0.f, ge = 0.f, lse = 0.f, ent = 0.f, lpt = 0.f;
             bool live = false;
             if (MODE == kStats || MODE == kGrad) {
                 const int m = item_tile<MODE>(p, item, 0).m * BM + row;
@@ -334,7 +341,8 @@ __global__ void __launch_bounds__(256, 1)
                             ge = p.dentropy[m] * p.scale;
                             ent = p.entropy[m];
                         }
-                        lse2 = p.lse[m] * kLog2e;
+                        lse = p.lse[m];
+                        lpt = p.target_logp[m];
                         live = target >= 0 || (p.dentropy && p.dentropy[m] != 0.f);
                     }
                 }
@@ -370,10 +378,11 @@ __global__ void __launch_bounds__(256, 1)
                         const int at = target - (p.b_row0 + n0 + c);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float lp = fmaf(__uint_as_float(raw[i]), c2, -lse2);
-                            const float pr = ex2(lp);
+                            float lp = fmaf(__uint_as_float(raw[i]), zscale, -lse);
+                            if (i == at) lp = lpt;
+                            const float pr = ex2(lp * kLog2e);
                             float f = g1;
-                            if (p.dentropy) f = fmaf(ge, fmaf(fmaxf(lp, -1e30f), kLn2, ent), f);
+                            if (p.dentropy) f = fmaf(ge, fmaxf(lp, -1e30f) + ent, f);
                             v[i] = -pr * f + (i == at ? g1 : 0.f);
                             if (!live) v[i] = 0.f;
                         }
@@ -399,6 +408,9 @@ __global__ void __launch_bounds__(256, 1)
                         const long long at = ((long long)s * p.M + m) * p.N + n0 + c;
                         // (cnt is a multiple of 8: rows of the operands are)
                         if (p.part || !p.out_bf16) {
+                            const float f = uncut((w.kb_hi - w.kb_lo) * (BK / 16));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f);
                             float *dst = (p.part ? p.part : static_cast<float *>(p.out)) + at;
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
@@ -561,14 +573,45 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
         es += __shfl_xor_sync(FULL, es, o);
     }
     if (__any_sync(FULL, nan)) sum = __int_as_float(0x7fffffff);
-    const float l2 = log2f(sum);
-    const float lse = (m + l2) * kLn2;
-    if (lane == 0) {
-        if (p.logp) p.logp[row] = target >= 0 ? (zt - m - l2) * kLn2 : 0.f;
-        if (p.lse) p.lse[row] = lse;
-        if (p.entropy) p.entropy[row] = (l2 - es / sum) * kLn2;
+    // A logit known more exactly (log2 units) takes its place in the sums; peaked rows, whose
+    // sums are a few such terms, are as exact as these.
+    auto replace = [&](float was, double is) {
+        const float d0 = was - mu, d1 = (float)(is - (double)mu);
+        const float e0 = ex2(d0), e1 = exp2f(d1);
+        sum += e1 - e0;
+        es += e1 * d1 - e0 * d0;
+    };
+    constexpr double kLog2e = 1.4426950408889634;
+    const int esize = BF16 ? 2 : 4;
+    const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
+    auto logit = [&](int id) {
+        return dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane) *
+               (double)p.scale;
+    };
+    double z_target = (double)zt * kLn2;
+    bool replaced = true;  // the target's logit in the sums
+    if (target >= 0) {
+        const double e = logit(target);
+        if (isfinite(e) && isfinite(zt)) {
+            z_target = e;
+            replaced = false;
+        }
     }
-    if (LIST == 0) return;
+    auto finish = [&]() -> double {
+        if (!replaced) replace(zt, z_target * kLog2e);
+        const float l = logf(sum);
+        const double lse = (double)m * 0.6931471805599453 + (double)l;
+        if (lane == 0) {
+            if (p.logp) p.logp[row] = target >= 0 ? (float)(z_target - lse) : 0.f;
+            if (p.lse) p.lse[row] = (float)lse;
+            if (p.entropy) p.entropy[row] = l - es / sum * kLn2;
+        }
+        return lse;
+    };
+    if (LIST == 0) {
+        finish();
+        return;
+    }
     // the largest LIST of all ranges: rounds over the lists' heads
     float head[kLaneLists];
     int head_id[kLaneLists], taken[kLaneLists] = {};
@@ -618,16 +661,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
             }
     }
     // their exact order
-    const int esize = BF16 ? 2 : 4;
-    const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
     double z = (double)my_val * 0.6931471805599453;
     for (int c = 0; c < want; ++c) {
         const int id = __shfl_sync(FULL, my_id, c);
+        const float was = __shfl_sync(FULL, my_val, c);
         if (id < 0) break;
-        const double e = dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane) *
-                         (double)p.scale;
-        if (lane == c && isfinite(e)) z = e;
+        const double e = id == target ? z_target : logit(id);
+        if (!isfinite(e) || !isfinite(was)) continue;
+        if (lane == c) z = e;
+        if (id == target) replaced = true;
+        replace(was, e * kLog2e);
     }
+    const double lse = finish();
     int rank = 0;
     for (int c = 0; c < want; ++c) {
         const double oz = __shfl_sync(FULL, z, c);
@@ -637,7 +682,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
     const int found = __popc(__ballot_sync(FULL, my_id >= 0));
     if (my_id >= 0 && rank < p.top) {
         p.top_ids[(long long)row * p.top + rank] = my_id;
-        p.top_logp[(long long)row * p.top + rank] = (float)(z - (double)lse);
+        p.top_logp[(long long)row * p.top + rank] = (float)(z - lse);
     }
     if (lane >= found && lane < p.top) {  // fewer numbers than places
         p.top_ids[(long long)row * p.top + lane] = -1;
@@ -696,17 +741,29 @@ __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long lon
     }
 }
 
-// Copy of h with zeros in rows that have no part in the gradient (whatever those hold).
-__global__ void __launch_bounds__(256) live_rows_kernel(const LiveRowsParams p)
+// One warp per row: a copy of h with zeros in rows that have no part in the gradient (whatever
+// those hold), and the log probability of the row's target from its logit's products carried
+// beyond fp32: G's one large element is the difference of 1 and that probability.
+template <bool BF16>
+__global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p)
 {
-    const int vecs = p.row_bytes / 16;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (long long)p.N * vecs) return;
-    const int r = (int)(i / vecs), c = (int)(i - (long long)r * vecs);
-    const bool live = (p.targets && token_at(p.targets, p.index_bytes, r, p.V, p.status) >= 0) ||
-                      (p.dentropy && p.dentropy[r] != 0.f);
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.h) + r * p.ld_bytes) + c;
-    static_cast<uint4 *>(p.out)[i] = live ? *src : make_uint4(0, 0, 0, 0);
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (row >= p.N) return;
+    constexpr int ESIZE = BF16 ? 2 : 4;
+    const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
+    const bool live = target >= 0 || (p.dentropy && p.dentropy[row] != 0.f);
+    const int vecs = p.d * ESIZE / 16;
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.h) + row * p.h_ld * ESIZE);
+    uint4 *dst = static_cast<uint4 *>(p.out) + (long long)row * vecs;
+    for (int c = lane; c < vecs; c += 32) dst[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    if (target < 0) {
+        if (lane == 0) p.target_logp[row] = 0.f;
+        return;
+    }
+    const double z = dot_exact<BF16>(src, static_cast<const char *>(p.w) + target * p.w_ld * ESIZE, p.d, lane) *
+                     (double)p.scale;
+    if (lane == 0) p.target_logp[row] = (float)(z - (double)p.lse[row]);
 }
 
 } // namespace
@@ -754,10 +811,11 @@ cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv
     return cudaGetLastError();
 }
 
-cudaError_t launch_live_rows(const LiveRowsParams &p, cudaStream_t s)
+cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
 {
-    const long long vecs = (long long)p.N * (p.row_bytes / 16);
-    live_rows_kernel<<<(unsigned)((vecs + 255) / 256), 256, 0, s>>>(p);
+    const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
+    if (bf16) grad_rows_kernel<true><<<grid, kMergeWarps * 32, 0, s>>>(p);
+    else grad_rows_kernel<false><<<grid, kMergeWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -98,6 +98,7 @@ struct GemmParams {
     float *list_val;       // [splits][list][M]
     int *list_id;
     const float *lse, *entropy, *dlogp, *dentropy;  // (the last two may be null)
+    const float *target_logp;
     __nv_bfloat16 *g;      // [g_pieces][M][g_ld]
     long long g_ld, g_plane;
     int g_pieces;
@@ -123,16 +124,18 @@ cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
                              cudaStream_t s);
 
-struct LiveRowsParams {
-    const void *h;         // rows ld_bytes apart
-    void *out;             // [N][row_bytes]
-    long long ld_bytes;
-    int N, V, row_bytes, index_bytes;
+struct GradRowsParams {
+    const void *h, *w;
+    void *out;             // [N][d]
+    float *target_logp;    // [N]
+    long long h_ld, w_ld;
+    int N, V, d, index_bytes;
     const void *targets;
-    const float *dentropy;
+    const float *lse, *dentropy;
+    float scale;
     unsigned int *status;
 };
-cudaError_t launch_live_rows(const LiveRowsParams &p, cudaStream_t s);
+cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s);
 
 struct MergeParams {
     const float4 *stats;

@@ -115,7 +115,7 @@ struct GradPlan {
     int bn, mb_h, mb_w, nb;       // tiles of dh and of a chunk's dW
     int split_h, split_w, parts_h;
     long long g_ld, g_plane;
-    size_t live, h_planes, w_planes, g, part_h, part_w, total;
+    size_t live, target_logp, h_planes, w_planes, g, part_h, part_w, total;
 };
 
 GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
@@ -142,6 +142,8 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
     const size_t row = (size_t)d * 2 * txl::kMaxPieces;
     g.live = o;
     o = up256(o + (size_t)N * d * elem(dtype));
+    g.target_logp = o;
+    o = up256(o + (size_t)N * 4);
     g.h_planes = o;
     if (dtype == TXL_F32) o = up256(o + N * row);
     g.w_planes = o;
@@ -386,19 +388,25 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     unsigned int *status = txl::device_status_word();
     if (!status) return TXL_ERR_CUDA;
 
-    // h without the rows that have no part, then both operands' bf16 terms
-    txl::LiveRowsParams l{};
+    // h without the rows that have no part, and the targets' log probabilities; then both
+    // operands' bf16 terms
+    txl::GradRowsParams l{};
     l.h = h;
+    l.w = w;
     l.out = ws + g.live;
-    l.ld_bytes = h_stride * elem(dtype);
+    l.target_logp = reinterpret_cast<float *>(ws + g.target_logp);
+    l.h_ld = h_stride;
+    l.w_ld = w_stride;
     l.N = N;
     l.V = V;
-    l.row_bytes = d * elem(dtype);
+    l.d = d;
     l.index_bytes = index_type;
     l.targets = targets;
+    l.lse = lse;
     l.dentropy = dentropy;
+    l.scale = scale;
     l.status = status;
-    cudaError_t e = txl::launch_live_rows(l, st);
+    cudaError_t e = txl::launch_grad_rows(l, dtype == TXL_BF16, st);
     if (dtype == TXL_F32) {
         if (e == cudaSuccess)
             e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), d, N, d,
@@ -419,6 +427,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.targets = targets;
     base.index_bytes = index_type;
     base.lse = lse;
+    base.target_logp = l.target_logp;
     base.entropy = entropy;
     base.dlogp = dlogp;
     base.dentropy = dentropy;
