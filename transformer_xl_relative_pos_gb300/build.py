@@ -26,7 +26,8 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libtxl_gb300_debug.so")
 SOURCES = ["txl_api.cu", "relattn_tc.cu", "relattn_combine.cu", "relattn_decode.cu",
            "relattn_decode_mma.cu", "relattn_f32.cu", "relpos.cu", "mem.cu", "relattn_noalloc.cu",
            "project.cu", "relattn_bwd.cu", "paged.cu", "page_pool.cu",
-           "relattn_tree.cu", "relattn_tree_f32.cu", "embed.cu", "logprob.cu", "vocab_api.cu"]
+           "relattn_tree.cu", "relattn_tree_f32.cu", "embed.cu", "logprob.cu", "logprob_few.cu", "logprob_merge.cu",
+           "vocab_api.cu"]
 HEADERS = [os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "decode.h"),
            os.path.join(CSRC, "decode_common.cuh"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "paged.h"),
            os.path.join(CSRC, "tree_common.cuh"), os.path.join(CSRC, "vocab.h"),

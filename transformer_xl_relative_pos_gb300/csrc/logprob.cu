@@ -36,13 +36,6 @@ constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual align
 constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
 
-// The tensor core's fp32 accumulators cut each addition instead of rounding it, so a sum of
-// `steps` additions (16 products each) comes out too small, on average by 0.2 (terms of random
-// sign) to 0.3 (terms of one sign) times steps * 2^-24 of its value (measured for 4 to 256 steps);
-// results that are fp32 are scaled by the mean of that.  1024 wide: root mean square error 15 to 19
-// times 2^-24 without it, 3 to 9 with it.
-__device__ __forceinline__ float uncut(int steps) { return fmaf((float)steps, 0.27f * 5.9604645e-8f, 1.f); }
-
 static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 
@@ -322,7 +315,7 @@ __global__ void __launch_bounds__(256, 1)
         const int row = wq * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
         constexpr float kLog2e = 1.4426950408889634f;
-        const float zscale = p.scale * uncut(p.kb * (BK / 16)), c2 = zscale * kLog2e;
+        const float zscale = p.scale * uncut_scale(p.kb * (BK / 16)), c2 = zscale * kLog2e;
         bool ok = true;
         int tile = 0;
         for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
@@ -408,7 +401,7 @@ __global__ void __launch_bounds__(256, 1)
                         const long long at = ((long long)s * p.M + m) * p.N + n0 + c;
                         // (cnt is a multiple of 8: rows of the operands are)
                         if (p.part || !p.out_bf16) {
-                            const float f = uncut((w.kb_hi - w.kb_lo) * (BK / 16));
+                            const float f = uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16));
 #pragma unroll
                             for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f);
                             float *dst = (p.part ? p.part : static_cast<float *>(p.out)) + at;
@@ -478,294 +471,6 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmPa
     return cudaGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// joining the vocabulary ranges of a row
-// ---------------------------------------------------------------------------
-
-// a + b exactly as hi + lo (Knuth's two-sum).
-__device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
-{
-    const float s = __fadd_rn(hi, x), bb = __fadd_rn(s, -hi);
-    lo += (hi - (s - bb)) + (x - bb);
-    hi = s;
-}
-
-// h_i . w_j to about 2^-45 of its terms' size, over a warp: products split exactly (a bf16
-// product is an fp32 value; an fp32 one is a product and its rounding error by fma), sums
-// carried with their errors.
-template <bool BF16>
-__device__ double dot_exact(const void *h, const void *w, int d, int lane)
-{
-    float hi = 0.f, lo = 0.f;
-    if (BF16) {
-        const uint4 *a = static_cast<const uint4 *>(h), *b = static_cast<const uint4 *>(w);
-        for (int c = lane; c < d / 8; c += 32) {
-            const uint4 x = __ldg(a + c), y = __ldg(b + c);
-            const uint32_t *xp = &x.x, *yp = &y.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                two_sum(hi, lo, __fmul_rn(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16)));
-                two_sum(hi, lo, __fmul_rn(__uint_as_float(xp[i] & 0xffff0000u),
-                                          __uint_as_float(yp[i] & 0xffff0000u)));
-            }
-        }
-    } else {
-        const float4 *a = static_cast<const float4 *>(h), *b = static_cast<const float4 *>(w);
-        for (int c = lane; c < d / 4; c += 32) {
-            const float4 x = __ldg(a + c), y = __ldg(b + c);
-            const float *xp = &x.x, *yp = &y.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float q = __fmul_rn(xp[i], yp[i]);
-                two_sum(hi, lo, q);
-                lo += fmaf(xp[i], yp[i], -q);
-            }
-        }
-    }
-    double z = (double)hi + (double)lo;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    return z;
-}
-
-constexpr int kMergeWarps = 4;
-constexpr int kLaneLists = kMaxStatSplits / 32;
-
-// One warp per row.
-template <bool BF16, int LIST>
-__global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const MergeParams p)
-{
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-    if (row >= p.N) return;
-    constexpr unsigned FULL = 0xffffffffu;
-    constexpr float kLn2 = 0.6931471805599453f;
-    const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
-    // softmax statistics: lane s holds ranges s, s + 32, ...
-    float4 st[kLaneLists];
-    float m = -INFINITY, zt = 0.f;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < kLaneLists; ++i) {
-        const int s = lane + 32 * i;
-        st[i] = s < p.splits ? p.stats[(long long)s * p.N + row] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        m = fmaxf(m, st[i].x);
-        nan = nan || st[i].y != st[i].y;
-        zt += st[i].w;  // (zero but in the target's range)
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        zt += __shfl_xor_sync(FULL, zt, o);
-    }
-    const float mu = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, es = 0.f;
-#pragma unroll
-    for (int i = 0; i < kLaneLists; ++i) {
-        if (st[i].y == 0.f) continue;
-        const float d = st[i].x - mu, f = exp2f(d);
-        sum += st[i].y * f;
-        es += (st[i].z + st[i].y * d) * f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(FULL, sum, o);
-        es += __shfl_xor_sync(FULL, es, o);
-    }
-    if (__any_sync(FULL, nan)) sum = __int_as_float(0x7fffffff);
-    // A logit known more exactly (log2 units) takes its place in the sums; peaked rows, whose
-    // sums are a few such terms, are as exact as these.
-    auto replace = [&](float was, double is) {
-        const float d0 = was - mu, d1 = (float)(is - (double)mu);
-        const float e0 = ex2(d0), e1 = exp2f(d1);
-        sum += e1 - e0;
-        es += e1 * d1 - e0 * d0;
-    };
-    constexpr double kLog2e = 1.4426950408889634;
-    const int esize = BF16 ? 2 : 4;
-    const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
-    auto logit = [&](int id) {
-        return dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane) *
-               (double)p.scale;
-    };
-    double z_target = (double)zt * kLn2;
-    bool replaced = true;  // the target's logit in the sums
-    if (target >= 0) {
-        const double e = logit(target);
-        if (isfinite(e) && isfinite(zt)) {
-            z_target = e;
-            replaced = false;
-        }
-    }
-    auto finish = [&]() -> double {
-        if (!replaced) replace(zt, z_target * kLog2e);
-        const float l = logf(sum);
-        const double lse = (double)m * 0.6931471805599453 + (double)l;
-        if (lane == 0) {
-            if (p.logp) p.logp[row] = target >= 0 ? (float)(z_target - lse) : 0.f;
-            if (p.lse) p.lse[row] = (float)lse;
-            if (p.entropy) p.entropy[row] = l - es / sum * kLn2;
-        }
-        return lse;
-    };
-    if (LIST == 0) {
-        finish();
-        return;
-    }
-    // the largest LIST of all ranges: rounds over the lists' heads
-    float head[kLaneLists];
-    int head_id[kLaneLists], taken[kLaneLists] = {};
-    auto load_head = [&](int i) {
-        const int s = lane + 32 * i;
-        head[i] = -INFINITY;
-        head_id[i] = -1;
-        if (s < p.splits && taken[i] < LIST) {
-            const long long at = ((long long)s * LIST + taken[i]) * p.N + row;
-            head_id[i] = p.list_id[at];
-            if (head_id[i] >= 0) head[i] = p.list_val[at];
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < kLaneLists; ++i) load_head(i);
-    const int want = min(p.top + kSpareTop, LIST);
-    float my_val = 0.f;   // candidate of lane c
-    int my_id = -1;
-    for (int c = 0; c < want; ++c) {
-        float v = -INFINITY;
-        int id = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < kLaneLists; ++i)
-            if (head_id[i] >= 0 && (head[i] > v || (head[i] == v && head_id[i] < id))) {
-                v = head[i];
-                id = head_id[i];
-            }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(FULL, v, o);
-            const int oid = __shfl_xor_sync(FULL, id, o);
-            if (ov > v || (ov == v && oid < id)) {
-                v = ov;
-                id = oid;
-            }
-        }
-        if (id == 0x7fffffff) break;
-        if (lane == c) {
-            my_val = v;
-            my_id = id;
-        }
-#pragma unroll
-        for (int i = 0; i < kLaneLists; ++i)
-            if (head_id[i] == id) {
-                ++taken[i];
-                load_head(i);
-            }
-    }
-    // their exact order
-    double z = (double)my_val * 0.6931471805599453;
-    for (int c = 0; c < want; ++c) {
-        const int id = __shfl_sync(FULL, my_id, c);
-        const float was = __shfl_sync(FULL, my_val, c);
-        if (id < 0) break;
-        const double e = id == target ? z_target : logit(id);
-        if (!isfinite(e) || !isfinite(was)) continue;
-        if (lane == c) z = e;
-        if (id == target) replaced = true;
-        replace(was, e * kLog2e);
-    }
-    const double lse = finish();
-    int rank = 0;
-    for (int c = 0; c < want; ++c) {
-        const double oz = __shfl_sync(FULL, z, c);
-        const int oid = __shfl_sync(FULL, my_id, c);
-        if (oid >= 0 && (oz > z || (oz == z && oid < my_id))) ++rank;
-    }
-    const int found = __popc(__ballot_sync(FULL, my_id >= 0));
-    if (my_id >= 0 && rank < p.top) {
-        p.top_ids[(long long)row * p.top + rank] = my_id;
-        p.top_logp[(long long)row * p.top + rank] = (float)(z - lse);
-    }
-    if (lane >= found && lane < p.top) {  // fewer numbers than places
-        p.top_ids[(long long)row * p.top + lane] = -1;
-        p.top_logp[(long long)row * p.top + lane] = __int_as_float(0x7fffffff);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// small passes
-// ---------------------------------------------------------------------------
-
-template <bool BF16>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float4 *part, int parts, long long vecs,
-                                                        void *out)
-{
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= vecs) return;
-    float4 a = __ldcs(part + i);
-    for (int s = 1; s < parts; ++s) {
-        const float4 b = __ldcs(part + s * vecs + i);
-        a.x += b.x;
-        a.y += b.y;
-        a.z += b.z;
-        a.w += b.w;
-    }
-    if (BF16)
-        reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-    else
-        reinterpret_cast<float4 *>(out)[i] = a;
-}
-
-// x = t0 + t1 + t2, each the bf16 nearest to what is left (exact but for what falls below
-// bf16's range).  An infinite or NaN value is its first term; a finite one that rounds to
-// infinity is cut instead.
-__global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long long ld, int rows, int d,
-                                                        __nv_bfloat16 *planes)
-{
-    const long long pairs = (long long)rows * (d / 2);
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= pairs) return;
-    const int r = (int)(i / (d / 2)), c = (int)(i - (long long)r * (d / 2)) * 2;
-    const float2 v = *reinterpret_cast<const float2 *>(x + r * ld + c);
-    float a = v.x, b = v.y;
-    for (int t = 0; t < kMaxPieces; ++t) {
-        auto term = [](float y) {
-            const __nv_bfloat16 n = __float2bfloat16_rn(y);
-            return __hisinf(n) && !isinf(y) ? __float2bfloat16_rz(y) : n;
-        };
-        const __nv_bfloat16 ta = term(a), tb = term(b);
-        __nv_bfloat162 o;
-        o.x = ta;
-        o.y = tb;
-        *reinterpret_cast<__nv_bfloat162 *>(planes + ((long long)t * rows + r) * d + c) = o;
-        a = isfinite(a) ? a - __bfloat162float(ta) : 0.f;
-        b = isfinite(b) ? b - __bfloat162float(tb) : 0.f;
-    }
-}
-
-// One warp per row: a copy of h with zeros in rows that have no part in the gradient (whatever
-// those hold), and the log probability of the row's target from its logit's products carried
-// beyond fp32: G's one large element is the difference of 1 and that probability.
-template <bool BF16>
-__global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p)
-{
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-    if (row >= p.N) return;
-    constexpr int ESIZE = BF16 ? 2 : 4;
-    const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
-    const bool live = target >= 0 || (p.dentropy && p.dentropy[row] != 0.f);
-    const int vecs = p.d * ESIZE / 16;
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.h) + row * p.h_ld * ESIZE);
-    uint4 *dst = static_cast<uint4 *>(p.out) + (long long)row * vecs;
-    for (int c = lane; c < vecs; c += 32) dst[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-    if (target < 0) {
-        if (lane == 0) p.target_logp[row] = 0.f;
-        return;
-    }
-    const double z = dot_exact<BF16>(src, static_cast<const char *>(p.w) + target * p.w_ld * ESIZE, p.d, lane) *
-                     (double)p.scale;
-    if (lane == 0) p.target_logp[row] = (float)(z - (double)p.lse[row]);
-}
-
 } // namespace
 
 cudaError_t launch_logprob_stats(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
@@ -791,48 +496,6 @@ cudaError_t launch_product_dw(const CUtensorMap &a, const CUtensorMap &b, const 
                               cudaStream_t s)
 {
     return launch_gemm<kDw, 0>(a, b, p, s);
-}
-
-cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void *out, bool bf16,
-                             cudaStream_t s)
-{
-    const long long vecs = elems / 4;
-    const unsigned grid = (unsigned)((vecs + 255) / 256);
-    if (bf16) sum_parts_kernel<true><<<grid, 256, 0, s>>>(reinterpret_cast<const float4 *>(part), parts, vecs, out);
-    else sum_parts_kernel<false><<<grid, 256, 0, s>>>(reinterpret_cast<const float4 *>(part), parts, vecs, out);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             cudaStream_t s)
-{
-    const long long pairs = (long long)rows * (d / 2);
-    split_f32_kernel<<<(unsigned)((pairs + 255) / 256), 256, 0, s>>>(x, ld, rows, d, planes);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
-{
-    const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
-    if (bf16) grad_rows_kernel<true><<<grid, kMergeWarps * 32, 0, s>>>(p);
-    else grad_rows_kernel<false><<<grid, kMergeWarps * 32, 0, s>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_logprob_merge(const MergeParams &p, bool bf16, cudaStream_t s)
-{
-    const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
-    const int threads = kMergeWarps * 32;
-    if (bf16) {
-        if (p.list == 0) logprob_merge_kernel<true, 0><<<grid, threads, 0, s>>>(p);
-        else if (p.list == 12) logprob_merge_kernel<true, 12><<<grid, threads, 0, s>>>(p);
-        else logprob_merge_kernel<true, 20><<<grid, threads, 0, s>>>(p);
-    } else {
-        if (p.list == 0) logprob_merge_kernel<false, 0><<<grid, threads, 0, s>>>(p);
-        else if (p.list == 12) logprob_merge_kernel<false, 12><<<grid, threads, 0, s>>>(p);
-        else logprob_merge_kernel<false, 20><<<grid, threads, 0, s>>>(p);
-    }
-    return cudaGetLastError();
 }
 
 } // namespace txl

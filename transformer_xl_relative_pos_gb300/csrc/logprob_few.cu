@@ -1,0 +1,314 @@
+// Statistics of the logits of a few states (up to kFewRows): decoding steps, drafted trees.
+//
+// The table is what such a call reads; it streams through a ring of TMA copies as the A
+// operand of tcgen05 (128 vocabulary rows a tile), the states are the B operand (bn of them,
+// from L2 again for every tile), so that a tile of logits has its vocabulary in TMEM's lanes
+// and the states in its columns.  The epilogue's warps turn 64 columns at a time through
+// shared memory; each warp then owns eight states, four logits a lane, and every lane keeps the
+// statistics of the logits it has seen.  For the largest logits only the maximum of each four is
+// written; logprob_few_merge finds them among those.  Bound by the table's bytes.
+//   warp 0      TMA producer
+//   warp 1      MMA issuer
+//   warp 2      TMEM allocator
+//   warps 4-11  epilogue
+#include "vocab.h"
+#include "ptx.cuh"
+
+namespace txl {
+namespace {
+
+using namespace ptx;
+
+constexpr int BM = 128, BK = 64, MAX_NS = 10;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int RING = 184 * 1024;
+constexpr int TURN_LD = BM + 4;                      // floats of a state's logits
+constexpr int OFF_TURN = RING;                       // [64][TURN_LD]
+constexpr int OFF_TARGET = OFF_TURN + 64 * TURN_LD * 4;
+constexpr int OFF_BAR = OFF_TARGET + kFewRows * 4;
+constexpr int N_BAR = 2 * MAX_NS + 4;
+constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // (slack for the manual alignment)
+constexpr uint32_t TM_COLS = 512;
+constexpr int ACC = 256;                             // columns of an accumulator
+constexpr int kEpiWarps = 8;
+
+static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
+static_assert(kFewRows <= ACC, "states lie in an accumulator's columns");
+
+__device__ __forceinline__ void epi_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+}
+
+// Whether any thread of the epilogue says so; a barrier of its warps.
+__device__ __forceinline__ bool epi_any(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred b, 1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "n"(kEpiWarps * 32)
+                 : "memory");
+    return r != 0;
+}
+
+template <int GROUPS>
+__global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
+    logprob_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
+                       const GemmParams p, int ns)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stage_bytes = A_BYTES + p.bn * BK * 2;
+    // this block's tiles of the vocabulary
+    const int t_lo = (int)((long long)blockIdx.x * p.nb / p.splits);
+    const int t_hi = (int)((long long)(blockIdx.x + 1) * p.nb / p.splits);
+
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+    uint64_t *empty = full + MAX_NS;
+    uint64_t *acc_full = empty + MAX_NS;
+    uint64_t *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ns; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + s, 1);
+            mbar_init(acc_empty + s, kEpiWarps * 32);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, TM_COLS);
+        tmem_relinquish();
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint64_t wait_ns = p.wait_ns;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tensormap(&tm_w);
+            prefetch_tensormap(&tm_h);
+            const uint64_t once = policy_evict_first(), often = policy_evict_last();
+            bool ok = true;
+            int it = 0;
+            for (int t = t_lo; t < t_hi && ok; ++t)
+                for (int pr = 0; pr < p.n_pairs && ok; ++pr) {
+                    // (pairs are given as terms of h by terms of w)
+                    const int ph = (p.pair_a >> (4 * pr)) & 15, pw = (p.pair_b >> (4 * pr)) & 15;
+                    for (int kb = 0; kb < p.kb; ++kb) {
+                        const int s = it % ns;
+                        if (!(ok = mbar_wait(empty + s, ((it / ns) & 1) ^ 1, abort_flag, wait_ns))) break;
+                        uint8_t *st = smem + s * stage_bytes;
+                        mbar_arrive_expect_tx(full + s, stage_bytes);
+                        tma_load_3d_hint(st, &tm_w, full + s, kb * BK, t * BM, pw, once);
+                        tma_load_3d_hint(st + A_BYTES, &tm_h, full + s, kb * BK, 0, ph, often);
+                        ++it;
+                    }
+                }
+            if (!ok) {
+                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+                *abort_flag = 1;
+                const int zero = 0;
+                for (int i = max(0, it - ns); i < it; ++i)
+                    mbar_wait(full + i % ns, (i / ns) & 1, &zero, wait_ns);
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t ID = idesc_bf16_f32(BM, p.bn, false);
+        auto elect = []() -> bool {
+            uint32_t el;
+            asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+                         : "=r"(el));
+            return el != 0;
+        };
+        const uint64_t dA = sdesc_sw128(smem_u32(smem)), dB = sdesc_sw128(smem_u32(smem + A_BYTES));
+        const int steps = p.n_pairs * p.kb;
+        bool ok = true;
+        int it = 0, tile = 0;
+        for (int t = t_lo; t < t_hi; ++t) {
+            const int buf = tile & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile >> 1) & 1) ^ 1, abort_flag, wait_ns));
+            if (!ok) break;
+            tc_fence_after_sync();
+            for (int k = 0; k < steps; ++k, ++it) {
+                const int s = it % ns;
+                ok = __all_sync(0xffffffffu, mbar_wait(full + s, (it / ns) & 1, abort_flag, wait_ns));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t off = (uint64_t)((s * stage_bytes) >> 4);
+                if (elect()) {
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        mma_bf16_ss(tmem + buf * ACC, dA + off + kk * 2, dB + off + kk * 2, ID,
+                                    (k > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(empty + s);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (elect()) mma_commit(acc_full + buf);
+            __syncwarp();
+            ++tile;
+        }
+        if (!ok) {
+            if (lane == 0) {
+                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (elect()) mma_commit(acc_full + (tile & 1));
+            __syncwarp();
+            const int zero = 0;
+            mbar_wait(acc_full + (tile & 1), (tile >> 1) & 1, &zero, wait_ns);
+        }
+    } else if (warp >= 4) {
+        constexpr unsigned FULL = 0xffffffffu;
+        const int we = warp - 4, quarter = we & 3, half = we >> 2;
+        float *turn = reinterpret_cast<float *>(smem + OFF_TURN);
+        int *targets = reinterpret_cast<int *>(smem + OFF_TARGET);
+        const float c2 = p.scale * uncut_scale(p.kb * (BK / 16)) * 1.4426950408889634f;
+        for (int i = threadIdx.x - 128; i < p.M; i += kEpiWarps * 32)
+            targets[i] = p.targets ? token_at(p.targets, p.index_bytes, i, p.V, p.status) : -1;
+        // running statistics of this lane's logits of state 64 g + 8 we + j
+        float m[GROUPS * 8], sum[GROUPS * 8], es[GROUPS * 8];
+#pragma unroll
+        for (int i = 0; i < GROUPS * 8; ++i) {
+            m[i] = -INFINITY;
+            sum[i] = es[i] = 0.f;
+        }
+        bool ok = true;
+        int tile = 0;
+        for (int t = t_lo; t < t_hi; ++t, ++tile) {
+            const int buf = tile & 1;
+            ok = __all_sync(FULL, mbar_wait(acc_full + buf, (tile >> 1) & 1, abort_flag, wait_ns) && !*abort_flag);
+            // (all warps of the epilogue meet at its barriers: they leave together)
+            if (epi_any(!ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const int id0 = t * BM + lane * 4, left = p.N - id0;  // (p.N: the vocabulary)
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const int c = g * 64 + half * 32;
+                if (c < p.M) {
+                    uint32_t raw[32];
+                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * ACC + c, raw);
+                    tmem_ld_wait(raw);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        turn[(half * 32 + i) * TURN_LD + quarter * 32 + lane] = __uint_as_float(raw[i]);
+                }
+                if (g + 1 == GROUPS) {
+                    tc_fence_before_sync();
+                    mbar_arrive(acc_empty + buf);
+                }
+                epi_sync();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int st = g * 64 + we * 8 + j, k = g * 8 + j;
+                    if (st >= p.M) break;
+                    const float4 z = *reinterpret_cast<const float4 *>(turn + (we * 8 + j) * TURN_LD + lane * 4);
+                    float v[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = i < left ? fmaf(v[i], c2, 0.f) : -INFINITY;
+                    const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                    const float m_new = fmaxf(m[k], top);
+                    const float mu = m_new == -INFINITY ? 0.f : m_new;
+                    const float diff = m[k] - mu, f = ex2(diff);  // (-inf before the first number)
+                    // (sums of zero stay so: not zero times infinity)
+                    float s_new = sum[k] * f, e_new = sum[k] == 0.f ? 0.f : (es[k] + sum[k] * diff) * f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float d = v[i] - mu, e = ex2(d);
+                        s_new += e;
+                        e_new = fmaf(e, fmaxf(d, -1e30f), e_new);
+                    }
+                    m[k] = m_new;
+                    sum[k] = s_new;
+                    es[k] = e_new;
+                    if (p.group_key) {
+                        // the largest of the lane's four: NaN has no place in the order
+                        const bool any = (v[0] == v[0] && left > 0) || (v[1] == v[1] && left > 1) ||
+                                         (v[2] == v[2] && left > 2) || (v[3] == v[3] && left > 3);
+                        p.group_key[((long long)st * p.nb + t) * 32 + lane] = any ? order_key(top) : 0u;
+                    }
+                    const int at = targets[st] - id0;
+                    if ((unsigned)at < 4u)
+                        p.target_z[st] = at & 2 ? (at & 1 ? v[3] : v[2]) : (at & 1 ? v[1] : v[0]);
+                }
+                epi_sync();  // (the buffer is free again)
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.status, TXL_STATUS_TIMEOUT);
+            *abort_flag = 1;
+        }
+        if (ok) {
+#pragma unroll
+            for (int k = 0; k < GROUPS * 8; ++k) {
+                const int st = (k >> 3) * 64 + we * 8 + (k & 7);
+                float top = m[k];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                const float mu = top == -INFINITY ? 0.f : top;
+                const float d = m[k] - mu, f = ex2(d);
+                float s = sum[k] * f, e = sum[k] == 0.f ? 0.f : (es[k] + sum[k] * d) * f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    s += __shfl_xor_sync(FULL, s, o);
+                    e += __shfl_xor_sync(FULL, e, o);
+                }
+                if (lane == 0 && st < p.M)
+                    p.stats[(long long)blockIdx.x * p.M + st] = make_float4(top, s, e, 0.f);
+            }
+        }
+        tc_fence_before_sync();
+    }
+
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, TM_COLS);
+    }
+}
+
+template <int GROUPS>
+cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p, cudaStream_t s)
+{
+    static bool attr_set[64] = {};  // the attribute is set once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(logprob_few_kernel<GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const int ns = min(MAX_NS, RING / (A_BYTES + p.bn * BK * 2));
+    logprob_few_kernel<GROUPS><<<(unsigned)p.splits, (4 + kEpiWarps) * 32, SMEM_BYTES, s>>>(tm_w, tm_h, p, ns);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p,
+                               cudaStream_t s)
+{
+    const int groups = (p.M + 63) / 64;
+    if (groups == 1) return launch<1>(tm_w, tm_h, p, s);
+    return groups == 2 ? launch<2>(tm_w, tm_h, p, s) : launch<4>(tm_w, tm_h, p, s);
+}
+
+} // namespace txl

@@ -71,10 +71,30 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16,
 constexpr int kMaxTop = 16;      // alternatives of a row
 constexpr int kSpareTop = 4;     // candidates kept beyond them, for the exact order
 constexpr int kMaxStatSplits = 160;  // vocabulary ranges of a row
+constexpr int kMaxRowSplits = 64;    // ... of more than kFewRows rows
+constexpr int kFewRows = 256;    // states up to which the vocabulary takes the tiles' rows
 constexpr int kMaxPieces = 3;    // bf16 terms of an fp32 operand
 
 // Candidates kept per row and vocabulary range for `top` alternatives.
 constexpr int list_length(int top) { return top == 0 ? 0 : top <= 8 ? 12 : 20; }
+
+// The tensor core's fp32 accumulators cut each addition instead of rounding it, so a sum of
+// `steps` additions (16 products each) comes out too small, on average by 0.2 (terms of random
+// sign) to 0.3 (terms of one sign) times steps * 2^-24 of its value (measured for 4 to 256 steps);
+// results that are fp32 are scaled by the mean of that.  1024 wide: root mean square error 15 to 19
+// times 2^-24 without it, 3 to 9 with it.
+__device__ __forceinline__ float uncut_scale(int steps) { return fmaf((float)steps, 0.27f * 5.9604645e-8f, 1.f); }
+
+// Order of floats as unsigned integers; 0 is below every number (NaN has none).
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 
 // One GEMM over 128 x bn tiles, bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
 // Which operands, and what becomes of a tile, is the kernel's mode.
@@ -97,6 +117,8 @@ struct GemmParams {
     float4 *stats;         // [splits][M]: maximum, sum, weighted sum (log2 units), target's logit
     float *list_val;       // [splits][list][M]
     int *list_id;
+    unsigned *group_key;   // few states: [M][nb][32] order of the largest of four logits, or null
+    float *target_z;       // few states: [M], log2 units (where there is a target)
     const float *lse, *entropy, *dlogp, *dentropy;  // (the last two may be null)
     const float *target_logp;
     __nv_bfloat16 *g;      // [g_pieces][M][g_ld]
@@ -110,6 +132,10 @@ struct GemmParams {
 
 cudaError_t launch_logprob_stats(const CUtensorMap &tm_h, const CUtensorMap &tm_w,
                                  const GemmParams &p, int list, cudaStream_t s);
+// The same for M <= kFewRows states: tiles of 128 vocabulary rows (nb of them, bn states wide),
+// `splits` blocks.
+cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p,
+                               cudaStream_t s);
 cudaError_t launch_logprob_grad(const CUtensorMap &tm_h, const CUtensorMap &tm_w,
                                 const GemmParams &p, cudaStream_t s);
 // dh = G W (G rows of the vocabulary) and dW = G^T h (contraction over the rows).
@@ -141,6 +167,9 @@ struct MergeParams {
     const float4 *stats;
     const float *list_val;
     const int *list_id;
+    const unsigned *group_key;
+    const float *target_z;
+    int nb;                // vocabulary tiles of 128
     int splits, N, V, d, top, list;
     const void *h, *w;
     long long h_ld, w_ld;
@@ -151,6 +180,7 @@ struct MergeParams {
     int *top_ids;
     unsigned int *status;
 };
+cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_logprob_merge(const MergeParams &p, bool bf16, cudaStream_t s);
 
 } // namespace txl

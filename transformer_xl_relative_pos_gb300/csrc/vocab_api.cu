@@ -79,18 +79,26 @@ int choose_parts(long long units, int steps, int most, double extra)
 }
 
 struct StatsPlan {
+    bool few;                     // the vocabulary in the tiles' rows
     int mb, nb, bn, splits, list;
-    size_t h_planes, w_planes, stats, val, id, total;  // offsets
+    size_t h_planes, w_planes, stats, val, id, keys, target_z, total;  // offsets
 };
 
 StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
 {
     StatsPlan s{};
-    s.mb = ceil_div(N, 128);
-    s.bn = tile_columns(V);
-    if (s.bn < 256 && V > 256) s.bn = 256;
-    s.nb = ceil_div(V, s.bn);
-    s.splits = choose_parts(s.mb, s.nb, txl::kMaxStatSplits, 0.5);
+    s.few = N <= txl::kFewRows;
+    if (s.few) {
+        s.mb = 1;
+        s.bn = std::max(16, ceil_div(N, 16) * 16);
+        s.nb = ceil_div(V, 128);
+        s.splits = std::min(s.nb, std::min(txl::device_sm_count(), txl::kMaxStatSplits));
+    } else {
+        s.mb = ceil_div(N, 128);
+        s.bn = std::min<long long>(256, up64(V));
+        s.nb = ceil_div(V, s.bn);
+        s.splits = choose_parts(s.mb, s.nb, txl::kMaxRowSplits, 0.5);
+    }
     s.list = txl::list_length(top);
     size_t o = 0;
     const size_t row = (size_t)d * 2 * txl::kMaxPieces;
@@ -100,10 +108,15 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     if (dtype == TXL_F32) o = up256(o + V * row);
     s.stats = o;
     o = up256(o + (size_t)s.splits * N * sizeof(float4));
+    const size_t lists = s.few ? 0 : (size_t)s.splits * s.list * N * 4;
     s.val = o;
-    o = up256(o + (size_t)s.splits * s.list * N * 4);
+    o = up256(o + lists);
     s.id = o;
-    s.total = up256(o + (size_t)s.splits * s.list * N * 4);
+    o = up256(o + lists);
+    s.keys = o;
+    if (s.few && top > 0) o = up256(o + (size_t)N * s.nb * 32 * 4);
+    s.target_z = o;
+    s.total = s.few ? up256(o + (size_t)N * 4) : o;
     return s;
 }
 
@@ -304,7 +317,9 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
     CUtensorMap tm_h, tm_w;
-    if (!map_of(&tm_h, oh, N, d, 128) || !map_of(&tm_w, ow, V, d, (unsigned)s.bn)) return TXL_ERR_CUDA;
+    if (!map_of(&tm_h, oh, N, d, s.few ? (unsigned)s.bn : 128u) ||
+        !map_of(&tm_w, ow, V, d, s.few ? 128u : (unsigned)s.bn))
+        return TXL_ERR_CUDA;
     GemmParams p{};
     p.M = N;
     p.N = V;
@@ -324,12 +339,19 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.stats = reinterpret_cast<float4 *>(ws + s.stats);
     p.list_val = reinterpret_cast<float *>(ws + s.val);
     p.list_id = reinterpret_cast<int *>(ws + s.id);
-    if (txl::launch_logprob_stats(tm_h, tm_w, p, s.list, st) != cudaSuccess) return TXL_ERR_CUDA;
+    p.group_key = top > 0 ? reinterpret_cast<unsigned *>(ws + s.keys) : nullptr;
+    p.target_z = reinterpret_cast<float *>(ws + s.target_z);
+    if ((s.few ? txl::launch_logprob_few(tm_w, tm_h, p, st)
+               : txl::launch_logprob_stats(tm_h, tm_w, p, s.list, st)) != cudaSuccess)
+        return TXL_ERR_CUDA;
 
     txl::MergeParams m{};
     m.stats = p.stats;
     m.list_val = p.list_val;
     m.list_id = p.list_id;
+    m.group_key = p.group_key;
+    m.target_z = p.target_z;
+    m.nb = s.nb;
     m.splits = s.splits;
     m.N = N;
     m.V = V;
@@ -349,7 +371,8 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     m.top_logp = top_logp;
     m.top_ids = top_ids;
     m.status = status;
-    return status_of(txl::launch_logprob_merge(m, dtype == TXL_BF16, st));
+    return status_of(s.few ? txl::launch_logprob_few_merge(m, dtype == TXL_BF16, st)
+                           : txl::launch_logprob_merge(m, dtype == TXL_BF16, st));
 }
 
 size_t txl_logprob_bwd_workspace_size(int N, int V, int d, int dtype, int grad_dtype)
