@@ -12,7 +12,12 @@ using namespace ptx;
 // joining the vocabulary ranges of a row
 // ---------------------------------------------------------------------------
 
-// a + b exactly as hi + lo (Knuth's two-sum).
+// A number as hi + lo, |lo| at most half a unit of hi's last place.
+struct Wide {
+    float hi, lo;
+};
+
+// hi + lo + x, the sum of hi and x exactly (Knuth's two-sum).
 __device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
 {
     const float s = __fadd_rn(hi, x), bb = __fadd_rn(s, -hi);
@@ -22,11 +27,12 @@ __device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
 
 // h_i . w_j to about 2^-45 of its terms' size, over a warp: products split exactly (a bf16
 // product is an fp32 value; an fp32 one is a product and its rounding error by fma), sums
-// carried with their errors, four chains a lane.  Where that is no number, the plain sum.
+// carried with their errors, four chains a lane.  Where that is no number, the plain sum.  (All in
+// fp32: the fp64 units give one result where the fp32 ones give 64.)
 template <bool BF16>
-__device__ double dot_exact(const void *h, const void *w, int d, int lane)
+__device__ Wide dot_exact(const void *h, const void *w, int d, int lane)
 {
-    float hi[4] = {}, lo[4] = {}, plain = 0.f;
+    float hi[4] = {}, lo[4] = {};
     if (BF16) {
         const uint4 *a = static_cast<const uint4 *>(h), *b = static_cast<const uint4 *>(w);
 #pragma unroll 4
@@ -35,12 +41,9 @@ __device__ double dot_exact(const void *h, const void *w, int d, int lane)
             const uint32_t xp[4] = {x.x, x.y, x.z, x.w}, yp[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float q0 = __fmul_rn(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16));
-                const float q1 = __fmul_rn(__uint_as_float(xp[i] & 0xffff0000u),
-                                           __uint_as_float(yp[i] & 0xffff0000u));
-                two_sum(hi[i], lo[i], q0);
-                two_sum(hi[i], lo[i], q1);
-                plain += q0 + q1;
+                two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16)));
+                two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(xp[i] & 0xffff0000u),
+                                                __uint_as_float(yp[i] & 0xffff0000u)));
             }
         }
     } else {
@@ -54,7 +57,6 @@ __device__ double dot_exact(const void *h, const void *w, int d, int lane)
                 const float q = __fmul_rn(xp[i], yp[i]);
                 two_sum(hi[i], lo[i], q);
                 lo[i] += fmaf(xp[i], yp[i], -q);
-                plain += q;
             }
         }
     }
@@ -63,15 +65,35 @@ __device__ double dot_exact(const void *h, const void *w, int d, int lane)
         two_sum(hi[0], lo[0], hi[i]);
         lo[0] += lo[i];
     }
-    double z = (double)hi[0] + (double)lo[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (!isfinite(z)) {
+    for (int o = 16; o > 0; o >>= 1) {
+        const float ohi = __shfl_xor_sync(0xffffffffu, hi[0], o), olo = __shfl_xor_sync(0xffffffffu, lo[0], o);
+        two_sum(hi[0], lo[0], ohi);
+        lo[0] += olo;
+    }
+    Wide z{__fadd_rn(hi[0], lo[0]), 0.f};
+    z.lo = lo[0] - __fadd_rn(z.hi, -hi[0]);
+    if (!isfinite(z.hi)) {
+        float plain = 0.f;
+        for (int c = lane; c < d; c += 32)
+            plain += BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(h)[c]) *
+                                __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c])
+                          : static_cast<const float *>(h)[c] * static_cast<const float *>(w)[c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) plain += __shfl_xor_sync(0xffffffffu, plain, o);
-        z = plain;
+        z = {plain, 0.f};
     }
     return z;
+}
+
+// Order of scale * z as integers, 0 for no number: by the product's sign (the scale only
+// stretches it).
+__device__ __forceinline__ unsigned long long wide_key(Wide z, float scale)
+{
+    if (!(z.hi * scale == z.hi * scale)) return 0ull;
+    if (scale == 0.f) return 1ull;
+    const float s = scale < 0.f ? -1.f : 1.f;
+    return (unsigned long long)order_key(z.hi * s + 0.f) << 32 | order_key(isfinite(z.hi) ? z.lo * s + 0.f : 0.f);
 }
 
 constexpr int kMergeWarps = 4;
@@ -120,28 +142,35 @@ __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int
     return r;
 }
 
-// A logit known more exactly (log2 units) takes its place in the sums: peaked rows, whose sums
-// are a few such terms, are as exact as these.
-__device__ __forceinline__ void replace_term(float mu, float was, double is, float &ds, float &de)
+// scale * z in log2 units less mu.
+__device__ __forceinline__ float above(const MergeParams &p, Wide z, float mu)
 {
-    const float d0 = was - mu, d1 = (float)(is - (double)mu);
+    return fmaf(z.hi, p.c_hi, -mu) + fmaf(z.hi, p.c_lo, z.lo * p.c_hi);
+}
+
+// A logit known more exactly (d1 above mu) takes its place in the sums: peaked rows, whose sums
+// are a few such terms, are as exact as these.
+__device__ __forceinline__ void replace_term(float mu, float was, float d1, float &ds, float &de)
+{
+    const float d0 = was - mu;
     const float e0 = ex2(d0), e1 = exp2f(d1);
     ds = e1 - e0;
     de = e1 * d1 - e0 * d0;
 }
 
-// Row outputs from the sums (one thread); returns lse.
-__device__ __forceinline__ double row_outputs(const MergeParams &p, int row, const RowSums &r, int target,
-                                              double z_target, bool write)
+// Row outputs from the sums; d_target: the target's logit above mu (log2 units).  Returns
+// log(sum): a log probability is its logit above mu, times ln 2, less that.
+__device__ __forceinline__ float row_outputs(const MergeParams &p, int row, const RowSums &r, int target,
+                                             float d_target, bool write)
 {
     const float l = logf(r.sum);
-    const double lse = (double)r.m * 0.6931471805599453 + (double)l;
     if (write) {
-        if (p.logp) p.logp[row] = target >= 0 ? (float)(z_target - lse) : 0.f;
-        if (p.lse) p.lse[row] = (float)lse;
+        if (p.logp) p.logp[row] = target >= 0 ? fmaf(d_target, kLn2, -l) : 0.f;
+        // (ln 2 to fp64; a maximum of -infinity stands for itself)
+        if (p.lse) p.lse[row] = fmaf(r.m, kLn2, r.m > -INFINITY ? fmaf(r.m, -1.9046542e-9f, l) : l);
         if (p.entropy) p.entropy[row] = l - r.es / r.sum * kLn2;
     }
-    return lse;
+    return l;
 }
 
 // Rows of the statistics kernel: one warp each.  Its ranges' lists are two a lane.
@@ -156,9 +185,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
     const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
     const int esize = BF16 ? 2 : 4;
     const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
-    auto logit = [&](int id) {
-        return dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane) *
-               (double)p.scale;
+    auto exact = [&](int id) {
+        return dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane);
     };
     // the largest of all ranges, from the heads of their lists
     const int want = LIST > 0 ? min(p.top + kSpareTop, LIST) : 0;
@@ -209,28 +237,33 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
     const int found = __popc(__ballot_sync(FULL, my_id >= 0));
     // exact logits of the candidates, and of the target where it is none of them
     RowSums r = join_stats<PER>(p, row, lane);
-    double z = (double)my_val * kLn2, z_target = (double)r.zt * kLn2;
+    float d_mine = my_val - r.mu, d_target = r.zt - r.mu;
+    unsigned long long order = my_id >= 0 ? (unsigned long long)order_key(my_val) << 32 : 0ull;
     float ds = 0.f, de = 0.f;
     bool listed = false;
     for (int c = 0; c < found; ++c) {
         const int id = __shfl_sync(FULL, my_id, c);
-        const double e = logit(id);
-        if (lane == c && isfinite(e) && isfinite(my_val)) {
-            z = e;
-            replace_term(r.mu, my_val, e * 1.4426950408889634, ds, de);
+        const Wide e = exact(id);
+        if (lane == c) {
+            // (beside infinite ones the rounded logit orders as well)
+            const unsigned long long k = wide_key(e, p.scale);
+            if (k) order = k;
+            if (isfinite(e.hi) && isfinite(my_val)) {
+                d_mine = above(p, e, r.mu);
+                replace_term(r.mu, my_val, d_mine, ds, de);
+            }
         }
         if (id == target) {
             listed = true;
-            z_target = __shfl_sync(FULL, z, c);
+            d_target = __shfl_sync(FULL, d_mine, c);
         }
     }
     if (target >= 0 && !listed) {
-        const double e = logit(target);
-        if (isfinite(e) && isfinite(r.zt)) {
-            z_target = e;
-            if (lane == 31) {   // (found is below 32: this lane has no candidate)
-                replace_term(r.mu, r.zt, e * 1.4426950408889634, ds, de);
-            }
+        const Wide e = exact(target);
+        if (isfinite(e.hi) && isfinite(r.zt)) {
+            d_target = above(p, e, r.mu);
+            // (found is below 32: this lane has no candidate)
+            if (lane == 31) replace_term(r.mu, r.zt, d_target, ds, de);
         }
     }
 #pragma unroll
@@ -240,17 +273,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
     }
     r.sum += ds;
     r.es += de;
-    const double lse = row_outputs(p, row, r, target, z_target, lane == 0);
+    const float l = row_outputs(p, row, r, target, d_target, lane == 0);
     if (LIST == 0) return;
     int rank = 0;
     for (int c = 0; c < found; ++c) {
-        const double oz = __shfl_sync(FULL, z, c);
+        const unsigned long long other = __shfl_sync(FULL, order, c);
         const int oid = __shfl_sync(FULL, my_id, c);
-        if (oz > z || (oz == z && oid < my_id)) ++rank;
+        if (other > order || (other == order && oid < my_id)) ++rank;
     }
     if (my_id >= 0 && rank < p.top) {
         p.top_ids[(long long)row * p.top + rank] = my_id;
-        p.top_logp[(long long)row * p.top + rank] = (float)(z - lse);
+        p.top_logp[(long long)row * p.top + rank] = fmaf(d_mine, kLn2, -l);
     }
     if (lane >= found && lane < p.top) {  // fewer numbers than places
         p.top_ids[(long long)row * p.top + lane] = -1;
@@ -268,14 +301,6 @@ constexpr int kFewCap = 256;                          // groups above the thresh
 constexpr int kFewWant = kMaxTop + kSpareTop;
 constexpr int kFewLoads = 4;                          // 16-byte loads of a thread in flight
 
-// Order of doubles as integers (their comparisons are slow); 0 stands for no number.
-__device__ __forceinline__ unsigned long long wide_key(double z)
-{
-    z += 0.0;  // (zeros of one sign)
-    const long long u = __double_as_longlong(z);
-    return z == z ? (unsigned long long)u ^ ((unsigned long long)(u >> 63) | 0x8000000000000000ull) : 0ull;
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const MergeParams p)
 {
@@ -287,10 +312,10 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     __shared__ int s_best_at[kFewWarps];
     __shared__ unsigned g_key[kFewWant];              // the groups, in order
     __shared__ int g_at[kFewWant];
-    __shared__ double s_z[4 * kFewWant + 1];          // members' exact logits, then the target's
-    __shared__ unsigned long long s_wide[4 * kFewWant];
+    __shared__ Wide s_z[4 * kFewWant + 1];            // members' exact products, then the target's
+    __shared__ unsigned long long s_order[4 * kFewWant];
     __shared__ RowSums s_sums;
-    __shared__ double s_lse;
+    __shared__ float s_l;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x;
     const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
@@ -397,51 +422,51 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     const int jobs = 4 * groups;
     for (int c = warp; c <= jobs; c += kFewWarps) {
         const int id = c == 0 ? target : g_at[(c - 1) >> 2] * 4 + ((c - 1) & 3);
-        double e = __longlong_as_double(0x7ff8000000000000LL);  // no such token
+        Wide e{__int_as_float(0x7fffffff), 0.f};  // no such token
         if (id >= 0 && id < p.V)
-            e = dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane) *
-                (double)p.scale;
+            e = dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane);
         if (lane == 0) {
             s_z[c == 0 ? 4 * kFewWant : c - 1] = e;
-            if (c > 0) s_wide[c - 1] = wide_key(e);
+            if (c > 0) s_order[c - 1] = wide_key(e, p.scale);
         }
     }
     __syncthreads();
     // places in the order, while the first warp finishes the sums
     int rank = 0;
     const int c = tid - 32;
-    const bool on = c >= 0 && c < jobs && s_wide[c] != 0;
+    const bool on = c >= 0 && c < jobs && s_order[c] != 0;
     if (on) {
-        const unsigned long long k = s_wide[c];
+        const unsigned long long k = s_order[c];
         const int id = g_at[c >> 2] * 4 + (c & 3);
+#pragma unroll 4
         for (int o = 0; o < jobs; ++o) {
-            const unsigned long long ok = s_wide[o];
-            rank += ok > k || (ok == k && g_at[o >> 2] * 4 + (o & 3) < id);
+            const unsigned long long other = s_order[o];
+            rank += other > k || (other == k && g_at[o >> 2] * 4 + (o & 3) < id);
         }
     }
     const int found = __syncthreads_count(on);
+    const RowSums r0 = s_sums;
     if (warp == 0) {
-        RowSums r = s_sums;
+        RowSums r = r0;
         if (target >= 0) r.zt = p.target_z[row];
-        double z_target = (double)r.zt * kLn2;
-        float ds = 0.f, de = 0.f;
+        float d_target = r.zt - r.mu, ds = 0.f, de = 0.f;
         bool replaced = false;
         if (lane < groups) {
             // the group's maximum was its largest member's logit
             int at = 0;
             for (int i = 1; i < 4; ++i)
-                if (s_wide[4 * lane + i] > s_wide[4 * lane + at]) at = i;
-            const double best = s_z[4 * lane + at];
+                if (s_order[4 * lane + i] > s_order[4 * lane + at]) at = i;
+            const Wide best = s_z[4 * lane + at];
             const float was = key_value(g_key[lane]);
-            if (isfinite(best) && isfinite(was)) replace_term(r.mu, was, best * 1.4426950408889634, ds, de);
+            if (isfinite(best.hi) && isfinite(was)) replace_term(r.mu, was, above(p, best, r.mu), ds, de);
             replaced = g_at[lane] * 4 + at == target;
         }
         const bool in_sums = __any_sync(FULL, replaced);
         if (target >= 0) {
-            const double e = s_z[4 * kFewWant];
-            if (isfinite(e) && isfinite(r.zt)) {
-                z_target = e;
-                if (!in_sums && lane == 31) replace_term(r.mu, r.zt, e * 1.4426950408889634, ds, de);
+            const Wide e = s_z[4 * kFewWant];
+            if (isfinite(e.hi) && isfinite(r.zt)) {
+                d_target = above(p, e, r.mu);
+                if (!in_sums && lane == 31) replace_term(r.mu, r.zt, d_target, ds, de);
             }
         }
 #pragma unroll
@@ -451,13 +476,15 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         }
         r.sum += ds;
         r.es += de;
-        const double lse = row_outputs(p, row, r, target, z_target, lane == 0);
-        if (lane == 0) s_lse = lse;
+        const float l = row_outputs(p, row, r, target, d_target, lane == 0);
+        if (lane == 0) s_l = l;
     }
     __syncthreads();
     if (on && rank < p.top) {
         p.top_ids[(long long)row * p.top + rank] = g_at[c >> 2] * 4 + (c & 3);
-        p.top_logp[(long long)row * p.top + rank] = (float)(s_z[c] - s_lse);
+        const Wide z = s_z[c];
+        const float d = isfinite(z.hi) ? above(p, z, r0.mu) : z.hi * p.scale - r0.mu;
+        p.top_logp[(long long)row * p.top + rank] = fmaf(d, kLn2, -s_l);
     }
     if (tid >= found && tid < p.top) {  // fewer numbers than places
         p.top_ids[(long long)row * p.top + tid] = -1;
@@ -537,9 +564,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
         if (lane == 0) p.target_logp[row] = 0.f;
         return;
     }
-    const double z = dot_exact<BF16>(src, static_cast<const char *>(p.w) + target * p.w_ld * ESIZE, p.d, lane) *
-                     (double)p.scale;
-    if (lane == 0) p.target_logp[row] = (float)(z - (double)p.lse[row]);
+    const Wide z = dot_exact<BF16>(src, static_cast<const char *>(p.w) + target * p.w_ld * ESIZE, p.d, lane);
+    if (lane == 0) p.target_logp[row] = fmaf(z.hi, p.scale, -p.lse[row]) + z.lo * p.scale;
 }
 
 } // namespace

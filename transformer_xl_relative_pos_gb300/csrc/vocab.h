@@ -175,7 +175,7 @@ struct MergeParams {
     long long h_ld, w_ld;
     const void *targets;
     int index_bytes;
-    float scale;
+    float scale, c_hi, c_lo;  // c: scale / ln 2 as a pair
     float *logp, *lse, *entropy, *top_logp;
     int *top_ids;
     unsigned int *status;

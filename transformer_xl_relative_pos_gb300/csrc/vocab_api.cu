@@ -365,6 +365,9 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     m.targets = targets;
     m.index_bytes = index_type;
     m.scale = scale;
+    const double c = (double)scale * 1.4426950408889634;
+    m.c_hi = (float)c;
+    m.c_lo = (float)(c - (double)m.c_hi);
     m.logp = logp;
     m.lse = lse;
     m.entropy = entropy;
