@@ -99,7 +99,7 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
         if (lane == 0) {
             prefetch_tensormap(&tm_w);
             prefetch_tensormap(&tm_h);
-            const uint64_t once = policy_evict_first(), often = policy_evict_last();
+            const uint64_t often = policy_evict_last();
             bool ok = true;
             int it = 0;
             for (int t = t_lo; t < t_hi && ok; ++t)
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                         if (!(ok = mbar_wait(empty + s, ((it / ns) & 1) ^ 1, abort_flag, wait_ns))) break;
                         uint8_t *st = smem + s * stage_bytes;
                         mbar_arrive_expect_tx(full + s, stage_bytes);
-                        tma_load_3d_hint(st, &tm_w, full + s, kb * BK, t * BM, pw, once);
+                        tma_load_3d(st, &tm_w, full + s, kb * BK, t * BM, pw);
                         tma_load_3d_hint(st + A_BYTES, &tm_h, full + s, kb * BK, 0, ph, often);
                         ++it;
                     }
@@ -237,7 +237,12 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                     m[k] = m_new;
                     sum[k] = s_new;
                     es[k] = e_new;
-                    if (p.group_key) {
+                    if (p.logits) {
+                        const float none = __int_as_float(0x7fffffff);
+                        *reinterpret_cast<float4 *>(p.logits + ((long long)st * p.nb + t) * BM + lane * 4) =
+                            make_float4(left > 0 ? v[0] : none, left > 1 ? v[1] : none, left > 2 ? v[2] : none,
+                                        left > 3 ? v[3] : none);
+                    } else if (p.group_key) {
                         // the largest of the lane's four: NaN has no place in the order
                         const bool any = (v[0] == v[0] && left > 0) || (v[1] == v[1] && left > 1) ||
                                          (v[2] == v[2] && left > 2) || (v[3] == v[3] && left > 3);

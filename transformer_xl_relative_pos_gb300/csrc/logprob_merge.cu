@@ -293,18 +293,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
 
 // Rows of the kernel for few states: a block each.  The `want` largest logits lie in the `want`
 // groups of four with the largest maxima.  Those are found by a threshold that at least `want`
-// threads' own maxima reach (a search over the order's upper bits), then ranked among all that
-// reach it; their members' exact logits give the order.
-constexpr int kFewThreads = 512;
-constexpr int kFewWarps = kFewThreads / 32;
+// warps' own maxima reach, then ranked among all that reach it.  Where the logits themselves were
+// written (FULL: few states beside the width), the `want` largest of the groups' members are the
+// candidates, else all members; the candidates' exact products give the order.
+constexpr int kFewWarps = 32;
+constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewCap = 256;                          // groups above the threshold
 constexpr int kFewWant = kMaxTop + kSpareTop;
 constexpr int kFewLoads = 4;                          // 16-byte loads of a thread in flight
+static_assert(kFewWant < kFewWarps, "a threshold from the warps' maxima");
 
-template <bool BF16>
+// Logits (log2 units) as their order, NaN as 0.
+__device__ __forceinline__ unsigned logit_key(unsigned bits)
+{
+    const float v = __uint_as_float(bits);
+    return v == v ? order_key(v) : 0u;
+}
+
+template <bool BF16, bool FULL>
 __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const MergeParams p)
 {
-    constexpr unsigned FULL = 0xffffffffu;
+    constexpr unsigned ALL = 0xffffffffu;
     __shared__ unsigned s_key[kFewCap];
     __shared__ int s_at[kFewCap];
     __shared__ int s_count;
@@ -312,7 +321,10 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     __shared__ int s_best_at[kFewWarps];
     __shared__ unsigned g_key[kFewWant];              // the groups, in order
     __shared__ int g_at[kFewWant];
-    __shared__ Wide s_z[4 * kFewWant + 1];            // members' exact products, then the target's
+    __shared__ unsigned m_key[4 * kFewWant];          // FULL: their members
+    __shared__ int c_id[4 * kFewWant];                // the candidates
+    __shared__ float c_was[4 * kFewWant];             // ... their logits in the sums (NaN: not known)
+    __shared__ Wide s_z[4 * kFewWant + 1];            // ... their exact products, then the target's
     __shared__ unsigned long long s_order[4 * kFewWant];
     __shared__ RowSums s_sums;
     __shared__ float s_l;
@@ -321,87 +333,102 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
     const int esize = BF16 ? 2 : 4;
     const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
-    int groups = 0;                                   // found
+    const float nan = __int_as_float(0x7fffffff);
+    int jobs = 0;                                     // candidates
     if (p.top > 0) {
-        const int n = p.nb * 8, want = min(p.top + kSpareTop, kFewWant);  // (n: of four groups)
-        const uint4 *key = reinterpret_cast<const uint4 *>(p.group_key) + (long long)row * n;
+        // vectors of four groups' maxima, or of one group's logits
+        const int n = FULL ? p.nb * 32 : p.nb * 8, want = min(p.top + kSpareTop, kFewWant);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.group_key) + (long long)row * n;
         auto scan = [&](auto take) {
             for (int i0 = tid; i0 < n; i0 += kFewThreads * kFewLoads) {
                 uint4 k[kFewLoads];
 #pragma unroll
                 for (int u = 0; u < kFewLoads; ++u) {
                     const int i = i0 + u * kFewThreads;
-                    k[u] = i < n ? key[i] : make_uint4(0, 0, 0, 0);
+                    k[u] = i < n ? src[i] : FULL ? make_uint4(~0u, ~0u, ~0u, ~0u) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int u = 0; u < kFewLoads; ++u) take(k[u], (i0 + u * kFewThreads) * 4);
+                for (int u = 0; u < kFewLoads; ++u) {
+                    const int i = i0 + u * kFewThreads;
+                    if (FULL) {
+                        take(max(max(logit_key(k[u].x), logit_key(k[u].y)),
+                                 max(logit_key(k[u].z), logit_key(k[u].w))), i);
+                    } else {
+                        take(k[u].x, i * 4);
+                        take(k[u].y, i * 4 + 1);
+                        take(k[u].z, i * 4 + 2);
+                        take(k[u].w, i * 4 + 3);
+                    }
+                }
             }
         };
         unsigned mine = 0;
-        scan([&](const uint4 &k, int) { mine = max(mine, max(max(k.x, k.y), max(k.z, k.w))); });
+        scan([&](unsigned k, int) { mine = max(mine, k); });
+        const unsigned most = __reduce_max_sync(ALL, mine);
+        if (lane == 0) s_best_key[warp] = most;
         if (tid == 0) s_count = 0;
-        unsigned thr = 0;
-        for (int bit = 31; bit >= 14; --bit) {
-            const unsigned t = thr | 1u << bit;
-            if (__syncthreads_count(mine >= t) >= want) thr = t;
-        }
-        thr = max(thr, 1u);
-        if (mine >= thr)
-            scan([&](const uint4 &k, int at0) {
-                const unsigned ks[4] = {k.x, k.y, k.z, k.w};
+        __syncthreads();
+        // the want-th largest of the warps' maxima (a warp's own: distinct groups)
+        const unsigned w_key = s_best_key[lane];
+        int ahead = 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (ks[q] >= thr) {
-                        const int at = atomicAdd(&s_count, 1);
-                        if (at < kFewCap) {
-                            s_key[at] = ks[q];
-                            s_at[at] = at0 + q;
-                        }
+        for (int o = 0; o < kFewWarps; ++o) {
+            const unsigned other = __shfl_sync(ALL, w_key, o);
+            ahead += (other > w_key) | ((other == w_key) & (o < lane));
+        }
+        const unsigned thr = max(1u, __reduce_max_sync(ALL, ahead == want - 1 ? w_key : 0u));
+        if (mine >= thr)
+            scan([&](unsigned k, int at_group) {
+                if (k >= thr) {
+                    const int at = atomicAdd(&s_count, 1);
+                    if (at < kFewCap) {
+                        s_key[at] = k;
+                        s_at[at] = at_group;
                     }
+                }
             });
         __syncthreads();
         const int count = s_count;
+        int groups = 0;
         if (count <= kFewCap) {
             if (tid < count) {
                 int rank = 0;
                 const unsigned k = s_key[tid];
                 const int at = s_at[tid];
-                for (int c = 0; c < count; ++c) rank += s_key[c] > k || (s_key[c] == k && s_at[c] < at);
+#pragma unroll 4
+                for (int c = 0; c < count; ++c) rank += (s_key[c] > k) | ((s_key[c] == k) & (s_at[c] < at));
                 if (rank < want) {
                     g_key[rank] = k;
                     g_at[rank] = at;
                 }
             }
-            __syncthreads();
             groups = min(count, want);
         } else {
             // very many equal maxima: one after the other, the lowest group of equal ones first
-            const unsigned *one = reinterpret_cast<const unsigned *>(key);
             unsigned last_key = 0xffffffffu;
             int last_at = -1;
             for (int c = 0; c < want; ++c) {
                 unsigned bk = 0;
                 int ba = 0x7fffffff;
-                for (int i = tid; i < n * 4; i += kFewThreads) {
-                    const unsigned k = one[i];
+                scan([&](unsigned k, int i) {
                     const bool left = k < last_key || (k == last_key && i > last_at);
-                    if (k && left && k > bk) {
+                    if (left && (k > bk || (k == bk && i < ba))) {
                         bk = k;
                         ba = i;
                     }
-                }
-                unsigned top = __reduce_max_sync(FULL, bk);
-                int at = (int)__reduce_min_sync(FULL, bk == top ? (unsigned)ba : 0x7fffffffu);
+                });
+                unsigned top = __reduce_max_sync(ALL, bk);
+                int at = (int)__reduce_min_sync(ALL, bk == top ? (unsigned)ba : 0x7fffffffu);
+                __syncthreads();
                 if (lane == 0) {
                     s_best_key[warp] = top;
                     s_best_at[warp] = at;
                 }
                 __syncthreads();
-                bk = lane < kFewWarps ? s_best_key[lane] : 0;
-                ba = lane < kFewWarps ? s_best_at[lane] : 0x7fffffff;
-                top = __reduce_max_sync(FULL, bk);
-                at = (int)__reduce_min_sync(FULL, bk == top ? (unsigned)ba : 0x7fffffffu);
-                __syncthreads();
+                bk = s_best_key[lane];
+                ba = s_best_at[lane];
+                top = __reduce_max_sync(ALL, bk);
+                at = (int)__reduce_min_sync(ALL, bk == top ? (unsigned)ba : 0x7fffffffu);
                 if (!top) break;
                 if (tid == 0) {
                     g_key[c] = top;
@@ -411,20 +438,48 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
                 last_at = at;
                 groups = c + 1;
             }
-            __syncthreads();
         }
+        __syncthreads();
+        // the candidates
+        const int members = 4 * groups;
+        const int id = tid < members ? g_at[tid >> 2] * 4 + (tid & 3) : 0;
+        if (FULL) {
+            const float *logit = reinterpret_cast<const float *>(p.group_key) + (long long)row * p.nb * 128;
+            const float v = tid < members ? logit[id] : nan;
+            const unsigned k = tid < members && id < p.V && v == v ? order_key(v) : 0u;
+            if (tid < members) m_key[tid] = k;
+            const int some = __syncthreads_count(k != 0);
+            if (k) {
+                int rank = 0;
+#pragma unroll 4
+                for (int o = 0; o < members; ++o) {
+                    const int oid = g_at[o >> 2] * 4 + (o & 3);
+                    rank += (m_key[o] > k) | ((m_key[o] == k) & (oid < id));
+                }
+                if (rank < want) {
+                    c_id[rank] = id;
+                    c_was[rank] = v;
+                }
+            }
+            jobs = min(some, want);
+        } else {
+            if (tid < members) {
+                c_id[tid] = id < p.V ? id : -1;
+                c_was[tid] = nan;
+            }
+            jobs = members;
+        }
+        __syncthreads();
     }
     // the ranges' sums (last warp); exact logits, the target's first
     if (warp == kFewWarps - 1) {
         const RowSums r = join_stats<kLaneLists>(p, row, lane);
         if (lane == 0) s_sums = r;
     }
-    const int jobs = 4 * groups;
     for (int c = warp; c <= jobs; c += kFewWarps) {
-        const int id = c == 0 ? target : g_at[(c - 1) >> 2] * 4 + ((c - 1) & 3);
-        Wide e{__int_as_float(0x7fffffff), 0.f};  // no such token
-        if (id >= 0 && id < p.V)
-            e = dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane);
+        const int id = c == 0 ? target : c_id[c - 1];
+        Wide e{nan, 0.f};  // no such token
+        if (id >= 0) e = dot_exact<BF16>(h, static_cast<const char *>(p.w) + id * p.w_ld * esize, p.d, lane);
         if (lane == 0) {
             s_z[c == 0 ? 4 * kFewWant : c - 1] = e;
             if (c > 0) s_order[c - 1] = wide_key(e, p.scale);
@@ -437,11 +492,11 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     const bool on = c >= 0 && c < jobs && s_order[c] != 0;
     if (on) {
         const unsigned long long k = s_order[c];
-        const int id = g_at[c >> 2] * 4 + (c & 3);
+        const int id = c_id[c];
 #pragma unroll 4
         for (int o = 0; o < jobs; ++o) {
             const unsigned long long other = s_order[o];
-            rank += other > k || (other == k && g_at[o >> 2] * 4 + (o & 3) < id);
+            rank += (other > k) | ((other == k) & (c_id[o] < id));
         }
     }
     const int found = __syncthreads_count(on);
@@ -451,17 +506,18 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         if (target >= 0) r.zt = p.target_z[row];
         float d_target = r.zt - r.mu, ds = 0.f, de = 0.f;
         bool replaced = false;
-        if (lane < groups) {
-            // the group's maximum was its largest member's logit
-            int at = 0;
-            for (int i = 1; i < 4; ++i)
-                if (s_order[4 * lane + i] > s_order[4 * lane + at]) at = i;
-            const Wide best = s_z[4 * lane + at];
-            const float was = key_value(g_key[lane]);
+        if (lane < (FULL ? jobs : jobs / 4)) {
+            // (without the logits themselves: a group's maximum was its largest member's)
+            int at = FULL ? lane : 4 * lane;
+            if (!FULL)
+                for (int i = 1; i < 4; ++i)
+                    if (s_order[4 * lane + i] > s_order[at]) at = 4 * lane + i;
+            const Wide best = s_z[at];
+            const float was = FULL ? c_was[lane] : key_value(g_key[lane]);
             if (isfinite(best.hi) && isfinite(was)) replace_term(r.mu, was, above(p, best, r.mu), ds, de);
-            replaced = g_at[lane] * 4 + at == target;
+            replaced = c_id[at] == target;
         }
-        const bool in_sums = __any_sync(FULL, replaced);
+        const bool in_sums = __any_sync(ALL, replaced);
         if (target >= 0) {
             const Wide e = s_z[4 * kFewWant];
             if (isfinite(e.hi) && isfinite(r.zt)) {
@@ -471,8 +527,8 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            ds += __shfl_xor_sync(FULL, ds, o);
-            de += __shfl_xor_sync(FULL, de, o);
+            ds += __shfl_xor_sync(ALL, ds, o);
+            de += __shfl_xor_sync(ALL, de, o);
         }
         r.sum += ds;
         r.es += de;
@@ -481,7 +537,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     }
     __syncthreads();
     if (on && rank < p.top) {
-        p.top_ids[(long long)row * p.top + rank] = g_at[c >> 2] * 4 + (c & 3);
+        p.top_ids[(long long)row * p.top + rank] = c_id[c];
         const Wide z = s_z[c];
         const float d = isfinite(z.hi) ? above(p, z, r0.mu) : z.hi * p.scale - r0.mu;
         p.top_logp[(long long)row * p.top + rank] = fmaf(d, kLn2, -s_l);
@@ -598,8 +654,11 @@ cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
 
 cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream_t s)
 {
-    if (bf16) logprob_few_merge_kernel<true><<<(unsigned)p.N, kFewThreads, 0, s>>>(p);
-    else logprob_few_merge_kernel<false><<<(unsigned)p.N, kFewThreads, 0, s>>>(p);
+    const unsigned grid = (unsigned)p.N;
+    if (bf16 && p.full) logprob_few_merge_kernel<true, true><<<grid, kFewThreads, 0, s>>>(p);
+    else if (bf16) logprob_few_merge_kernel<true, false><<<grid, kFewThreads, 0, s>>>(p);
+    else if (p.full) logprob_few_merge_kernel<false, true><<<grid, kFewThreads, 0, s>>>(p);
+    else logprob_few_merge_kernel<false, false><<<grid, kFewThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -80,6 +80,7 @@ int choose_parts(long long units, int steps, int most, double extra)
 
 struct StatsPlan {
     bool few;                     // the vocabulary in the tiles' rows
+    bool full;                    // ... and the logits written
     int mb, nb, bn, splits, list;
     size_t h_planes, w_planes, stats, val, id, keys, target_z, total;  // offsets
 };
@@ -92,6 +93,10 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
         s.mb = 1;
         s.bn = std::max(16, ceil_div(N, 16) * 16);
         s.nb = ceil_div(V, 128);
+        // The logits of up to d / 16 states are an eighth of the table's bytes at most; with them the
+        // merge forms a quarter of the exact products (one state, 32000 x 1024, eight alternatives:
+        // 4.8 us less).
+        s.full = top > 0 && (long long)N * 16 <= d && N <= 64;
         s.splits = std::min(s.nb, std::min(txl::device_sm_count(), txl::kMaxStatSplits));
     } else {
         s.mb = ceil_div(N, 128);
@@ -114,7 +119,7 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     s.id = o;
     o = up256(o + lists);
     s.keys = o;
-    if (s.few && top > 0) o = up256(o + (size_t)N * s.nb * 32 * 4);
+    if (s.few && top > 0) o = up256(o + (size_t)N * s.nb * (s.full ? 128 : 32) * 4);
     s.target_z = o;
     s.total = s.few ? up256(o + (size_t)N * 4) : o;
     return s;
@@ -340,6 +345,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.list_val = reinterpret_cast<float *>(ws + s.val);
     p.list_id = reinterpret_cast<int *>(ws + s.id);
     p.group_key = top > 0 ? reinterpret_cast<unsigned *>(ws + s.keys) : nullptr;
+    p.logits = s.full ? reinterpret_cast<float *>(ws + s.keys) : nullptr;
     p.target_z = reinterpret_cast<float *>(ws + s.target_z);
     if ((s.few ? txl::launch_logprob_few(tm_w, tm_h, p, st)
                : txl::launch_logprob_stats(tm_h, tm_w, p, s.list, st)) != cudaSuccess)
@@ -350,6 +356,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     m.list_val = p.list_val;
     m.list_id = p.list_id;
     m.group_key = p.group_key;
+    m.full = s.full;
     m.target_z = p.target_z;
     m.nb = s.nb;
     m.splits = s.splits;
