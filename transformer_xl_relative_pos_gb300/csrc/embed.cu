@@ -7,13 +7,18 @@
 //
 // Both move rows and are bound by HBM.  The gradient first sorts the positions
 // by their tokens (a stable radix sort), then sums runs of equal tokens in
-// chunks of kChunk positions; a run that crosses chunks leaves one partial per
+// chunks of positions, a warp each; a run that crosses chunks leaves one partial per
 // chunk, which a last launch sums in their order.  No sum depends on the order
 // in which blocks run, so results repeat bit for bit.
+#include <algorithm>
+
 #include "vocab.h"
+#include "ptx.cuh"
 
 namespace txl {
 namespace {
+
+using namespace ptx;
 
 // ---------------------------------------------------------------------------
 // rows as 16-byte vectors
@@ -76,316 +81,469 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedParam
 // ---------------------------------------------------------------------------
 // positions sorted by token
 // ---------------------------------------------------------------------------
-// LSD radix sort of (key, position): key = token, or V for a position without
-// one.  Up to kTiles tiles of consecutive positions, one block each; a pass is
-// a histogram per tile and a scatter whose blocks read all histograms.  One tile
-// needs no histogram launch.  Within a block, rows of kSortThreads positions are
-// ranked in order: by warp (match of equal digits), then over the warps' counts.
+// LSD radix sort of (key, position): key = token, or V for a position without one.  One launch:
+// a thread-block cluster (one block for few positions), a warp for each stretch of consecutive
+// positions.  A pass counts each warp's digits, exchanges the blocks' counts through distributed
+// shared memory, and lets every warp put its stretch in place in order: 32 positions at a time,
+// equal digits ranked by match.  Stable, so equal tokens stay in the order of their positions.
+// Bound by the scattered stores of a few SMs, hence one of 8 bytes for each position.
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kTiles = 64;
+constexpr int kSortCluster = 8, kSortWide = 16;  // blocks; more than 8 need the device's consent
+constexpr int kSortAlone = 2048;        // positions up to which one block sorts
+constexpr int kHeld = 8;                // rows of 32 positions a warp holds in registers
 constexpr int kDigit = 9;
-constexpr int kBins = 1 << kDigit;  // one bin a thread
+constexpr int kBins = 1 << kDigit;      // one bin a thread
 static_assert(kBins == kSortThreads, "a thread keeps one bin");
 
 struct SortParams {
-    const void *tokens;      // first pass: keys come from here
-    const int *key_in, *pos_in;
-    int *key_out, *pos_out;
-    int *hist;               // [tiles][kBins]
-    unsigned int *present;   // bit per token, or null
-    int index_bytes, n, V, shift, tile, tiles, present_words;
+    const void *tokens;
+    int2 *pair[2];           // (key, position): pass i reads buffer i & 1 and writes the other
+    int *crossing;           // counter of the runs that cross chunks, zeroed here
+    uint4 *zero;             // the gradient, zeroed by the blocks that do not sort (null: left alone)
+    long long zero_vecs;
+    int index_bytes, n, V, passes, per_warp, blocks;
     unsigned int *status;
 };
 
-__device__ __forceinline__ int sort_key(const SortParams &p, int i)
+__device__ __forceinline__ void cluster_sync_all()
 {
-    if (p.key_in) return p.key_in[i];
-    const int id = token_at(p.tokens, p.index_bytes, i, p.V, p.status);
-    return id < 0 ? p.V : id;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p)
+// A word of another block's shared memory (the same place in it).
+__device__ __forceinline__ int cluster_word(const int *p, int block)
 {
-    __shared__ int bins[kBins];
-    bins[threadIdx.x] = 0;
-    if (p.present)
-        for (int i = blockIdx.x * kSortThreads + threadIdx.x; i < p.present_words;
-             i += gridDim.x * kSortThreads)
-            p.present[i] = 0;
-    __syncthreads();
-    const int lo = blockIdx.x * p.tile, hi = min(p.n, lo + p.tile);
-    for (int i = lo + threadIdx.x; i < hi; i += kSortThreads)
-        atomicAdd(bins + ((sort_key(p, i) >> p.shift) & (kBins - 1)), 1);
-    __syncthreads();
-    p.hist[blockIdx.x * kBins + threadIdx.x] = bins[threadIdx.x];
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(block));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortParams p)
+// ALONE: one block, whose positions stay in shared memory between passes.
+template <bool ALONE>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
 {
-    __shared__ int base[kBins];                 // next place of each digit
-    __shared__ int count[kSortWarps][kBins];    // of the current row, per warp
+    __shared__ int place[kSortWarps][kBins];    // a warp's counts, then its next places
+    __shared__ int total[kBins];                // the block's counts
     __shared__ int warp_sum[kSortWarps];
+    __shared__ int2 s_pair[ALONE ? kSortAlone : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // this tile's first place of digit `tid`: all smaller digits, and its own in earlier tiles
-    int total = 0, before = 0;
-    for (int t = 0; t < p.tiles; ++t) {
-        const int c = p.hist[t * kBins + tid];
-        total += c;
-        before += t < (int)blockIdx.x ? c : 0;
+    const int block = blockIdx.x;
+    const long long lo_ = ((long long)block * kSortWarps + warp) * p.per_warp;
+    const int lo = (int)min((long long)p.n, lo_), hi = (int)min((long long)p.n, lo_ + p.per_warp);
+    chain_go();
+    if (block >= p.blocks) {
+        // The table's gradient is zero where no token points; the sums then write the others.  Clearing
+        // all of it beside the sort costs the rows that are written twice and saves the wait for what
+        // the sort finds (65536 tokens, 32000 x 1024: 82 us with the absent rows cleared by the sums).
+        const long long stride = (long long)(gridDim.x - p.blocks) * kSortThreads;
+        for (long long i = (long long)(block - p.blocks) * kSortThreads + tid; i < p.zero_vecs; i += stride)
+            p.zero[i] = make_uint4(0, 0, 0, 0);
+        return;
     }
-    int incl = total;
+    if (block == 0 && tid == 0) *p.crossing = 0;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * kDigit;
+        const bool last = pass + 1 == p.passes;
+        const int2 *in = p.pair[pass & 1];
+        int2 *out = p.pair[(pass & 1) ^ 1];
+        // kHeld rows of 32 positions at a time in registers
+        int key[kHeld], pos[kHeld];
+        auto load = [&](int i0) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        incl += lane >= o ? v : 0;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int prefix = incl - total;
-    for (int w = 0; w < warp; ++w) prefix += warp_sum[w];
-    base[tid] = prefix + before;
-    const int lo = blockIdx.x * p.tile, hi = min(p.n, lo + p.tile);
-    for (int row = lo; row < hi; row += kSortThreads) {
+            for (int k = 0; k < kHeld; ++k) {
+                const int i = i0 + k * 32 + lane;
+                key[k] = -1;
+                pos[k] = i;
+                if (i >= hi) continue;
+                if (pass == 0) {
+                    const int id = token_at(p.tokens, p.index_bytes, i, p.V, p.status);
+                    key[k] = id < 0 ? p.V : id;
+                } else {
+                    const int2 v = ALONE ? s_pair[i] : __ldcg(in + i);
+                    key[k] = v.x;
+                    pos[k] = v.y;
+                }
+            }
+        };
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) count[w][tid] = 0;
+        for (int w = 0; w < kSortWarps; ++w) place[w][tid] = 0;
         __syncthreads();
-        const int i = row + tid;
-        const bool on = i < hi;
-        const int key = on ? sort_key(p, i) : 0;
-        const int digit = (key >> p.shift) & (kBins - 1);
-        const unsigned live = __ballot_sync(0xffffffffu, on);
-        const unsigned same = __match_any_sync(0xffffffffu, digit) & live;
-        const int rank = __popc(same & ((1u << lane) - 1));
-        if (on && rank == 0) count[warp][digit] = __popc(same);
+        load(lo);
+        for (int i0 = lo; i0 < hi; i0 += kHeld * 32) {
+            if (i0 > lo) load(i0);
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k)
+                if (key[k] >= 0) atomicAdd(&place[warp][(key[k] >> shift) & (kBins - 1)], 1);
+        }
         __syncthreads();
-        // places of each warp's digits in this row, and the next row's base
-        int at = base[tid];
+        // thread = bin: the warps' counts to starts within the block
+        int sum = 0;
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-            const int c = count[w][tid];
-            count[w][tid] = at;
-            at += c;
+            const int c = place[w][tid];
+            place[w][tid] = sum;
+            sum += c;
         }
-        base[tid] = at;
-        __syncthreads();
-        if (on) {
-            const int to = count[warp][digit] + rank;
-            TXL_CHECK(to >= 0 && to < p.n, p.status);
-            p.key_out[to] = key;
-            p.pos_out[to] = p.pos_in ? p.pos_in[i] : i;
-            if (p.present && key < p.V) {
-                const unsigned bit = 1u << (key & 31);
-                if (!(p.present[key >> 5] & bit)) atomicOr(p.present + (key >> 5), bit);
+        total[tid] = sum;
+        int all = sum, before = 0;
+        if (!ALONE) {
+            cluster_sync_all();
+            all = 0;
+#pragma unroll 8
+            for (int b = 0; b < p.blocks; ++b) {
+                const int c = cluster_word(total + tid, b);
+                all += c;
+                before += b < block ? c : 0;
             }
         }
+        int incl = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            incl += lane >= o ? v : 0;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
+        int start = incl - all + before;
+        for (int w = 0; w < warp; ++w) start += warp_sum[w];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) place[w][tid] += start;
+        __syncthreads();
+        if (hi - lo > kHeld * 32) load(lo);
+        for (int i0 = lo; i0 < hi; i0 += kHeld * 32) {
+            if (i0 > lo) load(i0);
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                if (i0 + k * 32 >= hi) break;
+                const bool on = key[k] >= 0;
+                const int digit = on ? (key[k] >> shift) & (kBins - 1) : kBins + lane;
+                const unsigned same = __match_any_sync(0xffffffffu, digit);
+                const int rank = __popc(same & ((1u << lane) - 1));
+                int to = 0;
+                if (on) to = place[warp][digit] + rank;
+                __syncwarp();
+                if (on && rank == 0) place[warp][digit] = to + __popc(same);
+                __syncwarp();
+                if (!on) continue;
+                TXL_CHECK(to >= 0 && to < p.n, p.status);
+                const int2 v = make_int2(key[k], pos[k]);
+                if (ALONE && !last) s_pair[to] = v;
+                else __stcg(out + to, v);
+            }
+        }
+        // what this pass has put in place is read by other warps and blocks
+        if (last) break;
+        if (ALONE) {
+            __syncthreads();
+        } else {
+            __threadfence();
+            cluster_sync_all();
+        }
     }
+    // (no block leaves while another may still read its counts)
+    if (!ALONE) cluster_sync_all();
 }
 
 // ---------------------------------------------------------------------------
 // sums over runs
 // ---------------------------------------------------------------------------
 
-constexpr int kChunk = 32;        // positions of a warp
-constexpr int kSlice = 256;       // columns of a warp (eight a lane)
+constexpr int kRow = 32;          // positions at a time
+constexpr int kMaxChunk = 64;     // positions of a warp, at most
 constexpr int kSumWarps = 4;
+constexpr int kBatch = 8;         // rows in flight, and as many being summed
+constexpr int kJoinWarps = 16;
 
 struct SumParams {
-    const int *key, *pos;
-    const unsigned int *present;
+    const int2 *pair;             // (key, position), sorted
     const void *dout;
     long long dout_ld;
     void *demb;
-    float *part;                  // [chunks][2][slices * kSlice]: of a run from before, of one into the next
-    int n, V, d, chunks, slices, sum_blocks, accumulate;
+    float *part;                  // [chunks][2][part_ld]: of a run from before, of one into the next
+    long long part_ld;
+    int *crossing, *cross_chunk;  // chunks in which a run begins that goes on in the next
+    int n, V, d, chunk, chunks, slices, accumulate;
     float scale;
     unsigned int *status;
 };
 
-struct Acc {
-    float v[8];
+// Columns of a lane: 16 bytes of dout.
+template <bool BF16>
+struct Cols {
+    static constexpr int N = BF16 ? 8 : 4;
 };
 
 template <bool BF16>
-__device__ __forceinline__ Acc load_row(const SumParams &p, int t, int col)
+__device__ __forceinline__ void add_row(float (&a)[Cols<BF16>::N], const uint4 &r)
 {
-    Acc a;
-    if (BF16) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(
-            static_cast<const __nv_bfloat16 *>(p.dout) + t * p.dout_ld + col));
-        const float2 f0 = bf2_to_f2(v.x), f1 = bf2_to_f2(v.y), f2 = bf2_to_f2(v.z), f3 = bf2_to_f2(v.w);
-        a = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
-    } else {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p.dout) +
-                                                           t * p.dout_ld + col);
-        const float4 x = __ldcs(s), y = __ldcs(s + 1);
-        a = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            const float2 f = bf2_to_f2(w[i]);
+            a[2 * i] += f.x;
+            a[2 * i + 1] += f.y;
+        } else {
+            a[i] += __uint_as_float(w[i]);
+        }
     }
-    return a;
 }
 
-template <bool GRAD_BF16>
-__device__ __forceinline__ void store_row(const SumParams &p, int v, int col, const Acc &a)
+// N sums (4 or 8) of a row of demb, from column col on.
+template <bool GRAD_BF16, int N>
+__device__ __forceinline__ void store_row(const SumParams &p, int v, int col, const float (&a)[N])
 {
     const long long at = (long long)v * p.d + col;
-    if (GRAD_BF16) {
-        uint4 o;
-        o.x = f2_to_bf2(a.v[0] * p.scale, a.v[1] * p.scale);
-        o.y = f2_to_bf2(a.v[2] * p.scale, a.v[3] * p.scale);
-        o.z = f2_to_bf2(a.v[4] * p.scale, a.v[5] * p.scale);
-        o.w = f2_to_bf2(a.v[6] * p.scale, a.v[7] * p.scale);
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.demb) + at) = o;
-    } else {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.demb) + at);
-        float4 x = make_float4(a.v[0] * p.scale, a.v[1] * p.scale, a.v[2] * p.scale, a.v[3] * p.scale);
-        float4 y = make_float4(a.v[4] * p.scale, a.v[5] * p.scale, a.v[6] * p.scale, a.v[7] * p.scale);
-        if (p.accumulate) {
-            const float4 ox = o[0], oy = o[1];
-            x = make_float4(ox.x + x.x, ox.y + x.y, ox.z + x.z, ox.w + x.w);
-            y = make_float4(oy.x + y.x, oy.y + y.y, oy.z + y.z, oy.w + y.w);
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+        float4 x = make_float4(a[q] * p.scale, a[q + 1] * p.scale, a[q + 2] * p.scale, a[q + 3] * p.scale);
+        if (GRAD_BF16) {
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.demb) + at + q) =
+                make_uint2(f2_to_bf2(x.x, x.y), f2_to_bf2(x.z, x.w));
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.demb) + at + q);
+            if (p.accumulate) {
+                const float4 y = *o;
+                x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+            }
+            *o = x;
         }
-        o[0] = x;
-        o[1] = y;
     }
 }
 
-__device__ __forceinline__ void store_part(float *part, const Acc &a)
-{
-    float4 *o = reinterpret_cast<float4 *>(part);
-    o[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
-    o[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
-}
-
-// Blocks below sum_blocks: one warp per (chunk, slice).  The rest write the rows of
-// tokens that do not occur, 32 tokens a warp.
+// One warp per (chunk, slice).
 template <bool BF16, bool GRAD_BF16>
 __global__ void __launch_bounds__(kSumWarps * 32) sum_runs_kernel(const SumParams p)
 {
+    constexpr int COLS = Cols<BF16>::N, SLICE = 32 * COLS;
+    constexpr unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if ((int)blockIdx.x >= p.sum_blocks) {
-        const int word = ((int)blockIdx.x - p.sum_blocks) * kSumWarps + warp;
-        const int v0 = word * 32;
-        if (v0 >= p.V) return;
-        unsigned absent = ~p.present[word];
-        if (p.V - v0 < 32) absent &= (1u << (p.V - v0)) - 1;
-        Acc zero{};
-        for (; absent; absent &= absent - 1) {
-            const int v = v0 + __ffs(absent) - 1;
-            for (int col = lane * 8; col < p.d; col += kSlice) store_row<GRAD_BF16>(p, v, col, zero);
-        }
-        return;
-    }
+    chain_wait();
+    chain_go();
     const int item = (int)blockIdx.x * kSumWarps + warp;
     const int chunk = item / p.slices, slice = item - chunk * p.slices;
     if (chunk >= p.chunks) return;
-    const int col = slice * kSlice + lane * 8;
+    const int col = slice * SLICE + lane * COLS;
     const bool col_on = col < p.d;
-    const int lo = chunk * kChunk, cnt = min(kChunk, p.n - lo);
-    const int my_key = lane < cnt ? p.key[lo + lane] : p.V;
-    const int my_pos = lane < cnt ? p.pos[lo + lane] : 0;
-    const int prev = lo > 0 ? p.key[lo - 1] : -1;
-    const int next = lo + cnt < p.n ? p.key[lo + cnt] : -1;
-    float *part = p.part + ((long long)chunk * 2 * p.slices + slice) * kSlice + lane * 8;
-    const long long tail = (long long)p.slices * kSlice;
-    int i = 0;
-    while (i < cnt) {
-        const int key = __shfl_sync(0xffffffffu, my_key, i);
-        if (key >= p.V) break;  // (positions without a token come last)
-        const unsigned same = __ballot_sync(0xffffffffu, lane < cnt && my_key == key);
-        const int end = i + __popc(same);
-        Acc a{};
-        for (; i < end; i += 4) {
-            Acc r[4];
+    const int lo = (int)min((long long)p.n, (long long)chunk * p.chunk), hi = min(p.n, lo + p.chunk);
+    const int prev = lo > 0 ? p.pair[lo - 1].x : -1;
+    // 32 positions and the key behind them; positions without a token (key V) come last
+    struct Row {
+        int key, pos, next, live;
+        unsigned ends;   // of runs
+    };
+    auto load = [&](int i0) {
+        Row r;
+        const int i = i0 + lane;
+        const int2 v = i < hi ? p.pair[i] : make_int2(p.V, 0);
+        r.key = v.x;
+        r.pos = v.y;
+        const int behind = min(i0 + kRow, hi);
+        r.next = behind < p.n ? p.pair[behind].x : -1;
+        return r;
+    };
+    auto settle = [&](Row &r, int i0) {
+        r.live = __popc(__ballot_sync(FULL, r.key < p.V));
+        int after = __shfl_down_sync(FULL, r.key, 1);
+        if (lane == 31 || i0 + lane + 1 == hi) after = r.next;
+        r.ends = __ballot_sync(FULL, r.key != after || i0 + lane + 1 == hi);
+    };
+    const char *dout = static_cast<const char *>(p.dout) + (long long)col * (BF16 ? 2 : 4);
+    const long long ld = p.dout_ld * (BF16 ? 2 : 4);
+    uint4 in[2][kBatch];
+    auto fetch = [&](uint4 (&v)[kBatch], const Row &r, int k0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = __shfl_sync(0xffffffffu, my_pos, (i + k) & 31);
-                if (i + k < end && col_on) r[k] = load_row<BF16>(p, t, col);
-                else r[k] = Acc{};
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) a.v[c] += r[k].v[c];
+        for (int k = 0; k < kBatch; ++k) {
+            const int t = __shfl_sync(FULL, r.pos, (k0 + k) & 31);
+            const int id = __shfl_sync(FULL, r.key, (k0 + k) & 31);
+            v[k] = id < p.V && col_on ? __ldcs(reinterpret_cast<const uint4 *>(dout + t * ld))
+                                      : make_uint4(0, 0, 0, 0);
         }
-        i = end;
-        const bool from_before = key == prev && end - __popc(same) == 0;
-        const bool into_next = end == cnt && key == next;
-        if (from_before) store_part(part, a);
-        else if (into_next) store_part(part + tail, a);
-        else if (col_on) store_row<GRAD_BF16>(p, key, col, a);
+    };
+    float *part = p.part + (long long)chunk * 2 * p.part_ld + col;
+    float a[COLS] = {};
+    bool first = true;   // the chunk's first run
+    Row cur = load(lo);
+    fetch(in[0], cur, 0);
+    for (int i0 = lo; i0 < hi; i0 += kRow) {
+        settle(cur, i0);
+        Row ahead{p.V, 0, -1, 0, 0u};
+        if (i0 + kRow < hi) ahead = load(i0 + kRow);
+#pragma unroll
+        for (int b = 0; b < kRow / kBatch; ++b) {
+            const int k0 = b * kBatch;
+            if (k0 >= cur.live) break;
+            if (b + 1 < kRow / kBatch) fetch(in[(b + 1) & 1], cur, k0 + kBatch);
+            else fetch(in[(b + 1) & 1], ahead, 0);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (k0 + k >= cur.live) break;
+                add_row<BF16>(a, in[b & 1][k]);
+                if (!(cur.ends >> (k0 + k) & 1)) continue;
+                const int id = __shfl_sync(FULL, cur.key, k0 + k);
+                const bool from_before = first && id == prev;
+                const bool into_next = i0 + k0 + k + 1 == hi && id == cur.next;
+                if (col_on) {
+                    if (from_before || into_next) {
+                        float4 *o = reinterpret_cast<float4 *>(part + (from_before ? 0 : p.part_ld));
+#pragma unroll
+                        for (int q = 0; q < COLS / 4; ++q)
+                            o[q] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+                    } else {
+                        store_row<GRAD_BF16>(p, id, col, a);
+                    }
+                }
+                if (into_next && !from_before && slice == 0 && lane == 0)
+                    p.cross_chunk[atomicAdd(p.crossing, 1)] = chunk;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) a[c] = 0.f;
+                first = false;
+            }
+        }
+        if (cur.live < kRow) break;
+        cur = ahead;
     }
 }
 
 // Runs that begin in a chunk and go on in the next: the chunk's tail, then the heads of the
-// chunks the run reaches.  One block per (chunk, slice), mostly without such a run.
+// chunks the run reaches.  A block takes one run at a time (of the list that the sums left, in
+// any order); its warps are 128-column slices by shares of the chunks.
 template <bool GRAD_BF16>
-__global__ void __launch_bounds__(kSumWarps * 32) join_runs_kernel(const SumParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32) join_runs_kernel(const SumParams p, int wide)
 {
-    const int chunk = blockIdx.x, slice = blockIdx.y;
+    constexpr unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int last = chunk * kChunk + kChunk - 1;
-    if (last + 1 >= p.n) return;
-    const int key = p.key[last];
-    if (key >= p.V || p.key[last + 1] != key) return;
-    // (the run began in an earlier chunk)
-    if (chunk > 0 && p.key[chunk * kChunk - 1] == key) return;
-    // the last chunk whose first position has the key: a search over the sorted keys
-    int in = chunk + 1, out = p.chunks;
-    while (out - in > 1) {
-        const int mid = (in + out) / 2;
-        if (p.key[mid * kChunk] == key) in = mid;
-        else out = mid;
-    }
-    __shared__ float sums[kSumWarps][kSlice];
-    const long long row = 2LL * p.slices * kSlice;
-    const float *part = p.part + (long long)slice * kSlice + lane * 8;
-    Acc a{};
-    // partials over the warps in turn, then the warps' sums in their order
-    for (int c = chunk + warp; c <= in; c += kSumWarps) {
-        const float *src = part + c * row + (c == chunk ? (long long)p.slices * kSlice : 0);
-        const float4 x = reinterpret_cast<const float4 *>(src)[0], y = reinterpret_cast<const float4 *>(src)[1];
-        a.v[0] += x.x; a.v[1] += x.y; a.v[2] += x.z; a.v[3] += x.w;
-        a.v[4] += y.x; a.v[5] += y.y; a.v[6] += y.z; a.v[7] += y.w;
-    }
-    store_part(&sums[warp][lane * 8], a);
-    __syncthreads();
-    const int col = slice * kSlice + lane * 8;
-    if (warp > 0 || col >= p.d) return;
-    for (int w = 1; w < kSumWarps; ++w)
+    const int shares = kJoinWarps / wide, slice = warp % wide, share = warp / wide;
+    __shared__ float4 sums[kJoinWarps][32];
+    chain_wait();
+    const int runs = *p.crossing;
+    for (int run = blockIdx.x; run < runs; run += gridDim.x) {
+        const int chunk = p.cross_chunk[run];
+        const int key = p.pair[(long long)(chunk + 1) * p.chunk - 1].x;
+        // the last chunk whose first position has the key, 32 ways at a time over the sorted keys
+        int in = chunk + 1, out = p.chunks;
+        while (out - in > 1) {
+            const int step = (out - in + 31) / 32, at = in + lane * step;
+            const bool has = at < out && p.pair[(long long)at * p.chunk].x == key;
+            const int n = __popc(__ballot_sync(FULL, has));  // (lane 0 has it)
+            const int lo = in + (n - 1) * step;
+            out = min(out, lo + step);
+            in = lo;
+        }
+        for (int c0 = slice * 128; c0 < p.d + wide * 128; c0 += wide * 128) {
+            const int col = c0 + lane * 4;
+            const bool any = c0 - slice * 128 < p.d;   // (the same for the whole block)
+            if (!any) break;
+            float a[4] = {};
+            // four loads in flight; then the shares' sums in their order
+            for (int c = chunk + share; c <= in; c += 4 * shares) {
+                float4 x[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) a.v[c] += sums[w][lane * 8 + c];
-    store_row<GRAD_BF16>(p, key, col, a);
+                for (int k = 0; k < 4; ++k) {
+                    const int ck = c + k * shares;
+                    x[k] = ck <= in && col < p.d
+                               ? *reinterpret_cast<const float4 *>(p.part + (2LL * ck + (ck == chunk)) * p.part_ld + col)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    a[0] += x[k].x;
+                    a[1] += x[k].y;
+                    a[2] += x[k].z;
+                    a[3] += x[k].w;
+                }
+            }
+            sums[warp][lane] = make_float4(a[0], a[1], a[2], a[3]);
+            __syncthreads();
+            if (share == 0 && col < p.d) {
+                for (int w = 1; w < shares; ++w) {
+                    const float4 x = sums[w * wide + slice][lane];
+                    a[0] += x.x;
+                    a[1] += x.y;
+                    a[2] += x.z;
+                    a[3] += x.w;
+                }
+                store_row<GRAD_BF16>(p, key, col, a);
+            }
+            __syncthreads();
+        }
+    }
 }
 
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-    size_t key[2], pos[2], hist, present, part, total;
-    int chunks, slices, words;
+    size_t pair[2], cross, part, total;
+    long long part_ld;
+    int chunk, chunks;
 };
 
-Layout layout(int n, int V, int d)
+// Positions of a warp: as many as leave some 512 warps for each slice of columns, in rows of 32.
+// Longer stretches leave fewer partial sums to join and fewer rows in flight (65536 tokens of 1024:
+// sums and joins 37 + 25 us with 32 positions, 47 + 8 with 128).
+int chunk_of(int n) { return std::min(kMaxChunk, std::max(kRow, n / 512 / kRow * kRow)); }
+
+Layout layout(int n, int d)
 {
     Layout l{};
-    l.chunks = (int)(((long long)n + kChunk - 1) / kChunk);
-    l.slices = (d + kSlice - 1) / kSlice;
-    l.words = (int)(((long long)V + 31) / 32);
+    l.chunk = chunk_of(n);
+    l.chunks = (int)(((long long)n + l.chunk - 1) / l.chunk);
+    l.part_ld = (d + 31) / 32 * 32;
     size_t o = 0;
     for (int i = 0; i < 2; ++i) {
-        l.key[i] = o;
-        o = up(o + (size_t)n * 4);
-        l.pos[i] = o;
-        o = up(o + (size_t)n * 4);
+        l.pair[i] = o;
+        o = up(o + (size_t)n * 8);
     }
-    l.hist = o;
-    o = up(o + (size_t)kTiles * kBins * 4);
-    l.present = o;
-    o = up(o + (size_t)l.words * 4);
+    l.cross = o;
+    o = up(o + ((size_t)l.chunks + 1) * 4);
     l.part = o;
-    l.total = up(o + (size_t)l.chunks * 2 * l.slices * kSlice * 4);
+    l.total = up(o + (size_t)l.chunks * 2 * l.part_ld * 4);
     return l;
+}
+
+template <bool BF16, bool GRAD_BF16>
+cudaError_t sum_and_join(const SumParams &r, int sum_blocks, cudaStream_t s)
+{
+    cudaError_t e = launch_chained(sum_runs_kernel<BF16, GRAD_BF16>, dim3((unsigned)sum_blocks),
+                                   kSumWarps * 32, 0, s, r);
+    if (e == cudaSuccess && r.chunks > 1) {
+        int wide = 1;   // slices of 128 columns side by side
+        while (wide < 8 && wide * 128 < r.d) wide *= 2;
+        const unsigned blocks = (unsigned)std::min(r.chunks - 1, 4 * device_sm_count());
+        e = launch_chained(join_runs_kernel<GRAD_BF16>, dim3(blocks), kJoinWarps * 32, 0, s, r, wide);
+    }
+    return e;
+}
+
+// Whether the device takes clusters of kSortWide blocks of the sort (asked once).
+bool wide_clusters()
+{
+    static int known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!known[dev]) {
+        int n = 0;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kSortWide);
+        cfg.blockDim = dim3(kSortThreads);
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = kSortWide;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const bool ok =
+            cudaFuncSetAttribute(sort_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, sort_kernel<false>, &cfg) == cudaSuccess && n > 0;
+        if (!ok) cudaGetLastError();
+        known[dev] = ok ? 1 : -1;
+    }
+    return known[dev] > 0;
 }
 
 } // namespace
@@ -401,68 +559,74 @@ cudaError_t launch_embed_fwd(const EmbedParams &p, bool bf16, cudaStream_t s)
     return cudaGetLastError();
 }
 
-size_t embed_bwd_workspace_bytes(int n, int V, int d) { return layout(n, V, d).total; }
+size_t embed_bwd_workspace_bytes(int n, int d) { return layout(n, d).total; }
 
 cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16, void *workspace,
                              cudaStream_t s)
 {
-    const Layout l = layout(p.n, p.V, p.d);
+    const Layout l = layout(p.n, p.d);
     char *ws = static_cast<char *>(workspace);
     SortParams q{};
     q.tokens = p.tokens;
+    for (int i = 0; i < 2; ++i) q.pair[i] = reinterpret_cast<int2 *>(ws + l.pair[i]);
+    q.crossing = reinterpret_cast<int *>(ws + l.cross);
     q.index_bytes = p.index_bytes;
     q.n = p.n;
     q.V = p.V;
-    q.hist = reinterpret_cast<int *>(ws + l.hist);
-    q.present_words = l.words;
     q.status = p.status;
-    // tiles of whole rows of the block's threads
-    q.tile = (int)((((long long)p.n + kTiles - 1) / kTiles + kSortThreads - 1) / kSortThreads * kSortThreads);
-    q.tiles = (int)(((long long)p.n + q.tile - 1) / q.tile);
     int bits = 1;
     while (((long long)p.V >> bits) != 0) ++bits;  // (the key V stands for no token)
-    int from = 0;
-    for (int shift = 0; shift < bits; shift += kDigit) {
-        q.shift = shift;
-        q.present = shift == 0 ? reinterpret_cast<unsigned int *>(ws + l.present) : nullptr;
-        q.key_in = shift == 0 ? nullptr : reinterpret_cast<const int *>(ws + l.key[from]);
-        q.pos_in = shift == 0 ? nullptr : reinterpret_cast<const int *>(ws + l.pos[from]);
-        q.key_out = reinterpret_cast<int *>(ws + l.key[from ^ 1]);
-        q.pos_out = reinterpret_cast<int *>(ws + l.pos[from ^ 1]);
-        sort_count_kernel<<<q.tiles, kSortThreads, 0, s>>>(q);
-        sort_scatter_kernel<<<q.tiles, kSortThreads, 0, s>>>(q);
-        from ^= 1;
+    q.passes = (bits + kDigit - 1) / kDigit;
+    // (a cluster's exchange costs what some 2000 positions do)
+    q.blocks = p.n <= kSortAlone ? 1 : p.n <= kSortAlone * 8 || !wide_clusters() ? kSortCluster : kSortWide;
+    const int warps = q.blocks * kSortWarps;
+    q.per_warp = (int)((((long long)p.n + warps - 1) / warps + 31) / 32 * 32);
+    cudaLaunchConfig_t cfg{};
+    int more = 0;   // blocks that clear the gradient, in whole clusters
+    if (!p.accumulate) {
+        q.zero = static_cast<uint4 *>(p.demb);
+        q.zero_vecs = (long long)p.V * p.d * (grad_bf16 ? 2 : 4) / 16;
+        const long long want = (q.zero_vecs + kSortThreads * 8 - 1) / (kSortThreads * 8);
+        const long long room = 2LL * device_sm_count() - q.blocks;
+        more = (int)((std::min(want, room) + q.blocks - 1) / q.blocks * q.blocks);
     }
+    cfg.gridDim = dim3((unsigned)(q.blocks + more));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)q.blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = q.blocks == 1 ? cudaLaunchKernelEx(&cfg, sort_kernel<true>, q)
+                                        : cudaLaunchKernelEx(&cfg, sort_kernel<false>, q);
+    if (e != cudaSuccess) return e;
+    const int sorted = q.passes & 1;
+
     SumParams r{};
-    r.key = reinterpret_cast<const int *>(ws + l.key[from]);
-    r.pos = reinterpret_cast<const int *>(ws + l.pos[from]);
-    r.present = reinterpret_cast<const unsigned int *>(ws + l.present);
+    r.pair = q.pair[sorted];
     r.dout = p.dout;
     r.dout_ld = p.dout_ld;
     r.demb = p.demb;
     r.part = reinterpret_cast<float *>(ws + l.part);
+    r.part_ld = l.part_ld;
+    r.crossing = q.crossing;
+    r.cross_chunk = q.crossing + 1;
+    r.chunk = l.chunk;
     r.n = p.n;
     r.V = p.V;
     r.d = p.d;
     r.chunks = l.chunks;
-    r.slices = l.slices;
+    const int slice = bf16 ? 256 : 128;
+    r.slices = (p.d + slice - 1) / slice;
     r.accumulate = p.accumulate;
     r.scale = p.scale;
     r.status = p.status;
-    r.sum_blocks = (int)(((long long)l.chunks * l.slices + kSumWarps - 1) / kSumWarps);
-    const int fill_blocks = p.accumulate ? 0 : (l.words + kSumWarps - 1) / kSumWarps;
-    const unsigned grid = (unsigned)(r.sum_blocks + fill_blocks);
-    const int threads = kSumWarps * 32;
-    if (bf16 && grad_bf16) sum_runs_kernel<true, true><<<grid, threads, 0, s>>>(r);
-    else if (bf16) sum_runs_kernel<true, false><<<grid, threads, 0, s>>>(r);
-    else if (grad_bf16) sum_runs_kernel<false, true><<<grid, threads, 0, s>>>(r);
-    else sum_runs_kernel<false, false><<<grid, threads, 0, s>>>(r);
-    if (l.chunks > 1) {
-        const dim3 join((unsigned)(l.chunks - 1), (unsigned)l.slices);
-        if (grad_bf16) join_runs_kernel<true><<<join, threads, 0, s>>>(r);
-        else join_runs_kernel<false><<<join, threads, 0, s>>>(r);
-    }
-    return cudaGetLastError();
+    const int sum_blocks = (int)(((long long)l.chunks * r.slices + kSumWarps - 1) / kSumWarps);
+    if (bf16 && grad_bf16) return sum_and_join<true, true>(r, sum_blocks, s);
+    if (bf16) return sum_and_join<true, false>(r, sum_blocks, s);
+    return grad_bf16 ? sum_and_join<false, true>(r, sum_blocks, s) : sum_and_join<false, false>(r, sum_blocks, s);
 }
 
 } // namespace txl

@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(256, 1)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint64_t wait_ns = p.wait_ns;
+    chain_wait();
+    chain_go();
 
     if (warp == 0) {
         // ===================== TMA producer =====================================
@@ -467,6 +469,7 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmPa
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const unsigned grid = (unsigned)min(p.n_items, device_sm_count());
+    if (p.chained) return launch_chained(vocab_gemm_kernel<MODE, LIST>, dim3(grid), 256, SMEM_BYTES, s, a, b, p);
     vocab_gemm_kernel<MODE, LIST><<<grid, 256, SMEM_BYTES, s>>>(a, b, p);
     return cudaGetLastError();
 }

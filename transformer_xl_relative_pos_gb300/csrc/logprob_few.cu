@@ -94,6 +94,8 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint64_t wait_ns = p.wait_ns;
+    chain_wait();
+    chain_go();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -302,6 +304,9 @@ cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmP
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const int ns = min(MAX_NS, RING / (A_BYTES + p.bn * BK * 2));
+    if (p.chained)
+        return launch_chained(logprob_few_kernel<GROUPS>, dim3((unsigned)p.splits), (4 + kEpiWarps) * 32, SMEM_BYTES,
+                              s, tm_w, tm_h, p, ns);
     logprob_few_kernel<GROUPS><<<(unsigned)p.splits, (4 + kEpiWarps) * 32, SMEM_BYTES, s>>>(tm_w, tm_h, p, ns);
     return cudaGetLastError();
 }

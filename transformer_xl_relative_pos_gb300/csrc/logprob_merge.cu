@@ -178,6 +178,7 @@ template <bool BF16, int LIST>
 __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const MergeParams p)
 {
     constexpr unsigned FULL = 0xffffffffu;
+    chain_wait();
     constexpr int PER = kMaxRowSplits / 32, WANT = LIST > 0 ? LIST : 1;
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     __shared__ unsigned s_key[kFewCap];
     __shared__ int s_at[kFewCap];
     __shared__ int s_count;
-    __shared__ unsigned s_best_key[kFewWarps];
+    __shared__ unsigned s_thr, s_best_key[kFewWarps];
     __shared__ int s_best_at[kFewWarps];
     __shared__ unsigned g_key[kFewWant];              // the groups, in order
     __shared__ int g_at[kFewWant];
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     __shared__ float s_l;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x;
+    chain_wait();
     const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
     const int esize = BF16 ? 2 : 4;
     const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
@@ -369,14 +371,19 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         if (tid == 0) s_count = 0;
         __syncthreads();
         // the want-th largest of the warps' maxima (a warp's own: distinct groups)
-        const unsigned w_key = s_best_key[lane];
-        int ahead = 0;
+        if (warp == 0) {
+            const unsigned w_key = s_best_key[lane];
+            int ahead = 0;
 #pragma unroll
-        for (int o = 0; o < kFewWarps; ++o) {
-            const unsigned other = __shfl_sync(ALL, w_key, o);
-            ahead += (other > w_key) | ((other == w_key) & (o < lane));
+            for (int o = 0; o < kFewWarps; ++o) {
+                const unsigned other = __shfl_sync(ALL, w_key, o);
+                ahead += (other > w_key) | ((other == w_key) & (o < lane));
+            }
+            const unsigned t = __reduce_max_sync(ALL, ahead == want - 1 ? w_key : 0u);
+            if (lane == 0) s_thr = max(1u, t);
         }
-        const unsigned thr = max(1u, __reduce_max_sync(ALL, ahead == want - 1 ? w_key : 0u));
+        __syncthreads();
+        const unsigned thr = s_thr;
         if (mine >= thr)
             scan([&](unsigned k, int at_group) {
                 if (k >= thr) {
@@ -556,6 +563,8 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float4 *part, int parts, long long vecs,
                                                         void *out)
 {
+    chain_wait();
+    chain_go();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= vecs) return;
     float4 a = __ldcs(part + i);
@@ -578,6 +587,8 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float4 *part, int 
 __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long long ld, int rows, int vecs,
                                                         __nv_bfloat16 *planes)
 {
+    chain_wait();
+    chain_go();
     const long long total = (long long)rows * vecs;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= total) return;
@@ -606,6 +617,7 @@ __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long lon
 template <bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p)
 {
+    chain_go();
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (row >= p.N) return;
@@ -631,16 +643,17 @@ cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void
 {
     const long long vecs = elems / 4;
     const unsigned grid = (unsigned)((vecs + 255) / 256);
-    if (bf16) sum_parts_kernel<true><<<grid, 256, 0, s>>>(reinterpret_cast<const float4 *>(part), parts, vecs, out);
-    else sum_parts_kernel<false><<<grid, 256, 0, s>>>(reinterpret_cast<const float4 *>(part), parts, vecs, out);
-    return cudaGetLastError();
+    return launch_chained(bf16 ? sum_parts_kernel<true> : sum_parts_kernel<false>, dim3(grid), 256, 0, s,
+                          reinterpret_cast<const float4 *>(part), parts, vecs, out);
 }
 
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             cudaStream_t s)
+                             bool chained, cudaStream_t s)
 {
     const long long vecs = (long long)rows * (d / 8);
-    split_f32_kernel<<<(unsigned)((vecs + 255) / 256), 256, 0, s>>>(x, ld, rows, d / 8, planes);
+    const unsigned grid = (unsigned)((vecs + 255) / 256);
+    if (chained) return launch_chained(split_f32_kernel, dim3(grid), 256, 0, s, x, ld, rows, d / 8, planes);
+    split_f32_kernel<<<grid, 256, 0, s>>>(x, ld, rows, d / 8, planes);
     return cudaGetLastError();
 }
 
@@ -655,32 +668,22 @@ cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
 cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream_t s)
 {
     const unsigned grid = (unsigned)p.N;
-    if (bf16 && p.full) logprob_few_merge_kernel<true, true><<<grid, kFewThreads, 0, s>>>(p);
-    else if (bf16) logprob_few_merge_kernel<true, false><<<grid, kFewThreads, 0, s>>>(p);
-    else if (p.full) logprob_few_merge_kernel<false, true><<<grid, kFewThreads, 0, s>>>(p);
-    else logprob_few_merge_kernel<false, false><<<grid, kFewThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    auto *kernel = bf16 ? (p.full ? logprob_few_merge_kernel<true, true> : logprob_few_merge_kernel<true, false>)
+                        : (p.full ? logprob_few_merge_kernel<false, true> : logprob_few_merge_kernel<false, false>);
+    return launch_chained(kernel, dim3(grid), kFewThreads, 0, s, p);
 }
 
 template <bool BF16, int LIST>
-void merge(const MergeParams &p, cudaStream_t s)
+cudaError_t merge(const MergeParams &p, cudaStream_t s)
 {
     const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
-    logprob_merge_kernel<BF16, LIST><<<grid, kMergeWarps * 32, 0, s>>>(p);
+    return launch_chained(logprob_merge_kernel<BF16, LIST>, dim3(grid), kMergeWarps * 32, 0, s, p);
 }
 
 cudaError_t launch_logprob_merge(const MergeParams &p, bool bf16, cudaStream_t s)
 {
-    if (bf16) {
-        if (p.list == 0) merge<true, 0>(p, s);
-        else if (p.list == 12) merge<true, 12>(p, s);
-        else merge<true, 20>(p, s);
-    } else {
-        if (p.list == 0) merge<false, 0>(p, s);
-        else if (p.list == 12) merge<false, 12>(p, s);
-        else merge<false, 20>(p, s);
-    }
-    return cudaGetLastError();
+    if (bf16) return p.list == 0 ? merge<true, 0>(p, s) : p.list == 12 ? merge<true, 12>(p, s) : merge<true, 20>(p, s);
+    return p.list == 0 ? merge<false, 0>(p, s) : p.list == 12 ? merge<false, 12>(p, s) : merge<false, 20>(p, s);
 }
 
 } // namespace txl

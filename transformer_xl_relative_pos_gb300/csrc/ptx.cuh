@@ -22,6 +22,11 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 
+// A kernel launched behind another with leave to begin early: wait for the end of the one
+// before it (returns at once in an ordinary launch); give the one behind it leave to begin.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------

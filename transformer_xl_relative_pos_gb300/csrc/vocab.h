@@ -17,6 +17,26 @@ int device_sm_count();
 bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long long rows,
                      long long ld, long long planes, long long plane, unsigned box_rows);
 
+// A launch that may begin while its predecessor in the stream still runs: the kernel waits for
+// that one's end and writes (chain_wait) before it reads or writes anything, so only launch and
+// set-up overlap.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                           const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ---------------------------------------------------------------------------
 // token ids
 // ---------------------------------------------------------------------------
@@ -60,7 +80,7 @@ struct EmbedBwdParams {
     int accumulate;
     unsigned int *status;
 };
-size_t embed_bwd_workspace_bytes(int n, int V, int d);
+size_t embed_bwd_workspace_bytes(int n, int d);
 cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16, void *workspace,
                              cudaStream_t s);
 
@@ -106,6 +126,7 @@ struct GemmParams {
     int n_items;
     int n_pairs;           // products of terms: term (pair_a >> 4 i) & 15 of A by that of B
     unsigned pair_a, pair_b;
+    int chained;           // launched behind another kernel of the same call
     int b_row0;            // offset of B's rows (the vocabulary chunk's first)
     unsigned int *status;
     unsigned long long wait_ns;
@@ -149,7 +170,7 @@ cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void
                              cudaStream_t s);
 // fp32 rows as three bf16 terms: planes [3][rows][d].
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             cudaStream_t s);
+                             bool chained, cudaStream_t s);
 
 struct GradRowsParams {
     const void *h, *w;

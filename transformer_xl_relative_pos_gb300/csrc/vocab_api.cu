@@ -241,7 +241,7 @@ int txl_embed_fwd(const void *tokens, int index_type, const void *emb, long long
 size_t txl_embed_bwd_workspace_size(int n, int V, int d)
 {
     if (check_sizes(n, V, d) != TXL_OK) return 0;
-    return n == 0 ? 0 : txl::embed_bwd_workspace_bytes(n, V, d);
+    return n == 0 ? 0 : txl::embed_bwd_workspace_bytes(n, d);
 }
 
 int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long long dout_stride,
@@ -260,7 +260,7 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
     if (n == 0)
         return accumulate ? TXL_OK
                           : status_of(cudaMemsetAsync(demb, 0, (size_t)V * d * elem(grad_dtype), s));
-    if (!workspace || workspace_bytes < txl::embed_bwd_workspace_bytes(n, V, d)) return TXL_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < txl::embed_bwd_workspace_bytes(n, d)) return TXL_ERR_WORKSPACE;
     if (!on(workspace, 256)) return TXL_ERR_MISALIGNED;
     txl::EmbedBwdParams p{};
     p.status = txl::device_status_word();
@@ -313,10 +313,10 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
 
     if (dtype == TXL_F32) {
         cudaError_t e = txl::launch_split_f32(static_cast<const float *>(h), h_stride, N, d,
-                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), st);
+                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), false, st);
         if (e == cudaSuccess)
             e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), true, st);
         if (e != cudaSuccess) return TXL_ERR_CUDA;
     }
     const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
@@ -326,6 +326,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
         !map_of(&tm_w, ow, V, d, s.few ? 128u : (unsigned)s.bn))
         return TXL_ERR_CUDA;
     GemmParams p{};
+    p.chained = dtype == TXL_F32;
     p.M = N;
     p.N = V;
     p.V = V;
@@ -443,16 +444,17 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     if (dtype == TXL_F32) {
         if (e == cudaSuccess)
             e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), d, N, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), true, st);
         if (e == cudaSuccess)
             e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), true, st);
     }
     if (e != cudaSuccess) return TXL_ERR_CUDA;
     const Operand oh = operand(ws + g.live, d, ws + g.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + g.w_planes, V, d, dtype);
 
     GemmParams base{};
+    base.chained = 1;
     base.status = status;
     base.wait_ns = txl::wait_limit_ns();
     base.V = V;
