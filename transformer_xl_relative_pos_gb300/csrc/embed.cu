@@ -107,19 +107,11 @@ struct SortParams {
     unsigned int *status;
 };
 
-__device__ __forceinline__ void cluster_sync_all()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // A word of another block's shared memory (the same place in it).
 __device__ __forceinline__ int cluster_word(const int *p, int block)
 {
-    uint32_t at;
     int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at)
-                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(block));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, (uint32_t)block)) : "memory");
     return v;
 }
 

@@ -25,19 +25,26 @@ namespace {
 
 using namespace ptx;
 
-constexpr int BM = 128, BK = 64, NS = 4, MAX_BN = 256;
+constexpr int BM = 128, BK = 64, MAX_BN = 256;
 constexpr int A_BYTES = BM * BK * 2;
-constexpr int B_BYTES = MAX_BN * BK * 2;
-constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int OFF_BAR = NS * STAGE;
-constexpr int N_BAR = 2 * NS + 4;
-constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
-constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
-constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
+constexpr int RING = 192 * 1024;
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
+constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
 
-static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
+// A block alone multiplies 128 x bn tiles; a pair of blocks 256 x bn, each holding half of
+// B's columns, so that a block reads a third less from L2 for the same work (ring stages of 32
+// instead of 48 KB, six instead of four).
+template <bool PAIR>
+struct Ring {
+    static constexpr int B_BYTES = MAX_BN * BK * 2 / (PAIR ? 2 : 1);
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int NS = RING / STAGE;
+    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 4) * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
+    static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
+};
 
 enum Mode { kStats, kGrad, kDh, kDw };
 
@@ -168,23 +175,28 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
     }
 }
 
-template <Mode MODE, int LIST>
+template <Mode MODE, int LIST, bool PAIR>
 __global__ void __launch_bounds__(256, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const GemmParams p)
 {
     constexpr bool A_MN = MODE == kDw, B_MN = MODE == kDh || MODE == kDw;
+    using R = Ring<PAIR>;
+    constexpr int NS = R::NS, STAGE = R::STAGE, BLOCKS = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / BLOCKS, units = gridDim.x / BLOCKS;  // block or pair
 
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+    // full (counted on block 0 of a pair), empty, accumulators full and empty (block 0)
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::OFF_BAR);
     uint64_t *empty = full + NS;
     uint64_t *acc_full = empty + NS;
     uint64_t *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + R::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + R::OFF_MISC + 4);
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(full + s, 1);
@@ -192,17 +204,23 @@ __global__ void __launch_bounds__(256, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + s, 1);
-            mbar_init(acc_empty + s, 128);
+            mbar_init(acc_empty + s, 4 * BLOCKS);  // (the epilogue's warps)
         }
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 2) {
-        tmem_alloc(tmem_slot, TM_COLS);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(tmem_slot, TM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, TM_COLS);
+            tmem_relinquish();
+        }
         tc_fence_before_sync();
     }
     __syncthreads();
+    if (PAIR) cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint64_t wait_ns = p.wait_ns;
@@ -214,32 +232,38 @@ __global__ void __launch_bounds__(256, 1)
         if (lane == 0) {
             prefetch_tensormap(&tm_a);
             prefetch_tensormap(&tm_b);
+            const int own_bn = p.bn / BLOCKS;  // columns of B in this block
+            const uint32_t stage_tx = (uint32_t)(A_BYTES + own_bn * BK * 2) * BLOCKS;
             bool ok = true;
             int it = 0;  // stages filled
-            for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
+            for (int item = unit; item < p.n_items && ok; item += units) {
                 const int nt = item_tiles<MODE>(p, item);
                 for (int t = 0; t < nt && ok; ++t) {
                     const Tile w = item_tile<MODE>(p, item, t);
-                    const int m0 = w.m * BM, n0 = w.n * p.bn;
+                    const int m0 = (w.m * BLOCKS + rank) * BM, n0 = w.n * p.bn + rank * own_bn;
                     for (int pr = 0; pr < p.n_pairs && ok; ++pr) {
                         const int pa = (p.pair_a >> (4 * pr)) & 15, pb = (p.pair_b >> (4 * pr)) & 15;
                         for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
                             const int s = it % NS;
                             if (!(ok = mbar_wait(empty + s, ((it / NS) & 1) ^ 1, abort_flag, wait_ns))) break;
                             uint8_t *st = smem + s * STAGE;
-                            mbar_arrive_expect_tx(full + s, A_BYTES + p.bn * BK * 2);
+                            if (rank == 0) mbar_arrive_expect_tx(full + s, stage_tx);
+                            const uint32_t bar = PAIR ? cluster_addr(full + s, 0) : 0u;
+                            auto load = [&](uint8_t *dst, const CUtensorMap *map, int c0, int c1, int c2) {
+                                if (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+                                else tma_load_3d(dst, map, full + s, c0, c1, c2);
+                            };
                             if (A_MN) {
                                 for (int x = 0; x < BM / 64; ++x)
-                                    tma_load_3d(st + x * SLAB, &tm_a, full + s, m0 + x * 64, kb * BK, pa);
+                                    load(st + x * SLAB, &tm_a, m0 + x * 64, kb * BK, pa);
                             } else {
-                                tma_load_3d(st, &tm_a, full + s, kb * BK, m0, pa);
+                                load(st, &tm_a, kb * BK, m0, pa);
                             }
                             if (B_MN) {
-                                for (int x = 0; x < p.bn / 64; ++x)
-                                    tma_load_3d(st + A_BYTES + x * SLAB, &tm_b, full + s, n0 + x * 64,
-                                                p.b_row0 + kb * BK, pb);
+                                for (int x = 0; x < own_bn / 64; ++x)
+                                    load(st + A_BYTES + x * SLAB, &tm_b, n0 + x * 64, p.b_row0 + kb * BK, pb);
                             } else {
-                                tma_load_3d(st + A_BYTES, &tm_b, full + s, kb * BK, p.b_row0 + n0, pb);
+                                load(st + A_BYTES, &tm_b, kb * BK, p.b_row0 + n0, pb);
                             }
                             ++it;
                         }
@@ -249,14 +273,22 @@ __global__ void __launch_bounds__(256, 1)
             if (!ok) {
                 atomicOr(p.status, TXL_STATUS_TIMEOUT);
                 *abort_flag = 1;
+                // copies in flight land before the block ends: counted on block 0's barriers, which
+                // the other block gives a millisecond
                 const int zero = 0;
-                for (int i = max(0, it - NS); i < it; ++i)
-                    mbar_wait(full + i % NS, (i / NS) & 1, &zero, wait_ns);
+                if (rank == 0) {
+                    for (int i = max(0, it - NS); i < it; ++i)
+                        mbar_wait(full + i % NS, (i / NS) & 1, &zero, wait_ns);
+                } else {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < 1000000ull) {
+                    }
+                }
             }
         }
     } else if (warp == 1) {
-        // ===================== MMA issuer =======================================
-        const uint32_t ID = idesc_bf16_f32(BM, p.bn, B_MN) | (A_MN ? 1u << 15 : 0u);
+        // ===================== MMA issuer (block 0 of a pair) ====================
+        const uint32_t ID = idesc_bf16_f32(BM * BLOCKS, p.bn, B_MN) | (A_MN ? 1u << 15 : 0u);
         const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + A_BYTES);
         const uint64_t dA = A_MN ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
         const uint64_t dB = B_MN ? sdesc_sw128_mn(b0, SLAB) : sdesc_sw128(b0);
@@ -267,9 +299,13 @@ __global__ void __launch_bounds__(256, 1)
                          : "=r"(el));
             return el != 0;
         };
+        auto commit = [&](uint64_t *bar) {
+            if (PAIR) mma_commit_pair(bar);
+            else mma_commit(bar);
+        };
         bool ok = true;
         int it = 0, tile = 0;
-        for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
+        for (int item = unit; item < p.n_items && ok && rank == 0; item += units) {
             const int nt = item_tiles<MODE>(p, item);
             for (int t = 0; t < nt && ok; ++t) {
                 const Tile w = item_tile<MODE>(p, item, t);
@@ -287,15 +323,18 @@ __global__ void __launch_bounds__(256, 1)
                     const uint64_t off = (uint64_t)((s * STAGE) >> 4);
                     if (elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            mma_bf16_ss(acc, dA + off + kk * STEP_A, dB + off + kk * STEP_B, ID,
-                                        (k > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit(empty + s);
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint64_t a = dA + off + kk * STEP_A, b = dB + off + kk * STEP_B;
+                            const uint32_t more = k > 0 || kk > 0 ? 1u : 0u;
+                            if (PAIR) mma_bf16_ss_pair(acc, a, b, ID, more);
+                            else mma_bf16_ss(acc, a, b, ID, more);
+                        }
+                        commit(empty + s);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (elect()) mma_commit(acc_full + buf);
+                if (elect()) commit(acc_full + buf);
                 __syncwarp();
                 ++tile;
             }
@@ -306,7 +345,7 @@ __global__ void __launch_bounds__(256, 1)
                 atomicOr(p.status, TXL_STATUS_TIMEOUT);
                 *abort_flag = 1;
             }
-            if (elect()) mma_commit(acc_full + (tile & 1));
+            if (elect()) commit(acc_full + (tile & 1));
             __syncwarp();
             const int zero = 0;
             mbar_wait(acc_full + (tile & 1), (tile >> 1) & 1, &zero, wait_ns);
@@ -320,14 +359,14 @@ __global__ void __launch_bounds__(256, 1)
         const float zscale = p.scale * uncut_scale(p.kb * (BK / 16)), c2 = zscale * kLog2e;
         bool ok = true;
         int tile = 0;
-        for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
+        for (int item = unit; item < p.n_items && ok; item += units) {
             const int nt = item_tiles<MODE>(p, item);
             RowStats<LIST> r;
             int target = -1;
             float g1 = 0.f, ge = 0.f, lse = 0.f, ent = 0.f, lpt = 0.f;
             bool live = false;
             if (MODE == kStats || MODE == kGrad) {
-                const int m = item_tile<MODE>(p, item, 0).m * BM + row;
+                const int m = (item_tile<MODE>(p, item, 0).m * BLOCKS + rank) * BM + row;
                 if (m < p.M) {
                     if (p.targets) target = token_at(p.targets, p.index_bytes, m, p.V, p.status);
                     if (MODE == kGrad) {
@@ -351,7 +390,7 @@ __global__ void __launch_bounds__(256, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const int m = w.m * BM + row, n0 = w.n * p.bn;
+                const int m = (w.m * BLOCKS + rank) * BM + row, n0 = w.n * p.bn;
                 // (a warp whose rows lie behind the last has nothing to do)
                 const int cols = m - lane < p.M ? min(p.bn, p.N - n0) : 0;
 #pragma unroll 1
@@ -426,10 +465,14 @@ __global__ void __launch_bounds__(256, 1)
                     }
                 }
                 tc_fence_before_sync();
-                mbar_arrive(acc_empty + buf);
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(cluster_addr(acc_empty + buf, 0));
+                    else mbar_arrive(acc_empty + buf);
+                }
             }
             if (MODE == kStats && ok) {
-                const int s = item / p.mb, m = (item - s * p.mb) * BM + row;
+                const int s = item / p.mb, m = ((item - s * p.mb) * BLOCKS + rank) * BM + row;
                 if (m < p.M) {
                     p.stats[(long long)s * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
 #pragma unroll
@@ -449,29 +492,36 @@ __global__ void __launch_bounds__(256, 1)
     }
 
     __syncthreads();
+    if (PAIR) cluster_sync_all();
     if (warp == 2) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, TM_COLS);
+        if (PAIR) tmem_dealloc_pair(tmem, TM_COLS);
+        else tmem_dealloc(tmem, TM_COLS);
     }
+}
+
+template <Mode MODE, int LIST, bool PAIR>
+cudaError_t launch_units(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p, cudaStream_t s)
+{
+    static bool attr_set[64] = {};  // the attribute is set once per device
+    constexpr int BLOCKS = PAIR ? 2 : 1, SMEM = Ring<PAIR>::SMEM_BYTES;
+    auto *kernel = vocab_gemm_kernel<MODE, LIST, PAIR>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const unsigned grid = (unsigned)(min(p.n_items, device_sm_count() / BLOCKS) * BLOCKS);
+    return launch_grid(kernel, dim3(grid), 256, SMEM, s, p.chained != 0, BLOCKS, a, b, p);
 }
 
 template <Mode MODE, int LIST>
 cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p, cudaStream_t s)
 {
-    static bool attr_set[64] = {};  // the attribute is set once per device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(vocab_gemm_kernel<MODE, LIST>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_set[dev] = true;
-    }
-    const unsigned grid = (unsigned)min(p.n_items, device_sm_count());
-    if (p.chained) return launch_chained(vocab_gemm_kernel<MODE, LIST>, dim3(grid), 256, SMEM_BYTES, s, a, b, p);
-    vocab_gemm_kernel<MODE, LIST><<<grid, 256, SMEM_BYTES, s>>>(a, b, p);
-    return cudaGetLastError();
+    return p.pair ? launch_units<MODE, LIST, true>(a, b, p, s) : launch_units<MODE, LIST, false>(a, b, p, s);
 }
 
 } // namespace

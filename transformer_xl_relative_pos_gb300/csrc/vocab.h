@@ -17,24 +17,38 @@ int device_sm_count();
 bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long long rows,
                      long long ld, long long planes, long long plane, unsigned box_rows);
 
-// A launch that may begin while its predecessor in the stream still runs: the kernel waits for
-// that one's end and writes (chain_wait) before it reads or writes anything, so only launch and
-// set-up overlap.
+// A launch in clusters of `cluster` blocks.  Chained: it may begin while its predecessor in the
+// stream still runs; the kernel waits for that one's end and writes (chain_wait) before it reads
+// or writes anything, so only launch and set-up overlap.
 template <typename... P, typename... A>
-cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
-                           const A &...args)
+cudaError_t launch_grid(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                        bool chained, unsigned cluster, const A &...args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2] = {};
+    cfg.attrs = attr;
+    if (chained) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                           const A &...args)
+{
+    return launch_grid(kernel, grid, threads, smem, s, true, 1, args...);
 }
 
 // ---------------------------------------------------------------------------
@@ -116,7 +130,7 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// One GEMM over 128 x bn tiles, bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
+// One GEMM over 128 x bn tiles (256 x bn for pairs of blocks), bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
 // Which operands, and what becomes of a tile, is the kernel's mode.
 struct GemmParams {
     int M, N;              // rows and columns of the product
@@ -127,6 +141,7 @@ struct GemmParams {
     int n_pairs;           // products of terms: term (pair_a >> 4 i) & 15 of A by that of B
     unsigned pair_a, pair_b;
     int chained;           // launched behind another kernel of the same call
+    int pair;              // two blocks a tile: 256 rows
     int b_row0;            // offset of B's rows (the vocabulary chunk's first)
     unsigned int *status;
     unsigned long long wait_ns;

@@ -14,6 +14,7 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? TXL_OK : TXL_ERR_CUDA; 
 cudaStream_t stream_of(void *s) { return static_cast<cudaStream_t>(s); }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 long long up64(long long x) { return (x + 63) / 64 * 64; }
+long long up128(long long x) { return (x + 127) / 128 * 128; }
 int elem(int dtype) { return dtype == TXL_BF16 ? 2 : 4; }
 
 constexpr int kMaxRows = 1 << 28;   // rows, tokens
@@ -53,18 +54,12 @@ int check_sizes(int n, int V, int d)
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// Columns of a tile over `cols` columns: as few tiles as 256 columns allow, of equal width.
-int tile_columns(long long cols)
-{
-    const int n = ceil_div(cols, 256);
-    return (int)std::min<long long>(256, up64(ceil_div(cols, n)));
-}
 
-// Parts of `steps` equal steps for each of `units` blocks of work, one block per SM at a time:
+// Parts of `steps` equal steps for each of `units` units of work, `blocks` SMs each:
 // waves * (steps of the longest part + what a part costs besides).
-int choose_parts(long long units, int steps, int most, double extra)
+int choose_parts(long long units, int steps, int most, double extra, int blocks)
 {
-    const int sms = txl::device_sm_count();
+    const int sms = txl::device_sm_count() / blocks;
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= std::min(steps, most); ++s) {
@@ -82,6 +77,7 @@ struct StatsPlan {
     bool few;                     // the vocabulary in the tiles' rows
     bool full;                    // ... and the logits written
     int mb, nb, bn, splits, list;
+    bool pair;
     size_t h_planes, w_planes, stats, val, id, keys, target_z, total;  // offsets
 };
 
@@ -99,10 +95,11 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
         s.full = top > 0 && (long long)N * 16 <= d && N <= 64;
         s.splits = std::min(s.nb, std::min(txl::device_sm_count(), txl::kMaxStatSplits));
     } else {
-        s.mb = ceil_div(N, 128);
-        s.bn = std::min<long long>(256, up64(V));
+        s.pair = true;
+        s.mb = ceil_div(N, 256);
+        s.bn = std::min<long long>(256, up128(V));
         s.nb = ceil_div(V, s.bn);
-        s.splits = choose_parts(s.mb, s.nb, txl::kMaxRowSplits, 0.5);
+        s.splits = choose_parts(s.mb, s.nb, txl::kMaxRowSplits, 0.5, 2);
     }
     s.list = txl::list_length(top);
     size_t o = 0;
@@ -130,7 +127,9 @@ constexpr size_t kGradBytes = (size_t)1 << 30;  // of G in the workspace: vocabu
 struct GradPlan {
     int chunk, chunks;            // vocabulary rows at a time
     int pieces;                   // terms of G
-    int bn, mb_h, mb_w, nb;       // tiles of dh and of a chunk's dW
+    bool pair_g, pair_h, pair_w;  // pairs of blocks for G, dh, dW
+    int bn_g;                     // columns of G's tiles
+    int bn, mb_g, mb_h, mb_w, nb; // ... of dh's and a chunk's dW's; rows of tiles
     int split_h, split_w, parts_h;
     long long g_ld, g_plane;
     size_t live, target_logp, h_planes, w_planes, g, part_h, part_w, total;
@@ -146,15 +145,18 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
     g.chunks = ceil_div(V, g.chunk);
     if (g.chunks > 1) g.chunk = (int)up64(ceil_div(V, g.chunks));
     g.chunks = ceil_div(V, g.chunk);
-    g.g_ld = up64(g.chunk);
+    g.g_ld = up128(g.chunk);
     g.g_plane = g.g_ld * N;
-    g.bn = tile_columns(d);
+    g.pair_g = g.pair_h = g.pair_w = true;
+    g.bn_g = (int)std::min<long long>(256, up128(g.chunk));
+    g.bn = (int)up128(ceil_div(d, ceil_div(d, 256)));
     g.nb = ceil_div(d, g.bn);
-    g.mb_h = ceil_div(N, 128);
-    g.mb_w = ceil_div(g.chunk, 128);
+    g.mb_g = ceil_div(N, g.pair_g ? 256 : 128);
+    g.mb_h = ceil_div(N, g.pair_h ? 256 : 128);
+    g.mb_w = ceil_div(g.chunk, g.pair_w ? 256 : 128);
     // (a part costs its tile's write and the sum's reads: about eight steps of 64)
-    g.split_h = choose_parts((long long)g.mb_h * g.nb, ceil_div(g.chunk, 64), 16, 8.0);
-    g.split_w = choose_parts((long long)g.mb_w * g.nb, ceil_div(N, 64), 16, 8.0);
+    g.split_h = choose_parts((long long)g.mb_h * g.nb, ceil_div(g.chunk, 64), 16, 8.0, g.pair_h ? 2 : 1);
+    g.split_w = choose_parts((long long)g.mb_w * g.nb, ceil_div(N, 64), 16, 8.0, g.pair_w ? 2 : 1);
     g.parts_h = g.chunks * g.split_h;
     size_t o = 0;
     const size_t row = (size_t)d * 2 * txl::kMaxPieces;
@@ -323,10 +325,11 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
     CUtensorMap tm_h, tm_w;
     if (!map_of(&tm_h, oh, N, d, s.few ? (unsigned)s.bn : 128u) ||
-        !map_of(&tm_w, ow, V, d, s.few ? 128u : (unsigned)s.bn))
+        !map_of(&tm_w, ow, V, d, s.few ? 128u : (unsigned)(s.pair ? s.bn / 2 : s.bn)))
         return TXL_ERR_CUDA;
     GemmParams p{};
     p.chained = dtype == TXL_F32;
+    p.pair = s.pair;
     p.M = N;
     p.N = V;
     p.V = V;
@@ -470,9 +473,9 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.g_ld = g.g_ld;
     base.g_plane = g.g_plane;
     base.g_pieces = g.pieces;
-    const int bn_v = std::min<long long>(256, up64(std::min(V, g.chunk)));
+    const int bn_v = g.bn_g;
     CUtensorMap h_rows, w_rows, h_cols, w_cols;
-    if (!map_of(&h_rows, oh, N, d, 128) || !map_of(&w_rows, ow, V, d, (unsigned)bn_v) ||
+    if (!map_of(&h_rows, oh, N, d, 128) || !map_of(&w_rows, ow, V, d, (unsigned)(g.pair_g ? bn_v / 2 : bn_v)) ||
         !map_of(&h_cols, oh, N, d, 64) || !map_of(&w_cols, ow, V, d, 64))
         return TXL_ERR_CUDA;
     for (int c = 0; c < g.chunks; ++c) {
@@ -481,7 +484,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         GemmParams p = base;
         p.M = N;
         p.N = cols;
-        p.mb = g.mb_h;
+        p.pair = g.pair_g;
+        p.mb = g.mb_g;
         p.bn = bn_v;
         p.nb = ceil_div(cols, bn_v);
         p.kb = ceil_div(d, 64);
@@ -497,6 +501,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             GemmParams q = base;
             q.M = N;
             q.N = d;
+            q.pair = g.pair_h;
             q.mb = g.mb_h;
             q.nb = g.nb;
             q.bn = g.bn;
@@ -518,7 +523,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             GemmParams q = base;
             q.M = cols;
             q.N = d;
-            q.mb = ceil_div(cols, 128);
+            q.pair = g.pair_w;
+            q.mb = ceil_div(cols, g.pair_w ? 256 : 128);
             q.nb = g.nb;
             q.bn = g.bn;
             q.kb = ceil_div(N, 64);
