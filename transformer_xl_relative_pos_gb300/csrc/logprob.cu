@@ -30,6 +30,9 @@ constexpr int A_BYTES = BM * BK * 2;
 constexpr int RING = 192 * 1024;
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
 constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
+constexpr int OUT_BYTES = BM * 128;
+constexpr int kEpiWarps = 8;                      // two halves of a tile's columns, four warps each
+constexpr int kThreads = (4 + kEpiWarps) * 32;
 
 // A block alone multiplies 128 x bn tiles; a pair of blocks 256 x bn, each holding half of
 // B's columns, so that a block reads a third less from L2 for the same work (ring stages of 32
@@ -39,7 +42,8 @@ struct Ring {
     static constexpr int B_BYTES = MAX_BN * BK * 2 / (PAIR ? 2 : 1);
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int NS = RING / STAGE;
-    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int OFF_OUT = NS * STAGE;    // a tile of 128 rows x 128 bytes per half
+    static constexpr int OFF_BAR = OFF_OUT + 2 * OUT_BYTES;
     static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
     static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
@@ -175,10 +179,26 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
     }
 }
 
+// Barrier of the warps of one half of the epilogue; whether any of its threads says so.
+__device__ __forceinline__ void half_sync(int half)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kEpiWarps * 16) : "memory");
+}
+__device__ __forceinline__ bool half_any(int half, bool x)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred b, %2, %3, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "r"(1 + half), "n"(kEpiWarps * 16)
+                 : "memory");
+    return r != 0;
+}
+
 template <Mode MODE, int LIST, bool PAIR>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                      const GemmParams p)
+                      const __grid_constant__ CUtensorMap tm_out, const GemmParams p)
 {
     constexpr bool A_MN = MODE == kDw, B_MN = MODE == kDh || MODE == kDw;
     using R = Ring<PAIR>;
@@ -204,7 +224,7 @@ __global__ void __launch_bounds__(256, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + s, 1);
-            mbar_init(acc_empty + s, 4 * BLOCKS);  // (the epilogue's warps)
+            mbar_init(acc_empty + s, kEpiWarps * BLOCKS);  // (the epilogue's warps)
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -351,12 +371,33 @@ __global__ void __launch_bounds__(256, 1)
             mbar_wait(acc_full + (tile & 1), (tile >> 1) & 1, &zero, wait_ns);
         }
     } else if (warp >= 4) {
-        // ===================== epilogue: thread = row ===========================
-        const int wq = warp - 4;
+        // ===================== epilogue: thread = row, half of the columns =======
+        const int wq = warp & 3, half = (warp - 4) >> 2;
         const int row = wq * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
+        uint8_t *out = smem + R::OFF_OUT + half * OUT_BYTES;
+        const bool issuer = wq == 0 && lane == 0;  // of the half's stores
         constexpr float kLog2e = 1.4426950408889634f;
         const float zscale = p.scale * uncut_scale(p.kb * (BK / 16)), c2 = zscale * kLog2e;
+        // 128 bytes of each row, turned by the swizzle, then one store of the half's 128 rows
+        auto store = [&](const uint4 (&v)[8], int c0, int m0, int plane) {
+            if (issuer) bulk_wait_read();
+            half_sync(half);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4 *>(out + row * 128 + ((q ^ (row & 7)) << 4)) = v[q];
+            fence_proxy_async_smem();
+            half_sync(half);
+            if (issuer) {
+                tma_store_3d(&tm_out, out, c0, m0, plane);
+                bulk_commit();
+            }
+        };
+        auto pack = [](const float (&v)[32], uint4 *o) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                  pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        };
         bool ok = true;
         int tile = 0;
         for (int item = unit; item < p.n_items && ok; item += units) {
@@ -364,21 +405,20 @@ __global__ void __launch_bounds__(256, 1)
             RowStats<LIST> r;
             int target = -1;
             float g1 = 0.f, ge = 0.f, lse = 0.f, ent = 0.f, lpt = 0.f;
-            bool live = false;
             if (MODE == kStats || MODE == kGrad) {
                 const int m = (item_tile<MODE>(p, item, 0).m * BLOCKS + rank) * BM + row;
-                if (m < p.M) {
-                    if (p.targets) target = token_at(p.targets, p.index_bytes, m, p.V, p.status);
-                    if (MODE == kGrad) {
-                        if (target >= 0 && p.dlogp) g1 = p.dlogp[m] * p.scale;
-                        if (p.dentropy) {
-                            ge = p.dentropy[m] * p.scale;
-                            ent = p.entropy[m];
-                        }
-                        lse = p.lse[m];
+                if (m < p.M && p.targets) target = token_at(p.targets, p.index_bytes, m, p.V, p.status);
+                // (rows without a part: zeros all through, their states have been cleared)
+                if (MODE == kGrad && m < p.M && (target >= 0 || (p.dentropy && p.dentropy[m] != 0.f))) {
+                    if (target >= 0) {
+                        g1 = p.dlogp[m] * p.scale;
                         lpt = p.target_logp[m];
-                        live = target >= 0 || (p.dentropy && p.dentropy[m] != 0.f);
                     }
+                    if (p.dentropy) {
+                        ge = p.dentropy[m] * p.scale;
+                        ent = p.entropy[m];
+                    }
+                    lse = p.lse[m];
                 }
                 if (MODE == kStats) r.clear();
             }
@@ -388,80 +428,100 @@ __global__ void __launch_bounds__(256, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (tile >> 1) & 1, abort_flag, wait_ns)) &&
                      !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
+                // (the half's warps meet at its barriers: they leave together)
+                if (MODE != kStats) ok = !half_any(half, !ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const int m = (w.m * BLOCKS + rank) * BM + row, n0 = w.n * p.bn;
-                // (a warp whose rows lie behind the last has nothing to do)
-                const int cols = m - lane < p.M ? min(p.bn, p.N - n0) : 0;
-#pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
-                    uint32_t raw[32];
+                const int m0 = (w.m * BLOCKS + rank) * BM, n0 = w.n * p.bn;
+                // (a block whose rows lie behind the last has nothing to write)
+                const int c_lo = half * (p.bn / 2), c_hi = m0 < p.M ? min((half + 1) * (p.bn / 2), p.N - n0) : 0;
+                const bool empty_part = w.kb_lo == w.kb_hi;  // (nothing was accumulated)
+                auto logits = [&](uint32_t (&raw)[32], int c) {
                     tmem_ld32(tq + buf * MAX_BN + c, raw);
                     tmem_ld_wait(raw);
-                    const int cnt = min(32, cols - c);
-                    if (w.kb_lo == w.kb_hi)  // (an empty part: nothing was accumulated)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) raw[i] = 0;
-                    if (MODE == kStats) {
+                };
+                if (MODE == kStats) {
+                    // (a warp whose rows lie behind the last has nothing to do)
+                    const int stop = m0 + wq * 32 < p.M ? c_hi : 0;
+#pragma unroll 1
+                    for (int c = c_lo; c < stop; c += 32) {
+                        uint32_t raw[32];
+                        logits(raw, c);
+                        const int cnt = min(32, c_hi - c);
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = i < cnt ? __uint_as_float(raw[i]) * c2 : -INFINITY;
                         take<LIST>(r, v, n0 + c, cnt, target);
-                    } else if (MODE == kGrad) {
-                        float v[32];
-                        const int at = target - (p.b_row0 + n0 + c);
+                    }
+                } else if (MODE == kGrad) {
+                    const int at0 = target < 0 ? -1 : target - p.b_row0 - n0;  // column of the tile
+#pragma unroll 1
+                    for (int c = c_lo; c < c_hi; c += 64) {
+                        float v[2][32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float lp = fmaf(__uint_as_float(raw[i]), zscale, -lse);
-                            if (i == at) lp = lpt;
-                            const float pr = ex2(lp * kLog2e);
-                            float f = g1;
-                            if (p.dentropy) f = fmaf(ge, fmaxf(lp, -1e30f) + ent, f);
-                            v[i] = -pr * f + (i == at ? g1 : 0.f);
-                            if (!live) v[i] = 0.f;
-                        }
-                        if (m < p.M) {
-                            for (int g = 0; g < p.g_pieces; ++g) {
-                                uint4 *dst = reinterpret_cast<uint4 *>(p.g + g * p.g_plane + (long long)m * p.g_ld + n0 + c);
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t raw[32];
+                            logits(raw, c + 32 * x);
+                            if (p.dentropy) {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                                                        pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                                                        pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-                                if (g + 1 < p.g_pieces)
+                                for (int i = 0; i < 32; ++i) {
+                                    const float lp = fmaf(__uint_as_float(raw[i]), zscale, -lse);
+                                    v[x][i] = -ex2(lp * kLog2e) * fmaf(ge, fmaxf(lp, -1e30f) + ent, g1);
+                                }
+                            } else {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) {
-                                        const float hi = __bfloat162float(__float2bfloat16_rn(v[i]));
-                                        v[i] = isfinite(v[i]) ? v[i] - hi : 0.f;
-                                    }
+                                for (int i = 0; i < 32; ++i)
+                                    v[x][i] = ex2(fmaf(__uint_as_float(raw[i]), zscale, -lse) * kLog2e) * -g1;
+                            }
+                            const int at = at0 - c - 32 * x;
+                            if (__any_sync(0xffffffffu, (unsigned)at < 32u && target >= 0)) {
+                                // the target's element, from its exact logit
+                                const float pt = ex2(lpt * kLog2e);
+                                const float f = p.dentropy ? fmaf(ge, fmaxf(lpt, -1e30f) + ent, g1) : g1;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i == at && target >= 0) v[x][i] = fmaf(-pt, f, g1);
                             }
                         }
-                    } else if (m < p.M) {
-                        const int s = p.part ? item / (p.mb * p.nb) : 0;
-                        const long long at = ((long long)s * p.M + m) * p.N + n0 + c;
-                        // (cnt is a multiple of 8: rows of the operands are)
-                        if (p.part || !p.out_bf16) {
-                            const float f = uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16));
+                        for (int g = 0; g < p.g_pieces; ++g) {
+                            uint4 o[8];
+                            pack(v[0], o);
+                            pack(v[1], o + 4);
+                            store(o, n0 + c, m0, g);
+                            if (g + 1 < p.g_pieces)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f);
-                            float *dst = (p.part ? p.part : static_cast<float *>(p.out)) + at;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (4 * q < cnt)
-                                    reinterpret_cast<uint4 *>(dst)[q] =
-                                        make_uint4(raw[4 * q], raw[4 * q + 1], raw[4 * q + 2], raw[4 * q + 3]);
-                        } else {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
-                            const float *v = reinterpret_cast<const float *>(raw);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (8 * q < cnt)
-                                    dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                                                        pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                                                        pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                                for (int i = 0; i < 64; ++i) {
+                                    float &y = v[i >> 5][i & 31];
+                                    y = isfinite(y) ? y - __bfloat162float(__float2bfloat16_rn(y)) : 0.f;
+                                }
                         }
+                    }
+                } else if (p.part || !p.out_bf16) {
+                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16));
+#pragma unroll 1
+                    for (int c = c_lo; c < c_hi; c += 32) {
+                        uint32_t raw[32];
+                        logits(raw, c);
+                        uint4 o[8];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            (&o[i >> 2].x)[i & 3] = empty_part ? 0u : __float_as_uint(__uint_as_float(raw[i]) * f);
+                        store(o, n0 + c, m0, p.part ? item / (p.mb * p.nb) : 0);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = c_lo; c < c_hi; c += 64) {
+                        uint4 o[8];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t raw[32];
+                            logits(raw, c + 32 * x);
+                            float v[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = empty_part ? 0.f : __uint_as_float(raw[i]);
+                            pack(v, o + 4 * x);
+                        }
+                        store(o, n0 + c, m0, 0);
                     }
                 }
                 tc_fence_before_sync();
@@ -474,16 +534,18 @@ __global__ void __launch_bounds__(256, 1)
             if (MODE == kStats && ok) {
                 const int s = item / p.mb, m = ((item - s * p.mb) * BLOCKS + rank) * BM + row;
                 if (m < p.M) {
-                    p.stats[(long long)s * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
+                    const long long part = 2 * s + half;
+                    p.stats[part * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
 #pragma unroll
                     for (int j = 0; j < LIST; ++j) {
-                        const long long at = ((long long)s * LIST + j) * p.M + m;
+                        const long long at = (part * LIST + j) * p.M + m;
                         p.list_val[at] = r.val[j];
                         p.list_id[at] = r.id[j];
                     }
                 }
             }
         }
+        if (MODE != kStats && issuer) bulk_wait_all();
         if (!ok && lane == 0) {
             atomicOr(p.status, TXL_STATUS_TIMEOUT);
             *abort_flag = 1;
@@ -501,7 +563,8 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 template <Mode MODE, int LIST, bool PAIR>
-cudaError_t launch_units(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p, cudaStream_t s)
+cudaError_t launch_units(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const GemmParams &p,
+                         cudaStream_t s)
 {
     static bool attr_set[64] = {};  // the attribute is set once per device
     constexpr int BLOCKS = PAIR ? 2 : 1, SMEM = Ring<PAIR>::SMEM_BYTES;
@@ -515,13 +578,14 @@ cudaError_t launch_units(const CUtensorMap &a, const CUtensorMap &b, const GemmP
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const unsigned grid = (unsigned)(min(p.n_items, device_sm_count() / BLOCKS) * BLOCKS);
-    return launch_grid(kernel, dim3(grid), 256, SMEM, s, p.chained != 0, BLOCKS, a, b, p);
+    return launch_grid(kernel, dim3(grid), kThreads, SMEM, s, p.chained != 0, BLOCKS, a, b, out, p);
 }
 
 template <Mode MODE, int LIST>
-cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p, cudaStream_t s)
+cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const GemmParams &p,
+                        cudaStream_t s)
 {
-    return p.pair ? launch_units<MODE, LIST, true>(a, b, p, s) : launch_units<MODE, LIST, false>(a, b, p, s);
+    return p.pair ? launch_units<MODE, LIST, true>(a, b, out, p, s) : launch_units<MODE, LIST, false>(a, b, out, p, s);
 }
 
 } // namespace
@@ -529,26 +593,27 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmPa
 cudaError_t launch_logprob_stats(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
                                  int list, cudaStream_t s)
 {
-    if (list == 0) return launch_gemm<kStats, 0>(a, b, p, s);
-    return list == 12 ? launch_gemm<kStats, 12>(a, b, p, s) : launch_gemm<kStats, 20>(a, b, p, s);
+    // (no tile is stored)
+    if (list == 0) return launch_gemm<kStats, 0>(a, b, a, p, s);
+    return list == 12 ? launch_gemm<kStats, 12>(a, b, a, p, s) : launch_gemm<kStats, 20>(a, b, a, p, s);
 }
 
-cudaError_t launch_logprob_grad(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
-                                cudaStream_t s)
+cudaError_t launch_logprob_grad(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                                const GemmParams &p, cudaStream_t s)
 {
-    return launch_gemm<kGrad, 0>(a, b, p, s);
+    return launch_gemm<kGrad, 0>(a, b, out, p, s);
 }
 
-cudaError_t launch_product_dh(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
-                              cudaStream_t s)
+cudaError_t launch_product_dh(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                              const GemmParams &p, cudaStream_t s)
 {
-    return launch_gemm<kDh, 0>(a, b, p, s);
+    return launch_gemm<kDh, 0>(a, b, out, p, s);
 }
 
-cudaError_t launch_product_dw(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
-                              cudaStream_t s)
+cudaError_t launch_product_dw(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                              const GemmParams &p, cudaStream_t s)
 {
-    return launch_gemm<kDw, 0>(a, b, p, s);
+    return launch_gemm<kDw, 0>(a, b, out, p, s);
 }
 
 } // namespace txl

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
 {
     constexpr unsigned FULL = 0xffffffffu;
     chain_wait();
-    constexpr int PER = kMaxRowSplits / 32, WANT = LIST > 0 ? LIST : 1;
+    constexpr int PER = 2 * kMaxRowSplits / 32, WANT = LIST > 0 ? LIST : 1;
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (row >= p.N) return;

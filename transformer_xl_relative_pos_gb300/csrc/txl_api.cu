@@ -92,17 +92,19 @@ bool make_map(CUtensorMap *map, const void *base, long long rows, long long oute
     return r == CUDA_SUCCESS;
 }
 
-// 3-D bf16 view [planes][rows][inner] (rows ld elements apart) in 64 x box_rows boxes.
+// 3-D bf16 or fp32 view [planes][rows][inner] (rows ld elements apart) in boxes of 128 bytes x
+// box_rows.
 bool encode_planes(CUtensorMap *map, const void *base, long long inner, long long rows, long long ld,
-                   long long planes, long long plane, unsigned box_rows)
+                   long long planes, long long plane, unsigned box_rows, bool f32)
 {
+    const cuuint64_t e = f32 ? 4 : 2;
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)plane * 2};
-    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * e, (cuuint64_t)plane * e};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / e), box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -323,7 +325,13 @@ int device_sm_count() { return sm_count(); }
 bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long long rows,
                      long long ld, long long planes, long long plane, unsigned box_rows)
 {
-    return encode_planes(map, base, inner, rows, ld, planes, plane, box_rows);
+    return encode_planes(map, base, inner, rows, ld, planes, plane, box_rows, false);
+}
+
+bool make_map_planes_f32(CUtensorMap *map, const void *base, long long inner, long long rows,
+                         long long ld, long long planes, long long plane, unsigned box_rows)
+{
+    return encode_planes(map, base, inner, rows, ld, planes, plane, box_rows, true);
 }
 
 } // namespace txl

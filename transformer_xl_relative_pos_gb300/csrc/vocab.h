@@ -16,6 +16,9 @@ int device_sm_count();
 // 64 x box_rows box and 128-byte swizzle.
 bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long long rows,
                      long long ld, long long planes, long long plane, unsigned box_rows);
+// The same of fp32 in 32 x box_rows boxes.
+bool make_map_planes_f32(CUtensorMap *map, const void *base, long long inner, long long rows,
+                         long long ld, long long planes, long long plane, unsigned box_rows);
 
 // A launch in clusters of `cluster` blocks.  Chained: it may begin while its predecessor in the
 // stream still runs; the kernel waits for that one's end and writes (chain_wait) before it reads
@@ -105,7 +108,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16,
 constexpr int kMaxTop = 16;      // alternatives of a row
 constexpr int kSpareTop = 4;     // candidates kept beyond them, for the exact order
 constexpr int kMaxStatSplits = 160;  // vocabulary ranges of a row
-constexpr int kMaxRowSplits = 64;    // ... of more than kFewRows rows
+constexpr int kMaxRowSplits = 32;    // ... of more than kFewRows rows, two halves of tiles each
 constexpr int kFewRows = 256;    // states up to which the vocabulary takes the tiles' rows
 constexpr int kMaxPieces = 3;    // bf16 terms of an fp32 operand
 
@@ -150,20 +153,17 @@ struct GemmParams {
     int index_bytes;
     int V;                 // the whole vocabulary
     float scale;
-    float4 *stats;         // [splits][M]: maximum, sum, weighted sum (log2 units), target's logit
-    float *list_val;       // [splits][list][M]
+    float4 *stats;         // [2 splits][M] (halves of tiles): maximum, sum, weighted sum (log2 units), target's logit
+    float *list_val;       // [2 splits][list][M]
     int *list_id;
     unsigned *group_key;   // few states: [M][nb][32] order of the largest of four logits, or null
     float *logits;         // ... or [M][nb][128] the logits themselves (log2 units; NaN behind V)
     float *target_z;       // few states: [M], log2 units (where there is a target)
     const float *lse, *entropy, *dlogp, *dentropy;  // (the last two may be null)
     const float *target_logp;
-    __nv_bfloat16 *g;      // [g_pieces][M][g_ld]
-    long long g_ld, g_plane;
-    int g_pieces;
+    int g_pieces;          // terms of G
     // products
-    float *part;           // [splits][M][N], or null: out directly
-    void *out;             // [M][N]
+    int part;              // fp32 parts [splits][M][N], or the result directly
     int out_bf16;
 };
 
@@ -173,13 +173,15 @@ cudaError_t launch_logprob_stats(const CUtensorMap &tm_h, const CUtensorMap &tm_
 // `splits` blocks.
 cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p,
                                cudaStream_t s);
-cudaError_t launch_logprob_grad(const CUtensorMap &tm_h, const CUtensorMap &tm_w,
+// tm_g: boxes of 64 columns and 128 rows, for the tiles' stores.
+cudaError_t launch_logprob_grad(const CUtensorMap &tm_h, const CUtensorMap &tm_w, const CUtensorMap &tm_g,
                                 const GemmParams &p, cudaStream_t s);
-// dh = G W (G rows of the vocabulary) and dW = G^T h (contraction over the rows).
-cudaError_t launch_product_dh(const CUtensorMap &tm_g, const CUtensorMap &tm_w, const GemmParams &p,
-                              cudaStream_t s);
-cudaError_t launch_product_dw(const CUtensorMap &tm_g, const CUtensorMap &tm_h, const GemmParams &p,
-                              cudaStream_t s);
+// dh = G W (G rows of the vocabulary) and dW = G^T h (contraction over the rows).  tm_out: the
+// result, or its parts one behind the other, in boxes of 128 bytes of columns and 128 rows.
+cudaError_t launch_product_dh(const CUtensorMap &tm_g, const CUtensorMap &tm_w, const CUtensorMap &tm_out,
+                              const GemmParams &p, cudaStream_t s);
+cudaError_t launch_product_dw(const CUtensorMap &tm_g, const CUtensorMap &tm_h, const CUtensorMap &tm_out,
+                              const GemmParams &p, cudaStream_t s);
 // out = sum over the parts, in their order.
 cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void *out, bool bf16,
                              cudaStream_t s);

@@ -109,8 +109,8 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     s.w_planes = o;
     if (dtype == TXL_F32) o = up256(o + V * row);
     s.stats = o;
-    o = up256(o + (size_t)s.splits * N * sizeof(float4));
-    const size_t lists = s.few ? 0 : (size_t)s.splits * s.list * N * 4;
+    o = up256(o + (size_t)(s.few ? 1 : 2) * s.splits * N * sizeof(float4));
+    const size_t lists = s.few ? 0 : (size_t)2 * s.splits * s.list * N * 4;
     s.val = o;
     o = up256(o + lists);
     s.id = o;
@@ -208,6 +208,15 @@ Operand operand(const void *p, long long ld, const char *planes, int rows, int d
 bool map_of(CUtensorMap *map, const Operand &o, int rows, int d, unsigned box_rows)
 {
     return txl::make_map_planes(map, o.p, d, rows, o.ld, o.planes, o.plane, box_rows);
+}
+
+// A product's parts, or the result, for its tiles' stores.
+bool map_out(CUtensorMap *map, const GemmParams &p, char *base)
+{
+    const long long plane = (long long)p.M * p.N;
+    return p.part || !p.out_bf16
+               ? txl::make_map_planes_f32(map, base, p.N, p.M, p.N, p.part ? p.splits : 1, plane, 128)
+               : txl::make_map_planes(map, base, p.N, p.M, p.N, 1, plane, 128);
 }
 
 } // namespace
@@ -363,7 +372,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     m.full = s.full;
     m.target_z = p.target_z;
     m.nb = s.nb;
-    m.splits = s.splits;
+    m.splits = s.few ? s.splits : 2 * s.splits;
     m.N = N;
     m.V = V;
     m.d = d;
@@ -469,9 +478,6 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.entropy = entropy;
     base.dlogp = dlogp;
     base.dentropy = dentropy;
-    base.g = reinterpret_cast<__nv_bfloat16 *>(ws + g.g);
-    base.g_ld = g.g_ld;
-    base.g_plane = g.g_plane;
     base.g_pieces = g.pieces;
     const int bn_v = g.bn_g;
     CUtensorMap h_rows, w_rows, h_cols, w_cols;
@@ -493,11 +499,11 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         p.n_items = p.mb * p.nb;
         p.b_row0 = v0;
         set_pairs(p, oh.planes, ow.planes);
-        if (txl::launch_logprob_grad(h_rows, w_rows, p, st) != cudaSuccess) return TXL_ERR_CUDA;
         const Operand og = {ws + g.g, g.g_ld, g.pieces, g.g_plane};
+        CUtensorMap g_rows;
+        if (!map_of(&g_rows, og, N, cols, 128)) return TXL_ERR_CUDA;
+        if (txl::launch_logprob_grad(h_rows, w_rows, g_rows, p, st) != cudaSuccess) return TXL_ERR_CUDA;
         if (dh) {
-            CUtensorMap tm_g;
-            if (!map_of(&tm_g, og, N, cols, 128)) return TXL_ERR_CUDA;
             GemmParams q = base;
             q.M = N;
             q.N = d;
@@ -509,17 +515,18 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.splits = g.split_h;
             q.n_items = q.mb * q.nb * q.splits;
             q.b_row0 = v0;
-            q.part = g.parts_h > 1 ? reinterpret_cast<float *>(ws + g.part_h) + (size_t)c * g.split_h * N * d
-                                   : nullptr;
-            q.out = dh;
+            q.part = g.parts_h > 1;
             q.out_bf16 = dtype == TXL_BF16;
+            CUtensorMap out;
+            if (!map_out(&out, q, q.part ? ws + g.part_h + (size_t)c * g.split_h * N * d * 4 : (char *)dh))
+                return TXL_ERR_CUDA;
             set_pairs(q, dtype == TXL_F32 ? g.pieces : 1, ow.planes);
-            if (txl::launch_product_dh(tm_g, w_cols, q, st) != cudaSuccess) return TXL_ERR_CUDA;
+            if (txl::launch_product_dh(g_rows, w_cols, out, q, st) != cudaSuccess) return TXL_ERR_CUDA;
         }
         if (dw) {
             CUtensorMap tm_g;
             if (!map_of(&tm_g, og, N, cols, 64)) return TXL_ERR_CUDA;
-            char *out = static_cast<char *>(dw) + (size_t)v0 * d * elem(grad_dtype);
+            char *rows = static_cast<char *>(dw) + (size_t)v0 * d * elem(grad_dtype);
             GemmParams q = base;
             q.M = cols;
             q.N = d;
@@ -530,13 +537,15 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.kb = ceil_div(N, 64);
             q.splits = g.split_w;
             q.n_items = q.mb * q.nb * q.splits;
-            q.part = g.split_w > 1 ? reinterpret_cast<float *>(ws + g.part_w) : nullptr;
-            q.out = out;
+            q.part = g.split_w > 1;
             q.out_bf16 = grad_dtype == TXL_BF16;
+            CUtensorMap out;
+            if (!map_out(&out, q, q.part ? ws + g.part_w : rows)) return TXL_ERR_CUDA;
             set_pairs(q, g.pieces, oh.planes);
-            if (txl::launch_product_dw(tm_g, h_cols, q, st) != cudaSuccess) return TXL_ERR_CUDA;
-            if (q.part && txl::launch_sum_parts(q.part, g.split_w, (long long)cols * d, out,
-                                                grad_dtype == TXL_BF16, st) != cudaSuccess)
+            if (txl::launch_product_dw(tm_g, h_cols, out, q, st) != cudaSuccess) return TXL_ERR_CUDA;
+            if (q.part && txl::launch_sum_parts(reinterpret_cast<float *>(ws + g.part_w), g.split_w,
+                                                (long long)cols * d, rows, grad_dtype == TXL_BF16,
+                                                st) != cudaSuccess)
                 return TXL_ERR_CUDA;
         }
     }
