@@ -54,20 +54,56 @@ int check_sizes(int n, int V, int d)
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
+// Tiles of a product of `rows` x `cols`: one block's 128 rows or a pair's 256, 128 or 256 columns,
+// and parts of its longer dimension where there are fewer tiles than SMs.
+struct Shape {
+    bool pair;
+    int bn, mb, nb, parts;
+};
 
-// Parts of `steps` equal steps for each of `units` units of work, `blocks` SMs each:
-// waves * (steps of the longest part + what a part costs besides).
-int choose_parts(long long units, int steps, int most, double extra, int blocks)
+// What a part adds besides its own work, in cycles: its start and end (the first copies, the last
+// tile's epilogue).
+constexpr double kUnitCost = 5000.0;
+
+// Cycles of one 64-wide step: the MMAs' (256 columns: 512) or the copies' at some 58 bytes a cycle
+// and SM, as measured of the statistics of 2048 x 131072 (pairs: 602 cycles a step, single blocks 653,
+// where L2 is also read less often than it is copied from).
+double step_cycles(bool pair, int bn)
 {
-    const int sms = txl::device_sm_count() / blocks;
-    int best = 1;
+    const double copies = (16384.0 + 128.0 * (pair ? bn / 2 : bn)) / 58.0;
+    return std::max(2.0 * bn, copies);
+}
+
+// `steps`: 64-wide steps of a tile.  split: 0 none, 1 the steps (parts of `part_bytes` each are then
+// written and read again), 2 the tiles of a row block (ranges of columns).
+Shape choose_shape(long long rows, long long cols, int steps, int split, int most, double part_bytes)
+{
+    const int sms = txl::device_sm_count();
+    Shape best{};
     double least = 0.0;
-    for (int s = 1; s <= std::min(steps, most); ++s) {
-        const double waves = (double)((units * s + sms - 1) / sms);
-        const double cost = waves * (ceil_div(steps, s) + extra) + 0.002 * s;
-        if (s == 1 || cost < least) {
-            best = s;
-            least = cost;
+    for (int kind = 0; kind < 4; ++kind) {
+        Shape s{};
+        s.pair = kind < 2;
+        s.bn = kind % 2 ? 128 : 256;
+        if (s.bn == 256 && cols <= 128) continue;
+        const int blocks = s.pair ? 2 : 1;
+        s.mb = ceil_div(rows, 128 * blocks);
+        s.nb = ceil_div(cols, s.bn);
+        const int units = sms / blocks;
+        const double step = step_cycles(s.pair, s.bn);
+        const int n = split == 1 ? std::min(most, steps) : split == 2 ? std::min(most, s.nb) : 1;
+        for (s.parts = 1; s.parts <= n; ++s.parts) {
+            const long long items = split == 2 ? (long long)s.mb * s.parts : (long long)s.mb * s.nb * s.parts;
+            const double waves = (double)((items + units - 1) / units);
+            const double work = split == 1 ? (double)ceil_div(steps, s.parts)
+                                           : (double)steps * (split == 2 ? ceil_div(s.nb, s.parts) : 1);
+            // (parts: written and read at 3.6 kB a cycle)
+            const double cost = waves * (work * step + kUnitCost) +
+                                (split == 1 && s.parts > 1 ? s.parts * 2.0 * part_bytes / 3600.0 : 0.0);
+            if (best.mb == 0 || cost < least) {
+                best = s;
+                least = cost;
+            }
         }
     }
     return best;
@@ -95,11 +131,13 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
         s.full = top > 0 && (long long)N * 16 <= d && N <= 64;
         s.splits = std::min(s.nb, std::min(txl::device_sm_count(), txl::kMaxStatSplits));
     } else {
-        s.pair = true;
-        s.mb = ceil_div(N, 256);
-        s.bn = std::min<long long>(256, up128(V));
-        s.nb = ceil_div(V, s.bn);
-        s.splits = choose_parts(s.mb, s.nb, txl::kMaxRowSplits, 0.5, 2);
+        const int terms = dtype == TXL_F32 ? 6 : 1;
+        const Shape c = choose_shape(N, V, ceil_div(d, 64) * terms, 2, txl::kMaxRowSplits, 0.0);
+        s.pair = c.pair;
+        s.mb = c.mb;
+        s.bn = c.bn;
+        s.nb = c.nb;
+        s.splits = c.parts;
     }
     s.list = txl::list_length(top);
     size_t o = 0;
@@ -127,12 +165,10 @@ constexpr size_t kGradBytes = (size_t)1 << 30;  // of G in the workspace: vocabu
 struct GradPlan {
     int chunk, chunks;            // vocabulary rows at a time
     int pieces;                   // terms of G
-    bool pair_g, pair_h, pair_w;  // pairs of blocks for G, dh, dW
-    int bn_g;                     // columns of G's tiles
-    int bn, mb_g, mb_h, mb_w, nb; // ... of dh's and a chunk's dW's; rows of tiles
-    int split_h, split_w, parts_h;
+    Shape g, h, w;                // tiles of G, of dh, and of a chunk's dW
+    int parts_h;                  // of dh, over all chunks
     long long g_ld, g_plane;
-    size_t live, target_logp, h_planes, w_planes, g, part_h, part_w, total;
+    size_t live, target_logp, h_planes, w_planes, g_at, part_h, part_w, total;
 };
 
 GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
@@ -147,17 +183,14 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
     g.chunks = ceil_div(V, g.chunk);
     g.g_ld = up128(g.chunk);
     g.g_plane = g.g_ld * N;
-    g.pair_g = g.pair_h = g.pair_w = true;
-    g.bn_g = (int)std::min<long long>(256, up128(g.chunk));
-    g.bn = (int)up128(ceil_div(d, ceil_div(d, 256)));
-    g.nb = ceil_div(d, g.bn);
-    g.mb_g = ceil_div(N, g.pair_g ? 256 : 128);
-    g.mb_h = ceil_div(N, g.pair_h ? 256 : 128);
-    g.mb_w = ceil_div(g.chunk, g.pair_w ? 256 : 128);
-    // (a part costs its tile's write and the sum's reads: about eight steps of 64)
-    g.split_h = choose_parts((long long)g.mb_h * g.nb, ceil_div(g.chunk, 64), 16, 8.0, g.pair_h ? 2 : 1);
-    g.split_w = choose_parts((long long)g.mb_w * g.nb, ceil_div(N, 64), 16, 8.0, g.pair_w ? 2 : 1);
-    g.parts_h = g.chunks * g.split_h;
+    const int terms = dtype == TXL_F32 ? 6 : 1, terms_w = dtype == TXL_F32 ? 6 : g.pieces;
+    g.g = choose_shape(N, g.chunk, ceil_div(d, 64) * terms, 0, 1, 0.0);
+    g.h = choose_shape(N, d, ceil_div(g.chunk, 64) * terms, 1, 16, (double)N * d * 4);
+    g.w = choose_shape(g.chunk, d, ceil_div(N, 64) * terms_w, 1, 16, (double)g.chunk * d * 4);
+    // (parts are of the contraction's own 64-wide steps)
+    g.h.parts = std::min(g.h.parts, ceil_div(g.chunk, 64));
+    g.w.parts = std::min(g.w.parts, ceil_div(N, 64));
+    g.parts_h = g.chunks * g.h.parts;
     size_t o = 0;
     const size_t row = (size_t)d * 2 * txl::kMaxPieces;
     g.live = o;
@@ -168,12 +201,12 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
     if (dtype == TXL_F32) o = up256(o + N * row);
     g.w_planes = o;
     if (dtype == TXL_F32) o = up256(o + V * row);
-    g.g = o;
+    g.g_at = o;
     o = up256(o + (size_t)g.pieces * g.g_plane * 2);
     g.part_h = o;
     if (g.parts_h > 1) o = up256(o + (size_t)g.parts_h * N * d * 4);
     g.part_w = o;
-    if (g.split_w > 1) o = up256(o + (size_t)g.split_w * g.chunk * d * 4);
+    if (g.w.parts > 1) o = up256(o + (size_t)g.w.parts * g.chunk * d * 4);
     g.total = o;
     return g;
 }
@@ -479,9 +512,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.dlogp = dlogp;
     base.dentropy = dentropy;
     base.g_pieces = g.pieces;
-    const int bn_v = g.bn_g;
     CUtensorMap h_rows, w_rows, h_cols, w_cols;
-    if (!map_of(&h_rows, oh, N, d, 128) || !map_of(&w_rows, ow, V, d, (unsigned)(g.pair_g ? bn_v / 2 : bn_v)) ||
+    if (!map_of(&h_rows, oh, N, d, 128) || !map_of(&w_rows, ow, V, d, (unsigned)(g.g.pair ? g.g.bn / 2 : g.g.bn)) ||
         !map_of(&h_cols, oh, N, d, 64) || !map_of(&w_cols, ow, V, d, 64))
         return TXL_ERR_CUDA;
     for (int c = 0; c < g.chunks; ++c) {
@@ -490,16 +522,16 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         GemmParams p = base;
         p.M = N;
         p.N = cols;
-        p.pair = g.pair_g;
-        p.mb = g.mb_g;
-        p.bn = bn_v;
-        p.nb = ceil_div(cols, bn_v);
+        p.pair = g.g.pair;
+        p.mb = g.g.mb;
+        p.bn = g.g.bn;
+        p.nb = ceil_div(cols, p.bn);
         p.kb = ceil_div(d, 64);
         p.splits = 1;
         p.n_items = p.mb * p.nb;
         p.b_row0 = v0;
         set_pairs(p, oh.planes, ow.planes);
-        const Operand og = {ws + g.g, g.g_ld, g.pieces, g.g_plane};
+        const Operand og = {ws + g.g_at, g.g_ld, g.pieces, g.g_plane};
         CUtensorMap g_rows;
         if (!map_of(&g_rows, og, N, cols, 128)) return TXL_ERR_CUDA;
         if (txl::launch_logprob_grad(h_rows, w_rows, g_rows, p, st) != cudaSuccess) return TXL_ERR_CUDA;
@@ -507,18 +539,18 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             GemmParams q = base;
             q.M = N;
             q.N = d;
-            q.pair = g.pair_h;
-            q.mb = g.mb_h;
-            q.nb = g.nb;
-            q.bn = g.bn;
+            q.pair = g.h.pair;
+            q.mb = g.h.mb;
+            q.nb = g.h.nb;
+            q.bn = g.h.bn;
             q.kb = ceil_div(cols, 64);
-            q.splits = g.split_h;
+            q.splits = g.h.parts;
             q.n_items = q.mb * q.nb * q.splits;
             q.b_row0 = v0;
             q.part = g.parts_h > 1;
             q.out_bf16 = dtype == TXL_BF16;
             CUtensorMap out;
-            if (!map_out(&out, q, q.part ? ws + g.part_h + (size_t)c * g.split_h * N * d * 4 : (char *)dh))
+            if (!map_out(&out, q, q.part ? ws + g.part_h + (size_t)c * g.h.parts * N * d * 4 : (char *)dh))
                 return TXL_ERR_CUDA;
             set_pairs(q, dtype == TXL_F32 ? g.pieces : 1, ow.planes);
             if (txl::launch_product_dh(g_rows, w_cols, out, q, st) != cudaSuccess) return TXL_ERR_CUDA;
@@ -530,20 +562,20 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             GemmParams q = base;
             q.M = cols;
             q.N = d;
-            q.pair = g.pair_w;
-            q.mb = ceil_div(cols, g.pair_w ? 256 : 128);
-            q.nb = g.nb;
-            q.bn = g.bn;
+            q.pair = g.w.pair;
+            q.mb = ceil_div(cols, g.w.pair ? 256 : 128);
+            q.nb = g.w.nb;
+            q.bn = g.w.bn;
             q.kb = ceil_div(N, 64);
-            q.splits = g.split_w;
+            q.splits = g.w.parts;
             q.n_items = q.mb * q.nb * q.splits;
-            q.part = g.split_w > 1;
+            q.part = g.w.parts > 1;
             q.out_bf16 = grad_dtype == TXL_BF16;
             CUtensorMap out;
             if (!map_out(&out, q, q.part ? ws + g.part_w : rows)) return TXL_ERR_CUDA;
             set_pairs(q, g.pieces, oh.planes);
             if (txl::launch_product_dw(tm_g, h_cols, out, q, st) != cudaSuccess) return TXL_ERR_CUDA;
-            if (q.part && txl::launch_sum_parts(reinterpret_cast<float *>(ws + g.part_w), g.split_w,
+            if (q.part && txl::launch_sum_parts(reinterpret_cast<float *>(ws + g.part_w), g.w.parts,
                                                 (long long)cols * d, rows, grad_dtype == TXL_BF16,
                                                 st) != cudaSuccess)
                 return TXL_ERR_CUDA;
