@@ -53,6 +53,20 @@ __device__ __forceinline__ bool epi_any(bool x)
     return r != 0;
 }
 
+// Maximum, sum and weighted sum (log2 units, relative to the maximum) of some of a row's logits.
+struct LaneSums {
+    float m, s, es;
+
+    __device__ __forceinline__ LaneSums with(const LaneSums &o) const
+    {
+        const float top = fmaxf(m, o.m), mu = top == -INFINITY ? 0.f : top;
+        const float d0 = m - mu, d1 = o.m - mu, f0 = ex2(d0), f1 = ex2(d1);
+        // (sums of zero stay so: not zero times infinity)
+        const float e0 = s == 0.f ? 0.f : (es + s * d0) * f0, e1 = o.s == 0.f ? 0.f : (o.es + o.s * d1) * f1;
+        return {top, fmaf(s, f0, o.s * f1), e0 + e1};
+    }
+};
+
 template <int GROUPS>
 __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
     logprob_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
@@ -244,7 +258,8 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                         *reinterpret_cast<float4 *>(p.logits + ((long long)st * p.nb + t) * BM + lane * 4) =
                             make_float4(left > 0 ? v[0] : none, left > 1 ? v[1] : none, left > 2 ? v[2] : none,
                                         left > 3 ? v[3] : none);
-                    } else if (p.group_key) {
+                    }
+                    if (p.group_key) {
                         // the largest of the lane's four: NaN has no place in the order
                         const bool any = (v[0] == v[0] && left > 0) || (v[1] == v[1] && left > 1) ||
                                          (v[2] == v[2] && left > 2) || (v[3] == v[3] && left > 3);
@@ -262,22 +277,33 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
             *abort_flag = 1;
         }
         if (ok) {
+            // over the lanes: of eight states each half of the lanes keeps four, then two, then one
+            // (nine exchanges of three values instead of forty)
 #pragma unroll
-            for (int k = 0; k < GROUPS * 8; ++k) {
-                const int st = (k >> 3) * 64 + we * 8 + (k & 7);
-                float top = m[k];
+            for (int g = 0; g < GROUPS; ++g) {
+                if (g * 64 >= p.M) break;
+                LaneSums a[8];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-                const float mu = top == -INFINITY ? 0.f : top;
-                const float d = m[k] - mu, f = ex2(d);
-                float s = sum[k] * f, e = sum[k] == 0.f ? 0.f : (es[k] + sum[k] * d) * f;
+                for (int j = 0; j < 8; ++j) a[j] = {m[g * 8 + j], sum[g * 8 + j], es[g * 8 + j]};
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    s += __shfl_xor_sync(FULL, s, o);
-                    e += __shfl_xor_sync(FULL, e, o);
+                for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
+                    const bool upper = lane & o;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= n) break;
+                        const LaneSums send = upper ? a[j] : a[j + n], keep = upper ? a[j + n] : a[j];
+                        a[j] = keep.with({__shfl_xor_sync(FULL, send.m, o), __shfl_xor_sync(FULL, send.s, o),
+                                          __shfl_xor_sync(FULL, send.es, o)});
+                    }
                 }
-                if (lane == 0 && st < p.M)
-                    p.stats[(long long)blockIdx.x * p.M + st] = make_float4(top, s, e, 0.f);
+#pragma unroll
+                for (int o = 2; o > 0; o >>= 1)
+                    a[0] = a[0].with({__shfl_xor_sync(FULL, a[0].m, o), __shfl_xor_sync(FULL, a[0].s, o),
+                                      __shfl_xor_sync(FULL, a[0].es, o)});
+                // (lane bits 4, 3, 2 chose the state's bits 2, 1, 0)
+                const int st = g * 64 + we * 8 + (lane >> 2);
+                if ((lane & 3) == 0 && st < p.M)
+                    p.stats[(long long)blockIdx.x * p.M + st] = make_float4(a[0].m, a[0].s, a[0].es, 0.f);
             }
         }
         tc_fence_before_sync();

@@ -304,13 +304,6 @@ constexpr int kFewWant = kMaxTop + kSpareTop;
 constexpr int kFewLoads = 4;                          // 16-byte loads of a thread in flight
 static_assert(kFewWant < kFewWarps, "a threshold from the warps' maxima");
 
-// Logits (log2 units) as their order, NaN as 0.
-__device__ __forceinline__ unsigned logit_key(unsigned bits)
-{
-    const float v = __uint_as_float(bits);
-    return v == v ? order_key(v) : 0u;
-}
-
 template <bool BF16, bool FULL>
 __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const MergeParams p)
 {
@@ -338,32 +331,34 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     const float nan = __int_as_float(0x7fffffff);
     int jobs = 0;                                     // candidates
     if (p.top > 0) {
-        // vectors of four groups' maxima, or of one group's logits
-        const int n = FULL ? p.nb * 32 : p.nb * 8, want = min(p.top + kSpareTop, kFewWant);
+        // vectors of four groups' maxima; the first kFewLoads of a thread stay in its registers
+        const int n = p.nb * 8, want = min(p.top + kSpareTop, kFewWant);
         const uint4 *src = reinterpret_cast<const uint4 *>(p.group_key) + (long long)row * n;
+        uint4 held[kFewLoads];
+        auto load = [&](uint4 (&k)[kFewLoads], int i0) {
+#pragma unroll
+            for (int u = 0; u < kFewLoads; ++u) {
+                const int i = i0 + u * kFewThreads;
+                k[u] = i < n ? src[i] : make_uint4(0, 0, 0, 0);
+            }
+        };
         auto scan = [&](auto take) {
             for (int i0 = tid; i0 < n; i0 += kFewThreads * kFewLoads) {
-                uint4 k[kFewLoads];
+                uint4 more[kFewLoads];
+                const bool first = i0 == tid;
+                if (!first) load(more, i0);
 #pragma unroll
                 for (int u = 0; u < kFewLoads; ++u) {
-                    const int i = i0 + u * kFewThreads;
-                    k[u] = i < n ? src[i] : FULL ? make_uint4(~0u, ~0u, ~0u, ~0u) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int u = 0; u < kFewLoads; ++u) {
-                    const int i = i0 + u * kFewThreads;
-                    if (FULL) {
-                        take(max(max(logit_key(k[u].x), logit_key(k[u].y)),
-                                 max(logit_key(k[u].z), logit_key(k[u].w))), i);
-                    } else {
-                        take(k[u].x, i * 4);
-                        take(k[u].y, i * 4 + 1);
-                        take(k[u].z, i * 4 + 2);
-                        take(k[u].w, i * 4 + 3);
-                    }
+                    const uint4 k = first ? held[u] : more[u];
+                    const int i = (i0 + u * kFewThreads) * 4;
+                    take(k.x, i);
+                    take(k.y, i + 1);
+                    take(k.z, i + 2);
+                    take(k.w, i + 3);
                 }
             }
         };
+        load(held, tid);
         unsigned mine = 0;
         scan([&](unsigned k, int) { mine = max(mine, k); });
         const unsigned most = __reduce_max_sync(ALL, mine);
@@ -418,6 +413,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
                 unsigned bk = 0;
                 int ba = 0x7fffffff;
                 scan([&](unsigned k, int i) {
+                    if (!k) return;
                     const bool left = k < last_key || (k == last_key && i > last_at);
                     if (left && (k > bk || (k == bk && i < ba))) {
                         bk = k;
@@ -451,7 +447,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         const int members = 4 * groups;
         const int id = tid < members ? g_at[tid >> 2] * 4 + (tid & 3) : 0;
         if (FULL) {
-            const float *logit = reinterpret_cast<const float *>(p.group_key) + (long long)row * p.nb * 128;
+            const float *logit = p.logits + (long long)row * p.nb * 128;
             const float v = tid < members ? logit[id] : nan;
             const unsigned k = tid < members && id < p.V && v == v ? order_key(v) : 0u;
             if (tid < members) m_key[tid] = k;
@@ -493,9 +489,10 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         }
     }
     __syncthreads();
-    // places in the order, while the first warp finishes the sums
+    if (FULL && warp > 0) return;
+    // places in the order, while the first warp finishes the sums; FULL: it does both
     int rank = 0;
-    const int c = tid - 32;
+    const int c = FULL ? tid : tid - 32;
     const bool on = c >= 0 && c < jobs && s_order[c] != 0;
     if (on) {
         const unsigned long long k = s_order[c];
@@ -506,10 +503,10 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
             rank += (other > k) | ((other == k) & (c_id[o] < id));
         }
     }
-    const int found = __syncthreads_count(on);
-    const RowSums r0 = s_sums;
+    const int found = FULL ? __popc(__ballot_sync(ALL, on)) : __syncthreads_count(on);
+    RowSums r = s_sums;
+    float l = 0.f;
     if (warp == 0) {
-        RowSums r = r0;
         if (target >= 0) r.zt = p.target_z[row];
         float d_target = r.zt - r.mu, ds = 0.f, de = 0.f;
         bool replaced = false;
@@ -539,15 +536,18 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         }
         r.sum += ds;
         r.es += de;
-        const float l = row_outputs(p, row, r, target, d_target, lane == 0);
-        if (lane == 0) s_l = l;
+        l = row_outputs(p, row, r, target, d_target, lane == 0);
+        if (!FULL && lane == 0) s_l = l;
     }
-    __syncthreads();
+    if (!FULL) {
+        __syncthreads();
+        l = s_l;
+    }
     if (on && rank < p.top) {
         p.top_ids[(long long)row * p.top + rank] = c_id[c];
         const Wide z = s_z[c];
-        const float d = isfinite(z.hi) ? above(p, z, r0.mu) : z.hi * p.scale - r0.mu;
-        p.top_logp[(long long)row * p.top + rank] = fmaf(d, kLn2, -s_l);
+        const float d = isfinite(z.hi) ? above(p, z, r.mu) : z.hi * p.scale - r.mu;
+        p.top_logp[(long long)row * p.top + rank] = fmaf(d, kLn2, -l);
     }
     if (tid >= found && tid < p.top) {  // fewer numbers than places
         p.top_ids[(long long)row * p.top + tid] = -1;
@@ -668,8 +668,8 @@ cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
 cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream_t s)
 {
     const unsigned grid = (unsigned)p.N;
-    auto *kernel = bf16 ? (p.full ? logprob_few_merge_kernel<true, true> : logprob_few_merge_kernel<true, false>)
-                        : (p.full ? logprob_few_merge_kernel<false, true> : logprob_few_merge_kernel<false, false>);
+    auto *kernel = bf16 ? (p.logits ? logprob_few_merge_kernel<true, true> : logprob_few_merge_kernel<true, false>)
+                        : (p.logits ? logprob_few_merge_kernel<false, true> : logprob_few_merge_kernel<false, false>);
     return launch_chained(kernel, dim3(grid), kFewThreads, 0, s, p);
 }
 

@@ -157,7 +157,7 @@ struct GemmParams {
     float *list_val;       // [2 splits][list][M]
     int *list_id;
     unsigned *group_key;   // few states: [M][nb][32] order of the largest of four logits, or null
-    float *logits;         // ... or [M][nb][128] the logits themselves (log2 units; NaN behind V)
+    float *logits;         // ... and [M][nb][128] the logits (log2 units; NaN behind V), or null
     float *target_z;       // few states: [M], log2 units (where there is a target)
     const float *lse, *entropy, *dlogp, *dentropy;  // (the last two may be null)
     const float *target_logp;
@@ -206,8 +206,8 @@ struct MergeParams {
     const float4 *stats;
     const float *list_val;
     const int *list_id;
-    const void *group_key; // full: the logits
-    int full;
+    const unsigned *group_key;
+    const float *logits;   // or null
     const float *target_z;
     int nb;                // vocabulary tiles of 128
     int splits, N, V, d, top, list;

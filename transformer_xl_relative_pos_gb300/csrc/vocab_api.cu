@@ -114,7 +114,7 @@ struct StatsPlan {
     bool full;                    // ... and the logits written
     int mb, nb, bn, splits, list;
     bool pair;
-    size_t h_planes, w_planes, stats, val, id, keys, target_z, total;  // offsets
+    size_t h_planes, w_planes, stats, val, id, keys, logits, target_z, total;  // offsets
 };
 
 StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
@@ -154,7 +154,9 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     s.id = o;
     o = up256(o + lists);
     s.keys = o;
-    if (s.few && top > 0) o = up256(o + (size_t)N * s.nb * (s.full ? 128 : 32) * 4);
+    if (s.few && top > 0) o = up256(o + (size_t)N * s.nb * 32 * 4);
+    s.logits = o;
+    if (s.full) o = up256(o + (size_t)N * s.nb * 128 * 4);
     s.target_z = o;
     s.total = s.few ? up256(o + (size_t)N * 4) : o;
     return s;
@@ -391,7 +393,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.list_val = reinterpret_cast<float *>(ws + s.val);
     p.list_id = reinterpret_cast<int *>(ws + s.id);
     p.group_key = top > 0 ? reinterpret_cast<unsigned *>(ws + s.keys) : nullptr;
-    p.logits = s.full ? reinterpret_cast<float *>(ws + s.keys) : nullptr;
+    p.logits = s.full ? reinterpret_cast<float *>(ws + s.logits) : nullptr;
     p.target_z = reinterpret_cast<float *>(ws + s.target_z);
     if ((s.few ? txl::launch_logprob_few(tm_w, tm_h, p, st)
                : txl::launch_logprob_stats(tm_h, tm_w, p, s.list, st)) != cudaSuccess)
@@ -402,7 +404,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     m.list_val = p.list_val;
     m.list_id = p.list_id;
     m.group_key = p.group_key;
-    m.full = s.full;
+    m.logits = p.logits;
     m.target_z = p.target_z;
     m.nb = s.nb;
     m.splits = s.few ? s.splits : 2 * s.splits;
