@@ -569,11 +569,12 @@ int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new, const txl_row
  * Token ids and targets lie on the device as int32 or int64 (txl_index_type).  -1
  * stands for none (padding); any other value outside [0, V) is taken as -1 and
  * records TXL_ERR_INDEX for txl_device_status.
- * Rows of d elements: d a multiple of 8, at most 65536; row strides in elements, multiples
- * of 16 bytes, at least d (so h may be, say, the last position of every segment);
- * pointers of rows 16-byte, of other arrays as their element, workspaces 256-byte
- * aligned.  Outputs overlap neither inputs nor one another.  Workspaces are the
- * caller's, their contents undefined before and after; calls that may run at the same
+ * Rows of d elements, d at most 65536 and (but for txl_embed_fwd) 16 bytes' worth or a
+ * multiple: of 8 elements, of 4 where all rows are fp32 in txl_embed_bwd.  Row strides in
+ * elements, multiples of 16 bytes, at least d (so h may be, say, the last position of every
+ * segment); pointers of rows 16-byte, of other arrays as their element, workspaces 256-byte
+ * aligned.  txl_embed_fwd takes any d, stride and element-aligned pointers.  Outputs and workspaces that overlap inputs or one another are
+ * refused (TXL_ERR_INVALID_ARG).  Workspaces are the caller's, their contents undefined before and after; calls that may run at the same
  * time need one each.  n, N and V up to 2^28; n or N = 0 is allowed.
  */
 typedef enum {

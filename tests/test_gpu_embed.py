@@ -22,7 +22,8 @@ def _ok():
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("n,V,d,scale,ids", [
     (1, 1, 8, 1.0, torch.int64), (7, 204, 512, 1.0, torch.int64), (33, 5, 264, 16.25, torch.int32),
-    (1000, 3001, 1032, 22.627, torch.int32), (0, 9, 64, 1.0, torch.int64)])
+    (1000, 3001, 1032, 22.627, torch.int32), (0, 9, 64, 1.0, torch.int64),
+    (50, 11, 1, 1.5, torch.int64), (129, 40, 13, 1.0, torch.int32), (300, 7, 100, 0.3, torch.int64)])
 def test_embed_fwd(n, V, d, scale, ids, dtype):
     g = torch.Generator().manual_seed(n + V)
     emb = torch.randn(V, d, generator=g).to(dtype)
@@ -81,7 +82,7 @@ def _check_grad(dout, tok, V, scale, grad, dtype_out):
 # (tokens, vocabulary, width): one token; a few; every token often; hardly any twice; more than one
 # chunk of positions each; wider than a column slice; vocabularies of two and three digits'
 # passes; ends inside words and chunks
-GRADS = [(1, 1, 8), (31, 3, 64), (33, 204, 520), (257, 7, 264), (2000, 3, 72), (1025, 5003, 256),
+GRADS = [(1, 1, 8), (31, 3, 64), (2049, 40, 24), (70000, 1000, 8), (20000, 7, 264), (33, 204, 520), (257, 7, 264), (2000, 3, 72), (1025, 5003, 256),
          (700, 300001, 8), (5000, 512, 40), (40000, 513, 16)]
 
 
@@ -112,6 +113,15 @@ def test_embed_bwd_runs_at_chunk_borders(n, kind):
     grad = txl.embed_bwd(dout, tok, V)
     _ok()
     _check_grad(dout, tok, V, 1.0, grad, F32)
+
+
+def test_embed_bwd_fp32_rows_of_four():
+    g = torch.Generator().manual_seed(77)
+    tok = model.tokens_with_padding(900, 33, g).to(dev())
+    dout = torch.randn(900, 132, generator=g).to(dev())
+    grad = txl.embed_bwd(dout, tok, 33)
+    _ok()
+    _check_grad(dout, tok, 33, 1.0, grad, F32)
 
 
 def test_embed_bwd_bf16_output_strides_and_masked_garbage():
@@ -177,7 +187,9 @@ def test_embed_refusals():
     with pytest.raises(ValueError):
         txl.embed_fwd(tok, emb, out=torch.zeros(3, 8, device=dev()))
     with pytest.raises(txl.TxlError):
-        txl.embed_fwd(tok, torch.zeros(4, 12, device=dev()))
+        txl.embed_bwd(torch.zeros(3, 6, device=dev()), tok, 4)
+    with pytest.raises(txl.TxlError):
+        txl.embed_fwd(tok, emb, out=emb[:3])
     with pytest.raises(ValueError):
         txl.embed_bwd(torch.zeros(2, 16, device=dev()), tok, 4)
     with pytest.raises(ValueError):

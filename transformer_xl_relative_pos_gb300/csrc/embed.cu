@@ -35,46 +35,57 @@ __device__ __forceinline__ uint32_t f2_to_bf2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-__device__ __forceinline__ uint4 scaled(uint4 v, float s, bool bf16)
+template <bool BF16>
+__device__ __forceinline__ uint4 scaled(uint4 v, float s)
 {
-    if (!bf16)
-        return make_uint4(__float_as_uint(__uint_as_float(v.x) * s), __float_as_uint(__uint_as_float(v.y) * s),
-                          __float_as_uint(__uint_as_float(v.z) * s), __float_as_uint(__uint_as_float(v.w) * s));
-    uint32_t *w = &v.x;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = bf2_to_f2(w[i]);
-        w[i] = f2_to_bf2(f.x * s, f.y * s);
+        w[i] = BF16 ? f2_to_bf2(f.x * s, f.y * s) : __float_as_uint(__uint_as_float(w[i]) * s);
     }
-    return v;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float scaled(float v, float s)
+{
+    return v * s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ __nv_bfloat16 scaled(__nv_bfloat16 v, float s)
+{
+    return __float2bfloat16_rn(__bfloat162float(v) * s);
 }
 
 constexpr int kFwdThreads = 256;
 constexpr int kFwdVecs = 4;  // vectors a thread keeps in flight
 
-// Flat over (position, vector).
-template <bool BF16>
+// Flat over (position, vector): 16 bytes, or an element where widths, strides or addresses ask
+// for it.
+template <bool BF16, typename VEC>
 __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedParams p, int row_vec,
                                                                 long long emb_vec)
 {
     const long long total = (long long)p.n * row_vec;
     const long long base = (long long)blockIdx.x * (kFwdThreads * kFwdVecs) + threadIdx.x;
-    const uint4 *emb = static_cast<const uint4 *>(p.emb);
-    uint4 *out = static_cast<uint4 *>(p.out);
-    uint4 v[kFwdVecs];
+    const VEC *emb = static_cast<const VEC *>(p.emb);
+    VEC *out = static_cast<VEC *>(p.out);
+    VEC v[kFwdVecs];
 #pragma unroll
     for (int k = 0; k < kFwdVecs; ++k) {
         const long long i = base + k * kFwdThreads;
-        v[k] = make_uint4(0, 0, 0, 0);
+        v[k] = VEC{};
         if (i >= total) continue;
         const int t = (int)(i / row_vec), c = (int)(i - (long long)t * row_vec);
         const int id = token_at(p.tokens, p.index_bytes, t, p.V, p.status);
-        if (id >= 0) v[k] = __ldg(emb + id * emb_vec + c);
+        if (id >= 0) v[k] = emb[id * emb_vec + c];
     }
 #pragma unroll
     for (int k = 0; k < kFwdVecs; ++k) {
         const long long i = base + k * kFwdThreads;
-        if (i < total) out[i] = p.scale == 1.f ? v[k] : scaled(v[k], p.scale, BF16);
+        if (i < total) out[i] = p.scale == 1.f ? v[k] : scaled<BF16>(v[k], p.scale);
     }
 }
 
@@ -543,11 +554,16 @@ bool wide_clusters()
 cudaError_t launch_embed_fwd(const EmbedParams &p, bool bf16, cudaStream_t s)
 {
     const int per = bf16 ? 8 : 4;
-    const int row_vec = p.d / per;
+    const bool wide = p.d % per == 0 && p.emb_ld % per == 0 &&
+                      (reinterpret_cast<uintptr_t>(p.emb) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0;
+    const int row_vec = wide ? p.d / per : p.d;
+    const long long ld = wide ? p.emb_ld / per : p.emb_ld;
     const long long total = (long long)p.n * row_vec;
     const unsigned grid = (unsigned)((total + kFwdThreads * kFwdVecs - 1) / (kFwdThreads * kFwdVecs));
-    if (bf16) embed_fwd_kernel<true><<<grid, kFwdThreads, 0, s>>>(p, row_vec, p.emb_ld / per);
-    else embed_fwd_kernel<false><<<grid, kFwdThreads, 0, s>>>(p, row_vec, p.emb_ld / per);
+    if (wide && bf16) embed_fwd_kernel<true, uint4><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
+    else if (wide) embed_fwd_kernel<false, uint4><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
+    else if (bf16) embed_fwd_kernel<true, __nv_bfloat16><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
+    else embed_fwd_kernel<false, float><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
     return cudaGetLastError();
 }
 

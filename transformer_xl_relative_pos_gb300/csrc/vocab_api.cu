@@ -1,6 +1,7 @@
 // C-ABI entry points of the token embedding and of the log probabilities (include/txl.h):
 // argument validation, work division, workspace layout, launches.
 #include <algorithm>
+#include <initializer_list>
 
 #include "txl.h"
 #include "vocab.h"
@@ -41,11 +42,41 @@ int check_rows(const void *p, long long stride, int rows, int d, int dtype)
     return stride > (1LL << 36) ? TXL_ERR_UNSUPPORTED : TXL_OK;
 }
 
-int check_sizes(int n, int V, int d)
+// d a multiple of `unit`.
+int check_sizes(int n, int V, int d, int unit)
 {
     if (n < 0 || V < 1 || d < 1) return TXL_ERR_INVALID_ARG;
-    if (d % 8 != 0 || n > kMaxRows || V > kMaxVocab || d > kMaxWidth) return TXL_ERR_UNSUPPORTED;
+    if (d % unit != 0 || n > kMaxRows || V > kMaxVocab || d > kMaxWidth) return TXL_ERR_UNSUPPORTED;
     return TXL_OK;
+}
+
+// 16 bytes of elements of this type, or of the narrower of two.
+int unit_of(int dtype, int other = TXL_F32)
+{
+    return dtype == TXL_BF16 || other == TXL_BF16 ? 8 : 4;
+}
+
+// A range of memory; what is written must overlap nothing else.
+struct Range {
+    const void *p;
+    size_t bytes;
+};
+
+Range rows_range(const void *p, long long stride, int rows, int d, int dtype)
+{
+    return {p, rows < 1 ? 0 : ((size_t)(rows - 1) * stride + d) * elem(dtype)};
+}
+
+// Whether one of the first n_out ranges (outputs) overlaps any other.
+bool overlap(std::initializer_list<Range> r, int n_out)
+{
+    const Range *a = r.begin();
+    for (int i = 0; i < n_out; ++i)
+        for (int j = i + 1; j < (int)r.size(); ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
+            if (x && y && a[i].bytes && a[j].bytes && x < y + a[j].bytes && y < x + a[i].bytes) return true;
+        }
+    return false;
 }
 
 // ---------------------------------------------------------------------------
@@ -262,13 +293,17 @@ int txl_embed_fwd(const void *tokens, int index_type, const void *emb, long long
                   void *out, int n, int V, int d, float scale, int dtype, void *stream)
 {
     int rc;
-    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(n, V, d)) != TXL_OK) return rc;
+    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(n, V, d, 1)) != TXL_OK) return rc;
     if ((rc = check_ids(tokens, index_type)) != TXL_OK) return rc;
-    if (!emb || (n > 0 && (!tokens || !out)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
-    if ((rc = check_rows(emb, emb_stride, V, d, dtype)) != TXL_OK) return rc;
-    if (!on(out, 16)) return TXL_ERR_MISALIGNED;
+    if (!emb || (n > 0 && (!tokens || !out)) || !(scale == scale) || emb_stride < 1) return TXL_ERR_INVALID_ARG;
+    if (emb_stride < d && V > 1) return TXL_ERR_SHAPE;
+    if (emb_stride > (1LL << 36)) return TXL_ERR_UNSUPPORTED;
+    if (!on(emb, (size_t)elem(dtype)) || !on(out, (size_t)elem(dtype))) return TXL_ERR_MISALIGNED;
+    if (overlap({{out, (size_t)n * d * elem(dtype)}, {tokens, (size_t)n * index_type},
+                 rows_range(emb, emb_stride, V, d, dtype)}, 1))
+        return TXL_ERR_INVALID_ARG;
     if (n == 0) return TXL_OK;
-    if ((long long)n * d / 4 / 1024 > 0x7ffffff0LL) return TXL_ERR_UNSUPPORTED;
+    if ((long long)n * d / 1024 > 0x7ffffff0LL) return TXL_ERR_UNSUPPORTED;
     txl::EmbedParams p{};
     p.status = txl::device_status_word();
     if (!p.status) return TXL_ERR_CUDA;
@@ -286,7 +321,7 @@ int txl_embed_fwd(const void *tokens, int index_type, const void *emb, long long
 
 size_t txl_embed_bwd_workspace_size(int n, int V, int d)
 {
-    if (check_sizes(n, V, d) != TXL_OK) return 0;
+    if (check_sizes(n, V, d, unit_of(TXL_F32)) != TXL_OK) return 0;
     return n == 0 ? 0 : txl::embed_bwd_workspace_bytes(n, d);
 }
 
@@ -296,12 +331,15 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
 {
     int rc;
     if ((rc = check_type(dtype)) != TXL_OK || (rc = check_type(grad_dtype)) != TXL_OK) return rc;
-    if ((rc = check_sizes(n, V, d)) != TXL_OK) return rc;
+    if ((rc = check_sizes(n, V, d, unit_of(dtype, grad_dtype))) != TXL_OK) return rc;
     if ((rc = check_ids(tokens, index_type)) != TXL_OK) return rc;
     if (!demb || (n > 0 && (!tokens || !dout)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
     if (accumulate && grad_dtype != TXL_F32) return TXL_ERR_UNSUPPORTED;
     if (n > 0 && (rc = check_rows(dout, dout_stride, n, d, dtype)) != TXL_OK) return rc;
     if (!on(demb, 16)) return TXL_ERR_MISALIGNED;
+    if (overlap({{demb, (size_t)V * d * elem(grad_dtype)}, {workspace, n > 0 ? workspace_bytes : 0},
+                 {tokens, (size_t)n * index_type}, rows_range(dout, dout_stride, n, d, dtype)}, 2))
+        return TXL_ERR_INVALID_ARG;
     cudaStream_t s = stream_of(stream);
     if (n == 0)
         return accumulate ? TXL_OK
@@ -326,7 +364,7 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
 
 size_t txl_logprob_fwd_workspace_size(int N, int V, int d, int top, int dtype)
 {
-    if (check_sizes(N, V, d) != TXL_OK || check_type(dtype) != TXL_OK || top < 0 || top > txl::kMaxTop)
+    if (check_sizes(N, V, d, 8) != TXL_OK || check_type(dtype) != TXL_OK || top < 0 || top > txl::kMaxTop)
         return 0;
     return N == 0 ? 0 : plan_stats(N, V, d, dtype, top).total;
 }
@@ -337,7 +375,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
                     int dtype, void *workspace, size_t workspace_bytes, void *stream)
 {
     int rc;
-    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(N, V, d)) != TXL_OK) return rc;
+    if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(N, V, d, 8)) != TXL_OK) return rc;
     if ((rc = check_ids(targets, index_type)) != TXL_OK) return rc;
     if (top < 0 || !w || (N > 0 && !h) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
     if (top > txl::kMaxTop) return TXL_ERR_UNSUPPORTED;
@@ -348,6 +386,11 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     for (const void *p : {(const void *)logp, (const void *)lse, (const void *)entropy,
                           (const void *)top_logp, (const void *)top_ids})
         if (!on(p, 4)) return TXL_ERR_MISALIGNED;
+    const size_t row4 = (size_t)N * 4;
+    if (overlap({{logp, row4}, {lse, row4}, {entropy, row4}, {top_logp, row4 * top}, {top_ids, row4 * top},
+                 {workspace, N > 0 ? workspace_bytes : 0}, {targets, (size_t)N * index_type},
+                 rows_range(h, h_stride, N, d, dtype), rows_range(w, w_stride, V, d, dtype)}, 6))
+        return TXL_ERR_INVALID_ARG;
     if (N == 0) return TXL_OK;
     const StatsPlan s = plan_stats(N, V, d, dtype, top);
     if (!workspace || workspace_bytes < s.total) return TXL_ERR_WORKSPACE;
@@ -435,7 +478,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
 
 size_t txl_logprob_bwd_workspace_size(int N, int V, int d, int dtype, int grad_dtype)
 {
-    if (check_sizes(N, V, d) != TXL_OK || check_type(dtype) != TXL_OK || check_type(grad_dtype) != TXL_OK)
+    if (check_sizes(N, V, d, 8) != TXL_OK || check_type(dtype) != TXL_OK || check_type(grad_dtype) != TXL_OK)
         return 0;
     return N == 0 ? 0 : plan_grad(N, V, d, dtype, grad_dtype).total;
 }
@@ -448,7 +491,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
 {
     int rc;
     if ((rc = check_type(dtype)) != TXL_OK || (rc = check_type(grad_dtype)) != TXL_OK) return rc;
-    if ((rc = check_sizes(N, V, d)) != TXL_OK) return rc;
+    if ((rc = check_sizes(N, V, d, 8)) != TXL_OK) return rc;
     if ((rc = check_ids(targets, index_type)) != TXL_OK) return rc;
     if (!w || (!dh && !dw) || (N > 0 && (!h || !lse)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
     if ((targets == nullptr) != (dlogp == nullptr)) return TXL_ERR_INVALID_ARG;
@@ -459,6 +502,12 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     if (!on(dh, 16) || !on(dw, 16)) return TXL_ERR_MISALIGNED;
     for (const void *p : {(const void *)lse, (const void *)entropy, (const void *)dlogp, (const void *)dentropy})
         if (!on(p, 4)) return TXL_ERR_MISALIGNED;
+    const size_t row4 = (size_t)N * 4;
+    if (overlap({{dh, (size_t)N * d * elem(dtype)}, {dw, (size_t)V * d * elem(grad_dtype)},
+                 {workspace, N > 0 ? workspace_bytes : 0}, {targets, (size_t)N * index_type},
+                 rows_range(h, h_stride, N, d, dtype), rows_range(w, w_stride, V, d, dtype), {lse, row4},
+                 {entropy, row4}, {dlogp, row4}, {dentropy, row4}}, 3))
+        return TXL_ERR_INVALID_ARG;
     cudaStream_t st = stream_of(stream);
     if (N == 0)
         return dw ? status_of(cudaMemsetAsync(dw, 0, (size_t)V * d * elem(grad_dtype), st)) : TXL_OK;

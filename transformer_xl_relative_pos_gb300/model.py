@@ -2,6 +2,7 @@
 
 "Transformer-XL: Attentive Language Models Beyond a Fixed-Length Context",
 §3.3 N-layer summary, for n = 1..N:
+    h^0 = word embeddings                               -> embed_fwd (kernel)
     h~  = [SG(m^{n-1}) o h^{n-1}]                      -> mem_concat (kernel)
     q, k, v = h W_q^T, h~ W_kE^T, h~ W_v^T             -> torch matmul (one
                                                            GEMM per operand set)
@@ -11,6 +12,8 @@
                                                            residual, LayerNorm)
 and the memory of each layer advances to the newest M states of its input
 (§3.2)                                                  -> mem_update (kernel).
+``log_probs`` gives the log probabilities of tokens under softmax(h E^T) with the
+embedding table E                                       -> logprob_fwd (kernel).
 With ``cache_kv`` the stack also keeps, per layer, the memory's projected keys
 and values: the memory rows and W_kE, W_v do not change at evaluation, so k and
 v of the memory are the ones projected when those states were the segment, and
@@ -100,12 +103,15 @@ class XLStack:
 
     params: draws from ``txl_inputs.draw_stack`` (CPU fp32); weights are moved
     to ``device`` in ``dtype``.  ``segment(tokens)`` processes one segment
-    [B, L] and returns the top layer's states [B, L, d] (``dtype``)."""
+    [B, L] and returns the top layer's states [B, L, d] (``dtype``).  Token -1: none, a
+    zero embedding.  ``emb_scale``: factor of the embeddings (they enter as they are by
+    default)."""
 
     MAX_DRAFT = 64  # nodes of a drafted tree
 
     def __init__(self, params: dict, H: int, M: int, device, dtype=torch.bfloat16,
-                 cache_kv: bool = False, graphs: bool = False, paged: bool = False):
+                 cache_kv: bool = False, graphs: bool = False, paged: bool = False,
+                 emb_scale: float = 1.0):
         if paged and (cache_kv or graphs):
             raise ValueError("paged keeps its own keys and values (no cache_kv) and is not "
                              "replayed from graphs")
@@ -120,6 +126,7 @@ class XLStack:
         self._full_segments = 0  # eager segments run with full memories
         to = lambda t: t.to(device=self.device, dtype=dtype).contiguous()
         self.emb = to(params["emb"])
+        self.emb_scale = float(emb_scale)
         self.u = to(params["u"])
         self.v_bias = to(params["v_bias"])
         self.layers = [{k: to(v) for k, v in lay.items()} for lay in params["layers"]]
@@ -305,6 +312,26 @@ class XLStack:
             self._restore(st, snap)
         return out
 
+    def _embed(self, tokens: torch.Tensor) -> torch.Tensor:
+        """h^0 of tokens [B, L]."""
+        if not self.emb.is_cuda:  # (a stack on the host, its kernels replaced by the caller)
+            return self.emb[tokens] * self.emb_scale
+        return txl.embed_fwd(tokens.contiguous(), self.emb, scale=self.emb_scale)
+
+    def log_probs(self, h: torch.Tensor, targets=None, *, top: int = 0, scale: float = 1.0) -> txl.LogProbs:
+        """Log probabilities under softmax(scale * h E^T) with the stack's embedding table E,
+        for states h [..., d] of ``segment`` or ``draft``: of ``targets`` [...] (-1: none), the
+        entropy, and the ``top`` most probable tokens.  Of a segment's states, position t's
+        target is the token at t + 1; a drafted node's candidates for children are its top_ids."""
+        if targets is not None:
+            targets = torch.as_tensor(targets).to(self.device).contiguous()
+        return txl.logprob_fwd(h, self.emb, targets, top=top, scale=scale)
+
+    def score(self, tokens: torch.Tensor, targets: torch.Tensor, *, top: int = 0) -> txl.LogProbs:
+        """One segment [B, L] and the log probabilities of its targets [B, L] (each
+        position's next token; -1: none)."""
+        return self.log_probs(self.segment(tokens), targets, top=top)
+
     def draft(self, tokens: torch.Tensor, parents: torch.Tensor, n_nodes=None) -> torch.Tensor:
         """The top layer's states [B, N, d] of a tree of N <= 64 drafted tokens
         [B, N] per sequence (paged): node i follows node parents[b, i] < i of its
@@ -324,7 +351,7 @@ class XLStack:
         parents = i32(parents)
         n_nodes = None if n_nodes is None else i32(n_nodes)
         H, dh = self.H, self.dh
-        h = self.emb[tokens.to(self.device)]
+        h = self._embed(tokens.to(self.device))
         # q, k and v of every layer as its projection leaves them
         qkv = torch.empty(len(self.layers), B, N, 3, H, dh, dtype=self.dtype, device=self.device)
         for n, lay in enumerate(self.layers):
@@ -388,7 +415,7 @@ class XLStack:
 
     def _segment(self, tokens: torch.Tensor) -> torch.Tensor:
         B, L = tokens.shape
-        h = self.emb[tokens]
+        h = self._embed(tokens)
         for n, lay in enumerate(self.layers):
             st = self.states[n]
             M_cur = st.fill
