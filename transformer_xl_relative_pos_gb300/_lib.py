@@ -738,6 +738,7 @@ class PagePool:
 # ---------------------------------------------------------------------------
 
 _INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _on_device(index: int, name: str, stream, *args):
@@ -766,38 +767,44 @@ def _made_on(index: int, stream):
     return torch.cuda.stream(stream)
 
 
-def _table(t, name: str) -> tuple[int, int, int, int]:
-    """Device, rows, width and row stride of a [V, d] table or a matrix of rows."""
+def _cuda_tensor(t, name: str, index: int | None = None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be [rows, d], got {list(t.shape)}")
-    _code(t.dtype)
-    rows, d = t.shape
-    if d > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be dense in its last dimension (strides {t.stride()})")
-    return t.get_device(), rows, d, (t.stride(0) if rows > 1 else d)
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on another device than the table")
+
+
+def _table(t, name: str) -> tuple[int, int, int, int]:
+    """Device, rows, width and row stride of a [V, d] table."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        _cuda_tensor(t, name)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows, d], got {list(shape)}")
+    if t.dtype not in _CODES:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)")
+    rows, d = shape
+    if strides[1] != 1 and d > 1:
+        raise ValueError(f"{name} must be dense in its last dimension (strides {strides})")
+    return t.get_device(), rows, d, strides[0] if rows > 1 else d
 
 
 def _rows_of(t, name: str, d: int, dtype, index: int) -> tuple[int, int]:
     """Rows and row stride of a [..., d] operand whose rows are equally spaced."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on another device than the table")
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or index < 0:
+        _cuda_tensor(t, name, index)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, strides = t.shape, t.stride()
-    if len(shape) < 1 or shape[-1] != d:
+    shape = t.shape
+    if len(shape) < 1 or shape[-1] != d or d < 1:
         raise ValueError(f"{name} must be [..., {d}], got {list(shape)}")
     n = t.numel() // d
-    if n == 0 or (n == 1 and (d == 1 or strides[-1] == 1)):
+    if n == 0 or t.is_contiguous():
         return n, d
-    if d > 1 and strides[-1] != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and d > 1:
         raise ValueError(f"{name} must be dense in its last dimension (strides {strides})")
     stride, run = None, 1
     for size, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
@@ -808,23 +815,20 @@ def _rows_of(t, name: str, d: int, dtype, index: int) -> tuple[int, int]:
         elif st != stride * run:
             raise ValueError(f"{name} must have equally spaced rows (strides {strides})")
         run *= size
-    return n, stride
+    return n, d if stride is None else stride
 
 
 def _ids(t, name: str, n: int, index: int) -> tuple[int, int]:
     """Address and index type of n contiguous token ids."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers)")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on another device than the table")
-    if t.dtype not in _INDEX_BYTES:
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _cuda_tensor(t, name, index)
+    kind = _INDEX_BYTES.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must hold {n} ids, contiguous, got {list(t.shape)} with strides "
                          f"{t.stride()}")
-    return t.data_ptr(), _INDEX_BYTES[t.dtype]
+    return t.data_ptr(), kind
 
 
 def _room(workspace, size: int, index: int, stream):
@@ -839,18 +843,19 @@ def _room(workspace, size: int, index: int, stream):
 
 
 def embed_fwd(tokens, emb, *, scale: float = 1.0, out=None, stream=None):
-    """Rows of the table emb [V, d] (bf16 or fp32, rows at any stride of 16 bytes' multiples)
-    times ``scale`` for the ids ``tokens`` (int32 or int64, any shape): [*tokens.shape, d].  -1:
-    a row of zeros."""
+    """Rows of the table emb [V, d] (bf16 or fp32, rows at any stride) times ``scale`` for the ids
+    ``tokens`` (int32 or int64, any shape): [*tokens.shape, d].  -1: a row of zeros."""
     index, V, d, stride = _table(emb, "emb")
-    n = tokens.numel()
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("tokens must be a torch.Tensor")
+    n, dtype = tokens.numel(), emb.dtype
     at, kind = _ids(tokens, "tokens", n, index)
     shape = (*tokens.shape, d)
     if out is None:
         with _made_on(index, stream):
-            out = torch.empty(shape, dtype=emb.dtype, device=emb.device)
+            out = torch.empty(shape, dtype=dtype, device=emb.device)
     _on_device(index, "txl_embed_fwd", stream, at, kind, emb.data_ptr(), stride,
-               _ptr(out, "out", emb.dtype, shape, index), n, V, d, scale, _code(emb.dtype))
+               _ptr(out, "out", dtype, shape, index), n, V, d, scale, _CODES[dtype])
     return out
 
 
@@ -865,6 +870,9 @@ def embed_bwd(dout, tokens, V: int, *, scale: float = 1.0, dtype=torch.float32, 
     spaced rows), in ``dtype`` (or that of ``out``); with ``accumulate`` added to ``out`` (fp32).
     ``workspace``: a device buffer of at least :func:`embed_bwd_workspace_size` bytes (allocated
     when omitted)."""
+    for t, name in ((tokens, "tokens"), (dout, "dout")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
     n, d, index = tokens.numel(), dout.shape[-1], dout.get_device()
     rows, stride = _rows_of(dout, "dout", d, dout.dtype, index)
     if rows != n:

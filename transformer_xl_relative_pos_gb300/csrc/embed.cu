@@ -93,8 +93,7 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedParam
 // positions sorted by token
 // ---------------------------------------------------------------------------
 // LSD radix sort of (key, position): key = token, or V for a position without one.  One launch:
-// a thread-block cluster (one block for few positions), a warp for each stretch of consecutive
-// positions.  A pass counts each warp's digits, exchanges the blocks' counts through distributed
+// a thread-block cluster, a warp for each stretch of consecutive positions.  A pass counts each warp's digits, exchanges the blocks' counts through distributed
 // shared memory, and lets every warp put its stretch in place in order: 32 positions at a time,
 // equal digits ranked by match.  Stable, so equal tokens stay in the order of their positions.
 // Bound by the scattered stores of a few SMs, hence one of 8 bytes for each position.
@@ -102,7 +101,6 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedParam
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCluster = 8, kSortWide = 16;  // blocks; more than 8 need the device's consent
-constexpr int kSortAlone = 2048;        // positions up to which one block sorts
 constexpr int kHeld = 8;                // rows of 32 positions a warp holds in registers
 constexpr int kDigit = 9;
 constexpr int kBins = 1 << kDigit;      // one bin a thread
@@ -126,26 +124,28 @@ __device__ __forceinline__ int cluster_word(const int *p, int block)
     return v;
 }
 
-// ALONE: one block, whose positions stay in shared memory between passes.
-template <bool ALONE>
+// The table's gradient is zero where no token points; the sums then write the others.  Clearing
+// all of it beside the sort costs the rows that are written twice and saves the wait for what
+// the sort finds (65536 tokens, 32000 x 1024: 82 us with the absent rows cleared by the sums).
+__device__ __forceinline__ void clear_gradient(const SortParams &p, int threads)
+{
+    const long long stride = (long long)(gridDim.x - p.blocks) * threads;
+    for (long long i = (long long)(blockIdx.x - p.blocks) * threads + threadIdx.x; i < p.zero_vecs; i += stride)
+        p.zero[i] = make_uint4(0, 0, 0, 0);
+}
+
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
 {
     __shared__ int place[kSortWarps][kBins];    // a warp's counts, then its next places
     __shared__ int total[kBins];                // the block's counts
     __shared__ int warp_sum[kSortWarps];
-    __shared__ int2 s_pair[ALONE ? kSortAlone : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int block = blockIdx.x;
     const long long lo_ = ((long long)block * kSortWarps + warp) * p.per_warp;
     const int lo = (int)min((long long)p.n, lo_), hi = (int)min((long long)p.n, lo_ + p.per_warp);
     chain_go();
     if (block >= p.blocks) {
-        // The table's gradient is zero where no token points; the sums then write the others.  Clearing
-        // all of it beside the sort costs the rows that are written twice and saves the wait for what
-        // the sort finds (65536 tokens, 32000 x 1024: 82 us with the absent rows cleared by the sums).
-        const long long stride = (long long)(gridDim.x - p.blocks) * kSortThreads;
-        for (long long i = (long long)(block - p.blocks) * kSortThreads + tid; i < p.zero_vecs; i += stride)
-            p.zero[i] = make_uint4(0, 0, 0, 0);
+        clear_gradient(p, kSortThreads);
         return;
     }
     if (block == 0 && tid == 0) *p.crossing = 0;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
                     const int id = token_at(p.tokens, p.index_bytes, i, p.V, p.status);
                     key[k] = id < 0 ? p.V : id;
                 } else {
-                    const int2 v = ALONE ? s_pair[i] : __ldcg(in + i);
+                    const int2 v = __ldcg(in + i);
                     key[k] = v.x;
                     pos[k] = v.y;
                 }
@@ -193,16 +193,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
             sum += c;
         }
         total[tid] = sum;
-        int all = sum, before = 0;
-        if (!ALONE) {
-            cluster_sync_all();
-            all = 0;
+        cluster_sync_all();
+        int all = 0, before = 0;
 #pragma unroll 8
-            for (int b = 0; b < p.blocks; ++b) {
-                const int c = cluster_word(total + tid, b);
-                all += c;
-                before += b < block ? c : 0;
-            }
+        for (int b = 0; b < p.blocks; ++b) {
+            const int c = cluster_word(total + tid, b);
+            all += c;
+            before += b < block ? c : 0;
         }
         int incl = all;
 #pragma unroll
@@ -234,22 +231,70 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
                 __syncwarp();
                 if (!on) continue;
                 TXL_CHECK(to >= 0 && to < p.n, p.status);
-                const int2 v = make_int2(key[k], pos[k]);
-                if (ALONE && !last) s_pair[to] = v;
-                else __stcg(out + to, v);
+                __stcg(out + to, make_int2(key[k], pos[k]));
             }
         }
         // what this pass has put in place is read by other warps and blocks
         if (last) break;
-        if (ALONE) {
-            __syncthreads();
-        } else {
-            __threadfence();
-            cluster_sync_all();
-        }
+        __threadfence();
+        cluster_sync_all();
     }
     // (no block leaves while another may still read its counts)
-    if (!ALONE) cluster_sync_all();
+    cluster_sync_all();
+}
+
+// Up to kRankMost positions: each one's place is the number of keys before it, counted by
+// comparing with all of them.  A block places 32 positions, each of its warps against an
+// eighth of the keys.  2047 positions 4 us, where a block with two radix passes took 11.
+constexpr int kRankMost = 4096;
+constexpr int kRankThreads = 256;
+
+__global__ void __launch_bounds__(kRankThreads) rank_sort_kernel(const SortParams p)
+{
+    __shared__ int4 s_key[kRankMost / 4];
+    __shared__ int s_rank[32];
+    chain_go();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((int)blockIdx.x >= p.blocks) {
+        clear_gradient(p, kRankThreads);
+        return;
+    }
+    if (blockIdx.x == 0 && tid == 0) *p.crossing = 0;
+    if (tid < 32) s_rank[tid] = 0;
+    int *keys = reinterpret_cast<int *>(s_key);
+    const int padded = (p.n + 31) / 32 * 32;
+    for (int i = tid; i < padded; i += kRankThreads) {
+        int key = 0x7ffffffe;  // (behind the last: after everything)
+        if (i < p.n) {
+            const int id = token_at(p.tokens, p.index_bytes, i, p.V, p.status);
+            key = id < 0 ? p.V : id;
+        }
+        keys[i] = key;
+    }
+    __syncthreads();
+    const int i0 = blockIdx.x * 32, mine = keys[i0 + lane];
+    // rows of 32 keys in turn over the warps: rows before this one count equal keys too
+    int rank = 0;
+    for (int r = warp; r < padded / 32; r += kRankThreads / 32) {
+        const int limit = mine + (r * 32 < i0 ? 1 : 0);
+        if (r * 32 == i0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) rank += keys[i0 + j] < mine || (keys[i0 + j] == mine && j < lane);
+            continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int4 k = s_key[r * 8 + j];
+            rank += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+        }
+    }
+    atomicAdd(s_rank + lane, rank);
+    __syncthreads();
+    if (warp == 0 && i0 + lane < p.n) {
+        const int to = s_rank[lane];
+        TXL_CHECK(to >= 0 && to < p.n, p.status);
+        p.pair[0][to] = make_int2(mine, i0 + lane);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -269,7 +314,8 @@ struct SumParams {
     void *demb;
     float *part;                  // [chunks][2][part_ld]: of a run from before, of one into the next
     long long part_ld;
-    int *crossing, *cross_chunk;  // chunks in which a run begins that goes on in the next
+    int *crossing;                // runs that begin in a chunk and go on in the next:
+    int2 *cross;                  // ... the chunk and the key of each
     int n, V, d, chunk, chunks, slices, accumulate;
     float scale;
     unsigned int *status;
@@ -402,7 +448,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_runs_kernel(const SumParam
                     }
                 }
                 if (into_next && !from_before && slice == 0 && lane == 0)
-                    p.cross_chunk[atomicAdd(p.crossing, 1)] = chunk;
+                    p.cross[atomicAdd(p.crossing, 1)] = make_int2(chunk, id);
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) a[c] = 0.f;
                 first = false;
@@ -426,17 +472,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_runs_kernel(const SumPar
     chain_wait();
     const int runs = *p.crossing;
     for (int run = blockIdx.x; run < runs; run += gridDim.x) {
-        const int chunk = p.cross_chunk[run];
-        const int key = p.pair[(long long)(chunk + 1) * p.chunk - 1].x;
-        // the last chunk whose first position has the key, 32 ways at a time over the sorted keys
-        int in = chunk + 1, out = p.chunks;
-        while (out - in > 1) {
-            const int step = (out - in + 31) / 32, at = in + lane * step;
-            const bool has = at < out && p.pair[(long long)at * p.chunk].x == key;
-            const int n = __popc(__ballot_sync(FULL, has));  // (lane 0 has it)
-            const int lo = in + (n - 1) * step;
-            out = min(out, lo + step);
-            in = lo;
+        const int2 begin = p.cross[run];
+        const int chunk = begin.x, key = begin.y;
+        // the last chunk whose first position has the key, 32 chunks at a time
+        int in = chunk;
+        while (true) {
+            const int at = in + 1 + lane;
+            const bool has = at < p.chunks && p.pair[(long long)at * p.chunk].x == key;
+            const unsigned all = __ballot_sync(FULL, has);
+            in += __popc(all);
+            if (all != FULL) break;
         }
         for (int c0 = slice * 128; c0 < p.d + wide * 128; c0 += wide * 128) {
             const int col = c0 + lane * 4;
@@ -503,7 +548,7 @@ Layout layout(int n, int d)
         o = up(o + (size_t)n * 8);
     }
     l.cross = o;
-    o = up(o + ((size_t)l.chunks + 1) * 4);
+    o = up(o + ((size_t)l.chunks + 1) * 8);
     l.part = o;
     l.total = up(o + (size_t)l.chunks * 2 * l.part_ld * 4);
     return l;
@@ -541,8 +586,8 @@ bool wide_clusters()
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         const bool ok =
-            cudaFuncSetAttribute(sort_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-            cudaOccupancyMaxActiveClusters(&n, sort_kernel<false>, &cfg) == cudaSuccess && n > 0;
+            cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, sort_kernel, &cfg) == cudaSuccess && n > 0;
         if (!ok) cudaGetLastError();
         known[dev] = ok ? 1 : -1;
     }
@@ -585,32 +630,25 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16,
     int bits = 1;
     while (((long long)p.V >> bits) != 0) ++bits;  // (the key V stands for no token)
     q.passes = (bits + kDigit - 1) / kDigit;
-    // (a cluster's exchange costs what some 2000 positions do)
-    q.blocks = p.n <= kSortAlone ? 1 : p.n <= kSortAlone * 8 || !wide_clusters() ? kSortCluster : kSortWide;
+    const bool few = p.n <= kRankMost;
+    const int threads = few ? kRankThreads : kSortThreads;
+    q.blocks = few ? (p.n + 31) / 32 : p.n <= 16384 || !wide_clusters() ? kSortCluster : kSortWide;
     const int warps = q.blocks * kSortWarps;
     q.per_warp = (int)((((long long)p.n + warps - 1) / warps + 31) / 32 * 32);
-    cudaLaunchConfig_t cfg{};
     int more = 0;   // blocks that clear the gradient, in whole clusters
     if (!p.accumulate) {
         q.zero = static_cast<uint4 *>(p.demb);
         q.zero_vecs = (long long)p.V * p.d * (grad_bf16 ? 2 : 4) / 16;
-        const long long want = (q.zero_vecs + kSortThreads * 8 - 1) / (kSortThreads * 8);
-        const long long room = 2LL * device_sm_count() - q.blocks;
-        more = (int)((std::min(want, room) + q.blocks - 1) / q.blocks * q.blocks);
+        const long long want = (q.zero_vecs + threads * 8 - 1) / (threads * 8);
+        const long long room = std::max(1LL, (few ? 4LL : 2LL) * device_sm_count() - q.blocks);
+        const int unit = few ? 1 : q.blocks;
+        more = (int)((std::min(want, room) + unit - 1) / unit * unit);
     }
-    cfg.gridDim = dim3((unsigned)(q.blocks + more));
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)q.blocks;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = q.blocks == 1 ? cudaLaunchKernelEx(&cfg, sort_kernel<true>, q)
-                                        : cudaLaunchKernelEx(&cfg, sort_kernel<false>, q);
+    const dim3 grid((unsigned)(q.blocks + more));
+    const cudaError_t e = few ? launch_grid(rank_sort_kernel, grid, kRankThreads, 0, s, false, 1, q)
+                              : launch_grid(sort_kernel, grid, kSortThreads, 0, s, false, (unsigned)q.blocks, q);
     if (e != cudaSuccess) return e;
-    const int sorted = q.passes & 1;
+    const int sorted = few ? 0 : q.passes & 1;
 
     SumParams r{};
     r.pair = q.pair[sorted];
@@ -620,7 +658,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16,
     r.part = reinterpret_cast<float *>(ws + l.part);
     r.part_ld = l.part_ld;
     r.crossing = q.crossing;
-    r.cross_chunk = q.crossing + 1;
+    r.cross = reinterpret_cast<int2 *>(ws + l.cross) + 1;
     r.chunk = l.chunk;
     r.n = p.n;
     r.V = p.V;
