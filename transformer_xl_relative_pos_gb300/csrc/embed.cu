@@ -154,20 +154,27 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
         const bool last = pass + 1 == p.passes;
         const int2 *in = p.pair[pass & 1];
         int2 *out = p.pair[(pass & 1) ^ 1];
-        // kHeld rows of 32 positions at a time in registers
+        // kHeld rows of 32 positions at a time in registers (all loads before the first is looked at)
         int key[kHeld], pos[kHeld];
         auto load = [&](int i0) {
+            if (pass == 0) {
+                long long id[kHeld];
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
-                const int i = i0 + k * 32 + lane;
-                key[k] = -1;
-                pos[k] = i;
-                if (i >= hi) continue;
-                if (pass == 0) {
-                    const int id = token_at(p.tokens, p.index_bytes, i, p.V, p.status);
-                    key[k] = id < 0 ? p.V : id;
-                } else {
-                    const int2 v = __ldcg(in + i);
+                for (int k = 0; k < kHeld; ++k) {
+                    const int i = i0 + k * 32 + lane;
+                    pos[k] = i;
+                    id[k] = i < hi ? raw_token(p.tokens, p.index_bytes, i) : -1;
+                }
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) {
+                    const int t = checked_token(id[k], p.V, p.status);
+                    key[k] = pos[k] >= hi ? -1 : t < 0 ? p.V : t;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) {
+                    const int i = i0 + k * 32 + lane;
+                    const int2 v = i < hi ? __ldcg(in + i) : make_int2(-1, 0);
                     key[k] = v.x;
                     pos[k] = v.y;
                 }
@@ -195,9 +202,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
         total[tid] = sum;
         cluster_sync_all();
         int all = 0, before = 0;
-#pragma unroll 8
-        for (int b = 0; b < p.blocks; ++b) {
-            const int c = cluster_word(total + tid, b);
+#pragma unroll
+        for (int b = 0; b < kSortWide; ++b) {
+            const int c = b < p.blocks ? cluster_word(total + tid, b) : 0;
             all += c;
             before += b < block ? c : 0;
         }

@@ -7,14 +7,14 @@
 //   dh_i   = scale sum_j G_ij w_j,  dW_j = scale sum_i G_ij h_i
 //
 // One GEMM kernel on tcgen05 (bf16 operands, fp32 accumulators in TMEM), in
-// four modes that differ in their operands' layout and in what becomes of a tile:
+// three modes that differ in their operands' layout and in what becomes of a tile:
 //   kStats   h W^T; a block keeps 128 rows and walks over a range of the
 //            vocabulary, each row's running maximum, sum, weighted sum, target
 //            logit and largest logits in the registers of the thread that owns it:
 //            the N x V logits are never written.  launch_logprob_merge joins the
 //            ranges.
 //   kGrad    h W^T again; a tile becomes G, as bf16 terms in the workspace
-//   kDh, kDw G W and G^T h
+//   kProducts  dh = G W and dW = G^T h, the tiles of both in one launch
 // fp32 operands are three bf16 terms each (their leading 24 bits); a product of two
 // such operands is the six products of terms whose weight is above 2^-24.
 #include "vocab.h"
@@ -50,36 +50,46 @@ struct Ring {
     static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 };
 
-enum Mode { kStats, kGrad, kDh, kDw };
+enum Mode { kStats, kGrad, kProducts };
 
 // Tile `t` of the `n_tiles` that item `item` consists of.
 struct Tile {
     int m, n, kb_lo, kb_hi;
 };
 
+// Item `item` of a launch: of the first of its products, or (kProducts) the second, whose items
+// follow.
 template <Mode MODE>
-__device__ __forceinline__ int item_tiles(const GemmParams &p, int item)
-{
-    if (MODE != kStats) return 1;
-    const int s = item / p.mb;
-    return (int)((long long)(s + 1) * p.nb / p.splits) - (int)((long long)s * p.nb / p.splits);
-}
+struct Item {
+    int side, at;
 
-template <Mode MODE>
-__device__ __forceinline__ Tile item_tile(const GemmParams &p, int item, int t)
-{
-    if (MODE == kStats) {
-        const int s = item / p.mb;
-        return {item - s * p.mb, (int)((long long)s * p.nb / p.splits) + t, 0, p.kb};
+    __device__ __forceinline__ Item(const GemmLaunch &g, int item)
+    {
+        side = MODE == kProducts && item >= g.p[0].n_items ? 1 : 0;
+        at = side ? item - g.p[0].n_items : item;
     }
-    if (MODE == kGrad) {  // (neighbouring blocks share a tile of w)
-        const int n = item / p.mb;
-        return {item - n * p.mb, n, 0, p.kb};
+    // Tiles of it.
+    __device__ __forceinline__ int tiles(const GemmParams &p) const
+    {
+        if (MODE != kStats) return 1;
+        const int s = at / p.mb;
+        return (int)((long long)(s + 1) * p.nb / p.splits) - (int)((long long)s * p.nb / p.splits);
     }
-    const int per = p.mb * p.nb, s = item / per, mn = item - s * per;
-    return {mn / p.nb, mn % p.nb, (int)((long long)s * p.kb / p.splits),
-            (int)((long long)(s + 1) * p.kb / p.splits)};
-}
+    __device__ __forceinline__ Tile tile(const GemmParams &p, int t) const
+    {
+        if (MODE == kStats) {
+            const int s = at / p.mb;
+            return {at - s * p.mb, (int)((long long)s * p.nb / p.splits) + t, 0, p.kb};
+        }
+        if (MODE == kGrad) {  // (neighbouring blocks share a tile of w)
+            const int n = at / p.mb;
+            return {at - n * p.mb, n, 0, p.kb};
+        }
+        const int per = p.mb * p.nb, s = at / per, mn = at - s * per;
+        return {mn / p.nb, mn % p.nb, (int)((long long)s * p.kb / p.splits),
+                (int)((long long)(s + 1) * p.kb / p.splits)};
+    }
+};
 
 // What a thread keeps of its row while it walks over the vocabulary (log2 units).
 template <int LIST>
@@ -197,10 +207,12 @@ __device__ __forceinline__ bool half_any(int half, bool x)
 
 template <Mode MODE, int LIST, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                      const __grid_constant__ CUtensorMap tm_out, const GemmParams p)
+    vocab_gemm_kernel(const __grid_constant__ GemmLaunch g)
 {
-    constexpr bool A_MN = MODE == kDw, B_MN = MODE == kDh || MODE == kDw;
+    // (dW's A operand, G^T, is MN-major; both products' B operand is)
+    constexpr bool B_MN = MODE == kProducts;
+    const int n_items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
+    unsigned int *status = g.p[0].status;
     using R = Ring<PAIR>;
     constexpr int NS = R::NS, STAGE = R::STAGE, BLOCKS = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
@@ -243,55 +255,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PAIR) cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const uint64_t wait_ns = p.wait_ns;
+    const uint64_t wait_ns = g.p[0].wait_ns;
     chain_wait();
     chain_go();
 
     if (warp == 0) {
         // ===================== TMA producer =====================================
         if (lane == 0) {
-            prefetch_tensormap(&tm_a);
-            prefetch_tensormap(&tm_b);
-            const int own_bn = p.bn / BLOCKS;  // columns of B in this block
-            const uint32_t stage_tx = (uint32_t)(A_BYTES + own_bn * BK * 2) * BLOCKS;
+            const uint32_t full0 = PAIR ? cluster_addr(full, 0) : 0u;
+            for (int i = 0; i < (MODE == kProducts ? 2 : 1); ++i) {
+                prefetch_tensormap(&g.maps[i].a);
+                prefetch_tensormap(&g.maps[i].b);
+            }
             bool ok = true;
-            int it = 0;  // stages filled
-            for (int item = unit; item < p.n_items && ok; item += units) {
-                const int nt = item_tiles<MODE>(p, item);
+            int it = 0, s = 0;  // stages filled; the next one
+            uint32_t phase = 1;
+            for (int item = unit; item < n_items && ok; item += units) {
+                const Item<MODE> i(g, item);
+                const GemmParams &p = g.p[i.side];
+                // (in registers: the loop below issues a step's copies in a few hundred cycles, and reads
+                // of parameters would be repeated after every one)
+                const CUtensorMap *tm_a = &g.maps[i.side].a, *tm_b = &g.maps[i.side].b;
+                const int bn = p.bn, own_bn = bn / BLOCKS;  // columns of B in this block
+                const int b_row0 = p.b_row0, n_pairs = p.n_pairs;
+                const unsigned pair_a = p.pair_a, pair_b = p.pair_b;
+                const uint32_t stage_tx = (uint32_t)(A_BYTES + own_bn * BK * 2) * BLOCKS;
+                const bool a_mn = MODE == kProducts && i.side;
+                const int nt = i.tiles(p);
                 for (int t = 0; t < nt && ok; ++t) {
-                    const Tile w = item_tile<MODE>(p, item, t);
-                    const int m0 = (w.m * BLOCKS + rank) * BM, n0 = w.n * p.bn + rank * own_bn;
-                    for (int pr = 0; pr < p.n_pairs && ok; ++pr) {
-                        const int pa = (p.pair_a >> (4 * pr)) & 15, pb = (p.pair_b >> (4 * pr)) & 15;
+                    const Tile w = i.tile(p, t);
+                    const int m0 = (w.m * BLOCKS + rank) * BM, n0 = w.n * bn + rank * own_bn;
+                    for (int pr = 0; pr < n_pairs && ok; ++pr) {
+                        const int pa = (pair_a >> (4 * pr)) & 15, pb = (pair_b >> (4 * pr)) & 15;
                         for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
-                            const int s = it % NS;
-                            if (!(ok = mbar_wait(empty + s, ((it / NS) & 1) ^ 1, abort_flag, wait_ns))) break;
+                            if (!(ok = mbar_wait(empty + s, phase, abort_flag, wait_ns))) break;
                             uint8_t *st = smem + s * STAGE;
                             if (rank == 0) mbar_arrive_expect_tx(full + s, stage_tx);
-                            const uint32_t bar = PAIR ? cluster_addr(full + s, 0) : 0u;
+                            const uint32_t bar = full0 + s * 8;
                             auto load = [&](uint8_t *dst, const CUtensorMap *map, int c0, int c1, int c2) {
                                 if (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
                                 else tma_load_3d(dst, map, full + s, c0, c1, c2);
                             };
-                            if (A_MN) {
+                            if (a_mn) {
+#pragma unroll
                                 for (int x = 0; x < BM / 64; ++x)
-                                    load(st + x * SLAB, &tm_a, m0 + x * 64, kb * BK, pa);
+                                    load(st + x * SLAB, tm_a, m0 + x * 64, kb * BK, pa);
                             } else {
-                                load(st, &tm_a, kb * BK, m0, pa);
+                                load(st, tm_a, kb * BK, m0, pa);
                             }
                             if (B_MN) {
-                                for (int x = 0; x < own_bn / 64; ++x)
-                                    load(st + A_BYTES + x * SLAB, &tm_b, n0 + x * 64, p.b_row0 + kb * BK, pb);
+#pragma unroll
+                                for (int x = 0; x < MAX_BN / BLOCKS / 64; ++x)
+                                    if (x * 64 < own_bn)
+                                        load(st + A_BYTES + x * SLAB, tm_b, n0 + x * 64, b_row0 + kb * BK, pb);
                             } else {
-                                load(st + A_BYTES, &tm_b, kb * BK, p.b_row0 + n0, pb);
+                                load(st + A_BYTES, tm_b, kb * BK, b_row0 + n0, pb);
                             }
                             ++it;
+                            if (++s == NS) {
+                                s = 0;
+                                phase ^= 1;
+                            }
                         }
                     }
                 }
             }
             if (!ok) {
-                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+                atomicOr(status, TXL_STATUS_TIMEOUT);
                 *abort_flag = 1;
                 // copies in flight land before the block ends: counted on block 0's barriers, which
                 // the other block gives a millisecond
@@ -308,11 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ===================== MMA issuer (block 0 of a pair) ====================
-        const uint32_t ID = idesc_bf16_f32(BM * BLOCKS, p.bn, B_MN) | (A_MN ? 1u << 15 : 0u);
         const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + A_BYTES);
-        const uint64_t dA = A_MN ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
         const uint64_t dB = B_MN ? sdesc_sw128_mn(b0, SLAB) : sdesc_sw128(b0);
-        constexpr int STEP_A = A_MN ? 16 * 128 / 16 : 2, STEP_B = B_MN ? 16 * 128 / 16 : 2;
+        constexpr int STEP_B = B_MN ? 16 * 128 / 16 : 2;
         auto elect = []() -> bool {
             uint32_t el;
             asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}"
@@ -324,27 +352,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             else mma_commit(bar);
         };
         bool ok = true;
-        int it = 0, tile = 0;
-        for (int item = unit; item < p.n_items && ok && rank == 0; item += units) {
-            const int nt = item_tiles<MODE>(p, item);
+        int s = 0, tile = 0;
+        uint32_t phase = 0;
+        for (int item = unit; item < n_items && ok && rank == 0; item += units) {
+            const Item<MODE> i(g, item);
+            const GemmParams &p = g.p[i.side];
+            const bool a_mn = MODE == kProducts && i.side;
+            const uint32_t ID = idesc_bf16_f32(BM * BLOCKS, p.bn, B_MN) | (a_mn ? 1u << 15 : 0u);
+            const uint64_t dA = a_mn ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
+            const int step_a = a_mn ? 16 * 128 / 16 : 2;
+            const int nt = i.tiles(p);
             for (int t = 0; t < nt && ok; ++t) {
-                const Tile w = item_tile<MODE>(p, item, t);
+                const Tile w = i.tile(p, t);
                 const int steps = p.n_pairs * (w.kb_hi - w.kb_lo);
                 const int buf = tile & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile >> 1) & 1) ^ 1, abort_flag, wait_ns));
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t acc = tmem + buf * MAX_BN;
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const int s = it % NS;
-                    ok = __all_sync(0xffffffffu, mbar_wait(full + s, (it / NS) & 1, abort_flag, wait_ns));
+                for (int k = 0; k < steps; ++k) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(full + s, phase, abort_flag, wait_ns));
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint64_t off = (uint64_t)((s * STAGE) >> 4);
                     if (elect()) {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk) {
-                            const uint64_t a = dA + off + kk * STEP_A, b = dB + off + kk * STEP_B;
+                            const uint64_t a = dA + off + kk * step_a, b = dB + off + kk * STEP_B;
                             const uint32_t more = k > 0 || kk > 0 ? 1u : 0u;
                             if (PAIR) mma_bf16_ss_pair(acc, a, b, ID, more);
                             else mma_bf16_ss(acc, a, b, ID, more);
@@ -352,6 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         commit(empty + s);
                     }
                     __syncwarp();
+                    if (++s == NS) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
                 if (!ok) break;
                 if (elect()) commit(acc_full + buf);
@@ -362,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) {
             // let what was issued drain before the memory is freed
             if (lane == 0) {
-                atomicOr(p.status, TXL_STATUS_TIMEOUT);
+                atomicOr(status, TXL_STATUS_TIMEOUT);
                 *abort_flag = 1;
             }
             if (elect()) commit(acc_full + (tile & 1));
@@ -378,8 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *out = smem + R::OFF_OUT + half * OUT_BYTES;
         const bool issuer = wq == 0 && lane == 0;  // of the half's stores
         constexpr float kLog2e = 1.4426950408889634f;
-        const float zscale = p.scale * uncut_scale(p.kb * (BK / 16)), c2 = zscale * kLog2e;
+        const float zscale = g.p[0].scale * uncut_scale(g.p[0].kb * (BK / 16)), c2 = zscale * kLog2e;
         // 128 bytes of each row, turned by the swizzle, then one store of the half's 128 rows
+        const CUtensorMap *tm_out = &g.maps[0].out;
         auto store = [&](const uint4 (&v)[8], int c0, int m0, int plane) {
             if (issuer) bulk_wait_read();
             half_sync(half);
@@ -388,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             half_sync(half);
             if (issuer) {
-                tma_store_3d(&tm_out, out, c0, m0, plane);
+                tma_store_3d(tm_out, out, c0, m0, plane);
                 bulk_commit();
             }
         };
@@ -400,13 +439,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true;
         int tile = 0;
-        for (int item = unit; item < p.n_items && ok; item += units) {
-            const int nt = item_tiles<MODE>(p, item);
+        for (int item = unit; item < n_items && ok; item += units) {
+            const Item<MODE> it(g, item);
+            const GemmParams &p = g.p[it.side];
+            tm_out = &g.maps[it.side].out;
+            const int nt = it.tiles(p);
             RowStats<LIST> r;
             int target = -1;
             float g1 = 0.f, ge = 0.f, lse = 0.f, ent = 0.f, lpt = 0.f;
             if (MODE == kStats || MODE == kGrad) {
-                const int m = (item_tile<MODE>(p, item, 0).m * BLOCKS + rank) * BM + row;
+                const int m = (it.tile(p, 0).m * BLOCKS + rank) * BM + row;
                 if (m < p.M && p.targets) target = token_at(p.targets, p.index_bytes, m, p.V, p.status);
                 // (rows without a part: zeros all through, their states have been cleared)
                 if (MODE == kGrad && m < p.M && (target >= 0 || (p.dentropy && p.dentropy[m] != 0.f))) {
@@ -423,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (MODE == kStats) r.clear();
             }
             for (int t = 0; t < nt && ok; ++t, ++tile) {
-                const Tile w = item_tile<MODE>(p, item, t);
+                const Tile w = it.tile(p, t);
                 const int buf = tile & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (tile >> 1) & 1, abort_flag, wait_ns)) &&
                      !*abort_flag;
@@ -483,12 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if (i == at && target >= 0) v[x][i] = fmaf(-pt, f, g1);
                             }
                         }
-                        for (int g = 0; g < p.g_pieces; ++g) {
+                        for (int piece = 0; piece < p.g_pieces; ++piece) {
                             uint4 o[8];
                             pack(v[0], o);
                             pack(v[1], o + 4);
-                            store(o, n0 + c, m0, g);
-                            if (g + 1 < p.g_pieces)
+                            store(o, n0 + c, m0, piece);
+                            if (piece + 1 < p.g_pieces)
 #pragma unroll
                                 for (int i = 0; i < 64; ++i) {
                                     float &y = v[i >> 5][i & 31];
@@ -506,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             (&o[i >> 2].x)[i & 3] = empty_part ? 0u : __float_as_uint(__uint_as_float(raw[i]) * f);
-                        store(o, n0 + c, m0, p.part ? item / (p.mb * p.nb) : 0);
+                        store(o, n0 + c, m0, p.part ? it.at / (p.mb * p.nb) : 0);
                     }
                 } else {
 #pragma unroll 1
@@ -532,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (MODE == kStats && ok) {
-                const int s = item / p.mb, m = ((item - s * p.mb) * BLOCKS + rank) * BM + row;
+                const int s = it.at / p.mb, m = ((it.at - s * p.mb) * BLOCKS + rank) * BM + row;
                 if (m < p.M) {
                     const long long part = 2 * s + half;
                     p.stats[part * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
@@ -547,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (MODE != kStats && issuer) bulk_wait_all();
         if (!ok && lane == 0) {
-            atomicOr(p.status, TXL_STATUS_TIMEOUT);
+            atomicOr(status, TXL_STATUS_TIMEOUT);
             *abort_flag = 1;
         }
         tc_fence_before_sync();
@@ -563,8 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <Mode MODE, int LIST, bool PAIR>
-cudaError_t launch_units(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const GemmParams &p,
-                         cudaStream_t s)
+cudaError_t launch_units(const GemmLaunch &g, cudaStream_t s)
 {
     static bool attr_set[64] = {};  // the attribute is set once per device
     constexpr int BLOCKS = PAIR ? 2 : 1, SMEM = Ring<PAIR>::SMEM_BYTES;
@@ -577,43 +618,27 @@ cudaError_t launch_units(const CUtensorMap &a, const CUtensorMap &b, const CUten
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    const unsigned grid = (unsigned)(min(p.n_items, device_sm_count() / BLOCKS) * BLOCKS);
-    return launch_grid(kernel, dim3(grid), kThreads, SMEM, s, p.chained != 0, BLOCKS, a, b, out, p);
+    const int items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
+    const unsigned grid = (unsigned)(min(items, device_sm_count() / BLOCKS) * BLOCKS);
+    return launch_grid(kernel, dim3(grid), kThreads, SMEM, s, g.chained, BLOCKS, g);
 }
 
 template <Mode MODE, int LIST>
-cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const GemmParams &p,
-                        cudaStream_t s)
+cudaError_t launch_gemm(const GemmLaunch &g, cudaStream_t s)
 {
-    return p.pair ? launch_units<MODE, LIST, true>(a, b, out, p, s) : launch_units<MODE, LIST, false>(a, b, out, p, s);
+    return g.pair ? launch_units<MODE, LIST, true>(g, s) : launch_units<MODE, LIST, false>(g, s);
 }
 
 } // namespace
 
-cudaError_t launch_logprob_stats(const CUtensorMap &a, const CUtensorMap &b, const GemmParams &p,
-                                 int list, cudaStream_t s)
+cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s)
 {
-    // (no tile is stored)
-    if (list == 0) return launch_gemm<kStats, 0>(a, b, a, p, s);
-    return list == 12 ? launch_gemm<kStats, 12>(a, b, a, p, s) : launch_gemm<kStats, 20>(a, b, a, p, s);
+    if (list == 0) return launch_gemm<kStats, 0>(g, s);
+    return list == 12 ? launch_gemm<kStats, 12>(g, s) : launch_gemm<kStats, 20>(g, s);
 }
 
-cudaError_t launch_logprob_grad(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                                const GemmParams &p, cudaStream_t s)
-{
-    return launch_gemm<kGrad, 0>(a, b, out, p, s);
-}
+cudaError_t launch_logprob_grad(const GemmLaunch &g, cudaStream_t s) { return launch_gemm<kGrad, 0>(g, s); }
 
-cudaError_t launch_product_dh(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                              const GemmParams &p, cudaStream_t s)
-{
-    return launch_gemm<kDh, 0>(a, b, out, p, s);
-}
-
-cudaError_t launch_product_dw(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                              const GemmParams &p, cudaStream_t s)
-{
-    return launch_gemm<kDw, 0>(a, b, out, p, s);
-}
+cudaError_t launch_products(const GemmLaunch &g, cudaStream_t s) { return launch_gemm<kProducts, 0>(g, s); }
 
 } // namespace txl

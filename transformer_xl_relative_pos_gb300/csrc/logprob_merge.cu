@@ -29,61 +29,65 @@ __device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
 // product is an fp32 value; an fp32 one is a product and its rounding error by fma), sums
 // carried with their errors, four chains a lane.  Where that is no number, the plain sum.  (All in
 // fp32: the fp64 units give one result where the fp32 ones give 64.)
-template <bool BF16>
-__device__ Wide dot_exact(const void *h, const void *w, int d, int lane)
-{
-    float hi[4] = {}, lo[4] = {};
-    if (BF16) {
-        const uint4 *a = static_cast<const uint4 *>(h), *b = static_cast<const uint4 *>(w);
-#pragma unroll 4
-        for (int c = lane; c < d / 8; c += 32) {
-            const uint4 x = __ldg(a + c), y = __ldg(b + c);
-            const uint32_t xp[4] = {x.x, x.y, x.z, x.w}, yp[4] = {y.x, y.y, y.z, y.w};
+struct ExactSum {
+    float hi[4] = {}, lo[4] = {}, plain = 0.f;
+
+    // Sixteen bytes of each operand.
+    template <bool BF16>
+    __device__ __forceinline__ void add(const uint4 &x, const uint4 &y)
+    {
+        const uint32_t xp[4] = {x.x, x.y, x.z, x.w}, yp[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16)));
-                two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(xp[i] & 0xffff0000u),
-                                                __uint_as_float(yp[i] & 0xffff0000u)));
-            }
-        }
-    } else {
-        const float4 *a = static_cast<const float4 *>(h), *b = static_cast<const float4 *>(w);
-#pragma unroll 4
-        for (int c = lane; c < d / 4; c += 32) {
-            const float4 x = __ldg(a + c), y = __ldg(b + c);
-            const float xp[4] = {x.x, x.y, x.z, x.w}, yp[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float q = __fmul_rn(xp[i], yp[i]);
+        for (int i = 0; i < 4; ++i) {
+            if (BF16) {
+                const float q0 = __fmul_rn(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16));
+                const float q1 = __fmul_rn(__uint_as_float(xp[i] & 0xffff0000u),
+                                           __uint_as_float(yp[i] & 0xffff0000u));
+                two_sum(hi[i], lo[i], q0);
+                two_sum(hi[i], lo[i], q1);
+                plain += q0 + q1;
+            } else {
+                const float a = __uint_as_float(xp[i]), b = __uint_as_float(yp[i]), q = __fmul_rn(a, b);
                 two_sum(hi[i], lo[i], q);
-                lo[i] += fmaf(xp[i], yp[i], -q);
+                lo[i] += fmaf(a, b, -q);
+                plain += q;
             }
         }
     }
+
+    __device__ __forceinline__ Wide over_warp()
+    {
 #pragma unroll
-    for (int i = 1; i < 4; ++i) {
-        two_sum(hi[0], lo[0], hi[i]);
-        lo[0] += lo[i];
-    }
+        for (int i = 1; i < 4; ++i) {
+            two_sum(hi[0], lo[0], hi[i]);
+            lo[0] += lo[i];
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float ohi = __shfl_xor_sync(0xffffffffu, hi[0], o), olo = __shfl_xor_sync(0xffffffffu, lo[0], o);
-        two_sum(hi[0], lo[0], ohi);
-        lo[0] += olo;
-    }
-    Wide z{__fadd_rn(hi[0], lo[0]), 0.f};
-    z.lo = lo[0] - __fadd_rn(z.hi, -hi[0]);
-    if (!isfinite(z.hi)) {
-        float plain = 0.f;
-        for (int c = lane; c < d; c += 32)
-            plain += BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(h)[c]) *
-                                __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c])
-                          : static_cast<const float *>(h)[c] * static_cast<const float *>(w)[c];
+        for (int o = 16; o > 0; o >>= 1) {
+            const float ohi = __shfl_xor_sync(0xffffffffu, hi[0], o), olo = __shfl_xor_sync(0xffffffffu, lo[0], o);
+            two_sum(hi[0], lo[0], ohi);
+            lo[0] += olo;
+        }
+        Wide z{__fadd_rn(hi[0], lo[0]), 0.f};
+        z.lo = lo[0] - __fadd_rn(z.hi, -hi[0]);
+        if (!isfinite(z.hi)) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) plain += __shfl_xor_sync(0xffffffffu, plain, o);
-        z = {plain, 0.f};
+            for (int o = 16; o > 0; o >>= 1) plain += __shfl_xor_sync(0xffffffffu, plain, o);
+            z = {plain, 0.f};
+        }
+        return z;
     }
-    return z;
+};
+
+template <bool BF16>
+__device__ __forceinline__ Wide dot_exact(const void *h, const void *w, int d, int lane)
+{
+    const uint4 *a = static_cast<const uint4 *>(h), *b = static_cast<const uint4 *>(w);
+    const int vecs = d / (BF16 ? 8 : 4);
+    ExactSum sum;
+#pragma unroll 4
+    for (int c = lane; c < vecs; c += 32) sum.add<BF16>(__ldg(a + c), __ldg(b + c));
+    return sum.over_warp();
 }
 
 // Order of scale * z as integers, 0 for no number: by the product's sign (the scale only
@@ -559,33 +563,42 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
 // small passes
 // ---------------------------------------------------------------------------
 
-template <bool BF16>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float4 *part, int parts, long long vecs,
-                                                        void *out)
+// Blocks below blocks0 sum the first result, the others the second.  Four parts in flight.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const PartsSum r0, const PartsSum r1, int blocks0)
 {
+    const bool second = (int)blockIdx.x >= blocks0;
+    const PartsSum r = second ? r1 : r0;
+    const long long vecs = r.elems / 4;
+    const long long i = (long long)((int)blockIdx.x - (second ? blocks0 : 0)) * 256 + threadIdx.x;
     chain_wait();
     chain_go();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= vecs) return;
-    float4 a = __ldcs(part + i);
-    for (int s = 1; s < parts; ++s) {
-        const float4 b = __ldcs(part + s * vecs + i);
-        a.x += b.x;
-        a.y += b.y;
-        a.z += b.z;
-        a.w += b.w;
+    const float4 *part = reinterpret_cast<const float4 *>(r.part) + i;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < r.parts; s += 4) {
+        float4 b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            b[k] = s + k < r.parts ? __ldcs(part + (s + k) * vecs) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a.x += b[k].x;
+            a.y += b[k].y;
+            a.z += b[k].z;
+            a.w += b[k].w;
+        }
     }
-    if (BF16)
-        reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    if (r.bf16)
+        static_cast<uint2 *>(r.out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
     else
-        reinterpret_cast<float4 *>(out)[i] = a;
+        static_cast<float4 *>(r.out)[i] = a;
 }
 
 // x = t0 + t1 + t2, each the bf16 nearest to what is left (exact but for what falls below
 // bf16's range).  An infinite or NaN value is its first term; a finite one that rounds to
 // infinity is cut instead.  Eight values a thread.
 __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long long ld, int rows, int vecs,
-                                                        __nv_bfloat16 *planes)
+                                                        __nv_bfloat16 *planes, int plane_vecs)
 {
     chain_wait();
     chain_go();
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long lon
             const uint32_t bits = __bfloat16_as_ushort(n);
             o[k / 2] = k & 1 ? o[k / 2] | bits << 16 : bits;
         }
-        reinterpret_cast<uint4 *>(planes)[t * total + i] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4 *>(planes)[((long long)t * rows + r) * plane_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -622,39 +635,53 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (row >= p.N) return;
     constexpr int ESIZE = BF16 ? 2 : 4;
-    const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
-    const bool live = target >= 0 || (p.dentropy && p.dentropy[row] != 0.f);
     const int vecs = p.d * ESIZE / 16;
     const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.h) + row * p.h_ld * ESIZE);
-    uint4 *dst = static_cast<uint4 *>(p.out) + (long long)row * vecs;
-    for (int c = lane; c < vecs; c += 32) dst[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-    if (target < 0) {
-        if (lane == 0) p.target_logp[row] = 0.f;
-        return;
+    uint4 *dst = static_cast<uint4 *>(p.out) + (long long)row * (p.out_ld * ESIZE / 16);
+    const long long id = p.targets ? raw_token(p.targets, p.index_bytes, row) : -1;
+    // (the row does not wait for the token, the table's row does)
+    uint4 h[4];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = c0 + 32 * k < vecs ? __ldg(src + c0 + 32 * k) : make_uint4(0, 0, 0, 0);
+    };
+    load(lane);
+    const int target = checked_token(id, p.V, p.status);
+    const bool live = target >= 0 || (p.dentropy && p.dentropy[row] != 0.f);
+    const uint4 *w = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.w) + max(target, 0) * p.w_ld * ESIZE);
+    ExactSum sum;
+    for (int c0 = lane; c0 < vecs; c0 += 128) {
+        if (c0 > lane) load(c0);
+        uint4 y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            y[k] = target >= 0 && c0 + 32 * k < vecs ? __ldg(w + c0 + 32 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (c0 + 32 * k < vecs) dst[c0 + 32 * k] = live ? h[k] : make_uint4(0, 0, 0, 0);
+            sum.add<BF16>(h[k], y[k]);
+        }
     }
-    const Wide z = dot_exact<BF16>(src, static_cast<const char *>(p.w) + target * p.w_ld * ESIZE, p.d, lane);
-    if (lane == 0) p.target_logp[row] = fmaf(z.hi, p.scale, -p.lse[row]) + z.lo * p.scale;
+    const Wide z = sum.over_warp();
+    if (lane == 0) p.target_logp[row] = target < 0 ? 0.f : fmaf(z.hi, p.scale, -p.lse[row]) + z.lo * p.scale;
 }
 
 } // namespace
 
-cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void *out, bool bf16,
-                             cudaStream_t s)
+cudaError_t launch_sum_parts(const PartsSum (&r)[2], cudaStream_t s)
 {
-    const long long vecs = elems / 4;
-    const unsigned grid = (unsigned)((vecs + 255) / 256);
-    return launch_chained(bf16 ? sum_parts_kernel<true> : sum_parts_kernel<false>, dim3(grid), 256, 0, s,
-                          reinterpret_cast<const float4 *>(part), parts, vecs, out);
+    const auto blocks = [](const PartsSum &x) { return (int)((x.elems / 4 + 255) / 256); };
+    const int b0 = blocks(r[0]), b1 = blocks(r[1]);
+    if (b0 + b1 == 0) return cudaSuccess;
+    return launch_chained(sum_parts_kernel, dim3((unsigned)(b0 + b1)), 256, 0, s, r[0], r[1], b0);
 }
 
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             bool chained, cudaStream_t s)
+                             int plane_ld, bool chained, cudaStream_t s)
 {
     const long long vecs = (long long)rows * (d / 8);
-    const unsigned grid = (unsigned)((vecs + 255) / 256);
-    if (chained) return launch_chained(split_f32_kernel, dim3(grid), 256, 0, s, x, ld, rows, d / 8, planes);
-    split_f32_kernel<<<grid, 256, 0, s>>>(x, ld, rows, d / 8, planes);
-    return cudaGetLastError();
+    return launch_grid(split_f32_kernel, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, chained, 1, x, ld, rows,
+                       d / 8, planes, plane_ld / 8);
 }
 
 cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)

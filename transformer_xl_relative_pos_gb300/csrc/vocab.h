@@ -58,18 +58,27 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, si
 // token ids
 // ---------------------------------------------------------------------------
 
-// Token i of an int32 or int64 array: its id in [0, V), or -1 for none.  Any other value is
-// taken as none and recorded.
-__device__ __forceinline__ int token_at(const void *tokens, int index_bytes, long long i, int V,
-                                        unsigned int *status)
+__device__ __forceinline__ long long raw_token(const void *tokens, int index_bytes, long long i)
 {
-    const long long t = index_bytes == 8 ? __ldg(static_cast<const long long *>(tokens) + i)
-                                         : __ldg(static_cast<const int *>(tokens) + i);
+    return index_bytes == 8 ? __ldg(static_cast<const long long *>(tokens) + i)
+                            : __ldg(static_cast<const int *>(tokens) + i);
+}
+
+// A token's id in [0, V), or -1 for none.  Any other value is taken as none and recorded.
+__device__ __forceinline__ int checked_token(long long t, int V, unsigned int *status)
+{
     if (t < -1 || t >= V) {
         atomicOr(status, TXL_STATUS_INDEX);
         return -1;
     }
     return (int)t;
+}
+
+// Token i of an int32 or int64 array.
+__device__ __forceinline__ int token_at(const void *tokens, int index_bytes, long long i, int V,
+                                        unsigned int *status)
+{
+    return checked_token(raw_token(tokens, index_bytes, i), V, status);
 }
 
 // ---------------------------------------------------------------------------
@@ -137,14 +146,12 @@ __device__ __forceinline__ float key_value(uint32_t k)
 // Which operands, and what becomes of a tile, is the kernel's mode.
 struct GemmParams {
     int M, N;              // rows and columns of the product
-    int mb, nb, bn;        // tiles, and columns of one (a multiple of 64, at most 256)
+    int mb, nb, bn;        // tiles, and columns of one (128 or 256)
     int kb;                // 64-wide steps along the contraction
     int splits;            // statistics: ranges of the columns; products: of the contraction
     int n_items;
     int n_pairs;           // products of terms: term (pair_a >> 4 i) & 15 of A by that of B
     unsigned pair_a, pair_b;
-    int chained;           // launched behind another kernel of the same call
-    int pair;              // two blocks a tile: 256 rows
     int b_row0;            // offset of B's rows (the vocabulary chunk's first)
     unsigned int *status;
     unsigned long long wait_ns;
@@ -167,31 +174,42 @@ struct GemmParams {
     int out_bf16;
 };
 
-cudaError_t launch_logprob_stats(const CUtensorMap &tm_h, const CUtensorMap &tm_w,
-                                 const GemmParams &p, int list, cudaStream_t s);
-// The same for M <= kFewRows states: tiles of 128 vocabulary rows (nb of them, bn states wide),
+// A launch: the statistics, the gradient of the logits, or both products (p[0] dh, p[1] dW; one
+// of them may have no items).  Operands in boxes of 64 elements; out: boxes of 128 bytes of columns
+// and 128 rows for the tiles' stores (G's terms; a product or its parts one behind the other).
+struct GemmLaunch {
+    struct {
+        CUtensorMap a, b, out;
+    } maps[2];
+    GemmParams p[2];
+    bool chained;          // launched behind another kernel of the same call
+    bool pair;             // two blocks a tile: 256 rows
+};
+
+cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s);
+// h against w for M <= kFewRows states: tiles of 128 vocabulary rows (nb of them, bn states wide),
 // `splits` blocks.
 cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p,
-                               cudaStream_t s);
-// tm_g: boxes of 64 columns and 128 rows, for the tiles' stores.
-cudaError_t launch_logprob_grad(const CUtensorMap &tm_h, const CUtensorMap &tm_w, const CUtensorMap &tm_g,
-                                const GemmParams &p, cudaStream_t s);
-// dh = G W (G rows of the vocabulary) and dW = G^T h (contraction over the rows).  tm_out: the
-// result, or its parts one behind the other, in boxes of 128 bytes of columns and 128 rows.
-cudaError_t launch_product_dh(const CUtensorMap &tm_g, const CUtensorMap &tm_w, const CUtensorMap &tm_out,
-                              const GemmParams &p, cudaStream_t s);
-cudaError_t launch_product_dw(const CUtensorMap &tm_g, const CUtensorMap &tm_h, const CUtensorMap &tm_out,
-                              const GemmParams &p, cudaStream_t s);
-// out = sum over the parts, in their order.
-cudaError_t launch_sum_parts(const float *part, int parts, long long elems, void *out, bool bf16,
-                             cudaStream_t s);
-// fp32 rows as three bf16 terms: planes [3][rows][d].
+                               bool chained, cudaStream_t s);
+cudaError_t launch_logprob_grad(const GemmLaunch &g, cudaStream_t s);
+// dh = G W (contraction over the vocabulary) and dW = G^T h (over the rows).
+cudaError_t launch_products(const GemmLaunch &g, cudaStream_t s);
+// out = sum over the parts, in their order; of up to two results (elems 0: none).
+struct PartsSum {
+    const float *part;
+    void *out;
+    long long elems;
+    int parts, bf16;
+};
+cudaError_t launch_sum_parts(const PartsSum (&r)[2], cudaStream_t s);
+// fp32 rows as three bf16 terms: planes [3][rows][plane_ld].
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             bool chained, cudaStream_t s);
+                             int plane_ld, bool chained, cudaStream_t s);
 
 struct GradRowsParams {
     const void *h, *w;
-    void *out;             // [N][d]
+    void *out;             // [N][out_ld]
+    int out_ld;
     float *target_logp;    // [N]
     long long h_ld, w_ld;
     int N, V, d, index_bytes;

@@ -85,6 +85,10 @@ bool overlap(std::initializer_list<Range> r, int n_out)
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
+// Row stride of rows in the workspace: whole lines of 128 bytes of bf16, so that a tile's 128-byte
+// rows do not straddle two (fp32 rows of 520 as terms of stride 520: 815 cycles a step, against 510).
+int line_ld(int d) { return (int)up64(d); }
+
 // Tiles of a product of `rows` x `cols`: one block's 128 rows or a pair's 256, 128 or 256 columns,
 // and parts of its longer dimension where there are fewer tiles than SMs.
 struct Shape {
@@ -105,9 +109,9 @@ double step_cycles(bool pair, int bn)
     return std::max(2.0 * bn, copies);
 }
 
-// `steps`: 64-wide steps of a tile.  split: 0 none, 1 the steps (parts of `part_bytes` each are then
-// written and read again), 2 the tiles of a row block (ranges of columns).
-Shape choose_shape(long long rows, long long cols, int steps, int split, int most, double part_bytes)
+// `steps`: 64-wide steps of a tile; parts: up to `most` ranges of a row block's tiles (0: an item
+// a tile).
+Shape choose_shape(long long rows, long long cols, int steps, int most)
 {
     const int sms = txl::device_sm_count();
     Shape best{};
@@ -122,20 +126,66 @@ Shape choose_shape(long long rows, long long cols, int steps, int split, int mos
         s.nb = ceil_div(cols, s.bn);
         const int units = sms / blocks;
         const double step = step_cycles(s.pair, s.bn);
-        const int n = split == 1 ? std::min(most, steps) : split == 2 ? std::min(most, s.nb) : 1;
+        const int n = std::max(1, std::min(most, s.nb));
         for (s.parts = 1; s.parts <= n; ++s.parts) {
-            const long long items = split == 2 ? (long long)s.mb * s.parts : (long long)s.mb * s.nb * s.parts;
+            const long long items = (long long)s.mb * (most ? s.parts : s.nb);
             const double waves = (double)((items + units - 1) / units);
-            const double work = split == 1 ? (double)ceil_div(steps, s.parts)
-                                           : (double)steps * (split == 2 ? ceil_div(s.nb, s.parts) : 1);
-            // (parts: written and read at 3.6 kB a cycle)
-            const double cost = waves * (work * step + kUnitCost) +
-                                (split == 1 && s.parts > 1 ? s.parts * 2.0 * part_bytes / 3600.0 : 0.0);
+            const double cost = waves * ((double)steps * (most ? ceil_div(s.nb, s.parts) : 1) * step + kUnitCost);
             if (best.mb == 0 || cost < least) {
                 best = s;
                 least = cost;
             }
         }
+    }
+    return best;
+}
+
+// The tiles and parts of two products that share a launch: the tiles of the second follow those
+// of the first over the units in turn.  Parts in a few steps; the same kind of unit for both.
+struct Two {
+    Shape a, b;
+};
+
+Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&most)[2])
+{
+    static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    const int sms = txl::device_sm_count();
+    Two best{};
+    double least = 0.0;
+    struct Option {
+        Shape s;
+        long long items;
+        double cost, extra;  // cycles of an item, of the parts' sum
+    };
+    for (int pair = 1; pair >= 0; --pair) {
+        const int blocks = pair ? 2 : 1, units = sms / blocks;
+        Option o[2][16];
+        int n[2] = {};
+        for (int i = 0; i < 2; ++i)
+            for (const int bn : {256, 128}) {
+                if (bn == 256 && cols <= 128) continue;
+                for (const int parts : kParts) {
+                    if (parts > most[i]) break;
+                    Option &x = o[i][n[i]++];
+                    x.s = {pair != 0, bn, ceil_div(rows[i], 128 * blocks), ceil_div(cols, bn), parts};
+                    x.items = (long long)x.s.mb * x.s.nb * parts;
+                    x.cost = (double)ceil_div(steps[i], parts) * step_cycles(x.s.pair, bn) + kUnitCost;
+                    x.extra = parts > 1 ? parts * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
+                }
+            }
+        for (int i = 0; i < n[0]; ++i)
+            for (int j = 0; j < n[1]; ++j) {
+                const Option &x = o[0][i], &y = o[1][j];
+                const long long rx = x.items % units, ry = y.items % units;
+                double cost = (double)(x.items / units) * x.cost + (double)(y.items / units) * y.cost;
+                const double last = (rx ? x.cost : 0.0) + (ry ? y.cost : 0.0);
+                cost += rx + ry > units ? last : std::max(rx ? x.cost : 0.0, ry ? y.cost : 0.0);
+                cost += x.extra + y.extra;
+                if (best.a.mb == 0 || cost < least) {
+                    best = {x.s, y.s};
+                    least = cost;
+                }
+            }
     }
     return best;
 }
@@ -163,7 +213,7 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
         s.splits = std::min(s.nb, std::min(txl::device_sm_count(), txl::kMaxStatSplits));
     } else {
         const int terms = dtype == TXL_F32 ? 6 : 1;
-        const Shape c = choose_shape(N, V, ceil_div(d, 64) * terms, 2, txl::kMaxRowSplits, 0.0);
+        const Shape c = choose_shape(N, V, ceil_div(d, 64) * terms, txl::kMaxRowSplits);
         s.pair = c.pair;
         s.mb = c.mb;
         s.bn = c.bn;
@@ -172,7 +222,7 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     }
     s.list = txl::list_length(top);
     size_t o = 0;
-    const size_t row = (size_t)d * 2 * txl::kMaxPieces;
+    const size_t row = (size_t)line_ld(d) * 2 * txl::kMaxPieces;
     s.h_planes = o;
     if (dtype == TXL_F32) o = up256(o + N * row);
     s.w_planes = o;
@@ -204,7 +254,7 @@ struct GradPlan {
     size_t live, target_logp, h_planes, w_planes, g_at, part_h, part_w, total;
 };
 
-GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
+GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
 {
     GradPlan g{};
     g.pieces = dtype == TXL_F32 ? 3 : grad_dtype == TXL_F32 ? 2 : 1;
@@ -217,17 +267,16 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
     g.g_ld = up128(g.chunk);
     g.g_plane = g.g_ld * N;
     const int terms = dtype == TXL_F32 ? 6 : 1, terms_w = dtype == TXL_F32 ? 6 : g.pieces;
-    g.g = choose_shape(N, g.chunk, ceil_div(d, 64) * terms, 0, 1, 0.0);
-    g.h = choose_shape(N, d, ceil_div(g.chunk, 64) * terms, 1, 16, (double)N * d * 4);
-    g.w = choose_shape(g.chunk, d, ceil_div(N, 64) * terms_w, 1, 16, (double)g.chunk * d * 4);
-    // (parts are of the contraction's own 64-wide steps)
-    g.h.parts = std::min(g.h.parts, ceil_div(g.chunk, 64));
-    g.w.parts = std::min(g.w.parts, ceil_div(N, 64));
+    g.g = choose_shape(N, g.chunk, ceil_div(d, 64) * terms, 0);
+    const int kb_h = ceil_div(g.chunk, 64), kb_w = ceil_div(N, 64);
+    const Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h * terms, kb_w * terms_w}, {kb_h, kb_w});
+    g.h = two.a;
+    g.w = two.b;
     g.parts_h = g.chunks * g.h.parts;
     size_t o = 0;
-    const size_t row = (size_t)d * 2 * txl::kMaxPieces;
+    const size_t row = (size_t)line_ld(d) * 2 * txl::kMaxPieces;
     g.live = o;
-    o = up256(o + (size_t)N * d * elem(dtype));
+    o = up256(o + (size_t)N * line_ld(d) * elem(dtype));
     g.target_logp = o;
     o = up256(o + (size_t)N * 4);
     g.h_planes = o;
@@ -242,6 +291,23 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
     if (g.w.parts > 1) o = up256(o + (size_t)g.w.parts * g.chunk * d * 4);
     g.total = o;
     return g;
+}
+
+// A training loop asks for one plan again and again: the thread's last one is kept (its sizes, that
+// is; choosing takes some microseconds).
+GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
+{
+    struct Last {
+        int key[6] = {};
+        GradPlan plan;
+    };
+    static thread_local Last last;
+    const int key[6] = {N, V, d, dtype, grad_dtype, txl::device_sm_count()};
+    if (!std::equal(key, key + 6, last.key)) {
+        last.plan = make_grad_plan(N, V, d, dtype, grad_dtype);
+        std::copy(key, key + 6, last.key);
+    }
+    return last.plan;
 }
 
 // Products of terms of two operands with pa and pb bf16 terms, the smallest first.
@@ -268,7 +334,7 @@ struct Operand {
 Operand operand(const void *p, long long ld, const char *planes, int rows, int d, int dtype)
 {
     if (dtype == TXL_BF16) return {p, ld, 1, ld * rows};
-    return {planes, d, txl::kMaxPieces, (long long)rows * d};
+    return {planes, line_ld(d), txl::kMaxPieces, (long long)rows * line_ld(d)};
 }
 
 bool map_of(CUtensorMap *map, const Operand &o, int rows, int d, unsigned box_rows)
@@ -402,21 +468,21 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
 
     if (dtype == TXL_F32) {
         cudaError_t e = txl::launch_split_f32(static_cast<const float *>(h), h_stride, N, d,
-                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), false, st);
+                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), line_ld(d), false, st);
         if (e == cudaSuccess)
             e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), true, st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), line_ld(d), true, st);
         if (e != cudaSuccess) return TXL_ERR_CUDA;
     }
     const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
-    CUtensorMap tm_h, tm_w;
-    if (!map_of(&tm_h, oh, N, d, s.few ? (unsigned)s.bn : 128u) ||
-        !map_of(&tm_w, ow, V, d, s.few ? 128u : (unsigned)(s.pair ? s.bn / 2 : s.bn)))
+    txl::GemmLaunch l{};
+    l.chained = dtype == TXL_F32;
+    l.pair = s.pair;
+    if (!map_of(&l.maps[0].a, oh, N, d, s.few ? (unsigned)s.bn : 128u) ||
+        !map_of(&l.maps[0].b, ow, V, d, s.few ? 128u : (unsigned)(s.pair ? s.bn / 2 : s.bn)))
         return TXL_ERR_CUDA;
-    GemmParams p{};
-    p.chained = dtype == TXL_F32;
-    p.pair = s.pair;
+    GemmParams &p = l.p[0];
     p.M = N;
     p.N = V;
     p.V = V;
@@ -438,8 +504,8 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.group_key = top > 0 ? reinterpret_cast<unsigned *>(ws + s.keys) : nullptr;
     p.logits = s.full ? reinterpret_cast<float *>(ws + s.logits) : nullptr;
     p.target_z = reinterpret_cast<float *>(ws + s.target_z);
-    if ((s.few ? txl::launch_logprob_few(tm_w, tm_h, p, st)
-               : txl::launch_logprob_stats(tm_h, tm_w, p, s.list, st)) != cudaSuccess)
+    if ((s.few ? txl::launch_logprob_few(l.maps[0].b, l.maps[0].a, p, l.chained, st)
+               : txl::launch_logprob_stats(l, s.list, st)) != cudaSuccess)
         return TXL_ERR_CUDA;
 
     txl::MergeParams m{};
@@ -524,6 +590,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     l.h = h;
     l.w = w;
     l.out = ws + g.live;
+    l.out_ld = line_ld(d);
     l.target_logp = reinterpret_cast<float *>(ws + g.target_logp);
     l.h_ld = h_stride;
     l.w_ld = w_stride;
@@ -539,18 +606,17 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     cudaError_t e = txl::launch_grad_rows(l, dtype == TXL_BF16, st);
     if (dtype == TXL_F32) {
         if (e == cudaSuccess)
-            e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), d, N, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), true, st);
+            e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), line_ld(d), N, d,
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), line_ld(d), true, st);
         if (e == cudaSuccess)
             e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), true, st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), line_ld(d), true, st);
     }
     if (e != cudaSuccess) return TXL_ERR_CUDA;
-    const Operand oh = operand(ws + g.live, d, ws + g.h_planes, N, d, dtype);
+    const Operand oh = operand(ws + g.live, line_ld(d), ws + g.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + g.w_planes, V, d, dtype);
 
     GemmParams base{};
-    base.chained = 1;
     base.status = status;
     base.wait_ns = txl::wait_limit_ns();
     base.V = V;
@@ -558,22 +624,27 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.targets = targets;
     base.index_bytes = index_type;
     base.lse = lse;
-    base.target_logp = l.target_logp;
     base.entropy = entropy;
+    base.target_logp = l.target_logp;
     base.dlogp = dlogp;
     base.dentropy = dentropy;
     base.g_pieces = g.pieces;
-    CUtensorMap h_rows, w_rows, h_cols, w_cols;
-    if (!map_of(&h_rows, oh, N, d, 128) || !map_of(&w_rows, ow, V, d, (unsigned)(g.g.pair ? g.g.bn / 2 : g.g.bn)) ||
-        !map_of(&h_cols, oh, N, d, 64) || !map_of(&w_cols, ow, V, d, 64))
+    txl::GemmLaunch grad{}, prod{};
+    grad.chained = prod.chained = true;
+    grad.pair = g.g.pair;
+    prod.pair = g.h.pair;
+    if (!map_of(&grad.maps[0].a, oh, N, d, 128) ||
+        !map_of(&grad.maps[0].b, ow, V, d, (unsigned)(g.g.pair ? g.g.bn / 2 : g.g.bn)) ||
+        !map_of(&prod.maps[0].b, ow, V, d, 64) || !map_of(&prod.maps[1].b, oh, N, d, 64))
         return TXL_ERR_CUDA;
+    const Operand og = {ws + g.g_at, g.g_ld, g.pieces, g.g_plane};
     for (int c = 0; c < g.chunks; ++c) {
         const int v0 = c * g.chunk, cols = std::min(g.chunk, V - v0);
         // G of the chunk
-        GemmParams p = base;
+        GemmParams &p = grad.p[0];
+        p = base;
         p.M = N;
         p.N = cols;
-        p.pair = g.g.pair;
         p.mb = g.g.mb;
         p.bn = g.g.bn;
         p.nb = ceil_div(cols, p.bn);
@@ -582,15 +653,15 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         p.n_items = p.mb * p.nb;
         p.b_row0 = v0;
         set_pairs(p, oh.planes, ow.planes);
-        const Operand og = {ws + g.g_at, g.g_ld, g.pieces, g.g_plane};
-        CUtensorMap g_rows;
-        if (!map_of(&g_rows, og, N, cols, 128)) return TXL_ERR_CUDA;
-        if (txl::launch_logprob_grad(h_rows, w_rows, g_rows, p, st) != cudaSuccess) return TXL_ERR_CUDA;
+        if (!map_of(&grad.maps[0].out, og, N, cols, 128)) return TXL_ERR_CUDA;
+        if (txl::launch_logprob_grad(grad, st) != cudaSuccess) return TXL_ERR_CUDA;
+        prod.maps[0].a = grad.maps[0].out;
+        prod.p[0] = prod.p[1] = base;
+        txl::PartsSum sums[2] = {};
         if (dh) {
-            GemmParams q = base;
+            GemmParams &q = prod.p[0];
             q.M = N;
             q.N = d;
-            q.pair = g.h.pair;
             q.mb = g.h.mb;
             q.nb = g.h.nb;
             q.bn = g.h.bn;
@@ -600,20 +671,19 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.b_row0 = v0;
             q.part = g.parts_h > 1;
             q.out_bf16 = dtype == TXL_BF16;
-            CUtensorMap out;
-            if (!map_out(&out, q, q.part ? ws + g.part_h + (size_t)c * g.h.parts * N * d * 4 : (char *)dh))
-                return TXL_ERR_CUDA;
             set_pairs(q, dtype == TXL_F32 ? g.pieces : 1, ow.planes);
-            if (txl::launch_product_dh(g_rows, w_cols, out, q, st) != cudaSuccess) return TXL_ERR_CUDA;
+            if (!map_out(&prod.maps[0].out, q,
+                         q.part ? ws + g.part_h + (size_t)c * g.h.parts * N * d * 4 : (char *)dh))
+                return TXL_ERR_CUDA;
+            if (q.part && c + 1 == g.chunks)
+                sums[0] = {reinterpret_cast<float *>(ws + g.part_h), dh, (long long)N * d, g.parts_h,
+                           dtype == TXL_BF16};
         }
         if (dw) {
-            CUtensorMap tm_g;
-            if (!map_of(&tm_g, og, N, cols, 64)) return TXL_ERR_CUDA;
             char *rows = static_cast<char *>(dw) + (size_t)v0 * d * elem(grad_dtype);
-            GemmParams q = base;
+            GemmParams &q = prod.p[1];
             q.M = cols;
             q.N = d;
-            q.pair = g.w.pair;
             q.mb = ceil_div(cols, g.w.pair ? 256 : 128);
             q.nb = g.w.nb;
             q.bn = g.w.bn;
@@ -622,20 +692,17 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.n_items = q.mb * q.nb * q.splits;
             q.part = g.w.parts > 1;
             q.out_bf16 = grad_dtype == TXL_BF16;
-            CUtensorMap out;
-            if (!map_out(&out, q, q.part ? ws + g.part_w : rows)) return TXL_ERR_CUDA;
             set_pairs(q, g.pieces, oh.planes);
-            if (txl::launch_product_dw(tm_g, h_cols, out, q, st) != cudaSuccess) return TXL_ERR_CUDA;
-            if (q.part && txl::launch_sum_parts(reinterpret_cast<float *>(ws + g.part_w), g.w.parts,
-                                                (long long)cols * d, rows, grad_dtype == TXL_BF16,
-                                                st) != cudaSuccess)
+            if (!map_of(&prod.maps[1].a, og, N, cols, 64) ||
+                !map_out(&prod.maps[1].out, q, q.part ? ws + g.part_w : rows))
                 return TXL_ERR_CUDA;
+            if (q.part)
+                sums[1] = {reinterpret_cast<float *>(ws + g.part_w), rows, (long long)cols * d, g.w.parts,
+                           grad_dtype == TXL_BF16};
         }
+        if (txl::launch_products(prod, st) != cudaSuccess) return TXL_ERR_CUDA;
+        if (txl::launch_sum_parts(sums, st) != cudaSuccess) return TXL_ERR_CUDA;
     }
-    if (dh && g.parts_h > 1 &&
-        txl::launch_sum_parts(reinterpret_cast<float *>(ws + g.part_h), g.parts_h, (long long)N * d, dh,
-                              dtype == TXL_BF16, st) != cudaSuccess)
-        return TXL_ERR_CUDA;
     return TXL_OK;
 }
 
