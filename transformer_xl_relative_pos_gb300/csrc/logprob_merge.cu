@@ -625,8 +625,9 @@ __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long lon
 }
 
 // One warp per row: a copy of h with zeros in rows that have no part in the gradient (whatever
-// those hold), and the log probability of the row's target from its logit's products carried
-// beyond fp32: G's one large element is the difference of 1 and that probability.
+// those hold), and the log probability of the row's target from its logit summed with rounding (of fp32
+// operands: carried beyond fp32), not by the accumulators that cut: G's one large element is the
+// difference of 1 and that probability.
 template <bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p)
 {
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
     const bool live = target >= 0 || (p.dentropy && p.dentropy[row] != 0.f);
     const uint4 *w = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.w) + max(target, 0) * p.w_ld * ESIZE);
     ExactSum sum;
+    float chain[4] = {};  // (bf16: rounded sums will do beside G's own rounding)
     for (int c0 = lane; c0 < vecs; c0 += 128) {
         if (c0 > lane) load(c0);
         uint4 y[4];
@@ -659,10 +661,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (c0 + 32 * k < vecs) dst[c0 + 32 * k] = live ? h[k] : make_uint4(0, 0, 0, 0);
-            sum.add<BF16>(h[k], y[k]);
+            if (BF16) {
+                const uint32_t xp[4] = {h[k].x, h[k].y, h[k].z, h[k].w}, yp[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    chain[i] = fmaf(__uint_as_float(xp[i] << 16), __uint_as_float(yp[i] << 16), chain[i]);
+                    chain[i] = fmaf(__uint_as_float(xp[i] & 0xffff0000u), __uint_as_float(yp[i] & 0xffff0000u),
+                                    chain[i]);
+                }
+            } else {
+                sum.add<BF16>(h[k], y[k]);
+            }
         }
     }
-    const Wide z = sum.over_warp();
+    Wide z{(chain[0] + chain[1]) + (chain[2] + chain[3]), 0.f};
+    if (BF16) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z.hi += __shfl_xor_sync(0xffffffffu, z.hi, o);
+    } else {
+        z = sum.over_warp();
+    }
     if (lane == 0) p.target_logp[row] = target < 0 ? 0.f : fmaf(z.hi, p.scale, -p.lse[row]) + z.lo * p.scale;
 }
 

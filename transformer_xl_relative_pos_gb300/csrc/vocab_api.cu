@@ -86,7 +86,8 @@ bool overlap(std::initializer_list<Range> r, int n_out)
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Row stride of rows in the workspace: whole lines of 128 bytes of bf16, so that a tile's 128-byte
-// rows do not straddle two (fp32 rows of 520 as terms of stride 520: 815 cycles a step, against 510).
+// rows do not straddle two (G of 333 x 5003 from fp32 rows of 520: 28.8 us with terms of stride 520, 24.3
+// so).
 int line_ld(int d) { return (int)up64(d); }
 
 // Tiles of a product of `rows` x `cols`: one block's 128 rows or a pair's 256, 128 or 256 columns,
@@ -96,9 +97,9 @@ struct Shape {
     int bn, mb, nb, parts;
 };
 
-// What a part adds besides its own work, in cycles: its start and end (the first copies, the last
-// tile's epilogue).
-constexpr double kUnitCost = 5000.0;
+// What an item adds besides its steps, in cycles: its epilogue runs beside the next item's steps,
+// but its accumulator's first use and its stores do not quite.
+constexpr double kUnitCost = 1500.0;
 
 // Cycles of one 64-wide step: the MMAs' (256 columns: 512) or the copies' at some 58 bytes a cycle
 // and SM, as measured of the statistics of 2048 x 131072 (pairs: 602 cycles a step, single blocks 653,
