@@ -165,3 +165,47 @@ def test_a_training_step_of_one_tied_layer():
     only = txl.logprob_bwd(h, Ed, D(nxt), res.lse, D(dlogp), entropy=res.entropy, dentropy=D(dent),
                            grad_dtype=F32)[1]
     assert float((only.cpu().double() - want).norm() / want.norm()) > 0.2
+
+
+def test_captured_behind_copies_and_other_streams():
+    # calls in one graph behind a copy, behind torch kernels, behind one another and behind a second
+    # stream that joins: replays follow what those leave
+    V, d, n = 300, 64, 500
+    g = torch.Generator().manual_seed(4)
+    E = (torch.randn(V, d, generator=g) * 0.3).to(BF).to(dev())
+    src = torch.randint(0, V, (n,), generator=g).to(dev())
+    toks, h = torch.zeros_like(src), torch.zeros(n, d, dtype=BF, device=dev())
+    dlogp = torch.randn(n, generator=g).to(dev())
+    other = torch.cuda.Stream()
+
+    def step(stream=None):
+        toks.copy_(src)                                    # a copy, then our kernel
+        h.copy_(txl.embed_fwd(toks, E, scale=2.0))
+        if stream is not None:                             # a second stream in between
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                h.mul_(1.5)
+            torch.cuda.current_stream().wait_stream(stream)
+        else:
+            h.mul_(1.5)
+        res = txl.logprob_fwd(h, E, toks, top=3)
+        few = txl.logprob_fwd(h[:20], E, toks[:20], top=3)
+        dh, dE = txl.logprob_bwd(h, E, toks, res.lse, dlogp, grad_dtype=F32)
+        txl.embed_bwd(dh, toks, V, out=dE, accumulate=True)
+        return [*res, *few, dh, dE]
+
+    want = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(other)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        _ok()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    src.copy_(torch.flip(src, (0,)))
+    want = [t.clone() for t in step()]
+    graph.replay()
+    _ok()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedParam
     const VEC *emb = static_cast<const VEC *>(p.emb);
     VEC *out = static_cast<VEC *>(p.out);
     VEC v[kFwdVecs];
+    chain_wait();
+    chain_go();
 #pragma unroll
     for (int k = 0; k < kFwdVecs; ++k) {
         const long long i = base + k * kFwdThreads;
@@ -143,6 +145,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
     const int block = blockIdx.x;
     const long long lo_ = ((long long)block * kSortWarps + warp) * p.per_warp;
     const int lo = (int)min((long long)p.n, lo_), hi = (int)min((long long)p.n, lo_ + p.per_warp);
+    chain_wait();
     chain_go();
     if (block >= p.blocks) {
         clear_gradient(p, kSortThreads);
@@ -260,6 +263,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_sort_kernel(const SortParam
 {
     __shared__ int4 s_key[kRankMost / 4];
     __shared__ int s_rank[32];
+    chain_wait();
     chain_go();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int)blockIdx.x >= p.blocks) {
@@ -477,6 +481,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_runs_kernel(const SumPar
     const int shares = kJoinWarps / wide, slice = warp % wide, share = warp / wide;
     __shared__ float4 sums[kJoinWarps][32];
     chain_wait();
+    chain_go();
     const int runs = *p.crossing;
     for (int run = blockIdx.x; run < runs; run += gridDim.x) {
         const int2 begin = p.cross[run];
@@ -564,13 +569,12 @@ Layout layout(int n, int d)
 template <bool BF16, bool GRAD_BF16>
 cudaError_t sum_and_join(const SumParams &r, int sum_blocks, cudaStream_t s)
 {
-    cudaError_t e = launch_chained(sum_runs_kernel<BF16, GRAD_BF16>, dim3((unsigned)sum_blocks),
-                                   kSumWarps * 32, 0, s, r);
+    cudaError_t e = launch_grid(sum_runs_kernel<BF16, GRAD_BF16>, dim3((unsigned)sum_blocks), kSumWarps * 32, 0, s, 1, r);
     if (e == cudaSuccess && r.chunks > 1) {
         int wide = 1;   // slices of 128 columns side by side
         while (wide < 8 && wide * 128 < r.d) wide *= 2;
         const unsigned blocks = (unsigned)std::min(r.chunks - 1, 4 * device_sm_count());
-        e = launch_chained(join_runs_kernel<GRAD_BF16>, dim3(blocks), kJoinWarps * 32, 0, s, r, wide);
+        e = launch_grid(join_runs_kernel<GRAD_BF16>, dim3(blocks), kJoinWarps * 32, 0, s, 1, r, wide);
     }
     return e;
 }
@@ -612,11 +616,9 @@ cudaError_t launch_embed_fwd(const EmbedParams &p, bool bf16, cudaStream_t s)
     const long long ld = wide ? p.emb_ld / per : p.emb_ld;
     const long long total = (long long)p.n * row_vec;
     const unsigned grid = (unsigned)((total + kFwdThreads * kFwdVecs - 1) / (kFwdThreads * kFwdVecs));
-    if (wide && bf16) embed_fwd_kernel<true, uint4><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
-    else if (wide) embed_fwd_kernel<false, uint4><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
-    else if (bf16) embed_fwd_kernel<true, __nv_bfloat16><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
-    else embed_fwd_kernel<false, float><<<grid, kFwdThreads, 0, s>>>(p, row_vec, ld);
-    return cudaGetLastError();
+    auto *kernel = wide ? (bf16 ? embed_fwd_kernel<true, uint4> : embed_fwd_kernel<false, uint4>)
+                        : (bf16 ? embed_fwd_kernel<true, __nv_bfloat16> : embed_fwd_kernel<false, float>);
+    return launch_grid(kernel, dim3(grid), kFwdThreads, 0, s, 1, p, row_vec, ld);
 }
 
 size_t embed_bwd_workspace_bytes(int n, int d) { return layout(n, d).total; }
@@ -652,8 +654,8 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16,
         more = (int)((std::min(want, room) + unit - 1) / unit * unit);
     }
     const dim3 grid((unsigned)(q.blocks + more));
-    const cudaError_t e = few ? launch_grid(rank_sort_kernel, grid, kRankThreads, 0, s, false, 1, q)
-                              : launch_grid(sort_kernel, grid, kSortThreads, 0, s, false, (unsigned)q.blocks, q);
+    const cudaError_t e = few ? launch_grid(rank_sort_kernel, grid, kRankThreads, 0, s, 1, q)
+                              : launch_grid(sort_kernel, grid, kSortThreads, 0, s, (unsigned)q.blocks, q);
     if (e != cudaSuccess) return e;
     const int sorted = few ? 0 : q.passes & 1;
 

@@ -620,7 +620,7 @@ cudaError_t launch_units(const GemmLaunch &g, cudaStream_t s)
     }
     const int items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
     const unsigned grid = (unsigned)(min(items, device_sm_count() / BLOCKS) * BLOCKS);
-    return launch_grid(kernel, dim3(grid), kThreads, SMEM, s, g.chained, BLOCKS, g);
+    return launch_grid(kernel, dim3(grid), kThreads, SMEM, s, BLOCKS, g);
 }
 
 template <Mode MODE, int LIST>

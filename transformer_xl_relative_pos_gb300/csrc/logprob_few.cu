@@ -317,8 +317,7 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
 }
 
 template <int GROUPS>
-cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p, bool chained,
-                   cudaStream_t s)
+cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p, cudaStream_t s)
 {
     static bool attr_set[64] = {};  // the attribute is set once per device
     int dev = 0;
@@ -331,21 +330,18 @@ cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmP
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const int ns = min(MAX_NS, RING / (A_BYTES + p.bn * BK * 2));
-    if (chained)
-        return launch_chained(logprob_few_kernel<GROUPS>, dim3((unsigned)p.splits), (4 + kEpiWarps) * 32, SMEM_BYTES,
-                              s, tm_w, tm_h, p, ns);
-    logprob_few_kernel<GROUPS><<<(unsigned)p.splits, (4 + kEpiWarps) * 32, SMEM_BYTES, s>>>(tm_w, tm_h, p, ns);
-    return cudaGetLastError();
+    return launch_grid(logprob_few_kernel<GROUPS>, dim3((unsigned)p.splits), (4 + kEpiWarps) * 32, SMEM_BYTES, s, 1,
+                       tm_w, tm_h, p, ns);
 }
 
 } // namespace
 
 cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p,
-                               bool chained, cudaStream_t s)
+                               cudaStream_t s)
 {
     const int groups = (p.M + 63) / 64;
-    if (groups == 1) return launch<1>(tm_w, tm_h, p, chained, s);
-    return groups == 2 ? launch<2>(tm_w, tm_h, p, chained, s) : launch<4>(tm_w, tm_h, p, chained, s);
+    if (groups == 1) return launch<1>(tm_w, tm_h, p, s);
+    return groups == 2 ? launch<2>(tm_w, tm_h, p, s) : launch<4>(tm_w, tm_h, p, s);
 }
 
 } // namespace txl

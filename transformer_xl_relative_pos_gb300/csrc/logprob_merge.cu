@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
 {
     constexpr unsigned FULL = 0xffffffffu;
     chain_wait();
+    chain_go();
     constexpr int PER = 2 * kMaxRowSplits / 32, WANT = LIST > 0 ? LIST : 1;
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x;
     chain_wait();
+    chain_go();
     const int target = p.targets ? token_at(p.targets, p.index_bytes, row, p.V, p.status) : -1;
     const int esize = BF16 ? 2 : 4;
     const char *h = static_cast<const char *>(p.h) + row * p.h_ld * esize;
@@ -631,6 +633,7 @@ __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long lon
 template <bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p)
 {
+    chain_wait();
     chain_go();
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
@@ -691,23 +694,22 @@ cudaError_t launch_sum_parts(const PartsSum (&r)[2], cudaStream_t s)
     const auto blocks = [](const PartsSum &x) { return (int)((x.elems / 4 + 255) / 256); };
     const int b0 = blocks(r[0]), b1 = blocks(r[1]);
     if (b0 + b1 == 0) return cudaSuccess;
-    return launch_chained(sum_parts_kernel, dim3((unsigned)(b0 + b1)), 256, 0, s, r[0], r[1], b0);
+    return launch_grid(sum_parts_kernel, dim3((unsigned)(b0 + b1)), 256, 0, s, 1, r[0], r[1], b0);
 }
 
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             int plane_ld, bool chained, cudaStream_t s)
+                             int plane_ld, cudaStream_t s)
 {
     const long long vecs = (long long)rows * (d / 8);
-    return launch_grid(split_f32_kernel, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, chained, 1, x, ld, rows,
+    return launch_grid(split_f32_kernel, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, 1, x, ld, rows,
                        d / 8, planes, plane_ld / 8);
 }
 
 cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
 {
     const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
-    if (bf16) grad_rows_kernel<true><<<grid, kMergeWarps * 32, 0, s>>>(p);
-    else grad_rows_kernel<false><<<grid, kMergeWarps * 32, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_grid(bf16 ? grad_rows_kernel<true> : grad_rows_kernel<false>, dim3(grid), kMergeWarps * 32, 0, s, 1,
+                       p);
 }
 
 cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream_t s)
@@ -715,14 +717,14 @@ cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream
     const unsigned grid = (unsigned)p.N;
     auto *kernel = bf16 ? (p.logits ? logprob_few_merge_kernel<true, true> : logprob_few_merge_kernel<true, false>)
                         : (p.logits ? logprob_few_merge_kernel<false, true> : logprob_few_merge_kernel<false, false>);
-    return launch_chained(kernel, dim3(grid), kFewThreads, 0, s, p);
+    return launch_grid(kernel, dim3(grid), kFewThreads, 0, s, 1, p);
 }
 
 template <bool BF16, int LIST>
 cudaError_t merge(const MergeParams &p, cudaStream_t s)
 {
     const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
-    return launch_chained(logprob_merge_kernel<BF16, LIST>, dim3(grid), kMergeWarps * 32, 0, s, p);
+    return launch_grid(logprob_merge_kernel<BF16, LIST>, dim3(grid), kMergeWarps * 32, 0, s, 1, p);
 }
 
 cudaError_t launch_logprob_merge(const MergeParams &p, bool bf16, cudaStream_t s)

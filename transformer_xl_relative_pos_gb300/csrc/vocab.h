@@ -20,12 +20,13 @@ bool make_map_planes(CUtensorMap *map, const void *base, long long inner, long l
 bool make_map_planes_f32(CUtensorMap *map, const void *base, long long inner, long long rows,
                          long long ld, long long planes, long long plane, unsigned box_rows);
 
-// A launch in clusters of `cluster` blocks.  Chained: it may begin while its predecessor in the
-// stream still runs; the kernel waits for that one's end and writes (chain_wait) before it reads
-// or writes anything, so only launch and set-up overlap.
+// A launch in clusters of `cluster` blocks that may begin while its predecessor in the stream
+// still runs: every kernel here waits for that one's end and writes (chain_wait) before it reads or
+// writes anything, so only launches and set-up overlap.  After a kernel that gives no leave
+// (chain_go) it is an ordinary launch.
 template <typename... P, typename... A>
 cudaError_t launch_grid(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
-                        bool chained, unsigned cluster, const A &...args)
+                        unsigned cluster, const A &...args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -34,24 +35,16 @@ cudaError_t launch_grid(void (*kernel)(P...), dim3 grid, unsigned threads, size_
     cfg.stream = s;
     cudaLaunchAttribute attr[2] = {};
     cfg.attrs = attr;
-    if (chained) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
     if (cluster > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = cluster;
-        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
-                           const A &...args)
-{
-    return launch_grid(kernel, grid, threads, smem, s, true, 1, args...);
 }
 
 // ---------------------------------------------------------------------------
@@ -182,7 +175,6 @@ struct GemmLaunch {
         CUtensorMap a, b, out;
     } maps[2];
     GemmParams p[2];
-    bool chained;          // launched behind another kernel of the same call
     bool pair;             // two blocks a tile: 256 rows
 };
 
@@ -190,7 +182,7 @@ cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s);
 // h against w for M <= kFewRows states: tiles of 128 vocabulary rows (nb of them, bn states wide),
 // `splits` blocks.
 cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p,
-                               bool chained, cudaStream_t s);
+                               cudaStream_t s);
 cudaError_t launch_logprob_grad(const GemmLaunch &g, cudaStream_t s);
 // dh = G W (contraction over the vocabulary) and dW = G^T h (over the rows).
 cudaError_t launch_products(const GemmLaunch &g, cudaStream_t s);
@@ -204,7 +196,7 @@ struct PartsSum {
 cudaError_t launch_sum_parts(const PartsSum (&r)[2], cudaStream_t s);
 // fp32 rows as three bf16 terms: planes [3][rows][plane_ld].
 cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             int plane_ld, bool chained, cudaStream_t s);
+                             int plane_ld, cudaStream_t s);
 
 struct GradRowsParams {
     const void *h, *w;

@@ -469,16 +469,15 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
 
     if (dtype == TXL_F32) {
         cudaError_t e = txl::launch_split_f32(static_cast<const float *>(h), h_stride, N, d,
-                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), line_ld(d), false, st);
+                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), line_ld(d), st);
         if (e == cudaSuccess)
             e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), line_ld(d), true, st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), line_ld(d), st);
         if (e != cudaSuccess) return TXL_ERR_CUDA;
     }
     const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
     txl::GemmLaunch l{};
-    l.chained = dtype == TXL_F32;
     l.pair = s.pair;
     if (!map_of(&l.maps[0].a, oh, N, d, s.few ? (unsigned)s.bn : 128u) ||
         !map_of(&l.maps[0].b, ow, V, d, s.few ? 128u : (unsigned)(s.pair ? s.bn / 2 : s.bn)))
@@ -505,7 +504,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.group_key = top > 0 ? reinterpret_cast<unsigned *>(ws + s.keys) : nullptr;
     p.logits = s.full ? reinterpret_cast<float *>(ws + s.logits) : nullptr;
     p.target_z = reinterpret_cast<float *>(ws + s.target_z);
-    if ((s.few ? txl::launch_logprob_few(l.maps[0].b, l.maps[0].a, p, l.chained, st)
+    if ((s.few ? txl::launch_logprob_few(l.maps[0].b, l.maps[0].a, p, st)
                : txl::launch_logprob_stats(l, s.list, st)) != cudaSuccess)
         return TXL_ERR_CUDA;
 
@@ -608,10 +607,10 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     if (dtype == TXL_F32) {
         if (e == cudaSuccess)
             e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), line_ld(d), N, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), line_ld(d), true, st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), line_ld(d), st);
         if (e == cudaSuccess)
             e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), line_ld(d), true, st);
+                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), line_ld(d), st);
     }
     if (e != cudaSuccess) return TXL_ERR_CUDA;
     const Operand oh = operand(ws + g.live, line_ld(d), ws + g.h_planes, N, d, dtype);
@@ -631,7 +630,6 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.dentropy = dentropy;
     base.g_pieces = g.pieces;
     txl::GemmLaunch grad{}, prod{};
-    grad.chained = prod.chained = true;
     grad.pair = g.g.pair;
     prod.pair = g.h.pair;
     if (!map_of(&grad.maps[0].a, oh, N, d, 128) ||
