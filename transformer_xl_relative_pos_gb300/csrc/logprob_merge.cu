@@ -598,32 +598,83 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const PartsSum r0, const
 
 // x = t0 + t1 + t2, each the bf16 nearest to what is left (exact but for what falls below
 // bf16's range).  An infinite or NaN value is its first term; a finite one that rounds to
-// infinity is cut instead.  Eight values a thread.
-__global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long long ld, int rows, int vecs,
-                                                        __nv_bfloat16 *planes, int plane_vecs)
+// infinity is cut instead.
+__device__ __forceinline__ float next_term(float &x)
+{
+    __nv_bfloat16 n = __float2bfloat16_rn(x);
+    if (__hisinf(n) && !isinf(x)) n = __float2bfloat16_rz(x);
+    const float t = __bfloat162float(n);
+    x = isfinite(x) ? x - t : 0.f;
+    return t;
+}
+
+// Four values: their terms to the three planes (dst of the first, planes `plane` elements apart).
+__device__ __forceinline__ void split4(const uint4 &x, __nv_bfloat16 *dst, long long plane)
+{
+    float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+#pragma unroll
+    for (int t = 0; t < kMaxPieces; ++t) {
+        float y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = next_term(v[k]);
+        *reinterpret_cast<uint2 *>(dst + t * plane) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    }
+}
+
+// A thread takes two vectors of eight, `threads` apart.
+__device__ __forceinline__ void split_block(const SplitRows &r, long long block, int threads)
+{
+    const int vecs = r.d / 8;
+    const long long total = (long long)r.rows * vecs, base = block * threads * 2 + threadIdx.x;
+    const long long plane = (long long)r.rows * r.plane_ld;
+    uint4 v[2][2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const long long i = base + k * threads;
+        if (i >= total) continue;
+        const int row = (int)(i / vecs), c = (int)(i - (long long)row * vecs);
+        const uint4 *src = reinterpret_cast<const uint4 *>(r.x + row * r.ld + c * 8);
+        v[k][0] = __ldcs(src);
+        v[k][1] = __ldcs(src + 1);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const long long i = base + k * threads;
+        if (i >= total) continue;
+        const int row = (int)(i / vecs), c = (int)(i - (long long)row * vecs);
+        __nv_bfloat16 *dst = r.planes + (long long)row * r.plane_ld + c * 8;
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x[4 * j] = __uint_as_float(v[k][j].x);
+            x[4 * j + 1] = __uint_as_float(v[k][j].y);
+            x[4 * j + 2] = __uint_as_float(v[k][j].z);
+            x[4 * j + 3] = __uint_as_float(v[k][j].w);
+        }
+#pragma unroll
+        for (int t = 0; t < kMaxPieces; ++t) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = next_term(x[j]);
+            *reinterpret_cast<uint4 *>(dst + t * plane) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                           pack_bf16x2(y[6], y[7]));
+        }
+    }
+}
+
+long long split_blocks(const SplitRows &r, int threads)
+{
+    return ((long long)r.rows * (r.d / 8) + threads * 2 - 1) / (threads * 2);
+}
+
+// Two operands in one launch.
+__global__ void __launch_bounds__(256) split_f32_kernel(const SplitRows r0, const SplitRows r1, long long blocks0)
 {
     chain_wait();
     chain_go();
-    const long long total = (long long)rows * vecs;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const int r = (int)(i / vecs), c = (int)(i - (long long)r * vecs);
-    const float4 *src = reinterpret_cast<const float4 *>(x + r * ld + c * 8);
-    const float4 lo = __ldcs(src), hi = __ldcs(src + 1);
-    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int t = 0; t < kMaxPieces; ++t) {
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            __nv_bfloat16 n = __float2bfloat16_rn(v[k]);
-            if (__hisinf(n) && !isinf(v[k])) n = __float2bfloat16_rz(v[k]);
-            v[k] = isfinite(v[k]) ? v[k] - __bfloat162float(n) : 0.f;
-            const uint32_t bits = __bfloat16_as_ushort(n);
-            o[k / 2] = k & 1 ? o[k / 2] | bits << 16 : bits;
-        }
-        reinterpret_cast<uint4 *>(planes)[((long long)t * rows + r) * plane_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    if (blockIdx.x < blocks0) split_block(r0, blockIdx.x, 256);
+    else split_block(r1, blockIdx.x - blocks0, 256);
 }
 
 // One warp per row: a copy of h with zeros in rows that have no part in the gradient (whatever
@@ -631,17 +682,22 @@ __global__ void __launch_bounds__(256) split_f32_kernel(const float *x, long lon
 // operands: carried beyond fp32), not by the accumulators that cut: G's one large element is the
 // difference of 1 and that probability.
 template <bool BF16>
-__global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p)
+__global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradRowsParams p, int row_blocks)
 {
     chain_wait();
     chain_go();
+    if (!BF16 && (int)blockIdx.x >= row_blocks) {  // the table's terms, in the same launch
+        split_block(p.table, (int)blockIdx.x - row_blocks, kMergeWarps * 32);
+        return;
+    }
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (row >= p.N) return;
     constexpr int ESIZE = BF16 ? 2 : 4;
     const int vecs = p.d * ESIZE / 16;
     const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.h) + row * p.h_ld * ESIZE);
-    uint4 *dst = static_cast<uint4 *>(p.out) + (long long)row * (p.out_ld * ESIZE / 16);
+    // (fp32: as terms)
+    __nv_bfloat16 *out = p.out + (long long)row * p.out_ld;
     const long long id = p.targets ? raw_token(p.targets, p.index_bytes, row) : -1;
     // (the row does not wait for the token, the table's row does)
     uint4 h[4];
@@ -663,7 +719,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
             y[k] = target >= 0 && c0 + 32 * k < vecs ? __ldg(w + c0 + 32 * k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (c0 + 32 * k < vecs) dst[c0 + 32 * k] = live ? h[k] : make_uint4(0, 0, 0, 0);
+            const int c = c0 + 32 * k;
+            if (c < vecs) {
+                const uint4 x = live ? h[k] : make_uint4(0, 0, 0, 0);
+                if (BF16) reinterpret_cast<uint4 *>(out)[c] = x;
+                else split4(x, out + c * 4, (long long)p.N * p.out_ld);
+            }
             if (BF16) {
                 const uint32_t xp[4] = {h[k].x, h[k].y, h[k].z, h[k].w}, yp[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
@@ -697,19 +758,18 @@ cudaError_t launch_sum_parts(const PartsSum (&r)[2], cudaStream_t s)
     return launch_grid(sum_parts_kernel, dim3((unsigned)(b0 + b1)), 256, 0, s, 1, r[0], r[1], b0);
 }
 
-cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             int plane_ld, cudaStream_t s)
+cudaError_t launch_split_f32(const SplitRows &h, const SplitRows &w, cudaStream_t s)
 {
-    const long long vecs = (long long)rows * (d / 8);
-    return launch_grid(split_f32_kernel, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, 1, x, ld, rows,
-                       d / 8, planes, plane_ld / 8);
+    const long long b0 = split_blocks(h, 256), b1 = split_blocks(w, 256);
+    return launch_grid(split_f32_kernel, dim3((unsigned)(b0 + b1)), 256, 0, s, 1, h, w, b0);
 }
 
 cudaError_t launch_grad_rows(const GradRowsParams &p, bool bf16, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((p.N + kMergeWarps - 1) / kMergeWarps);
-    return launch_grid(bf16 ? grad_rows_kernel<true> : grad_rows_kernel<false>, dim3(grid), kMergeWarps * 32, 0, s, 1,
-                       p);
+    const int threads = kMergeWarps * 32, rows = (p.N + kMergeWarps - 1) / kMergeWarps;
+    if (bf16) return launch_grid(grad_rows_kernel<true>, dim3((unsigned)rows), threads, 0, s, 1, p, rows);
+    return launch_grid(grad_rows_kernel<false>, dim3((unsigned)(rows + split_blocks(p.table, threads))), threads, 0, s,
+                       1, p, rows);
 }
 
 cudaError_t launch_logprob_few_merge(const MergeParams &p, bool bf16, cudaStream_t s)

@@ -194,14 +194,22 @@ struct PartsSum {
     int parts, bf16;
 };
 cudaError_t launch_sum_parts(const PartsSum (&r)[2], cudaStream_t s);
-// fp32 rows as three bf16 terms: planes [3][rows][plane_ld].
-cudaError_t launch_split_f32(const float *x, long long ld, int rows, int d, __nv_bfloat16 *planes,
-                             int plane_ld, cudaStream_t s);
+// fp32 rows [rows] of d, ld apart, as three bf16 terms: planes [3][rows][plane_ld].
+struct SplitRows {
+    const float *x;
+    long long ld;
+    int rows, d, plane_ld;
+    __nv_bfloat16 *planes;
+};
+cudaError_t launch_split_f32(const SplitRows &h, const SplitRows &w, cudaStream_t s);
 
+// h without the rows that have no part (fp32: as terms), and the targets' log probabilities;
+// fp32: the table's terms too.
 struct GradRowsParams {
     const void *h, *w;
-    void *out;             // [N][out_ld]
+    __nv_bfloat16 *out;    // [N][out_ld], or [3][N][out_ld]
     int out_ld;
+    SplitRows table;
     float *target_logp;    // [N]
     long long h_ld, w_ld;
     int N, V, d, index_bytes;

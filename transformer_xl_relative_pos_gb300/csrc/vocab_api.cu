@@ -252,7 +252,7 @@ struct GradPlan {
     Shape g, h, w;                // tiles of G, of dh, and of a chunk's dW
     int parts_h;                  // of dh, over all chunks
     long long g_ld, g_plane;
-    size_t live, target_logp, h_planes, w_planes, g_at, part_h, part_w, total;
+    size_t live, target_logp, w_planes, g_at, part_h, part_w, total;
 };
 
 GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
@@ -277,11 +277,9 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     size_t o = 0;
     const size_t row = (size_t)line_ld(d) * 2 * txl::kMaxPieces;
     g.live = o;
-    o = up256(o + (size_t)N * line_ld(d) * elem(dtype));
+    o = up256(o + (dtype == TXL_F32 ? N * row : (size_t)N * line_ld(d) * 2));
     g.target_logp = o;
     o = up256(o + (size_t)N * 4);
-    g.h_planes = o;
-    if (dtype == TXL_F32) o = up256(o + N * row);
     g.w_planes = o;
     if (dtype == TXL_F32) o = up256(o + V * row);
     g.g_at = o;
@@ -336,6 +334,11 @@ Operand operand(const void *p, long long ld, const char *planes, int rows, int d
 {
     if (dtype == TXL_BF16) return {p, ld, 1, ld * rows};
     return {planes, line_ld(d), txl::kMaxPieces, (long long)rows * line_ld(d)};
+}
+
+txl::SplitRows split_of(const void *x, long long ld, int rows, int d, char *planes)
+{
+    return {static_cast<const float *>(x), ld, rows, d, line_ld(d), reinterpret_cast<__nv_bfloat16 *>(planes)};
 }
 
 bool map_of(CUtensorMap *map, const Operand &o, int rows, int d, unsigned box_rows)
@@ -467,14 +470,10 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     unsigned int *status = txl::device_status_word();
     if (!status) return TXL_ERR_CUDA;
 
-    if (dtype == TXL_F32) {
-        cudaError_t e = txl::launch_split_f32(static_cast<const float *>(h), h_stride, N, d,
-                                              reinterpret_cast<__nv_bfloat16 *>(ws + s.h_planes), line_ld(d), st);
-        if (e == cudaSuccess)
-            e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + s.w_planes), line_ld(d), st);
-        if (e != cudaSuccess) return TXL_ERR_CUDA;
-    }
+    if (dtype == TXL_F32 &&
+        txl::launch_split_f32(split_of(h, h_stride, N, d, ws + s.h_planes),
+                              split_of(w, w_stride, V, d, ws + s.w_planes), st) != cudaSuccess)
+        return TXL_ERR_CUDA;
     const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
     txl::GemmLaunch l{};
@@ -584,12 +583,12 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     unsigned int *status = txl::device_status_word();
     if (!status) return TXL_ERR_CUDA;
 
-    // h without the rows that have no part, and the targets' log probabilities; then both
-    // operands' bf16 terms
+    // h without the rows that have no part, and the targets' log probabilities; fp32: both
+    // operands' terms
     txl::GradRowsParams l{};
     l.h = h;
     l.w = w;
-    l.out = ws + g.live;
+    l.out = reinterpret_cast<__nv_bfloat16 *>(ws + g.live);
     l.out_ld = line_ld(d);
     l.target_logp = reinterpret_cast<float *>(ws + g.target_logp);
     l.h_ld = h_stride;
@@ -603,17 +602,10 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     l.dentropy = dentropy;
     l.scale = scale;
     l.status = status;
-    cudaError_t e = txl::launch_grad_rows(l, dtype == TXL_BF16, st);
-    if (dtype == TXL_F32) {
-        if (e == cudaSuccess)
-            e = txl::launch_split_f32(reinterpret_cast<const float *>(ws + g.live), line_ld(d), N, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.h_planes), line_ld(d), st);
-        if (e == cudaSuccess)
-            e = txl::launch_split_f32(static_cast<const float *>(w), w_stride, V, d,
-                                      reinterpret_cast<__nv_bfloat16 *>(ws + g.w_planes), line_ld(d), st);
-    }
-    if (e != cudaSuccess) return TXL_ERR_CUDA;
-    const Operand oh = operand(ws + g.live, line_ld(d), ws + g.h_planes, N, d, dtype);
+    if (dtype == TXL_F32) l.table = split_of(w, w_stride, V, d, ws + g.w_planes);
+    if (txl::launch_grad_rows(l, dtype == TXL_BF16, st) != cudaSuccess) return TXL_ERR_CUDA;
+    const int h_terms = dtype == TXL_F32 ? txl::kMaxPieces : 1;
+    const Operand oh = {ws + g.live, line_ld(d), h_terms, (long long)N * line_ld(d)};
     const Operand ow = operand(w, w_stride, ws + g.w_planes, V, d, dtype);
 
     GemmParams base{};
