@@ -53,19 +53,35 @@ __device__ __forceinline__ bool epi_any(bool x)
     return r != 0;
 }
 
-// Maximum, sum and weighted sum (log2 units, relative to the maximum) of some of a row's logits.
-struct LaneSums {
-    float m, s, es;
+// Statistics of eight states from 32 lanes' each ([maximum, sum, weighted sum][8][33] floats): lanes
+// 4 j .. 4 j + 3 join state j's.
+constexpr int kOwn = 3 * 8 * 33;
+static_assert(kEpiWarps * kOwn <= 64 * TURN_LD, "the warps' parts of the turning buffer");
 
-    __device__ __forceinline__ LaneSums with(const LaneSums &o) const
-    {
-        const float top = fmaxf(m, o.m), mu = top == -INFINITY ? 0.f : top;
-        const float d0 = m - mu, d1 = o.m - mu, f0 = ex2(d0), f1 = ex2(d1);
-        // (sums of zero stay so: not zero times infinity)
-        const float e0 = s == 0.f ? 0.f : (es + s * d0) * f0, e1 = o.s == 0.f ? 0.f : (o.es + o.s * d1) * f1;
-        return {top, fmaf(s, f0, o.s * f1), e0 + e1};
+__device__ __noinline__ float4 join_lanes(const float *own, int lane)
+{
+    constexpr unsigned FULL = 0xffffffffu;
+    const float *m = own + (lane >> 2) * 33 + (lane & 3) * 8, *s = m + 8 * 33, *es = s + 8 * 33;
+    float top = m[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, m[i]);
+    top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+    const float mu = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, weighted = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+        // (before its first number a lane's maximum is -infinity and its sums are zero)
+        const float d = fmaxf(m[i] - mu, -1e30f), f = ex2(d);
+        sum = fmaf(s[i], f, sum);
+        weighted = fmaf(fmaf(s[i], d, es[i]), f, weighted);
     }
-};
+    sum += __shfl_xor_sync(FULL, sum, 1);
+    weighted += __shfl_xor_sync(FULL, weighted, 1);
+    sum += __shfl_xor_sync(FULL, sum, 2);
+    weighted += __shfl_xor_sync(FULL, weighted, 2);
+    return make_float4(top, sum, weighted, 0.f);
+}
 
 template <int GROUPS>
 __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
@@ -214,6 +230,7 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
             }
             tc_fence_after_sync();
             const int id0 = t * BM + lane * 4, left = p.N - id0;  // (p.N: the vocabulary)
+            const bool whole = (t + 1) * BM <= p.N;
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
                 const int c = g * 64 + half * 32;
@@ -237,13 +254,16 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                     const float4 z = *reinterpret_cast<const float4 *>(turn + (we * 8 + j) * TURN_LD + lane * 4);
                     float v[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = i < left ? fmaf(v[i], c2, 0.f) : -INFINITY;
+                    for (int i = 0; i < 4; ++i) v[i] = fmaf(v[i], c2, 0.f);  // (+ 0: zeros of one sign)
+                    if (!whole)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = i < left ? v[i] : -INFINITY;
                     const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                     const float m_new = fmaxf(m[k], top);
                     const float mu = m_new == -INFINITY ? 0.f : m_new;
-                    const float diff = m[k] - mu, f = ex2(diff);  // (-inf before the first number)
-                    // (sums of zero stay so: not zero times infinity)
-                    float s_new = sum[k] * f, e_new = sum[k] == 0.f ? 0.f : (es[k] + sum[k] * diff) * f;
+                    // (before the first number the maximum is -infinity and the sums are zero)
+                    const float diff = fmaxf(m[k] - mu, -1e30f), f = ex2(diff);
+                    float s_new = sum[k] * f, e_new = fmaf(sum[k], diff, es[k]) * f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float d = v[i] - mu, e = ex2(d);
@@ -259,12 +279,9 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                             make_float4(left > 0 ? v[0] : none, left > 1 ? v[1] : none, left > 2 ? v[2] : none,
                                         left > 3 ? v[3] : none);
                     }
-                    if (p.group_key) {
-                        // the largest of the lane's four: NaN has no place in the order
-                        const bool any = (v[0] == v[0] && left > 0) || (v[1] == v[1] && left > 1) ||
-                                         (v[2] == v[2] && left > 2) || (v[3] == v[3] && left > 3);
-                        p.group_key[((long long)st * p.nb + t) * 32 + lane] = any ? order_key(top) : 0u;
-                    }
+                    // the largest of the lane's four: NaN has no place in the order, nor has a lane behind V
+                    if (p.group_key)
+                        p.group_key[((long long)st * p.nb + t) * 32 + lane] = top == top && left > 0 ? order_key(top) : 0u;
                     const int at = targets[st] - id0;
                     if ((unsigned)at < 4u)
                         p.target_z[st] = at & 2 ? (at & 1 ? v[3] : v[2]) : (at & 1 ? v[1] : v[0]);
@@ -277,33 +294,23 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
             *abort_flag = 1;
         }
         if (ok) {
-            // over the lanes: of eight states each half of the lanes keeps four, then two, then one
-            // (nine exchanges of three values instead of forty)
+            // over the lanes, through the warp's part of the turning buffer, four lanes a state (in one
+            // copy of the code: a kernel's cold instructions cost more here than the arithmetic)
+            float *own = turn + we * kOwn;
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
                 if (g * 64 >= p.M) break;
-                LaneSums a[8];
+                __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] = {m[g * 8 + j], sum[g * 8 + j], es[g * 8 + j]};
-#pragma unroll
-                for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
-                    const bool upper = lane & o;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= n) break;
-                        const LaneSums send = upper ? a[j] : a[j + n], keep = upper ? a[j + n] : a[j];
-                        a[j] = keep.with({__shfl_xor_sync(FULL, send.m, o), __shfl_xor_sync(FULL, send.s, o),
-                                          __shfl_xor_sync(FULL, send.es, o)});
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    own[j * 33 + lane] = m[g * 8 + j];
+                    own[(8 + j) * 33 + lane] = sum[g * 8 + j];
+                    own[(16 + j) * 33 + lane] = es[g * 8 + j];
                 }
-#pragma unroll
-                for (int o = 2; o > 0; o >>= 1)
-                    a[0] = a[0].with({__shfl_xor_sync(FULL, a[0].m, o), __shfl_xor_sync(FULL, a[0].s, o),
-                                      __shfl_xor_sync(FULL, a[0].es, o)});
-                // (lane bits 4, 3, 2 chose the state's bits 2, 1, 0)
+                __syncwarp();
                 const int st = g * 64 + we * 8 + (lane >> 2);
-                if ((lane & 3) == 0 && st < p.M)
-                    p.stats[(long long)blockIdx.x * p.M + st] = make_float4(a[0].m, a[0].s, a[0].es, 0.f);
+                const float4 r = join_lanes(own, lane);
+                if ((lane & 3) == 0 && st < p.M) p.stats[(long long)blockIdx.x * p.M + st] = r;
             }
         }
         tc_fence_before_sync();
