@@ -348,25 +348,23 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
                 k[u] = i < n ? src[i] : make_uint4(0, 0, 0, 0);
             }
         };
-        auto scan = [&](auto take) {
+        // (the code below is run once by a block: it is kept short, a cold instruction costs more
+        // than its work)
+        const unsigned *one = reinterpret_cast<const unsigned *>(src);
+        auto scan = [&](auto take) {   // take(mask of a thread's 16 maxima, place of the first)
             for (int i0 = tid; i0 < n; i0 += kFewThreads * kFewLoads) {
-                uint4 more[kFewLoads];
-                const bool first = i0 == tid;
-                if (!first) load(more, i0);
-#pragma unroll
-                for (int u = 0; u < kFewLoads; ++u) {
-                    const uint4 k = first ? held[u] : more[u];
-                    const int i = (i0 + u * kFewThreads) * 4;
-                    take(k.x, i);
-                    take(k.y, i + 1);
-                    take(k.z, i + 2);
-                    take(k.w, i + 3);
-                }
+                if (i0 > tid) load(held, i0);
+                take(i0);
             }
+            if (n > kFewThreads * kFewLoads) load(held, tid);
         };
         load(held, tid);
         unsigned mine = 0;
-        scan([&](unsigned k, int) { mine = max(mine, k); });
+        scan([&](int) {
+#pragma unroll
+            for (int u = 0; u < kFewLoads; ++u)
+                mine = max(mine, max(max(held[u].x, held[u].y), max(held[u].z, held[u].w)));
+        });
         const unsigned most = __reduce_max_sync(ALL, mine);
         if (lane == 0) s_best_key[warp] = most;
         if (tid == 0) s_count = 0;
@@ -386,12 +384,18 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
         __syncthreads();
         const unsigned thr = s_thr;
         if (mine >= thr)
-            scan([&](unsigned k, int at_group) {
-                if (k >= thr) {
+            scan([&](int i0) {
+                unsigned hits = 0;
+#pragma unroll
+                for (int u = 0; u < kFewLoads; ++u)
+                    hits |= ((held[u].x >= thr) | (held[u].y >= thr) << 1 | (held[u].z >= thr) << 2 |
+                             (held[u].w >= thr) << 3) << (4 * u);
+                for (; hits; hits &= hits - 1) {
+                    const int bit = __ffs(hits) - 1, place = (i0 + (bit >> 2) * kFewThreads) * 4 + (bit & 3);
                     const int at = atomicAdd(&s_count, 1);
                     if (at < kFewCap) {
-                        s_key[at] = k;
-                        s_at[at] = at_group;
+                        s_key[at] = one[place];
+                        s_at[at] = place;
                     }
                 }
             });
@@ -418,14 +422,14 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
             for (int c = 0; c < want; ++c) {
                 unsigned bk = 0;
                 int ba = 0x7fffffff;
-                scan([&](unsigned k, int i) {
-                    if (!k) return;
-                    const bool left = k < last_key || (k == last_key && i > last_at);
-                    if (left && (k > bk || (k == bk && i < ba))) {
+                for (int i = tid; i < n * 4; i += kFewThreads) {
+                    const unsigned k = one[i];
+                    const bool left = k && (k < last_key || (k == last_key && i > last_at));
+                    if (left && k > bk) {
                         bk = k;
                         ba = i;
                     }
-                });
+                }
                 unsigned top = __reduce_max_sync(ALL, bk);
                 int at = (int)__reduce_min_sync(ALL, bk == top ? (unsigned)ba : 0x7fffffffu);
                 __syncthreads();
