@@ -649,8 +649,8 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
  *   them may be NULL.  Written, not accumulated.
  * A row without a target and with dentropy 0 (or NULL) has no part, whatever its h and
  * statistics hold: its dh is zero.
- * G enters its products with w, and with h for a bf16 dw, rounded to bf16; with h for an fp32 dw
- * of bf16 operands as a bf16 pair (value and residual), and for fp32 operands as three terms.
+ * G enters its products rounded to bf16; as a bf16 pair (value and residual) with h for an fp32
+ * dw of bf16 operands, and in both products for N <= 128; and for fp32 operands as three terms.
  * Sums are fp32 in a fixed order: results repeat bit for bit.
  *   workspace: txl_logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype) bytes (G in chunks
  *   of the vocabulary, up to about 1 GiB, and partial sums).

@@ -244,11 +244,12 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     return s;
 }
 
+constexpr int kPairRows = 128;
 constexpr size_t kGradBytes = (size_t)1 << 30;  // of G in the workspace: vocabulary chunks beyond
 
 struct GradPlan {
     int chunk, chunks;            // vocabulary rows at a time
-    int pieces;                   // terms of G
+    int pieces, pieces_h;         // terms of G, and those that dh takes
     Shape g, h, w;                // tiles of G, of dh, and of a chunk's dW
     int parts_h;                  // of dh, over all chunks
     long long g_ld, g_plane;
@@ -258,7 +259,13 @@ struct GradPlan {
 GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
 {
     GradPlan g{};
-    g.pieces = dtype == TXL_F32 ? 3 : grad_dtype == TXL_F32 ? 2 : 1;
+    // Terms of G.  One bf16 value for bf16 gradients: its rounding is as large as the result's own, and
+    // averages over the rows.  Few rows do not average, and their products are bound by the table's
+    // bytes: up to 128 rows (about where two terms' MMAs take as long as reading and writing the
+    // table) G is a pair.
+    const bool few = N <= kPairRows;
+    g.pieces_h = dtype == TXL_F32 ? 3 : few ? 2 : 1;
+    g.pieces = dtype == TXL_F32 ? 3 : few || grad_dtype == TXL_F32 ? 2 : 1;
     const long long most = (long long)(kGradBytes / ((size_t)g.pieces * 2 * std::max(N, 1)));
     g.chunk = V;
     if (V > std::max(64LL, most)) g.chunk = (int)std::max(64LL, most / 64 * 64);
@@ -267,10 +274,11 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     g.chunks = ceil_div(V, g.chunk);
     g.g_ld = up128(g.chunk);
     g.g_plane = g.g_ld * N;
-    const int terms = dtype == TXL_F32 ? 6 : 1, terms_w = dtype == TXL_F32 ? 6 : g.pieces;
+    const int terms = dtype == TXL_F32 ? 6 : 1, terms_h = dtype == TXL_F32 ? 6 : g.pieces_h,
+              terms_w = dtype == TXL_F32 ? 6 : g.pieces;
     g.g = choose_shape(N, g.chunk, ceil_div(d, 64) * terms, 0);
     const int kb_h = ceil_div(g.chunk, 64), kb_w = ceil_div(N, 64);
-    const Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h * terms, kb_w * terms_w}, {kb_h, kb_w});
+    const Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h * terms_h, kb_w * terms_w}, {kb_h, kb_w});
     g.h = two.a;
     g.w = two.b;
     g.parts_h = g.chunks * g.h.parts;
@@ -662,7 +670,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.b_row0 = v0;
             q.part = g.parts_h > 1;
             q.out_bf16 = dtype == TXL_BF16;
-            set_pairs(q, dtype == TXL_F32 ? g.pieces : 1, ow.planes);
+            set_pairs(q, g.pieces_h, ow.planes);
             if (!map_out(&prod.maps[0].out, q,
                          q.part ? ws + g.part_h + (size_t)c * g.h.parts * N * d * 4 : (char *)dh))
                 return TXL_ERR_CUDA;
