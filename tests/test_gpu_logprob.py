@@ -45,15 +45,21 @@ def _check_fwd(res, ref, top):
     if ref.t is not None:
         _close(res.logp, ref.logp, ref.logp_off, "logp")
     if top:
-        assert torch.equal(res.top_ids.cpu().long().reshape(ref.top_ids.shape), ref.top_ids)
-        _close(res.top_logp, ref.top_logp, ref.logp_off[:, None], "top_logp")
+        ids, logp = (x.cpu().reshape(-1, top) for x in (res.top_ids.long(), res.top_logp))
+        some = ref.top_ids.shape[1]    # (a vocabulary may have fewer)
+        assert torch.equal(ids[:, :some], ref.top_ids) and bool((ids[:, some:] == -1).all())
+        _close(logp[:, :some], ref.top_logp, ref.logp_off[:, None], "top_logp")
+        assert bool(logp[:, some:].isnan().all())
 
 
 # (rows, vocabulary, width, alternatives, scale): one row; less than a tile of rows and columns;
 # ends inside tiles, 32-column groups and 64-wide steps; several row tiles; as many
 # alternatives as the vocabulary has
 FWD = [(1, 1, 8, 1, 1.0), (1, 5000, 512, 8, 1.0), (3, 16, 24, 16, -0.7), (17, 204, 512, 5, 1.0),
-       (130, 333, 72, 3, 0.5), (129, 2049, 200, 16, 1.3), (300, 1000, 64, 0, 1.0), (64, 9001, 128, 9, 1.0)]
+       (130, 333, 72, 3, 0.5), (129, 2049, 200, 16, 1.3), (256, 700, 64, 2, 1.0), (64, 9001, 128, 9, 1.0),
+       # more than 256 rows: the rows in the tiles' rows
+       (300, 1000, 64, 0, 1.0), (300, 333, 72, 3, -0.5), (257, 5, 16, 16, 1.0), (700, 2049, 200, 16, 1.3),
+       (515, 9001, 128, 9, 1.0), (1000, 130, 520, 8, 0.0), (400, 40000, 24, 1, 1.0)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -68,10 +74,11 @@ def test_logprob_fwd(N, V, d, top, scale, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_logprob_ties_go_to_the_lowest_index(dtype):
+@pytest.mark.parametrize("N", [40, 300])
+def test_logprob_ties_go_to_the_lowest_index(N, dtype):
     # small whole numbers: every product and sum is exact, and many logits are equal
     g = torch.Generator().manual_seed(3)
-    h = torch.randint(-2, 3, (40, 16), generator=g).to(dtype)
+    h = torch.randint(-2, 3, (N, 16), generator=g).to(dtype)
     w = torch.randint(-1, 2, (700, 16), generator=g).to(dtype)
     h[7] = 0      # every logit equal
     res = txl.logprob_fwd(h.to(dev()), w.to(dev()), top=16)
@@ -83,10 +90,11 @@ def test_logprob_ties_go_to_the_lowest_index(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_logprob_order_beyond_single_precision(dtype):
+@pytest.mark.parametrize("N", [2, 300])
+def test_logprob_order_beyond_single_precision(N, dtype):
     # six logits that are all 2^24 in fp32 sums, told apart by the exact ones; two are equal
     d, V = 64, 600
-    h = torch.zeros(2, d, dtype=dtype)
+    h = torch.zeros(N, d, dtype=dtype)
     h[:, 0], h[:, 1] = 4096.0, 1.0
     w = torch.zeros(V, d, dtype=dtype)
     best = torch.tensor([5, 590, 17, 256, 300, 31])
@@ -94,11 +102,12 @@ def test_logprob_order_beyond_single_precision(dtype):
     w[best, 1] = torch.tensor([1.0, 4.0, 2.0, 4.0, 7.0, 3.0]).to(dtype) * 0.03125
     res = txl.logprob_fwd(h.to(dev()), w.to(dev()), top=6)
     _ok()
-    assert res.top_ids.tolist() == [[300, 256, 590, 31, 17, 5]] * 2
+    assert res.top_ids.tolist() == [[300, 256, 590, 31, 17, 5]] * N
     assert torch.equal(res.top_ids.cpu().long(), model.LogProb(h, w, None, 1.0, 6).top_ids)
 
 
-def test_logprob_infinite_logits():
+@pytest.mark.parametrize("repeat", [1, 60])
+def test_logprob_infinite_logits(repeat):
     d, V = 64, 300
     g = torch.Generator().manual_seed(4)
     h = torch.randn(5, d, generator=g).to(BF)
@@ -109,8 +118,13 @@ def test_logprob_infinite_logits():
     h[3, 0] = -1.0                      # ... and makes this row's logits +inf
     h[4] = float("nan")
     t = torch.tensor([1, 3, -1, 4, 5])
-    res = txl.logprob_fwd(h.to(dev()), w.to(dev()), t.to(dev()), top=5)
+    # (300 rows: the kernel of many)
+    res = txl.logprob_fwd(h.repeat(repeat, 1).to(dev()), w.to(dev()), t.repeat(repeat).to(dev()), top=5)
     _ok()
+    res = txl.LogProbs(*(x.view(repeat, 5, *x.shape[1:]) for x in res))
+    same = lambda x: all(torch.equal(x[0].nan_to_num(7, 8, 9), y.nan_to_num(7, 8, 9)) for y in x)
+    assert all(same(x) for x in res)
+    res = txl.LogProbs(*(x[0] for x in res))
     keep = torch.ones(V, dtype=torch.bool)
     keep[::3] = False
     ref = model.LogProb(h[:3], w[keep], None, 1.0, 5)
@@ -124,16 +138,17 @@ def test_logprob_infinite_logits():
     assert res.top_ids[4].tolist() == [-1] * 5
 
 
-def test_logprob_fewer_numbers_than_places_and_all_minus_infinity():
-    h = torch.ones(2, 8, dtype=BF)
+@pytest.mark.parametrize("N", [2, 300])
+def test_logprob_fewer_numbers_than_places_and_all_minus_infinity(N):
+    h = torch.ones(N, 8, dtype=BF)
     w = torch.zeros(3, 8, dtype=BF)
     w[1] = float("nan")
     res = txl.logprob_fwd(h.to(dev()), w.to(dev()), top=4)
     assert res.top_ids[0].tolist() == [0, 2, -1, -1] and bool(res.lse.isnan().all())
     w = torch.full((3, 8), float("-inf"), dtype=BF)
-    res = txl.logprob_fwd(h.to(dev()), w.to(dev()), torch.zeros(2, dtype=torch.int64, device=dev()), top=3)
+    res = txl.logprob_fwd(h.to(dev()), w.to(dev()), torch.zeros(N, dtype=torch.int64, device=dev()), top=3)
     _ok()
-    assert res.lse.tolist() == [-math.inf] * 2 and bool(res.logp.isnan().all())
+    assert res.lse.tolist() == [-math.inf] * N and bool(res.logp.isnan().all())
     assert res.top_ids[1].tolist() == [0, 1, 2]
 
 

@@ -104,7 +104,7 @@ constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCluster = 8, kSortWide = 16;  // blocks; more than 8 need the device's consent
 constexpr int kHeld = 8;                // rows of 32 positions a warp holds in registers
-constexpr int kDigit = 9;
+constexpr int kDigit = 9;                // bits of a pass, at most
 constexpr int kBins = 1 << kDigit;      // one bin a thread
 static_assert(kBins == kSortThreads, "a thread keeps one bin");
 
@@ -114,7 +114,7 @@ struct SortParams {
     int *crossing;           // counter of the runs that cross chunks, zeroed here
     uint4 *zero;             // the gradient, zeroed by the blocks that do not sort (null: left alone)
     long long zero_vecs;
-    int index_bytes, n, V, passes, per_warp, blocks;
+    int index_bytes, n, V, passes, digit, per_warp, blocks;  // digit: bits of a pass
     unsigned int *status;
 };
 
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
     }
     if (block == 0 && tid == 0) *p.crossing = 0;
     for (int pass = 0; pass < p.passes; ++pass) {
-        const int shift = pass * kDigit;
+        const int shift = pass * p.digit, mask = (1 << p.digit) - 1;
         const bool last = pass + 1 == p.passes;
         const int2 *in = p.pair[pass & 1];
         int2 *out = p.pair[(pass & 1) ^ 1];
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
             if (i0 > lo) load(i0);
 #pragma unroll
             for (int k = 0; k < kHeld; ++k)
-                if (key[k] >= 0) atomicAdd(&place[warp][(key[k] >> shift) & (kBins - 1)], 1);
+                if (key[k] >= 0) atomicAdd(&place[warp][(key[k] >> shift) & mask], 1);
         }
         __syncthreads();
         // thread = bin: the warps' counts to starts within the block
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
         int all = 0, before = 0;
 #pragma unroll
         for (int b = 0; b < kSortWide; ++b) {
-            const int c = b < p.blocks ? cluster_word(total + tid, b) : 0;
+            const int c = b < p.blocks && tid <= mask ? cluster_word(total + tid, b) : 0;
             all += c;
             before += b < block ? c : 0;
         }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p)
             for (int k = 0; k < kHeld; ++k) {
                 if (i0 + k * 32 >= hi) break;
                 const bool on = key[k] >= 0;
-                const int digit = on ? (key[k] >> shift) & (kBins - 1) : kBins + lane;
+                const int digit = on ? (key[k] >> shift) & mask : kBins + lane;
                 const unsigned same = __match_any_sync(0xffffffffu, digit);
                 const int rank = __popc(same & ((1u << lane) - 1));
                 int to = 0;
@@ -639,6 +639,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams &p, bool bf16, bool grad_bf16,
     int bits = 1;
     while (((long long)p.V >> bits) != 0) ++bits;  // (the key V stands for no token)
     q.passes = (bits + kDigit - 1) / kDigit;
+    q.digit = (bits + q.passes - 1) / q.passes;
     const bool few = p.n <= kRankMost;
     const int threads = few ? kRankThreads : kSortThreads;
     q.blocks = few ? (p.n + 31) / 32 : p.n <= 16384 || !wide_clusters() ? kSortCluster : kSortWide;

@@ -27,28 +27,25 @@ using namespace ptx;
 
 constexpr int BM = 128, BK = 64, MAX_BN = 256;
 constexpr int A_BYTES = BM * BK * 2;
-constexpr int RING = 192 * 1024;
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
 constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
 constexpr int OUT_BYTES = BM * 128;
 constexpr int kEpiWarps = 8;                      // two halves of a tile's columns, four warps each
 constexpr int kThreads = (4 + kEpiWarps) * 32;
 
-// A block alone multiplies 128 x bn tiles; a pair of blocks 256 x bn, each holding half of
-// B's columns, so that a block reads a third less from L2 for the same work (ring stages of 32
-// instead of 48 KB, six instead of four).
-template <bool PAIR>
-struct Ring {
-    static constexpr int B_BYTES = MAX_BN * BK * 2 / (PAIR ? 2 : 1);
-    static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int NS = RING / STAGE;
-    static constexpr int OFF_OUT = NS * STAGE;    // a tile of 128 rows x 128 bytes per half
-    static constexpr int OFF_BAR = OFF_OUT + 2 * OUT_BYTES;
-    static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 4) * 8;
-    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
-    static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
-};
+// A pair of blocks multiplies 256 x bn tiles, each block holding half of A's rows and of B's
+// columns (a block alone with 128 x bn tiles reads half as much again from L2 for the same work: the
+// statistics of 2048 x 131072 306 us, with pairs 287).
+constexpr int B_BYTES = MAX_BN / 2 * BK * 2;
+constexpr int STAGE = A_BYTES + B_BYTES;
+constexpr int NS = 192 * 1024 / STAGE;
+constexpr int OFF_OUT = NS * STAGE;               // a tile of 128 rows x 128 bytes per half
+constexpr int OFF_BAR = OFF_OUT + 2 * OUT_BYTES;
+constexpr int OFF_MISC = OFF_BAR + (2 * NS + 4) * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
+
+static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 
 enum Mode { kStats, kGrad, kProducts };
 
@@ -205,7 +202,7 @@ __device__ __forceinline__ bool half_any(int half, bool x)
     return r != 0;
 }
 
-template <Mode MODE, int LIST, bool PAIR>
+template <Mode MODE, int LIST>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ GemmLaunch g)
 {
@@ -213,22 +210,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool B_MN = MODE == kProducts;
     const int n_items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
     unsigned int *status = g.p[0].status;
-    using R = Ring<PAIR>;
-    constexpr int NS = R::NS, STAGE = R::STAGE, BLOCKS = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / BLOCKS, units = gridDim.x / BLOCKS;  // block or pair
+    const int rank = (int)cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
-    // full (counted on block 0 of a pair), empty, accumulators full and empty (block 0)
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::OFF_BAR);
+    // full (counted on block 0), empty, accumulators full and empty (block 0)
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
     uint64_t *empty = full + NS;
     uint64_t *acc_full = empty + NS;
     uint64_t *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + R::OFF_MISC);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + R::OFF_MISC + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(full + s, 1);
@@ -236,23 +231,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + s, 1);
-            mbar_init(acc_empty + s, kEpiWarps * BLOCKS);  // (the epilogue's warps)
+            mbar_init(acc_empty + s, kEpiWarps * 2);  // (the epilogue's warps)
         }
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 2) {
-        if (PAIR) {
-            tmem_alloc_pair(tmem_slot, TM_COLS);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(tmem_slot, TM_COLS);
-            tmem_relinquish();
-        }
+        tmem_alloc_pair(tmem_slot, TM_COLS);
+        tmem_relinquish_pair();
         tc_fence_before_sync();
     }
     __syncthreads();
-    if (PAIR) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint64_t wait_ns = g.p[0].wait_ns;
@@ -262,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ===================== TMA producer =====================================
         if (lane == 0) {
-            const uint32_t full0 = PAIR ? cluster_addr(full, 0) : 0u;
+            const uint32_t full0 = cluster_addr(full, 0);
             for (int i = 0; i < (MODE == kProducts ? 2 : 1); ++i) {
                 prefetch_tensormap(&g.maps[i].a);
                 prefetch_tensormap(&g.maps[i].b);
@@ -270,21 +260,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             int it = 0, s = 0;  // stages filled; the next one
             uint32_t phase = 1;
-            for (int item = unit; item < n_items && ok; item += units) {
+            for (int item = pair; item < n_items && ok; item += pairs) {
                 const Item<MODE> i(g, item);
                 const GemmParams &p = g.p[i.side];
                 // (in registers: the loop below issues a step's copies in a few hundred cycles, and reads
                 // of parameters would be repeated after every one)
                 const CUtensorMap *tm_a = &g.maps[i.side].a, *tm_b = &g.maps[i.side].b;
-                const int bn = p.bn, own_bn = bn / BLOCKS;  // columns of B in this block
+                const int bn = p.bn, own_bn = bn / 2;  // columns of B in this block
                 const int b_row0 = p.b_row0, n_pairs = p.n_pairs;
                 const unsigned pair_a = p.pair_a, pair_b = p.pair_b;
-                const uint32_t stage_tx = (uint32_t)(A_BYTES + own_bn * BK * 2) * BLOCKS;
+                const uint32_t stage_tx = (uint32_t)(A_BYTES + own_bn * BK * 2) * 2;
                 const bool a_mn = MODE == kProducts && i.side;
                 const int nt = i.tiles(p);
                 for (int t = 0; t < nt && ok; ++t) {
                     const Tile w = i.tile(p, t);
-                    const int m0 = (w.m * BLOCKS + rank) * BM, n0 = w.n * bn + rank * own_bn;
+                    const int m0 = (w.m * 2 + rank) * BM, n0 = w.n * bn + rank * own_bn;
                     for (int pr = 0; pr < n_pairs && ok; ++pr) {
                         const int pa = (pair_a >> (4 * pr)) & 15, pb = (pair_b >> (4 * pr)) & 15;
                         for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
@@ -292,24 +282,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint8_t *st = smem + s * STAGE;
                             if (rank == 0) mbar_arrive_expect_tx(full + s, stage_tx);
                             const uint32_t bar = full0 + s * 8;
-                            auto load = [&](uint8_t *dst, const CUtensorMap *map, int c0, int c1, int c2) {
-                                if (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
-                                else tma_load_3d(dst, map, full + s, c0, c1, c2);
-                            };
                             if (a_mn) {
 #pragma unroll
                                 for (int x = 0; x < BM / 64; ++x)
-                                    load(st + x * SLAB, tm_a, m0 + x * 64, kb * BK, pa);
+                                    tma_load_3d_pair(st + x * SLAB, tm_a, bar, m0 + x * 64, kb * BK, pa);
                             } else {
-                                load(st, tm_a, kb * BK, m0, pa);
+                                tma_load_3d_pair(st, tm_a, bar, kb * BK, m0, pa);
                             }
                             if (B_MN) {
 #pragma unroll
-                                for (int x = 0; x < MAX_BN / BLOCKS / 64; ++x)
+                                for (int x = 0; x < MAX_BN / 2 / 64; ++x)
                                     if (x * 64 < own_bn)
-                                        load(st + A_BYTES + x * SLAB, tm_b, n0 + x * 64, b_row0 + kb * BK, pb);
+                                        tma_load_3d_pair(st + A_BYTES + x * SLAB, tm_b, bar, n0 + x * 64, b_row0 + kb * BK, pb);
                             } else {
-                                load(st + A_BYTES, tm_b, kb * BK, b_row0 + n0, pb);
+                                tma_load_3d_pair(st + A_BYTES, tm_b, bar, kb * BK, b_row0 + n0, pb);
                             }
                             ++it;
                             if (++s == NS) {
@@ -337,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // ===================== MMA issuer (block 0 of a pair) ====================
+        // ===================== MMA issuer (block 0) ==============================
         const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + A_BYTES);
         const uint64_t dB = B_MN ? sdesc_sw128_mn(b0, SLAB) : sdesc_sw128(b0);
         constexpr int STEP_B = B_MN ? 16 * 128 / 16 : 2;
@@ -347,18 +333,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : "=r"(el));
             return el != 0;
         };
-        auto commit = [&](uint64_t *bar) {
-            if (PAIR) mma_commit_pair(bar);
-            else mma_commit(bar);
-        };
         bool ok = true;
         int s = 0, tile = 0;
         uint32_t phase = 0;
-        for (int item = unit; item < n_items && ok && rank == 0; item += units) {
+        for (int item = pair; item < n_items && ok && rank == 0; item += pairs) {
             const Item<MODE> i(g, item);
             const GemmParams &p = g.p[i.side];
             const bool a_mn = MODE == kProducts && i.side;
-            const uint32_t ID = idesc_bf16_f32(BM * BLOCKS, p.bn, B_MN) | (a_mn ? 1u << 15 : 0u);
+            const uint32_t ID = idesc_bf16_f32(2 * BM, p.bn, B_MN) | (a_mn ? 1u << 15 : 0u);
             const uint64_t dA = a_mn ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
             const int step_a = a_mn ? 16 * 128 / 16 : 2;
             const int nt = i.tiles(p);
@@ -378,12 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect()) {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk) {
-                            const uint64_t a = dA + off + kk * step_a, b = dB + off + kk * STEP_B;
-                            const uint32_t more = k > 0 || kk > 0 ? 1u : 0u;
-                            if (PAIR) mma_bf16_ss_pair(acc, a, b, ID, more);
-                            else mma_bf16_ss(acc, a, b, ID, more);
+                            mma_bf16_ss_pair(acc, dA + off + kk * step_a, dB + off + kk * STEP_B, ID,
+                                             k > 0 || kk > 0 ? 1u : 0u);
                         }
-                        commit(empty + s);
+                        mma_commit_pair(empty + s);
                     }
                     __syncwarp();
                     if (++s == NS) {
@@ -392,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                if (elect()) commit(acc_full + buf);
+                if (elect()) mma_commit_pair(acc_full + buf);
                 __syncwarp();
                 ++tile;
             }
@@ -403,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 atomicOr(status, TXL_STATUS_TIMEOUT);
                 *abort_flag = 1;
             }
-            if (elect()) commit(acc_full + (tile & 1));
+            if (elect()) mma_commit_pair(acc_full + (tile & 1));
             __syncwarp();
             const int zero = 0;
             mbar_wait(acc_full + (tile & 1), (tile >> 1) & 1, &zero, wait_ns);
@@ -413,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp & 3, half = (warp - 4) >> 2;
         const int row = wq * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
-        uint8_t *out = smem + R::OFF_OUT + half * OUT_BYTES;
+        uint8_t *out = smem + OFF_OUT + half * OUT_BYTES;
         const bool issuer = wq == 0 && lane == 0;  // of the half's stores
         constexpr float kLog2e = 1.4426950408889634f;
         const float zscale = g.p[0].scale * uncut_scale(g.p[0].kb * (BK / 16)), c2 = zscale * kLog2e;
@@ -439,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true;
         int tile = 0;
-        for (int item = unit; item < n_items && ok; item += units) {
+        for (int item = pair; item < n_items && ok; item += pairs) {
             const Item<MODE> it(g, item);
             const GemmParams &p = g.p[it.side];
             tm_out = &g.maps[it.side].out;
@@ -448,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int target = -1;
             float g1 = 0.f, ge = 0.f, lse = 0.f, ent = 0.f, lpt = 0.f;
             if (MODE == kStats || MODE == kGrad) {
-                const int m = (it.tile(p, 0).m * BLOCKS + rank) * BM + row;
+                const int m = (it.tile(p, 0).m * 2 + rank) * BM + row;
                 if (m < p.M && p.targets) target = token_at(p.targets, p.index_bytes, m, p.V, p.status);
                 // (rows without a part: zeros all through, their states have been cleared)
                 if (MODE == kGrad && m < p.M && (target >= 0 || (p.dentropy && p.dentropy[m] != 0.f))) {
@@ -474,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (MODE != kStats) ok = !half_any(half, !ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const int m0 = (w.m * BLOCKS + rank) * BM, n0 = w.n * p.bn;
+                const int m0 = (w.m * 2 + rank) * BM, n0 = w.n * p.bn;
                 // (a block whose rows lie behind the last has nothing to write)
                 const int c_lo = half * (p.bn / 2), c_hi = m0 < p.M ? min((half + 1) * (p.bn / 2), p.N - n0) : 0;
                 const bool empty_part = w.kb_lo == w.kb_hi;  // (nothing was accumulated)
@@ -568,13 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(cluster_addr(acc_empty + buf, 0));
-                    else mbar_arrive(acc_empty + buf);
-                }
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_empty + buf, 0));
             }
             if (MODE == kStats && ok) {
-                const int s = it.at / p.mb, m = ((it.at - s * p.mb) * BLOCKS + rank) * BM + row;
+                const int s = it.at / p.mb, m = ((it.at - s * p.mb) * 2 + rank) * BM + row;
                 if (m < p.M) {
                     const long long part = 2 * s + half;
                     p.stats[part * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
@@ -596,37 +573,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     __syncthreads();
-    if (PAIR) cluster_sync_all();
+    cluster_sync_all();
     if (warp == 2) {
         tc_fence_after_sync();
-        if (PAIR) tmem_dealloc_pair(tmem, TM_COLS);
-        else tmem_dealloc(tmem, TM_COLS);
+        tmem_dealloc_pair(tmem, TM_COLS);
     }
-}
-
-template <Mode MODE, int LIST, bool PAIR>
-cudaError_t launch_units(const GemmLaunch &g, cudaStream_t s)
-{
-    static bool attr_set[64] = {};  // the attribute is set once per device
-    constexpr int BLOCKS = PAIR ? 2 : 1, SMEM = Ring<PAIR>::SMEM_BYTES;
-    auto *kernel = vocab_gemm_kernel<MODE, LIST, PAIR>;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_set[dev] = true;
-    }
-    const int items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
-    const unsigned grid = (unsigned)(min(items, device_sm_count() / BLOCKS) * BLOCKS);
-    return launch_grid(kernel, dim3(grid), kThreads, SMEM, s, BLOCKS, g);
 }
 
 template <Mode MODE, int LIST>
 cudaError_t launch_gemm(const GemmLaunch &g, cudaStream_t s)
 {
-    return g.pair ? launch_units<MODE, LIST, true>(g, s) : launch_units<MODE, LIST, false>(g, s);
+    static bool attr_set[64] = {};  // the attribute is set once per device
+    auto *kernel = vocab_gemm_kernel<MODE, LIST>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const int items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
+    const unsigned grid = (unsigned)(min(items, device_sm_count() / 2) * 2);
+    return launch_grid(kernel, dim3(grid), kThreads, SMEM_BYTES, s, 2, g);
 }
 
 } // namespace

@@ -135,7 +135,7 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// One GEMM over 128 x bn tiles (256 x bn for pairs of blocks), bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
+// One GEMM over 256 x bn tiles, bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
 // Which operands, and what becomes of a tile, is the kernel's mode.
 struct GemmParams {
     int M, N;              // rows and columns of the product
@@ -175,7 +175,6 @@ struct GemmLaunch {
         CUtensorMap a, b, out;
     } maps[2];
     GemmParams p[2];
-    bool pair;             // two blocks a tile: 256 rows
 };
 
 cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s);

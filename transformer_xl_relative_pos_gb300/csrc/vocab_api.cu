@@ -90,48 +90,36 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // so).
 int line_ld(int d) { return (int)up64(d); }
 
-// Tiles of a product of `rows` x `cols`: one block's 128 rows or a pair's 256, 128 or 256 columns,
-// and parts of its longer dimension where there are fewer tiles than SMs.
+// Tiles of a product of `rows` x `cols`: 256 rows (a pair of blocks'), 128 or 256 columns, and parts
+// of its longer dimension where there are fewer tiles than pairs.
 struct Shape {
-    bool pair;
     int bn, mb, nb, parts;
 };
 
 // What an item adds besides its steps, in cycles: its epilogue runs beside the next item's steps,
 // but its accumulator's first use and its stores do not quite.
-constexpr double kUnitCost = 1500.0;
+constexpr double kItemCost = 1500.0;
 
 // Cycles of one 64-wide step: the MMAs' (256 columns: 512) or the copies' at some 58 bytes a cycle
-// and SM, as measured of the statistics of 2048 x 131072 (pairs: 602 cycles a step, single blocks 653,
-// where L2 is also read less often than it is copied from).
-double step_cycles(bool pair, int bn)
-{
-    const double copies = (16384.0 + 128.0 * (pair ? bn / 2 : bn)) / 58.0;
-    return std::max(2.0 * bn, copies);
-}
+// and SM (602 cycles a step in the statistics of 2048 x 131072).
+double step_cycles(int bn) { return std::max(2.0 * bn, (16384.0 + 64.0 * bn) / 58.0); }
 
 // `steps`: 64-wide steps of a tile; parts: up to `most` ranges of a row block's tiles (0: an item
 // a tile).
 Shape choose_shape(long long rows, long long cols, int steps, int most)
 {
-    const int sms = txl::device_sm_count();
+    const int pairs = txl::device_sm_count() / 2;
     Shape best{};
     double least = 0.0;
-    for (int kind = 0; kind < 4; ++kind) {
-        Shape s{};
-        s.pair = kind < 2;
-        s.bn = kind % 2 ? 128 : 256;
-        if (s.bn == 256 && cols <= 128) continue;
-        const int blocks = s.pair ? 2 : 1;
-        s.mb = ceil_div(rows, 128 * blocks);
-        s.nb = ceil_div(cols, s.bn);
-        const int units = sms / blocks;
-        const double step = step_cycles(s.pair, s.bn);
+    for (const int bn : {256, 128}) {
+        if (bn == 256 && cols <= 128) continue;
+        Shape s{bn, ceil_div(rows, 256), ceil_div(cols, bn), 1};
         const int n = std::max(1, std::min(most, s.nb));
-        for (s.parts = 1; s.parts <= n; ++s.parts) {
+        for (; s.parts <= n; ++s.parts) {
             const long long items = (long long)s.mb * (most ? s.parts : s.nb);
-            const double waves = (double)((items + units - 1) / units);
-            const double cost = waves * ((double)steps * (most ? ceil_div(s.nb, s.parts) : 1) * step + kUnitCost);
+            const double waves = (double)((items + pairs - 1) / pairs);
+            const double work = (double)steps * (most ? ceil_div(s.nb, s.parts) : 1);
+            const double cost = waves * (work * step_cycles(bn) + kItemCost);
             if (best.mb == 0 || cost < least) {
                 best = s;
                 least = cost;
@@ -141,8 +129,8 @@ Shape choose_shape(long long rows, long long cols, int steps, int most)
     return best;
 }
 
-// The tiles and parts of two products that share a launch: the tiles of the second follow those
-// of the first over the units in turn.  Parts in a few steps; the same kind of unit for both.
+// The tiles and parts of two products that share a launch: the items of the second follow those of
+// the first over the pairs in turn.
 struct Two {
     Shape a, b;
 };
@@ -150,44 +138,40 @@ struct Two {
 Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&most)[2])
 {
     static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16};
-    const int sms = txl::device_sm_count();
-    Two best{};
-    double least = 0.0;
+    const int pairs = txl::device_sm_count() / 2;
     struct Option {
         Shape s;
         long long items;
-        double cost, extra;  // cycles of an item, of the parts' sum
+        double cost, extra;  // cycles of an item, and of the parts' writes and reads (3.6 kB a cycle)
     };
-    for (int pair = 1; pair >= 0; --pair) {
-        const int blocks = pair ? 2 : 1, units = sms / blocks;
-        Option o[2][16];
-        int n[2] = {};
-        for (int i = 0; i < 2; ++i)
-            for (const int bn : {256, 128}) {
-                if (bn == 256 && cols <= 128) continue;
-                for (const int parts : kParts) {
-                    if (parts > most[i]) break;
-                    Option &x = o[i][n[i]++];
-                    x.s = {pair != 0, bn, ceil_div(rows[i], 128 * blocks), ceil_div(cols, bn), parts};
-                    x.items = (long long)x.s.mb * x.s.nb * parts;
-                    x.cost = (double)ceil_div(steps[i], parts) * step_cycles(x.s.pair, bn) + kUnitCost;
-                    x.extra = parts > 1 ? parts * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
-                }
+    Option o[2][16];
+    int n[2] = {};
+    for (int i = 0; i < 2; ++i)
+        for (const int bn : {256, 128}) {
+            if (bn == 256 && cols <= 128) continue;
+            for (const int parts : kParts) {
+                if (parts > most[i]) break;
+                Option &x = o[i][n[i]++];
+                x.s = {bn, ceil_div(rows[i], 256), ceil_div(cols, bn), parts};
+                x.items = (long long)x.s.mb * x.s.nb * parts;
+                x.cost = (double)ceil_div(steps[i], parts) * step_cycles(bn) + kItemCost;
+                x.extra = parts > 1 ? parts * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
             }
-        for (int i = 0; i < n[0]; ++i)
-            for (int j = 0; j < n[1]; ++j) {
-                const Option &x = o[0][i], &y = o[1][j];
-                const long long rx = x.items % units, ry = y.items % units;
-                double cost = (double)(x.items / units) * x.cost + (double)(y.items / units) * y.cost;
-                const double last = (rx ? x.cost : 0.0) + (ry ? y.cost : 0.0);
-                cost += rx + ry > units ? last : std::max(rx ? x.cost : 0.0, ry ? y.cost : 0.0);
-                cost += x.extra + y.extra;
-                if (best.a.mb == 0 || cost < least) {
-                    best = {x.s, y.s};
-                    least = cost;
-                }
+        }
+    Two best{};
+    double least = 0.0;
+    for (int i = 0; i < n[0]; ++i)
+        for (int j = 0; j < n[1]; ++j) {
+            const Option &x = o[0][i], &y = o[1][j];
+            const long long rx = x.items % pairs, ry = y.items % pairs;
+            const double lx = rx ? x.cost : 0.0, ly = ry ? y.cost : 0.0;
+            const double cost = (double)(x.items / pairs) * x.cost + (double)(y.items / pairs) * y.cost +
+                                (rx + ry > pairs ? lx + ly : std::max(lx, ly)) + x.extra + y.extra;
+            if (best.a.mb == 0 || cost < least) {
+                best = {x.s, y.s};
+                least = cost;
             }
-    }
+        }
     return best;
 }
 
@@ -195,7 +179,6 @@ struct StatsPlan {
     bool few;                     // the vocabulary in the tiles' rows
     bool full;                    // ... and the logits written
     int mb, nb, bn, splits, list;
-    bool pair;
     size_t h_planes, w_planes, stats, val, id, keys, logits, target_z, total;  // offsets
 };
 
@@ -215,7 +198,6 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
     } else {
         const int terms = dtype == TXL_F32 ? 6 : 1;
         const Shape c = choose_shape(N, V, ceil_div(d, 64) * terms, txl::kMaxRowSplits);
-        s.pair = c.pair;
         s.mb = c.mb;
         s.bn = c.bn;
         s.nb = c.nb;
@@ -340,7 +322,7 @@ struct Operand {
 
 Operand operand(const void *p, long long ld, const char *planes, int rows, int d, int dtype)
 {
-    if (dtype == TXL_BF16) return {p, ld, 1, ld * rows};
+    if (dtype == TXL_BF16) return {p, ld, 1, ld};  // (one plane: its stride is of no meaning)
     return {planes, line_ld(d), txl::kMaxPieces, (long long)rows * line_ld(d)};
 }
 
@@ -485,9 +467,8 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     const Operand oh = operand(h, h_stride, ws + s.h_planes, N, d, dtype);
     const Operand ow = operand(w, w_stride, ws + s.w_planes, V, d, dtype);
     txl::GemmLaunch l{};
-    l.pair = s.pair;
     if (!map_of(&l.maps[0].a, oh, N, d, s.few ? (unsigned)s.bn : 128u) ||
-        !map_of(&l.maps[0].b, ow, V, d, s.few ? 128u : (unsigned)(s.pair ? s.bn / 2 : s.bn)))
+        !map_of(&l.maps[0].b, ow, V, d, s.few ? 128u : (unsigned)s.bn / 2))
         return TXL_ERR_CUDA;
     GemmParams &p = l.p[0];
     p.M = N;
@@ -630,10 +611,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.dentropy = dentropy;
     base.g_pieces = g.pieces;
     txl::GemmLaunch grad{}, prod{};
-    grad.pair = g.g.pair;
-    prod.pair = g.h.pair;
     if (!map_of(&grad.maps[0].a, oh, N, d, 128) ||
-        !map_of(&grad.maps[0].b, ow, V, d, (unsigned)(g.g.pair ? g.g.bn / 2 : g.g.bn)) ||
+        !map_of(&grad.maps[0].b, ow, V, d, (unsigned)g.g.bn / 2) ||
         !map_of(&prod.maps[0].b, ow, V, d, 64) || !map_of(&prod.maps[1].b, oh, N, d, 64))
         return TXL_ERR_CUDA;
     const Operand og = {ws + g.g_at, g.g_ld, g.pieces, g.g_plane};
@@ -683,7 +662,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             GemmParams &q = prod.p[1];
             q.M = cols;
             q.N = d;
-            q.mb = ceil_div(cols, g.w.pair ? 256 : 128);
+            q.mb = ceil_div(cols, 256);
             q.nb = g.w.nb;
             q.bn = g.w.bn;
             q.kb = ceil_div(N, 64);
