@@ -100,6 +100,9 @@ struct Shape {
 // but its accumulator's first use and its stores do not quite.
 constexpr double kItemCost = 1500.0;
 
+// The launch that sums parts, in cycles.
+constexpr double kSumLaunch = 4500.0;
+
 // Cycles of one 64-wide step: the MMAs' (256 columns: 512) or the copies' at some 58 bytes a cycle
 // and SM (602 cycles a step in the statistics of 2048 x 131072).
 double step_cycles(int bn) { return std::max(2.0 * bn, (16384.0 + 64.0 * bn) / 58.0); }
@@ -166,7 +169,8 @@ Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2]
             const long long rx = x.items % pairs, ry = y.items % pairs;
             const double lx = rx ? x.cost : 0.0, ly = ry ? y.cost : 0.0;
             const double cost = (double)(x.items / pairs) * x.cost + (double)(y.items / pairs) * y.cost +
-                                (rx + ry > pairs ? lx + ly : std::max(lx, ly)) + x.extra + y.extra;
+                                (rx + ry > pairs ? lx + ly : std::max(lx, ly)) + x.extra + y.extra +
+                                (x.s.parts > 1 || y.s.parts > 1 ? kSumLaunch : 0.0);
             if (best.a.mb == 0 || cost < least) {
                 best = {x.s, y.s};
                 least = cost;
