@@ -15,6 +15,7 @@
 //            ranges.
 //   kGrad    h W^T again; a tile becomes G, as bf16 terms in the workspace
 //   kProducts  dh = G W and dW = G^T h, the tiles of both in one launch
+// Where G is a bf16 pair, a stage holds both terms beside one tile of the other operand.
 // fp32 operands are three bf16 terms each (their leading 24 bits); a product of two
 // such operands is the six products of terms whose weight is above 2^-24.
 #include "vocab.h"
@@ -37,14 +38,14 @@ constexpr int kThreads = (4 + kEpiWarps) * 32;
 // columns (a block alone with 128 x bn tiles reads half as much again from L2 for the same work: the
 // statistics of 2048 x 131072 306 us, with pairs 287).
 constexpr int B_BYTES = MAX_BN / 2 * BK * 2;
-constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int NS = 192 * 1024 / STAGE;
-constexpr int OFF_OUT = NS * STAGE;               // a tile of 128 rows x 128 bytes per half
+constexpr int STAGE = A_BYTES + B_BYTES;          // (two terms of A: one A_BYTES more)
+constexpr int RING = 192 * 1024, MAX_NS = RING / STAGE;
+constexpr int OFF_OUT = RING;                     // a tile of 128 rows x 128 bytes per half
 constexpr int OFF_BAR = OFF_OUT + 2 * OUT_BYTES;
-constexpr int OFF_MISC = OFF_BAR + (2 * NS + 4) * 8;
+constexpr int OFF_MISC = OFF_BAR + (2 * MAX_NS + 4) * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
 
-static_assert(STAGE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 
 enum Mode { kStats, kGrad, kProducts };
@@ -208,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     // (dW's A operand, G^T, is MN-major; both products' B operand is)
     constexpr bool B_MN = MODE == kProducts;
+    // stages of the ring: A's rows (of two terms, if a product has them), then B's columns
+    const int stage = g.dual ? STAGE + A_BYTES : STAGE, ns = RING / stage;
+    const int off_b = g.dual ? 2 * A_BYTES : A_BYTES;
     const int n_items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
     unsigned int *status = g.p[0].status;
     extern __shared__ uint8_t smem_raw[];
@@ -219,13 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // full (counted on block 0), empty, accumulators full and empty (block 0)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
-    uint64_t *empty = full + NS;
-    uint64_t *acc_full = empty + NS;
+    uint64_t *empty = full + MAX_NS;
+    uint64_t *acc_full = empty + MAX_NS;
     uint64_t *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < ns; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
@@ -268,8 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const CUtensorMap *tm_a = &g.maps[i.side].a, *tm_b = &g.maps[i.side].b;
                 const int bn = p.bn, own_bn = bn / 2;  // columns of B in this block
                 const int b_row0 = p.b_row0, n_pairs = p.n_pairs;
+                const bool two = p.two_terms;
                 const unsigned pair_a = p.pair_a, pair_b = p.pair_b;
-                const uint32_t stage_tx = (uint32_t)(A_BYTES + own_bn * BK * 2) * 2;
+                const uint32_t stage_tx = (uint32_t)((two ? 2 : 1) * A_BYTES + own_bn * BK * 2) * 2;
                 const bool a_mn = MODE == kProducts && i.side;
                 const int nt = i.tiles(p);
                 for (int t = 0; t < nt && ok; ++t) {
@@ -279,26 +284,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int pa = (pair_a >> (4 * pr)) & 15, pb = (pair_b >> (4 * pr)) & 15;
                         for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
                             if (!(ok = mbar_wait(empty + s, phase, abort_flag, wait_ns))) break;
-                            uint8_t *st = smem + s * STAGE;
+                            uint8_t *st = smem + s * stage;
                             if (rank == 0) mbar_arrive_expect_tx(full + s, stage_tx);
                             const uint32_t bar = full0 + s * 8;
-                            if (a_mn) {
+                            for (int t = 0; t < (MODE == kProducts && two ? 2 : 1); ++t) {
+                                if (a_mn) {
 #pragma unroll
-                                for (int x = 0; x < BM / 64; ++x)
-                                    tma_load_3d_pair(st + x * SLAB, tm_a, bar, m0 + x * 64, kb * BK, pa);
-                            } else {
-                                tma_load_3d_pair(st, tm_a, bar, kb * BK, m0, pa);
+                                    for (int x = 0; x < BM / 64; ++x)
+                                        tma_load_3d_pair(st + t * A_BYTES + x * SLAB, tm_a, bar, m0 + x * 64, kb * BK,
+                                                         pa + t);
+                                } else {
+                                    tma_load_3d_pair(st + t * A_BYTES, tm_a, bar, kb * BK, m0, pa + t);
+                                }
                             }
                             if (B_MN) {
 #pragma unroll
                                 for (int x = 0; x < MAX_BN / 2 / 64; ++x)
                                     if (x * 64 < own_bn)
-                                        tma_load_3d_pair(st + A_BYTES + x * SLAB, tm_b, bar, n0 + x * 64, b_row0 + kb * BK, pb);
+                                        tma_load_3d_pair(st + off_b + x * SLAB, tm_b, bar, n0 + x * 64, b_row0 + kb * BK, pb);
                             } else {
-                                tma_load_3d_pair(st + A_BYTES, tm_b, bar, kb * BK, b_row0 + n0, pb);
+                                tma_load_3d_pair(st + off_b, tm_b, bar, kb * BK, b_row0 + n0, pb);
                             }
                             ++it;
-                            if (++s == NS) {
+                            if (++s == ns) {
                                 s = 0;
                                 phase ^= 1;
                             }
@@ -313,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the other block gives a millisecond
                 const int zero = 0;
                 if (rank == 0) {
-                    for (int i = max(0, it - NS); i < it; ++i)
-                        mbar_wait(full + i % NS, (i / NS) & 1, &zero, wait_ns);
+                    for (int i = max(0, it - ns); i < it; ++i)
+                        mbar_wait(full + i % ns, (i / ns) & 1, &zero, wait_ns);
                 } else {
                     const uint64_t t0 = globaltimer_ns();
                     while (globaltimer_ns() - t0 < 1000000ull) {
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ===================== MMA issuer (block 0) ==============================
-        const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + A_BYTES);
+        const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + off_b);
         const uint64_t dB = B_MN ? sdesc_sw128_mn(b0, SLAB) : sdesc_sw128(b0);
         constexpr int STEP_B = B_MN ? 16 * 128 / 16 : 2;
         auto elect = []() -> bool {
@@ -343,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ID = idesc_bf16_f32(2 * BM, p.bn, B_MN) | (a_mn ? 1u << 15 : 0u);
             const uint64_t dA = a_mn ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
             const int step_a = a_mn ? 16 * 128 / 16 : 2;
+            const bool two = MODE == kProducts && p.two_terms;
             const int nt = i.tiles(p);
             for (int t = 0; t < nt && ok; ++t) {
                 const Tile w = i.tile(p, t);
@@ -356,17 +365,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, mbar_wait(full + s, phase, abort_flag, wait_ns));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint64_t off = (uint64_t)((s * STAGE) >> 4);
+                    const uint64_t off = (uint64_t)((s * stage) >> 4);
                     if (elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk) {
+                        for (int kk = 0; kk < BK / 16; ++kk)
                             mma_bf16_ss_pair(acc, dA + off + kk * step_a, dB + off + kk * STEP_B, ID,
                                              k > 0 || kk > 0 ? 1u : 0u);
-                        }
+                        if (two)
+#pragma unroll
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                mma_bf16_ss_pair(acc, dA + off + (A_BYTES >> 4) + kk * step_a, dB + off + kk * STEP_B,
+                                                 ID, 1u);
                         mma_commit_pair(empty + s);
                     }
                     __syncwarp();
-                    if (++s == NS) {
+                    if (++s == ns) {
                         s = 0;
                         phase ^= 1;
                     }
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else if (p.part || !p.out_bf16) {
-                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16));
+                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16) * (p.two_terms ? 2 : 1));
 #pragma unroll 1
                     for (int c = c_lo; c < c_hi; c += 32) {
                         uint32_t raw[32];

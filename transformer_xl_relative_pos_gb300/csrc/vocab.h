@@ -145,6 +145,7 @@ struct GemmParams {
     int n_items;
     int n_pairs;           // products of terms: term (pair_a >> 4 i) & 15 of A by that of B
     unsigned pair_a, pair_b;
+    int two_terms;         // products: A's terms 0 and 1 by B's one in the same step (n_pairs 1)
     int b_row0;            // offset of B's rows (the vocabulary chunk's first)
     unsigned int *status;
     unsigned long long wait_ns;
@@ -175,6 +176,7 @@ struct GemmLaunch {
         CUtensorMap a, b, out;
     } maps[2];
     GemmParams p[2];
+    bool dual;             // room for two terms of A in a stage
 };
 
 cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s);

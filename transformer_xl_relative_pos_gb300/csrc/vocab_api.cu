@@ -306,8 +306,13 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
 // Products of terms of two operands with pa and pb bf16 terms, the smallest first.
 void set_pairs(GemmParams &p, int pa, int pb)
 {
-    static constexpr int order[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
     p.n_pairs = 0;
+    if (pa == 2 && pb == 1) {
+        p.n_pairs = 1;
+        p.two_terms = 1;
+        return;
+    }
+    static constexpr int order[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
     for (const auto &o : order)
         if (o[0] < pa && o[1] < pb) {
             p.pair_a |= (unsigned)o[0] << (4 * p.n_pairs);
@@ -682,6 +687,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
                 sums[1] = {reinterpret_cast<float *>(ws + g.part_w), rows, (long long)cols * d, g.w.parts,
                            grad_dtype == TXL_BF16};
         }
+        prod.dual = prod.p[0].two_terms || prod.p[1].two_terms;
         if (txl::launch_products(prod, st) != cudaSuccess) return TXL_ERR_CUDA;
         if (txl::launch_sum_parts(sums, st) != cudaSuccess) return TXL_ERR_CUDA;
     }
