@@ -30,7 +30,7 @@ constexpr int BM = 128, BK = 64, MAX_BN = 256;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
 constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
-constexpr int OUT_BYTES = BM * 128;
+constexpr int OUT_BYTES = 32 * 128;               // a warp's rows of a stored tile
 constexpr int kEpiWarps = 8;                      // two halves of a tile's columns, four warps each
 constexpr int kThreads = (4 + kEpiWarps) * 32;
 
@@ -40,8 +40,8 @@ constexpr int kThreads = (4 + kEpiWarps) * 32;
 constexpr int B_BYTES = MAX_BN / 2 * BK * 2;
 constexpr int STAGE = A_BYTES + B_BYTES;          // (two terms of A: one A_BYTES more)
 constexpr int RING = 192 * 1024, MAX_NS = RING / STAGE;
-constexpr int OFF_OUT = RING;                     // a tile of 128 rows x 128 bytes per half
-constexpr int OFF_BAR = OFF_OUT + 2 * OUT_BYTES;
+constexpr int OFF_OUT = RING;
+constexpr int OFF_BAR = OFF_OUT + kEpiWarps * OUT_BYTES;
 constexpr int OFF_MISC = OFF_BAR + (2 * MAX_NS + 4) * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
 
@@ -185,22 +185,6 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
             }
         }
     }
-}
-
-// Barrier of the warps of one half of the epilogue; whether any of its threads says so.
-__device__ __forceinline__ void half_sync(int half)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kEpiWarps * 16) : "memory");
-}
-__device__ __forceinline__ bool half_any(int half, bool x)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred b, %2, %3, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-                 : "=r"(r)
-                 : "r"((uint32_t)x), "r"(1 + half), "n"(kEpiWarps * 16)
-                 : "memory");
-    return r != 0;
 }
 
 template <Mode MODE, int LIST>
@@ -406,21 +390,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp & 3, half = (warp - 4) >> 2;
         const int row = wq * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
-        uint8_t *out = smem + OFF_OUT + half * OUT_BYTES;
-        const bool issuer = wq == 0 && lane == 0;  // of the half's stores
+        uint8_t *out = smem + OFF_OUT + (warp - 4) * OUT_BYTES;
         constexpr float kLog2e = 1.4426950408889634f;
         const float zscale = g.p[0].scale * uncut_scale(g.p[0].kb * (BK / 16)), c2 = zscale * kLog2e;
-        // 128 bytes of each row, turned by the swizzle, then one store of the half's 128 rows
+        // 128 bytes of each of the warp's rows, turned by the swizzle, then one store.  Each warp for
+        // itself: with four that met at barriers around one store of 128 rows the products of
+        // 64 x 32000 x 1024 took 45.1 us, so 39.9; from 2048 rows on both take the same.
         const CUtensorMap *tm_out = &g.maps[0].out;
         auto store = [&](const uint4 (&v)[8], int c0, int m0, int plane) {
-            if (issuer) bulk_wait_read();
-            half_sync(half);
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4 *>(out + row * 128 + ((q ^ (row & 7)) << 4)) = v[q];
+            for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) << 4)) = v[q];
             fence_proxy_async_smem();
-            half_sync(half);
-            if (issuer) {
-                tma_store_3d(tm_out, out, c0, m0, plane);
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(tm_out, out, c0, m0 + wq * 32, plane);
                 bulk_commit();
             }
         };
@@ -463,23 +448,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (tile >> 1) & 1, abort_flag, wait_ns)) &&
                      !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
-                // (the half's warps meet at its barriers: they leave together)
-                if (MODE != kStats) ok = !half_any(half, !ok);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const int m0 = (w.m * 2 + rank) * BM, n0 = w.n * p.bn;
-                // (a block whose rows lie behind the last has nothing to write)
-                const int c_lo = half * (p.bn / 2), c_hi = m0 < p.M ? min((half + 1) * (p.bn / 2), p.N - n0) : 0;
+                // (a warp whose rows lie behind the last has nothing to do)
+                const int c_lo = half * (p.bn / 2),
+                          c_hi = m0 + wq * 32 < p.M ? min((half + 1) * (p.bn / 2), p.N - n0) : 0;
                 const bool empty_part = w.kb_lo == w.kb_hi;  // (nothing was accumulated)
                 auto logits = [&](uint32_t (&raw)[32], int c) {
                     tmem_ld32(tq + buf * MAX_BN + c, raw);
                     tmem_ld_wait(raw);
                 };
                 if (MODE == kStats) {
-                    // (a warp whose rows lie behind the last has nothing to do)
-                    const int stop = m0 + wq * 32 < p.M ? c_hi : 0;
 #pragma unroll 1
-                    for (int c = c_lo; c < stop; c += 32) {
+                    for (int c = c_lo; c < c_hi; c += 32) {
                         uint32_t raw[32];
                         logits(raw, c);
                         const int cnt = min(32, c_hi - c);
@@ -577,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (MODE != kStats && issuer) bulk_wait_all();
+        if (MODE != kStats && lane == 0) bulk_wait_all();
         if (!ok && lane == 0) {
             atomicOr(status, TXL_STATUS_TIMEOUT);
             *abort_flag = 1;

@@ -170,7 +170,7 @@ struct GemmParams {
 
 // A launch: the statistics, the gradient of the logits, or both products (p[0] dh, p[1] dW; one
 // of them may have no items).  Operands in boxes of 64 elements; out: boxes of 128 bytes of columns
-// and 128 rows for the tiles' stores (G's terms; a product or its parts one behind the other).
+// and 32 rows for the tiles' stores (G's terms; a product or its parts one behind the other).
 struct GemmLaunch {
     struct {
         CUtensorMap a, b, out;

@@ -350,8 +350,8 @@ bool map_out(CUtensorMap *map, const GemmParams &p, char *base)
 {
     const long long plane = (long long)p.M * p.N;
     return p.part || !p.out_bf16
-               ? txl::make_map_planes_f32(map, base, p.N, p.M, p.N, p.part ? p.splits : 1, plane, 128)
-               : txl::make_map_planes(map, base, p.N, p.M, p.N, 1, plane, 128);
+               ? txl::make_map_planes_f32(map, base, p.N, p.M, p.N, p.part ? p.splits : 1, plane, 32)
+               : txl::make_map_planes(map, base, p.N, p.M, p.N, 1, plane, 32);
 }
 
 } // namespace
@@ -640,9 +640,9 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         p.n_items = p.mb * p.nb;
         p.b_row0 = v0;
         set_pairs(p, oh.planes, ow.planes);
-        if (!map_of(&grad.maps[0].out, og, N, cols, 128)) return TXL_ERR_CUDA;
+        if (!map_of(&grad.maps[0].out, og, N, cols, 32) || !map_of(&prod.maps[0].a, og, N, cols, 128))
+            return TXL_ERR_CUDA;
         if (txl::launch_logprob_grad(grad, st) != cudaSuccess) return TXL_ERR_CUDA;
-        prod.maps[0].a = grad.maps[0].out;
         prod.p[0] = prod.p[1] = base;
         txl::PartsSum sums[2] = {};
         if (dh) {
