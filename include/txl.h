@@ -573,9 +573,11 @@ int txl_relattn_tree_fwd(const txl_rows *q, const txl_rows *k_new, const txl_row
  * multiple: of 8 elements, of 4 where all rows are fp32 in txl_embed_bwd.  Row strides in
  * elements, multiples of 16 bytes, at least d (so h may be, say, the last position of every
  * segment); pointers of rows 16-byte, of other arrays as their element, workspaces 256-byte
- * aligned.  txl_embed_fwd takes any d, stride and element-aligned pointers.  Outputs and workspaces that overlap inputs or one another are
- * refused (TXL_ERR_INVALID_ARG).  Workspaces are the caller's, their contents undefined before and after; calls that may run at the same
- * time need one each.  n, N and V up to 2^28; n or N = 0 is allowed.
+ * aligned.  txl_embed_fwd takes any d, stride and element-aligned pointers.  Outputs and
+ * workspaces that overlap inputs or one another are refused (TXL_ERR_INVALID_ARG), as are
+ * scales that are not finite.  Workspaces are the caller's, their contents undefined before
+ * and after; calls that may run at the same time need one each.  n, N and V up to 2^28; n or
+ * N = 0 is allowed.
  */
 typedef enum {
     TXL_I32 = 4,
@@ -653,7 +655,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
  * dw of bf16 operands, and in both products for N <= 128; and for fp32 operands as three terms.
  * Sums are fp32 in a fixed order: results repeat bit for bit.
  *   workspace: txl_logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype) bytes (G in chunks
- *   of the vocabulary, up to about 1 GiB, and partial sums).
+ *   of the vocabulary, up to about 1 GiB or 128 columns, and partial sums).
  * Errors: as txl_logprob_fwd.
  */
 size_t txl_logprob_bwd_workspace_size(int N, int V, int d, int dtype, int grad_dtype);

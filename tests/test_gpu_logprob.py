@@ -396,3 +396,107 @@ def test_logprob_refusals():
             bad()
         assert e.value.status == status
     assert txl.device_status() == 0
+
+
+def test_lone_rows_with_any_stride():
+    # (a stride that leads nowhere: C callers pass what their array has)
+    for N, V in ((1, 50), (5, 1), (1, 1)):
+        d = 64
+        h, w, t = (x.to(dev()) for x in _inputs(N, V, d, BF, N + V))
+        lse, dlogp = torch.zeros(N, device=dev()), torch.ones(N, device=dev())
+        dh, dw = torch.zeros_like(h), torch.zeros_like(w)
+        hs, ws = 8 if N == 1 else d, 8 if V == 1 else d
+        kind = 4 if t.dtype == torch.int32 else 8
+        room = torch.empty(max(txl.logprob_fwd_workspace_size(N, V, d), txl.logprob_bwd_workspace_size(N, V, d)),
+                           dtype=torch.uint8, device=dev())
+        stream = torch.cuda.current_stream().cuda_stream
+        ptr = lambda *x: [y.data_ptr() for y in x]
+        assert txl.lib().txl_logprob_fwd(h.data_ptr(), hs, w.data_ptr(), ws, t.data_ptr(), kind, None,
+                                         lse.data_ptr(), None, None, None, N, V, d, 0, 1.0, txl.BF16,
+                                         room.data_ptr(), room.numel(), stream) == 0
+        assert txl.lib().txl_logprob_bwd(h.data_ptr(), hs, w.data_ptr(), ws, t.data_ptr(), kind, lse.data_ptr(),
+                                         None, dlogp.data_ptr(), None, dh.data_ptr(), dw.data_ptr(), N, V, d, 1.0,
+                                         txl.BF16, txl.BF16, room.data_ptr(), room.numel(), stream) == 0
+        _ok()
+        assert torch.equal(lse, txl.logprob_fwd(h, w, t).lse)
+        want = txl.logprob_bwd(h, w, t, lse, dlogp)
+        assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])
+
+
+def test_tables_past_two_to_the_31_elements():
+    V, d = 33000, 65536
+    g = torch.Generator(device=dev()).manual_seed(9)
+    w = torch.empty(V, d, dtype=BF, device=dev())
+    w.normal_(0.0, 0.02, generator=g)
+    ids = torch.tensor([V - 1, 3, V - 2, V - 1, -1], device=dev())
+    x = txl.embed_fwd(ids, w)
+    assert torch.equal(x[:4], w[ids[:4]]) and bool((x[4] == 0).all())
+    dtab = txl.embed_bwd(x, ids, V, dtype=BF)
+    # (two equal rows of bf16 sum exactly, but for a doubled largest value)
+    assert torch.equal(dtab[V - 1], 2 * w[V - 1]) and torch.equal(dtab[V - 2], w[V - 2]) and torch.equal(dtab[3], w[3])
+    assert int((dtab.abs().amax(1) > 0).sum()) == 3
+    del dtab
+    h = torch.randn(5, d, generator=g, device=dev()).to(BF)
+    t = torch.tensor([V - 1, V - 2, 0, -1, 32768], device=dev(), dtype=torch.int32)
+    res = txl.logprob_fwd(h, w, t, scale=0.25, top=4)
+    dlogp = torch.tensor([1.0, -0.5, 0.3, 7.0, 2.0], device=dev())
+    dh, dw = txl.logprob_bwd(h, w, t, res.lse, dlogp, scale=0.25)
+    _ok()
+    z = torch.cat([0.25 * (h.double() @ w[i:i + 4096].double().t()) for i in range(0, V, 4096)], 1).cpu()
+    lse = torch.logsumexp(z, 1)
+    off = d * model.F32_CUT * 0.25 * (h.double().abs() @ w[:4096].double().abs().t()).max().item() * 1.1
+    assert float((res.lse.cpu().double() - lse).abs().max()) <= off
+    lp = z - lse[:, None]
+    live = t.cpu() >= 0
+    want = lp.gather(1, t.cpu().long().clamp(min=0)[:, None])[:, 0] * live
+    assert float((res.logp.cpu().double() - want).abs().max()) <= 2 * off
+    assert torch.equal(res.top_ids.cpu().long(), torch.sort(z, dim=1, descending=True, stable=True)[1][:, :4])
+    # the last rows of dW: G a bf16 pair (residuals of 2^-16), one rounding of the result, probabilities
+    # off by the logits' bound
+    some = torch.arange(V - 200, V)
+    hit = (some[None, :] == t.cpu()[:, None]).double()
+    G = 0.25 * (dlogp.cpu().double() * live)[:, None] * (hit - torch.exp(lp[:, some]))
+    p_off = 0.25 * (dlogp.cpu().double().abs() * live)[:, None] * torch.exp(lp[:, some]) * 2 * off
+    h64 = h.cpu().double()
+    tol = ((G.abs() * 2.0 ** -16 + p_off).t() @ h64.abs()) * 1.1 + model.BF16_HALF * (G.t() @ h64).abs() + 1e-30
+    assert bool(((dw[V - 200:].cpu().double() - G.t() @ h64).abs() <= tol).all())
+    # dh along some columns, over all of the table
+    cols = slice(d - 64, d)
+    G = 0.25 * (dlogp.cpu().double() * live)[:, None] * (torch.nn.functional.one_hot(t.cpu().long().clamp(min=0), V)
+                                                        * live[:, None] - torch.exp(lp))
+    W = w[:, cols].cpu().double()
+    size = G.abs() @ W.abs()
+    tol = (2.0 ** -16 + V * model.F32_CUT + 2 * off) * size * 1.1 + model.BF16_HALF * (G @ W).abs() + 1e-30
+    assert bool(((dh[:, cols].cpu().double() - G @ W).abs() <= tol).all())
+
+
+def test_two_host_threads_on_their_own_streams():
+    import threading
+
+    cases = []
+    for seed, (N, V, d, top) in enumerate(((5, 3000, 256, 4), (300, 1000, 64, 0))):
+        h, w, t = (x.to(dev()) for x in _inputs(N, V, d, BF, seed))
+        dlogp = torch.randn(N, device=dev())
+        res = txl.logprob_fwd(h, w, t, top=top)
+        cases.append((h, w, t, dlogp, top, res, txl.logprob_bwd(h, w, t, res.lse, dlogp)))
+    _ok()
+    failures = []
+
+    def run(h, w, t, dlogp, top, res, grads):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = txl.logprob_fwd(h, w, t, top=top)
+                    back = txl.logprob_bwd(h, w, t, got.lse, dlogp)
+                    same = [torch.equal(a, b) for a, b in zip((*got, *back), (*res, *grads)) if a is not None]
+                    assert all(same), same
+        except BaseException as e:
+            failures.append(e)
+
+    threads = [threading.Thread(target=run, args=c) for c in cases]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join(120)
+    assert not failures, failures
+    _ok()

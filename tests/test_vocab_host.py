@@ -90,6 +90,13 @@ def test_logprob_bwd_refuses(kw, want):
     assert bwd(**kw) == want
 
 
+@pytest.mark.parametrize("call", [embed, embed_bwd, fwd, bwd])
+@pytest.mark.parametrize("scale", [float("inf"), -float("inf")])
+def test_infinite_scales_are_refused(call, scale):
+    # (times the zeros of an absent token it would be NaN)
+    assert call(scale=scale) == INVALID
+
+
 def test_workspace_sizes():
     assert txl.embed_bwd_workspace_size(0, 10, 16) == 0
     assert txl.embed_bwd_workspace_size(100, 10, 6) == 0       # refused sizes need none

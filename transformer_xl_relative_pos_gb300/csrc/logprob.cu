@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint32_t full0 = cluster_addr(full, 0);
             for (int i = 0; i < (MODE == kProducts ? 2 : 1); ++i) {
+                if (g.p[i].n_items == 0) continue;  // (a gradient that is not wanted has no maps)
                 prefetch_tensormap(&g.maps[i].a);
                 prefetch_tensormap(&g.maps[i].b);
             }

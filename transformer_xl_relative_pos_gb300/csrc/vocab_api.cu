@@ -1,6 +1,7 @@
 // C-ABI entry points of the token embedding and of the log probabilities (include/txl.h):
 // argument validation, work division, workspace layout, launches.
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "txl.h"
@@ -321,6 +322,9 @@ void set_pairs(GemmParams &p, int pa, int pb)
         }
 }
 
+// (a lone row may come with any stride: its own width then)
+long long own_ld(long long ld, int rows, int d) { return rows > 1 ? ld : d; }
+
 // The bf16 terms of a [rows][d] operand: itself, or its planes in the workspace.
 struct Operand {
     const void *p;
@@ -331,7 +335,7 @@ struct Operand {
 
 Operand operand(const void *p, long long ld, const char *planes, int rows, int d, int dtype)
 {
-    if (dtype == TXL_BF16) return {p, ld, 1, ld};  // (one plane: its stride is of no meaning)
+    if (dtype == TXL_BF16) return {p, own_ld(ld, rows, d), 1, own_ld(ld, rows, d)};  // (one plane: its stride is of no meaning)
     return {planes, line_ld(d), txl::kMaxPieces, (long long)rows * line_ld(d)};
 }
 
@@ -364,7 +368,7 @@ int txl_embed_fwd(const void *tokens, int index_type, const void *emb, long long
     int rc;
     if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(n, V, d, 1)) != TXL_OK) return rc;
     if ((rc = check_ids(tokens, index_type)) != TXL_OK) return rc;
-    if (!emb || (n > 0 && (!tokens || !out)) || !(scale == scale) || emb_stride < 1) return TXL_ERR_INVALID_ARG;
+    if (!emb || (n > 0 && (!tokens || !out)) || !std::isfinite(scale) || emb_stride < 1) return TXL_ERR_INVALID_ARG;
     if (emb_stride < d && V > 1) return TXL_ERR_SHAPE;
     if (emb_stride > (1LL << 36)) return TXL_ERR_UNSUPPORTED;
     if (!on(emb, (size_t)elem(dtype)) || !on(out, (size_t)elem(dtype))) return TXL_ERR_MISALIGNED;
@@ -402,7 +406,7 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
     if ((rc = check_type(dtype)) != TXL_OK || (rc = check_type(grad_dtype)) != TXL_OK) return rc;
     if ((rc = check_sizes(n, V, d, unit_of(dtype, grad_dtype))) != TXL_OK) return rc;
     if ((rc = check_ids(tokens, index_type)) != TXL_OK) return rc;
-    if (!demb || (n > 0 && (!tokens || !dout)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if (!demb || (n > 0 && (!tokens || !dout)) || !std::isfinite(scale)) return TXL_ERR_INVALID_ARG;
     if (accumulate && grad_dtype != TXL_F32) return TXL_ERR_UNSUPPORTED;
     if (n > 0 && (rc = check_rows(dout, dout_stride, n, d, dtype)) != TXL_OK) return rc;
     if (!on(demb, 16)) return TXL_ERR_MISALIGNED;
@@ -446,7 +450,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     int rc;
     if ((rc = check_type(dtype)) != TXL_OK || (rc = check_sizes(N, V, d, 8)) != TXL_OK) return rc;
     if ((rc = check_ids(targets, index_type)) != TXL_OK) return rc;
-    if (top < 0 || !w || (N > 0 && !h) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if (top < 0 || !w || (N > 0 && !h) || !std::isfinite(scale)) return TXL_ERR_INVALID_ARG;
     if (top > txl::kMaxTop) return TXL_ERR_UNSUPPORTED;
     if (N > 0 && top > 0 && (!top_logp || !top_ids)) return TXL_ERR_INVALID_ARG;
     if (N > 0 && !logp && !lse && !entropy && top == 0) return TXL_ERR_INVALID_ARG;
@@ -556,7 +560,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     if ((rc = check_type(dtype)) != TXL_OK || (rc = check_type(grad_dtype)) != TXL_OK) return rc;
     if ((rc = check_sizes(N, V, d, 8)) != TXL_OK) return rc;
     if ((rc = check_ids(targets, index_type)) != TXL_OK) return rc;
-    if (!w || (!dh && !dw) || (N > 0 && (!h || !lse)) || !(scale == scale)) return TXL_ERR_INVALID_ARG;
+    if (!w || (!dh && !dw) || (N > 0 && (!h || !lse)) || !std::isfinite(scale)) return TXL_ERR_INVALID_ARG;
     if ((targets == nullptr) != (dlogp == nullptr)) return TXL_ERR_INVALID_ARG;
     if (N > 0 && ((!dlogp && !dentropy) || (dentropy && !entropy))) return TXL_ERR_INVALID_ARG;
     if (dtype == TXL_F32 && grad_dtype != TXL_F32) return TXL_ERR_UNSUPPORTED;
