@@ -17,7 +17,9 @@
 //   kProducts  dh = G W and dW = G^T h, the tiles of both in one launch
 // Where G is a bf16 pair, a stage holds both terms beside one tile of the other operand.
 // fp32 operands are three bf16 terms each (their leading 24 bits); a product of two
-// such operands is the six products of terms whose weight is above 2^-24.
+// such operands is the six products of terms whose weight is above 2^-24.  A step of them loads
+// each term once, three stages for six products (where every product had its own two tiles, the
+// gradient of 333 x 5003 x 520 took 73 us, so 61).
 #include "vocab.h"
 #include "ptx.cuh"
 
@@ -29,7 +31,8 @@ using namespace ptx;
 constexpr int BM = 128, BK = 64, MAX_BN = 256;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int SLAB = BK * 128;                    // 64 MN elements x BK rows
-constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns
+constexpr uint32_t TM_COLS = 512;                 // two accumulators of 256 columns,
+constexpr int REST = 128;                         // ... or of 128 and, behind them, the small products
 constexpr int OUT_BYTES = 32 * 128;               // a warp's rows of a stored tile
 constexpr int kEpiWarps = 8;                      // two halves of a tile's columns, four warps each
 constexpr int kThreads = (4 + kEpiWarps) * 32;
@@ -38,14 +41,13 @@ constexpr int kThreads = (4 + kEpiWarps) * 32;
 // columns (a block alone with 128 x bn tiles reads half as much again from L2 for the same work: the
 // statistics of 2048 x 131072 306 us, with pairs 287).
 constexpr int B_BYTES = MAX_BN / 2 * BK * 2;
-constexpr int STAGE = A_BYTES + B_BYTES;          // (two terms of A: one A_BYTES more)
-constexpr int RING = 192 * 1024, MAX_NS = RING / STAGE;
+constexpr int RING = 192 * 1024, MAX_NS = RING / (A_BYTES + B_BYTES / 2);
 constexpr int OFF_OUT = RING;
 constexpr int OFF_BAR = OFF_OUT + kEpiWarps * OUT_BYTES;
 constexpr int OFF_MISC = OFF_BAR + (2 * MAX_NS + 4) * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // (slack for the manual alignment)
 
-static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+static_assert(A_BYTES % 1024 == 0 && B_BYTES % 2048 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 
 enum Mode { kStats, kGrad, kProducts };
@@ -187,15 +189,17 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
     }
 }
 
-template <Mode MODE, int LIST>
+// THREE: three terms of both operands.
+template <Mode MODE, int LIST, bool THREE>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ GemmLaunch g)
 {
     // (dW's A operand, G^T, is MN-major; both products' B operand is)
     constexpr bool B_MN = MODE == kProducts;
-    // stages of the ring: A's rows (of two terms, if a product has them), then B's columns
-    const int stage = g.dual ? STAGE + A_BYTES : STAGE, ns = RING / stage;
-    const int off_b = g.dual ? 2 * A_BYTES : A_BYTES;
+    // stages of the ring: A's rows (two terms of them, if a product has them), then B's columns
+    const bool dual = MODE == kProducts && !THREE && (g.p[0].terms == 2 || g.p[1].terms == 2);
+    const int off_b = dual ? 2 * A_BYTES : A_BYTES;
+    const int stage = off_b + (THREE ? B_BYTES / 2 : B_BYTES), ns = RING / stage;
     const int n_items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
     unsigned int *status = g.p[0].status;
     extern __shared__ uint8_t smem_raw[];
@@ -256,18 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // of parameters would be repeated after every one)
                 const CUtensorMap *tm_a = &g.maps[i.side].a, *tm_b = &g.maps[i.side].b;
                 const int bn = p.bn, own_bn = bn / 2;  // columns of B in this block
-                const int b_row0 = p.b_row0, n_pairs = p.n_pairs;
-                const bool two = p.two_terms;
-                const unsigned pair_a = p.pair_a, pair_b = p.pair_b;
+                const int b_row0 = p.b_row0;
+                const bool two = !THREE && p.terms == 2;
                 const uint32_t stage_tx = (uint32_t)((two ? 2 : 1) * A_BYTES + own_bn * BK * 2) * 2;
                 const bool a_mn = MODE == kProducts && i.side;
                 const int nt = i.tiles(p);
                 for (int t = 0; t < nt && ok; ++t) {
                     const Tile w = i.tile(p, t);
                     const int m0 = (w.m * 2 + rank) * BM, n0 = w.n * bn + rank * own_bn;
-                    for (int pr = 0; pr < n_pairs && ok; ++pr) {
-                        const int pa = (pair_a >> (4 * pr)) & 15, pb = (pair_b >> (4 * pr)) & 15;
-                        for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
+                    for (int kb = w.kb_lo; kb < w.kb_hi && ok; ++kb) {
+                        for (int term = 0; term < (THREE ? 3 : 1); ++term) {
                             if (!(ok = mbar_wait(empty + s, phase, abort_flag, wait_ns))) break;
                             uint8_t *st = smem + s * stage;
                             if (rank == 0) mbar_arrive_expect_tx(full + s, stage_tx);
@@ -277,18 +279,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                     for (int x = 0; x < BM / 64; ++x)
                                         tma_load_3d_pair(st + t * A_BYTES + x * SLAB, tm_a, bar, m0 + x * 64, kb * BK,
-                                                         pa + t);
+                                                         term + t);
                                 } else {
-                                    tma_load_3d_pair(st + t * A_BYTES, tm_a, bar, kb * BK, m0, pa + t);
+                                    tma_load_3d_pair(st + t * A_BYTES, tm_a, bar, kb * BK, m0, term + t);
                                 }
                             }
                             if (B_MN) {
 #pragma unroll
                                 for (int x = 0; x < MAX_BN / 2 / 64; ++x)
                                     if (x * 64 < own_bn)
-                                        tma_load_3d_pair(st + off_b + x * SLAB, tm_b, bar, n0 + x * 64, b_row0 + kb * BK, pb);
+                                        tma_load_3d_pair(st + off_b + x * SLAB, tm_b, bar, n0 + x * 64, b_row0 + kb * BK, term);
                             } else {
-                                tma_load_3d_pair(st + off_b, tm_b, bar, kb * BK, b_row0 + n0, pb);
+                                tma_load_3d_pair(st + off_b, tm_b, bar, kb * BK, b_row0 + n0, term);
                             }
                             ++it;
                             if (++s == ns) {
@@ -336,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ID = idesc_bf16_f32(2 * BM, p.bn, B_MN) | (a_mn ? 1u << 15 : 0u);
             const uint64_t dA = a_mn ? sdesc_sw128_mn(a0, SLAB) : sdesc_sw128(a0);
             const int step_a = a_mn ? 16 * 128 / 16 : 2;
-            const bool two = MODE == kProducts && p.two_terms;
+            const bool two = MODE == kProducts && !THREE && p.terms == 2;
             const int nt = i.tiles(p);
             for (int t = 0; t < nt && ok; ++t) {
                 const Tile w = i.tile(p, t);
-                const int steps = p.n_pairs * (w.kb_hi - w.kb_lo);
+                const int steps = w.kb_hi - w.kb_lo;
                 const int buf = tile & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile >> 1) & 1) ^ 1, abort_flag, wait_ns));
                 if (!ok) break;
@@ -351,7 +353,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint64_t off = (uint64_t)((s * stage) >> 4);
-                    if (elect()) {
+                    if (THREE) {
+                        // terms 0, 1, 2 of both in three stages: their products of weight 1 in one
+                        // accumulator, those of weight 2^-8 and 2^-16 in another, whose cut
+                        // additions do not matter
+                        const int first = s;
+                        auto product = [&](uint32_t to, uint64_t x, uint64_t y, bool add) {
+#pragma unroll
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                mma_bf16_ss_pair(to, dA + x + kk * step_a, dB + y + kk * STEP_B, ID,
+                                                 add || kk > 0 ? 1u : 0u);
+                        };
+                        if (elect()) product(acc, off, off, k > 0);
+                        __syncwarp();
+                        for (int term = 1; term < 3; ++term) {
+                            if (++s == ns) {
+                                s = 0;
+                                phase ^= 1;
+                            }
+                            ok = __all_sync(0xffffffffu, mbar_wait(full + s, phase, abort_flag, wait_ns));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            const uint64_t at = (uint64_t)((s * stage) >> 4);
+                            if (elect()) {
+                                product(acc + REST, at, off, k > 0 || term > 1);
+                                product(acc + REST, off, at, true);
+                                if (term == 1) product(acc + REST, at, at, true);
+                                mma_commit_pair(empty + s);
+                                if (term == 2) mma_commit_pair(empty + first);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                    } else if (elect()) {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
                             mma_bf16_ss_pair(acc, dA + off + kk * step_a, dB + off + kk * STEP_B, ID,
@@ -456,15 +490,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c_lo = half * (p.bn / 2),
                           c_hi = m0 + wq * 32 < p.M ? min((half + 1) * (p.bn / 2), p.N - n0) : 0;
                 const bool empty_part = w.kb_lo == w.kb_hi;  // (nothing was accumulated)
-                auto logits = [&](uint32_t (&raw)[32], int c) {
+                auto sums = [&](uint32_t (&raw)[32], int c) {
                     tmem_ld32(tq + buf * MAX_BN + c, raw);
-                    tmem_ld_wait(raw);
+                    if (THREE) {
+                        uint32_t rest[32];
+                        tmem_ld32(tq + buf * MAX_BN + REST + c, rest);
+                        tmem_ld_wait(raw);
+                        tmem_ld_wait(rest);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            raw[i] = __float_as_uint(__uint_as_float(raw[i]) + __uint_as_float(rest[i]));
+                    } else {
+                        tmem_ld_wait(raw);
+                    }
                 };
                 if (MODE == kStats) {
 #pragma unroll 1
                     for (int c = c_lo; c < c_hi; c += 32) {
                         uint32_t raw[32];
-                        logits(raw, c);
+                        sums(raw, c);
                         const int cnt = min(32, c_hi - c);
                         float v[32];
 #pragma unroll
@@ -479,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             uint32_t raw[32];
-                            logits(raw, c + 32 * x);
+                            sums(raw, c + 32 * x);
                             if (p.dentropy) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) {
@@ -515,11 +559,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else if (p.part || !p.out_bf16) {
-                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16) * (p.two_terms ? 2 : 1));
+                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16) * (!THREE && p.terms == 2 ? 2 : 1));
 #pragma unroll 1
                     for (int c = c_lo; c < c_hi; c += 32) {
                         uint32_t raw[32];
-                        logits(raw, c);
+                        sums(raw, c);
                         uint4 o[8];
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -533,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             uint32_t raw[32];
-                            logits(raw, c + 32 * x);
+                            sums(raw, c + 32 * x);
                             float v[32];
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = empty_part ? 0.f : __uint_as_float(raw[i]);
@@ -576,11 +620,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <Mode MODE, int LIST>
-cudaError_t launch_gemm(const GemmLaunch &g, cudaStream_t s)
+template <Mode MODE, int LIST, bool THREE>
+cudaError_t launch_gemm_of(const GemmLaunch &g, cudaStream_t s)
 {
     static bool attr_set[64] = {};  // the attribute is set once per device
-    auto *kernel = vocab_gemm_kernel<MODE, LIST>;
+    auto *kernel = vocab_gemm_kernel<MODE, LIST, THREE>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -592,6 +636,14 @@ cudaError_t launch_gemm(const GemmLaunch &g, cudaStream_t s)
     const int items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
     const unsigned grid = (unsigned)(min(items, device_sm_count() / 2) * 2);
     return launch_grid(kernel, dim3(grid), kThreads, SMEM_BYTES, s, 2, g);
+}
+
+template <Mode MODE, int LIST>
+cudaError_t launch_gemm(const GemmLaunch &g, cudaStream_t s)
+{
+    // (products: both have three terms, or neither; one may be absent)
+    const bool three = g.p[0].terms == 3 || (MODE == kProducts && g.p[1].terms == 3);
+    return three ? launch_gemm_of<MODE, LIST, true>(g, s) : launch_gemm_of<MODE, LIST, false>(g, s);
 }
 
 } // namespace

@@ -83,7 +83,8 @@ __device__ __noinline__ float4 join_lanes(const float *own, int lane)
     return make_float4(top, sum, weighted, 0.f);
 }
 
-template <int GROUPS>
+// THREE: three terms of both operands.
+template <int GROUPS, bool THREE>
 __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
     logprob_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
                        const GemmParams p, int ns)
@@ -92,6 +93,9 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // two accumulators in turn; with three terms, up to 128 states: two of 128 columns with the small
+    // products behind each; beyond: one, its small products in the other's place
+    constexpr int BUFS = THREE && GROUPS > 2 ? 1 : 2, REST = GROUPS > 2 ? ACC : ACC / 2;
     const int stage_bytes = A_BYTES + p.bn * BK * 2;
     // this block's tiles of the vocabulary
     const int t_lo = (int)((long long)blockIdx.x * p.nb / p.splits);
@@ -135,16 +139,14 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
             bool ok = true;
             int it = 0;
             for (int t = t_lo; t < t_hi && ok; ++t)
-                for (int pr = 0; pr < p.n_pairs && ok; ++pr) {
-                    // (pairs are given as terms of h by terms of w)
-                    const int ph = (p.pair_a >> (4 * pr)) & 15, pw = (p.pair_b >> (4 * pr)) & 15;
-                    for (int kb = 0; kb < p.kb; ++kb) {
+                for (int kb = 0; kb < p.kb && ok; ++kb) {
+                    for (int term = 0; term < (THREE ? 3 : 1); ++term) {
                         const int s = it % ns;
                         if (!(ok = mbar_wait(empty + s, ((it / ns) & 1) ^ 1, abort_flag, wait_ns))) break;
                         uint8_t *st = smem + s * stage_bytes;
                         mbar_arrive_expect_tx(full + s, stage_bytes);
-                        tma_load_3d(st, &tm_w, full + s, kb * BK, t * BM, pw);
-                        tma_load_3d_hint(st + A_BYTES, &tm_h, full + s, kb * BK, 0, ph, often);
+                        tma_load_3d(st, &tm_w, full + s, kb * BK, t * BM, term);
+                        tma_load_3d_hint(st + A_BYTES, &tm_h, full + s, kb * BK, 0, term, often);
                         ++it;
                     }
                 }
@@ -165,28 +167,44 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
             return el != 0;
         };
         const uint64_t dA = sdesc_sw128(smem_u32(smem)), dB = sdesc_sw128(smem_u32(smem + A_BYTES));
-        const int steps = p.n_pairs * p.kb;
         bool ok = true;
         int it = 0, tile = 0;
         for (int t = t_lo; t < t_hi; ++t) {
-            const int buf = tile & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile >> 1) & 1) ^ 1, abort_flag, wait_ns));
+            const int buf = tile % BUFS;
+            ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile / BUFS) & 1) ^ 1, abort_flag, wait_ns));
             if (!ok) break;
             tc_fence_after_sync();
-            for (int k = 0; k < steps; ++k, ++it) {
-                const int s = it % ns;
-                ok = __all_sync(0xffffffffu, mbar_wait(full + s, (it / ns) & 1, abort_flag, wait_ns));
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint64_t off = (uint64_t)((s * stage_bytes) >> 4);
-                if (elect()) {
+            const uint32_t acc = tmem + buf * ACC;
+            auto product = [&](uint32_t to, uint64_t x, uint64_t y, bool add) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        mma_bf16_ss(tmem + buf * ACC, dA + off + kk * 2, dB + off + kk * 2, ID,
-                                    (k > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(empty + s);
+                for (int kk = 0; kk < BK / 16; ++kk)
+                    mma_bf16_ss(to, dA + x + kk * 2, dB + y + kk * 2, ID, add || kk > 0 ? 1u : 0u);
+            };
+            for (int k = 0; k < p.kb && ok; ++k) {
+                // the product of the first terms in one accumulator; those of three terms whose weights are
+                // 2^-8 and 2^-16 in another, whose cut additions do not matter
+                uint64_t first = 0;
+                for (int term = 0; term < (THREE ? 3 : 1); ++term, ++it) {
+                    const int s = it % ns;
+                    ok = __all_sync(0xffffffffu, mbar_wait(full + s, (it / ns) & 1, abort_flag, wait_ns));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t at = (uint64_t)((s * stage_bytes) >> 4);
+                    if (term == 0) first = at;
+                    if (elect()) {
+                        if (term == 0) {
+                            product(acc, at, at, k > 0);
+                        } else {
+                            product(acc + REST, at, first, k > 0 || term > 1);
+                            product(acc + REST, first, at, true);
+                            if (term == 1) product(acc + REST, at, at, true);
+                        }
+                        // (of three terms, the first stage is free with the last)
+                        if (term > 0 || !THREE) mma_commit(empty + s);
+                        if (term == 2) mma_commit(empty + (it - 2) % ns);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (!ok) break;
             if (elect()) mma_commit(acc_full + buf);
@@ -198,10 +216,10 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                 atomicOr(p.status, TXL_STATUS_TIMEOUT);
                 *abort_flag = 1;
             }
-            if (elect()) mma_commit(acc_full + (tile & 1));
+            if (elect()) mma_commit(acc_full + tile % BUFS);
             __syncwarp();
             const int zero = 0;
-            mbar_wait(acc_full + (tile & 1), (tile >> 1) & 1, &zero, wait_ns);
+            mbar_wait(acc_full + tile % BUFS, (tile / BUFS) & 1, &zero, wait_ns);
         }
     } else if (warp >= 4) {
         constexpr unsigned FULL = 0xffffffffu;
@@ -221,8 +239,8 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
         bool ok = true;
         int tile = 0;
         for (int t = t_lo; t < t_hi; ++t, ++tile) {
-            const int buf = tile & 1;
-            ok = __all_sync(FULL, mbar_wait(acc_full + buf, (tile >> 1) & 1, abort_flag, wait_ns) && !*abort_flag);
+            const int buf = tile % BUFS;
+            ok = __all_sync(FULL, mbar_wait(acc_full + buf, (tile / BUFS) & 1, abort_flag, wait_ns) && !*abort_flag);
             // (all warps of the epilogue meet at its barriers: they leave together)
             if (epi_any(!ok)) {
                 ok = false;
@@ -238,6 +256,14 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                     uint32_t raw[32];
                     tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * ACC + c, raw);
                     tmem_ld_wait(raw);
+                    if (THREE) {
+                        uint32_t rest[32];
+                        tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * ACC + REST + c, rest);
+                        tmem_ld_wait(rest);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            raw[i] = __float_as_uint(__uint_as_float(raw[i]) + __uint_as_float(rest[i]));
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         turn[(half * 32 + i) * TURN_LD + quarter * 32 + lane] = __uint_as_float(raw[i]);
@@ -323,7 +349,7 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
     }
 }
 
-template <int GROUPS>
+template <int GROUPS, bool THREE>
 cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmParams &p, cudaStream_t s)
 {
     static bool attr_set[64] = {};  // the attribute is set once per device
@@ -331,13 +357,13 @@ cudaError_t launch(const CUtensorMap &tm_w, const CUtensorMap &tm_h, const GemmP
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(logprob_few_kernel<GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(logprob_few_kernel<GROUPS, THREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SMEM_BYTES);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const int ns = min(MAX_NS, RING / (A_BYTES + p.bn * BK * 2));
-    return launch_grid(logprob_few_kernel<GROUPS>, dim3((unsigned)p.splits), (4 + kEpiWarps) * 32, SMEM_BYTES, s, 1,
+    return launch_grid(logprob_few_kernel<GROUPS, THREE>, dim3((unsigned)p.splits), (4 + kEpiWarps) * 32, SMEM_BYTES, s, 1,
                        tm_w, tm_h, p, ns);
 }
 
@@ -347,8 +373,10 @@ cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h,
                                cudaStream_t s)
 {
     const int groups = (p.M + 63) / 64;
-    if (groups == 1) return launch<1>(tm_w, tm_h, p, s);
-    return groups == 2 ? launch<2>(tm_w, tm_h, p, s) : launch<4>(tm_w, tm_h, p, s);
+    const bool three = p.terms == 3;
+    if (groups == 1) return three ? launch<1, true>(tm_w, tm_h, p, s) : launch<1, false>(tm_w, tm_h, p, s);
+    if (groups == 2) return three ? launch<2, true>(tm_w, tm_h, p, s) : launch<2, false>(tm_w, tm_h, p, s);
+    return three ? launch<4, true>(tm_w, tm_h, p, s) : launch<4, false>(tm_w, tm_h, p, s);
 }
 
 } // namespace txl

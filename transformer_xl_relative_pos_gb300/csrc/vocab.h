@@ -135,7 +135,7 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// One GEMM over 256 x bn tiles, bf16 operands (a_pieces, b_pieces terms each), fp32 sums.
+// One GEMM over 256 x bn tiles (bn 128 with three terms), bf16 operands, fp32 sums.
 // Which operands, and what becomes of a tile, is the kernel's mode.
 struct GemmParams {
     int M, N;              // rows and columns of the product
@@ -143,9 +143,7 @@ struct GemmParams {
     int kb;                // 64-wide steps along the contraction
     int splits;            // statistics: ranges of the columns; products: of the contraction
     int n_items;
-    int n_pairs;           // products of terms: term (pair_a >> 4 i) & 15 of A by that of B
-    unsigned pair_a, pair_b;
-    int two_terms;         // products: A's terms 0 and 1 by B's one in the same step (n_pairs 1)
+    int terms;             // of the operands: 1; 2 (products: two of A by one of B); 3 (three of each)
     int b_row0;            // offset of B's rows (the vocabulary chunk's first)
     unsigned int *status;
     unsigned long long wait_ns;
@@ -176,7 +174,6 @@ struct GemmLaunch {
         CUtensorMap a, b, out;
     } maps[2];
     GemmParams p[2];
-    bool dual;             // room for two terms of A in a stage
 };
 
 cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s);

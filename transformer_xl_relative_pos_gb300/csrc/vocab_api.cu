@@ -104,26 +104,34 @@ constexpr double kItemCost = 1500.0;
 // The launch that sums parts, in cycles.
 constexpr double kSumLaunch = 4500.0;
 
-// Cycles of one 64-wide step: the MMAs' (256 columns: 512) or the copies' at some 58 bytes a cycle
-// and SM (602 cycles a step in the statistics of 2048 x 131072).
-double step_cycles(int bn) { return std::max(2.0 * bn, (16384.0 + 64.0 * bn) / 58.0); }
+// Cycles of one 64-wide step of `terms` (GemmParams): the MMAs' (one product, 256 columns: 512) or the
+// copies' at some 58 bytes a cycle and SM (602 cycles a step in the statistics of 2048 x 131072).
+double step_cycles(int bn, int terms)
+{
+    const int products = terms == 3 ? 6 : terms, a = terms, b = terms == 3 ? 3 : 1;
+    return std::max(2.0 * bn * products, (16384.0 * a + 64.0 * bn * b) / 58.0);
+}
+
+// Whether tiles of bn columns are a choice: 256 only past 128 columns, and not with three terms, whose
+// two accumulators take the room (nor would they gain: their steps are bound by the MMAs).
+bool columns_fit(int bn, long long cols, int terms) { return bn == 128 || (cols > 128 && terms < 3); }
 
 // `steps`: 64-wide steps of a tile; parts: up to `most` ranges of a row block's tiles (0: an item
 // a tile).
-Shape choose_shape(long long rows, long long cols, int steps, int most)
+Shape choose_shape(long long rows, long long cols, int steps, int terms, int most)
 {
     const int pairs = txl::device_sm_count() / 2;
     Shape best{};
     double least = 0.0;
     for (const int bn : {256, 128}) {
-        if (bn == 256 && cols <= 128) continue;
+        if (!columns_fit(bn, cols, terms)) continue;
         Shape s{bn, ceil_div(rows, 256), ceil_div(cols, bn), 1};
         const int n = std::max(1, std::min(most, s.nb));
         for (; s.parts <= n; ++s.parts) {
             const long long items = (long long)s.mb * (most ? s.parts : s.nb);
             const double waves = (double)((items + pairs - 1) / pairs);
             const double work = (double)steps * (most ? ceil_div(s.nb, s.parts) : 1);
-            const double cost = waves * (work * step_cycles(bn) + kItemCost);
+            const double cost = waves * (work * step_cycles(bn, terms) + kItemCost);
             if (best.mb == 0 || cost < least) {
                 best = s;
                 least = cost;
@@ -139,7 +147,7 @@ struct Two {
     Shape a, b;
 };
 
-Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&most)[2])
+Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&terms)[2])
 {
     static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16};
     const int pairs = txl::device_sm_count() / 2;
@@ -152,13 +160,13 @@ Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2]
     int n[2] = {};
     for (int i = 0; i < 2; ++i)
         for (const int bn : {256, 128}) {
-            if (bn == 256 && cols <= 128) continue;
+            if (!columns_fit(bn, cols, terms[i])) continue;
             for (const int parts : kParts) {
-                if (parts > most[i]) break;
+                if (parts > steps[i]) break;
                 Option &x = o[i][n[i]++];
                 x.s = {bn, ceil_div(rows[i], 256), ceil_div(cols, bn), parts};
                 x.items = (long long)x.s.mb * x.s.nb * parts;
-                x.cost = (double)ceil_div(steps[i], parts) * step_cycles(bn) + kItemCost;
+                x.cost = (double)ceil_div(steps[i], parts) * step_cycles(bn, terms[i]) + kItemCost;
                 x.extra = parts > 1 ? parts * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
             }
         }
@@ -190,7 +198,10 @@ struct StatsPlan {
 StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
 {
     StatsPlan s{};
-    s.few = N <= txl::kFewRows;
+    // (fp32 past 128 states has one accumulator at a time there, and less room for stages: 200 states,
+    // 5003 x 520, 39.8 us where the states in the tiles' rows take 29.0; with alternatives, whose lists
+    // cost those more, 48.6 and 49.7; 256 states, 32000 x 512: 94 and 93, 106 and 115)
+    s.few = N <= txl::kFewRows && !(dtype == TXL_F32 && N > 128 && top == 0);
     if (s.few) {
         s.mb = 1;
         s.bn = std::max(16, ceil_div(N, 16) * 16);
@@ -201,8 +212,7 @@ StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
         s.full = top > 0 && (long long)N * 16 <= d && N <= 64;
         s.splits = std::min(s.nb, std::min(txl::device_sm_count(), txl::kMaxStatSplits));
     } else {
-        const int terms = dtype == TXL_F32 ? 6 : 1;
-        const Shape c = choose_shape(N, V, ceil_div(d, 64) * terms, txl::kMaxRowSplits);
+        const Shape c = choose_shape(N, V, ceil_div(d, 64), dtype == TXL_F32 ? 3 : 1, txl::kMaxRowSplits);
         s.mb = c.mb;
         s.bn = c.bn;
         s.nb = c.nb;
@@ -261,11 +271,9 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     g.chunks = ceil_div(V, g.chunk);
     g.g_ld = up128(g.chunk);
     g.g_plane = g.g_ld * N;
-    const int terms = dtype == TXL_F32 ? 6 : 1, terms_h = dtype == TXL_F32 ? 6 : g.pieces_h,
-              terms_w = dtype == TXL_F32 ? 6 : g.pieces;
-    g.g = choose_shape(N, g.chunk, ceil_div(d, 64) * terms, 0);
+    g.g = choose_shape(N, g.chunk, ceil_div(d, 64), dtype == TXL_F32 ? 3 : 1, 0);
     const int kb_h = ceil_div(g.chunk, 64), kb_w = ceil_div(N, 64);
-    const Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h * terms_h, kb_w * terms_w}, {kb_h, kb_w});
+    const Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, kb_w}, {g.pieces_h, g.pieces});
     g.h = two.a;
     g.w = two.b;
     g.parts_h = g.chunks * g.h.parts;
@@ -302,24 +310,6 @@ GradPlan plan_grad(int N, int V, int d, int dtype, int grad_dtype)
         std::copy(key, key + 6, last.key);
     }
     return last.plan;
-}
-
-// Products of terms of two operands with pa and pb bf16 terms, the smallest first.
-void set_pairs(GemmParams &p, int pa, int pb)
-{
-    p.n_pairs = 0;
-    if (pa == 2 && pb == 1) {
-        p.n_pairs = 1;
-        p.two_terms = 1;
-        return;
-    }
-    static constexpr int order[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
-    for (const auto &o : order)
-        if (o[0] < pa && o[1] < pb) {
-            p.pair_a |= (unsigned)o[0] << (4 * p.n_pairs);
-            p.pair_b |= (unsigned)o[1] << (4 * p.n_pairs);
-            ++p.n_pairs;
-        }
 }
 
 // (a lone row may come with any stride: its own width then)
@@ -493,7 +483,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.kb = ceil_div(d, 64);
     p.splits = s.splits;
     p.n_items = s.mb * s.splits;
-    set_pairs(p, oh.planes, ow.planes);
+    p.terms = oh.planes;
     p.status = status;
     p.wait_ns = txl::wait_limit_ns();
     p.targets = targets;
@@ -643,7 +633,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         p.splits = 1;
         p.n_items = p.mb * p.nb;
         p.b_row0 = v0;
-        set_pairs(p, oh.planes, ow.planes);
+        p.terms = oh.planes;
         if (!map_of(&grad.maps[0].out, og, N, cols, 32) || !map_of(&prod.maps[0].a, og, N, cols, 128))
             return TXL_ERR_CUDA;
         if (txl::launch_logprob_grad(grad, st) != cudaSuccess) return TXL_ERR_CUDA;
@@ -662,7 +652,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.b_row0 = v0;
             q.part = g.parts_h > 1;
             q.out_bf16 = dtype == TXL_BF16;
-            set_pairs(q, g.pieces_h, ow.planes);
+            q.terms = g.pieces_h;
             if (!map_out(&prod.maps[0].out, q,
                          q.part ? ws + g.part_h + (size_t)c * g.h.parts * N * d * 4 : (char *)dh))
                 return TXL_ERR_CUDA;
@@ -683,7 +673,7 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.n_items = q.mb * q.nb * q.splits;
             q.part = g.w.parts > 1;
             q.out_bf16 = grad_dtype == TXL_BF16;
-            set_pairs(q, g.pieces, oh.planes);
+            q.terms = g.pieces;
             if (!map_of(&prod.maps[1].a, og, N, cols, 64) ||
                 !map_out(&prod.maps[1].out, q, q.part ? ws + g.part_w : rows))
                 return TXL_ERR_CUDA;
@@ -691,7 +681,6 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
                 sums[1] = {reinterpret_cast<float *>(ws + g.part_w), rows, (long long)cols * d, g.w.parts,
                            grad_dtype == TXL_BF16};
         }
-        prod.dual = prod.p[0].two_terms || prod.p[1].two_terms;
         if (txl::launch_products(prod, st) != cudaSuccess) return TXL_ERR_CUDA;
         if (txl::launch_sum_parts(sums, st) != cudaSuccess) return TXL_ERR_CUDA;
     }
