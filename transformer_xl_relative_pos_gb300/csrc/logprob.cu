@@ -91,6 +91,31 @@ struct Item {
     }
 };
 
+// The items of one pair in turn: every pairs-th of the first product, then of the second; pairs that
+// have one less of the first take `early` of the second before all share the rest.
+template <Mode MODE>
+struct Turn {
+    int pair, pairs, n0, n1, own0, fewer, early;
+
+    __device__ __forceinline__ Turn(const GemmLaunch &g, int pair_, int pairs_) : pair(pair_), pairs(pairs_)
+    {
+        n0 = g.p[0].n_items;
+        n1 = MODE == kProducts ? g.p[1].n_items : 0;
+        own0 = (n0 - pair + pairs - 1) / pairs;  // (n0 >= 0 and pair < pairs: not negative)
+        fewer = pairs - n0 % pairs;
+        early = MODE == kProducts && pair >= n0 % pairs ? g.early : 0;
+    }
+    // Item k of the pair, or -1 behind its last.
+    __device__ __forceinline__ int item(const GemmLaunch &g, int k) const
+    {
+        if (k < own0) return pair + k * pairs;
+        if (MODE != kProducts) return -1;
+        k -= own0;
+        const int at = k < early ? pair - (pairs - fewer) + k * fewer : g.early * fewer + pair + (k - early) * pairs;
+        return at < n1 ? n0 + at : -1;
+    }
+};
+
 // What a thread keeps of its row while it walks over the vocabulary (log2 units).
 template <int LIST>
 struct RowStats {
@@ -200,14 +225,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool dual = MODE == kProducts && !THREE && (g.p[0].terms == 2 || g.p[1].terms == 2);
     const int off_b = dual ? 2 * A_BYTES : A_BYTES;
     const int stage = off_b + (THREE ? B_BYTES / 2 : B_BYTES), ns = RING / stage;
-    const int n_items = g.p[0].n_items + (MODE == kProducts ? g.p[1].n_items : 0);
     unsigned int *status = g.p[0].status;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const Turn<MODE> turn(g, blockIdx.x / 2, gridDim.x / 2);
 
     // full (counted on block 0), empty, accumulators full and empty (block 0)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
@@ -253,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             int it = 0, s = 0;  // stages filled; the next one
             uint32_t phase = 1;
-            for (int item = pair; item < n_items && ok; item += pairs) {
+            for (int k = 0, item; ok && (item = turn.item(g, k)) >= 0; ++k) {
                 const Item<MODE> i(g, item);
                 const GemmParams &p = g.p[i.side];
                 // (in registers: the loop below issues a step's copies in a few hundred cycles, and reads
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int s = 0, tile = 0;
         uint32_t phase = 0;
-        for (int item = pair; item < n_items && ok && rank == 0; item += pairs) {
+        for (int turns = 0, item; ok && rank == 0 && (item = turn.item(g, turns)) >= 0; ++turns) {
             const Item<MODE> i(g, item);
             const GemmParams &p = g.p[i.side];
             const bool a_mn = MODE == kProducts && i.side;
@@ -452,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true;
         int tile = 0;
-        for (int item = pair; item < n_items && ok; item += pairs) {
+        for (int k = 0, item; ok && (item = turn.item(g, k)) >= 0; ++k) {
             const Item<MODE> it(g, item);
             const GemmParams &p = g.p[it.side];
             tm_out = &g.maps[it.side].out;

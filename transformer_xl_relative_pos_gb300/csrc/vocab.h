@@ -174,6 +174,7 @@ struct GemmLaunch {
         CUtensorMap a, b, out;
     } maps[2];
     GemmParams p[2];
+    int early;             // products: items of the second that pairs with fewer of the first begin with
 };
 
 cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s);

@@ -101,6 +101,12 @@ struct Shape {
 // but its accumulator's first use and its stores do not quite.
 constexpr double kItemCost = 1500.0;
 
+// Steps of a part of a product of fp32 operands, at most (of up to 16 parts): the accumulators' cut
+// additions are made good on average only, and a longer chain leaves more of them.  dh of 2048 x 32000 x
+// 512, relative to its norm, in parts of 500 steps 9.5e-6, of 125 6.7e-6, of 63 1.6e-6, of 32 1.3e-6 (the
+// whole gradient 673, 682, 689 and 701 us; fp32 library products 4.5e-6).
+constexpr int kMaxChain = 64;
+
 // The launch that sums parts, in cycles.
 constexpr double kSumLaunch = 4500.0;
 
@@ -141,8 +147,34 @@ Shape choose_shape(long long rows, long long cols, int steps, int terms, int mos
     return best;
 }
 
-// The tiles and parts of two products that share a launch: the items of the second follow those of
-// the first over the pairs in turn.
+double item_cycles(int steps, int bn, int terms) { return (double)steps * step_cycles(bn, terms) + kItemCost; }
+
+// Two products share a launch: the items of the first over the pairs in turn, then those of the
+// second, of which the pairs that have one less of the first begin with `early`.  The cycles of the
+// longest pair, and the best `early`.  (Without it the gradient of 2048 x 32000 x 1024 has pairs of 474
+// steps where the mean is 421; with it 442.)
+struct Turns {
+    int early;
+    double cycles;
+};
+
+Turns take_turns(long long n0, double c0, long long n1, double c1)
+{
+    const long long pairs = std::min<long long>(n0 + n1, txl::device_sm_count() / 2);
+    const long long more = n0 % pairs, fewer = pairs - more, k = n0 / pairs;
+    // (an item of the first is worth about c0 / c1 of the second)
+    const long long about = more ? (long long)(c0 / c1) : 0, most = more ? std::min(n1 / fewer, about + 1) : 0;
+    Turns best{0, 0.0};
+    for (long long e = std::max(0LL, std::min(most, about - 1)); e <= most; ++e) {
+        const long long rest = n1 - e * fewer, f = rest / pairs, x = rest % pairs;
+        const double a = more ? (double)(k + 1) * c0 + (double)(f + (x > 0)) * c1 : 0.0,
+                     b = (double)k * c0 + (double)(e + f + (x > more)) * c1, cycles = std::max(a, b);
+        if (best.cycles == 0.0 || cycles < best.cycles) best = {(int)e, cycles};
+    }
+    return best;
+}
+
+// The tiles and parts of two products that share a launch.
 struct Two {
     Shape a, b;
 };
@@ -150,7 +182,6 @@ struct Two {
 Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&terms)[2])
 {
     static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16};
-    const int pairs = txl::device_sm_count() / 2;
     struct Option {
         Shape s;
         long long items;
@@ -163,10 +194,11 @@ Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2]
             if (!columns_fit(bn, cols, terms[i])) continue;
             for (const int parts : kParts) {
                 if (parts > steps[i]) break;
+                if (terms[i] == 3 && parts < std::min(16, ceil_div(steps[i], kMaxChain))) continue;
                 Option &x = o[i][n[i]++];
                 x.s = {bn, ceil_div(rows[i], 256), ceil_div(cols, bn), parts};
                 x.items = (long long)x.s.mb * x.s.nb * parts;
-                x.cost = (double)ceil_div(steps[i], parts) * step_cycles(bn, terms[i]) + kItemCost;
+                x.cost = item_cycles(ceil_div(steps[i], parts), bn, terms[i]);
                 x.extra = parts > 1 ? parts * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
             }
         }
@@ -175,10 +207,7 @@ Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2]
     for (int i = 0; i < n[0]; ++i)
         for (int j = 0; j < n[1]; ++j) {
             const Option &x = o[0][i], &y = o[1][j];
-            const long long rx = x.items % pairs, ry = y.items % pairs;
-            const double lx = rx ? x.cost : 0.0, ly = ry ? y.cost : 0.0;
-            const double cost = (double)(x.items / pairs) * x.cost + (double)(y.items / pairs) * y.cost +
-                                (rx + ry > pairs ? lx + ly : std::max(lx, ly)) + x.extra + y.extra +
+            const double cost = take_turns(x.items, x.cost, y.items, y.cost).cycles + x.extra + y.extra +
                                 (x.s.parts > 1 || y.s.parts > 1 ? kSumLaunch : 0.0);
             if (best.a.mb == 0 || cost < least) {
                 best = {x.s, y.s};
@@ -681,6 +710,11 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
                 sums[1] = {reinterpret_cast<float *>(ws + g.part_w), rows, (long long)cols * d, g.w.parts,
                            grad_dtype == TXL_BF16};
         }
+        const GemmParams &q0 = prod.p[0], &q1 = prod.p[1];
+        prod.early = 0;
+        if (dh && dw)
+            prod.early = take_turns(q0.n_items, item_cycles(ceil_div(q0.kb, q0.splits), q0.bn, q0.terms), q1.n_items,
+                                    item_cycles(ceil_div(q1.kb, q1.splits), q1.bn, q1.terms)).early;
         if (txl::launch_products(prod, st) != cudaSuccess) return TXL_ERR_CUDA;
         if (txl::launch_sum_parts(sums, st) != cudaSuccess) return TXL_ERR_CUDA;
     }
