@@ -57,6 +57,8 @@ def _check_fwd(res, ref, top):
 # alternatives as the vocabulary has
 FWD = [(1, 1, 8, 1, 1.0), (1, 5000, 512, 8, 1.0), (3, 16, 24, 16, -0.7), (17, 204, 512, 5, 1.0),
        (130, 333, 72, 3, 0.5), (129, 2049, 200, 16, 1.3), (256, 700, 64, 2, 1.0), (64, 9001, 128, 9, 1.0),
+       # without alternatives: either form, by the vocabulary
+       (100, 700, 40, 0, 1.0), (200, 1000, 64, 0, -0.8), (256, 20001, 64, 0, 1.0), (65, 128, 512, 0, 2.0),
        # more than 256 rows: the rows in the tiles' rows
        (300, 1000, 64, 0, 1.0), (300, 333, 72, 3, -0.5), (257, 5, 16, 16, 1.0), (700, 2049, 200, 16, 1.3),
        (515, 9001, 128, 9, 1.0), (1000, 130, 520, 8, 0.0), (400, 40000, 24, 1, 1.0)]

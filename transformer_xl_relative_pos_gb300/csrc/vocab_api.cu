@@ -227,10 +227,14 @@ struct StatsPlan {
 StatsPlan plan_stats(int N, int V, int d, int dtype, int top)
 {
     StatsPlan s{};
-    // (fp32 past 128 states has one accumulator at a time there, and less room for stages: 200 states,
-    // 5003 x 520, 39.8 us where the states in the tiles' rows take 29.0; with alternatives, whose lists
-    // cost those more, 48.6 and 49.7; 256 states, 32000 x 512: 94 and 93, 106 and 115)
-    s.few = N <= txl::kFewRows && !(dtype == TXL_F32 && N > 128 && top == 0);
+    // Up to kFewRows states the vocabulary takes the tiles' rows: the table is read at DRAM's rate, and
+    // alternatives need no lists (4 of them, 32000 x 1024 in bf16: 64, 128, 256 states 21.2, 24.2, 35.8 us;
+    // with the states in the tiles' rows 60 each).  Without alternatives the other way is no slower where
+    // the vocabulary leaves SMs without a tile: 5003 x 256, 64, 96, 160, 256 states 7.0, 8.4, 12.0, 13.9 us
+    // and 8.2, 8.1, 8.5, 8.5; but 131072 x 512, 160 and 256 states 43 and 53, and 61; 32000 x 1024 23.4 and
+    // 25.7, and 24.7.  In fp32 (5003 x 520) from 129 states on: 29.7 us and 28.4, 200 states 39.8 and 29.0.
+    const bool idle = ceil_div(V, 128) < txl::device_sm_count();
+    s.few = N <= txl::kFewRows && !(top == 0 && idle && N > (dtype == TXL_F32 ? 128 : 64));
     if (s.few) {
         s.mb = 1;
         s.bn = std::max(16, ceil_div(N, 16) * 16);
