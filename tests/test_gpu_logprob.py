@@ -226,7 +226,9 @@ def _check_grads(got, ref, N, V, dtype, dw_dtype, dlogp, dent, lse, ent):
 
 
 BWD = [(1, 1, 8, 1.0), (5, 204, 512, 1.0), (130, 333, 72, -0.5), (129, 2049, 200, 1.3),
-       (700, 100, 264, 1.0), (33, 5003, 64, 0.7), (257, 7000, 640, 1.0)]
+       (700, 100, 264, 1.0), (33, 5003, 64, 0.7), (257, 7000, 640, 1.0),
+       # few rows over many words: both terms of G apart, sums of many parts
+       (5, 9001, 200, 1.0), (100, 9001, 72, -0.8), (127, 30001, 264, 1.0)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "bf16_f32", "f32"])
@@ -320,6 +322,41 @@ def test_logprob_bwd_in_vocabulary_chunks():
     assert bool(((dh[some].cpu().double() - part.cpu().double()).abs() <= tol).all())
     tol = (model.BF16_HALF + N * model.F32_CUT + 1e-4) * size + model.BF16_HALF * want.abs()
     assert bool(((dw[59000:59200].double() - want).abs() <= tol).all())
+
+
+def test_logprob_bwd_of_few_rows_in_vocabulary_chunks():
+    # G of all logits, a pair, is past the workspace's limit
+    N, V, d = 128, 2200000, 8
+    g = torch.Generator(device=dev()).manual_seed(4)
+    h = torch.randn(N, d, generator=g, device=dev()).to(BF)
+    w = torch.randn(V, d, generator=g, device=dev()).to(BF) * 0.5
+    t = torch.randint(0, V, (N,), generator=g, device=dev())
+    t[::5] = -1
+    assert txl.logprob_bwd_workspace_size(N, V, d) < 4 * N * V
+    lse = txl.logprob_fwd(h, w, t).lse
+    dlogp = torch.randn(N, generator=g, device=dev())
+    dh, dw = txl.logprob_bwd(h, w, t, lse, dlogp)
+    _ok()
+    live = (t >= 0).double() * dlogp.double()
+    want_h, size = torch.zeros(N, d, dtype=torch.float64, device=dev()), torch.zeros(N, d, dtype=torch.float64, device=dev())
+    lse64 = torch.logsumexp(torch.cat([torch.logsumexp(h.double() @ w[i:i + 275000].double().t(), 1, keepdim=True)
+                                       for i in range(0, V, 275000)], 1), 1)
+    for i in range(0, V, 275000):
+        W = w[i:i + 275000].double()
+        G = -live[:, None] * torch.exp(h.double() @ W.t() - lse64[:, None])
+        at = t - i
+        here = (at >= 0) & (at < 275000) & (t >= 0)
+        G[here, at[here]] += live[here]
+        want_h += G @ W
+        size += G.abs() @ W.abs()
+        # G a pair (2^-16), its logits' sums of 8 and the log-sum-exp's error (V 2^-23 at most, of its terms),
+        # sums of N; one rounding of the result
+        tol = (2.0 ** -16 + V * model.F32_CUT + N * model.F32_CUT) * (G.abs().t() @ h.double().abs())
+        got = dw[i:i + 275000].double()
+        want = G.t() @ h.double()
+        assert bool(((got - want).abs() <= tol + model.BF16_HALF * want.abs() + 1e-30).all())
+    tol = (2.0 ** -16 + 2 * V * model.F32_CUT) * size + model.BF16_HALF * want_h.abs() + 1e-30
+    assert bool(((dh.double() - want_h).abs() <= tol).all())
 
 
 def test_logprob_bwd_against_differences():

@@ -15,7 +15,9 @@
 //            ranges.
 //   kGrad    h W^T again; a tile becomes G, as bf16 terms in the workspace
 //   kProducts  dh = G W and dW = G^T h, the tiles of both in one launch
-// Where G is a bf16 pair, a stage holds both terms beside one tile of the other operand.
+// Where G is a bf16 pair, a stage holds both terms beside one tile of the other operand, or (few rows) the
+// pair's blocks take one term each in dh, and dW the terms in steps of their own: less room a stage, and half
+// the MMAs of dh (the gradient of 64 x 32000 x 1024 60 us, 70 with both terms in each stage).
 // fp32 operands are three bf16 terms each (their leading 24 bits); a product of two
 // such operands is the six products of terms whose weight is above 2^-24.  A step of them loads
 // each term once, three stages for six products (where every product had its own two tiles, the
@@ -219,6 +221,8 @@ template <Mode MODE, int LIST, bool THREE>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ GemmLaunch g)
 {
+    // (products have no list: LIST 1 is their form for few rows, with GemmParams' stacked and twice)
+    constexpr bool FEW = MODE == kProducts && LIST > 0;
     // (dW's A operand, G^T, is MN-major; both products' B operand is)
     constexpr bool B_MN = MODE == kProducts;
     // stages of the ring: A's rows (two terms of them, if a product has them), then B's columns
@@ -286,26 +290,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int bn = p.bn, own_bn = bn / 2;  // columns of B in this block
                 const int b_row0 = p.b_row0;
                 const bool two = !THREE && p.terms == 2;
-                const uint32_t stage_tx = (uint32_t)((two ? 2 : 1) * A_BYTES + own_bn * BK * 2) * 2;
-                const bool a_mn = MODE == kProducts && i.side;
+                const bool a_mn = MODE == kProducts && i.side, stacked = FEW && p.stacked;
+                const int twice = FEW ? p.twice : 0;
+                // (whole boxes in the products of many rows: the copies' rate is their bound, and what this would
+                // ask of it takes 5 us of 166 there)
+                constexpr bool WHOLE = MODE == kProducts && !FEW;
+                const uint32_t a_tx = (two ? 2 : 1) * (WHOLE || a_mn ? A_BYTES : p.a_rows * BK * 2), b_tx = own_bn * BK * 2;
+                const int M = p.M;
                 const int nt = i.tiles(p);
                 for (int t = 0; t < nt && ok; ++t) {
                     const Tile w = i.tile(p, t);
-                    const int m0 = (w.m * 2 + rank) * BM, n0 = w.n * bn + rank * own_bn;
-                    for (int kb = w.kb_lo; kb < w.kb_hi && ok; ++kb) {
+                    const int m0 = stacked ? 0 : (w.m * 2 + rank) * BM, n0 = w.n * bn + rank * own_bn;
+                    // (rows behind the last are not loaded: what they multiply is not stored)
+                    const bool load_a = WHOLE || m0 < M;
+                    const uint32_t stage_tx = (WHOLE || stacked || (w.m * 2 + 1) * BM < M ? 2 : 1) * a_tx + 2 * b_tx;
+                    const int plane0 = stacked ? rank : 0;
+                    for (int k = w.kb_lo << twice; k < w.kb_hi << twice && ok; ++k) {
+                        const int kb = k >> twice, plane = plane0 + (k & twice);
                         for (int term = 0; term < (THREE ? 3 : 1); ++term) {
                             if (!(ok = mbar_wait(empty + s, phase, abort_flag, wait_ns))) break;
                             uint8_t *st = smem + s * stage;
                             if (rank == 0) mbar_arrive_expect_tx(full + s, stage_tx);
                             const uint32_t bar = full0 + s * 8;
-                            for (int t = 0; t < (MODE == kProducts && two ? 2 : 1); ++t) {
+                            for (int t = 0; t < (MODE == kProducts && two ? 2 : 1) && load_a; ++t) {
                                 if (a_mn) {
 #pragma unroll
                                     for (int x = 0; x < BM / 64; ++x)
                                         tma_load_3d_pair(st + t * A_BYTES + x * SLAB, tm_a, bar, m0 + x * 64, kb * BK,
-                                                         term + t);
+                                                         plane + term + t);
                                 } else {
-                                    tma_load_3d_pair(st + t * A_BYTES, tm_a, bar, kb * BK, m0, term + t);
+                                    tma_load_3d_pair(st + t * A_BYTES, tm_a, bar, kb * BK, m0, plane + term + t);
                                 }
                             }
                             if (B_MN) {
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nt = i.tiles(p);
             for (int t = 0; t < nt && ok; ++t) {
                 const Tile w = i.tile(p, t);
-                const int steps = w.kb_hi - w.kb_lo;
+                const int steps = (w.kb_hi - w.kb_lo) << (FEW ? p.twice : 0);
                 const int buf = tile & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((tile >> 1) & 1) ^ 1, abort_flag, wait_ns));
                 if (!ok) break;
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const int m0 = (w.m * 2 + rank) * BM, n0 = w.n * p.bn;
+                const int m0 = FEW && p.stacked ? 0 : (w.m * 2 + rank) * BM, n0 = w.n * p.bn;
                 // (a warp whose rows lie behind the last has nothing to do)
                 const int c_lo = half * (p.bn / 2),
                           c_hi = m0 + wq * 32 < p.M ? min((half + 1) * (p.bn / 2), p.N - n0) : 0;
@@ -583,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else if (p.part || !p.out_bf16) {
-                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16) * (!THREE && p.terms == 2 ? 2 : 1));
+                    const float f = empty_part ? 0.f : uncut_scale((w.kb_hi - w.kb_lo) * (BK / 16) * ((!THREE && p.terms == 2) || (FEW && p.twice) ? 2 : 1));
 #pragma unroll 1
                     for (int c = c_lo; c < c_hi; c += 32) {
                         uint32_t raw[32];
@@ -592,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             (&o[i >> 2].x)[i & 3] = empty_part ? 0u : __float_as_uint(__uint_as_float(raw[i]) * f);
-                        store(o, n0 + c, m0, p.part ? it.at / (p.mb * p.nb) : 0);
+                        const int part = p.part ? it.at / (p.mb * p.nb) : 0;
+                        store(o, n0 + c, m0, FEW && p.stacked ? 2 * part + rank : part);
                     }
                 } else {
 #pragma unroll 1
@@ -680,6 +695,10 @@ cudaError_t launch_logprob_stats(const GemmLaunch &g, int list, cudaStream_t s)
 
 cudaError_t launch_logprob_grad(const GemmLaunch &g, cudaStream_t s) { return launch_gemm<kGrad, 0>(g, s); }
 
-cudaError_t launch_products(const GemmLaunch &g, cudaStream_t s) { return launch_gemm<kProducts, 0>(g, s); }
+cudaError_t launch_products(const GemmLaunch &g, cudaStream_t s)
+{
+    if (g.p[0].stacked || g.p[1].twice) return launch_gemm_of<kProducts, 1, false>(g, s);
+    return launch_gemm<kProducts, 0>(g, s);
+}
 
 } // namespace txl

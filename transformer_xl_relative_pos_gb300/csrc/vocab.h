@@ -144,6 +144,10 @@ struct GemmParams {
     int splits;            // statistics: ranges of the columns; products: of the contraction
     int n_items;
     int terms;             // of the operands: 1; 2 (products: two of A by one of B); 3 (three of each)
+    int twice;             // dW of few rows: both terms of G in steps of their own (terms 1), or 0
+    int a_rows;            // of A's boxes: less than 128 where M is, in the logits and in stacked products
+    int stacked;           // dh, M <= 128: a pair's blocks take a term of A each, the same rows and columns; their
+                           // sums are two parts
     int b_row0;            // offset of B's rows (the vocabulary chunk's first)
     unsigned int *status;
     unsigned long long wait_ns;
@@ -162,7 +166,7 @@ struct GemmParams {
     const float *target_logp;
     int g_pieces;          // terms of G
     // products
-    int part;              // fp32 parts [splits][M][N], or the result directly
+    int part;              // fp32 parts [splits][M][N] (stacked: twice as many), or the result directly
     int out_bf16;
 };
 

@@ -110,13 +110,21 @@ constexpr int kMaxChain = 64;
 // The launch that sums parts, in cycles.
 constexpr double kSumLaunch = 4500.0;
 
+// A cold step's latency, in cycles: over the ring's six stages, or four with two terms each, it is the least
+// that a step takes (29 x 56301 x 224, dh by 16 pairs with four stages: 760 cycles a step).
+constexpr double kColdStep = 3000.0;
+
 // Cycles of one 64-wide step of `terms` (GemmParams): the MMAs' (one product, 256 columns: 512) or the
 // copies' at some 58 bytes a cycle and SM (602 cycles a step in the statistics of 2048 x 131072).
-double step_cycles(int bn, int terms)
+double step_cycles(int bn, int terms, int a_rows = 128)
 {
     const int products = terms == 3 ? 6 : terms, a = terms, b = terms == 3 ? 3 : 1;
-    return std::max(2.0 * bn * products, (16384.0 * a + 64.0 * bn * b) / 58.0);
+    return std::max({2.0 * bn * products, (128.0 * a_rows * a + 64.0 * bn * b) / 58.0,
+                     kColdStep / (terms == 2 ? 4 : 6)});
 }
+
+// Rows of A's boxes.
+int box_rows(long long rows) { return rows < 128 ? (int)(rows + 7) / 8 * 8 : 128; }
 
 // Whether tiles of bn columns are a choice: 256 only past 128 columns, and not with three terms, whose
 // two accumulators take the room (nor would they gain: their steps are bound by the MMAs).
@@ -147,7 +155,10 @@ Shape choose_shape(long long rows, long long cols, int steps, int terms, int mos
     return best;
 }
 
-double item_cycles(int steps, int bn, int terms) { return (double)steps * step_cycles(bn, terms) + kItemCost; }
+double item_cycles(int steps, int bn, int terms, int a_rows = 128)
+{
+    return (double)steps * step_cycles(bn, terms, a_rows) + kItemCost;
+}
 
 // Two products share a launch: the items of the first over the pairs in turn, then those of the
 // second, of which the pairs that have one less of the first begin with `early`.  The cycles of the
@@ -177,29 +188,37 @@ Turns take_turns(long long n0, double c0, long long n1, double c1)
 // The tiles and parts of two products that share a launch.
 struct Two {
     Shape a, b;
+    double cycles;
 };
 
-Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&terms)[2])
+Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&terms)[2],
+               int planes)
 {
-    static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 15, 16, 19, 25, 32, 38, 50, 64, 76};
+    const int pairs = txl::device_sm_count() / 2;
     struct Option {
         Shape s;
         long long items;
         double cost, extra;  // cycles of an item, and of the parts' writes and reads (3.6 kB a cycle)
     };
-    Option o[2][16];
+    Option o[2][2 * (sizeof kParts / sizeof kParts[0])];
     int n[2] = {};
     for (int i = 0; i < 2; ++i)
         for (const int bn : {256, 128}) {
             if (!columns_fit(bn, cols, terms[i])) continue;
             for (const int parts : kParts) {
-                if (parts > steps[i]) break;
-                if (terms[i] == 3 && parts < std::min(16, ceil_div(steps[i], kMaxChain))) continue;
+                const int mb = ceil_div(rows[i], 256), nb = ceil_div(cols, bn);
+                const int least = terms[i] == 3 ? std::min(16, ceil_div(steps[i], kMaxChain)) : 1;
+                if (parts < least) continue;
+                // (four items a pair are as even as it needs)
+                if (parts > steps[i] || (parts > least && (long long)mb * nb * parts > 4 * pairs)) break;
                 Option &x = o[i][n[i]++];
-                x.s = {bn, ceil_div(rows[i], 256), ceil_div(cols, bn), parts};
+                x.s = {bn, mb, nb, parts};
                 x.items = (long long)x.s.mb * x.s.nb * parts;
-                x.cost = item_cycles(ceil_div(steps[i], parts), bn, terms[i]);
-                x.extra = parts > 1 ? parts * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
+                x.cost = item_cycles(ceil_div(steps[i], parts), bn, terms[i],
+                                     i == 0 && planes == 2 ? box_rows(rows[0]) : 128);
+                const int written = parts * (i ? 1 : planes);  // (planes: parts of dh that one of them leaves)
+                x.extra = written > 1 ? written * 2.0 * rows[i] * cols * 4 / 3600.0 : 0.0;
             }
         }
     Two best{};
@@ -208,9 +227,9 @@ Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2]
         for (int j = 0; j < n[1]; ++j) {
             const Option &x = o[0][i], &y = o[1][j];
             const double cost = take_turns(x.items, x.cost, y.items, y.cost).cycles + x.extra + y.extra +
-                                (x.s.parts > 1 || y.s.parts > 1 ? kSumLaunch : 0.0);
+                                (x.s.parts * planes > 1 || y.s.parts > 1 ? kSumLaunch : 0.0);
             if (best.a.mb == 0 || cost < least) {
-                best = {x.s, y.s};
+                best = {x.s, y.s, cost};
                 least = cost;
             }
         }
@@ -280,6 +299,7 @@ constexpr size_t kGradBytes = (size_t)1 << 30;  // of G in the workspace: vocabu
 struct GradPlan {
     int chunk, chunks;            // vocabulary rows at a time
     int pieces, pieces_h;         // terms of G, and those that dh takes
+    int stacked;                  // GemmParams, of dh
     Shape g, h, w;                // tiles of G, of dh, and of a chunk's dW
     int parts_h;                  // of dh, over all chunks
     long long g_ld, g_plane;
@@ -306,10 +326,16 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     g.g_plane = g.g_ld * N;
     g.g = choose_shape(N, g.chunk, ceil_div(d, 64), dtype == TXL_F32 ? 3 : 1, 0);
     const int kb_h = ceil_div(g.chunk, 64), kb_w = ceil_div(N, 64);
-    const Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, kb_w}, {g.pieces_h, g.pieces});
+    // (G a pair: its terms in the two blocks of a pair, which leaves parts to sum, or both in each)
+    Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, kb_w}, {g.pieces_h, g.pieces}, 1);
+    if (g.pieces_h == 2) {
+        const Two apart = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, 2 * kb_w}, {1, 1}, 2);
+        g.stacked = apart.cycles < two.cycles;
+        if (g.stacked) two = apart;
+    }
     g.h = two.a;
     g.w = two.b;
-    g.parts_h = g.chunks * g.h.parts;
+    g.parts_h = g.chunks * g.h.parts * (g.stacked ? 2 : 1);
     size_t o = 0;
     const size_t row = (size_t)line_ld(d) * 2 * txl::kMaxPieces;
     g.live = o;
@@ -376,8 +402,9 @@ bool map_of(CUtensorMap *map, const Operand &o, int rows, int d, unsigned box_ro
 bool map_out(CUtensorMap *map, const GemmParams &p, char *base)
 {
     const long long plane = (long long)p.M * p.N;
+    const int parts = p.part ? p.splits * (p.stacked ? 2 : 1) : 1;
     return p.part || !p.out_bf16
-               ? txl::make_map_planes_f32(map, base, p.N, p.M, p.N, p.part ? p.splits : 1, plane, 32)
+               ? txl::make_map_planes_f32(map, base, p.N, p.M, p.N, parts, plane, 32)
                : txl::make_map_planes(map, base, p.N, p.M, p.N, 1, plane, 32);
 }
 
@@ -517,6 +544,7 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
     p.splits = s.splits;
     p.n_items = s.mb * s.splits;
     p.terms = oh.planes;
+    p.a_rows = 128;
     p.status = status;
     p.wait_ns = txl::wait_limit_ns();
     p.targets = targets;
@@ -647,7 +675,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
     base.dentropy = dentropy;
     base.g_pieces = g.pieces;
     txl::GemmLaunch grad{}, prod{};
-    if (!map_of(&grad.maps[0].a, oh, N, d, 128) ||
+    const unsigned rows_box = (unsigned)box_rows(N);
+    if (!map_of(&grad.maps[0].a, oh, N, d, rows_box) ||
         !map_of(&grad.maps[0].b, ow, V, d, (unsigned)g.g.bn / 2) ||
         !map_of(&prod.maps[0].b, ow, V, d, 64) || !map_of(&prod.maps[1].b, oh, N, d, 64))
         return TXL_ERR_CUDA;
@@ -667,7 +696,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         p.n_items = p.mb * p.nb;
         p.b_row0 = v0;
         p.terms = oh.planes;
-        if (!map_of(&grad.maps[0].out, og, N, cols, 32) || !map_of(&prod.maps[0].a, og, N, cols, 128))
+        p.a_rows = box_rows(N);
+        if (!map_of(&grad.maps[0].out, og, N, cols, 32) || !map_of(&prod.maps[0].a, og, N, cols, g.stacked ? rows_box : 128))
             return TXL_ERR_CUDA;
         if (txl::launch_logprob_grad(grad, st) != cudaSuccess) return TXL_ERR_CUDA;
         prod.p[0] = prod.p[1] = base;
@@ -685,9 +715,11 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.b_row0 = v0;
             q.part = g.parts_h > 1;
             q.out_bf16 = dtype == TXL_BF16;
-            q.terms = g.pieces_h;
+            q.stacked = g.stacked;
+            q.terms = q.stacked ? 1 : g.pieces_h;
+            q.a_rows = q.stacked ? box_rows(N) : 128;
             if (!map_out(&prod.maps[0].out, q,
-                         q.part ? ws + g.part_h + (size_t)c * g.h.parts * N * d * 4 : (char *)dh))
+                         q.part ? ws + g.part_h + (size_t)c * (g.parts_h / g.chunks) * N * d * 4 : (char *)dh))
                 return TXL_ERR_CUDA;
             if (q.part && c + 1 == g.chunks)
                 sums[0] = {reinterpret_cast<float *>(ws + g.part_h), dh, (long long)N * d, g.parts_h,
@@ -706,7 +738,9 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.n_items = q.mb * q.nb * q.splits;
             q.part = g.w.parts > 1;
             q.out_bf16 = grad_dtype == TXL_BF16;
-            q.terms = g.pieces;
+            q.twice = g.stacked;
+            q.terms = g.stacked ? 1 : g.pieces;
+            q.a_rows = 128;
             if (!map_of(&prod.maps[1].a, og, N, cols, 64) ||
                 !map_out(&prod.maps[1].out, q, q.part ? ws + g.part_w : rows))
                 return TXL_ERR_CUDA;
@@ -717,8 +751,8 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
         const GemmParams &q0 = prod.p[0], &q1 = prod.p[1];
         prod.early = 0;
         if (dh && dw)
-            prod.early = take_turns(q0.n_items, item_cycles(ceil_div(q0.kb, q0.splits), q0.bn, q0.terms), q1.n_items,
-                                    item_cycles(ceil_div(q1.kb, q1.splits), q1.bn, q1.terms)).early;
+            prod.early = take_turns(q0.n_items, item_cycles(ceil_div(q0.kb, q0.splits), q0.bn, q0.terms, q0.a_rows), q1.n_items,
+                                    item_cycles(ceil_div(q1.kb << q1.twice, q1.splits), q1.bn, q1.terms)).early;
         if (txl::launch_products(prod, st) != cudaSuccess) return TXL_ERR_CUDA;
         if (txl::launch_sum_parts(sums, st) != cudaSuccess) return TXL_ERR_CUDA;
     }
