@@ -108,6 +108,28 @@ def test_logprob_order_beyond_single_precision(N, dtype):
     assert torch.equal(res.top_ids.cpu().long(), model.LogProb(h, w, None, 1.0, 6).top_ids)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,top", [(3, 0), (3, 8), (40, 8), (300, 0), (300, 8)])
+def test_logprob_of_nearly_certain_tokens(N, top, dtype):
+    # log p = -sum of the others' exp(z - z_t), here 1e-8 to 1e-4: a sum of the others and the 1 keeps a few
+    # units of 2^-24 of it.  The 1 enters once in its thread's sum (N <= 256: two tiles at most, so three
+    # additions that may round by 2^-24 each; else one for 32 columns of at most 3000 / 4: 24, of a random
+    # walk's 5 within six deviations 15 half units) and is rounded once more where the ranges are joined;
+    # the others are off by their logits' errors (2^-20 of the value at the sizes here).
+    V, d = 3000, 128
+    g = torch.Generator().manual_seed(40 + N)
+    w = (torch.randn(V, d, generator=g) * 0.2).to(dtype)
+    t = torch.randint(0, V, (N,), generator=g)
+    lift = torch.linspace(4.5, 6.5, N)[:, None]
+    h = (torch.randn(N, d, generator=g) * 0.3 + w[t].double() * lift).to(dtype)
+    res = txl.logprob_fwd(h.to(dev()), w.to(dev()), t.to(dev()), top=top)
+    _ok()
+    ref = model.LogProb(h, w, t, 1.0, 0)
+    assert float(ref.logp.max()) > -1e-6
+    units = 4 if N <= 256 else 16
+    _close(res.logp, ref.logp, units * 2.0 ** -24 + 2.0 ** -20 * ref.logp.abs() + ref.logp.abs() * ref.logp_off, "logp")
+
+
 @pytest.mark.parametrize("repeat", [1, 60])
 def test_logprob_infinite_logits(repeat):
     d, V = 64, 300

@@ -121,14 +121,14 @@ struct Turn {
 // What a thread keeps of its row while it walks over the vocabulary (log2 units).
 template <int LIST>
 struct RowStats {
-    float m, s, es, zt;
+    float m, s, lo, es, zt;   // the sum is s + lo
     float val[LIST > 0 ? LIST : 1];
     int id[LIST > 0 ? LIST : 1];
 
     __device__ __forceinline__ void clear()
     {
         m = -INFINITY;
-        s = es = zt = 0.f;
+        s = lo = es = zt = 0.f;
 #pragma unroll
         for (int j = 0; j < LIST; ++j) {
             val[j] = __int_as_float(0x7fffffff);  // NaN: an empty place, which any number takes
@@ -181,17 +181,24 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
         const float f = ex2(diff);
         r.es = (r.s > 0.f || r.s != r.s) ? (r.es + r.s * diff) * f : 0.f;
         r.s *= f;
+        r.lo *= f;
         r.m = m_new;
     }
-    float cs[2] = {0.f, 0.f}, ce[2] = {0.f, 0.f};
+    // (as a tree, and with its rounding kept: beside one term near 1 the others count)
+    float cs[4], ce[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float d = t[i] - mu, e = ex2(d);
-        cs[i & 1] += e;
-        // (a logit of -inf has weight zero)
-        ce[i & 1] = fmaf(e, fmaxf(d, -1e30f), ce[i & 1]);
+    for (int q = 0; q < 4; ++q) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = t[8 * q + i] - mu;
+            e[i] = ex2(d);
+            // (a logit of -inf has weight zero)
+            ce[i & 1] = fmaf(e[i], fmaxf(d, -1e30f), ce[i & 1]);
+        }
+        cs[q] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
     }
-    r.s += cs[0] + cs[1];
+    two_sum(r.s, r.lo, (cs[0] + cs[1]) + (cs[2] + cs[3]));
     r.es += ce[0] + ce[1];
     const int at = target - col0;
     if (__any_sync(0xffffffffu, (unsigned)at < (unsigned)cnt)) {
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = it.at / p.mb, m = ((it.at - s * p.mb) * 2 + rank) * BM + row;
                 if (m < p.M) {
                     const long long part = 2 * s + half;
-                    p.stats[part * p.M + m] = make_float4(r.m, r.s, r.es, r.zt);
+                    p.stats[part * p.M + m] = make_float4(r.m, r.s + r.lo, r.es, r.zt);
 #pragma unroll
                     for (int j = 0; j < LIST; ++j) {
                         const long long at = (part * LIST + j) * p.M + m;

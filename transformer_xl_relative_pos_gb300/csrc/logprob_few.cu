@@ -53,7 +53,7 @@ __device__ __forceinline__ bool epi_any(bool x)
     return r != 0;
 }
 
-// Statistics of eight states from 32 lanes' each ([maximum, sum, weighted sum][8][33] floats): lanes
+// Statistics (maximum, sum, weighted sum, the sum's low part) of eight states from 32 lanes' each ([maximum, sum, weighted sum][8][33] floats): lanes
 // 4 j .. 4 j + 3 join state j's.
 constexpr int kOwn = 3 * 8 * 33;
 static_assert(kEpiWarps * kOwn <= 64 * TURN_LD, "the warps' parts of the turning buffer");
@@ -68,19 +68,22 @@ __device__ __noinline__ float4 join_lanes(const float *own, int lane)
     top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
     top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
     const float mu = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, weighted = 0.f;
+    float sum = 0.f, lo = 0.f, weighted = 0.f;
 #pragma unroll 4
     for (int i = 0; i < 8; ++i) {
         // (before its first number a lane's maximum is -infinity and its sums are zero)
         const float d = fmaxf(m[i] - mu, -1e30f), f = ex2(d);
-        sum = fmaf(s[i], f, sum);
+        two_sum(sum, lo, s[i] * f);
         weighted = fmaf(fmaf(s[i], d, es[i]), f, weighted);
     }
-    sum += __shfl_xor_sync(FULL, sum, 1);
-    weighted += __shfl_xor_sync(FULL, weighted, 1);
-    sum += __shfl_xor_sync(FULL, sum, 2);
-    weighted += __shfl_xor_sync(FULL, weighted, 2);
-    return make_float4(top, sum, weighted, 0.f);
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+        const float hi = __shfl_xor_sync(FULL, sum, o), olo = __shfl_xor_sync(FULL, lo, o);
+        two_sum(sum, lo, hi);
+        lo += olo;
+        weighted += __shfl_xor_sync(FULL, weighted, o);
+    }
+    return make_float4(top, sum, weighted, lo);
 }
 
 // THREE: three terms of both operands.
@@ -289,15 +292,15 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                     const float mu = m_new == -INFINITY ? 0.f : m_new;
                     // (before the first number the maximum is -infinity and the sums are zero)
                     const float diff = fmaxf(m[k] - mu, -1e30f), f = ex2(diff);
-                    float s_new = sum[k] * f, e_new = fmaf(sum[k], diff, es[k]) * f;
+                    float e_new = fmaf(sum[k], diff, es[k]) * f, e4[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float d = v[i] - mu, e = ex2(d);
-                        s_new += e;
-                        e_new = fmaf(e, fmaxf(d, -1e30f), e_new);
+                        const float d = v[i] - mu;
+                        e4[i] = ex2(d);
+                        e_new = fmaf(e4[i], fmaxf(d, -1e30f), e_new);
                     }
                     m[k] = m_new;
-                    sum[k] = s_new;
+                    sum[k] = fmaf(sum[k], f, (e4[0] + e4[1]) + (e4[2] + e4[3]));
                     es[k] = e_new;
                     if (p.logits) {
                         const float none = __int_as_float(0x7fffffff);

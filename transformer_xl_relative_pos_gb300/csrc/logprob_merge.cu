@@ -17,14 +17,6 @@ struct Wide {
     float hi, lo;
 };
 
-// hi + lo + x, the sum of hi and x exactly (Knuth's two-sum).
-__device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
-{
-    const float s = __fadd_rn(hi, x), bb = __fadd_rn(s, -hi);
-    lo += (hi - (s - bb)) + (x - bb);
-    hi = s;
-}
-
 // h_i . w_j to about 2^-45 of its terms' size, over a warp: products split exactly (a bf16
 // product is an fp32 value; an fp32 one is a product and its rounding error by fma), sums
 // carried with their errors, four chains a lane.  Where that is no number, the plain sum.  (All in
@@ -106,15 +98,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // Softmax statistics of a row from its ranges', over a warp: lane s holds ranges s, s + 32, ...
 struct RowSums {
-    float m, mu, sum, es, zt;
+    float m, mu, sum, lo, es, zt;
 };
 
-template <int PER>
+// The sum is hi + lo: beside one term near 1 the others count, its logarithm is theirs.  FEW: the ranges'
+// sums come as pairs (their fourth place).
+template <int PER, bool FEW>
 __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int lane)
 {
     constexpr unsigned FULL = 0xffffffffu;
     float4 st[PER];
-    RowSums r{-INFINITY, 0.f, 0.f, 0.f, 0.f};
+    RowSums r{-INFINITY, 0.f, 0.f, 0.f, 0.f, 0.f};
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -122,7 +116,7 @@ __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int
         st[i] = s < p.splits ? p.stats[(long long)s * p.N + row] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         r.m = fmaxf(r.m, st[i].x);
         nan = nan || st[i].y != st[i].y;
-        r.zt += st[i].w;  // (zero but in the target's range)
+        if (!FEW) r.zt += st[i].w;  // (zero but in the target's range)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -134,12 +128,15 @@ __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int
     for (int i = 0; i < PER; ++i) {
         if (st[i].y == 0.f) continue;
         const float d = st[i].x - r.mu, f = exp2f(d);
-        r.sum += st[i].y * f;
+        two_sum(r.sum, r.lo, st[i].y * f);
+        if (FEW) r.lo = fmaf(st[i].w, f, r.lo);
         r.es += (st[i].z + st[i].y * d) * f;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        r.sum += __shfl_xor_sync(FULL, r.sum, o);
+        const float hi = __shfl_xor_sync(FULL, r.sum, o), lo = __shfl_xor_sync(FULL, r.lo, o);
+        two_sum(r.sum, r.lo, hi);
+        r.lo += lo;
         r.es += __shfl_xor_sync(FULL, r.es, o);
     }
     if (__any_sync(FULL, nan)) r.sum = __int_as_float(0x7fffffff);
@@ -156,10 +153,10 @@ __device__ __forceinline__ float above(const MergeParams &p, Wide z, float mu)
 // are a few such terms, are as exact as these.
 __device__ __forceinline__ void replace_term(float mu, float was, float d1, float &ds, float &de)
 {
-    const float d0 = was - mu;
-    const float e0 = ex2(d0), e1 = exp2f(d1);
-    ds = e1 - e0;
-    de = e1 * d1 - e0 * d0;
+    // (as a multiple of the term that was there: of two numbers near 1 the difference would be a rounding)
+    const float d0 = was - mu, e0 = ex2(d0);
+    ds = e0 * expm1f((d1 - d0) * kLn2);
+    de = fmaf(ds, d1, e0 * (d1 - d0));
 }
 
 // Row outputs from the sums; d_target: the target's logit above mu (log2 units).  Returns
@@ -167,7 +164,8 @@ __device__ __forceinline__ void replace_term(float mu, float was, float d1, floa
 __device__ __forceinline__ float row_outputs(const MergeParams &p, int row, const RowSums &r, int target,
                                              float d_target, bool write)
 {
-    const float l = logf(r.sum);
+    float l = logf(r.sum);
+    if (isfinite(l)) l += r.lo / r.sum;
     if (write) {
         if (p.logp) p.logp[row] = target >= 0 ? fmaf(d_target, kLn2, -l) : 0.f;
         // (ln 2 to fp64; a maximum of -infinity stands for itself)
@@ -242,7 +240,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
     }
     const int found = __popc(__ballot_sync(FULL, my_id >= 0));
     // exact logits of the candidates, and of the target where it is none of them
-    RowSums r = join_stats<PER>(p, row, lane);
+    RowSums r = join_stats<PER, false>(p, row, lane);
     float d_mine = my_val - r.mu, d_target = r.zt - r.mu;
     unsigned long long order = my_id >= 0 ? (unsigned long long)order_key(my_val) << 32 : 0ull;
     float ds = 0.f, de = 0.f;
@@ -277,7 +275,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
         ds += __shfl_xor_sync(FULL, ds, o);
         de += __shfl_xor_sync(FULL, de, o);
     }
-    r.sum += ds;
+    two_sum(r.sum, r.lo, ds);
     r.es += de;
     const float l = row_outputs(p, row, r, target, d_target, lane == 0);
     if (LIST == 0) return;
@@ -486,7 +484,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     }
     // the ranges' sums (last warp); exact logits, the target's first
     if (warp == kFewWarps - 1) {
-        const RowSums r = join_stats<kLaneLists>(p, row, lane);
+        const RowSums r = join_stats<kLaneLists, true>(p, row, lane);
         if (lane == 0) s_sums = r;
     }
     for (int c = warp; c <= jobs; c += kFewWarps) {
@@ -544,7 +542,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
             ds += __shfl_xor_sync(ALL, ds, o);
             de += __shfl_xor_sync(ALL, de, o);
         }
-        r.sum += ds;
+        two_sum(r.sum, r.lo, ds);
         r.es += de;
         l = row_outputs(p, row, r, target, d_target, lane == 0);
         if (!FULL && lane == 0) s_l = l;

@@ -135,6 +135,14 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// hi + lo + x, the sum of hi and x exactly (Knuth's two-sum).
+__device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
+{
+    const float s = __fadd_rn(hi, x), bb = __fadd_rn(s, -hi);
+    lo += (hi - (s - bb)) + (x - bb);
+    hi = s;
+}
+
 // One GEMM over 256 x bn tiles (bn 128 with three terms), bf16 operands, fp32 sums.
 // Which operands, and what becomes of a tile, is the kernel's mode.
 struct GemmParams {
@@ -156,7 +164,8 @@ struct GemmParams {
     int index_bytes;
     int V;                 // the whole vocabulary
     float scale;
-    float4 *stats;         // [2 splits][M] (halves of tiles): maximum, sum, weighted sum (log2 units), target's logit
+    float4 *stats;         // [2 splits][M] (halves of tiles): maximum, sum, weighted sum (log2 units), target's logit;
+                           // few states: [splits][M], the sum's low part in the last's place
     float *list_val;       // [2 splits][list][M]
     int *list_id;
     unsigned *group_key;   // few states: [M][nb][32] order of the largest of four logits, or null
