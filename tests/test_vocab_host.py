@@ -124,3 +124,29 @@ def test_binding_refuses_host_tensors_and_other_kinds():
         txl.embed_fwd(ids, [[0.0]])
     with pytest.raises(TypeError):
         txl.logprob_fwd([[0.0]], [[0.0]])
+
+
+@pytest.mark.parametrize("N,V,d", [(2048, 50257, 1024), (1024, 50257, 768), (2048, 50001, 512), (2048, 28000, 1024),
+                                   (1024, 33000, 1024), (4096, 42000, 512), (1100, 25001, 1032), (700, 50257, 1032),
+                                   (2048, 32000, 512), (1, 40000, 8), (5, 57344, 1272), (333, 5003, 520)])
+def test_every_size_of_the_gradient_has_tiles_and_parts(N, V, d):
+    # fp32: three bf16 terms of h, w and G in rows of whole lines, and the parts of dh that sums of at most
+    # 64 steps of 64 words (or 16 parts) leave
+    line, up128 = (d + 63) // 64 * 64, (V + 127) // 128 * 128
+    steps = (V + 63) // 64
+    parts = min(16, (steps + 63) // 64)
+    least = 6 * ((N + V) * line + N * up128) + (4 * parts * N * d if parts > 1 else 0)
+    assert txl.logprob_bwd_workspace_size(N, V, d, torch.float32) >= least
+
+
+def test_gradient_workspaces_over_many_sizes():
+    # (no size divides by nothing; rows of G are there whatever the type)
+    import random
+
+    rng = random.Random(17)
+    for _ in range(3000):
+        N, V, d = (int(2 ** rng.uniform(0, b)) for b in (14, 18, 9))
+        d *= 8
+        for dtype, grad in ((torch.bfloat16,) * 2, (torch.bfloat16, torch.float32), (torch.float32,) * 2):
+            assert txl.logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype=grad) >= N * min(V, 128) * 2
+            assert txl.logprob_fwd_workspace_size(N, V, d, dtype, top=rng.choice([0, 4])) >= N * 16

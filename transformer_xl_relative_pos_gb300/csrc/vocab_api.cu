@@ -191,27 +191,36 @@ struct Two {
     double cycles;
 };
 
+constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 15, 16, 19, 25, 32, 38, 50, 64, 76};
+constexpr int kPartChoices = sizeof kParts / sizeof kParts[0];
+
+// The first of kParts from place k on that is more than `parts`, or 0.
+int next_parts(int parts, int &k)
+{
+    while (k < kPartChoices && kParts[k] <= parts) ++k;
+    return k < kPartChoices ? kParts[k] : 0;
+}
+
 Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&terms)[2],
                int planes)
 {
-    static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 15, 16, 19, 25, 32, 38, 50, 64, 76};
     const int pairs = txl::device_sm_count() / 2;
     struct Option {
         Shape s;
         long long items;
         double cost, extra;  // cycles of an item, and of the parts' writes and reads (3.6 kB a cycle)
     };
-    Option o[2][2 * (sizeof kParts / sizeof kParts[0])];
+    Option o[2][2 * kPartChoices];  // (`least` and those of kParts above it: no more than kParts has)
     int n[2] = {};
     for (int i = 0; i < 2; ++i)
         for (const int bn : {256, 128}) {
             if (!columns_fit(bn, cols, terms[i])) continue;
-            for (const int parts : kParts) {
+            const int least = terms[i] == 3 ? std::min(16, ceil_div(steps[i], kMaxChain)) : 1;
+            for (int k = 0, parts = least; parts > 0; parts = next_parts(parts, k)) {
                 const int mb = ceil_div(rows[i], 256), nb = ceil_div(cols, bn);
-                const int least = terms[i] == 3 ? std::min(16, ceil_div(steps[i], kMaxChain)) : 1;
-                if (parts < least) continue;
-                // (four items a pair are as even as it needs)
-                if (parts > steps[i] || (parts > least && (long long)mb * nb * parts > 4 * pairs)) break;
+                // (the fewest that are allowed are always a choice; beyond them four items a pair are as even
+                // as it needs)
+                if (parts > least && (parts > steps[i] || (long long)mb * nb * parts > 4 * pairs)) break;
                 Option &x = o[i][n[i]++];
                 x.s = {bn, mb, nb, parts};
                 x.items = (long long)x.s.mb * x.s.nb * parts;
