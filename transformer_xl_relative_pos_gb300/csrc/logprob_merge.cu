@@ -78,7 +78,7 @@ __device__ __forceinline__ Wide dot_exact(const void *h, const void *w, int d, i
     const int vecs = d / (BF16 ? 8 : 4);
     ExactSum sum;
 #pragma unroll 4
-    for (int c = lane; c < vecs; c += 32) sum.add<BF16>(__ldg(a + c), __ldg(b + c));
+    for (int c = lane; c < vecs; c += 32) sum.add<BF16>(a[c], b[c]);
     return sum.over_warp();
 }
 
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
     uint4 h[4];
     auto load = [&](int c0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = c0 + 32 * k < vecs ? __ldg(src + c0 + 32 * k) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 4; ++k) h[k] = c0 + 32 * k < vecs ? src[c0 + 32 * k] : make_uint4(0, 0, 0, 0);
     };
     load(lane);
     const int target = checked_token(id, p.V, p.status);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) grad_rows_kernel(const GradR
         uint4 y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            y[k] = target >= 0 && c0 + 32 * k < vecs ? __ldg(w + c0 + 32 * k) : make_uint4(0, 0, 0, 0);
+            y[k] = target >= 0 && c0 + 32 * k < vecs ? w[c0 + 32 * k] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int c = c0 + 32 * k;

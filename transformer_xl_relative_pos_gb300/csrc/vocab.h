@@ -23,7 +23,9 @@ bool make_map_planes_f32(CUtensorMap *map, const void *base, long long inner, lo
 // A launch in clusters of `cluster` blocks that may begin while its predecessor in the stream
 // still runs: every kernel here waits for that one's end and writes (chain_wait) before it reads or
 // writes anything, so only launches and set-up overlap.  After a kernel that gives no leave
-// (chain_go) it is an ordinary launch.
+// (chain_go) it is an ordinary launch.  What such a kernel reads may still be written when its blocks
+// become resident, so no load here takes the non-coherent path (__ldg), which is for memory that
+// nothing writes in a kernel's lifetime.
 template <typename... P, typename... A>
 cudaError_t launch_grid(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
                         unsigned cluster, const A &...args)
@@ -53,8 +55,7 @@ cudaError_t launch_grid(void (*kernel)(P...), dim3 grid, unsigned threads, size_
 
 __device__ __forceinline__ long long raw_token(const void *tokens, int index_bytes, long long i)
 {
-    return index_bytes == 8 ? __ldg(static_cast<const long long *>(tokens) + i)
-                            : __ldg(static_cast<const int *>(tokens) + i);
+    return index_bytes == 8 ? static_cast<const long long *>(tokens)[i] : static_cast<const int *>(tokens)[i];
 }
 
 // A token's id in [0, V), or -1 for none.  Any other value is taken as none and recorded.
