@@ -61,3 +61,52 @@ def test_gradients_of_long_sums_over_several_tiles(N, V, d):
     want_h, want_w = _grads64(h, w, t, lse, dlogp)
     assert _rel(dh, want_h) <= F32_NORM and _rel(dw, want_w) <= F32_NORM
     assert torch.equal(dh, only_h) and torch.equal(dw, only_w)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,top", [(1, 8), (3, 0), (40, 8), (150, 3), (300, 0), (300, 8)])
+def test_nearly_certain_tokens_to_their_own_size(N, top, dtype):
+    # log p = -sum of the others' exp(z - z_t), 1e-12 to 6, to a relative error.  Whole numbers, so the
+    # accumulators' sums are exact; a logit beside the target's is then off by the factor to log2 units (its
+    # rounding, the product's, and the mean cut of 4 additions: 3 of 2^-24 of at most 17, 3.0e-6), by the
+    # rounding of its distance from the largest (half of 2^-18, below 64 log2 units, times ln 2: 1.3e-6) and by the
+    # exponential (2^-22): its term by 4.6e-6 of itself.  Sums of positive terms, 50 roundings of 2^-24 at most
+    # on a term's way: 3e-6.  Together below 2^-16.
+    # Beneath that stands what the largest logit's own rounding leaves: its exact value lies up to x = 2^-19
+    # log2 units above the rounded one that the sums are taken from, and log of the sum and logit, both of x ln 2
+    # = 2^-19.5, are subtracted.  In units of 2^-42: the factor's 49 bits of 64 (0.35), x rounded (0.35), its
+    # exponential less 1, argument and function (three of 2^-24: 1.1), the logarithm (one of 2^-23: 0.7), its sum
+    # with the low part's (0.35): 2.9, below 2^-40.  The entropy subtracts the weighted mean of the logits, x once
+    # more through five roundings (1.8): 4.7, below 2^-39.
+    V, d, scale = 3000, 64, 0.125
+    g = torch.Generator().manual_seed(60 + N)
+    h = torch.randint(-2, 3, (N, d), generator=g).double()
+    w = torch.randint(-1, 2, (V, d), generator=g).double()
+    t = torch.randperm(V, generator=g)[:N]
+    # (targets' rows along their states: logits of 9 to 38, where the others have 8.6 and more in all)
+    for i in range(N):
+        goal, at = 8.0 * (9.0 + 20.0 * ((i * 7) % max(N, 2)) / max(N - 1, 1)), h[i].abs().sum()
+        w[t[i]] = torch.sign(h[i]) * torch.ceil(goal / at)
+    z = scale * (h @ w.t())
+    others = z.clone()
+    others[torch.arange(N), t] = -float("inf")
+    logp = -torch.log1p(torch.exp(torch.logsumexp(others, 1) - z[torch.arange(N), t]))
+    D = lambda x: x.to(dtype).cuda()
+    res = txl.logprob_fwd(D(h), D(w), t.cuda(), scale=scale, top=top)
+    _ok()
+    lp = z - z[torch.arange(N), t][:, None] + logp[:, None]
+    lp[torch.arange(N), t] = logp
+    entropy = -(torch.exp(lp) * lp).sum(1)
+    rel = lambda x, want, floor=2.0 ** -40: (((x.cpu().double() - want).abs() - floor) / want.abs()).max().item()
+    got = rel(res.logp, logp)
+    print(f"{N} {top} {dtype}: log p {float(logp.min()):.1e} to {float(logp.max()):.1e}, off by {got:.1e}, "
+          f"entropy by {rel(res.entropy, entropy, 2.0 ** -39):.1e}")
+    assert float(logp.max()) > -1e-4 or N == 1
+    assert got <= 2.0 ** -16
+    # (terms p log p: the same error, and that of log p)
+    assert rel(res.entropy, entropy, 2.0 ** -39) <= 2.0 ** -15
+    if top:
+        best = torch.argmax(z, 1)
+        ours = best == t
+        assert torch.equal(res.top_ids[:, 0].cpu().long(), best) and bool(ours.any())
+        assert rel(res.top_logp[:, 0].cpu()[ours], logp[ours]) <= 2.0 ** -16

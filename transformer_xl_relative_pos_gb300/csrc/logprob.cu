@@ -22,6 +22,8 @@
 // such operands is the six products of terms whose weight is above 2^-24.  A step of them loads
 // each term once, three stages for six products (where every product had its own two tiles, the
 // gradient of 333 x 5003 x 520 took 73 us, so 61).
+#include <type_traits>
+
 #include "vocab.h"
 #include "ptx.cuh"
 
@@ -121,7 +123,7 @@ struct Turn {
 // What a thread keeps of its row while it walks over the vocabulary (log2 units).
 template <int LIST>
 struct RowStats {
-    float m, s, lo, es, zt;   // the sum is s + lo
+    float m, s, lo, es, zt;   // the sum is s + lo, and the maximum's own 1
     float val[LIST > 0 ? LIST : 1];
     int id[LIST > 0 ? LIST : 1];
 
@@ -176,29 +178,48 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
     for (int i = 1; i < 32; ++i) mx = fmaxf(mx, t[i]);
     const float m_new = fmaxf(r.m, mx);
     const float mu = m_new == -INFINITY ? 0.f : m_new;
-    if (m_new > r.m) {
+    const bool up = m_new > r.m;
+    bool far = false;   // a new maximum beside which the others are small
+    if (up) {
         const float diff = r.m - mu;  // (-inf before the first finite logit: sums are zero)
         const float f = ex2(diff);
-        r.es = (r.s > 0.f || r.s != r.s) ? (r.es + r.s * diff) * f : 0.f;
+        if (r.m > -INFINITY) {  // (the old maximum's 1 is one of the others now)
+            two_sum(r.s, r.lo, 1.f);
+            r.es = (r.es + r.s * diff) * f;
+        }
         r.s *= f;
         r.lo *= f;
         r.m = m_new;
+        far = !(f > 0.125f);
     }
-    // (as a tree, and with its rounding kept: beside one term near 1 the others count)
-    float cs[4], ce[2] = {0.f, 0.f};
+    // sums of the 32, as a tree; OWN: without the new maximum's 1 (equal ones beside it are added again).  Else
+    // it is taken from the whole: the others are an eighth at least, and lose 5 roundings of 2^-24 of 1.
+    // (2048 x 131072 x 1024: 351 us with the first for every new maximum, 346 so.)
+    float ce[2] = {0.f, 0.f}, more = 0.f;
+    auto sum = [&](auto own) {
+        float cs[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float e[8];
+        for (int q = 0; q < 4; ++q) {
+            float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = t[8 * q + i] - mu;
-            e[i] = ex2(d);
-            // (a logit of -inf has weight zero)
-            ce[i & 1] = fmaf(e[i], fmaxf(d, -1e30f), ce[i & 1]);
+            for (int i = 0; i < 8; ++i) {
+                const float d = t[8 * q + i] - mu;
+                e[i] = ex2(d);
+                // (a logit of -inf has weight zero)
+                ce[i & 1] = fmaf(e[i], fmaxf(d, -1e30f), ce[i & 1]);
+                if constexpr (decltype(own)::value) {
+                    const float its = far && t[8 * q + i] == mx ? 1.f : 0.f;
+                    e[i] -= its;
+                    more += its;
+                }
+            }
+            cs[q] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         }
-        cs[q] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-    }
-    two_sum(r.s, r.lo, (cs[0] + cs[1]) + (cs[2] + cs[3]));
+        two_sum(r.s, r.lo, (cs[0] + cs[1]) + (cs[2] + cs[3]));
+    };
+    if (__any_sync(0xffffffffu, far)) sum(std::true_type{});
+    else sum(std::false_type{});
+    if (up && more != 1.f) two_sum(r.s, r.lo, more - 1.f);
     r.es += ce[0] + ce[1];
     const int at = target - col0;
     if (__any_sync(0xffffffffu, (unsigned)at < (unsigned)cnt)) {

@@ -36,6 +36,13 @@ constexpr int kEpiWarps = 8;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
 static_assert(kFewRows <= ACC, "states lie in an accumulator's columns");
 
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ void epi_sync()
 {
     asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
@@ -53,8 +60,8 @@ __device__ __forceinline__ bool epi_any(bool x)
     return r != 0;
 }
 
-// Statistics (maximum, sum, weighted sum, the sum's low part) of eight states from 32 lanes' each ([maximum, sum, weighted sum][8][33] floats): lanes
-// 4 j .. 4 j + 3 join state j's.
+// Statistics (maximum, sum beside its 1, weighted sum) of eight states from 32 lanes' each ([maximum, sum,
+// weighted sum][8][33] floats): lanes 4 j .. 4 j + 3 join state j's.
 constexpr int kOwn = 3 * 8 * 33;
 static_assert(kEpiWarps * kOwn <= 64 * TURN_LD, "the warps' parts of the turning buffer");
 
@@ -73,8 +80,9 @@ __device__ __noinline__ float4 join_lanes(const float *own, int lane)
     for (int i = 0; i < 8; ++i) {
         // (before its first number a lane's maximum is -infinity and its sums are zero)
         const float d = fmaxf(m[i] - mu, -1e30f), f = ex2(d);
+        two_sum(sum, lo, f);
         two_sum(sum, lo, s[i] * f);
-        weighted = fmaf(fmaf(s[i], d, es[i]), f, weighted);
+        weighted = fmaf(fmaf(s[i] + 1.f, d, es[i]), f, weighted);
     }
 #pragma unroll
     for (int o = 1; o < 4; o *= 2) {
@@ -83,7 +91,8 @@ __device__ __noinline__ float4 join_lanes(const float *own, int lane)
         lo += olo;
         weighted += __shfl_xor_sync(FULL, weighted, o);
     }
-    return make_float4(top, sum, weighted, lo);
+    // (the largest one's own 1 is among the terms, so their sum is 1 at least)
+    return make_float4(top, top == -INFINITY ? sum : (sum - 1.f) + lo, weighted, 0.f);
 }
 
 // THREE: three terms of both operands.
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
         const float c2 = p.scale * uncut_scale(p.kb * (BK / 16)) * 1.4426950408889634f;
         for (int i = threadIdx.x - 128; i < p.M; i += kEpiWarps * 32)
             targets[i] = p.targets ? token_at(p.targets, p.index_bytes, i, p.V, p.status) : -1;
-        // running statistics of this lane's logits of state 64 g + 8 we + j
+        // running statistics of this lane's logits of state 64 g + 8 we + j; the sums leave the maximum's own 1 out
         float m[GROUPS * 8], sum[GROUPS * 8], es[GROUPS * 8];
 #pragma unroll
         for (int i = 0; i < GROUPS * 8; ++i) {
@@ -287,20 +296,24 @@ __global__ void __launch_bounds__((4 + kEpiWarps) * 32, 1)
                     if (!whole)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) v[i] = i < left ? v[i] : -INFINITY;
-                    const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                    // the four with their largest first (a maximum passes NaN over, a minimum takes it)
+                    const float a = fmaxf(v[0], v[1]), b = fmaxf(v[2], v[3]), top = fmaxf(a, b);
+                    const float u[4] = {top, min_nan(a, b), min_nan(v[0], v[1]), min_nan(v[2], v[3])};
                     const float m_new = fmaxf(m[k], top);
                     const float mu = m_new == -INFINITY ? 0.f : m_new;
                     // (before the first number the maximum is -infinity and the sums are zero)
                     const float diff = fmaxf(m[k] - mu, -1e30f), f = ex2(diff);
-                    float e_new = fmaf(sum[k], diff, es[k]) * f, e4[4];
+                    // (a maximum that another takes the place of is one of the others)
+                    const float one = top > m[k] ? 1.f : 0.f, others = sum[k] + one;
+                    float e_new = fmaf(others, diff, es[k]) * f, e4[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float d = v[i] - mu;
+                        const float d = u[i] - mu;
                         e4[i] = ex2(d);
                         e_new = fmaf(e4[i], fmaxf(d, -1e30f), e_new);
                     }
                     m[k] = m_new;
-                    sum[k] = fmaf(sum[k], f, (e4[0] + e4[1]) + (e4[2] + e4[3]));
+                    sum[k] = fmaf(others, f, ((e4[0] - one) + e4[1]) + (e4[2] + e4[3]));
                     es[k] = e_new;
                     if (p.logits) {
                         const float none = __int_as_float(0x7fffffff);

@@ -101,9 +101,8 @@ struct RowSums {
     float m, mu, sum, lo, es, zt;
 };
 
-// The sum is hi + lo: beside one term near 1 the others count, its logarithm is theirs.  FEW: the ranges'
-// sums come as pairs (their fourth place).
-template <int PER, bool FEW>
+// The sum is hi + lo: beside one term near 1 the others count, its logarithm is theirs.
+template <int PER>
 __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int lane)
 {
     constexpr unsigned FULL = 0xffffffffu;
@@ -116,7 +115,7 @@ __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int
         st[i] = s < p.splits ? p.stats[(long long)s * p.N + row] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         r.m = fmaxf(r.m, st[i].x);
         nan = nan || st[i].y != st[i].y;
-        if (!FEW) r.zt += st[i].w;  // (zero but in the target's range)
+        r.zt += st[i].w;  // (zero but in the target's range)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -126,11 +125,11 @@ __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int
     r.mu = r.m == -INFINITY ? 0.f : r.m;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (st[i].y == 0.f) continue;
+        if (st[i].x == -INFINITY && st[i].y == 0.f) continue;
         const float d = st[i].x - r.mu, f = exp2f(d);
+        two_sum(r.sum, r.lo, f);
         two_sum(r.sum, r.lo, st[i].y * f);
-        if (FEW) r.lo = fmaf(st[i].w, f, r.lo);
-        r.es += (st[i].z + st[i].y * d) * f;
+        r.es += (st[i].z + (st[i].y + 1.f) * d) * f;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const M
     }
     const int found = __popc(__ballot_sync(FULL, my_id >= 0));
     // exact logits of the candidates, and of the target where it is none of them
-    RowSums r = join_stats<PER, false>(p, row, lane);
+    RowSums r = join_stats<PER>(p, row, lane);
     float d_mine = my_val - r.mu, d_target = r.zt - r.mu;
     unsigned long long order = my_id >= 0 ? (unsigned long long)order_key(my_val) << 32 : 0ull;
     float ds = 0.f, de = 0.f;
@@ -484,7 +483,7 @@ __global__ void __launch_bounds__(kFewThreads) logprob_few_merge_kernel(const Me
     }
     // the ranges' sums (last warp); exact logits, the target's first
     if (warp == kFewWarps - 1) {
-        const RowSums r = join_stats<kLaneLists, true>(p, row, lane);
+        const RowSums r = join_stats<kLaneLists>(p, row, lane);
         if (lane == 0) s_sums = r;
     }
     for (int c = warp; c <= jobs; c += kFewWarps) {

@@ -136,6 +136,9 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// A sum of exponentials is kept beside its maximum's own term, the 1 that is left out of it: of a nearly
+// certain token the others are all that its log probability is, and next to a 1 they would be rounded to 2^-24.
+
 // hi + lo + x, the sum of hi and x exactly (Knuth's two-sum).
 __device__ __forceinline__ void two_sum(float &hi, float &lo, float x)
 {
@@ -165,8 +168,8 @@ struct GemmParams {
     int index_bytes;
     int V;                 // the whole vocabulary
     float scale;
-    float4 *stats;         // [2 splits][M] (halves of tiles): maximum, sum, weighted sum (log2 units), target's logit;
-                           // few states: [splits][M], the sum's low part in the last's place
+    float4 *stats;         // [2 splits][M] (halves of tiles): maximum, sum beside its own 1, weighted sum (log2
+                           // units), target's logit; few states: [splits][M], 0 in the last's place
     float *list_val;       // [2 splits][list][M]
     int *list_id;
     unsigned *group_key;   // few states: [M][nb][32] order of the largest of four logits, or null
