@@ -629,6 +629,9 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
  * TXL_BF16: products on the tensor cores, fp32 sums.  TXL_F32: operands as three bf16 terms
  * each (their leading 24 bits; values beneath bf16's subnormals are lost), six products on
  * the tensor cores, fp32 sums; there an infinite element of h or w makes a logit it enters NaN.
+ * The tensor cores cut each of a logit's d / 16 additions; it is scaled by the mean of that, which where nothing was
+ * cut (a state with one element) is d 2^-30 of its value.  The target's and the largest logits are
+ * formed again without.
  * A logit of -infinity has probability zero; a row with a logit of +infinity or NaN gives NaN.
  *   workspace: txl_logprob_fwd_workspace_size(N, V, d, top, dtype) bytes (0 for arguments
  *   out of range).
@@ -653,7 +656,9 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
  * statistics hold: its dh is zero.
  * G enters its products rounded to bf16; as a bf16 pair (value and residual) with h for an fp32
  * dw of bf16 operands, and in both products for N <= 128; and for fp32 operands as three terms.
- * Sums are fp32 in a fixed order: results repeat bit for bit.
+ * Sums are fp32 in a fixed order: results repeat bit for bit.  The tensor cores cut each of their additions;
+ * fp32 results are sums of parts of at most 512 of them, each scaled by the mean of what they cut, which where
+ * nothing was cut (one term among zeros) is 8.2e-6 of the value.
  *   workspace: txl_logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype) bytes (G in chunks
  *   of the vocabulary, up to about 1 GiB or 128 columns, and partial sums).
  * Errors: as txl_logprob_fwd.

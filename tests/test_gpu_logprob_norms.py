@@ -110,3 +110,46 @@ def test_nearly_certain_tokens_to_their_own_size(N, top, dtype):
         ours = best == t
         assert torch.equal(res.top_ids[:, 0].cpu().long(), best) and bool(ours.any())
         assert rel(res.top_logp[:, 0].cpu()[ours], logp[ours]) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("case,kind", [("one term of many rows", "bf16_f32"), ("one term of many rows", "f32"),
+                                       ("most rows padded", "bf16_f32"), ("one row of many words", "f32")])
+def test_fp32_gradients_of_sparse_sums(case, kind):
+    # a sum of one term, or a few, among many that are zero or tiny: nothing of it is cut, so the mean that the
+    # results are scaled by (0.27 of 2^-24 for each addition of a part's chain) is itself the error.  A chain has 256
+    # additions, of a bf16 pair's two terms 512: 8.2e-6.  The pair's own residual is 2^-18 of G at most, fp32's three
+    # terms are exact here, and the result's rounding 2^-24.  Together below 2^-16.
+    # (Sizes with more tiles than SMs, where no sum is split for their sake.)
+    dtype = F32 if kind == "f32" else BF
+    N, V, d = (20000, 12000, 1024) if case != "one row of many words" else (300, 400000, 1024)
+    g = torch.Generator(device=dev()).manual_seed(8)
+    # logits: 0 for most words, -60 for the words from 200 on (probability e^-65: as good as none)
+    h = torch.randint(1, 200, (N, d), generator=g, device=dev()).double() / 128
+    h[:, 0] = 1.0
+    w = torch.zeros(V, d, dtype=torch.float64, device=dev())
+    w[200:, 0] = -60.0
+    t = torch.full((N,), -1, device=dev())
+    dlogp = torch.ones(N, dtype=torch.float64, device=dev())
+    if case == "one term of many rows":
+        t[:] = torch.randint(0, 200, (N,), generator=g, device=dev())
+        t[::200] = 200 + torch.arange(N // 200, device=dev())      # each of a hundred words once
+        some = torch.arange(200, 200 + N // 200, device=dev())
+        want = h[::200]                                              # dw: G is 1 for its row, e^-65 for others
+    elif case == "most rows padded":
+        t[-7:] = torch.arange(207, 214, device=dev())
+        some = torch.arange(207, 214, device=dev())
+        want = h[-7:]
+    else:
+        # the words from 200 on with their own rows: dh of a row is its word's, less the mean of the first 200
+        w[200:, 1:] = torch.randint(1, 200, (V - 200, d - 1), generator=g, device=dev()).double() / 128
+        h[:, 1:] = 0.0
+        t[:] = 200 + torch.randint(0, V - 200, (N,), generator=g, device=dev())
+        want = w[t]                                                  # (the first 200 words' rows are zero)
+    D = lambda x: x.to(dtype)
+    lse = torch.logsumexp(h @ w.t(), 1).float()
+    dh, dw = txl.logprob_bwd(D(h), D(w), t, lse, dlogp.float(), grad_dtype=F32)
+    _ok()
+    got = dh if case == "one row of many words" else dw[some]
+    off = ((got.double() - want).abs() / want.abs()).max().item()
+    print(f"{case}, {kind}: off by {off:.2e}")
+    assert off <= 2.0 ** -16

@@ -131,10 +131,10 @@ def test_binding_refuses_host_tensors_and_other_kinds():
                                    (2048, 32000, 512), (1, 40000, 8), (5, 57344, 1272), (333, 5003, 520)])
 def test_every_size_of_the_gradient_has_tiles_and_parts(N, V, d):
     # fp32: three bf16 terms of h, w and G in rows of whole lines, and the parts of dh that sums of at most
-    # 64 steps of 64 words (or 16 parts) leave
+    # 64 steps of 64 words leave
     line, up128 = (d + 63) // 64 * 64, (V + 127) // 128 * 128
     steps = (V + 63) // 64
-    parts = min(16, (steps + 63) // 64)
+    parts = (steps + 63) // 64
     least = 6 * ((N + V) * line + N * up128) + (4 * parts * N * d if parts > 1 else 0)
     assert txl.logprob_bwd_workspace_size(N, V, d, torch.float32) >= least
 

@@ -101,10 +101,11 @@ struct Shape {
 // but its accumulator's first use and its stores do not quite.
 constexpr double kItemCost = 1500.0;
 
-// Steps of a part of a product of fp32 operands, at most (of up to 16 parts): the accumulators' cut
-// additions are made good on average only, and a longer chain leaves more of them.  dh of 2048 x 32000 x
-// 512, relative to its norm, in parts of 500 steps 9.5e-6, of 125 6.7e-6, of 63 1.6e-6, of 32 1.3e-6 (the
-// whole gradient 673, 682, 689 and 701 us; fp32 library products 4.5e-6).
+// Steps of a part of a product whose result is fp32, at most: the accumulators' cut additions are made good
+// on average only, and a longer chain leaves more of them.  fp32 dh of 2048 x 32000 x 512, relative to its norm, in
+// parts of 500 steps 9.5e-6, of 125 6.7e-6, of 63 1.6e-6, of 32 1.3e-6 (the whole gradient 673, 682, 689
+// and 701 us; fp32 library products 4.5e-6).  Where nothing is cut (one term among zeros) the mean itself is the
+// error: 4.1e-6 of the value with 64 steps, 8.2e-6 where G is a pair; a word of 20000 rows in one part 4.0e-5.
 constexpr int kMaxChain = 64;
 
 // The launch that sums parts, in cycles.
@@ -201,8 +202,9 @@ int next_parts(int parts, int &k)
     return k < kPartChoices ? kParts[k] : 0;
 }
 
+// (f32: whether the results are)
 Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2], const int (&terms)[2],
-               int planes)
+               const bool (&f32)[2], int planes)
 {
     const int pairs = txl::device_sm_count() / 2;
     struct Option {
@@ -215,7 +217,7 @@ Two choose_two(const long long (&rows)[2], long long cols, const int (&steps)[2]
     for (int i = 0; i < 2; ++i)
         for (const int bn : {256, 128}) {
             if (!columns_fit(bn, cols, terms[i])) continue;
-            const int least = terms[i] == 3 ? std::min(16, ceil_div(steps[i], kMaxChain)) : 1;
+            const int least = f32[i] ? ceil_div(steps[i], kMaxChain) : 1;
             for (int k = 0, parts = least; parts > 0; parts = next_parts(parts, k)) {
                 const int mb = ceil_div(rows[i], 256), nb = ceil_div(cols, bn);
                 // (the fewest that are allowed are always a choice; beyond them four items a pair are as even
@@ -335,10 +337,11 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     g.g_plane = g.g_ld * N;
     g.g = choose_shape(N, g.chunk, ceil_div(d, 64), dtype == TXL_F32 ? 3 : 1, 0);
     const int kb_h = ceil_div(g.chunk, 64), kb_w = ceil_div(N, 64);
+    const bool f32[2] = {dtype == TXL_F32, grad_dtype == TXL_F32};
     // (G a pair: its terms in the two blocks of a pair, which leaves parts to sum, or both in each)
-    Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, kb_w}, {g.pieces_h, g.pieces}, 1);
+    Two two = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, kb_w}, {g.pieces_h, g.pieces}, f32, 1);
     if (g.pieces_h == 2) {
-        const Two apart = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, 2 * kb_w}, {1, 1}, 2);
+        const Two apart = choose_two({(long long)N, (long long)g.chunk}, d, {kb_h, 2 * kb_w}, {1, 1}, f32, 2);
         g.stacked = apart.cycles < two.cycles;
         if (g.stacked) two = apart;
     }
