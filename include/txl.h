@@ -659,8 +659,9 @@ int txl_logprob_fwd(const void *h, long long h_stride, const void *w, long long 
  * Sums are fp32 in a fixed order: results repeat bit for bit.  The tensor cores cut each of their additions;
  * fp32 results are sums of parts of at most 512 of them, each scaled by the mean of what they cut, which where
  * nothing was cut (one term among zeros) is 8.2e-6 of the value.
- *   workspace: txl_logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype) bytes (G in chunks
- *   of the vocabulary, up to about 1 GiB or 128 columns, and partial sums).
+ *   workspace: txl_logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype) bytes: G in chunks
+ *   of the vocabulary, up to about 1 GiB or 128 columns, h once more (TXL_F32: and w, as three terms each), and
+ *   partial sums (past one chunk two fp32 dh or, where a chunk's is split, more).
  * Errors: as txl_logprob_fwd.
  */
 size_t txl_logprob_bwd_workspace_size(int N, int V, int d, int dtype, int grad_dtype);

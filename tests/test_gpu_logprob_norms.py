@@ -153,3 +153,26 @@ def test_fp32_gradients_of_sparse_sums(case, kind):
     off = ((got.double() - want).abs() / want.abs()).max().item()
     print(f"{case}, {kind}: off by {off:.2e}")
     assert off <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16_f32", "f32"])
+def test_dh_over_chunks_of_the_vocabulary(kind):
+    # G is past the workspace's limit: the chunks' sums of dh, added in their order.  bf16 results: G's rounding and
+    # the result's, 2^-8 each at most; fp32: F32_NORM above.
+    N, V, d = 20000, 60000, 16
+    dtype, grad = F32 if kind == "f32" else BF, BF if kind == "bf16" else F32
+    h, w, t, dlogp = _inputs(N, V, d, dtype, 9)
+    lse = torch.cat([torch.logsumexp(x.double() @ w.double().t(), 1) for x in h.split(4000)]).float()
+    ws = torch.full((txl.logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype=grad),), 255, dtype=torch.uint8,
+                    device=dev())
+    dh, dw = txl.logprob_bwd(h, w, t, lse, dlogp, grad_dtype=grad, workspace=ws)
+    again = txl.logprob_bwd(h, w, t, lse, dlogp, grad_dtype=grad, workspace=ws.fill_(255))
+    _ok()
+    want_h, want_w = torch.empty(N, d, dtype=torch.float64, device=dev()), 0.0
+    for i in range(0, N, 4000):
+        a = slice(i, i + 4000)
+        want_h[a], part = _grads64(h[a], w, t[a], lse[a], dlogp[a])
+        want_w = want_w + part
+    limit = lambda x: F32_NORM if kind == "f32" else 2 * 2.0 ** -8
+    assert _rel(dh, want_h) <= limit(dh) and _rel(dw, want_w) <= limit(dw)
+    assert torch.equal(dh, again[0]) and torch.equal(dw, again[1])

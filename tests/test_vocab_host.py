@@ -150,3 +150,16 @@ def test_gradient_workspaces_over_many_sizes():
         for dtype, grad in ((torch.bfloat16,) * 2, (torch.bfloat16, torch.float32), (torch.float32,) * 2):
             assert txl.logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype=grad) >= N * min(V, 128) * 2
             assert txl.logprob_fwd_workspace_size(N, V, d, dtype, top=rng.choice([0, 4])) >= N * 16
+
+
+@pytest.mark.parametrize("N", [65536, 262144, 1 << 20])
+@pytest.mark.parametrize("dtype,grad", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                        (torch.float32, torch.float32)])
+def test_the_gradients_workspace_grows_with_the_rows_not_their_square(N, dtype, grad):
+    # V x d = 131072 x 1024: chunks of G of 1 GiB (or 128 columns of three terms), h in bf16 or three terms of it, w in
+    # three terms, two fp32 dh, parts of a chunk's dw for chains of 64 steps (a quarter GiB) and of its dh (another)
+    V, d = 131072, 1024
+    terms = 3 if dtype == torch.float32 else 1
+    g = max(1 << 30, N * 128 * 2 * 3)
+    most = g + terms * N * d * 2 + (6 * V * d if terms == 3 else 0) + 2 * N * d * 4 + (1 << 29) + (1 << 28)
+    assert txl.logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype=grad) <= most

@@ -202,7 +202,7 @@ cudaError_t launch_logprob_few(const CUtensorMap &tm_w, const CUtensorMap &tm_h,
 cudaError_t launch_logprob_grad(const GemmLaunch &g, cudaStream_t s);
 // dh = G W (contraction over the vocabulary) and dW = G^T h (over the rows).
 cudaError_t launch_products(const GemmLaunch &g, cudaStream_t s);
-// out = sum over the parts, in their order; of up to two results (elems 0: none).
+// out = sum over the parts, in their order; of up to two results (elems 0: none).  out may be the first part.
 struct PartsSum {
     const float *part;
     void *out;

@@ -312,7 +312,7 @@ struct GradPlan {
     int pieces, pieces_h;         // terms of G, and those that dh takes
     int stacked;                  // GemmParams, of dh
     Shape g, h, w;                // tiles of G, of dh, and of a chunk's dW
-    int parts_h;                  // of dh, over all chunks
+    int parts_h;                  // of a chunk's dh
     long long g_ld, g_plane;
     size_t live, target_logp, w_planes, g_at, part_h, part_w, total;
 };
@@ -347,7 +347,7 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     }
     g.h = two.a;
     g.w = two.b;
-    g.parts_h = g.chunks * g.h.parts * (g.stacked ? 2 : 1);
+    g.parts_h = g.h.parts * (g.stacked ? 2 : 1);
     size_t o = 0;
     const size_t row = (size_t)line_ld(d) * 2 * txl::kMaxPieces;
     g.live = o;
@@ -358,8 +358,10 @@ GradPlan make_grad_plan(int N, int V, int d, int dtype, int grad_dtype)
     if (dtype == TXL_F32) o = up256(o + V * row);
     g.g_at = o;
     o = up256(o + (size_t)g.pieces * g.g_plane * 2);
+    // (past one chunk: what the chunks so far have summed, then a chunk's parts.  Parts of all chunks would
+    // be N rows for each of N V / 2^29 chunks)
     g.part_h = o;
-    if (g.parts_h > 1) o = up256(o + (size_t)g.parts_h * N * d * 4);
+    if (g.parts_h > 1 || g.chunks > 1) o = up256(o + (size_t)(g.parts_h + (g.chunks > 1)) * N * d * 4);
     g.part_w = o;
     if (g.w.parts > 1) o = up256(o + (size_t)g.w.parts * g.chunk * d * 4);
     g.total = o;
@@ -725,17 +727,20 @@ int txl_logprob_bwd(const void *h, long long h_stride, const void *w, long long 
             q.splits = g.h.parts;
             q.n_items = q.mb * q.nb * q.splits;
             q.b_row0 = v0;
-            q.part = g.parts_h > 1;
+            q.part = g.parts_h > 1 || g.chunks > 1;
             q.out_bf16 = dtype == TXL_BF16;
             q.stacked = g.stacked;
             q.terms = q.stacked ? 1 : g.pieces_h;
             q.a_rows = q.stacked ? box_rows(N) : 128;
-            if (!map_out(&prod.maps[0].out, q,
-                         q.part ? ws + g.part_h + (size_t)c * (g.parts_h / g.chunks) * N * d * 4 : (char *)dh))
+            float *so_far = reinterpret_cast<float *>(ws + g.part_h);
+            float *parts = so_far + (g.chunks > 1 ? (long long)N * d : 0);
+            if (!map_out(&prod.maps[0].out, q, q.part ? reinterpret_cast<char *>(parts) : (char *)dh))
                 return TXL_ERR_CUDA;
-            if (q.part && c + 1 == g.chunks)
-                sums[0] = {reinterpret_cast<float *>(ws + g.part_h), dh, (long long)N * d, g.parts_h,
-                           dtype == TXL_BF16};
+            // the chunks' sums in their order, the last one's to dh
+            const bool last = c + 1 == g.chunks;
+            if (q.part)
+                sums[0] = {c > 0 ? so_far : parts, last ? dh : so_far, (long long)N * d, g.parts_h + (c > 0),
+                           last && dtype == TXL_BF16};
         }
         if (dw) {
             char *rows = static_cast<char *>(dw) + (size_t)v0 * d * elem(grad_dtype);
