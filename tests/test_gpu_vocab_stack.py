@@ -209,3 +209,25 @@ def test_captured_behind_copies_and_other_streams():
     graph.replay()
     _ok()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(cache_kv=True), dict(cache_kv=True, graphs=True), dict(paged=True)])
+def test_ids_outside_the_vocabulary(kw):
+    # on the host they are refused before anything moves; on the device they count as none, and are recorded
+    s, other = stack(**kw), stack(**kw)
+    for i in range(3):
+        seg = tokens(W.B, W.L, seed=40 + i)
+        assert torch.equal(s.segment(seg), other.segment(seg))
+        wrong = seg.clone()
+        wrong[1, 5] = W.vocab
+        with pytest.raises(IndexError):
+            s.segment(wrong)
+        with pytest.raises(IndexError):
+            s.score(seg, wrong)
+    _ok()
+    none = wrong.clone()
+    none[1, 5] = -1
+    got, want = s.segment(wrong.to(dev())).clone(), other.segment(none)
+    assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    assert txl.device_status() == -8

@@ -104,7 +104,9 @@ class XLStack:
     params: draws from ``txl_inputs.draw_stack`` (CPU fp32); weights are moved
     to ``device`` in ``dtype``.  ``segment(tokens)`` processes one segment
     [B, L] and returns the top layer's states [B, L, d] (``dtype``).  Token -1: none, a
-    zero embedding.  ``emb_scale``: factor of the embeddings (they enter as they are by
+    zero embedding.  Other ids outside the vocabulary raise IndexError where they lie on the
+    host; ids on the device are not read back: there they count as none and are recorded for
+    ``device_status``.  ``emb_scale``: factor of the embeddings (they enter as they are by
     default)."""
 
     MAX_DRAFT = 64  # nodes of a drafted tree
@@ -272,6 +274,7 @@ class XLStack:
         the result lives in the graph's memory and is overwritten by the next
         replay of the same ring position."""
         B, L = tokens.shape
+        self._check_ids(tokens, "tokens")
         if self.paged:
             parents = torch.arange(-1, L - 1, dtype=torch.int32)
             h = self.draft(tokens, parents)
@@ -312,10 +315,18 @@ class XLStack:
             self._restore(st, snap)
         return out
 
+    def _check_ids(self, ids: torch.Tensor, name: str):
+        if ids.is_cuda or ids.numel() == 0:
+            return
+        V, low, high = self.emb.shape[0], int(ids.min()), int(ids.max())
+        if low < -1 or high >= V:
+            raise IndexError(f"{name}: {low if low < -1 else high} is none of the {V} words (nor -1)")
+
     def _embed(self, tokens: torch.Tensor) -> torch.Tensor:
         """h^0 of tokens [B, L]."""
         if not self.emb.is_cuda:  # (a stack on the host, its kernels replaced by the caller)
-            return self.emb[tokens] * self.emb_scale
+            rows = self.emb[tokens.clamp(min=0)] * self.emb_scale
+            return torch.where((tokens >= 0)[..., None], rows, torch.zeros_like(rows))
         return txl.embed_fwd(tokens.contiguous(), self.emb, scale=self.emb_scale)
 
     def log_probs(self, h: torch.Tensor, targets=None, *, top: int = 0, scale: float = 1.0) -> txl.LogProbs:
@@ -324,12 +335,16 @@ class XLStack:
         entropy, and the ``top`` most probable tokens.  Of a segment's states, position t's
         target is the token at t + 1; a drafted node's candidates for children are its top_ids."""
         if targets is not None:
-            targets = torch.as_tensor(targets).to(self.device).contiguous()
+            targets = torch.as_tensor(targets)
+            self._check_ids(targets, "targets")
+            targets = targets.to(self.device).contiguous()
         return txl.logprob_fwd(h, self.emb, targets, top=top, scale=scale)
 
     def score(self, tokens: torch.Tensor, targets: torch.Tensor, *, top: int = 0) -> txl.LogProbs:
         """One segment [B, L] and the log probabilities of its targets [B, L] (each
         position's next token; -1: none)."""
+        targets = torch.as_tensor(targets)
+        self._check_ids(targets, "targets")   # (before the stream moves on)
         return self.log_probs(self.segment(tokens), targets, top=top)
 
     def draft(self, tokens: torch.Tensor, parents: torch.Tensor, n_nodes=None) -> torch.Tensor:
@@ -343,6 +358,7 @@ class XLStack:
         B, N = tokens.shape
         if not 1 <= N <= self.MAX_DRAFT:
             raise ValueError(f"draft: 1 to {self.MAX_DRAFT} tokens")
+        self._check_ids(tokens, "tokens")
         if self.memory is None or self.memory.B != B:
             self.reset(B)
         # accept() looks at the tree as it was given (read back there if it lies on the device)
