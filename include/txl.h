@@ -632,7 +632,8 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
  * The tensor cores cut each of a logit's d / 16 additions; it is scaled by the mean of that, which where nothing was
  * cut (a state with one element) is d 2^-30 of its value.  The target's and the largest logits are
  * formed again without.
- * A logit of -infinity has probability zero; a row with a logit of +infinity or NaN gives NaN.
+ * A logit of -infinity has probability zero; a row with a logit of +infinity or NaN gives NaN.  Logits of more
+ * than 2^128 ln 2 (2.35e38) in size count as infinite.
  *   workspace: txl_logprob_fwd_workspace_size(N, V, d, top, dtype) bytes (0 for arguments
  *   out of range).
  * Errors: as txl_embed_bwd; TXL_ERR_UNSUPPORTED for top > 16.

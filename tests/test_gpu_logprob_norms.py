@@ -176,3 +176,52 @@ def test_dh_over_chunks_of_the_vocabulary(kind):
     limit = lambda x: F32_NORM if kind == "f32" else 2 * 2.0 ** -8
     assert _rel(dh, want_h) <= limit(dh) and _rel(dw, want_w) <= limit(dw)
     assert torch.equal(dh, again[0]) and torch.equal(dw, again[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("where", ["first words", "every other range", "all but one"])
+@pytest.mark.parametrize("N,top", [(3, 4), (100, 0), (300, 0), (300, 4)])
+def test_words_masked_by_the_lowest_value(N, top, where, dtype):
+    # logits of -1.7e38 (the type's lowest times 0.5) have no part in anything, whole chunks and ranges of them
+    # either; and a gradient of the entropies of 2^30 times their probability of zero is zero
+    V, d, scale = 6000, 64, 0.5
+    g = torch.Generator().manual_seed(N)
+    h = torch.randn(N, d, generator=g).to(dtype).double()
+    w = (torch.randn(V, d, generator=g) * 0.5).to(dtype).double()
+    h[:, 0] = 1.0
+    w[:, 0] = 0.0
+    at = torch.arange(V)
+    off = {"first words": at < 4000, "every other range": at // 640 % 2 == 0, "all but one": at != 4321}[where]
+    keep = at[~off]
+    w[off, 0] = float(torch.finfo(torch.bfloat16).min)
+    t = keep[torch.randint(0, len(keep), (N,), generator=g)]
+    D = lambda x: x.to(dtype).to(dev())
+    res = txl.logprob_fwd(D(h), D(w), t.to(dev()), scale=scale, top=top)
+    lp = torch.log_softmax(scale * h @ w[keep].t(), 1)
+    place = torch.searchsorted(keep, t)
+    entropy = -(torch.exp(lp) * lp).sum(1)
+    # (fp32 sums: 2^-20 of numbers of size 10)
+    close = lambda x, want: float((x.cpu().double() - want).abs().max()) <= 1e-5
+    assert close(res.logp, lp[torch.arange(N), place]) and close(res.entropy, entropy)
+    assert close(res.lse, torch.logsumexp(scale * h @ w[keep].t(), 1))
+    if top:
+        some = min(top, len(keep))
+        assert torch.equal(res.top_ids[:, :some].cpu().long(), keep[torch.sort(lp, 1, descending=True)[1][:, :some]])
+    factor = 2.0 ** 30
+    dlogp, dent = torch.randn(N, generator=g) * factor, torch.randn(N, generator=g) * factor
+    dh, dw = txl.logprob_bwd(D(h), D(w), t.to(dev()), res.lse, dlogp.to(dev()), entropy=res.entropy,
+                             dentropy=dent.to(dev()), scale=scale, grad_dtype=F32)
+    _ok()
+    assert bool(torch.isfinite(dh).all()) and bool(torch.isfinite(dw).all()) and bool((dw.cpu()[off] == 0).all())
+    lp = scale * h @ w[keep].t() - res.lse.cpu().double()[:, None]
+    p = torch.exp(lp)
+    G = -dlogp.double()[:, None] * p - dent.double()[:, None] * p * (lp + res.entropy.cpu().double()[:, None])
+    G[torch.arange(N), place] += dlogp.double()
+    want = scale * G.t() @ h
+    if where == "all but one":
+        return   # (one word is certain: its gradient is what is left of equal numbers)
+    # G: a bf16 pair, or terms, from statistics of 2^-20
+    assert _rel(dw.cpu()[keep], want) <= 2.0 ** -16
+    if N > 3:
+        # G rounded to bf16 once (in fp32: not), and the result
+        assert _rel(dh.cpu()[:, 1:], (scale * G @ w[keep])[:, 1:]) <= (2 * 2.0 ** -8 if dtype == BF else 2.0 ** -16)

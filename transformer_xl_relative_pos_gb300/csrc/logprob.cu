@@ -181,7 +181,8 @@ __device__ __forceinline__ void take(RowStats<LIST> &r, const float (&t)[32], in
     const bool up = m_new > r.m;
     bool far = false;   // a new maximum beside which the others are small
     if (up) {
-        const float diff = r.m - mu;  // (-inf before the first finite logit: sums are zero)
+        // (bounded: a finite maximum of 1e38 below, times a sum, would be infinite, and times 0 NaN)
+        const float diff = fmaxf(r.m - mu, -1e30f);
         const float f = ex2(diff);
         if (r.m > -INFINITY) {  // (the old maximum's 1 is one of the others now)
             two_sum(r.s, r.lo, 1.f);
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
         uint8_t *out = smem + OFF_OUT + (warp - 4) * OUT_BYTES;
         constexpr float kLog2e = 1.4426950408889634f;
+        constexpr float kNoWeight = -1e3f;  // log probabilities below have p = 0, which a gradient times them must not undo
         const float zscale = g.p[0].scale * uncut_scale(g.p[0].kb * (BK / 16)), c2 = zscale * kLog2e;
         // 128 bytes of each of the warp's rows, turned by the swizzle, then one store.  Each warp for
         // itself: with four that met at barriers around one store of 128 rows the products of
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) {
                                     const float lp = fmaf(__uint_as_float(raw[i]), zscale, -lse);
-                                    v[x][i] = -ex2(lp * kLog2e) * fmaf(ge, fmaxf(lp, -1e30f) + ent, g1);
+                                    v[x][i] = -ex2(lp * kLog2e) * fmaf(ge, fmaxf(lp, kNoWeight) + ent, g1);
                                 }
                             } else {
 #pragma unroll
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (__any_sync(0xffffffffu, (unsigned)at < 32u && target >= 0)) {
                                 // the target's element, from its exact logit
                                 const float pt = ex2(lpt * kLog2e);
-                                const float f = p.dentropy ? fmaf(ge, fmaxf(lpt, -1e30f) + ent, g1) : g1;
+                                const float f = p.dentropy ? fmaf(ge, fmaxf(lpt, kNoWeight) + ent, g1) : g1;
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     if (i == at && target >= 0) v[x][i] = fmaf(-pt, f, g1);

@@ -126,7 +126,7 @@ __device__ __forceinline__ RowSums join_stats(const MergeParams &p, int row, int
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         if (st[i].x == -INFINITY && st[i].y == 0.f) continue;
-        const float d = st[i].x - r.mu, f = exp2f(d);
+        const float d = fmaxf(st[i].x - r.mu, -1e30f), f = exp2f(d);  // (bounded: times a sum it stays finite)
         two_sum(r.sum, r.lo, f);
         two_sum(r.sum, r.lo, st[i].y * f);
         r.es += (st[i].z + (st[i].y + 1.f) * d) * f;
@@ -154,6 +154,7 @@ __device__ __forceinline__ void replace_term(float mu, float was, float d1, floa
 {
     // (as a multiple of the term that was there: of two numbers near 1 the difference would be a rounding)
     const float d0 = was - mu, e0 = ex2(d0);
+    if (e0 == 0.f) return;  // (nothing is in the sums; the difference may be anything)
     ds = e0 * expm1f((d1 - d0) * kLn2);
     de = fmaf(ds, d1, e0 * (d1 - d0));
 }
