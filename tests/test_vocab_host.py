@@ -163,3 +163,14 @@ def test_the_gradients_workspace_grows_with_the_rows_not_their_square(N, dtype, 
     g = max(1 << 30, N * 128 * 2 * 3)
     most = g + terms * N * d * 2 + (6 * V * d if terms == 3 else 0) + 2 * N * d * 4 + (1 << 29) + (1 << 28)
     assert txl.logprob_bwd_workspace_size(N, V, d, dtype, grad_dtype=grad) <= most
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 5, 2 ** 40 + 100])
+def test_counts_past_an_int_are_refused_not_cut(big):
+    # (2^32 + 5 rows are not 5)
+    for size in (txl.embed_bwd_workspace_size(big, 10, 16), txl.embed_bwd_workspace_size(10, big, 16),
+                 txl.logprob_fwd_workspace_size(big, 10, 16), txl.logprob_fwd_workspace_size(10, big, 16),
+                 txl.logprob_fwd_workspace_size(10, 10, 16, top=big), txl.logprob_bwd_workspace_size(big, 10, 16),
+                 txl.logprob_bwd_workspace_size(10, big, 16), txl.logprob_bwd_workspace_size(10, 10, big * 8)):
+        assert size == 0
+    assert txl.embed_bwd_workspace_size(-big, 10, 16) == 0

@@ -741,6 +741,14 @@ _INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
+def _counts(*n: int) -> tuple:
+    """Counts as C ints; one that is none stays as far out of range as an int goes, for the library to refuse
+    (ctypes would cut its high bits off)."""
+    if max(n) > 0x7fffffff or min(n) < -0x80000000:
+        return tuple(max(-0x80000000, min(x, 0x7fffffff)) for x in n)
+    return n
+
+
 def _on_device(index: int, name: str, stream, *args):
     """The library's function on device ``index`` and (unless given) its current stream."""
     if stream is None:
@@ -854,14 +862,17 @@ def embed_fwd(tokens, emb, *, scale: float = 1.0, out=None, stream=None):
     if out is None:
         with _made_on(index, stream):
             out = torch.empty(shape, dtype=dtype, device=emb.device)
-    _on_device(index, "txl_embed_fwd", stream, at, kind, emb.data_ptr(), stride,
-               _ptr(out, "out", dtype, shape, index), n, V, d, scale, _CODES[dtype])
+    at_out = _ptr(out, "out", dtype, shape, index)
+    if (n | V | d) >> 31:
+        n, V, d = _counts(n, V, d)
+    _on_device(index, "txl_embed_fwd", stream, at, kind, emb.data_ptr(), stride, at_out, n, V, d, scale,
+               _CODES[dtype])
     return out
 
 
 def embed_bwd_workspace_size(n: int, V: int, d: int) -> int:
     """Bytes of device workspace embed_bwd needs for n tokens."""
-    return int(lib().txl_embed_bwd_workspace_size(int(n), int(V), int(d)))
+    return int(lib().txl_embed_bwd_workspace_size(*_counts(int(n), int(V), int(d))))
 
 
 def embed_bwd(dout, tokens, V: int, *, scale: float = 1.0, dtype=torch.float32, out=None,
@@ -885,7 +896,7 @@ def embed_bwd(dout, tokens, V: int, *, scale: float = 1.0, dtype=torch.float32, 
             out = torch.empty(V, d, dtype=dtype, device=dout.device)
     workspace, ws, ws_bytes = _room(workspace, embed_bwd_workspace_size(n, V, d), index, stream)
     _on_device(index, "txl_embed_bwd", stream, at, kind, dout.data_ptr(), stride,
-               _ptr(out, "out", out.dtype, (V, d), index), n, V, d, scale, _code(dout.dtype),
+               _ptr(out, "out", out.dtype, (V, d), index), *_counts(n, V, d), scale, _code(dout.dtype),
                _code(out.dtype), int(accumulate), ws, ws_bytes)
     return out
 
@@ -903,7 +914,7 @@ class LogProbs(NamedTuple):
 
 def logprob_fwd_workspace_size(N: int, V: int, d: int, dtype=torch.bfloat16, *, top: int = 0) -> int:
     """Bytes of device workspace logprob_fwd needs for N states."""
-    return int(lib().txl_logprob_fwd_workspace_size(int(N), int(V), int(d), int(top), _code(dtype)))
+    return int(lib().txl_logprob_fwd_workspace_size(*_counts(int(N), int(V), int(d), int(top)), _code(dtype)))
 
 
 def logprob_fwd(h, w, targets=None, *, scale: float = 1.0, top: int = 0, out: LogProbs | None = None,
@@ -932,7 +943,7 @@ def logprob_fwd(h, w, targets=None, *, scale: float = 1.0, top: int = 0, out: Lo
     size = 0 if workspace is not None else logprob_fwd_workspace_size(N, V, d, w.dtype, top=top)
     workspace, ws, ws_bytes = _room(workspace, size, index, stream)
     _on_device(index, "txl_logprob_fwd", stream, h.data_ptr(), h_stride, w.data_ptr(), w_stride, at,
-               kind, *ptrs, N, V, d, top, scale, code, ws, ws_bytes)
+               kind, *ptrs, *_counts(N, V, d, top), scale, code, ws, ws_bytes)
     return out
 
 
@@ -940,7 +951,7 @@ def logprob_bwd_workspace_size(N: int, V: int, d: int, dtype=torch.bfloat16, *,
                                grad_dtype=None) -> int:
     """Bytes of device workspace logprob_bwd needs for N states."""
     grad = dtype if grad_dtype is None else grad_dtype
-    return int(lib().txl_logprob_bwd_workspace_size(int(N), int(V), int(d), _code(dtype), _code(grad)))
+    return int(lib().txl_logprob_bwd_workspace_size(*_counts(int(N), int(V), int(d)), _code(dtype), _code(grad)))
 
 
 def logprob_bwd(h, w, targets, lse, dlogp, *, entropy=None, dentropy=None, scale: float = 1.0,
@@ -970,7 +981,7 @@ def logprob_bwd(h, w, targets, lse, dlogp, *, entropy=None, dentropy=None, scale
     _on_device(index, "txl_logprob_bwd", stream, h.data_ptr(), h_stride, w.data_ptr(), w_stride, at,
                kind, _ptr(lse, "lse", f32, shape, index), at_of(entropy, "entropy", f32, shape),
                at_of(dlogp, "dlogp", f32, shape), at_of(dentropy, "dentropy", f32, shape),
-               at_of(dh, "dh", w.dtype, h.shape), at_of(dw, "dw", grad, (V, d)), N, V, d, scale,
+               at_of(dh, "dh", w.dtype, h.shape), at_of(dw, "dw", grad, (V, d)), *_counts(N, V, d), scale,
                _code(w.dtype), _code(grad), ws, ws_bytes)
     return dh, dw
 
