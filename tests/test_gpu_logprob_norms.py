@@ -1,11 +1,12 @@
 """The log probabilities' outputs on the GPU, held in the norm: errors relative to the whole
 output's norm against 64 bits, where the element-wise worst cases of vocab_model leave room for a
-lost term."""
+lost term (vocab_terms has inputs on which one shows)."""
 
 import pytest
 import torch
 
 import transformer_xl_relative_pos_gb300 as txl
+import vocab_terms as vt
 from parity import dev
 
 pytestmark = pytest.mark.gpu
@@ -225,3 +226,51 @@ def test_words_masked_by_the_lowest_value(N, top, where, dtype):
     if N > 3:
         # G rounded to bf16 once (in fp32: not), and the result
         assert _rel(dh.cpu()[:, 1:], (scale * G @ w[keep])[:, 1:]) <= (2 * 2.0 ** -8 if dtype == BF else 2.0 ** -16)
+
+
+@pytest.mark.parametrize("N,V,d", vt.UNIFORM)
+def test_every_term_of_fp32_operands_is_in_the_products(N, V, d):
+    # off by F32_NORM's arithmetic, with G = dlogp exp(-log V): the exponent in log2 units rounded (2^-21, times ln
+    # 2: 3.3e-7) and the exponential (2^-22).  Below 3e-6; a lost term is more (test_vocab_terms).
+    case = vt.Uniform(N, V, d)
+    D = lambda x: x.float().to(dev())
+    dh, dw = txl.logprob_bwd(D(case.h), D(case.w), case.t.to(dev()), case.lse.to(dev()), D(case.dlogp))
+    _ok()
+    want_h, want_w = case.exact()
+    print(f"dh {vt.rel(dh.cpu(), want_h):.1e}, dw {vt.rel(dw.cpu()[1:], want_w):.1e}")
+    assert vt.rel(dh.cpu(), want_h) <= vt.GRAD_LIMIT and vt.rel(dw.cpu()[1:], want_w) <= vt.GRAD_LIMIT
+
+
+@pytest.mark.parametrize("N,V,d", vt.STEEP)
+def test_every_term_of_fp32_operands_is_in_the_logits(N, V, d):
+    # logits of 30: 33 additions of d / 16 at most, each cut by 0 to 1 units of 2^-23 of up to 30 (0.29 of that at
+    # random, 6e-6, and 0.05 of 2^-24 each beside the mean: 3e-6), three roundings of up to 37 (2^-24 each: 6e-6):
+    # 1.5e-5 of a probability, 5e-7 of a log-sum-exp.
+    case = vt.Steep(N, V, d)
+    D = lambda x: x.float().to(dev())
+    res = txl.logprob_fwd(D(case.h), D(case.w), case.t.to(dev()), scale=case.scale)
+    _, dw = txl.logprob_bwd(D(case.h), D(case.w), case.t.to(dev()), case.lse.to(dev()), D(case.dlogp), scale=case.scale)
+    _ok()
+    off = vt.rel(dw.cpu()[1:], case.dw()), vt.rel(res.lse.cpu(), torch.logsumexp(case.z, 1))
+    print("dw %.1e, lse %.1e" % off)
+    assert off[0] <= vt.STEEP_LIMIT and off[1] <= vt.LSE_LIMIT
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,V,d,top", [(1, 5000, 512, 8), (17, 1204, 512, 5), (200, 9001, 200, 3), (100, 700, 40, 0),
+                                       (515, 9001, 128, 9), (300, 1000, 1024, 0), (2000, 5003, 264, 0)])
+def test_log_probabilities_in_the_norm(N, V, d, top, dtype):
+    # logits of some 2: d / 16 additions, 0.29 sqrt(64) 2^-23 at random and 0.07 * 64 * 2^-24 beside the mean, of 2:
+    # 1.1e-6 of a term of the sums; half a rounding or two of a result of 5 to 12.  Below 1e-6 of that.
+    h, w, t, _ = _inputs(N, V, d, dtype, 7 * N + V)
+    res = txl.logprob_fwd(h, w, t, top=top)
+    _ok()
+    lp = torch.log_softmax(h.double() @ w.double().t(), 1)
+    want = {"lse": torch.logsumexp(h.double() @ w.double().t(), 1), "entropy": -(torch.exp(lp) * lp).sum(1)}
+    live = t >= 0
+    want["logp"] = torch.where(live, lp.gather(1, t.clamp(min=0)[:, None])[:, 0], torch.zeros_like(lp[:, 0]))
+    if top:
+        want["top_logp"] = torch.sort(lp, 1, descending=True)[0][:, :top]
+    off = {k: _rel(getattr(res, k), x) for k, x in want.items() if float(x.norm())}
+    print(" ".join(f"{k} {x:.1e}" for k, x in off.items()))
+    assert all(x <= 1e-6 for x in off.values()), off
