@@ -177,6 +177,19 @@ def test_dh_over_chunks_of_the_vocabulary(kind):
     limit = lambda x: F32_NORM if kind == "f32" else 2 * 2.0 ** -8
     assert _rel(dh, want_h) <= limit(dh) and _rel(dw, want_w) <= limit(dw)
     assert torch.equal(dh, again[0]) and torch.equal(dw, again[1])
+    if kind != "bf16_f32":   # (where dw's type, that of w when it is not asked for, is the same)
+        only_h, _ = txl.logprob_bwd(h, w, t, lse, dlogp, grads=(torch.empty_like(h), None), workspace=ws.fill_(255))
+        _, only_w = txl.logprob_bwd(h, w, t, lse, dlogp, grads=(None, torch.empty_like(w)), workspace=ws)
+        assert torch.equal(dh, only_h) and torch.equal(dw, only_w)
+    # replays of a captured call follow its inputs
+    graph, out = torch.cuda.CUDAGraph(), (torch.empty_like(dh), torch.empty_like(dw))
+    with torch.cuda.graph(graph):
+        txl.logprob_bwd(h, w, t, lse, dlogp, grads=out, workspace=ws)
+    dlogp.neg_()
+    for _ in range(2):
+        graph.replay()
+    _ok()
+    assert torch.equal(out[0], -dh) and torch.equal(out[1], -dw)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -318,7 +318,7 @@ class XLStack:
     def _check_ids(self, ids: torch.Tensor, name: str):
         if ids.is_cuda or ids.numel() == 0:
             return
-        V, low, high = self.emb.shape[0], int(ids.min()), int(ids.max())
+        V, (low, high) = self.emb.shape[0], (int(x) for x in ids.aminmax())
         if low < -1 or high >= V:
             raise IndexError(f"{name}: {low if low < -1 else high} is none of the {V} words (nor -1)")
 
