@@ -619,9 +619,11 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
  *   entropy_i = lse_i - sum_j p_ij z_ij,  p_ij = exp(z_ij - lse_i)
  *   top_ids[i][0 .. top-1]  the `top` largest z_ij in descending order, equal ones by
  *             ascending j;  top_logp the z - lse of them.  The top + 4 largest by their
- *             fp32 sums are ordered by sums carried beyond fp32.  NaN logits are not
+ *             fp32 sums (up to 256 states without kept logits: those beside them in their fours too) are
+ *             ordered by sums carried beyond fp32; of more logits within fp32's rounding of one another
+ *             at the end of the list, which ones it holds goes by their fp32 sums.  NaN logits are not
  *             listed; places without a number hold id -1 and NaN.
- * The logits are never written.
+ * The logits are not kept (with alternatives, those of up to 64 and d / 16 states pass through the workspace).
  *   h [N] rows, w [V] rows of d, strides apart, both of dtype; targets [N] or NULL
  *   logp, lse, entropy [N] fp32, top_logp [N][top] fp32, top_ids [N][top] int32: each may
  *   be NULL (the last two only when top = 0)
@@ -630,8 +632,9 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
  * each (their leading 24 bits; values beneath bf16's subnormals are lost), six products on
  * the tensor cores, fp32 sums; there an infinite element of h or w makes a logit it enters NaN.
  * The tensor cores cut each of a logit's d / 16 additions; it is scaled by the mean of that, which where nothing was
- * cut (a state with one element) is d 2^-30 of its value.  The target's and the largest logits are
- * formed again without.
+ * cut (a state with one element) is d 2^-30 of its value.  The target's logit and, with alternatives, the
+ * largest are formed again without.  Sums of exponentials leave the largest's own 1 out, so log probabilities near 0
+ * are as exact as others, relative to their size, down to about 2^-40.
  * A logit of -infinity has probability zero; a row with a logit of +infinity or NaN gives NaN.  Logits of more
  * than 2^128 ln 2 (2.35e38) in size count as infinite.
  *   workspace: txl_logprob_fwd_workspace_size(N, V, d, top, dtype) bytes (0 for arguments

@@ -30,7 +30,7 @@ N-layer summary, Appendix B reversed table and shift):
   embed_fwd, embed_bwd  the scaled rows of the embedding table for given tokens, and
                   the table's gradient
   logprob_fwd     log probabilities of given tokens under softmax(h E^T), with the
-                  entropy and the most probable alternatives, without the logits
+                  entropy and the most probable alternatives; the logits are not kept
   logprob_bwd     its gradients of h and of the table
 """
 

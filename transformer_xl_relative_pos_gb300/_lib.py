@@ -922,7 +922,7 @@ def logprob_fwd(h, w, targets=None, *, scale: float = 1.0, top: int = 0, out: Lo
     """Under softmax(scale * h w^T), for each of the states h [..., d] (equally spaced rows) over
     the table w [V, d] (both bf16 or both fp32): the log probability of its target (int32 or
     int64, -1: none, gives 0), the log-sum-exp, the entropy, and the ``top`` (up to 16) most
-    probable tokens.  The logits are never written.  ``out``: a LogProbs of tensors to fill (None
+    probable tokens.  The logits are not kept.  ``out``: a LogProbs of tensors to fill (None
     entries are left out); ``workspace``: a device buffer of at least
     :func:`logprob_fwd_workspace_size` bytes (allocated when omitted)."""
     index, V, d, w_stride = _table(w, "w")
