@@ -634,7 +634,8 @@ int txl_embed_bwd(const void *tokens, int index_type, const void *dout, long lon
  * The tensor cores cut each of a logit's d / 16 additions; it is scaled by the mean of that, which where nothing was
  * cut (a state with one element) is d 2^-30 of its value.  The target's logit and, with alternatives, the
  * largest are formed again without.  Sums of exponentials leave the largest's own 1 out, so log probabilities near 0
- * are as exact as others, relative to their size, down to about 2^-40.
+ * are as exact as others, relative to their size, down to about 2^-45 times
+ * the largest logit.
  * A logit of -infinity has probability zero; a row with a logit of +infinity or NaN gives NaN.  Logits of more
  * than 2^128 ln 2 (2.35e38) in size count as infinite.
  *   workspace: txl_logprob_fwd_workspace_size(N, V, d, top, dtype) bytes (0 for arguments

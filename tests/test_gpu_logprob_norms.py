@@ -287,3 +287,26 @@ def test_log_probabilities_in_the_norm(N, V, d, top, dtype):
     off = {k: _rel(getattr(res, k), x) for k, x in want.items() if float(x.norm())}
     print(" ".join(f"{k} {x:.1e}" for k, x in off.items()))
     assert all(x <= 1e-6 for x in off.values()), off
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,d", [(3, 4096), (3, 65536), (300, 4096)])
+def test_logits_of_sparse_states(N, d, dtype):
+    # states of one element: nothing of a logit is cut, and the mean cut that it is scaled by, d 2^-30, is its
+    # error; beside it three roundings of logits of up to 24 and one of the result, and the sums' 2^-20
+    V = 700
+    g = torch.Generator().manual_seed(d + N)
+    h = torch.zeros(N, d, dtype=torch.float64)
+    at = torch.randint(0, d, (N,), generator=g)
+    h[torch.arange(N), at] = 4.0
+    w = (torch.randn(V, d, generator=g) * 1.5).to(dtype)
+    z = h @ w.double().t()
+    res = txl.logprob_fwd(h.to(dtype).to(dev()), w.to(dev()), top=2)
+    _ok()
+    most = float(z.abs().max())
+    off = (d * 2.0 ** -30 + 4 * 2.0 ** -24) * most + 2.0 ** -20
+    want = torch.logsumexp(z, 1)
+    assert most < 32 and float((res.lse.cpu().double() - want).abs().max()) <= off
+    best = torch.sort(z, dim=1, descending=True, stable=True)   # (bf16 words have equal elements)
+    assert torch.equal(res.top_ids.cpu().long(), best[1][:, :2])
+    assert float((res.top_logp.cpu().double() - (best[0][:, :2] - want[:, None])).abs().max()) <= 2 * off
